@@ -99,6 +99,12 @@ extern "C" {
 #define MOE_RS_ERR_BAD_HIDDEN (-14)       /* H not a multiple of 8 in [8, 8192]            */
 #define MOE_RS_ERR_NOT_MAPPED (-15)       /* host memory not mapped into the device space  */
 #define MOE_RS_ERR_BAD_DEBUG_KNOB (-16)   /* moe_route_sort_debug_set: unknown knob         */
+#define MOE_RS_ERR_BAD_DTYPE (-17)        /* a type code the operation does not take       */
+#define MOE_RS_ERR_BAD_COLS (-18)         /* row length not a multiple of 32 in [32, 32768],
+                                             a row stride below it, or an output width not a
+                                             multiple of 8 in [8, 65536]                   */
+#define MOE_RS_ERR_BAD_SEQUENCES (-19)    /* n_seq outside [1, 65536], or > 1 with no offsets */
+#define MOE_RS_ERR_BAD_ROWS (-20)         /* a negative number of rows                     */
 
 /* Device-side status bits, written to the first int32 of the workspace by every call. */
 #define MOE_RS_DEVICE_BAD_EXPERT_ID 0x1   /* moe_sort saw an id >= E; those routes dropped */
@@ -231,6 +237,122 @@ int moe_route_sort_from_host(const void* logits_host, void* logits_dev, const fl
                              int32_t* num_tokens_post_pad, void* workspace,
                              size_t workspace_bytes, const void* result_dev, void* result_host,
                              size_t result_bytes, cudaStream_t stream);
+
+/* ------------------------------------------------------------- training the router */
+
+/* Type codes of the operations below that take several. */
+#define MOE_RS_BF16 0
+#define MOE_RS_FP16 1
+#define MOE_RS_FP32 2
+
+/* Most sequences of one call. */
+#define MOE_RS_MAX_SEQUENCES 65536
+
+/* Bytes of device workspace that moe_balance_loss needs (16-byte aligned, any contents).  One
+ * workspace must not be used by two calls that can run at the same time.  0 for invalid
+ * arguments. */
+size_t moe_balance_workspace_bytes(int T, int E, int n_seq);
+
+/* Balance loss of a router over S = n_seq sequences of consecutive tokens, with the per-expert
+ * counts and mean probabilities it is made of.  x = float(bf16 logit), K = topk,
+ * sequence i = tokens [seq_offsets[i], seq_offsets[i+1]), n_i of them:
+ *   p_te = softmax(x_t)_e (softmax != 0), or s_te / sum_e s_te with s = 1 / (1 + exp(-x))
+ *   counts[i,e]     = routes (t in i, k) with topk_ids[t,k] == e
+ *   mean_probs[i,e] = mean of p_te over the tokens of i
+ *   loss[0]         = coef / S * sum_i sum_e (E * counts[i,e] / (K * n_i)) * mean_probs[i,e]
+ * (1 for a perfectly even router times coef, whatever E and K).  An empty sequence has zero
+ * counts and mean_probs, adds nothing to the loss and still counts in S.  Tokens outside every
+ * sequence (before the first border, behind the last) are left out.  seq_offsets: [S+1] int32
+ * device memory, non-decreasing; borders outside [0, T] act as 0 or T.  NULL with n_seq == 1: one
+ * sequence of all T tokens.  Ids outside [0, E) are dropped routes: not counted.
+ * Logits may be -inf (a score and probability of 0; a row of nothing else adds 0); NaN or +inf
+ * logits give unspecified results.  logits_bf16 [T,E] 16-byte aligned, topk_ids [T,K]; outputs
+ * loss [1] fp32, counts [S,E] int32, mean_probs [S,E] fp32, all overwritten.  Sums are fp32 in a
+ * fixed order (the same bits every call); exponentials are the fast ones, within a few 2^-22.
+ * Limits: 1 <= E <= 4096, 1 <= K <= min(32, E), 1 <= S <= 65536, T >= 0, T*K in int32.
+ * No counterpart in the source pages. */
+int moe_balance_loss(const void* logits_bf16, const int32_t* topk_ids, const int32_t* seq_offsets,
+                     int T, int E, int topk, int n_seq, int softmax, float coef, float* loss,
+                     int32_t* counts, float* mean_probs, void* workspace, size_t workspace_bytes,
+                     cudaStream_t stream);
+
+/* Gradient to the logits of the routing weights and of the balance loss, in one pass:
+ *   grad_logits[t,e] = sum_k grad_weights[t,k] d w_tk / d x_te + grad_loss[0] d loss / d x_te
+ * where w_tk = routed_scale * u_k / (sum of u over the token's valid routes), u the sigmoid
+ * score of the routed logit (or its exponential, softmax != 0): the weights of moe_topk and
+ * moe_route_sort_softmax when no route is dropped.  The selection and the counts are constants of
+ * the gradient (the bias and the groups only steer the selection).
+ * grad_weights [T,K] fp32, or NULL: no weights term (topk_ids may then be NULL too).
+ * grad_loss [1] fp32 device memory, or NULL: no loss term (counts may then be NULL too);
+ * counts [S,E]: as moe_balance_loss wrote them, with the same sequences and coef.  Routes outside
+ * [0, E) take no part and their grad_weights are not used; an expert named twice by a token gets
+ * the sum.  Tokens outside every sequence have no loss term.  Every element of grad_logits [T,E]
+ * is written (16-byte aligned; grad_dtype MOE_RS_BF16 or MOE_RS_FP32, one rounding of an fp32
+ * sum).  Limits and logits as for moe_balance_loss; no workspace.  No counterpart in the source
+ * pages. */
+int moe_route_backward(const void* logits_bf16, const int32_t* topk_ids, const float* grad_weights,
+                       const float* grad_loss, const int32_t* counts, const int32_t* seq_offsets,
+                       int T, int E, int topk, int n_seq, int softmax, float routed_scale,
+                       float coef, void* grad_logits, int grad_dtype, cudaStream_t stream);
+
+/* ------------------------------------------- experts' products in 4-bit floating point */
+
+/* Microscaled 4-bit rows ("MXFP4"): 32 consecutive elements of a row share a scale 2^e held as
+ * the byte e + 127 (255: NaN), and each element is one of {0, 1/2, 1, 3/2, 2, 3, 4, 6} * 2^e with
+ * a sign: a 4-bit code, sign in bit 3, the magnitude's index in bits 0-2; byte j of a row holds
+ * columns 2j (low nibble) and 2j + 1.  codes: [rows, cols / 2] bytes, 16-byte aligned;
+ * scales: [rows, moe_mxfp4_scale_cols(cols)] bytes, 4-byte aligned, the bytes past cols / 32
+ * padding.  cols: a multiple of 32 in [32, MOE_RS_MXFP4_MAX_COLS]. */
+#define MOE_RS_MXFP4_MAX_COLS 32768
+#define MOE_RS_MXFP4_MAX_OUTS 65536
+
+/* Scale bytes per row: 4 * ceil(cols / 128).  0 for invalid cols. */
+int moe_mxfp4_scale_cols(int cols);
+
+/* Rows to MXFP4.  x: `rows` rows of `cols` elements of type x_dtype (MOE_RS_BF16, MOE_RS_FP16,
+ * MOE_RS_FP32), x_stride elements apart (>= cols), each row 16-byte aligned.  Per block of 32:
+ * e = floor(log2(largest magnitude)) - 2 clamped to [-127, 125]; codes are the nearest multiples,
+ * ties to the even code, saturating at 6 * 2^e.  A block of zeros has scale byte 0; a block with
+ * an infinity or a NaN has scale byte 255 and zero codes.  Padding scale bytes are written 0.
+ * Weights are quantised by the same call, once.  Errors: MOE_RS_ERR_BAD_DTYPE, _BAD_ROWS,
+ * _BAD_COLS, _OVERFLOW, _NULL_POINTER, _MISALIGNED, _ALIAS, _LAUNCH. */
+int moe_mxfp4_quantize(const void* x, int x_dtype, int64_t rows, int cols, int64_t x_stride,
+                       uint8_t* codes, uint8_t* scales, cudaStream_t stream);
+
+/* The values that MXFP4 rows stand for, into y (y_dtype MOE_RS_BF16 or MOE_RS_FP32, y_stride
+ * elements between rows, each row 16-byte aligned).  fp32 holds every value; bf16 holds every
+ * value that moe_mxfp4_quantize makes.  Errors as above. */
+int moe_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int cols,
+                         void* y, int y_dtype, int64_t y_stride, cudaStream_t stream);
+
+/* Bytes of device workspace of moe_experts_mxfp4 (16-byte aligned).  Its first int32 collects the
+ * MOE_RS_DEVICE_* bits of the calls that use it and is never cleared by them: zero it before
+ * first use.  Calls that run at the same time may share it. */
+size_t moe_experts_mxfp4_workspace_bytes(int T, int E, int topk, int block_m);
+
+/* The experts' products over a sorted list of routes (the block-grouped product that the sort
+ * metadata exists for), MXFP4 rows times MXFP4 weights.  For every row p < num_tokens_post_pad[0]
+ * whose r = sorted_token_ids[p] lies in [0, T*topk), e = expert_ids[p / block_m]:
+ *   out[r, n] = w_p * sum over k < cols of X[row, k] * W[e, n, k],     n < outs
+ * with row = r (x_per_route != 0: X has T*topk rows, for example the hidden rows of a second
+ * product) or r / topk (X has T rows, one per token), and w_p = sorted_weights[p], or 1 when
+ * sorted_weights is NULL.  Sums are fp32 and w_p is applied before the one rounding to out_dtype
+ * (MOE_RS_BF16 or MOE_RS_FP32).  out: [T*topk, outs], 16-byte aligned, row r being route r, so a
+ * second product reads it as it is and the sum over a token's experts is a sum of topk adjacent
+ * rows.  Rows of dropped routes are not written (a caller that drops routes clears them first).
+ * W: codes [E, outs, cols / 2], scales [E, outs, moe_mxfp4_scale_cols(cols)].
+ * sorted_token_ids, sorted_weights, expert_ids and num_tokens_post_pad are those of moe_sort or
+ * moe_route_sort with the same T, E, topk, block_m; blocks whose expert id lies outside [0, E)
+ * are skipped and set MOE_RS_DEVICE_BAD_EXPERT_ID.  A wait on the device that gives up sets
+ * MOE_RS_DEVICE_WAIT_TIMEOUT (outputs invalid).  Limits: those of moe_sort; cols as above; outs a
+ * multiple of 8 in [8, MOE_RS_MXFP4_MAX_OUTS].  No counterpart in the source pages, whose products
+ * belong to another library; the sizes of its 4-bit operator are those this call is tuned on. */
+int moe_experts_mxfp4(const uint8_t* x_codes, const uint8_t* x_scales, int x_per_route,
+                      const uint8_t* w_codes, const uint8_t* w_scales, int T, int E, int topk,
+                      int cols, int outs, int block_m, const int32_t* sorted_token_ids,
+                      const float* sorted_weights, const int32_t* expert_ids,
+                      const int32_t* num_tokens_post_pad, void* out, int out_dtype,
+                      void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /* ------------------------------------------------------- allocation-free variant */
 

@@ -38,3 +38,22 @@ from .binding import (  # noqa: F401
     route_sort_softmax,
     strerror,
 )
+from .experts import (  # noqa: F401
+    Mxfp4Rows,
+    experts_mxfp4,
+    moe_experts_mxfp4,
+    moe_experts_mxfp4_workspace_bytes,
+    moe_mxfp4_dequantize,
+    moe_mxfp4_quantize,
+    moe_mxfp4_scale_cols,
+    mxfp4_dequantize,
+    mxfp4_quantize,
+)
+from .training import (  # noqa: F401
+    BalanceBuffers,
+    balance_loss,
+    moe_balance_loss,
+    moe_balance_workspace_bytes,
+    moe_route_backward,
+    route_backward,
+)

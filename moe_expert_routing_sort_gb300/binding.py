@@ -84,6 +84,23 @@ def load() -> ctypes.CDLL:
         lib.moe_route_sort_noalloc_status.restype = I
         lib.moe_route_sort_debug_set.argtypes = [I, ctypes.c_longlong]
         lib.moe_route_sort_debug_set.restype = I
+        L = ctypes.c_int64
+        lib.moe_balance_workspace_bytes.argtypes = [I, I, I]
+        lib.moe_balance_workspace_bytes.restype = S
+        lib.moe_balance_loss.argtypes = [P, P, P, I, I, I, I, I, F, P, P, P, P, S, P]
+        lib.moe_balance_loss.restype = I
+        lib.moe_route_backward.argtypes = [P, P, P, P, P, P, I, I, I, I, I, F, F, P, I, P]
+        lib.moe_route_backward.restype = I
+        lib.moe_mxfp4_scale_cols.argtypes = [I]
+        lib.moe_mxfp4_scale_cols.restype = I
+        lib.moe_mxfp4_quantize.argtypes = [P, I, L, I, L, P, P, P]
+        lib.moe_mxfp4_quantize.restype = I
+        lib.moe_mxfp4_dequantize.argtypes = [P, P, L, I, P, I, L, P]
+        lib.moe_mxfp4_dequantize.restype = I
+        lib.moe_experts_mxfp4_workspace_bytes.argtypes = [I, I, I, I]
+        lib.moe_experts_mxfp4_workspace_bytes.restype = S
+        lib.moe_experts_mxfp4.argtypes = [P, P, I, P, P, I, I, I, I, I, I, P, P, P, P, P, I, P, S, P]
+        lib.moe_experts_mxfp4.restype = I
         _lib = lib
         return lib
 

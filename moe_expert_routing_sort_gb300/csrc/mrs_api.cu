@@ -9,6 +9,7 @@
 #include <mutex>
 
 #include "moe_route_sort.h"
+#include "mrs_args.h"
 #include "mrs_internal.h"
 
 namespace {
@@ -76,33 +77,6 @@ int check_route_shape(int T, int E, int G, int Kg, int K, float R) {
   if (static_cast<int64_t>(T) * K > INT32_MAX) return MOE_RS_ERR_OVERFLOW;
   return MOE_RS_OK;
 }
-
-struct Span {
-  uintptr_t lo, hi;  // [lo, hi)
-};
-
-Span span(const void* p, size_t bytes) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-  return Span{a, a + bytes};
-}
-
-bool overlap(const Span& a, const Span& b) {
-  if (a.lo == a.hi || b.lo == b.hi) return false;
-  return a.lo < b.hi && b.lo < a.hi;
-}
-
-// Outputs must not overlap each other or any input.
-bool any_alias(const Span* outs, int nout, const Span* ins, int nin) {
-  for (int i = 0; i < nout; ++i) {
-    for (int j = i + 1; j < nout; ++j)
-      if (overlap(outs[i], outs[j])) return true;
-    for (int j = 0; j < nin; ++j)
-      if (overlap(outs[i], ins[j])) return true;
-  }
-  return false;
-}
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 RouteShape make_shape(int E, int G, int Kg, int K, float R) {
   RouteShape sh{};
@@ -215,12 +189,6 @@ bool make_seg_shape(int E, int G, int Kg, int K, float R, int lanes, SegShape& s
   choose_unit_order(s, lanes);
   s.R = R;
   return true;
-}
-
-int launch_status(cudaError_t e) {
-  if (e == cudaSuccess) return MOE_RS_OK;
-  cudaGetLastError();  // clear a non-sticky launch error
-  return MOE_RS_ERR_LAUNCH;
 }
 
 // Multi-CTA route step.  Units are contiguous token ranges, one CTA each; with `sort`,
@@ -424,6 +392,13 @@ const char* moe_route_sort_strerror(int status) {
     case MOE_RS_ERR_NOT_MAPPED:
       return "host memory is not pinned and mapped into the device address space";
     case MOE_RS_ERR_BAD_DEBUG_KNOB: return "unknown moe_route_sort_debug_set knob";
+    case MOE_RS_ERR_BAD_DTYPE: return "a type code this operation does not take";
+    case MOE_RS_ERR_BAD_COLS:
+      return "row length must be a multiple of 32 in [32, 32768] (row strides at least that), "
+             "output width a multiple of 8 in [8, 65536]";
+    case MOE_RS_ERR_BAD_SEQUENCES:
+      return "n_seq must be in [1, 65536], and 1 without sequence offsets";
+    case MOE_RS_ERR_BAD_ROWS: return "the number of rows must be >= 0";
     default: return "unknown status";
   }
 }

@@ -1,0 +1,724 @@
+// mrs_balance.cu -- the balance loss of a router with its per-expert counts, and the gradient
+// of the routing weights and of that loss to the router logits.
+//
+// x = float(bf16 logit); S sequences of consecutive tokens, n_i tokens in sequence i:
+//   p_te    = softmax(x_t)_e, or sigmoid(x_te) / sum over e of sigmoid(x_te)
+//   c_ie    = routes of sequence i that go to expert e
+//   P_ie    = mean of p_te over the sequence
+//   loss    = coef / S * sum_i sum_e (E c_ie / (K n_i)) P_ie
+// The counts are constants of the gradient: with g_ie = grad_loss coef E c_ie / (S K n_i^2),
+//   softmax  dx_e = p_e (g_e - sum p g)        sigmoid  dx_e = p_e (1 - s_e) (g_e - sum p g)
+// and the routing weights w_k = R u_k / sum u (u = sigmoid or exp of the routed logits) add, at
+// the routed experts,    R q_k (gw_k - sum q gw), q = u / sum u      (times 1 - s_k for sigmoid).
+//
+// Both passes read the logits once.  A row belongs to a group of W warps (W = ceil(E / 1024)),
+// each lane holding up to 32 of its columns in registers, the same columns for every row: the
+// row sums are warp shuffles (and one exchange through shared memory when W > 1), and the
+// column sums of the loss stay in registers until the sequence or the CTA's token range ends.
+// A softmax row needs one reduction: every lane takes exponentials against its own maximum and
+// the reduction joins (maximum, sum) pairs.  The next row's loads are in flight while a row is
+// computed.  All sums are fp32 (the joined loss fp64) in an order fixed by the shape, so results
+// are the same bits every call.
+//
+// Partial column sums: CTA b of the first kernel and sequence i meet in at most one stretch of
+// tokens; it writes its sums to slot b + i (a monotone walk through (b, i): no two stretches
+// share a slot), and the second kernel adds the slots of each sequence in CTA order.
+#include <cmath>
+#include <type_traits>
+
+#include <cuda_bf16.h>
+
+#include "mrs_args.h"
+#include "mrs_internal.h"
+
+namespace mrs {
+
+constexpr int kBalThreads = 256;
+constexpr int kBalWarps = kBalThreads / 32;
+constexpr int kBalMaxCtas = 512;
+constexpr int kBalMaxJoin = 1024;  // CTAs of the second kernel
+constexpr float kLog2e = 1.4426950408889634f;
+// Below every finite bf16 and itself finite: maxima start here, so that a column of -inf gives a
+// term of exp(-inf) = 0 whatever the others hold, and a row of the type's lowest value is even.
+constexpr float kLowest = -3.402823466e38f;
+
+struct BalanceArgs {
+  const uint16_t* logits;
+  const int32_t* ids;
+  const int32_t* offsets;  // [S + 1], or null: one sequence of all T tokens
+  int T, E, K, S, W;       // W: warps per row
+  int tpc;                 // tokens per CTA
+  float coef;
+  float* loss;
+  int32_t* counts;
+  float* mean;
+  float* psum;      // [ctas + S][E] slots
+  int32_t* csum;    // [ctas + S][E]
+  double* partial;  // [kBalMaxJoin]
+  unsigned* ticket;
+};
+
+struct RouteBackwardArgs {
+  const uint16_t* logits;
+  const int32_t* ids;
+  const float* gw;         // [T, K] or null
+  const float* gl;         // [1] or null
+  const int32_t* counts;   // [S, E] (null with gl)
+  const int32_t* offsets;
+  int T, E, K, S, W, tpc;
+  float R, coef;
+  void* out;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Borders of the sequences, kept inside [0, T] whatever the array holds.
+__device__ __forceinline__ int seq_border(const int32_t* o, int i, int T) {
+  return o == nullptr ? (i == 0 ? 0 : T) : min(max(__ldg(o + i), 0), T);
+}
+
+// First sequence that ends behind token t (S if none does).
+__device__ __forceinline__ int seq_behind(const int32_t* o, int S, int T, int t) {
+  int lo = 0, hi = S;
+  while (lo < hi) {
+    const int m = (lo + hi) >> 1;
+    if (seq_border(o, m + 1, T) > t) hi = m;
+    else lo = m + 1;
+  }
+  return lo;
+}
+
+// The raw bits of a lane's columns of one row.  kVec: 16-byte vectors of 8 columns, vector v of
+// the lane being vector v * lanes + lane of the row; else single columns i * lanes + lane.
+// Columns past E read as -inf (a score and a probability of zero).
+template <int NC, bool kVec>
+struct RowBits {
+  uint32_t w[kVec ? NC / 2 : NC];
+  __device__ __forceinline__ void load(const uint16_t* row, int E, int lane, int lanes) {
+    if constexpr (kVec) {
+#pragma unroll
+      for (int v = 0; v < NC / 8; ++v) {
+        const int c = 8 * (v * lanes + lane);
+        uint4 q = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
+        if (c < E) q = __ldg(reinterpret_cast<const uint4*>(row + c));
+        w[4 * v] = q.x;
+        w[4 * v + 1] = q.y;
+        w[4 * v + 2] = q.z;
+        w[4 * v + 3] = q.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const int c = i * lanes + lane;
+        w[i] = c < E ? static_cast<uint32_t>(__ldg(row + c)) << 16 : 0xff800000u;
+      }
+    }
+  }
+  __device__ __forceinline__ void values(float (&x)[NC]) const {
+    if constexpr (kVec) {
+#pragma unroll
+      for (int i = 0; i < NC / 2; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NC; ++i) x[i] = __uint_as_float(w[i]);
+    }
+  }
+};
+
+// Column of a lane's element i (may be >= E).
+template <bool kVec>
+__device__ __forceinline__ int column_of(int i, int lane, int lanes) {
+  return kVec ? 8 * ((i >> 3) * lanes + lane) + (i & 7) : i * lanes + lane;
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(kFull, v, d);
+  return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, d));
+  return v;
+}
+
+// Barrier of the W warps of group `grp` (hardware barriers 1..).
+__device__ __forceinline__ void group_sync(int grp, int W) {
+  asm volatile("bar.sync %0, %1;" ::"r"(grp + 1), "r"(32 * W) : "memory");
+}
+
+// Scores of one row in place, and the row's sums.  On return x holds the terms u_e of the lane
+// (scaled by a factor of its own for softmax), `scale` turns a term into a probability, and
+// `dot` is sum over e of p_e g_e (kDot).  xchg: [2][W] float4 of the group, buffer `buf`.
+template <int NC, bool kSoftmax, bool kDot>
+__device__ __forceinline__ void row_terms(float (&x)[NC], const float (&g)[kDot ? NC : 1],
+                                          int W, int grp, int gw, float4* xchg, int buf,
+                                          float& scale, float& dot) {
+  float m = 0.0f, sum = 0.0f, sg = 0.0f;
+  if constexpr (kSoftmax) {
+    m = kLowest;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) m = fmaxf(m, x[i]);
+    // the difference first: exact near the maximum, where the terms matter
+#pragma unroll
+    for (int i = 0; i < NC; ++i) x[i] = ex2((x[i] - m) * kLog2e);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) x[i] = rcp(1.0f + ex2(-kLog2e * x[i]));
+  }
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    sum += x[i];
+    if constexpr (kDot) sg = fmaf(x[i], g[i], sg);
+  }
+  float f = 1.0f;  // the lane's factor
+  if constexpr (kSoftmax) {
+    const float M = warp_max(m);
+    f = ex2((m - M) * kLog2e);
+    sum *= f;
+    if constexpr (kDot) sg *= f;
+    m = M;
+  }
+  sum = warp_sum(sum);
+  if constexpr (kDot) sg = warp_sum(sg);
+  if (W > 1) {
+    float4* slot = xchg + buf * W;
+    if ((threadIdx.x & 31) == 0) slot[gw] = make_float4(m, sum, sg, 0.0f);
+    group_sync(grp, W);
+    float M = m;
+    if constexpr (kSoftmax)
+      for (int w = 0; w < W; ++w) M = fmaxf(M, slot[w].x);
+    sum = 0.0f;
+    sg = 0.0f;
+    for (int w = 0; w < W; ++w) {
+      const float4 q = slot[w];
+      const float r = kSoftmax ? ex2((q.x - M) * kLog2e) : 1.0f;
+      sum = fmaf(q.y, r, sum);
+      if constexpr (kDot) sg = fmaf(q.z, r, sg);
+    }
+    if constexpr (kSoftmax) f *= ex2((m - M) * kLog2e);
+  }
+  const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+  scale = f * inv;
+  dot = sg * inv;
+}
+
+// ------------------------------------------------------------------------------ the loss
+template <int NC, bool kVec, bool kSoftmax>
+__global__ void __launch_bounds__(kBalThreads) mrs_balance_rows_kernel(const BalanceArgs a) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ float4 xchg_s[kBalWarps][2];
+  float* red = reinterpret_cast<float*>(smem);                       // [groups][W * 32 * NC]
+  int* hist = reinterpret_cast<int*>(red + kBalThreads * NC);        // [E]
+  const int tid = threadIdx.x, warp = tid >> 5, W = a.W, E = a.E;
+  const int grp = warp / W, gw = warp - grp * W, groups = kBalWarps / W;
+  const int lanes = 32 * W, lane = 32 * gw + (tid & 31);
+  const bool idle = grp >= groups;  // W = 3 leaves two warps without a group
+  float4* xchg = &xchg_s[0][0] + grp * 2 * W;
+  pdl_trigger();
+  for (int e = tid; e < E; e += kBalThreads) hist[e] = 0;
+  pdl_wait();
+  if (blockIdx.x == 0 && tid == 0) *a.ticket = 0u;
+  __syncthreads();
+
+  const int t0 = min(static_cast<int>(blockIdx.x) * a.tpc, a.T);
+  const int t1 = min(a.T - t0, a.tpc) + t0;
+  float g0[1] = {0.0f};
+  int t = t0;
+  for (int i = seq_behind(a.offsets, a.S, a.T, t0); i < a.S && t < t1; ++i) {
+    const int lo = max(seq_border(a.offsets, i, a.T), t);
+    const int hi = min(seq_border(a.offsets, i + 1, a.T), t1);
+    if (hi <= lo) continue;
+    t = hi;
+    // counts of the stretch
+    const size_t r1 = static_cast<size_t>(hi) * a.K;
+    for (size_t r = static_cast<size_t>(lo) * a.K + tid; r < r1; r += kBalThreads) {
+      const int e = __ldg(a.ids + r);
+      if (e >= 0 && e < E) atomicAdd(hist + e, 1);  // integers: any order, the same sum
+    }
+    float acc[NC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) acc[c] = 0.0f;
+    if (!idle) {
+      RowBits<NC, kVec> next;
+      int row = lo + grp, buf = 0;
+      if (row < hi) next.load(a.logits + static_cast<size_t>(row) * E, E, lane, lanes);
+      for (; row < hi; row += groups) {
+        float x[NC], scale, dot;
+        next.values(x);
+        if (row + groups < hi)
+          next.load(a.logits + static_cast<size_t>(row + groups) * E, E, lane, lanes);
+        row_terms<NC, kSoftmax, false>(x, g0, W, grp, gw, xchg, buf, scale, dot);
+        buf ^= 1;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) acc[c] = fmaf(x[c], scale, acc[c]);
+      }
+      float* mine = red + static_cast<size_t>(grp) * lanes * NC;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) mine[column_of<kVec>(c, lane, lanes)] = acc[c];
+    }
+    __syncthreads();
+    const size_t slot = static_cast<size_t>(blockIdx.x + i) * E;
+    for (int e = tid; e < E; e += kBalThreads) {
+      float s = red[e];
+      for (int q = 1; q < groups; ++q) s += red[static_cast<size_t>(q) * lanes * NC + e];
+      a.psum[slot + e] = s;
+      a.csum[slot + e] = hist[e];
+      hist[e] = 0;
+    }
+    __syncthreads();
+  }
+}
+
+// Joins the slots: CTA (bx, by) takes 32 experts of the sequences by, by + gridDim.y, ...; warp w
+// the slots w, w + 8, ... of a sequence.  The last CTA to finish adds the loss.
+__global__ void __launch_bounds__(kBalThreads) mrs_balance_join_kernel(const BalanceArgs a) {
+  __shared__ float ps[kBalWarps][32];
+  __shared__ int cs[kBalWarps][32];
+  __shared__ double ls[kBalThreads];
+  __shared__ bool last;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int e = blockIdx.x * 32 + lane;
+  pdl_trigger();
+  pdl_wait();
+  double loss = 0.0;
+  for (int i = blockIdx.y; i < a.S; i += gridDim.y) {
+    const int lo = seq_border(a.offsets, i, a.T), hi = seq_border(a.offsets, i + 1, a.T);
+    float p = 0.0f;
+    int c = 0;
+    if (hi > lo && e < a.E) {
+      const int b1 = (hi - 1) / a.tpc;
+#pragma unroll 4
+      for (int b = lo / a.tpc + warp; b <= b1; b += kBalWarps) {
+        const size_t at = static_cast<size_t>(b + i) * a.E + e;
+        p += a.psum[at];
+        c += a.csum[at];
+      }
+    }
+    ps[warp][lane] = p;
+    cs[warp][lane] = c;
+    __syncthreads();
+    if (warp == 0 && e < a.E) {
+#pragma unroll
+      for (int w = 1; w < kBalWarps; ++w) {
+        p += ps[w][lane];
+        c += cs[w][lane];
+      }
+      const float n = static_cast<float>(max(hi - lo, 1));
+      const float mean = p / n;
+      const size_t at = static_cast<size_t>(i) * a.E + e;
+      a.counts[at] = c;
+      a.mean[at] = mean;
+      loss += static_cast<double>(c) * mean / n;
+    }
+    __syncthreads();
+  }
+  // this CTA's part of the loss, then everybody's
+  const int ctas = gridDim.x * gridDim.y;
+  if (warp == 0) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) loss += __shfl_xor_sync(kFull, loss, d);
+    if (lane == 0) {
+      a.partial[blockIdx.y * gridDim.x + blockIdx.x] = loss;
+      __threadfence();
+      last = atomicAdd(a.ticket, 1u) == static_cast<unsigned>(ctas - 1);
+      __threadfence();
+    }
+  }
+  __syncthreads();
+  if (!last) return;
+  double s = 0.0;
+  for (int q = tid; q < ctas; q += kBalThreads) s += __ldcg(a.partial + q);
+  ls[tid] = s;
+  __syncthreads();
+  for (int d = kBalThreads / 2; d > 0; d >>= 1) {
+    if (tid < d) ls[tid] += ls[tid + d];
+    __syncthreads();
+  }
+  if (tid == 0)
+    *a.loss = static_cast<float>(ls[0] * a.coef * a.E / (static_cast<double>(a.K) * a.S));
+}
+
+// -------------------------------------------------------------------------- the gradient
+template <int NC, bool kVec, bool kSoftmax, class Out>
+__global__ void __launch_bounds__(kBalThreads)
+    mrs_route_backward_kernel(const RouteBackwardArgs a) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ float4 xchg_s[kBalWarps][2];
+  const int tid = threadIdx.x, warp = tid >> 5, W = a.W, E = a.E, K = a.K, wl = tid & 31;
+  const int grp = warp / W, gw = warp - grp * W, groups = kBalWarps / W;
+  const int lanes = 32 * W, lane = 32 * gw + wl;
+  float4* xchg = &xchg_s[0][0] + grp * 2 * W;
+  // the routed experts' part of the group's current row, zero elsewhere; a warp only touches the
+  // columns that its own lanes hold
+  float* add = reinterpret_cast<float*>(smem) + static_cast<size_t>(grp) * lanes * NC;
+  pdl_trigger();
+  if (grp >= groups) return;  // W = 3 leaves two warps without a group
+#pragma unroll
+  for (int c = 0; c < NC; ++c) add[column_of<kVec>(c, lane, lanes)] = 0.0f;
+  __syncwarp();
+  pdl_wait();
+  const bool dense = a.gl != nullptr, sparse = a.gw != nullptr;
+  const float gl = dense ? __ldg(a.gl) : 0.0f;
+
+  const int t0 = min(static_cast<int>(blockIdx.x) * a.tpc, a.T);
+  const int t1 = min(a.T - t0, a.tpc) + t0;
+  int i = seq_behind(a.offsets, a.S, a.T, t0);
+  int buf = 0;
+  for (int t = t0; t < t1;) {
+    // the next stretch: a part of sequence i, or tokens of none (no balance term)
+    int hi = t1;
+    bool in_seq = false;
+    int lo_i = 0, hi_i = 0;
+    while (i < a.S) {
+      lo_i = seq_border(a.offsets, i, a.T);
+      hi_i = seq_border(a.offsets, i + 1, a.T);
+      if (hi_i > t && hi_i > lo_i) break;
+      ++i;
+    }
+    if (i < a.S) {
+      in_seq = lo_i <= t;
+      hi = min(t1, in_seq ? hi_i : lo_i);
+    }
+    float g[NC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) g[c] = 0.0f;
+    if (dense && in_seq) {
+      const float n = static_cast<float>(hi_i - lo_i);
+      const float f = gl * (a.coef / a.S) * (static_cast<float>(E) / K) / n / n;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const int e = column_of<kVec>(c, lane, lanes);
+        if (e < E) g[c] = f * static_cast<float>(__ldg(a.counts + static_cast<size_t>(i) * E + e));
+      }
+    }
+    RowBits<NC, kVec> next;
+    int row = t + grp;
+    int next_id = -1;
+    float next_gw = 0.0f;
+    auto fetch = [&](int r) {
+      next.load(a.logits + static_cast<size_t>(r) * E, E, lane, lanes);
+      if (sparse && wl < K) {
+        next_id = __ldg(a.ids + static_cast<size_t>(r) * K + wl);
+        next_gw = __ldg(a.gw + static_cast<size_t>(r) * K + wl);
+      }
+    };
+    if (row < hi) fetch(row);
+    for (; row < hi; row += groups) {
+      const uint16_t* xr = a.logits + static_cast<size_t>(row) * E;
+      float x[NC];
+      next.values(x);
+      int id = next_id;
+      float wg = next_gw;
+      const bool valid = sparse && wl < K && id >= 0 && id < E;
+      float xk = valid ? bf16_bits_to_float(__ldg(xr + id)) : -INFINITY;
+      if (row + groups < hi) fetch(row + groups);
+      float scale = 0.0f, dot = 0.0f;
+      if (dense) {
+        row_terms<NC, kSoftmax, true>(x, g, W, grp, gw, xchg, buf, scale, dot);
+        buf ^= 1;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          const float p = x[c] * scale;
+          x[c] = (kSoftmax ? p : p * (1.0f - x[c])) * (g[c] - dot);
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < NC; ++c) x[c] = 0.0f;
+      }
+      if (sparse) {
+        // every warp of the group works the K routes out, and keeps those in its columns
+        if (!valid) wg = 0.0f;
+        float u;
+        if (kSoftmax) {
+          const float m = fmaxf(warp_max(xk), kLowest);
+          u = ex2((xk - m) * kLog2e);
+        } else {
+          u = rcp(1.0f + ex2(-kLog2e * xk));  // 0 for a route that is none
+        }
+        const float su = warp_sum(u);
+        const float q = su > 0.0f ? u / su : 0.0f;
+        const float mean = warp_sum(q * wg);
+        float d = a.R * q * (wg - mean);
+        if (!kSoftmax) d *= 1.0f - u;
+        // an expert named twice: the lowest lane takes the sum, in slot order
+        const int key = valid ? id : -1 - wl;
+        const unsigned same = __match_any_sync(kFull, key);
+        if (__any_sync(kFull, (same & (same - 1u)) != 0u)) {
+          float s = 0.0f;
+          for (int l = 0; l < 32; ++l) {
+            const float o = __shfl_sync(kFull, d, l);
+            if ((same >> l) & 1u) s += o;
+          }
+          d = s;
+        }
+        const int owner = kVec ? (id >> 3) % lanes : id % lanes;
+        const bool put = valid && (same & lanemask_lt(wl)) == 0u && (owner >> 5) == gw;
+        if (put) add[id] = d;
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < NC; ++c) x[c] += add[column_of<kVec>(c, lane, lanes)];
+        __syncwarp();
+        if (put) add[id] = 0.0f;
+      }
+      Out* out = static_cast<Out*>(a.out) + static_cast<size_t>(row) * E;
+      if constexpr (kVec) {
+#pragma unroll
+        for (int v = 0; v < NC / 8; ++v) {
+          const int c = 8 * (v * lanes + lane);
+          if (c >= E) continue;
+          if constexpr (sizeof(Out) == 4) {
+            float4* o = reinterpret_cast<float4*>(out + c);
+            o[0] = make_float4(x[8 * v], x[8 * v + 1], x[8 * v + 2], x[8 * v + 3]);
+            o[1] = make_float4(x[8 * v + 4], x[8 * v + 5], x[8 * v + 6], x[8 * v + 7]);
+          } else {
+            // bf16 gradients: one rounding of the fp32 sum
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const __nv_bfloat162 b =
+                  __floats2bfloat162_rn(x[8 * v + 2 * j], x[8 * v + 2 * j + 1]);
+              w[j] = *reinterpret_cast<const uint32_t*>(&b);
+            }
+            *reinterpret_cast<uint4*>(out + c) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          const int e = c * lanes + lane;
+          if (e >= E) continue;
+          if constexpr (sizeof(Out) == 4) out[e] = x[c];
+          else out[e] = __float2bfloat16_rn(x[c]);
+        }
+      }
+    }
+    t = hi;
+  }
+}
+
+// ------------------------------------------------------------------------------ host side
+namespace {
+
+// Warps per row, columns per lane and the kind of loads for E experts.  16-byte loads need rows
+// that start on 16 bytes (E a multiple of 8).
+struct RowPlan {
+  int W, NC;
+  bool vec;
+};
+RowPlan row_plan(int E) {
+  RowPlan p{};
+  p.vec = E % 8 == 0;
+  p.W = (E + 1023) / 1024;
+  const int per = p.vec ? (E / 8 + 32 * p.W - 1) / (32 * p.W) * 8 : (E + 32 * p.W - 1) / (32 * p.W);
+  p.NC = per <= 8 ? 8 : (per <= 16 ? 16 : 32);
+  return p;
+}
+
+// Tokens per CTA: one row per group of warps until every SM has its share of the CTAs.
+int tokens_per_cta(int T, int W, int sms) {
+  const int groups = kBalWarps / W;
+  int ctas = 2 * sms < kBalMaxCtas ? 2 * sms : kBalMaxCtas;
+  const int most = (T + groups - 1) / groups;
+  if (most < ctas) ctas = most;
+  return (T + ctas - 1) / ctas;
+}
+
+struct BalanceLayout {
+  size_t ticket, partial, psum, csum, total;
+};
+// The largest number of CTAs of any device bounds the slots.
+BalanceLayout balance_layout(int T, int E, int S) {
+  const size_t most = static_cast<size_t>(T) < kBalMaxCtas ? static_cast<size_t>(T) : kBalMaxCtas;
+  const size_t slots = (most + static_cast<size_t>(S)) * static_cast<size_t>(E);
+  BalanceLayout l{};
+  l.partial = 16;
+  l.psum = l.partial + sizeof(double) * kBalMaxJoin;
+  l.csum = align16(l.psum + sizeof(float) * slots);
+  l.total = align16(l.csum + sizeof(int32_t) * slots);
+  return l;
+}
+
+int check_router(int T, int E, int K, int S) {
+  if (T < 0) return MOE_RS_ERR_BAD_TOKENS;
+  if (E < 1 || E > kMaxExperts) return MOE_RS_ERR_BAD_EXPERTS;
+  if (K < 1 || K > kMaxTopk || K > E) return MOE_RS_ERR_BAD_TOPK;
+  if (S < 1 || S > MOE_RS_MAX_SEQUENCES) return MOE_RS_ERR_BAD_SEQUENCES;
+  if (static_cast<int64_t>(T) * K > INT32_MAX) return MOE_RS_ERR_OVERFLOW;
+  return MOE_RS_OK;
+}
+
+bool sm_count(int& sms) {
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess &&
+         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess;
+}
+
+template <int NC, bool kVec>
+cudaError_t launch_balance(const BalanceArgs& a, bool softmax, int ctas, cudaStream_t st) {
+  auto* k = softmax ? mrs_balance_rows_kernel<NC, kVec, true>
+                    : mrs_balance_rows_kernel<NC, kVec, false>;
+  const size_t smem = sizeof(float) * kBalThreads * NC + sizeof(int) * static_cast<size_t>(a.E);
+  cudaError_t err =
+      cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (err != cudaSuccess) return err;
+  return launch_pdl(k, dim3(ctas), dim3(kBalThreads), smem, st, a);
+}
+
+template <int NC, bool kVec, class Out>
+cudaError_t launch_backward(const RouteBackwardArgs& a, bool softmax, int ctas, cudaStream_t st) {
+  auto* k = softmax ? mrs_route_backward_kernel<NC, kVec, true, Out>
+                    : mrs_route_backward_kernel<NC, kVec, false, Out>;
+  return launch_pdl(k, dim3(ctas), dim3(kBalThreads), sizeof(float) * kBalThreads * NC, st, a);
+}
+
+}  // namespace
+}  // namespace mrs
+
+using namespace mrs;
+
+extern "C" {
+
+size_t moe_balance_workspace_bytes(int T, int E, int n_seq) {
+  if (check_router(T, E, 1, n_seq)) return 0;
+  return balance_layout(T, E, n_seq).total;
+}
+
+int moe_balance_loss(const void* logits_bf16, const int32_t* topk_ids, const int32_t* seq_offsets,
+                     int T, int E, int topk, int n_seq, int softmax, float coef, float* loss,
+                     int32_t* counts, float* mean_probs, void* workspace, size_t workspace_bytes,
+                     cudaStream_t stream) {
+  int rc = check_router(T, E, topk, n_seq);
+  if (rc) return rc;
+  if (!std::isfinite(coef)) return MOE_RS_ERR_BAD_SCALE;
+  if (!seq_offsets && n_seq != 1) return MOE_RS_ERR_BAD_SEQUENCES;
+  if (!workspace) return MOE_RS_ERR_WORKSPACE;
+  if (!loss || !counts || !mean_probs || (T > 0 && (!logits_bf16 || !topk_ids)))
+    return MOE_RS_ERR_NULL_POINTER;
+  const BalanceLayout l = balance_layout(T, E, n_seq);
+  if (workspace_bytes < l.total) return MOE_RS_ERR_WORKSPACE;
+  if (!aligned(workspace, 16) || !aligned(loss, 4) || !aligned(counts, 4) ||
+      !aligned(mean_probs, 4) || !aligned(seq_offsets, 4) ||
+      (T > 0 && (!aligned(logits_bf16, 16) || !aligned(topk_ids, 4))))
+    return MOE_RS_ERR_MISALIGNED;
+  const size_t SE = static_cast<size_t>(n_seq) * E;
+  const Span outs[] = {span(loss, 4), span(counts, 4 * SE), span(mean_probs, 4 * SE),
+                       span(workspace, workspace_bytes)};
+  const Span ins[] = {span(logits_bf16, 2 * static_cast<size_t>(T) * E),
+                      span(topk_ids, 4 * static_cast<size_t>(T) * topk),
+                      span(seq_offsets, seq_offsets ? 4 * (static_cast<size_t>(n_seq) + 1) : 0)};
+  if (any_alias(outs, 4, ins, 3)) return MOE_RS_ERR_ALIAS;
+  int sms = 0;
+  if (!sm_count(sms)) return launch_status(cudaErrorInvalidDevice);
+  const RowPlan p = row_plan(E);
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  BalanceArgs a{};
+  a.logits = static_cast<const uint16_t*>(logits_bf16);
+  a.ids = topk_ids;
+  a.offsets = seq_offsets;
+  a.T = T;
+  a.E = E;
+  a.K = topk;
+  a.S = n_seq;
+  a.W = p.W;
+  a.tpc = T > 0 ? tokens_per_cta(T, p.W, sms) : 1;
+  a.coef = coef;
+  a.loss = loss;
+  a.counts = counts;
+  a.mean = mean_probs;
+  a.ticket = reinterpret_cast<unsigned*>(ws);
+  a.partial = reinterpret_cast<double*>(ws + l.partial);
+  a.psum = reinterpret_cast<float*>(ws + l.psum);
+  a.csum = reinterpret_cast<int32_t*>(ws + l.csum);
+  const int ctas = T > 0 ? (T + a.tpc - 1) / a.tpc : 1;
+  cudaError_t err;
+  if (p.vec)
+    err = p.NC == 8    ? launch_balance<8, true>(a, softmax != 0, ctas, stream)
+          : p.NC == 16 ? launch_balance<16, true>(a, softmax != 0, ctas, stream)
+                       : launch_balance<32, true>(a, softmax != 0, ctas, stream);
+  else
+    err = p.NC == 8    ? launch_balance<8, false>(a, softmax != 0, ctas, stream)
+          : p.NC == 16 ? launch_balance<16, false>(a, softmax != 0, ctas, stream)
+                       : launch_balance<32, false>(a, softmax != 0, ctas, stream);
+  if (err != cudaSuccess) return launch_status(err);
+  const int gx = (E + 31) / 32;
+  int gy = kBalMaxJoin / gx < 8 ? 8 : kBalMaxJoin / gx;  // gx <= 128
+  if (gy > n_seq) gy = n_seq;
+  return launch_status(
+      launch_pdl(mrs_balance_join_kernel, dim3(gx, gy), dim3(kBalThreads), 0, stream, a));
+}
+
+int moe_route_backward(const void* logits_bf16, const int32_t* topk_ids, const float* grad_weights,
+                       const float* grad_loss, const int32_t* counts, const int32_t* seq_offsets,
+                       int T, int E, int topk, int n_seq, int softmax, float routed_scale,
+                       float coef, void* grad_logits, int grad_dtype, cudaStream_t stream) {
+  int rc = check_router(T, E, topk, n_seq);
+  if (rc) return rc;
+  if (grad_dtype != MOE_RS_BF16 && grad_dtype != MOE_RS_FP32) return MOE_RS_ERR_BAD_DTYPE;
+  if (!std::isfinite(coef) || !std::isfinite(routed_scale)) return MOE_RS_ERR_BAD_SCALE;
+  if (!seq_offsets && n_seq != 1) return MOE_RS_ERR_BAD_SEQUENCES;
+  if (T == 0) return MOE_RS_OK;
+  if (!logits_bf16 || !grad_logits || (grad_weights && !topk_ids) || (grad_loss && !counts))
+    return MOE_RS_ERR_NULL_POINTER;
+  if (!aligned(logits_bf16, 16) || !aligned(grad_logits, 16) || !aligned(topk_ids, 4) ||
+      !aligned(grad_weights, 4) || !aligned(grad_loss, 4) || !aligned(counts, 4) ||
+      !aligned(seq_offsets, 4))
+    return MOE_RS_ERR_MISALIGNED;
+  const size_t TE = static_cast<size_t>(T) * E, TK = static_cast<size_t>(T) * topk;
+  const Span outs[] = {span(grad_logits, (grad_dtype == MOE_RS_FP32 ? 4 : 2) * TE)};
+  const Span ins[] = {span(logits_bf16, 2 * TE),
+                      span(topk_ids, topk_ids ? 4 * TK : 0),
+                      span(grad_weights, grad_weights ? 4 * TK : 0),
+                      span(grad_loss, grad_loss ? 4 : 0),
+                      span(counts, counts ? 4 * static_cast<size_t>(n_seq) * E : 0),
+                      span(seq_offsets, seq_offsets ? 4 * (static_cast<size_t>(n_seq) + 1) : 0)};
+  if (any_alias(outs, 1, ins, 6)) return MOE_RS_ERR_ALIAS;
+  int sms = 0;
+  if (!sm_count(sms)) return launch_status(cudaErrorInvalidDevice);
+  const RowPlan p = row_plan(E);
+  RouteBackwardArgs a{};
+  a.logits = static_cast<const uint16_t*>(logits_bf16);
+  a.ids = topk_ids;
+  a.gw = grad_weights;
+  a.gl = grad_loss;
+  a.counts = counts;
+  a.offsets = seq_offsets;
+  a.T = T;
+  a.E = E;
+  a.K = topk;
+  a.S = n_seq;
+  a.W = p.W;
+  a.tpc = tokens_per_cta(T, p.W, sms);
+  a.R = routed_scale;
+  a.coef = coef;
+  a.out = grad_logits;
+  const int ctas = (T + a.tpc - 1) / a.tpc;
+  const bool sm = softmax != 0, f32 = grad_dtype == MOE_RS_FP32;
+  auto go = [&](auto nc, auto vec) {
+    constexpr int NC = decltype(nc)::value;
+    constexpr bool V = decltype(vec)::value;
+    return f32 ? launch_backward<NC, V, float>(a, sm, ctas, stream)
+               : launch_backward<NC, V, __nv_bfloat16>(a, sm, ctas, stream);
+  };
+  using std::integral_constant;
+  auto pick = [&](auto vec) {
+    return p.NC == 8    ? go(integral_constant<int, 8>{}, vec)
+           : p.NC == 16 ? go(integral_constant<int, 16>{}, vec)
+                        : go(integral_constant<int, 32>{}, vec);
+  };
+  return launch_status(p.vec ? pick(std::true_type{}) : pick(std::false_type{}));
+}
+
+}  // extern "C"
