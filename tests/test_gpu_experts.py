@@ -282,6 +282,21 @@ def test_nan_scale_reaches_its_rows_only():
     assert torch.equal(torch.isnan(out).cpu(), nan)
 
 
+def test_padding_scale_bytes_are_not_used():
+    T, E, K, N, B = 20, 4, 2, 64, 16
+    g = torch.Generator().manual_seed(6)
+    for cols in (32, 96, 160, 288):
+        ids = _routes(g, T, E, K, "uniform")
+        x, W = _rows(g, T, cols), _rows(g, E * N, cols)
+        W = mrs.Mxfp4Rows(W.codes.view(E, N, -1), W.scales.view(E, N, -1))
+        m = _sorted(ids, torch.ones(T, K), E, B)
+        lists = (m.sorted_token_ids, m.expert_ids, m.num_tokens_post_pad)
+        a = mrs.experts_mxfp4(x, W, T, K, B, *lists, dtype=torch.float32)
+        x.scales[:, cols // 32:] = 255
+        W.scales[:, :, cols // 32:] = 255
+        assert torch.equal(a, mrs.experts_mxfp4(x, W, T, K, B, *lists, dtype=torch.float32))
+
+
 def test_bad_expert_ids_and_list_entries_are_skipped():
     T, E, K, cols, N, B = 32, 4, 1, 128, 64, 16
     g = torch.Generator().manual_seed(4)
@@ -365,3 +380,27 @@ def test_a_moe_layer_from_router_to_output(T):
     y64, mag = _ref_product(ids, w, a, W2, I, True)
     y64, mag = y64.view(T, K, H).sum(1), mag.view(T, K, H).sum(1)
     assert ((y.double() - y64).abs() <= (I * 2.0 ** -23 + K * 2.0 ** -23) * mag + 1e-38).all()
+
+
+@pytest.mark.parametrize("B,cols", [(16, 512), (128, 2048)])
+def test_waits_that_give_up_are_reported_and_leave_the_next_call_right(B, cols):
+    T, E, K, N = 60, 4, 2, 256
+    g = torch.Generator().manual_seed(7)
+    ids = _routes(g, T, E, K, "uniform")
+    x, W = _rows(g, T, cols), _rows(g, E * N, cols)
+    W = mrs.Mxfp4Rows(W.codes.view(E, N, -1), W.scales.view(E, N, -1))
+    m = _sorted(ids, torch.ones(T, K), E, B)
+    lists = (m.sorted_token_ids, m.expert_ids, m.num_tokens_post_pad)
+    good = mrs.experts_mxfp4(x, W, T, K, B, *lists)
+    ws = torch.zeros(256, dtype=torch.uint8, device=DEV)
+    try:
+        mrs.moe_route_sort_debug_set(mrs.DEBUG_WAIT_LIMIT_NS, 0)
+        out = torch.full_like(good, 3.0)
+        mrs.experts_mxfp4(x, W, T, K, B, *lists, out=out, workspace=ws)
+        torch.cuda.synchronize()
+    finally:
+        mrs.moe_route_sort_debug_set(mrs.DEBUG_WAIT_LIMIT_NS, -1)
+    assert int(ws[:4].view(torch.int32)) == 2  # MOE_RS_DEVICE_WAIT_TIMEOUT
+    ws.zero_()
+    again = mrs.experts_mxfp4(x, W, T, K, B, *lists, workspace=ws)
+    assert torch.equal(again, good) and int(ws[:4].view(torch.int32)) == 0
