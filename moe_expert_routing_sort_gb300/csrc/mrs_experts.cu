@@ -6,24 +6,29 @@
 // X and W are E2M1 codes with one E8M0 scale per 32 columns; sums are fp32, the row's weight
 // (1 without weights) is applied in fp32, and the result is rounded once to the output type.
 //
-// One tile is 128 outputs of one expert (the M side of the tensor-core product: weights fill it
-// whatever the number of tokens) by the rows of one block (the N side, BN = 16 .. 128; blocks of
-// more rows are cut, blocks of fewer leave columns unused).  A persistent CTA per SM takes tiles
-// round robin, the output tiles of a block next to each other, so the SMs share a block's rows
-// and an expert's weights in L2.  Steps of 256 columns (128 bytes a row) go through a ring of
+// One tile is the rows of one block (the M side of the tensor-core product, 128 lanes of tensor
+// memory; blocks of more rows are cut, blocks of fewer leave lanes unused) by 128 outputs of its
+// expert (the N side).  Rows on the lanes make the result a row per thread, so the outputs leave
+// as 32-byte stores of whole sectors; a block of 16 rows costs the tensor core as much as one of
+// 128, which it has time for: such calls wait for the weights.  A persistent CTA per SM takes
+// tiles round robin, the output tiles of a block next to each other, so the SMs share a block's
+// rows and an expert's weights in L2.  Steps of 256 columns (128 bytes a row) go through a ring of
 // shared-memory stages; the warps of a CTA each have one task:
-//   0     tensor copies: the weights' tile, and the block's rows gathered by index four at a
-//         time, both in the 128-byte swizzle the tensor core reads
-//   1     one thread copies the step's scales to tensor memory and issues four products of 64
-//         columns; the tensor core applies the scales and adds into fp32 in tensor memory
-//   2, 3  scales of the weights and of the rows, from row-major bytes to the order that tensor
-//         memory wants (row r of 128: lane r % 32, word r / 32 of 4 scales)
-//   4-7   a finished tile from tensor memory to the output rows, while the next one is computed
-//         (two accumulators)
-// Every wait is bounded; a wait that gives up ends its warp's task with the status bit set, and
-// the CTA leaves once nothing of its own is in flight.
-#include <type_traits>
-
+//   0      one thread copies the weights' 128 rows (a tensor copy, in the 128-byte swizzle that
+//          the tensor core reads)
+//   1      one thread copies the step's scales to tensor memory and issues four products of 64
+//          columns; the tensor core applies the scales and adds into fp32 in tensor memory
+//   2, 3   the weights' scales, from row-major bytes to the order that tensor memory wants (row
+//          r of 128: lane r % 32, word r / 32 of 4 scales)
+//   4-7    a finished tile from tensor memory to the output rows, while the next one is computed
+//          (two accumulators)
+//   8-11   the block's rows, 16 bytes a thread into the same swizzle, four steps in flight, with
+//          their scales.  (Gathered by tensor copies of four rows each they took 37 ns a copy:
+//          1.2 us a step of 128 rows, against 0.14 us of products.)
+// Each task has the list entries of the next two tiles and the first scales of the next one in
+// flight, so a tile of two steps does not wait for them.  Every wait is bounded; a wait that gives
+// up ends its warp's task with the status bit set, and the CTA leaves once nothing of its own is
+// in flight.
 #include <cuda_bf16.h>
 
 #include "mrs_args.h"
@@ -33,7 +38,7 @@
 namespace mrs {
 
 struct ExpertsArgs {
-  const unsigned char *xs, *ws;  // scales
+  const unsigned char *xc, *xs, *ws;  // rows, their scales, the weights' scales
   const int32_t* sid;
   const float* sw;  // or null
   const int32_t* eid;
@@ -43,77 +48,80 @@ struct ExpertsArgs {
   unsigned long long wait_limit_ns;
   int routes, topk, per_route;
   int E, K, N, B, scols, max_rows;
-  int sub, subs;   // rows of a tile (<= BN), tiles along a block's rows
+  int sub, subs;   // rows of a tile (<= 128), tiles along a block's rows
   int ntile;       // tiles along the outputs
   int ksteps;      // steps of 256 columns
+  int wide_scales; // scale rows start on 16 bytes
+  int wide_out;    // output rows start on 32 bytes
 };
 
-constexpr int kExpThreads = 256;
-constexpr int kExpM = 128;           // outputs per tile
-constexpr int kStepBytes = 128;      // bytes of a row per step
-constexpr int kScaleBytes = 2048;    // weights' and rows' scales of a step: 2 x 2 x 512
-constexpr int kTmemCols = 512;
-constexpr int kScalePrefetch = 4;    // steps whose scales a warp keeps in flight
+constexpr int kExpThreads = 384;
+constexpr int kExpRows = 128;      // lanes of a tile: rows of a block
+constexpr int kExpOuts = 128;      // outputs of a tile
+constexpr int kStepBytes = 128;    // bytes of a row per step
+constexpr int kXBytes = kExpRows * kStepBytes;
+constexpr int kWBytes = kExpOuts * kStepBytes;
+constexpr int kScaleBytes = 2048;  // rows' and weights' scales of a step: 2 x 2 x 512
+constexpr int kStageBytes = kXBytes + kWBytes + kScaleBytes;
+constexpr int kStages = 6;         // what fits in 227 KB
+constexpr int kCopyDepth = 4;      // steps of rows in flight
+constexpr size_t kExpSmem = static_cast<size_t>(kStages) * kStageBytes + 1024;
+constexpr int kTmemCols = 512;     // 2 accumulators of 128 columns, 16 of scales per stage
+constexpr int kTmemScales = 2 * kExpOuts;
 
-template <int BN>
-struct ExpertsStage {
-  static constexpr int kA = kExpM * kStepBytes;
-  static constexpr int kB = BN * kStepBytes;
-  static constexpr int kBytes = kA + kB + kScaleBytes;
-  // as many as fit beside the barriers, at most 10
-  static constexpr int kFit = (227 * 1024 - 2048) / kBytes;
-  static constexpr int kStages = kFit < 10 ? kFit : 10;
-  static constexpr size_t kSmem = static_cast<size_t>(kStages) * kBytes + 1024;
-};
-
+// A tile of the list: its expert id is in flight or here (-1 past the last tile).
 struct ExpertsTile {
-  int p0, n0, e;
+  int it, p0, n0, e;
+  __device__ __forceinline__ void at(const ExpertsArgs& a, int i, int tiles) {
+    it = i;
+    const int b = i / a.ntile;
+    n0 = (i - b * a.ntile) * kExpOuts;
+    p0 = b * a.sub;
+    e = i < tiles ? __ldg(a.eid + b / a.subs) : -1;
+  }
+  __device__ __forceinline__ bool valid(const ExpertsArgs& a) const { return e >= 0 && e < a.E; }
+  // Entry i of the tile's rows (-1: a lane unused, or past the last tile).
+  __device__ __forceinline__ int entry(const ExpertsArgs& a, int i, int tiles) const {
+    return (it < tiles && i < a.sub) ? __ldg(a.sid + p0 + i) : -1;
+  }
 };
 
-// Tile `it` of the list; false if its block's expert id is none (every warp decides alike).
-__device__ __forceinline__ bool experts_tile(const ExpertsArgs& a, long long it, ExpertsTile& t) {
-  const int b = static_cast<int>(it / a.ntile);
-  t.n0 = static_cast<int>(it - static_cast<long long>(b) * a.ntile) * kExpM;
-  t.p0 = b * a.sub;
-  t.e = __ldg(a.eid + b / a.subs);
-  return t.e >= 0 && t.e < a.E;
-}
-
-// Row i of the tile: its route, or -1 (padding, an entry outside the routes, a column unused).
-__device__ __forceinline__ int experts_route(const ExpertsArgs& a, const ExpertsTile& t, int i) {
-  if (i >= a.sub) return -1;
-  const int r = __ldg(a.sid + t.p0 + i);
-  return r >= 0 && r < a.routes ? r : -1;
-}
-
-// Scales of a warp's rows (lane + 32 j of the tile) for step `ks`: word j of q[g] holds the four
-// bytes of row lane + 32 j at columns [256 ks + 128 g, + 128).  Null rows and bytes past the
-// `blocks` scales of a row give 0, a finite scale, whatever the padding holds.
-__device__ __forceinline__ void load_scales(const unsigned char* const (&row)[4], int ks,
-                                            int blocks, uint4 (&q)[2]) {
-  uint32_t w[2][4];
-#pragma unroll
-  for (int g = 0; g < 2; ++g) {
-    const int at = 8 * ks + 4 * g, left = blocks - at;
-    const uint32_t keep = left >= 4 ? ~0u : (1u << (8 * max(left, 0))) - 1u;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      w[g][j] = (row[j] != nullptr && left > 0)
-                    ? __ldg(reinterpret_cast<const uint32_t*>(row[j] + at)) & keep
-                    : 0u;
+// Scales of one row, 16 bytes (two steps) at a time.  Null rows and bytes past the row's K / 32
+// scales give 0, a finite scale, whatever the padding holds.
+__device__ __forceinline__ uint4 load_scales(const unsigned char* row, int pair, const ExpertsArgs& a) {
+  const int at = 16 * pair, left = a.K / 32 - at;
+  uint4 q = make_uint4(0u, 0u, 0u, 0u);
+  if (row == nullptr || left <= 0) return q;
+  if (a.wide_scales) {
+    q = __ldg(reinterpret_cast<const uint4*>(row + at));
+  } else {
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(row + at);
+    q.x = __ldg(p);
+    if (left > 4) q.y = __ldg(p + 1);
+    if (left > 8) q.z = __ldg(p + 2);
+    if (left > 12) q.w = __ldg(p + 3);
   }
-#pragma unroll
-  for (int g = 0; g < 2; ++g) q[g] = make_uint4(w[g][0], w[g][1], w[g][2], w[g][3]);
+  if (left < 16) {
+    auto keep = [&](uint32_t w, int n) {
+      return n >= 4 ? w : (n <= 0 ? 0u : w & ((1u << (8 * n)) - 1u));
+    };
+    q = make_uint4(keep(q.x, left), keep(q.y, left - 4), keep(q.z, left - 8), keep(q.w, left - 12));
+  }
+  return q;
 }
 
-template <int BN, class Out>
+__device__ __forceinline__ void store_shared(uint32_t dst, uint32_t v) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst), "r"(v) : "memory");
+}
+
+// Where the scales of row r of 128 start in a step's 512 bytes.
+__device__ __forceinline__ uint32_t scale_place(int r) { return 16 * (r & 31) + 4 * (r >> 5); }
+
+template <class Out>
 __global__ void __launch_bounds__(kExpThreads, 1)
-    mrs_experts_kernel(const __grid_constant__ CUtensorMap wmap,
-                       const __grid_constant__ CUtensorMap xmap, const ExpertsArgs a) {
-  using St = ExpertsStage<BN>;
-  constexpr int S = St::kStages;
+    mrs_experts_kernel(const __grid_constant__ CUtensorMap wmap, const ExpertsArgs a) {
   extern __shared__ unsigned char smem_raw[];
-  __shared__ unsigned long long full_s[S], scaled_s[S], empty_s[S], acc_full_s[2], acc_free_s[2],
+  __shared__ unsigned long long full_s[kStages], empty_s[kStages], acc_full_s[2], acc_free_s[2],
       done_s;
   __shared__ uint32_t tmem_s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -121,9 +129,8 @@ __global__ void __launch_bounds__(kExpThreads, 1)
   const unsigned long long limit = a.wait_limit_ns;
   pdl_trigger();
   if (tid == 0) {
-    for (int s = 0; s < S; ++s) {
-      mbar_init(&full_s[s], 1);
-      mbar_init(&scaled_s[s], 2);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full_s[s], 1 + 2 + 4);  // the weights' copy, their scales, the rows
       mbar_init(&empty_s[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -141,189 +148,285 @@ __global__ void __launch_bounds__(kExpThreads, 1)
   pdl_wait();
 
   const int rows = min(max(__ldg(a.npp), 0), a.max_rows);
-  const long long tiles = static_cast<long long>(rows / a.B) * a.subs * a.ntile;
-  ExpertsTile t;
+  const int tiles = rows / a.B * a.subs * a.ntile;
+  const int step = gridDim.x;
   bool ok = true;
   int stage = 0;
   uint32_t phase = 0;  // parity of the ring's current round
   auto advance = [&] {
-    if (++stage == S) {
+    if (++stage == kStages) {
       stage = 0;
       phase ^= 1u;
     }
   };
+  ExpertsTile t, n;
+  t.at(a, blockIdx.x, tiles);
 
   if (warp == 0) {
-    long long issued = 0;
-    for (long long it = blockIdx.x; ok && it < tiles; it += gridDim.x) {
-      if (!experts_tile(a, it, t)) {
-        if (lane == 0) atomicOr(a.status, MOE_RS_DEVICE_BAD_EXPERT_ID);
-        continue;
-      }
-      int row[4] = {0, 0, 0, 0};  // rows that are no route read row 0, and are not stored
-      if (4 * lane < BN) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int r = experts_route(a, t, 4 * lane + j);
-          row[j] = r < 0 ? 0 : (a.per_route ? r : r / a.topk);
+    if (lane == 0) {
+      long long issued = 0;
+      for (; ok && t.it < tiles; t = n) {
+        n.at(a, t.it + step, tiles);
+        if (!t.valid(a)) {
+          atomicOr(a.status, MOE_RS_DEVICE_BAD_EXPERT_ID);
+          continue;
+        }
+        for (int ks = 0; ks < a.ksteps; ++ks) {
+          ok = thread_wait(&empty_s[stage], phase ^ 1u, limit);
+          if (!ok) break;
+          mbar_expect(&full_s[stage], kWBytes);
+          tma_load_3d(base + stage * kStageBytes + kXBytes, &wmap, ks * kStepBytes, t.n0, t.e,
+                      &full_s[stage]);
+          ++issued;
+          advance();
         }
       }
-      for (int ks = 0; ks < a.ksteps; ++ks) {
-        ok = mbar_wait_bounded(&empty_s[stage], phase ^ 1u, limit);
-        if (!ok) break;
-        const uint32_t dst = base + stage * St::kBytes;
-        if (lane == 0) {
-          mbar_expect(&full_s[stage], St::kA + St::kB);
-          tma_load_3d(dst, &wmap, ks * kStepBytes, t.n0, t.e, &full_s[stage]);
-        }
-        __syncwarp();
-        if (4 * lane < BN)
-          tma_gather4(dst + St::kA + lane * 4 * kStepBytes, &xmap, ks * kStepBytes, row[0], row[1],
-                      row[2], row[3], &full_s[stage]);
-        __syncwarp();
-        ++issued;
-        advance();
+      if (!ok) {
+        // a copy still on its way must land before the CTA leaves; the phase it completes may be
+        // missing other arrivals, so this waits for what has no one to take it any more
+        for (long long q = issued > kStages ? issued - kStages : 0; q < issued; ++q)
+          thread_wait(&full_s[q % kStages], static_cast<uint32_t>(q / kStages) & 1u, kWaitLimitNs);
       }
-    }
-    if (!ok) {
-      // copies still on their way must land before the CTA leaves: the last S issued
-      for (long long q = issued > S ? issued - S : 0; q < issued; ++q)
-        mbar_wait_bounded(&full_s[q % S], static_cast<uint32_t>(q / S) & 1u, kWaitLimitNs);
     }
   } else if (warp == 1) {
-    int buf = 0;
-    uint32_t acc_phase = 0;
-    bool any = false;
-    for (long long it = blockIdx.x; ok && it < tiles; it += gridDim.x) {
-      if (!experts_tile(a, it, t)) continue;
-      ok = mbar_wait_bounded(&acc_free_s[buf], acc_phase ^ 1u, limit);
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t d = tmem + buf * BN;
-      for (int ks = 0; ks < a.ksteps; ++ks) {
-        ok = mbar_wait_bounded(&full_s[stage], phase, limit) &&
-             mbar_wait_bounded(&scaled_s[stage], phase, limit);
+    if (lane == 0) {
+      int buf = 0;
+      uint32_t acc_phase = 0;
+      bool any = false;
+      for (; ok && t.it < tiles; t = n) {
+        n.at(a, t.it + step, tiles);
+        if (!t.valid(a)) continue;
+        ok = thread_wait(&acc_free_s[buf], acc_phase ^ 1u, limit);
         if (!ok) break;
         tc_fence_after();
-        if (lane == 0) {
-          const uint32_t src = base + stage * St::kBytes, sc = src + St::kA + St::kB;
-          const uint32_t ts = tmem + 2 * BN + stage * 16;
-          const uint64_t da = desc_rows128(src), db = desc_rows128(src + St::kA);
-          const int parts = min(4, (a.K - 256 * ks + 63) >> 6);
+        const uint32_t d = tmem + buf * kExpOuts;
+        for (int ks = 0; ks < a.ksteps; ++ks) {
+          ok = thread_wait(&full_s[stage], phase, limit);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t src = base + stage * kStageBytes, sc = src + kXBytes + kWBytes;
+          const uint32_t ts = tmem + kTmemScales + stage * 16;
+          const uint64_t dx = desc_rows128(src), dw = desc_rows128(src + kXBytes);
+          const int parts = (a.K - 256 * ks + 63) >> 6;
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
             tc_copy_scales(ts + 4 * g, desc_scales(sc + 512 * g));
             tc_copy_scales(ts + 8 + 4 * g, desc_scales(sc + 1024 + 512 * g));
           }
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            if (q >= parts) break;  // columns past K
-            // 32 bytes further along the swizzled rows: 2 units of 16
-            tc_mma_mxf4(d, da + 2 * q, db + 2 * q, mxf4_word(kExpM, BN, (q & 1) * 2),
-                        ts + 4 * (q >> 1), ts + 8 + 4 * (q >> 1), ks > 0 || q > 0);
-          }
+          for (int q = 0; q < 4; ++q)
+            if (q < parts)  // else columns past K
+              // 32 bytes further along the swizzled rows: 2 units of 16
+              tc_mma_mxf4(d, dx + 2 * q, dw + 2 * q, mxf4_word(kExpRows, kExpOuts, (q & 1) * 2),
+                          ts + 4 * (q >> 1), ts + 8 + 4 * (q >> 1), ks > 0 || q > 0);
           tc_commit(&empty_s[stage]);
-          if (ks + 1 == a.ksteps) tc_commit(&acc_full_s[buf]);
+          any = true;
+          advance();
         }
-        any = true;
-        __syncwarp();
-        advance();
+        if (!ok) break;
+        tc_commit(&acc_full_s[buf]);
+        buf ^= 1;
+        if (buf == 0) acc_phase ^= 1u;
       }
-      buf ^= 1;
-      if (buf == 0) acc_phase ^= 1u;
-    }
-    // nothing of the tensor core may be in flight when tensor memory is given back
-    if (any) {
-      if (lane == 0) tc_commit(&done_s);
-      __syncwarp();
-      mbar_wait_bounded(&done_s, 0, kWaitLimitNs);
+      // nothing of the tensor core may be in flight when tensor memory is given back
+      if (any) {
+        tc_commit(&done_s);
+        thread_wait(&done_s, 0, kWaitLimitNs);
+      }
     }
   } else if (warp < 4) {
-    const bool weights = warp == 2;
-    for (long long it = blockIdx.x; ok && it < tiles; it += gridDim.x) {
-      if (!experts_tile(a, it, t)) continue;
-      const unsigned char* row[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int i = lane + 32 * j;
-        row[j] = nullptr;
-        if (weights) {
-          if (t.n0 + i < a.N)
-            row[j] = a.ws + (static_cast<size_t>(t.e) * a.N + t.n0 + i) * a.scols;
-        } else if (i < BN) {
-          const int r = experts_route(a, t, i);
-          if (r >= 0) row[j] = a.xs + static_cast<size_t>(a.per_route ? r : r / a.topk) * a.scols;
-        }
-      }
-      uint4 q[kScalePrefetch][2], n[kScalePrefetch][2];
-#pragma unroll
-      for (int c = 0; c < kScalePrefetch; ++c) load_scales(row, c, a.K / 32, n[c]);
-      for (int k0 = 0; ok && k0 < a.ksteps; k0 += kScalePrefetch) {
-#pragma unroll
-        for (int c = 0; c < kScalePrefetch; ++c) {
-          q[c][0] = n[c][0];
-          q[c][1] = n[c][1];
-          load_scales(row, k0 + kScalePrefetch + c, a.K / 32, n[c]);
-        }
-#pragma unroll
-        for (int c = 0; c < kScalePrefetch; ++c) {
-          if (k0 + c >= a.ksteps) break;
-          ok = mbar_wait_bounded(&empty_s[stage], phase ^ 1u, limit);
+    // two rows of weights a thread
+    const int r0 = tid - 64, r1 = r0 + 64;
+    ExpertsTile f;
+    n.at(a, t.it + step, tiles);
+    auto rowp = [&](const ExpertsTile& q, int r) -> const unsigned char* {
+      return q.valid(a) && q.n0 + r < a.N
+                 ? a.ws + (static_cast<size_t>(q.e) * a.N + q.n0 + r) * a.scols
+                 : nullptr;
+    };
+    const unsigned char *p0 = rowp(t, r0), *p1 = rowp(t, r1);
+    uint4 first0 = load_scales(p0, 0, a), first1 = load_scales(p1, 0, a);
+    for (; ok && t.it < tiles; t = n, n = f) {
+      f.at(a, n.it + step, tiles);
+      const unsigned char *n0 = rowp(n, r0), *n1 = rowp(n, r1);
+      uint4 c0, c1, a0 = first0, a1 = first1;
+      uint4 b0 = load_scales(p0, 1, a), b1 = load_scales(p1, 1, a);
+      first0 = load_scales(n0, 0, a);
+      first1 = load_scales(n1, 0, a);
+      if (t.valid(a)) {
+        for (int ks = 0; ks < a.ksteps; ++ks) {
+          if ((ks & 1) == 0) {
+            c0 = a0;
+            c1 = a1;
+            a0 = b0;
+            a1 = b1;
+            b0 = load_scales(p0, ks / 2 + 2, a);
+            b1 = load_scales(p1, ks / 2 + 2, a);
+          } else {
+            c0.x = c0.z;
+            c0.y = c0.w;
+            c1.x = c1.z;
+            c1.y = c1.w;
+          }
+          ok = warp_wait(&empty_s[stage], phase ^ 1u, limit);
           if (!ok) break;
-          const uint32_t dst = base + stage * St::kBytes + St::kA + St::kB + (weights ? 0 : 1024) +
-                               16 * lane;
-#pragma unroll
-          for (int g = 0; g < 2; ++g)
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + 512 * g),
-                         "r"(q[c][g].x), "r"(q[c][g].y), "r"(q[c][g].z), "r"(q[c][g].w)
-                         : "memory");
+          const uint32_t dst = base + stage * kStageBytes + kXBytes + kWBytes + 1024;
+          store_shared(dst + scale_place(r0), c0.x);
+          store_shared(dst + 512 + scale_place(r0), c0.y);
+          store_shared(dst + scale_place(r1), c1.x);
+          store_shared(dst + 512 + scale_place(r1), c1.y);
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&scaled_s[stage]);
+          if (lane == 0) mbar_arrive(&full_s[stage]);
           advance();
         }
       }
+      p0 = n0;
+      p1 = n1;
     }
-  } else {
-    const int quarter = warp - 4;
+  } else if (warp < 8) {
+    const int i = 32 * (warp - 4) + lane;  // the thread's row of a tile
+    const bool used = 32 * (warp - 4) < a.sub;
     int buf = 0;
     uint32_t acc_phase = 0;
-    for (long long it = blockIdx.x; ok && it < tiles; it += gridDim.x) {
-      if (!experts_tile(a, it, t)) continue;
-      constexpr int NJ = (BN + 31) / 32;
-      int route[NJ];
-      float weight[NJ];
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        const int i = lane + 32 * j;
-        route[j] = experts_route(a, t, i);
-        weight[j] = (a.sw != nullptr && route[j] >= 0) ? __ldg(a.sw + t.p0 + i) : 1.0f;
-      }
-      ok = mbar_wait_bounded(&acc_full_s[buf], acc_phase, limit);
+    int entry = t.entry(a, i, tiles);
+    for (; ok && t.it < tiles; t = n) {
+      n.at(a, t.it + step, tiles);
+      const int r = entry;
+      entry = n.entry(a, i, tiles);
+      if (!t.valid(a)) continue;
+      const bool put = r >= 0 && r < a.routes;
+      const float w = (a.sw != nullptr && put) ? __ldg(a.sw + t.p0 + i) : 1.0f;
+      ok = warp_wait(&acc_full_s[buf], acc_phase, limit);
       if (!ok) break;
-      tc_fence_after();
-      const int n = t.n0 + 32 * quarter + lane;
-      const uint32_t src = tmem + buf * BN + (static_cast<uint32_t>(32 * quarter) << 16);
+      if (used) {
+        tc_fence_after();
+        const uint32_t src = tmem + buf * kExpOuts + (static_cast<uint32_t>(32 * (warp - 4)) << 16);
+        Out* out = static_cast<Out*>(a.out) + (put ? static_cast<size_t>(r) * a.N : 0) + t.n0;
+        const int left = a.N - t.n0;  // a multiple of 8
 #pragma unroll
-      for (int c0 = 0; c0 < BN; c0 += 16) {
-        float v[16];
-        tmem_load16(src + c0, v);
+        for (int c0 = 0; c0 < kExpOuts; c0 += 32) {
+          uint32_t v[32];
+          tmem_load32(src + c0, v);
+          if constexpr (sizeof(Out) == 4) {
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          const int r = __shfl_sync(kFull, route[(c0 + c) >> 5], (c0 + c) & 31);
-          const float w = __shfl_sync(kFull, weight[(c0 + c) >> 5], (c0 + c) & 31);
-          if (r < 0 || n >= a.N) continue;
-          Out* o = static_cast<Out*>(a.out) + static_cast<size_t>(r) * a.N + n;
-          if constexpr (sizeof(Out) == 4) *o = w * v[c];
-          else *o = __float2bfloat16_rn(w * v[c]);
+            for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(w * __uint_as_float(v[c]));
+          } else {
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              const __nv_bfloat162 h = __floats2bfloat162_rn(w * __uint_as_float(v[2 * c]),
+                                                             w * __uint_as_float(v[2 * c + 1]));
+              v[c] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+          }
+          constexpr int kPer = 32 / sizeof(Out);  // outputs of 32 bytes
+#pragma unroll
+          for (int c = 0; put && c < 32 / kPer; ++c) {
+            const int at = c0 + kPer * c;
+            const uint32_t* q = v + 8 * c;
+            void* o = out + at;
+            if (a.wide_out && at + kPer <= left) {
+              asm volatile(
+                  "st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(o), "r"(q[0]),
+                  "r"(q[1]), "r"(q[2]), "r"(q[3]), "r"(q[4]), "r"(q[5]), "r"(q[6]), "r"(q[7])
+                  : "memory");
+            } else {
+              uint4* o4 = static_cast<uint4*>(o);
+              if (at + kPer / 2 <= left) o4[0] = make_uint4(q[0], q[1], q[2], q[3]);
+              if (at + kPer <= left) o4[1] = make_uint4(q[4], q[5], q[6], q[7]);
+            }
+          }
+          __syncwarp();
         }
+        tc_fence_before();
       }
-      tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&acc_free_s[buf]);
       buf ^= 1;
       if (buf == 0) acc_phase ^= 1u;
     }
+  } else {
+    // warp w copies rows 32 w .. 32 w + 31 of the block, four rows (8 lanes each) at a time; a lane
+    // knows the row that its scales come from
+    const int w32 = 32 * (warp - 8), i = w32 + lane;
+    const int mine = min(max(a.sub - w32, 0), 32);  // rows of this warp
+    const int chunk = lane & 7, sub4 = lane >> 3;
+    ExpertsTile f;
+    n.at(a, t.it + step, tiles);
+    auto source = [&](const ExpertsTile& q, int entry) -> int {
+      if (!q.valid(a) || entry < 0 || entry >= a.routes) return -1;
+      return a.per_route ? entry : entry / a.topk;
+    };
+    auto rowp = [&](int src) -> const unsigned char* {
+      return src < 0 ? nullptr : a.xs + static_cast<size_t>(src) * a.scols;
+    };
+    int src = source(t, t.entry(a, i, tiles)), entry_n = n.entry(a, i, tiles);
+    const unsigned char* p = rowp(src);
+    uint4 first = load_scales(p, 0, a);
+    const size_t half = static_cast<size_t>(a.K / 2);
+    int opened = 0;        // steps in flight
+    int tail = 0;          // stage of the oldest of them
+    auto close_oldest = [&] {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full_s[tail]);
+      if (++tail == kStages) tail = 0;
+      --opened;
+    };
+    for (; ok && t.it < tiles; t = n, n = f) {
+      f.at(a, n.it + step, tiles);
+      const int entry_f = f.entry(a, i, tiles);
+      const int src_n = source(n, entry_n);
+      entry_n = entry_f;
+      const unsigned char* pn = rowp(src_n);
+      uint4 cur, nx = first, nn = load_scales(p, 1, a);
+      first = load_scales(pn, 0, a);
+      if (t.valid(a)) {
+        // the 8 x 4 rows that this lane copies a chunk of
+        const unsigned char* from[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int s = __shfl_sync(kFull, src, 4 * j + sub4);
+          from[j] = s < 0 ? nullptr : a.xc + static_cast<size_t>(s) * half + 16 * chunk;
+        }
+        for (int ks = 0; ks < a.ksteps; ++ks) {
+          if ((ks & 1) == 0) {
+            cur = nx;
+            nx = nn;
+            nn = load_scales(p, ks / 2 + 2, a);
+          } else {
+            cur.x = cur.z;
+            cur.y = cur.w;
+          }
+          ok = warp_wait(&empty_s[stage], phase ^ 1u, limit);
+          if (!ok) break;
+          const uint32_t dst = base + stage * kStageBytes;
+          const bool in = ks * kStepBytes + 16 * chunk < a.K / 2;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            if (4 * j >= mine) break;
+            const int r = w32 + 4 * j + sub4;
+            const uint32_t to = dst + r * kStepBytes + 16 * (chunk ^ (r & 7));
+            // (rows that are no route and columns past K keep what was there: any codes, times
+            // finite scales, in rows that are not stored or against weights that read as zero)
+            if (from[j] != nullptr && in) copy16(to, from[j] + static_cast<size_t>(ks) * kStepBytes);
+          }
+          const uint32_t sc = dst + kXBytes + kWBytes + scale_place(i);
+          store_shared(sc, cur.x);
+          store_shared(sc + 512, cur.y);
+          copy_close();
+          if (++opened == kCopyDepth) {
+            copy_wait<kCopyDepth - 1>();
+            close_oldest();
+          }
+          advance();
+        }
+      }
+      src = src_n;
+      p = pn;
+    }
+    copy_wait<0>();
+    while (opened > 0) close_oldest();
   }
   if (!ok && lane == 0) atomicOr(a.status, MOE_RS_DEVICE_WAIT_TIMEOUT);
   tc_fence_before();
@@ -355,35 +458,31 @@ EncodeFn encode_fn() {
   return fn;
 }
 
-// Bytes in rows of `row` bytes, `n1` rows a matrix, `n2` matrices; the copied box is 128 bytes of
-// `box1` rows of one matrix.
-bool encode_rows(CUtensorMap* map, const void* p, size_t row, size_t n1, size_t n2, int box1,
-                 int rank) {
+// The weights: `outs` rows of `row` bytes for each of E experts; the copied box is 128 bytes of
+// 128 rows of one expert (rows past the last and bytes past the row's end read as zero).
+bool encode_weights(CUtensorMap* map, const void* p, size_t row, size_t outs, size_t E) {
   const EncodeFn fn = encode_fn();
   if (fn == nullptr) return false;
-  const cuuint64_t dims[3] = {row, n1, n2};
-  const cuuint64_t strides[2] = {row, row * n1};
-  const cuuint32_t box[3] = {kStepBytes, static_cast<cuuint32_t>(box1), 1};
+  const cuuint64_t dims[3] = {row, outs, E};
+  const cuuint64_t strides[2] = {row, row * outs};
+  const cuuint32_t box[3] = {kStepBytes, kExpOuts, 1};
   const cuuint32_t one[3] = {1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, static_cast<cuuint32_t>(rank),
-            const_cast<void*>(p), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(p), dims, strides, box, one,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BN, class Out>
-cudaError_t launch_experts(const CUtensorMap& wmap, const CUtensorMap& xmap, const ExpertsArgs& a,
-                           int grid, cudaStream_t st) {
-  auto* k = mrs_experts_kernel<BN, Out>;
-  const size_t smem = ExpertsStage<BN>::kSmem;
-  const cudaError_t err =
-      cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+template <class Out>
+cudaError_t launch_experts(const CUtensorMap& wmap, const ExpertsArgs& a, int grid,
+                           cudaStream_t st) {
+  auto* k = mrs_experts_kernel<Out>;
+  const cudaError_t err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(kExpSmem));
   if (err != cudaSuccess) return err;
-  return launch_pdl(k, dim3(grid), dim3(kExpThreads), smem, st, wmap, xmap, a);
+  return launch_pdl(k, dim3(grid), dim3(kExpThreads), kExpSmem, st, wmap, a);
 }
 
 }  // namespace
-
 }  // namespace mrs
 
 using namespace mrs;
@@ -440,11 +539,17 @@ int moe_experts_mxfp4(const uint8_t* x_codes, const uint8_t* x_scales, int x_per
                       span(expert_ids, 4 * (P / block_m)),
                       span(num_tokens_post_pad, 4)};
   if (any_alias(outs_s, 2, ins, 8)) return MOE_RS_ERR_ALIAS;
+  const bool f32 = out_dtype == MOE_RS_FP32;
+  const int64_t tiles = static_cast<int64_t>(P / block_m) *
+                        ((block_m + kExpRows - 1) / kExpRows) *
+                        ((outs + kExpOuts - 1) / kExpOuts);
+  if (tiles > INT32_MAX / 2) return MOE_RS_ERR_OVERFLOW;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return launch_status(cudaErrorInvalidDevice);
   ExpertsArgs a{};
+  a.xc = x_codes;
   a.xs = x_scales;
   a.ws = w_scales;
   a.sid = sorted_token_ids;
@@ -463,28 +568,17 @@ int moe_experts_mxfp4(const uint8_t* x_codes, const uint8_t* x_scales, int x_per
   a.scols = scols;
   a.max_rows = static_cast<int>(P);
   a.wait_limit_ns = debug_wait_limit_ns();
-  const int bn = block_m <= 16 ? 16 : (block_m >= 128 ? 128 : block_m);
-  a.sub = block_m < bn ? block_m : bn;
+  a.sub = block_m < kExpRows ? block_m : kExpRows;
   a.subs = block_m / a.sub;
-  a.ntile = (outs + kExpM - 1) / kExpM;
+  a.ntile = (outs + kExpOuts - 1) / kExpOuts;
   a.ksteps = (cols + 255) / 256;
-  CUtensorMap wmap, xmap;
-  if (!encode_rows(&wmap, w_codes, cols / 2, outs, E, kExpM, 3) ||
-      !encode_rows(&xmap, x_codes, cols / 2, xrows, 1, 1, 2))
-    return MOE_RS_ERR_LAUNCH;
-  const int64_t tiles = static_cast<int64_t>(P / block_m) * a.subs * a.ntile;
+  a.wide_scales = scols % 16 == 0 && aligned(x_scales, 16) && aligned(w_scales, 16);
+  a.wide_out = aligned(out, 32) && outs * (f32 ? 4 : 2) % 32 == 0;
+  CUtensorMap wmap;
+  if (!encode_weights(&wmap, w_codes, cols / 2, outs, E)) return MOE_RS_ERR_LAUNCH;
   const int grid = tiles < sms ? static_cast<int>(tiles) : sms;
-  const bool f32 = out_dtype == MOE_RS_FP32;
-  auto go = [&](auto n) {
-    constexpr int BN = decltype(n)::value;
-    return f32 ? launch_experts<BN, float>(wmap, xmap, a, grid, stream)
-               : launch_experts<BN, __nv_bfloat16>(wmap, xmap, a, grid, stream);
-  };
-  using std::integral_constant;
-  return launch_status(bn == 16   ? go(integral_constant<int, 16>{})
-                       : bn == 32 ? go(integral_constant<int, 32>{})
-                       : bn == 64 ? go(integral_constant<int, 64>{})
-                                  : go(integral_constant<int, 128>{}));
+  return launch_status(f32 ? launch_experts<float>(wmap, a, grid, stream)
+                           : launch_experts<__nv_bfloat16>(wmap, a, grid, stream));
 }
 
 }  // extern "C"

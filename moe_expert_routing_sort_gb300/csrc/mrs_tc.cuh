@@ -29,19 +29,19 @@ __device__ __forceinline__ void tc_fence_before() {
 __device__ __forceinline__ void tc_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
-// 32 lanes (the warp's quarter of tensor memory) x 16 columns of 32 bits.
-__device__ __forceinline__ void tmem_load16(uint32_t addr, float (&v)[16]) {
-  uint32_t r[16];
+// 32 lanes (the warp's quarter of tensor memory) x 32 columns of 32 bits.
+__device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t (&r)[32]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-      "%12, %13, %14, %15}, [%16];"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+      "%30, %31}, [%32];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
         "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(addr));
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 // -------------------------------------------------------------------------- descriptors
@@ -86,6 +86,37 @@ __device__ __forceinline__ void tc_commit(unsigned long long* mbar) {
       : "memory");
 }
 
+// Wait of one thread for phase `phase` of `mbar`, at most about `limit_ns` (0: report a timeout at
+// once without looking, a test hook).  The clock is only asked every 64 looks.
+__device__ __forceinline__ bool thread_wait(unsigned long long* mbar, uint32_t phase,
+                                            unsigned long long limit_ns) {
+  if (limit_ns == 0ull) return false;
+  unsigned long long t0 = 0ull;
+  for (uint32_t i = 1; !mbar_try_wait(mbar, phase); ++i) {
+    if ((i & 63u) != 0u) continue;
+    const unsigned long long t = globaltimer_ns();
+    if (t0 == 0ull) t0 = t;
+    else if (t - t0 > limit_ns) return false;
+  }
+  return true;
+}
+// The same for a whole warp: every lane looks (each gets the acquire), the answer is uniform.
+__device__ __forceinline__ bool warp_wait(unsigned long long* mbar, uint32_t phase,
+                                          unsigned long long limit_ns) {
+  return __all_sync(kFull, thread_wait(mbar, phase, limit_ns));
+}
+
+// ------------------------------------------------------------------------- thread copies
+// 16 bytes from global to shared memory, in the background.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_close() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
 // ------------------------------------------------------------------------- tensor copies
 __device__ __forceinline__ void mbar_arrive(unsigned long long* mbar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(mbar)) : "memory");
@@ -103,14 +134,4 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       "l"(map), "r"(smem_u32(mbar)), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
-// Four rows by index (the map's box is one row high), one behind another.
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, int x, int y0,
-                                            int y1, int y2, int y3, unsigned long long* mbar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
-      "l"(map), "r"(smem_u32(mbar)), "r"(x), "r"(y0), "r"(y1), "r"(y2), "r"(y3)
-      : "memory");
-}
-
 }  // namespace mrs
