@@ -14,17 +14,18 @@
 // tiles round robin, the output tiles of a block next to each other, so the SMs share a block's
 // rows and an expert's weights in L2.  Steps of 256 columns (128 bytes a row) go through a ring of
 // shared-memory stages; the warps of a CTA each have one task:
-//   0      one thread copies the weights' 128 rows (a tensor copy, in the 128-byte swizzle that
+//   0      copies the weights' 128 rows (a tensor copy, in the 128-byte swizzle that
 //          the tensor core reads)
-//   1      one thread copies the step's scales to tensor memory and issues four products of 64
+//   1      copies the step's scales to tensor memory and issues four products of 64
 //          columns; the tensor core applies the scales and adds into fp32 in tensor memory
-//   2, 3   the weights' scales, from row-major bytes to the order that tensor memory wants (row
-//          r of 128: lane r % 32, word r / 32 of 4 scales)
 //   4-7    a finished tile from tensor memory to the output rows, while the next one is computed
 //          (two accumulators)
-//   8-11   the block's rows, 16 bytes a thread into the same swizzle, four steps in flight, with
-//          their scales.  (Gathered by tensor copies of four rows each they took 37 ns a copy:
-//          1.2 us a step of 128 rows, against 0.14 us of products.)
+//   8-11   the block's rows, 16 bytes a thread into the same swizzle; the copies arrive on the
+//          stage's barrier themselves, so the whole ring is in flight.  (Gathered by tensor copies
+//          of four rows each they took 37 ns a copy: 1.2 us a step of 128 rows, against 0.14 us
+//          of products.)
+//   12-15  the scales of rows and weights, from row-major bytes to the order that tensor memory
+//          wants (row r of 128: lane r % 32, word r / 32 of 4 scales)
 // Each task has the list entries of the next two tiles and the first scales of the next one in
 // flight, so a tile of two steps does not wait for them.  Every wait is bounded; a wait that gives
 // up ends its warp's task with the status bit set, and the CTA leaves once nothing of its own is
@@ -55,7 +56,7 @@ struct ExpertsArgs {
   int wide_out;    // output rows start on 32 bytes
 };
 
-constexpr int kExpThreads = 384;
+constexpr int kExpThreads = 512;  // warps 2 and 3 only fill the quarter of the epilogue's lanes
 constexpr int kExpRows = 128;      // lanes of a tile: rows of a block
 constexpr int kExpOuts = 128;      // outputs of a tile
 constexpr int kStepBytes = 128;    // bytes of a row per step
@@ -64,7 +65,6 @@ constexpr int kWBytes = kExpOuts * kStepBytes;
 constexpr int kScaleBytes = 2048;  // rows' and weights' scales of a step: 2 x 2 x 512
 constexpr int kStageBytes = kXBytes + kWBytes + kScaleBytes;
 constexpr int kStages = 6;         // what fits in 227 KB
-constexpr int kCopyDepth = 4;      // steps of rows in flight
 constexpr size_t kExpSmem = static_cast<size_t>(kStages) * kStageBytes + 1024;
 constexpr int kTmemCols = 512;     // 2 accumulators of 128 columns, 16 of scales per stage
 constexpr int kTmemScales = 2 * kExpOuts;
@@ -86,28 +86,25 @@ struct ExpertsTile {
   }
 };
 
-// Scales of one row, 16 bytes (two steps) at a time.  Null rows and bytes past the row's K / 32
-// scales give 0, a finite scale, whatever the padding holds.
+// Scales of one row, 16 bytes (two steps) at a time; zeros past the row's end and for null rows.
+// Nothing here looks at what it loads: a use would wait for it.
 __device__ __forceinline__ uint4 load_scales(const unsigned char* row, int pair, const ExpertsArgs& a) {
   const int at = 16 * pair, left = a.K / 32 - at;
   uint4 q = make_uint4(0u, 0u, 0u, 0u);
   if (row == nullptr || left <= 0) return q;
-  if (a.wide_scales) {
-    q = __ldg(reinterpret_cast<const uint4*>(row + at));
-  } else {
-    const uint32_t* p = reinterpret_cast<const uint32_t*>(row + at);
-    q.x = __ldg(p);
-    if (left > 4) q.y = __ldg(p + 1);
-    if (left > 8) q.z = __ldg(p + 2);
-    if (left > 12) q.w = __ldg(p + 3);
-  }
-  if (left < 16) {
-    auto keep = [&](uint32_t w, int n) {
-      return n >= 4 ? w : (n <= 0 ? 0u : w & ((1u << (8 * n)) - 1u));
-    };
-    q = make_uint4(keep(q.x, left), keep(q.y, left - 4), keep(q.z, left - 8), keep(q.w, left - 12));
-  }
+  if (a.wide_scales) return __ldg(reinterpret_cast<const uint4*>(row + at));
+  const uint32_t* p = reinterpret_cast<const uint32_t*>(row + at);
+  q.x = __ldg(p);
+  if (left > 4) q.y = __ldg(p + 1);
+  if (left > 8) q.z = __ldg(p + 2);
+  if (left > 12) q.w = __ldg(p + 3);
   return q;
+}
+
+// The first `left` bytes of four scales: what lies behind a row's K / 32 scales is padding, and
+// its columns' products of zeros have to meet a finite scale.
+__device__ __forceinline__ uint32_t keep_scales(uint32_t w, int left) {
+  return left >= 4 ? w : (left <= 0 ? 0u : w & ((1u << (8 * left)) - 1u));
 }
 
 __device__ __forceinline__ void store_shared(uint32_t dst, uint32_t v) {
@@ -130,7 +127,8 @@ __global__ void __launch_bounds__(kExpThreads, 1)
   pdl_trigger();
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&full_s[s], 1 + 2 + 4);  // the weights' copy, their scales, the rows
+      // the weights' copy, the scales' four warps, the threads of the warps that copy rows
+      mbar_init(&full_s[s], 1 + 4 + 32 * ((a.sub + 31) / 32));
       mbar_init(&empty_s[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -163,51 +161,53 @@ __global__ void __launch_bounds__(kExpThreads, 1)
   t.at(a, blockIdx.x, tiles);
 
   if (warp == 0) {
-    if (lane == 0) {
-      long long issued = 0;
-      for (; ok && t.it < tiles; t = n) {
-        n.at(a, t.it + step, tiles);
-        if (!t.valid(a)) {
-          atomicOr(a.status, MOE_RS_DEVICE_BAD_EXPERT_ID);
-          continue;
-        }
-        for (int ks = 0; ks < a.ksteps; ++ks) {
-          ok = thread_wait(&empty_s[stage], phase ^ 1u, limit);
-          if (!ok) break;
+    long long issued = 0;
+    for (; ok && t.it < tiles; t = n) {
+      n.at(a, t.it + step, tiles);
+      if (!t.valid(a)) {
+        if (lane == 0) atomicOr(a.status, MOE_RS_DEVICE_BAD_EXPERT_ID);
+        continue;
+      }
+      for (int ks = 0; ks < a.ksteps; ++ks) {
+        ok = warp_wait(&empty_s[stage], phase ^ 1u, limit);
+        if (!ok) break;
+        if (elect_one()) {
           mbar_expect(&full_s[stage], kWBytes);
           tma_load_3d(base + stage * kStageBytes + kXBytes, &wmap, ks * kStepBytes, t.n0, t.e,
                       &full_s[stage]);
-          ++issued;
-          advance();
         }
-      }
-      if (!ok) {
-        // a copy still on its way must land before the CTA leaves; the phase it completes may be
-        // missing other arrivals, so this waits for what has no one to take it any more
-        for (long long q = issued > kStages ? issued - kStages : 0; q < issued; ++q)
-          thread_wait(&full_s[q % kStages], static_cast<uint32_t>(q / kStages) & 1u, kWaitLimitNs);
+        __syncwarp();
+        ++issued;
+        advance();
       }
     }
+    if (!ok) {
+      // a copy still on its way must land before the CTA leaves; the phase it completes may be
+      // missing other arrivals, so this waits for what has no one to take it any more
+      for (long long q = issued > kStages ? issued - kStages : 0; q < issued; ++q)
+        warp_wait(&full_s[q % kStages], static_cast<uint32_t>(q / kStages) & 1u, kWaitLimitNs);
+    }
   } else if (warp == 1) {
-    if (lane == 0) {
-      int buf = 0;
-      uint32_t acc_phase = 0;
-      bool any = false;
-      for (; ok && t.it < tiles; t = n) {
-        n.at(a, t.it + step, tiles);
-        if (!t.valid(a)) continue;
-        ok = thread_wait(&acc_free_s[buf], acc_phase ^ 1u, limit);
+    int buf = 0;
+    uint32_t acc_phase = 0;
+    bool any = false;
+    for (; ok && t.it < tiles; t = n) {
+      n.at(a, t.it + step, tiles);
+      if (!t.valid(a)) continue;
+      ok = warp_wait(&acc_free_s[buf], acc_phase ^ 1u, limit);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t d = tmem + buf * kExpOuts;
+      for (int ks = 0; ks < a.ksteps; ++ks) {
+        ok = warp_wait(&full_s[stage], phase, limit);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t d = tmem + buf * kExpOuts;
-        for (int ks = 0; ks < a.ksteps; ++ks) {
-          ok = thread_wait(&full_s[stage], phase, limit);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t src = base + stage * kStageBytes, sc = src + kXBytes + kWBytes;
-          const uint32_t ts = tmem + kTmemScales + stage * 16;
-          const uint64_t dx = desc_rows128(src), dw = desc_rows128(src + kXBytes);
-          const int parts = (a.K - 256 * ks + 63) >> 6;
+        fence_proxy_async_smem();  // the rows were written by threads
+        const uint32_t src = base + stage * kStageBytes, sc = src + kXBytes + kWBytes;
+        const uint32_t ts = tmem + kTmemScales + stage * 16;
+        const uint64_t dx = desc_rows128(src), dw = desc_rows128(src + kXBytes);
+        const int parts = (a.K - 256 * ks + 63) >> 6;
+        if (elect_one()) {
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
             tc_copy_scales(ts + 4 * g, desc_scales(sc + 512 * g));
@@ -220,71 +220,22 @@ __global__ void __launch_bounds__(kExpThreads, 1)
               tc_mma_mxf4(d, dx + 2 * q, dw + 2 * q, mxf4_word(kExpRows, kExpOuts, (q & 1) * 2),
                           ts + 4 * (q >> 1), ts + 8 + 4 * (q >> 1), ks > 0 || q > 0);
           tc_commit(&empty_s[stage]);
-          any = true;
-          advance();
+          if (ks + 1 == a.ksteps) tc_commit(&acc_full_s[buf]);
         }
-        if (!ok) break;
-        tc_commit(&acc_full_s[buf]);
-        buf ^= 1;
-        if (buf == 0) acc_phase ^= 1u;
+        __syncwarp();
+        any = true;
+        advance();
       }
-      // nothing of the tensor core may be in flight when tensor memory is given back
-      if (any) {
-        tc_commit(&done_s);
-        thread_wait(&done_s, 0, kWaitLimitNs);
-      }
+      buf ^= 1;
+      if (buf == 0) acc_phase ^= 1u;
     }
-  } else if (warp < 4) {
-    // two rows of weights a thread
-    const int r0 = tid - 64, r1 = r0 + 64;
-    ExpertsTile f;
-    n.at(a, t.it + step, tiles);
-    auto rowp = [&](const ExpertsTile& q, int r) -> const unsigned char* {
-      return q.valid(a) && q.n0 + r < a.N
-                 ? a.ws + (static_cast<size_t>(q.e) * a.N + q.n0 + r) * a.scols
-                 : nullptr;
-    };
-    const unsigned char *p0 = rowp(t, r0), *p1 = rowp(t, r1);
-    uint4 first0 = load_scales(p0, 0, a), first1 = load_scales(p1, 0, a);
-    for (; ok && t.it < tiles; t = n, n = f) {
-      f.at(a, n.it + step, tiles);
-      const unsigned char *n0 = rowp(n, r0), *n1 = rowp(n, r1);
-      uint4 c0, c1, a0 = first0, a1 = first1;
-      uint4 b0 = load_scales(p0, 1, a), b1 = load_scales(p1, 1, a);
-      first0 = load_scales(n0, 0, a);
-      first1 = load_scales(n1, 0, a);
-      if (t.valid(a)) {
-        for (int ks = 0; ks < a.ksteps; ++ks) {
-          if ((ks & 1) == 0) {
-            c0 = a0;
-            c1 = a1;
-            a0 = b0;
-            a1 = b1;
-            b0 = load_scales(p0, ks / 2 + 2, a);
-            b1 = load_scales(p1, ks / 2 + 2, a);
-          } else {
-            c0.x = c0.z;
-            c0.y = c0.w;
-            c1.x = c1.z;
-            c1.y = c1.w;
-          }
-          ok = warp_wait(&empty_s[stage], phase ^ 1u, limit);
-          if (!ok) break;
-          const uint32_t dst = base + stage * kStageBytes + kXBytes + kWBytes + 1024;
-          store_shared(dst + scale_place(r0), c0.x);
-          store_shared(dst + 512 + scale_place(r0), c0.y);
-          store_shared(dst + scale_place(r1), c1.x);
-          store_shared(dst + 512 + scale_place(r1), c1.y);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&full_s[stage]);
-          advance();
-        }
-      }
-      p0 = n0;
-      p1 = n1;
+    // nothing of the tensor core may be in flight when tensor memory is given back
+    if (any) {
+      if (elect_one()) tc_commit(&done_s);
+      __syncwarp();
+      warp_wait(&done_s, 0, kWaitLimitNs);
     }
-  } else if (warp < 8) {
+  } else if (warp >= 4 && warp < 8) {
     const int i = 32 * (warp - 4) + lane;  // the thread's row of a tile
     const bool used = 32 * (warp - 4) < a.sub;
     int buf = 0;
@@ -345,88 +296,114 @@ __global__ void __launch_bounds__(kExpThreads, 1)
       buf ^= 1;
       if (buf == 0) acc_phase ^= 1u;
     }
-  } else {
-    // warp w copies rows 32 w .. 32 w + 31 of the block, four rows (8 lanes each) at a time; a lane
-    // knows the row that its scales come from
-    const int w32 = 32 * (warp - 8), i = w32 + lane;
-    const int mine = min(max(a.sub - w32, 0), 32);  // rows of this warp
+  } else if (warp >= 8 && warp < 12) {
+    // warp w copies rows 32 w .. 32 w + 31 of the block, four rows (8 lanes each) at a time
+    const int w32 = 32 * (warp - 8);
+    const int mine = min(a.sub - w32, 32);  // rows of this warp
     const int chunk = lane & 7, sub4 = lane >> 3;
-    ExpertsTile f;
-    n.at(a, t.it + step, tiles);
-    auto source = [&](const ExpertsTile& q, int entry) -> int {
-      if (!q.valid(a) || entry < 0 || entry >= a.routes) return -1;
-      return a.per_route ? entry : entry / a.topk;
-    };
-    auto rowp = [&](int src) -> const unsigned char* {
-      return src < 0 ? nullptr : a.xs + static_cast<size_t>(src) * a.scols;
-    };
-    int src = source(t, t.entry(a, i, tiles)), entry_n = n.entry(a, i, tiles);
-    const unsigned char* p = rowp(src);
-    uint4 first = load_scales(p, 0, a);
     const size_t half = static_cast<size_t>(a.K / 2);
-    int opened = 0;        // steps in flight
-    int tail = 0;          // stage of the oldest of them
-    auto close_oldest = [&] {
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&full_s[tail]);
-      if (++tail == kStages) tail = 0;
-      --opened;
-    };
-    for (; ok && t.it < tiles; t = n, n = f) {
-      f.at(a, n.it + step, tiles);
-      const int entry_f = f.entry(a, i, tiles);
-      const int src_n = source(n, entry_n);
-      entry_n = entry_f;
-      const unsigned char* pn = rowp(src_n);
-      uint4 cur, nx = first, nn = load_scales(p, 1, a);
-      first = load_scales(pn, 0, a);
-      if (t.valid(a)) {
-        // the 8 x 4 rows that this lane copies a chunk of
+    // row 4 j + sub4 of the warp: two swizzles, for even and odd j
+    const uint32_t place = (w32 + sub4) * kStepBytes;
+    const uint32_t even = place + 16 * (chunk ^ sub4), odd = place + 16 * (chunk ^ (sub4 + 4));
+    if (mine > 0) {
+      int entry = t.entry(a, w32 + lane, tiles);
+      for (; ok && t.it < tiles; t = n) {
+        n.at(a, t.it + step, tiles);
+        const int r = entry;
+        entry = n.entry(a, w32 + lane, tiles);
+        if (!t.valid(a)) continue;
+        const int src = r >= 0 && r < a.routes ? (a.per_route ? r : r / a.topk) : -1;
+        // rows that are no route keep what was there: any codes, in rows that are not stored
         const unsigned char* from[8];
+        unsigned has = 0u;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const int s = __shfl_sync(kFull, src, 4 * j + sub4);
-          from[j] = s < 0 ? nullptr : a.xc + static_cast<size_t>(s) * half + 16 * chunk;
+          from[j] = a.xc + static_cast<size_t>(max(s, 0)) * half + 16 * chunk;
+          has |= s >= 0 ? 1u << j : 0u;
         }
         for (int ks = 0; ks < a.ksteps; ++ks) {
-          if ((ks & 1) == 0) {
-            cur = nx;
-            nx = nn;
-            nn = load_scales(p, ks / 2 + 2, a);
-          } else {
-            cur.x = cur.z;
-            cur.y = cur.w;
-          }
           ok = warp_wait(&empty_s[stage], phase ^ 1u, limit);
           if (!ok) break;
           const uint32_t dst = base + stage * kStageBytes;
-          const bool in = ks * kStepBytes + 16 * chunk < a.K / 2;
+          // (columns past K keep what was there too: they meet weights that read as zero)
+          const unsigned live = ks * kStepBytes + 16 * chunk < a.K / 2 ? has : 0u;
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             if (4 * j >= mine) break;
-            const int r = w32 + 4 * j + sub4;
-            const uint32_t to = dst + r * kStepBytes + 16 * (chunk ^ (r & 7));
-            // (rows that are no route and columns past K keep what was there: any codes, times
-            // finite scales, in rows that are not stored or against weights that read as zero)
-            if (from[j] != nullptr && in) copy16(to, from[j] + static_cast<size_t>(ks) * kStepBytes);
+            if ((live >> j) & 1u) copy16(dst + ((j & 1) ? odd : even) + 512 * j, from[j]);
+            from[j] += kStepBytes;
           }
-          const uint32_t sc = dst + kXBytes + kWBytes + scale_place(i);
-          store_shared(sc, cur.x);
-          store_shared(sc + 512, cur.y);
-          copy_close();
-          if (++opened == kCopyDepth) {
-            copy_wait<kCopyDepth - 1>();
-            close_oldest();
-          }
+          copy_arrive(&full_s[stage]);
           advance();
         }
       }
-      src = src_n;
-      p = pn;
+      copy_wait_all();
     }
-    copy_wait<0>();
-    while (opened > 0) close_oldest();
+  } else if (warp >= 12) {
+    // a thread has one row of the block and one of the weights
+    const int i = tid - 384;
+    ExpertsTile f;
+    n.at(a, t.it + step, tiles);
+    auto xrow = [&](const ExpertsTile& q, int r) -> const unsigned char* {
+      if (!q.valid(a) || r < 0 || r >= a.routes) return nullptr;
+      return a.xs + static_cast<size_t>(a.per_route ? r : r / a.topk) * a.scols;
+    };
+    auto wrow = [&](const ExpertsTile& q) -> const unsigned char* {
+      return q.valid(a) && q.n0 + i < a.N
+                 ? a.ws + (static_cast<size_t>(q.e) * a.N + q.n0 + i) * a.scols
+                 : nullptr;
+    };
+    const unsigned char *px = xrow(t, t.entry(a, i, tiles)), *pw = wrow(t);
+    int entry = n.entry(a, i, tiles);
+    uint4 firstx = load_scales(px, 0, a), firstw = load_scales(pw, 0, a);
+    const uint32_t place = base + kXBytes + kWBytes + scale_place(i);
+    for (; ok && t.it < tiles; t = n, n = f) {
+      f.at(a, n.it + step, tiles);
+      const unsigned char *nx = xrow(n, entry), *nw = wrow(n);
+      entry = f.entry(a, i, tiles);
+      uint4 cx, cw, ax = firstx, aw = firstw;
+      uint4 bx = load_scales(px, 1, a), bw = load_scales(pw, 1, a);
+      firstx = load_scales(nx, 0, a);
+      firstw = load_scales(nw, 0, a);
+      if (t.valid(a)) {
+        for (int ks = 0; ks < a.ksteps; ++ks) {
+          if ((ks & 1) == 0) {
+            cx = ax;
+            cw = aw;
+            ax = bx;
+            aw = bw;
+            bx = load_scales(px, ks / 2 + 2, a);
+            bw = load_scales(pw, ks / 2 + 2, a);
+          } else {
+            cx.x = cx.z;
+            cx.y = cx.w;
+            cw.x = cw.z;
+            cw.y = cw.w;
+          }
+          ok = warp_wait(&empty_s[stage], phase ^ 1u, limit);
+          if (!ok) break;
+          const uint32_t dst = place + stage * kStageBytes;
+          const int left = a.K / 32 - 8 * ks;
+          if (left < 8) {
+            cx.x = keep_scales(cx.x, left);
+            cx.y = keep_scales(cx.y, left - 4);
+            cw.x = keep_scales(cw.x, left);
+            cw.y = keep_scales(cw.y, left - 4);
+          }
+          store_shared(dst, cx.x);
+          store_shared(dst + 512, cx.y);
+          store_shared(dst + 1024, cw.x);
+          store_shared(dst + 1536, cw.y);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full_s[stage]);
+          advance();
+        }
+      }
+      px = nx;
+      pw = nw;
+    }
   }
   if (!ok && lane == 0) atomicOr(a.status, MOE_RS_DEVICE_WAIT_TIMEOUT);
   tc_fence_before();

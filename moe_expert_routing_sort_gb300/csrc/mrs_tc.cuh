@@ -64,6 +64,14 @@ __device__ __forceinline__ constexpr uint32_t mxf4_word(int M, int N, int id) {
 }
 
 // ------------------------------------------------------------------- one thread issues
+// One lane of a converged warp.  The operands of these instructions are the warp's, not a
+// lane's: behind this choice the compiler knows that one lane acts and keeps them in uniform
+// registers; behind `lane == 0` it does not, and issuing took longer than the products.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(p));
+  return p != 0u;
+}
 // 512 bytes of scales to tensor memory, repeated in its four lane quarters.
 __device__ __forceinline__ void tc_copy_scales(uint32_t tmem, uint64_t desc) {
   asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc)
@@ -111,11 +119,12 @@ __device__ __forceinline__ bool warp_wait(unsigned long long* mbar, uint32_t pha
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void copy_close() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int kLeft>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+// One arrival on the barrier (counted in its expected number) once this thread's copies so far
+// have landed.
+__device__ __forceinline__ void copy_arrive(unsigned long long* mbar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(mbar)) : "memory");
 }
+__device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // ------------------------------------------------------------------------- tensor copies
 __device__ __forceinline__ void mbar_arrive(unsigned long long* mbar) {
