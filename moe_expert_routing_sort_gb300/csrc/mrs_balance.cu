@@ -560,19 +560,16 @@ int check_router(int T, int E, int K, int S) {
   return MOE_RS_OK;
 }
 
-bool sm_count(int& sms) {
-  int dev = 0;
-  return cudaGetDevice(&dev) == cudaSuccess &&
-         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess;
-}
-
 template <int NC, bool kVec>
 cudaError_t launch_balance(const BalanceArgs& a, bool softmax, int ctas, cudaStream_t st) {
   auto* k = softmax ? mrs_balance_rows_kernel<NC, kVec, true>
                     : mrs_balance_rows_kernel<NC, kVec, false>;
   const size_t smem = sizeof(float) * kBalThreads * NC + sizeof(int) * static_cast<size_t>(a.E);
-  cudaError_t err =
-      cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  // with the kernel's own variables just above what every kernel is granted when E is largest
+  static SmemGrant granted[2];
+  const cudaError_t err =
+      grant_smem(reinterpret_cast<const void*>(k),
+                 sizeof(float) * kBalThreads * NC + sizeof(int) * kMaxExperts, granted[softmax]);
   if (err != cudaSuccess) return err;
   return launch_pdl(k, dim3(ctas), dim3(kBalThreads), smem, st, a);
 }
@@ -620,8 +617,8 @@ int moe_balance_loss(const void* logits_bf16, const int32_t* topk_ids, const int
                       span(topk_ids, 4 * static_cast<size_t>(T) * topk),
                       span(seq_offsets, seq_offsets ? 4 * (static_cast<size_t>(n_seq) + 1) : 0)};
   if (any_alias(outs, 4, ins, 3)) return MOE_RS_ERR_ALIAS;
-  int sms = 0;
-  if (!sm_count(sms)) return launch_status(cudaErrorInvalidDevice);
+  const int sms = sm_count();
+  if (sms == 0) return launch_status(cudaErrorInvalidDevice);
   const RowPlan p = row_plan(E);
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   BalanceArgs a{};
@@ -685,8 +682,8 @@ int moe_route_backward(const void* logits_bf16, const int32_t* topk_ids, const f
                       span(counts, counts ? 4 * static_cast<size_t>(n_seq) * E : 0),
                       span(seq_offsets, seq_offsets ? 4 * (static_cast<size_t>(n_seq) + 1) : 0)};
   if (any_alias(outs, 1, ins, 6)) return MOE_RS_ERR_ALIAS;
-  int sms = 0;
-  if (!sm_count(sms)) return launch_status(cudaErrorInvalidDevice);
+  const int sms = sm_count();
+  if (sms == 0) return launch_status(cudaErrorInvalidDevice);
   const RowPlan p = row_plan(E);
   RouteBackwardArgs a{};
   a.logits = static_cast<const uint16_t*>(logits_bf16);

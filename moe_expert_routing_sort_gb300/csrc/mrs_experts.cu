@@ -453,8 +453,8 @@ template <class Out>
 cudaError_t launch_experts(const CUtensorMap& wmap, const ExpertsArgs& a, int grid,
                            cudaStream_t st) {
   auto* k = mrs_experts_kernel<Out>;
-  const cudaError_t err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(kExpSmem));
+  static SmemGrant granted;
+  const cudaError_t err = grant_smem(reinterpret_cast<const void*>(k), kExpSmem, granted);
   if (err != cudaSuccess) return err;
   return launch_pdl(k, dim3(grid), dim3(kExpThreads), kExpSmem, st, wmap, a);
 }
@@ -521,10 +521,8 @@ int moe_experts_mxfp4(const uint8_t* x_codes, const uint8_t* x_scales, int x_per
                         ((block_m + kExpRows - 1) / kExpRows) *
                         ((outs + kExpOuts - 1) / kExpOuts);
   if (tiles > INT32_MAX / 2) return MOE_RS_ERR_OVERFLOW;
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return launch_status(cudaErrorInvalidDevice);
+  const int sms = sm_count();
+  if (sms == 0) return launch_status(cudaErrorInvalidDevice);
   ExpertsArgs a{};
   a.xc = x_codes;
   a.xs = x_scales;

@@ -1,6 +1,7 @@
 // mrs_internal.h -- argument blocks and launchers shared by the C ABI and the kernels.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -306,6 +307,14 @@ cudaError_t launch_small_grid(const SmallArgs& a, cudaStream_t st);
 size_t decode_grid_smem(int E, int T, int K);
 
 // ------------------------------------------------------------ per-context host state
+// SMs of the current device, asked once per device; 0 if the runtime cannot tell.
+int sm_count();
+// Grants `kernel` its dynamic shared memory on the current device, once per context; `g` is a
+// static that belongs to the kernel alone.
+struct SmemGrant {
+  std::atomic<unsigned long long> ctx[64];
+};
+cudaError_t grant_smem(const void* kernel, size_t bytes, SmemGrant& g);
 // Test hooks set through moe_route_sort_debug_set (process-wide).
 unsigned long long debug_wait_limit_ns();  // kWaitLimitNs unless lowered
 // Whether a call of T tokens over E experts (K routes per token, blocks of B rows) takes the

@@ -147,6 +147,22 @@ bool cluster_reach_sort(int T, int E, int K, int B) {
          padded_rows(T, E, K, B) <= kClusterMaxPadded;
 }
 
+int sm_count() {
+  static std::atomic<int> known[64];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) {
+    cudaGetLastError();
+    return 0;
+  }
+  if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
 bool current_context(int& dev, unsigned long long& ctx_id) {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) {
     cudaGetLastError();
@@ -160,6 +176,18 @@ bool current_context(int& dev, unsigned long long& ctx_id) {
     if (f.get_id(ctx, &id) == 0) ctx_id = id + 1;  // 0 stays "unknown"
   }
   return true;
+}
+
+cudaError_t grant_smem(const void* kernel, size_t bytes, SmemGrant& g) {
+  int dev = 0;
+  unsigned long long ctx = 0;
+  if (!current_context(dev, ctx)) return cudaErrorInvalidDevice;
+  const bool known = ctx != 0 && dev < 64;  // a context that cannot be told apart is asked again
+  if (known && g.ctx[dev].load(std::memory_order_acquire) == ctx) return cudaSuccess;
+  const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(bytes));
+  if (err == cudaSuccess && known) g.ctx[dev].store(ctx, std::memory_order_release);
+  return err;
 }
 
 const int32_t* proxy_state_for_launch(cudaStream_t st) {

@@ -6,13 +6,16 @@ metadata, with the quantisation of rows and weights (see include/moe_route_sort.
 """
 from __future__ import annotations
 
-from dataclasses import dataclass
 from typing import Optional
 
 import torch
 
-from .binding import _sort_sizes, load
-from .marshal import DTYPE_CODE, cuda_device, launch, need, rows_of
+from .binding import load
+from .marshal import DTYPE_CODE, Entry, cuda_device, need, rows_of
+
+_quantize = Entry("moe_mxfp4_quantize")
+_dequantize = Entry("moe_mxfp4_dequantize")
+_experts = Entry("moe_experts_mxfp4")
 
 
 def moe_mxfp4_scale_cols(cols: int) -> int:
@@ -23,17 +26,30 @@ def moe_experts_mxfp4_workspace_bytes(T: int, E: int, topk: int, block_m: int) -
     return int(load().moe_experts_mxfp4_workspace_bytes(T, E, topk, block_m))
 
 
-@dataclass
+def _scale_cols(cols: int) -> int:
+    return (cols + 127) // 128 * 4
+
+
 class Mxfp4Rows:
     """MXFP4 rows: ``codes`` [..., cols / 2] and ``scales`` [..., moe_mxfp4_scale_cols(cols)],
-    both uint8.  Weights of E experts are [E, outs, ...]."""
+    both uint8 on one CUDA device.  Weights of E experts are [E, outs, ...].  The two tensors are
+    checked here, once, and cannot be exchanged afterwards."""
 
-    codes: torch.Tensor
-    scales: torch.Tensor
+    __slots__ = ("_codes", "_scales", "lead", "cols", "device", "_args")
 
-    @property
-    def cols(self) -> int:
-        return 2 * self.codes.shape[-1]
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor):
+        self.device = cuda_device(codes, "codes")
+        self._codes, self._scales = codes, scales
+        self.lead = tuple(codes.shape[:-1])   # (rows,), or (E, outs)
+        self.cols = 2 * codes.shape[-1]
+        if tuple(scales.shape) != (*self.lead, _scale_cols(self.cols)):
+            raise ValueError(f"scales must be {(*self.lead, _scale_cols(self.cols))} for codes "
+                             f"{tuple(codes.shape)}, got {tuple(scales.shape)}")
+        self._args = (need(codes, torch.uint8, 0, self.device, "codes"),
+                      need(scales, torch.uint8, 0, self.device, "scales"))
+
+    codes = property(lambda self: self._codes)
+    scales = property(lambda self: self._scales)
 
     @classmethod
     def allocate(cls, rows, cols: int, device="cuda") -> "Mxfp4Rows":
@@ -53,20 +69,27 @@ def moe_mxfp4_quantize(x, codes, scales, stream=None) -> None:
     if x.dtype not in DTYPE_CODE:
         raise ValueError(f"x must be bfloat16, float16 or float32, got {x.dtype}")
     rows, cols, stride = rows_of(x, "x")
-    launch("moe_mxfp4_quantize", dev, stream, x.data_ptr(), DTYPE_CODE[x.dtype], rows, cols,
-           stride, need(codes, torch.uint8, rows * (cols // 2), dev, "codes"),
-           need(scales, torch.uint8, rows * ((cols + 127) // 128 * 4), dev, "scales"))
+    _quantize(dev, stream, x.data_ptr(), DTYPE_CODE[x.dtype], rows, cols, stride,
+              need(codes, torch.uint8, rows * (cols // 2), dev, "codes"),
+              need(scales, torch.uint8, rows * _scale_cols(cols), dev, "scales"))
 
 
 def mxfp4_quantize(x, out: Optional[Mxfp4Rows] = None, stream=None) -> Mxfp4Rows:
     """Quantise the rows of ``x`` ([..., cols]); allocates the result unless ``out`` is given."""
+    dev = cuda_device(x, "x")
+    code = DTYPE_CODE.get(x.dtype)
+    if code is None:
+        raise ValueError(f"x must be bfloat16, float16 or float32, got {x.dtype}")
+    shape = x.shape
     if out is None:
-        out = Mxfp4Rows.allocate(x.shape[:-1], x.shape[-1], device=x.device)
-    elif out.codes.shape[:-1] != x.shape[:-1] or out.cols != x.shape[-1]:
-        raise ValueError(f"out holds rows of shape {tuple(out.codes.shape)}, x is "
-                         f"{tuple(x.shape)}")
-    moe_mxfp4_quantize(x if x.dim() == 2 else x.reshape(-1, x.shape[-1]), out.codes, out.scales,
-                       stream=stream)
+        out = Mxfp4Rows.allocate(shape[:-1], shape[-1], device=x.device)
+    elif out.lead != shape[:-1] or out.cols != shape[-1] or out.device != dev:
+        raise ValueError(f"out holds rows of shape {tuple(out.codes.shape)} on cuda:{out.device}, "
+                         f"x is {tuple(shape)} on {x.device}")
+    if len(shape) != 2:
+        x = x.reshape(-1, shape[-1])
+    rows, cols, stride = rows_of(x, "x")
+    _quantize(dev, stream, x.data_ptr(), code, rows, cols, stride, *out._args)
     return out
 
 
@@ -77,23 +100,43 @@ def moe_mxfp4_dequantize(codes, scales, y, stream=None) -> None:
     if y.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError(f"y must be bfloat16 or float32, got {y.dtype}")
     rows, cols, stride = rows_of(y, "y")
-    launch("moe_mxfp4_dequantize", dev, stream,
-           need(codes, torch.uint8, rows * (cols // 2), dev, "codes"),
-           need(scales, torch.uint8, rows * ((cols + 127) // 128 * 4), dev, "scales"), rows, cols,
-           y.data_ptr(), DTYPE_CODE[y.dtype], stride)
+    _dequantize(dev, stream, need(codes, torch.uint8, rows * (cols // 2), dev, "codes"),
+                need(scales, torch.uint8, rows * _scale_cols(cols), dev, "scales"), rows, cols,
+                y.data_ptr(), DTYPE_CODE[y.dtype], stride)
 
 
 def mxfp4_dequantize(rows: Mxfp4Rows, dtype=torch.bfloat16, out: Optional[torch.Tensor] = None,
                      stream=None) -> torch.Tensor:
     """The values of ``rows`` as a tensor [..., cols]; allocates it unless ``out`` is given."""
-    shape = (*rows.codes.shape[:-1], rows.cols)
+    dev, cols = rows.device, rows.cols
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=rows.codes.device)
-    elif out.shape != shape:
-        raise ValueError(f"out is {tuple(out.shape)}, the rows are {shape}")
-    y = out if out.dim() == 2 else out.view(-1, rows.cols)
-    moe_mxfp4_dequantize(rows.codes, rows.scales, y, stream=stream)
+        out = torch.empty((*rows.lead, cols), dtype=dtype, device=rows.codes.device)
+    elif out.shape != (*rows.lead, cols) or out.get_device() != dev:
+        raise ValueError(f"out is {tuple(out.shape)} on {out.device}, the rows are "
+                         f"{(*rows.lead, cols)} on cuda:{dev}")
+    kind = out.dtype
+    if kind is not torch.bfloat16 and kind is not torch.float32:
+        raise ValueError(f"out must be bfloat16 or float32, got {kind}")
+    n, _, stride = rows_of(out if out.dim() == 2 else out.view(-1, cols), "out")
+    _dequantize(dev, stream, *rows._args, n, cols, out.data_ptr(), DTYPE_CODE[kind], stride)
     return out
+
+
+def _list_args(T, E, topk, block_m, outs, dev, sorted_token_ids, sorted_weights, expert_ids,
+               num_tokens_post_pad, out, workspace):
+    """Addresses of the sorted list, the output and the workspace, checked for this shape."""
+    kind = out.dtype
+    if kind is not torch.bfloat16 and kind is not torch.float32:
+        raise ValueError(f"out must be bfloat16 or float32, got {kind}")
+    n = T * topk
+    P = n + min(n, E) * (block_m - 1)  # as moe_sort_max_padded
+    return (need(sorted_token_ids, torch.int32, P, dev, "sorted_token_ids"),
+            None if sorted_weights is None else need(sorted_weights, torch.float32, P, dev,
+                                                     "sorted_weights"),
+            need(expert_ids, torch.int32, P // block_m if block_m > 0 else 0, dev, "expert_ids"),
+            need(num_tokens_post_pad, torch.int32, 1, dev, "num_tokens_post_pad"),
+            need(out, kind, n * outs, dev, "out"), DTYPE_CODE[kind],
+            need(workspace, torch.uint8, 0, dev, "workspace"), workspace.numel())
 
 
 def moe_experts_mxfp4(x_codes, x_scales, w_codes, w_scales, T, topk, block_m, sorted_token_ids,
@@ -103,44 +146,34 @@ def moe_experts_mxfp4(x_codes, x_scales, w_codes, w_scales, T, topk, block_m, so
     (bfloat16 or float32; row r is route r).  ``x_codes`` has T rows (one per token) or T * topk
     (one per route); ``w_codes`` is [E, outs, cols / 2]; the sorted list is that of moe_sort or
     moe_route_sort; ``sorted_weights`` may be None (rows are not scaled)."""
-    dev = cuda_device(x_codes, "x_codes")
-    if x_codes.dim() != 2 or w_codes.dim() != 3 or x_codes.shape[1] != w_codes.shape[2]:
-        raise ValueError("x_codes must be [rows, cols / 2] and w_codes [E, outs, cols / 2]")
-    (xr, half), (E, outs) = x_codes.shape, w_codes.shape[:2]
-    if xr != T and xr != T * topk:
-        raise ValueError(f"x_codes must have T = {T} or T * topk = {T * topk} rows, got {xr}")
-    if out.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError(f"out must be bfloat16 or float32, got {out.dtype}")
-    cols = 2 * half
-    sc = (cols + 127) // 128 * 4
-    P, NB = _sort_sizes(T, E, topk, block_m)
-    launch("moe_experts_mxfp4", dev, stream,
-           need(x_codes, torch.uint8, xr * half, dev, "x_codes"),
-           need(x_scales, torch.uint8, xr * sc, dev, "x_scales"), int(xr != T),
-           need(w_codes, torch.uint8, E * outs * half, dev, "w_codes"),
-           need(w_scales, torch.uint8, E * outs * sc, dev, "w_scales"), T, E, topk, cols, outs,
-           block_m, need(sorted_token_ids, torch.int32, P, dev, "sorted_token_ids"),
-           None if sorted_weights is None else need(sorted_weights, torch.float32, P, dev,
-                                                    "sorted_weights"),
-           need(expert_ids, torch.int32, NB, dev, "expert_ids"),
-           need(num_tokens_post_pad, torch.int32, 1, dev, "num_tokens_post_pad"),
-           need(out, out.dtype, T * topk * outs, dev, "out"), DTYPE_CODE[out.dtype],
-           need(workspace, torch.uint8, 0, dev, "workspace"), workspace.numel())
+    experts_mxfp4(Mxfp4Rows(x_codes, x_scales), Mxfp4Rows(w_codes, w_scales), T, topk, block_m,
+                  sorted_token_ids, expert_ids, num_tokens_post_pad, sorted_weights, out=out,
+                  workspace=workspace, stream=stream)
 
 
 def experts_mxfp4(x: Mxfp4Rows, w: Mxfp4Rows, T: int, topk: int, block_m: int, sorted_token_ids,
                   expert_ids, num_tokens_post_pad, sorted_weights=None, dtype=torch.bfloat16,
                   out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
                   stream=None) -> torch.Tensor:
-    """Run moe_experts_mxfp4; returns ``out`` [T * topk, outs].  Without ``out`` the rows of
-    dropped routes are zero (a new buffer is cleared first)."""
+    """Run moe_experts_mxfp4 on rows ``x`` and weights ``w`` [E, outs, ...]; returns ``out``
+    [T * topk, outs].  Without ``out`` the rows of dropped routes are zero (a new buffer is
+    cleared first)."""
+    dev = w.device
+    if len(x.lead) != 1 or len(w.lead) != 2 or x.cols != w.cols:
+        raise ValueError(f"x must be [rows, cols] and w [E, outs, cols], got {(*x.lead, x.cols)} "
+                         f"and {(*w.lead, w.cols)}")
+    if x.device != dev:
+        raise ValueError(f"x is on cuda:{x.device}, w on cuda:{dev}")
+    (xr,), (E, outs) = x.lead, w.lead
+    if xr != T and xr != T * topk:
+        raise ValueError(f"x must have T = {T} or T * topk = {T * topk} rows, got {xr}")
     if out is None:
-        out = torch.zeros(T * topk, w.codes.shape[1], dtype=dtype, device=w.codes.device)
+        out = torch.zeros(T * topk, outs, dtype=dtype, device=w.codes.device)
     if workspace is None:
-        workspace = torch.zeros(moe_experts_mxfp4_workspace_bytes(T, w.codes.shape[0], topk,
-                                                                  block_m),
+        workspace = torch.zeros(moe_experts_mxfp4_workspace_bytes(T, E, topk, block_m),
                                 dtype=torch.uint8, device=w.codes.device)
-    moe_experts_mxfp4(x.codes, x.scales, w.codes, w.scales, T, topk, block_m, sorted_token_ids,
-                      sorted_weights, expert_ids, num_tokens_post_pad, out, workspace,
-                      stream=stream)
+    xc, xs = x._args
+    _experts(dev, stream, xc, xs, 0 if xr == T else 1, *w._args, T, E, topk, x.cols, outs, block_m,
+             *_list_args(T, E, topk, block_m, outs, dev, sorted_token_ids, sorted_weights,
+                         expert_ids, num_tokens_post_pad, out, workspace))
     return out

@@ -1,7 +1,9 @@
-"""Argument checks and launch helpers shared by the training and experts bindings."""
-from __future__ import annotations
+"""Argument checks and the launch of C entry points shared by the training and experts bindings.
 
-import contextlib
+A call of these operators can take less time on the GPU than its checks take here, so a check asks
+each tensor for as little as it can, and containers check their own tensors once.
+"""
+from __future__ import annotations
 
 import torch
 
@@ -10,27 +12,31 @@ from .binding import _check, load
 # type codes of include/moe_route_sort.h
 DTYPE_CODE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
-_here = contextlib.nullcontext()
+_current_device = torch.cuda.current_device
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def need(t: torch.Tensor, dtype, numel: int, device: torch.device, name: str) -> int:
-    """Checks one dense device buffer of at least ``numel`` elements; returns its address."""
-    if t.dtype != dtype:
+def need(t: torch.Tensor, dtype, numel: int, device: int, name: str) -> int:
+    """Checks one dense buffer of at least ``numel`` elements on CUDA device ``device``; returns
+    its address."""
+    if (t.dtype is dtype and t.get_device() == device and t.is_contiguous()
+            and t.numel() >= numel):
+        return t.data_ptr()
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the other buffers on {device}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, other buffers on cuda:{device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.numel() < numel:
-        raise ValueError(f"{name} holds {t.numel()} elements; this shape needs {numel}")
-    return t.data_ptr()
+    raise ValueError(f"{name} holds {t.numel()} elements; this shape needs {numel}")
 
 
-def cuda_device(t: torch.Tensor, name: str) -> torch.device:
+def cuda_device(t: torch.Tensor, name: str) -> int:
     """The CUDA device of the call's first tensor, which the others are checked against."""
-    if not t.is_cuda:
+    d = t.get_device()
+    if d < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return t.device
+    return d
 
 
 def rows_of(t: torch.Tensor, name: str):
@@ -38,20 +44,34 @@ def rows_of(t: torch.Tensor, name: str):
     if t.dim() != 2:
         raise ValueError(f"{name} must be a matrix, got {tuple(t.shape)}")
     rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    stride, inner = t.stride()
+    if inner != 1 and cols > 1:
         raise ValueError(f"{name} must have dense rows")
-    return rows, cols, (t.stride(0) if rows > 1 else cols)
+    return rows, cols, (stride if rows > 1 else cols)
 
 
-def launch(name: str, device: torch.device, stream, *args) -> None:
-    """Calls C entry point ``name`` with ``device`` current on ``stream`` (None: the device's
-    current stream) and raises on a negative status."""
-    other = torch.cuda.current_device() != device.index
-    with torch.cuda.device(device) if other else _here:
+class Entry:
+    """C entry point ``name``, called with its device current and the stream as last argument;
+    raises on a negative status."""
+
+    __slots__ = ("name", "fn")
+
+    def __init__(self, name: str):
+        self.name = name
+        self.fn = None
+
+    def __call__(self, device: int, stream, *args) -> None:
+        fn = self.fn
+        if fn is None:
+            fn = self.fn = getattr(load(), self.name)
         if stream is None:
-            handle = torch.cuda.current_stream(device).cuda_stream
+            handle = _raw_stream(device)
         else:
             handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-        rc = getattr(load(), name)(*args, handle)
-    if rc:
-        _check(rc, name)
+        if _current_device() == device:
+            rc = fn(*args, handle)
+        else:
+            with torch.cuda.device(device):
+                rc = fn(*args, handle)
+        if rc:
+            _check(rc, self.name)

@@ -6,37 +6,48 @@ weights and of that loss to the logits (see include/moe_route_sort.h).
 """
 from __future__ import annotations
 
-from dataclasses import dataclass
 from typing import Optional
 
 import torch
 
 from .binding import load
-from .marshal import DTYPE_CODE, cuda_device, launch, need
+from .marshal import DTYPE_CODE, Entry, cuda_device, need
+
+_loss = Entry("moe_balance_loss")
+_backward = Entry("moe_route_backward")
 
 
 def moe_balance_workspace_bytes(T: int, E: int, n_seq: int = 1) -> int:
     return int(load().moe_balance_workspace_bytes(T, E, n_seq))
 
 
-@dataclass
 class BalanceBuffers:
-    """Outputs and workspace of the balance loss for one (T, E, n_seq)."""
+    """Outputs and workspace of the balance loss for one (T, E, n_seq): ``loss`` [1] float32,
+    ``counts`` [n_seq, E] int32, ``mean_probs`` [n_seq, E] float32.  The buffers are the
+    container's own and cannot be exchanged."""
 
-    loss: torch.Tensor        # [1] float32
-    counts: torch.Tensor      # [n_seq, E] int32
-    mean_probs: torch.Tensor  # [n_seq, E] float32
-    workspace: torch.Tensor
+    __slots__ = ("_loss", "_counts", "_mean", "_workspace", "_shape", "_args", "_ws")
 
-    @classmethod
-    def allocate(cls, T: int, E: int, n_seq: int = 1, device="cuda") -> "BalanceBuffers":
+    def __init__(self, T: int, E: int, n_seq: int, device):
         ws = moe_balance_workspace_bytes(T, E, n_seq)
         if ws == 0:
             raise ValueError("invalid shape for balance-loss buffers")
-        return cls(torch.empty(1, dtype=torch.float32, device=device),
-                   torch.empty(n_seq, E, dtype=torch.int32, device=device),
-                   torch.empty(n_seq, E, dtype=torch.float32, device=device),
-                   torch.empty(ws, dtype=torch.uint8, device=device))
+        self._loss = torch.empty(1, dtype=torch.float32, device=device)
+        self._counts = torch.empty(n_seq, E, dtype=torch.int32, device=device)
+        self._mean = torch.empty(n_seq, E, dtype=torch.float32, device=device)
+        self._workspace = torch.empty(ws, dtype=torch.uint8, device=device)
+        self._shape = (T, E, n_seq, self._loss.get_device())
+        self._args = (self._loss.data_ptr(), self._counts.data_ptr(), self._mean.data_ptr(),
+                      self._workspace.data_ptr(), ws)
+
+    loss = property(lambda self: self._loss)
+    counts = property(lambda self: self._counts)
+    mean_probs = property(lambda self: self._mean)
+    workspace = property(lambda self: self._workspace)
+
+    @classmethod
+    def allocate(cls, T: int, E: int, n_seq: int = 1, device="cuda") -> "BalanceBuffers":
+        return cls(T, E, n_seq, device)
 
 
 def _router(logits, topk_ids, seq_offsets):
@@ -50,12 +61,12 @@ def _router(logits, topk_ids, seq_offsets):
         if topk_ids.dim() != 2 or topk_ids.shape[0] != T:
             raise ValueError("topk_ids must be [T, topk] for logits [T, E]")
         K = topk_ids.shape[1]
-        pid = need(topk_ids, torch.int32, T * K, dev, "topk_ids")
+        pid = need(topk_ids, torch.int32, 0, dev, "topk_ids")
     S, po = 1, None
     if seq_offsets is not None:
         S = seq_offsets.numel() - 1
         po = need(seq_offsets, torch.int32, 1, dev, "seq_offsets")
-    return T, E, K, S, dev, need(logits, torch.bfloat16, T * E, dev, "logits"), pid, po
+    return T, E, K, S, dev, need(logits, torch.bfloat16, 0, dev, "logits"), pid, po
 
 
 def moe_balance_loss(logits, topk_ids, seq_offsets: Optional[torch.Tensor], softmax: bool,
@@ -65,22 +76,26 @@ def moe_balance_loss(logits, topk_ids, seq_offsets: Optional[torch.Tensor], soft
     if topk_ids is None:
         raise ValueError("topk_ids must be [T, topk]")
     T, E, K, S, dev, pl, pid, po = _router(logits, topk_ids, seq_offsets)
-    launch("moe_balance_loss", dev, stream, pl, pid, po, T, E, K, S, int(softmax), float(coef),
-           need(loss, torch.float32, 1, dev, "loss"),
-           need(counts, torch.int32, S * E, dev, "counts"),
-           need(mean_probs, torch.float32, S * E, dev, "mean_probs"),
-           need(workspace, torch.uint8, 0, dev, "workspace"), workspace.numel())
+    _loss(dev, stream, pl, pid, po, T, E, K, S, 1 if softmax else 0, coef,
+          need(loss, torch.float32, 1, dev, "loss"),
+          need(counts, torch.int32, S * E, dev, "counts"),
+          need(mean_probs, torch.float32, S * E, dev, "mean_probs"),
+          need(workspace, torch.uint8, 0, dev, "workspace"), workspace.numel())
 
 
 def balance_loss(logits, topk_ids, coef: float, softmax: bool = False,
                  seq_offsets: Optional[torch.Tensor] = None,
                  out: Optional[BalanceBuffers] = None, stream=None) -> BalanceBuffers:
     """Allocate (unless ``out`` is given) and run moe_balance_loss; returns the buffers."""
+    if topk_ids is None:
+        raise ValueError("topk_ids must be [T, topk]")
+    T, E, K, S, dev, pl, pid, po = _router(logits, topk_ids, seq_offsets)
     if out is None:
-        S = 1 if seq_offsets is None else seq_offsets.numel() - 1
-        out = BalanceBuffers.allocate(logits.shape[0], logits.shape[1], S, device=logits.device)
-    moe_balance_loss(logits, topk_ids, seq_offsets, softmax, coef, out.loss, out.counts,
-                     out.mean_probs, out.workspace, stream=stream)
+        out = BalanceBuffers.allocate(T, E, S, device=logits.device)
+    elif out._shape != (T, E, S, dev):
+        raise ValueError(f"out is for (T, E, n_seq, device) {out._shape}, the call is "
+                         f"{(T, E, S, dev)}")
+    _loss(dev, stream, pl, pid, po, T, E, K, S, 1 if softmax else 0, coef, *out._args)
     return out
 
 
@@ -95,16 +110,16 @@ def moe_route_backward(logits, topk_ids, grad_weights, grad_loss, counts, seq_of
         raise ValueError("grad_weights needs topk_ids")
     if grad_loss is not None and counts is None:
         raise ValueError("grad_loss needs the counts of the forward call")
-    if grad_logits.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError(f"grad_logits must be bfloat16 or float32, got {grad_logits.dtype}")
-    pw = None if grad_weights is None else need(grad_weights, torch.float32, T * K, dev,
-                                                "grad_weights")
-    pg = None if grad_loss is None else need(grad_loss, torch.float32, 1, dev, "grad_loss")
-    pc = None if counts is None else need(counts, torch.int32, S * E, dev, "counts")
-    launch("moe_route_backward", dev, stream, pl, pid, pw, pg, pc, po, T, E, K, S, int(softmax),
-           float(routed_scale), float(coef),
-           need(grad_logits, grad_logits.dtype, T * E, dev, "grad_logits"),
-           DTYPE_CODE[grad_logits.dtype])
+    dtype = grad_logits.dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
+        raise ValueError(f"grad_logits must be bfloat16 or float32, got {dtype}")
+    _backward(dev, stream, pl, pid,
+              None if grad_weights is None else need(grad_weights, torch.float32, T * K, dev,
+                                                     "grad_weights"),
+              None if grad_loss is None else need(grad_loss, torch.float32, 1, dev, "grad_loss"),
+              None if counts is None else need(counts, torch.int32, S * E, dev, "counts"),
+              po, T, E, K, S, 1 if softmax else 0, routed_scale, coef,
+              need(grad_logits, dtype, T * E, dev, "grad_logits"), DTYPE_CODE[dtype])
 
 
 def route_backward(logits, topk_ids, grad_weights=None, routed_scale: float = 1.0,
@@ -115,5 +130,5 @@ def route_backward(logits, topk_ids, grad_weights=None, routed_scale: float = 1.
     if out is None:
         out = torch.empty(logits.shape, dtype=dtype, device=logits.device)
     moe_route_backward(logits, topk_ids, grad_weights, grad_loss, counts, seq_offsets, softmax,
-                       routed_scale, coef, out, stream=stream)
+                       routed_scale, coef, out, stream)
     return out
