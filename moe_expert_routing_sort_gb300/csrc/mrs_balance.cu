@@ -11,18 +11,21 @@
 // and the routing weights w_k = R u_k / sum u (u = sigmoid or exp of the routed logits) add, at
 // the routed experts,    R q_k (gw_k - sum q gw), q = u / sum u      (times 1 - s_k for sigmoid).
 //
-// Both passes read the logits once.  A row belongs to a group of W warps (W = ceil(E / 1024)),
-// each lane holding up to 32 of its columns in registers, the same columns for every row: the
-// row sums are warp shuffles (and one exchange through shared memory when W > 1), and the
-// column sums of the loss stay in registers until the sequence or the CTA's token range ends.
-// A softmax row needs one reduction: every lane takes exponentials against its own maximum and
-// the reduction joins (maximum, sum) pairs.  The next row's loads are in flight while a row is
-// computed.  All sums are fp32 (the joined loss fp64) in an order fixed by the shape, so results
-// are the same bits every call.
+// Both passes read the logits once.  A row belongs to a group of W warps (W = ceil(E / 1024), or
+// ceil(E / 512) for rows that do not start on 16 bytes), each lane holding up to 32 of its columns
+// in registers, the same columns for every row: the row sums are warp shuffles (and one exchange
+// through shared memory when W > 1), and the column sums of the loss stay in registers until the
+// sequence or the CTA's token range ends.  A softmax row needs one reduction: every lane takes
+// exponentials against its own maximum and the reduction joins (maximum, sum) pairs.  Each lane
+// copies its own columns of the next rows to shared memory in the background (kDepth rows, 96 KB
+// on their way per SM: the loads of one row ahead in registers, 16 KB, left the memory idle:
+// T = 16384, E = 4096 37 us) and reads back only what it copied, so no wait is shared.  All sums
+// are fp32 in an order fixed by the shape: results are the same bits every call.
 //
 // Partial column sums: CTA b of the first kernel and sequence i meet in at most one stretch of
 // tokens; it writes its sums to slot b + i (a monotone walk through (b, i): no two stretches
-// share a slot), and the second kernel adds the slots of each sequence in CTA order.
+// share a slot), and the second kernel adds the slots of each sequence in CTA order.  A call of
+// few tokens is one CTA, which writes the results itself.
 #include <cmath>
 #include <type_traits>
 
@@ -30,12 +33,17 @@
 
 #include "mrs_args.h"
 #include "mrs_internal.h"
+#include "mrs_tc.cuh"
 
 namespace mrs {
 
-constexpr int kBalThreads = 256;
+constexpr int kBalThreads = 512;
+constexpr int kJoinThreads = 256;
+constexpr int kDepth = 4;          // rows of a lane in flight, the one it works on among them
 constexpr int kBalWarps = kBalThreads / 32;
-constexpr int kBalMaxCtas = 512;
+constexpr int kBalMaxCtas = 256;
+constexpr int kSoloRows = 4;       // rows per group up to which one CTA takes the call
+constexpr int kSoloSeqs = 8;
 constexpr int kBalMaxJoin = 1024;  // CTAs of the second kernel
 constexpr float kLog2e = 1.4426950408889634f;
 // Below every finite bf16 and itself finite: maxima start here, so that a column of -inf gives a
@@ -48,13 +56,14 @@ struct BalanceArgs {
   const int32_t* offsets;  // [S + 1], or null: one sequence of all T tokens
   int T, E, K, S, W;       // W: warps per row
   int tpc;                 // tokens per CTA
+  int solo;                // one CTA writes the results, no second kernel
   float coef;
   float* loss;
   int32_t* counts;
   float* mean;
   float* psum;      // [ctas + S][E] slots
   int32_t* csum;    // [ctas + S][E]
-  double* partial;  // [kBalMaxJoin]
+  float* partial;   // [kBalMaxJoin]
   unsigned* ticket;
 };
 
@@ -97,45 +106,82 @@ __device__ __forceinline__ int seq_behind(const int32_t* o, int S, int T, int t)
   return lo;
 }
 
-// The raw bits of a lane's columns of one row.  kVec: 16-byte vectors of 8 columns, vector v of
-// the lane being vector v * lanes + lane of the row; else single columns i * lanes + lane.
-// Columns past E read as -inf (a score and a probability of zero).
+// Rows of a lane on their way: the lane's columns of row `row`, `step` rows after the one before.
+// kVec: 16-byte vectors of 8 columns, vector v of the lane being vector v * lanes + lane of the
+// row, copied to shared memory (ring: 16 bytes per vector, thread and slot); else single columns
+// i * lanes + lane, one row ahead in registers.  Columns past E read as -inf (a score and a
+// probability of zero).
 template <int NC, bool kVec>
-struct RowBits {
-  uint32_t w[kVec ? NC / 2 : NC];
-  __device__ __forceinline__ void load(const uint16_t* row, int E, int lane, int lanes) {
+struct RowStream {
+  static constexpr int NV = NC / 8;
+  uint32_t next[kVec ? 1 : NC];
+  uint32_t ring;
+  int slot;
+
+  __device__ __forceinline__ void fetch(const uint16_t* logits, int E, int row, int hi, int lane,
+                                        int lanes, int at) {
+    const uint16_t* p = logits + static_cast<size_t>(row) * E;
     if constexpr (kVec) {
+      if (row < hi) {
 #pragma unroll
-      for (int v = 0; v < NC / 8; ++v) {
-        const int c = 8 * (v * lanes + lane);
-        uint4 q = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
-        if (c < E) q = __ldg(reinterpret_cast<const uint4*>(row + c));
-        w[4 * v] = q.x;
-        w[4 * v + 1] = q.y;
-        w[4 * v + 2] = q.z;
-        w[4 * v + 3] = q.w;
+        for (int v = 0; v < NV; ++v) {
+          const int c = 8 * (v * lanes + lane);
+          if (c < E) copy16(ring + 16 * kBalThreads * (at * NV + v), p + c);
+        }
       }
-    } else {
+      copy_close();  // a group per row, empty past the last, so that the count below holds
+    } else if (row < hi) {
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
         const int c = i * lanes + lane;
-        w[i] = c < E ? static_cast<uint32_t>(__ldg(row + c)) << 16 : 0xff800000u;
+        next[i] = c < E ? static_cast<uint32_t>(__ldg(p + c)) << 16 : 0xff800000u;
       }
     }
   }
-  __device__ __forceinline__ void values(float (&x)[NC]) const {
-    if constexpr (kVec) {
+  // Starts with rows row, row + step, ... below hi.
+  __device__ __forceinline__ void open(const uint16_t* logits, int E, int row, int step, int hi,
+                                       int lane, int lanes, uint32_t ring_base) {
+    ring = ring_base;
+    slot = 0;
 #pragma unroll
-      for (int i = 0; i < NC / 2; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    for (int d = 0; d < (kVec ? kDepth - 1 : 1); ++d)
+      fetch(logits, E, row + d * step, hi, lane, lanes, d);
+  }
+  // The values of row `row`, whose successors keep coming.
+  __device__ __forceinline__ void take(const uint16_t* logits, int E, int row, int step, int hi,
+                                       int lane, int lanes, float (&x)[NC]) {
+    if constexpr (kVec) {
+      fetch(logits, E, row + (kDepth - 1) * step, hi, lane, lanes, (slot + kDepth - 1) % kDepth);
+      copy_wait<kDepth - 1>();
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        uint32_t q[4] = {0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u};
+        if (8 * (v * lanes + lane) < E)
+          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3])
+                       : "r"(ring + 16 * kBalThreads * (slot * NV + v))
+                       : "memory");
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          x[8 * v + 2 * j] = __uint_as_float(q[j] << 16);
+          x[8 * v + 2 * j + 1] = __uint_as_float(q[j] & 0xffff0000u);
+        }
       }
+      slot = (slot + 1) % kDepth;
     } else {
 #pragma unroll
-      for (int i = 0; i < NC; ++i) x[i] = __uint_as_float(w[i]);
+      for (int i = 0; i < NC; ++i) x[i] = __uint_as_float(next[i]);
+      fetch(logits, E, row + step, hi, lane, lanes, 0);
     }
   }
 };
+
+// Shared memory of both row kernels: the ring, then NC floats per thread.
+template <int NC, bool kVec>
+__host__ __device__ constexpr size_t row_smem() {
+  return (kVec ? 16ull * kBalThreads * kDepth * (NC / 8) : 0ull) +
+         sizeof(float) * kBalThreads * NC;
+}
 
 // Column of a lane's element i (may be >= E).
 template <bool kVec>
@@ -220,48 +266,55 @@ template <int NC, bool kVec, bool kSoftmax>
 __global__ void __launch_bounds__(kBalThreads) mrs_balance_rows_kernel(const BalanceArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ float4 xchg_s[kBalWarps][2];
-  float* red = reinterpret_cast<float*>(smem);                       // [groups][W * 32 * NC]
-  int* hist = reinterpret_cast<int*>(red + kBalThreads * NC);        // [E]
+  float* red = reinterpret_cast<float*>(smem + row_smem<NC, kVec>()) - kBalThreads * NC;
+  int* hist = reinterpret_cast<int*>(smem + row_smem<NC, kVec>());  // [E]
   const int tid = threadIdx.x, warp = tid >> 5, W = a.W, E = a.E;
   const int grp = warp / W, gw = warp - grp * W, groups = kBalWarps / W;
   const int lanes = 32 * W, lane = 32 * gw + (tid & 31);
-  const bool idle = grp >= groups;  // W = 3 leaves two warps without a group
+  const bool idle = grp >= groups;  // a W that does not divide the warps leaves some without a group
   float4* xchg = &xchg_s[0][0] + grp * 2 * W;
+  const uint32_t ring = smem_u32(smem) + 16 * tid;
   pdl_trigger();
   for (int e = tid; e < E; e += kBalThreads) hist[e] = 0;
   pdl_wait();
-  if (blockIdx.x == 0 && tid == 0) *a.ticket = 0u;
+  if (blockIdx.x == 0 && tid == 0 && !a.solo) *a.ticket = 0u;
   __syncthreads();
 
   const int t0 = min(static_cast<int>(blockIdx.x) * a.tpc, a.T);
   const int t1 = min(a.T - t0, a.tpc) + t0;
   float g0[1] = {0.0f};
+  float loss = 0.0f;  // solo: this thread's experts
   int t = t0;
-  for (int i = seq_behind(a.offsets, a.S, a.T, t0); i < a.S && t < t1; ++i) {
-    const int lo = max(seq_border(a.offsets, i, a.T), t);
-    const int hi = min(seq_border(a.offsets, i + 1, a.T), t1);
-    if (hi <= lo) continue;
+  for (int i = a.solo ? 0 : seq_behind(a.offsets, a.S, a.T, t0); i < a.S && (t < t1 || a.solo);
+       ++i) {
+    const int lo_i = seq_border(a.offsets, i, a.T), hi_i = seq_border(a.offsets, i + 1, a.T);
+    const int lo = max(lo_i, t), hi = min(hi_i, t1);
+    if (hi <= lo) {
+      if (a.solo)
+        for (int e = tid; e < E; e += kBalThreads) {
+          a.counts[static_cast<size_t>(i) * E + e] = 0;
+          a.mean[static_cast<size_t>(i) * E + e] = 0.0f;
+        }
+      continue;
+    }
     t = hi;
+    RowStream<NC, kVec> rows;
+    int row = lo + grp;
+    if (!idle) rows.open(a.logits, E, row, groups, hi, lane, lanes, ring);
     // counts of the stretch
     const size_t r1 = static_cast<size_t>(hi) * a.K;
     for (size_t r = static_cast<size_t>(lo) * a.K + tid; r < r1; r += kBalThreads) {
       const int e = __ldg(a.ids + r);
       if (e >= 0 && e < E) atomicAdd(hist + e, 1);  // integers: any order, the same sum
     }
-    float acc[NC];
+    if (!idle && row < hi) {
+      float acc[NC];
 #pragma unroll
-    for (int c = 0; c < NC; ++c) acc[c] = 0.0f;
-    if (!idle) {
-      RowBits<NC, kVec> next;
-      int row = lo + grp, buf = 0;
-      if (row < hi) next.load(a.logits + static_cast<size_t>(row) * E, E, lane, lanes);
-      for (; row < hi; row += groups) {
+      for (int c = 0; c < NC; ++c) acc[c] = 0.0f;
+      for (int buf = 0; row < hi; row += groups, buf ^= 1) {
         float x[NC], scale, dot;
-        next.values(x);
-        if (row + groups < hi)
-          next.load(a.logits + static_cast<size_t>(row + groups) * E, E, lane, lanes);
+        rows.take(a.logits, E, row, groups, hi, lane, lanes, x);
         row_terms<NC, kSoftmax, false>(x, g0, W, grp, gw, xchg, buf, scale, dot);
-        buf ^= 1;
 #pragma unroll
         for (int c = 0; c < NC; ++c) acc[c] = fmaf(x[c], scale, acc[c]);
       }
@@ -269,86 +322,99 @@ __global__ void __launch_bounds__(kBalThreads) mrs_balance_rows_kernel(const Bal
 #pragma unroll
       for (int c = 0; c < NC; ++c) mine[column_of<kVec>(c, lane, lanes)] = acc[c];
     }
+    copy_wait_all();
     __syncthreads();
-    const size_t slot = static_cast<size_t>(blockIdx.x + i) * E;
+    const int had = min(groups, hi - lo);  // groups with a row of the stretch
+    const size_t slot = static_cast<size_t>(a.solo ? i : blockIdx.x + i) * E;
+    const float n = static_cast<float>(hi - lo);
     for (int e = tid; e < E; e += kBalThreads) {
       float s = red[e];
-      for (int q = 1; q < groups; ++q) s += red[static_cast<size_t>(q) * lanes * NC + e];
-      a.psum[slot + e] = s;
-      a.csum[slot + e] = hist[e];
+#pragma unroll 4
+      for (int q = 1; q < had; ++q) s += red[static_cast<size_t>(q) * lanes * NC + e];
+      const int c = hist[e];
       hist[e] = 0;
+      if (a.solo) {
+        const float mean = s / n;
+        a.counts[slot + e] = c;
+        a.mean[slot + e] = mean;
+        loss += static_cast<float>(c) * mean / n;
+      } else {
+        a.psum[slot + e] = s;
+        a.csum[slot + e] = c;
+      }
     }
     __syncthreads();
+  }
+  if (a.solo) {
+    loss = warp_sum(loss);
+    if ((tid & 31) == 0) red[warp] = loss;
+    __syncthreads();
+    if (warp == 0) {
+      loss = warp_sum(tid < kBalWarps ? red[tid] : 0.0f);
+      if (tid == 0) *a.loss = loss * (a.coef * a.E / (static_cast<float>(a.K) * a.S));
+    }
   }
 }
 
 // Joins the slots: CTA (bx, by) takes 32 experts of the sequences by, by + gridDim.y, ...; warp w
-// the slots w, w + 8, ... of a sequence.  The last CTA to finish adds the loss.
-__global__ void __launch_bounds__(kBalThreads) mrs_balance_join_kernel(const BalanceArgs a) {
-  __shared__ float ps[kBalWarps][32];
-  __shared__ int cs[kBalWarps][32];
-  __shared__ double ls[kBalThreads];
-  __shared__ bool last;
+// the slots w, w + 8, ... of a sequence.  The last CTA to finish adds the loss.  (In fp64 its few
+// divisions took 4 us; the terms are all of one sign, so fp32 loses nothing that shows.)
+__global__ void __launch_bounds__(kJoinThreads) mrs_balance_join_kernel(const BalanceArgs a) {
+  constexpr int kWarps = kJoinThreads / 32;
+  __shared__ float ps[2][kWarps][32];
+  __shared__ int cs[2][kWarps][32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int e = blockIdx.x * 32 + lane;
   pdl_trigger();
   pdl_wait();
-  double loss = 0.0;
-  for (int i = blockIdx.y; i < a.S; i += gridDim.y) {
+  float loss = 0.0f;
+  int buf = 0;
+  for (int i = blockIdx.y; i < a.S; i += gridDim.y, buf ^= 1) {
     const int lo = seq_border(a.offsets, i, a.T), hi = seq_border(a.offsets, i + 1, a.T);
     float p = 0.0f;
     int c = 0;
     if (hi > lo && e < a.E) {
-      const int b1 = (hi - 1) / a.tpc;
-#pragma unroll 4
-      for (int b = lo / a.tpc + warp; b <= b1; b += kBalWarps) {
-        const size_t at = static_cast<size_t>(b + i) * a.E + e;
-        p += a.psum[at];
-        c += a.csum[at];
+      const int b0 = lo / a.tpc + warp, b1 = (hi - 1) / a.tpc;
+      const size_t at = static_cast<size_t>(i) * a.E + e;
+#pragma unroll 8
+      for (int b = b0; b <= b1; b += kWarps) {
+        p += a.psum[at + static_cast<size_t>(b) * a.E];
+        c += a.csum[at + static_cast<size_t>(b) * a.E];
       }
     }
-    ps[warp][lane] = p;
-    cs[warp][lane] = c;
+    ps[buf][warp][lane] = p;
+    cs[buf][warp][lane] = c;
     __syncthreads();
     if (warp == 0 && e < a.E) {
 #pragma unroll
-      for (int w = 1; w < kBalWarps; ++w) {
-        p += ps[w][lane];
-        c += cs[w][lane];
+      for (int w = 1; w < kWarps; ++w) {
+        p += ps[buf][w][lane];
+        c += cs[buf][w][lane];
       }
       const float n = static_cast<float>(max(hi - lo, 1));
       const float mean = p / n;
       const size_t at = static_cast<size_t>(i) * a.E + e;
       a.counts[at] = c;
       a.mean[at] = mean;
-      loss += static_cast<double>(c) * mean / n;
+      loss += static_cast<float>(c) * mean / n;
     }
-    __syncthreads();
   }
+  if (warp != 0) return;
   // this CTA's part of the loss, then everybody's
   const int ctas = gridDim.x * gridDim.y;
-  if (warp == 0) {
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) loss += __shfl_xor_sync(kFull, loss, d);
-    if (lane == 0) {
-      a.partial[blockIdx.y * gridDim.x + blockIdx.x] = loss;
-      __threadfence();
-      last = atomicAdd(a.ticket, 1u) == static_cast<unsigned>(ctas - 1);
-      __threadfence();
-    }
+  loss = warp_sum(loss);
+  int last = 0;
+  if (lane == 0) {
+    a.partial[blockIdx.y * gridDim.x + blockIdx.x] = loss;
+    __threadfence();
+    last = atomicAdd(a.ticket, 1u) == static_cast<unsigned>(ctas - 1) ? 1 : 0;
+    __threadfence();
   }
-  __syncthreads();
-  if (!last) return;
-  double s = 0.0;
-  for (int q = tid; q < ctas; q += kBalThreads) s += __ldcg(a.partial + q);
-  ls[tid] = s;
-  __syncthreads();
-  for (int d = kBalThreads / 2; d > 0; d >>= 1) {
-    if (tid < d) ls[tid] += ls[tid + d];
-    __syncthreads();
-  }
-  if (tid == 0)
-    *a.loss = static_cast<float>(ls[0] * a.coef * a.E / (static_cast<double>(a.K) * a.S));
+  if (__shfl_sync(kFull, last, 0) == 0) return;
+  float s = 0.0f;
+  for (int q = lane; q < ctas; q += 32) s += __ldcg(a.partial + q);
+  s = warp_sum(s);
+  if (lane == 0) *a.loss = s * (a.coef * a.E / (static_cast<float>(a.K) * a.S));
 }
 
 // -------------------------------------------------------------------------- the gradient
@@ -363,9 +429,11 @@ __global__ void __launch_bounds__(kBalThreads)
   float4* xchg = &xchg_s[0][0] + grp * 2 * W;
   // the routed experts' part of the group's current row, zero elsewhere; a warp only touches the
   // columns that its own lanes hold
-  float* add = reinterpret_cast<float*>(smem) + static_cast<size_t>(grp) * lanes * NC;
+  float* add = reinterpret_cast<float*>(smem + row_smem<NC, kVec>()) - kBalThreads * NC +
+               static_cast<size_t>(grp) * lanes * NC;
+  const uint32_t ring = smem_u32(smem) + 16 * tid;
   pdl_trigger();
-  if (grp >= groups) return;  // W = 3 leaves two warps without a group
+  if (grp >= groups) return;  // a W that does not divide the warps leaves some without a group
 #pragma unroll
   for (int c = 0; c < NC; ++c) add[column_of<kVec>(c, lane, lanes)] = 0.0f;
   __syncwarp();
@@ -404,27 +472,27 @@ __global__ void __launch_bounds__(kBalThreads)
         if (e < E) g[c] = f * static_cast<float>(__ldg(a.counts + static_cast<size_t>(i) * E + e));
       }
     }
-    RowBits<NC, kVec> next;
+    RowStream<NC, kVec> rows;
     int row = t + grp;
     int next_id = -1;
     float next_gw = 0.0f;
     auto fetch = [&](int r) {
-      next.load(a.logits + static_cast<size_t>(r) * E, E, lane, lanes);
-      if (sparse && wl < K) {
+      if (sparse && wl < K && r < hi) {
         next_id = __ldg(a.ids + static_cast<size_t>(r) * K + wl);
         next_gw = __ldg(a.gw + static_cast<size_t>(r) * K + wl);
       }
     };
-    if (row < hi) fetch(row);
+    rows.open(a.logits, E, row, groups, hi, lane, lanes, ring);
+    fetch(row);
     for (; row < hi; row += groups) {
       const uint16_t* xr = a.logits + static_cast<size_t>(row) * E;
       float x[NC];
-      next.values(x);
       int id = next_id;
       float wg = next_gw;
       const bool valid = sparse && wl < K && id >= 0 && id < E;
       float xk = valid ? bf16_bits_to_float(__ldg(xr + id)) : -INFINITY;
-      if (row + groups < hi) fetch(row + groups);
+      fetch(row + groups);
+      rows.take(a.logits, E, row, groups, hi, lane, lanes, x);
       float scale = 0.0f, dot = 0.0f;
       if (dense) {
         row_terms<NC, kSoftmax, true>(x, g, W, grp, gw, xchg, buf, scale, dot);
@@ -505,6 +573,7 @@ __global__ void __launch_bounds__(kBalThreads)
         }
       }
     }
+    copy_wait_all();  // the groups past the last row are empty
     t = hi;
   }
 }
@@ -513,7 +582,8 @@ __global__ void __launch_bounds__(kBalThreads)
 namespace {
 
 // Warps per row, columns per lane and the kind of loads for E experts.  16-byte loads need rows
-// that start on 16 bytes (E a multiple of 8).
+// that start on 16 bytes (E a multiple of 8); without them a lane's next row is in registers, and
+// more than 16 columns would not fit there.
 struct RowPlan {
   int W, NC;
   bool vec;
@@ -521,16 +591,16 @@ struct RowPlan {
 RowPlan row_plan(int E) {
   RowPlan p{};
   p.vec = E % 8 == 0;
-  p.W = (E + 1023) / 1024;
+  p.W = p.vec ? (E + 1023) / 1024 : (E + 511) / 512;
   const int per = p.vec ? (E / 8 + 32 * p.W - 1) / (32 * p.W) * 8 : (E + 32 * p.W - 1) / (32 * p.W);
   p.NC = per <= 8 ? 8 : (per <= 16 ? 16 : 32);
   return p;
 }
 
-// Tokens per CTA: one row per group of warps until every SM has its share of the CTAs.
+// Tokens per CTA: one row per group of warps until every SM has a CTA.
 int tokens_per_cta(int T, int W, int sms) {
   const int groups = kBalWarps / W;
-  int ctas = 2 * sms < kBalMaxCtas ? 2 * sms : kBalMaxCtas;
+  int ctas = sms < kBalMaxCtas ? sms : kBalMaxCtas;
   const int most = (T + groups - 1) / groups;
   if (most < ctas) ctas = most;
   return (T + ctas - 1) / ctas;
@@ -545,7 +615,7 @@ BalanceLayout balance_layout(int T, int E, int S) {
   const size_t slots = (most + static_cast<size_t>(S)) * static_cast<size_t>(E);
   BalanceLayout l{};
   l.partial = 16;
-  l.psum = l.partial + sizeof(double) * kBalMaxJoin;
+  l.psum = l.partial + sizeof(float) * kBalMaxJoin;
   l.csum = align16(l.psum + sizeof(float) * slots);
   l.total = align16(l.csum + sizeof(int32_t) * slots);
   return l;
@@ -564,12 +634,11 @@ template <int NC, bool kVec>
 cudaError_t launch_balance(const BalanceArgs& a, bool softmax, int ctas, cudaStream_t st) {
   auto* k = softmax ? mrs_balance_rows_kernel<NC, kVec, true>
                     : mrs_balance_rows_kernel<NC, kVec, false>;
-  const size_t smem = sizeof(float) * kBalThreads * NC + sizeof(int) * static_cast<size_t>(a.E);
-  // with the kernel's own variables just above what every kernel is granted when E is largest
+  const size_t smem = row_smem<NC, kVec>() + sizeof(int) * static_cast<size_t>(a.E);
   static SmemGrant granted[2];
   const cudaError_t err =
       grant_smem(reinterpret_cast<const void*>(k),
-                 sizeof(float) * kBalThreads * NC + sizeof(int) * kMaxExperts, granted[softmax]);
+                 row_smem<NC, kVec>() + sizeof(int) * kMaxExperts, granted[softmax]);
   if (err != cudaSuccess) return err;
   return launch_pdl(k, dim3(ctas), dim3(kBalThreads), smem, st, a);
 }
@@ -578,7 +647,26 @@ template <int NC, bool kVec, class Out>
 cudaError_t launch_backward(const RouteBackwardArgs& a, bool softmax, int ctas, cudaStream_t st) {
   auto* k = softmax ? mrs_route_backward_kernel<NC, kVec, true, Out>
                     : mrs_route_backward_kernel<NC, kVec, false, Out>;
-  return launch_pdl(k, dim3(ctas), dim3(kBalThreads), sizeof(float) * kBalThreads * NC, st, a);
+  const size_t smem = row_smem<NC, kVec>();
+  static SmemGrant granted[2];
+  const cudaError_t err =
+      grant_smem(reinterpret_cast<const void*>(k), smem, granted[softmax]);
+  if (err != cudaSuccess) return err;
+  return launch_pdl(k, dim3(ctas), dim3(kBalThreads), smem, st, a);
+}
+
+// The kernels' instances: 8, 16 or 32 columns per lane in vectors, 8 or 16 without.
+template <class Go>
+cudaError_t with_plan(const RowPlan& p, Go go) {
+  using std::integral_constant;
+  using Vec = std::true_type;
+  using One = std::false_type;
+  if (!p.vec)
+    return p.NC == 8 ? go(integral_constant<int, 8>{}, One{})
+                     : go(integral_constant<int, 16>{}, One{});
+  return p.NC == 8    ? go(integral_constant<int, 8>{}, Vec{})
+         : p.NC == 16 ? go(integral_constant<int, 16>{}, Vec{})
+                      : go(integral_constant<int, 32>{}, Vec{});
 }
 
 }  // namespace
@@ -630,31 +718,27 @@ int moe_balance_loss(const void* logits_bf16, const int32_t* topk_ids, const int
   a.K = topk;
   a.S = n_seq;
   a.W = p.W;
-  a.tpc = T > 0 ? tokens_per_cta(T, p.W, sms) : 1;
+  const int groups = kBalWarps / p.W;
+  a.solo = T <= kSoloRows * groups && n_seq <= kSoloSeqs;
+  a.tpc = a.solo || T == 0 ? (T > 0 ? T : 1) : tokens_per_cta(T, p.W, sms);
   a.coef = coef;
   a.loss = loss;
   a.counts = counts;
   a.mean = mean_probs;
   a.ticket = reinterpret_cast<unsigned*>(ws);
-  a.partial = reinterpret_cast<double*>(ws + l.partial);
+  a.partial = reinterpret_cast<float*>(ws + l.partial);
   a.psum = reinterpret_cast<float*>(ws + l.psum);
   a.csum = reinterpret_cast<int32_t*>(ws + l.csum);
   const int ctas = T > 0 ? (T + a.tpc - 1) / a.tpc : 1;
-  cudaError_t err;
-  if (p.vec)
-    err = p.NC == 8    ? launch_balance<8, true>(a, softmax != 0, ctas, stream)
-          : p.NC == 16 ? launch_balance<16, true>(a, softmax != 0, ctas, stream)
-                       : launch_balance<32, true>(a, softmax != 0, ctas, stream);
-  else
-    err = p.NC == 8    ? launch_balance<8, false>(a, softmax != 0, ctas, stream)
-          : p.NC == 16 ? launch_balance<16, false>(a, softmax != 0, ctas, stream)
-                       : launch_balance<32, false>(a, softmax != 0, ctas, stream);
-  if (err != cudaSuccess) return launch_status(err);
+  const cudaError_t err = with_plan(p, [&](auto nc, auto vec) {
+    return launch_balance<decltype(nc)::value, decltype(vec)::value>(a, softmax != 0, ctas, stream);
+  });
+  if (err != cudaSuccess || a.solo) return launch_status(err);
   const int gx = (E + 31) / 32;
   int gy = kBalMaxJoin / gx < 8 ? 8 : kBalMaxJoin / gx;  // gx <= 128
   if (gy > n_seq) gy = n_seq;
   return launch_status(
-      launch_pdl(mrs_balance_join_kernel, dim3(gx, gy), dim3(kBalThreads), 0, stream, a));
+      launch_pdl(mrs_balance_join_kernel, dim3(gx, gy), dim3(kJoinThreads), 0, stream, a));
 }
 
 int moe_route_backward(const void* logits_bf16, const int32_t* topk_ids, const float* grad_weights,
@@ -703,19 +787,12 @@ int moe_route_backward(const void* logits_bf16, const int32_t* topk_ids, const f
   a.out = grad_logits;
   const int ctas = (T + a.tpc - 1) / a.tpc;
   const bool sm = softmax != 0, f32 = grad_dtype == MOE_RS_FP32;
-  auto go = [&](auto nc, auto vec) {
+  return launch_status(with_plan(p, [&](auto nc, auto vec) {
     constexpr int NC = decltype(nc)::value;
     constexpr bool V = decltype(vec)::value;
     return f32 ? launch_backward<NC, V, float>(a, sm, ctas, stream)
                : launch_backward<NC, V, __nv_bfloat16>(a, sm, ctas, stream);
-  };
-  using std::integral_constant;
-  auto pick = [&](auto vec) {
-    return p.NC == 8    ? go(integral_constant<int, 8>{}, vec)
-           : p.NC == 16 ? go(integral_constant<int, 16>{}, vec)
-                        : go(integral_constant<int, 32>{}, vec);
-  };
-  return launch_status(p.vec ? pick(std::true_type{}) : pick(std::false_type{}));
+  }));
 }
 
 }  // extern "C"

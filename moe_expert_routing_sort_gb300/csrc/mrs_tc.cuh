@@ -119,6 +119,12 @@ __device__ __forceinline__ bool warp_wait(unsigned long long* mbar, uint32_t pha
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+__device__ __forceinline__ void copy_close() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but this thread's last kLeft closed groups have landed.
+template <int kLeft>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
 // One arrival on the barrier (counted in its expected number) once this thread's copies so far
 // have landed.
 __device__ __forceinline__ void copy_arrive(unsigned long long* mbar) {
