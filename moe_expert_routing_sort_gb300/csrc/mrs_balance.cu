@@ -49,6 +49,9 @@ constexpr float kLog2e = 1.4426950408889634f;
 // Below every finite bf16 and itself finite: maxima start here, so that a column of -inf gives a
 // term of exp(-inf) = 0 whatever the others hold, and a row of the type's lowest value is even.
 constexpr float kLowest = -3.402823466e38f;
+// Finite logits further out than this count as this in a softmax: up to here the rounding of
+// m log2 e (below) is a factor of at most 2^3 that cancels, not one that overflows.
+constexpr float kFarLogit = 67108864.0f;  // 2^26
 
 struct BalanceArgs {
   const uint16_t* logits;
@@ -88,6 +91,37 @@ __device__ __forceinline__ float rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// Two fp32 values in one 64-bit register, for the instructions that take two at a time.
+using Two = unsigned long long;
+__device__ __forceinline__ Two two(float lo, float hi) {
+  Two r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void halves(Two v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+  Two r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ Two add2(Two a, Two b) {
+  Two r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ Two mul2(Two a, Two b) {
+  Two r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float sum2(Two v) {
+  float lo, hi;
+  halves(v, lo, hi);
+  return lo + hi;
 }
 
 // Borders of the sequences, kept inside [0, T] whatever the array holds.
@@ -149,7 +183,7 @@ struct RowStream {
   }
   // The values of row `row`, whose successors keep coming.
   __device__ __forceinline__ void take(const uint16_t* logits, int E, int row, int step, int hi,
-                                       int lane, int lanes, float (&x)[NC]) {
+                                       int lane, int lanes, Two (&x)[NC / 2]) {
     if constexpr (kVec) {
       fetch(logits, E, row + (kDepth - 1) * step, hi, lane, lanes, (slot + kDepth - 1) % kDepth);
       copy_wait<kDepth - 1>();
@@ -163,14 +197,14 @@ struct RowStream {
                        : "memory");
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          x[8 * v + 2 * j] = __uint_as_float(q[j] << 16);
-          x[8 * v + 2 * j + 1] = __uint_as_float(q[j] & 0xffff0000u);
+          x[4 * v + j] = two(__uint_as_float(q[j] << 16), __uint_as_float(q[j] & 0xffff0000u));
         }
       }
       slot = (slot + 1) % kDepth;
     } else {
 #pragma unroll
-      for (int i = 0; i < NC; ++i) x[i] = __uint_as_float(next[i]);
+      for (int i = 0; i < NC / 2; ++i)
+        x[i] = two(__uint_as_float(next[2 * i]), __uint_as_float(next[2 * i + 1]));
       fetch(logits, E, row + step, hi, lane, lanes, 0);
     }
   }
@@ -189,15 +223,20 @@ __device__ __forceinline__ int column_of(int i, int lane, int lanes) {
   return kVec ? 8 * ((i >> 3) * lanes + lane) + (i & 7) : i * lanes + lane;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(kFull, v, d);
   return v;
 }
 __device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, d));
-  return v;
+  float r;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
 }
 
 // Barrier of the W warps of group `grp` (hardware barriers 1..).
@@ -205,34 +244,78 @@ __device__ __forceinline__ void group_sync(int grp, int W) {
   asm volatile("bar.sync %0, %1;" ::"r"(grp + 1), "r"(32 * W) : "memory");
 }
 
+// Sigmoids of two values.  One reciprocal serves both, 1 / (a b) times the other, unless the
+// product of the two denominators could leave the range (x below about -43).
+__device__ __forceinline__ Two sigmoid2(Two x) {
+  float x0, x1, e0, e1;
+  halves(mul2(x, two(-kLog2e, -kLog2e)), x0, x1);
+  e0 = 1.0f + ex2(x0);
+  e1 = 1.0f + ex2(x1);
+  if (fmaxf(x0, x1) < 62.0f) {
+    const float r = rcp(e0 * e1);
+    return two(r * e1, r * e0);
+  }
+  return two(rcp(e0), rcp(e1));
+}
+
 // Scores of one row in place, and the row's sums.  On return x holds the terms u_e of the lane
 // (scaled by a factor of its own for softmax), `scale` turns a term into a probability, and
 // `dot` is sum over e of p_e g_e (kDot).  xchg: [2][W] float4 of the group, buffer `buf`.
+// A softmax lane takes 2^(x log2 e - m), m its own maximum times log2 e as rounded, and the
+// reduction rescales by differences of those same m: nothing is lost to the rounding of m.
 template <int NC, bool kSoftmax, bool kDot>
-__device__ __forceinline__ void row_terms(float (&x)[NC], const float (&g)[kDot ? NC : 1],
+__device__ __forceinline__ void row_terms(Two (&x)[NC / 2], const Two (&g)[kDot ? NC / 2 : 1],
                                           int W, int grp, int gw, float4* xchg, int buf,
                                           float& scale, float& dot) {
-  float m = 0.0f, sum = 0.0f, sg = 0.0f;
+  constexpr int N2 = NC / 2;
+  float m = 0.0f;
   if constexpr (kSoftmax) {
-    m = kLowest;
+    float top[4] = {kLowest, kLowest, kLowest, kLowest};
 #pragma unroll
-    for (int i = 0; i < NC; ++i) m = fmaxf(m, x[i]);
-    // the difference first: exact near the maximum, where the terms matter
+    for (int i = 0; i < N2; ++i) {
+      float lo, hi;
+      halves(x[i], lo, hi);
+      top[i & 3] = max3(top[i & 3], lo, hi);
+    }
+    m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+    if (!(fabsf(m) <= kFarLogit)) {  // also lanes of -inf alone
+      m = fminf(fmaxf(m, -kFarLogit), kFarLogit);
 #pragma unroll
-    for (int i = 0; i < NC; ++i) x[i] = ex2((x[i] - m) * kLog2e);
+      for (int i = 0; i < N2; ++i) {
+        float lo, hi;
+        halves(x[i], lo, hi);
+        lo = lo == -INFINITY ? lo : fminf(fmaxf(lo, -kFarLogit), kFarLogit);
+        hi = hi == -INFINITY ? hi : fminf(fmaxf(hi, -kFarLogit), kFarLogit);
+        x[i] = two(lo, hi);
+      }
+    }
+    m *= kLog2e;
+    const Two l = two(kLog2e, kLog2e), mm = two(-m, -m);
+#pragma unroll
+    for (int i = 0; i < N2; ++i) {
+      float lo, hi;
+      halves(fma2(x[i], l, mm), lo, hi);
+      x[i] = two(ex2(lo), ex2(hi));
+    }
   } else {
 #pragma unroll
-    for (int i = 0; i < NC; ++i) x[i] = rcp(1.0f + ex2(-kLog2e * x[i]));
+    for (int i = 0; i < N2; ++i) x[i] = sigmoid2(x[i]);
   }
+  Two s0 = 0ull, s1 = 0ull, d0 = 0ull, d1 = 0ull;
 #pragma unroll
-  for (int i = 0; i < NC; ++i) {
-    sum += x[i];
-    if constexpr (kDot) sg = fmaf(x[i], g[i], sg);
+  for (int i = 0; i < N2; i += 2) {
+    s0 = add2(s0, x[i]);
+    s1 = add2(s1, x[i + 1]);
+    if constexpr (kDot) {
+      d0 = fma2(x[i], g[i], d0);
+      d1 = fma2(x[i + 1], g[i + 1], d1);
+    }
   }
+  float sum = sum2(add2(s0, s1)), sg = kDot ? sum2(add2(d0, d1)) : 0.0f;
   float f = 1.0f;  // the lane's factor
   if constexpr (kSoftmax) {
     const float M = warp_max(m);
-    f = ex2((m - M) * kLog2e);
+    f = ex2(m - M);
     sum *= f;
     if constexpr (kDot) sg *= f;
     m = M;
@@ -250,11 +333,11 @@ __device__ __forceinline__ void row_terms(float (&x)[NC], const float (&g)[kDot 
     sg = 0.0f;
     for (int w = 0; w < W; ++w) {
       const float4 q = slot[w];
-      const float r = kSoftmax ? ex2((q.x - M) * kLog2e) : 1.0f;
+      const float r = kSoftmax ? ex2(q.x - M) : 1.0f;
       sum = fmaf(q.y, r, sum);
       if constexpr (kDot) sg = fmaf(q.z, r, sg);
     }
-    if constexpr (kSoftmax) f *= ex2((m - M) * kLog2e);
+    if constexpr (kSoftmax) f *= ex2(m - M);
   }
   const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
   scale = f * inv;
@@ -263,7 +346,7 @@ __device__ __forceinline__ void row_terms(float (&x)[NC], const float (&g)[kDot 
 
 // ------------------------------------------------------------------------------ the loss
 template <int NC, bool kVec, bool kSoftmax>
-__global__ void __launch_bounds__(kBalThreads) mrs_balance_rows_kernel(const BalanceArgs a) {
+__global__ void __launch_bounds__(kBalThreads, 1) mrs_balance_rows_kernel(const BalanceArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ float4 xchg_s[kBalWarps][2];
   float* red = reinterpret_cast<float*>(smem + row_smem<NC, kVec>()) - kBalThreads * NC;
@@ -282,7 +365,7 @@ __global__ void __launch_bounds__(kBalThreads) mrs_balance_rows_kernel(const Bal
 
   const int t0 = min(static_cast<int>(blockIdx.x) * a.tpc, a.T);
   const int t1 = min(a.T - t0, a.tpc) + t0;
-  float g0[1] = {0.0f};
+  Two g0[1] = {0ull};
   float loss = 0.0f;  // solo: this thread's experts
   int t = t0;
   for (int i = a.solo ? 0 : seq_behind(a.offsets, a.S, a.T, t0); i < a.S && (t < t1 || a.solo);
@@ -308,19 +391,31 @@ __global__ void __launch_bounds__(kBalThreads) mrs_balance_rows_kernel(const Bal
       if (e >= 0 && e < E) atomicAdd(hist + e, 1);  // integers: any order, the same sum
     }
     if (!idle && row < hi) {
-      float acc[NC];
+      Two acc[NC / 2];
 #pragma unroll
-      for (int c = 0; c < NC; ++c) acc[c] = 0.0f;
+      for (int c = 0; c < NC / 2; ++c) acc[c] = 0ull;
       for (int buf = 0; row < hi; row += groups, buf ^= 1) {
-        float x[NC], scale, dot;
+        Two x[NC / 2];
+        float scale, dot;
         rows.take(a.logits, E, row, groups, hi, lane, lanes, x);
         row_terms<NC, kSoftmax, false>(x, g0, W, grp, gw, xchg, buf, scale, dot);
+        const Two by = two(scale, scale);
 #pragma unroll
-        for (int c = 0; c < NC; ++c) acc[c] = fmaf(x[c], scale, acc[c]);
+        for (int c = 0; c < NC / 2; ++c) acc[c] = fma2(x[c], by, acc[c]);
       }
       float* mine = red + static_cast<size_t>(grp) * lanes * NC;
 #pragma unroll
-      for (int c = 0; c < NC; ++c) mine[column_of<kVec>(c, lane, lanes)] = acc[c];
+      for (int c = 0; c < NC / 2; ++c) {
+        const int at = column_of<kVec>(2 * c, lane, lanes);
+        float lo, hi;
+        halves(acc[c], lo, hi);
+        if constexpr (kVec) {
+          *reinterpret_cast<float2*>(mine + at) = make_float2(lo, hi);
+        } else {
+          mine[at] = lo;
+          mine[at + lanes] = hi;
+        }
+      }
     }
     copy_wait_all();
     __syncthreads();
@@ -419,7 +514,7 @@ __global__ void __launch_bounds__(kJoinThreads) mrs_balance_join_kernel(const Ba
 
 // -------------------------------------------------------------------------- the gradient
 template <int NC, bool kVec, bool kSoftmax, class Out>
-__global__ void __launch_bounds__(kBalThreads)
+__global__ void __launch_bounds__(kBalThreads, 1)
     mrs_route_backward_kernel(const RouteBackwardArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ float4 xchg_s[kBalWarps][2];
@@ -460,17 +555,19 @@ __global__ void __launch_bounds__(kBalThreads)
       in_seq = lo_i <= t;
       hi = min(t1, in_seq ? hi_i : lo_i);
     }
-    float g[NC];
+    Two g[NC / 2];
 #pragma unroll
-    for (int c = 0; c < NC; ++c) g[c] = 0.0f;
+    for (int c = 0; c < NC / 2; ++c) g[c] = 0ull;
     if (dense && in_seq) {
       const float n = static_cast<float>(hi_i - lo_i);
       const float f = gl * (a.coef / a.S) * (static_cast<float>(E) / K) / n / n;
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
+      auto of = [&](int c) {
         const int e = column_of<kVec>(c, lane, lanes);
-        if (e < E) g[c] = f * static_cast<float>(__ldg(a.counts + static_cast<size_t>(i) * E + e));
-      }
+        return e < E ? f * static_cast<float>(__ldg(a.counts + static_cast<size_t>(i) * E + e))
+                     : 0.0f;
+      };
+#pragma unroll
+      for (int c = 0; c < NC / 2; ++c) g[c] = two(of(2 * c), of(2 * c + 1));
     }
     RowStream<NC, kVec> rows;
     int row = t + grp;
@@ -486,7 +583,7 @@ __global__ void __launch_bounds__(kBalThreads)
     fetch(row);
     for (; row < hi; row += groups) {
       const uint16_t* xr = a.logits + static_cast<size_t>(row) * E;
-      float x[NC];
+      Two x[NC / 2];
       int id = next_id;
       float wg = next_gw;
       const bool valid = sparse && wl < K && id >= 0 && id < E;
@@ -497,14 +594,16 @@ __global__ void __launch_bounds__(kBalThreads)
       if (dense) {
         row_terms<NC, kSoftmax, true>(x, g, W, grp, gw, xchg, buf, scale, dot);
         buf ^= 1;
+        const Two by = two(scale, scale), less = two(-dot, -dot);
+        const Two one = two(1.0f, 1.0f), minus = two(-1.0f, -1.0f);
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          const float p = x[c] * scale;
-          x[c] = (kSoftmax ? p : p * (1.0f - x[c])) * (g[c] - dot);
+        for (int c = 0; c < NC / 2; ++c) {
+          const Two p = mul2(x[c], by), d = add2(g[c], less);
+          x[c] = kSoftmax ? mul2(p, d) : mul2(mul2(p, fma2(x[c], minus, one)), d);
         }
       } else {
 #pragma unroll
-        for (int c = 0; c < NC; ++c) x[c] = 0.0f;
+        for (int c = 0; c < NC / 2; ++c) x[c] = 0ull;
       }
       if (sparse) {
         // every warp of the group works the K routes out, and keeps those in its columns
@@ -536,8 +635,21 @@ __global__ void __launch_bounds__(kBalThreads)
         const bool put = valid && (same & lanemask_lt(wl)) == 0u && (owner >> 5) == gw;
         if (put) add[id] = d;
         __syncwarp();
+        if constexpr (kVec) {
 #pragma unroll
-        for (int c = 0; c < NC; ++c) x[c] += add[column_of<kVec>(c, lane, lanes)];
+          for (int v = 0; v < NC / 8; ++v) {
+            const float4* q = reinterpret_cast<const float4*>(add + 8 * (v * lanes + lane));
+            const float4 p0 = q[0], p1 = q[1];
+            x[4 * v] = add2(x[4 * v], two(p0.x, p0.y));
+            x[4 * v + 1] = add2(x[4 * v + 1], two(p0.z, p0.w));
+            x[4 * v + 2] = add2(x[4 * v + 2], two(p1.x, p1.y));
+            x[4 * v + 3] = add2(x[4 * v + 3], two(p1.z, p1.w));
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < NC / 2; ++c)
+            x[c] = add2(x[c], two(add[2 * c * lanes + lane], add[(2 * c + 1) * lanes + lane]));
+        }
         __syncwarp();
         if (put) add[id] = 0.0f;
       }
@@ -547,17 +659,19 @@ __global__ void __launch_bounds__(kBalThreads)
         for (int v = 0; v < NC / 8; ++v) {
           const int c = 8 * (v * lanes + lane);
           if (c >= E) continue;
+          float y[8];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) halves(x[4 * v + j], y[2 * j], y[2 * j + 1]);
           if constexpr (sizeof(Out) == 4) {
             float4* o = reinterpret_cast<float4*>(out + c);
-            o[0] = make_float4(x[8 * v], x[8 * v + 1], x[8 * v + 2], x[8 * v + 3]);
-            o[1] = make_float4(x[8 * v + 4], x[8 * v + 5], x[8 * v + 6], x[8 * v + 7]);
+            o[0] = make_float4(y[0], y[1], y[2], y[3]);
+            o[1] = make_float4(y[4], y[5], y[6], y[7]);
           } else {
             // bf16 gradients: one rounding of the fp32 sum
             uint32_t w[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const __nv_bfloat162 b =
-                  __floats2bfloat162_rn(x[8 * v + 2 * j], x[8 * v + 2 * j + 1]);
+              const __nv_bfloat162 b = __floats2bfloat162_rn(y[2 * j], y[2 * j + 1]);
               w[j] = *reinterpret_cast<const uint32_t*>(&b);
             }
             *reinterpret_cast<uint4*>(out + c) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -567,9 +681,12 @@ __global__ void __launch_bounds__(kBalThreads)
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
           const int e = c * lanes + lane;
+          float lo, hi;
+          halves(x[c / 2], lo, hi);
+          const float y = (c & 1) ? hi : lo;
           if (e >= E) continue;
-          if constexpr (sizeof(Out) == 4) out[e] = x[c];
-          else out[e] = __float2bfloat16_rn(x[c]);
+          if constexpr (sizeof(Out) == 4) out[e] = y;
+          else out[e] = __float2bfloat16_rn(y);
         }
       }
     }
