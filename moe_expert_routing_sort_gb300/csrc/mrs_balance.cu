@@ -93,37 +93,6 @@ __device__ __forceinline__ float rcp(float x) {
   return y;
 }
 
-// Two fp32 values in one 64-bit register, for the instructions that take two at a time.
-using Two = unsigned long long;
-__device__ __forceinline__ Two two(float lo, float hi) {
-  Two r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void halves(Two v, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
-  Two r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ Two add2(Two a, Two b) {
-  Two r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ Two mul2(Two a, Two b) {
-  Two r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ float sum2(Two v) {
-  float lo, hi;
-  halves(v, lo, hi);
-  return lo + hi;
-}
-
 // Borders of the sequences, kept inside [0, T] whatever the array holds.
 __device__ __forceinline__ int seq_border(const int32_t* o, int i, int T) {
   return o == nullptr ? (i == 0 ? 0 : T) : min(max(__ldg(o + i), 0), T);
@@ -143,11 +112,13 @@ __device__ __forceinline__ int seq_behind(const int32_t* o, int S, int T, int t)
 // Rows of a lane on their way: the lane's columns of row `row`, `step` rows after the one before.
 // kVec: 16-byte vectors of 8 columns, vector v of the lane being vector v * lanes + lane of the
 // row, copied to shared memory (ring: 16 bytes per vector, thread and slot); else single columns
-// i * lanes + lane, one row ahead in registers.  Columns past E read as -inf (a score and a
-// probability of zero).
-template <int NC, bool kVec>
+// i * lanes + lane, one row ahead in registers.  Columns past E read as -inf, a term of zero; for
+// sigmoids in vectors as -40, which keeps their lanes on the short way, and their terms are left
+// out of the row's sum.
+template <int NC, bool kVec, bool kSoftmax>
 struct RowStream {
   static constexpr int NV = NC / 8;
+  static constexpr uint32_t kPast = kSoftmax ? 0xff80ff80u : 0xc220c220u;
   uint32_t next[kVec ? 1 : NC];
   uint32_t ring;
   int slot;
@@ -183,13 +154,13 @@ struct RowStream {
   }
   // The values of row `row`, whose successors keep coming.
   __device__ __forceinline__ void take(const uint16_t* logits, int E, int row, int step, int hi,
-                                       int lane, int lanes, Two (&x)[NC / 2]) {
+                                       int lane, int lanes, float (&x)[NC]) {
     if constexpr (kVec) {
       fetch(logits, E, row + (kDepth - 1) * step, hi, lane, lanes, (slot + kDepth - 1) % kDepth);
       copy_wait<kDepth - 1>();
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
-        uint32_t q[4] = {0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u};
+        uint32_t q[4] = {kPast, kPast, kPast, kPast};
         if (8 * (v * lanes + lane) < E)
           asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                        : "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3])
@@ -197,18 +168,26 @@ struct RowStream {
                        : "memory");
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          x[4 * v + j] = two(__uint_as_float(q[j] << 16), __uint_as_float(q[j] & 0xffff0000u));
+          x[8 * v + 2 * j] = __uint_as_float(q[j] << 16);
+          x[8 * v + 2 * j + 1] = __uint_as_float(q[j] & 0xffff0000u);
         }
       }
       slot = (slot + 1) % kDepth;
     } else {
 #pragma unroll
-      for (int i = 0; i < NC / 2; ++i)
-        x[i] = two(__uint_as_float(next[2 * i]), __uint_as_float(next[2 * i + 1]));
+      for (int i = 0; i < NC; ++i) x[i] = __uint_as_float(next[i]);
       fetch(logits, E, row + step, hi, lane, lanes, 0);
     }
   }
 };
+
+template <int NC, bool kVec>
+__device__ __forceinline__ unsigned vectors_past(int E, int lane, int lanes) {
+  unsigned p = 0u;
+#pragma unroll
+  for (int v = 0; kVec && v < NC / 8; ++v) p |= 8 * (v * lanes + lane) >= E ? 1u << v : 0u;
+  return p;
+}
 
 // Shared memory of both row kernels: the ring, then NC floats per thread.
 template <int NC, bool kVec>
@@ -228,6 +207,11 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float r;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(kFull, v, d);
@@ -239,89 +223,100 @@ __device__ __forceinline__ float warp_max(float v) {
   return r;
 }
 
-// Barrier of the W warps of group `grp` (hardware barriers 1..).
+// Groups of W warps in a CTA.  A group of several warps has a hardware barrier of its own, of
+// which there are 15 beside the CTA's.
+__host__ __device__ constexpr int groups_of(int W) {
+  return W > 1 && kBalWarps / W > 15 ? 15 : kBalWarps / W;
+}
+
+// Barrier of the W warps of group `grp`.
 __device__ __forceinline__ void group_sync(int grp, int W) {
   asm volatile("bar.sync %0, %1;" ::"r"(grp + 1), "r"(32 * W) : "memory");
 }
 
-// Sigmoids of two values.  One reciprocal serves both, 1 / (a b) times the other, unless the
-// product of the two denominators could leave the range (x below about -43).
-__device__ __forceinline__ Two sigmoid2(Two x) {
-  float x0, x1, e0, e1;
-  halves(mul2(x, two(-kLog2e, -kLog2e)), x0, x1);
-  e0 = 1.0f + ex2(x0);
-  e1 = 1.0f + ex2(x1);
-  if (fmaxf(x0, x1) < 62.0f) {
-    const float r = rcp(e0 * e1);
-    return two(r * e1, r * e0);
+// Sigmoids in place.  One reciprocal serves two, 1 / (a b) times the other, unless a product of
+// two denominators could leave the range (a logit below about -43 in the lane).
+template <int NC>
+__device__ __forceinline__ void sigmoids(float (&x)[NC]) {
+  float low = x[0];
+#pragma unroll
+  for (int i = 1; i + 1 < NC; i += 2) low = min3(low, x[i], x[i + 1]);
+  low = fminf(low, x[NC - 1]);
+  if (low > -43.0f) {
+#pragma unroll
+    for (int i = 0; i < NC; i += 2) {
+      const float e0 = 1.0f + ex2(-kLog2e * x[i]), e1 = 1.0f + ex2(-kLog2e * x[i + 1]);
+      const float r = rcp(e0 * e1);
+      x[i] = r * e1;
+      x[i + 1] = r * e0;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) x[i] = rcp(1.0f + ex2(-kLog2e * x[i]));
   }
-  return two(rcp(e0), rcp(e1));
 }
 
 // Scores of one row in place, and the row's sums.  On return x holds the terms u_e of the lane
 // (scaled by a factor of its own for softmax), `scale` turns a term into a probability, and
-// `dot` is sum over e of p_e g_e (kDot).  xchg: [2][W] float4 of the group, buffer `buf`.
+// `dot` is sum over e of p_e g_e (kDot).  xchg: [2][W] float4 of the group, buffer `buf`; bit v of
+// `past`: the lane's v-th vector of 8 columns lies past E.
 // A softmax lane takes 2^(x log2 e - m), m its own maximum times log2 e as rounded, and the
 // reduction rescales by differences of those same m: nothing is lost to the rounding of m.
+// (Two values per instruction, .f32x2, was tried: packing the exponentials cost what it saved.)
 template <int NC, bool kSoftmax, bool kDot>
-__device__ __forceinline__ void row_terms(Two (&x)[NC / 2], const Two (&g)[kDot ? NC / 2 : 1],
-                                          int W, int grp, int gw, float4* xchg, int buf,
-                                          float& scale, float& dot) {
-  constexpr int N2 = NC / 2;
+__device__ __forceinline__ void row_terms(float (&x)[NC], const float (&g)[kDot ? NC : 1],
+                                          unsigned past, int W, int grp, int gw, float4* xchg, int buf, float& scale,
+                                          float& dot) {
   float m = 0.0f;
   if constexpr (kSoftmax) {
-    float top[4] = {kLowest, kLowest, kLowest, kLowest};
+    float top[2] = {kLowest, kLowest};
 #pragma unroll
-    for (int i = 0; i < N2; ++i) {
-      float lo, hi;
-      halves(x[i], lo, hi);
-      top[i & 3] = max3(top[i & 3], lo, hi);
+    for (int i = 0; i < NC; i += 4) {
+      top[0] = max3(top[0], x[i], x[i + 1]);
+      top[1] = max3(top[1], x[i + 2], x[i + 3]);
     }
-    m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+    m = fmaxf(top[0], top[1]);
     if (!(fabsf(m) <= kFarLogit)) {  // also lanes of -inf alone
       m = fminf(fmaxf(m, -kFarLogit), kFarLogit);
 #pragma unroll
-      for (int i = 0; i < N2; ++i) {
-        float lo, hi;
-        halves(x[i], lo, hi);
-        lo = lo == -INFINITY ? lo : fminf(fmaxf(lo, -kFarLogit), kFarLogit);
-        hi = hi == -INFINITY ? hi : fminf(fmaxf(hi, -kFarLogit), kFarLogit);
-        x[i] = two(lo, hi);
-      }
+      for (int i = 0; i < NC; ++i)
+        x[i] = x[i] == -INFINITY ? x[i] : fminf(fmaxf(x[i], -kFarLogit), kFarLogit);
     }
     m *= kLog2e;
-    const Two l = two(kLog2e, kLog2e), mm = two(-m, -m);
 #pragma unroll
-    for (int i = 0; i < N2; ++i) {
-      float lo, hi;
-      halves(fma2(x[i], l, mm), lo, hi);
-      x[i] = two(ex2(lo), ex2(hi));
-    }
+    for (int i = 0; i < NC; ++i) x[i] = ex2(fmaf(x[i], kLog2e, -m));
   } else {
-#pragma unroll
-    for (int i = 0; i < N2; ++i) x[i] = sigmoid2(x[i]);
+    sigmoids<NC>(x);
   }
-  Two s0 = 0ull, s1 = 0ull, d0 = 0ull, d1 = 0ull;
+  float sum = 0.0f, d4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-  for (int i = 0; i < N2; i += 2) {
-    s0 = add2(s0, x[i]);
-    s1 = add2(s1, x[i + 1]);
-    if constexpr (kDot) {
-      d0 = fma2(x[i], g[i], d0);
-      d1 = fma2(x[i + 1], g[i + 1], d1);
+  for (int v = 0; v < NC / 8; ++v) {
+    float s0 = x[8 * v], s1 = x[8 * v + 1];
+#pragma unroll
+    for (int i = 2; i < 8; i += 2) {
+      s0 += x[8 * v + i];
+      s1 += x[8 * v + i + 1];
     }
+    if (kSoftmax || ((past >> v) & 1u) == 0u) sum += s0 + s1;
   }
-  float sum = sum2(add2(s0, s1)), sg = kDot ? sum2(add2(d0, d1)) : 0.0f;
+  if constexpr (kDot) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) d4[i & 3] = fmaf(x[i], g[i], d4[i & 3]);
+  }
+  float sg = (d4[0] + d4[1]) + (d4[2] + d4[3]);
   float f = 1.0f;  // the lane's factor
   if constexpr (kSoftmax) {
     const float M = warp_max(m);
     f = ex2(m - M);
     sum *= f;
-    if constexpr (kDot) sg *= f;
+    sg *= f;
     m = M;
   }
-  sum = warp_sum(sum);
-  if constexpr (kDot) sg = warp_sum(sg);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) {
+    sum += __shfl_xor_sync(kFull, sum, d);
+    if constexpr (kDot) sg += __shfl_xor_sync(kFull, sg, d);
+  }
   if (W > 1) {
     float4* slot = xchg + buf * W;
     if ((threadIdx.x & 31) == 0) slot[gw] = make_float4(m, sum, sg, 0.0f);
@@ -339,7 +334,7 @@ __device__ __forceinline__ void row_terms(Two (&x)[NC / 2], const Two (&g)[kDot 
     }
     if constexpr (kSoftmax) f *= ex2(m - M);
   }
-  const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+  const float inv = sum > 0.0f ? rcp(sum) : 0.0f;
   scale = f * inv;
   dot = sg * inv;
 }
@@ -352,11 +347,12 @@ __global__ void __launch_bounds__(kBalThreads, 1) mrs_balance_rows_kernel(const 
   float* red = reinterpret_cast<float*>(smem + row_smem<NC, kVec>()) - kBalThreads * NC;
   int* hist = reinterpret_cast<int*>(smem + row_smem<NC, kVec>());  // [E]
   const int tid = threadIdx.x, warp = tid >> 5, W = a.W, E = a.E;
-  const int grp = warp / W, gw = warp - grp * W, groups = kBalWarps / W;
+  const int grp = warp / W, gw = warp - grp * W, groups = groups_of(W);
   const int lanes = 32 * W, lane = 32 * gw + (tid & 31);
   const bool idle = grp >= groups;  // a W that does not divide the warps leaves some without a group
   float4* xchg = &xchg_s[0][0] + grp * 2 * W;
   const uint32_t ring = smem_u32(smem) + 16 * tid;
+  const unsigned past = vectors_past<NC, kVec>(E, lane, lanes);
   pdl_trigger();
   for (int e = tid; e < E; e += kBalThreads) hist[e] = 0;
   pdl_wait();
@@ -365,7 +361,7 @@ __global__ void __launch_bounds__(kBalThreads, 1) mrs_balance_rows_kernel(const 
 
   const int t0 = min(static_cast<int>(blockIdx.x) * a.tpc, a.T);
   const int t1 = min(a.T - t0, a.tpc) + t0;
-  Two g0[1] = {0ull};
+  float g0[1] = {0.0f};
   float loss = 0.0f;  // solo: this thread's experts
   int t = t0;
   for (int i = a.solo ? 0 : seq_behind(a.offsets, a.S, a.T, t0); i < a.S && (t < t1 || a.solo);
@@ -381,7 +377,7 @@ __global__ void __launch_bounds__(kBalThreads, 1) mrs_balance_rows_kernel(const 
       continue;
     }
     t = hi;
-    RowStream<NC, kVec> rows;
+    RowStream<NC, kVec, kSoftmax> rows;
     int row = lo + grp;
     if (!idle) rows.open(a.logits, E, row, groups, hi, lane, lanes, ring);
     // counts of the stretch
@@ -391,30 +387,24 @@ __global__ void __launch_bounds__(kBalThreads, 1) mrs_balance_rows_kernel(const 
       if (e >= 0 && e < E) atomicAdd(hist + e, 1);  // integers: any order, the same sum
     }
     if (!idle && row < hi) {
-      Two acc[NC / 2];
+      float acc[NC];
 #pragma unroll
-      for (int c = 0; c < NC / 2; ++c) acc[c] = 0ull;
+      for (int c = 0; c < NC; ++c) acc[c] = 0.0f;
       for (int buf = 0; row < hi; row += groups, buf ^= 1) {
-        Two x[NC / 2];
-        float scale, dot;
+        float x[NC], scale, dot;
         rows.take(a.logits, E, row, groups, hi, lane, lanes, x);
-        row_terms<NC, kSoftmax, false>(x, g0, W, grp, gw, xchg, buf, scale, dot);
-        const Two by = two(scale, scale);
+        row_terms<NC, kSoftmax, false>(x, g0, past, W, grp, gw, xchg, buf, scale, dot);
 #pragma unroll
-        for (int c = 0; c < NC / 2; ++c) acc[c] = fma2(x[c], by, acc[c]);
+        for (int c = 0; c < NC; ++c) acc[c] = fmaf(x[c], scale, acc[c]);
       }
       float* mine = red + static_cast<size_t>(grp) * lanes * NC;
 #pragma unroll
-      for (int c = 0; c < NC / 2; ++c) {
-        const int at = column_of<kVec>(2 * c, lane, lanes);
-        float lo, hi;
-        halves(acc[c], lo, hi);
-        if constexpr (kVec) {
-          *reinterpret_cast<float2*>(mine + at) = make_float2(lo, hi);
-        } else {
-          mine[at] = lo;
-          mine[at + lanes] = hi;
-        }
+      for (int c = 0; c < NC; c += kVec ? 4 : 1) {
+        float* to = mine + column_of<kVec>(c, lane, lanes);
+        if constexpr (kVec)
+          *reinterpret_cast<float4*>(to) = make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
+        else
+          *to = acc[c];
       }
     }
     copy_wait_all();
@@ -519,7 +509,7 @@ __global__ void __launch_bounds__(kBalThreads, 1)
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ float4 xchg_s[kBalWarps][2];
   const int tid = threadIdx.x, warp = tid >> 5, W = a.W, E = a.E, K = a.K, wl = tid & 31;
-  const int grp = warp / W, gw = warp - grp * W, groups = kBalWarps / W;
+  const int grp = warp / W, gw = warp - grp * W, groups = groups_of(W);
   const int lanes = 32 * W, lane = 32 * gw + wl;
   float4* xchg = &xchg_s[0][0] + grp * 2 * W;
   // the routed experts' part of the group's current row, zero elsewhere; a warp only touches the
@@ -527,6 +517,7 @@ __global__ void __launch_bounds__(kBalThreads, 1)
   float* add = reinterpret_cast<float*>(smem + row_smem<NC, kVec>()) - kBalThreads * NC +
                static_cast<size_t>(grp) * lanes * NC;
   const uint32_t ring = smem_u32(smem) + 16 * tid;
+  const unsigned past = vectors_past<NC, kVec>(E, lane, lanes);
   pdl_trigger();
   if (grp >= groups) return;  // a W that does not divide the warps leaves some without a group
 #pragma unroll
@@ -555,21 +546,19 @@ __global__ void __launch_bounds__(kBalThreads, 1)
       in_seq = lo_i <= t;
       hi = min(t1, in_seq ? hi_i : lo_i);
     }
-    Two g[NC / 2];
+    float g[NC];
 #pragma unroll
-    for (int c = 0; c < NC / 2; ++c) g[c] = 0ull;
+    for (int c = 0; c < NC; ++c) g[c] = 0.0f;
     if (dense && in_seq) {
       const float n = static_cast<float>(hi_i - lo_i);
       const float f = gl * (a.coef / a.S) * (static_cast<float>(E) / K) / n / n;
-      auto of = [&](int c) {
-        const int e = column_of<kVec>(c, lane, lanes);
-        return e < E ? f * static_cast<float>(__ldg(a.counts + static_cast<size_t>(i) * E + e))
-                     : 0.0f;
-      };
 #pragma unroll
-      for (int c = 0; c < NC / 2; ++c) g[c] = two(of(2 * c), of(2 * c + 1));
+      for (int c = 0; c < NC; ++c) {
+        const int e = column_of<kVec>(c, lane, lanes);
+        if (e < E) g[c] = f * static_cast<float>(__ldg(a.counts + static_cast<size_t>(i) * E + e));
+      }
     }
-    RowStream<NC, kVec> rows;
+    RowStream<NC, kVec, kSoftmax> rows;
     int row = t + grp;
     int next_id = -1;
     float next_gw = 0.0f;
@@ -583,7 +572,7 @@ __global__ void __launch_bounds__(kBalThreads, 1)
     fetch(row);
     for (; row < hi; row += groups) {
       const uint16_t* xr = a.logits + static_cast<size_t>(row) * E;
-      Two x[NC / 2];
+      float x[NC];
       int id = next_id;
       float wg = next_gw;
       const bool valid = sparse && wl < K && id >= 0 && id < E;
@@ -592,18 +581,16 @@ __global__ void __launch_bounds__(kBalThreads, 1)
       rows.take(a.logits, E, row, groups, hi, lane, lanes, x);
       float scale = 0.0f, dot = 0.0f;
       if (dense) {
-        row_terms<NC, kSoftmax, true>(x, g, W, grp, gw, xchg, buf, scale, dot);
+        row_terms<NC, kSoftmax, true>(x, g, past, W, grp, gw, xchg, buf, scale, dot);
         buf ^= 1;
-        const Two by = two(scale, scale), less = two(-dot, -dot);
-        const Two one = two(1.0f, 1.0f), minus = two(-1.0f, -1.0f);
 #pragma unroll
-        for (int c = 0; c < NC / 2; ++c) {
-          const Two p = mul2(x[c], by), d = add2(g[c], less);
-          x[c] = kSoftmax ? mul2(p, d) : mul2(mul2(p, fma2(x[c], minus, one)), d);
+        for (int c = 0; c < NC; ++c) {
+          const float p = x[c] * scale;
+          x[c] = (kSoftmax ? p : fmaf(-p, x[c], p)) * (g[c] - dot);
         }
       } else {
 #pragma unroll
-        for (int c = 0; c < NC / 2; ++c) x[c] = 0ull;
+        for (int c = 0; c < NC; ++c) x[c] = 0.0f;
       }
       if (sparse) {
         // every warp of the group works the K routes out, and keeps those in its columns
@@ -637,18 +624,16 @@ __global__ void __launch_bounds__(kBalThreads, 1)
         __syncwarp();
         if constexpr (kVec) {
 #pragma unroll
-          for (int v = 0; v < NC / 8; ++v) {
-            const float4* q = reinterpret_cast<const float4*>(add + 8 * (v * lanes + lane));
-            const float4 p0 = q[0], p1 = q[1];
-            x[4 * v] = add2(x[4 * v], two(p0.x, p0.y));
-            x[4 * v + 1] = add2(x[4 * v + 1], two(p0.z, p0.w));
-            x[4 * v + 2] = add2(x[4 * v + 2], two(p1.x, p1.y));
-            x[4 * v + 3] = add2(x[4 * v + 3], two(p1.z, p1.w));
+          for (int c = 0; c < NC; c += 4) {
+            const float4 q = *reinterpret_cast<const float4*>(add + column_of<kVec>(c, lane, lanes));
+            x[c] += q.x;
+            x[c + 1] += q.y;
+            x[c + 2] += q.z;
+            x[c + 3] += q.w;
           }
         } else {
 #pragma unroll
-          for (int c = 0; c < NC / 2; ++c)
-            x[c] = add2(x[c], two(add[2 * c * lanes + lane], add[(2 * c + 1) * lanes + lane]));
+          for (int c = 0; c < NC; ++c) x[c] += add[column_of<kVec>(c, lane, lanes)];
         }
         __syncwarp();
         if (put) add[id] = 0.0f;
@@ -659,9 +644,7 @@ __global__ void __launch_bounds__(kBalThreads, 1)
         for (int v = 0; v < NC / 8; ++v) {
           const int c = 8 * (v * lanes + lane);
           if (c >= E) continue;
-          float y[8];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) halves(x[4 * v + j], y[2 * j], y[2 * j + 1]);
+          const float* y = x + 8 * v;
           if constexpr (sizeof(Out) == 4) {
             float4* o = reinterpret_cast<float4*>(out + c);
             o[0] = make_float4(y[0], y[1], y[2], y[3]);
@@ -681,12 +664,9 @@ __global__ void __launch_bounds__(kBalThreads, 1)
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
           const int e = c * lanes + lane;
-          float lo, hi;
-          halves(x[c / 2], lo, hi);
-          const float y = (c & 1) ? hi : lo;
           if (e >= E) continue;
-          if constexpr (sizeof(Out) == 4) out[e] = y;
-          else out[e] = __float2bfloat16_rn(y);
+          if constexpr (sizeof(Out) == 4) out[e] = x[c];
+          else out[e] = __float2bfloat16_rn(x[c]);
         }
       }
     }
@@ -700,7 +680,9 @@ namespace {
 
 // Warps per row, columns per lane and the kind of loads for E experts.  16-byte loads need rows
 // that start on 16 bytes (E a multiple of 8); without them a lane's next row is in registers, and
-// more than 16 columns would not fit there.
+// more than 16 columns would not fit there.  (The kernels are bound by the instructions they
+// issue, a third of them per row and not per column: twice the warps with half the columns took
+// T = 16384, E = 4096 from 45 to 50 us.)
 struct RowPlan {
   int W, NC;
   bool vec;
@@ -716,7 +698,7 @@ RowPlan row_plan(int E) {
 
 // Tokens per CTA: one row per group of warps until every SM has a CTA.
 int tokens_per_cta(int T, int W, int sms) {
-  const int groups = kBalWarps / W;
+  const int groups = groups_of(W);
   int ctas = sms < kBalMaxCtas ? sms : kBalMaxCtas;
   const int most = (T + groups - 1) / groups;
   if (most < ctas) ctas = most;
@@ -775,15 +757,13 @@ cudaError_t launch_backward(const RouteBackwardArgs& a, bool softmax, int ctas, 
 // The kernels' instances: 8, 16 or 32 columns per lane in vectors, 8 or 16 without.
 template <class Go>
 cudaError_t with_plan(const RowPlan& p, Go go) {
-  using std::integral_constant;
-  using Vec = std::true_type;
-  using One = std::false_type;
-  if (!p.vec)
-    return p.NC == 8 ? go(integral_constant<int, 8>{}, One{})
-                     : go(integral_constant<int, 16>{}, One{});
-  return p.NC == 8    ? go(integral_constant<int, 8>{}, Vec{})
-         : p.NC == 16 ? go(integral_constant<int, 16>{}, Vec{})
-                      : go(integral_constant<int, 32>{}, Vec{});
+  using N8 = std::integral_constant<int, 8>;
+  using N16 = std::integral_constant<int, 16>;
+  using N32 = std::integral_constant<int, 32>;
+  if (!p.vec) return p.NC == 8 ? go(N8{}, std::false_type{}) : go(N16{}, std::false_type{});
+  return p.NC == 8    ? go(N8{}, std::true_type{})
+         : p.NC == 16 ? go(N16{}, std::true_type{})
+                      : go(N32{}, std::true_type{});
 }
 
 }  // namespace
@@ -835,7 +815,7 @@ int moe_balance_loss(const void* logits_bf16, const int32_t* topk_ids, const int
   a.K = topk;
   a.S = n_seq;
   a.W = p.W;
-  const int groups = kBalWarps / p.W;
+  const int groups = groups_of(p.W);
   a.solo = T <= kSoloRows * groups && n_seq <= kSoloSeqs;
   a.tpc = a.solo || T == 0 ? (T > 0 ? T : 1) : tokens_per_cta(T, p.W, sms);
   a.coef = coef;
