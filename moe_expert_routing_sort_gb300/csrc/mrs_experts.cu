@@ -7,29 +7,35 @@
 // (1 without weights) is applied in fp32, and the result is rounded once to the output type.
 //
 // One tile is the rows of one block (the M side of the tensor-core product, 128 lanes of tensor
-// memory; blocks of more rows are cut, blocks of fewer leave lanes unused) by 128 outputs of its
-// expert (the N side).  Rows on the lanes make the result a row per thread, so the outputs leave
-// as 32-byte stores of whole sectors; a block of 16 rows costs the tensor core as much as one of
-// 128, which it has time for: such calls wait for the weights.  A persistent CTA per SM takes
-// tiles round robin, the output tiles of a block next to each other, so the SMs share a block's
-// rows and an expert's weights in L2.  Steps of 256 columns (128 bytes a row) go through a ring of
-// shared-memory stages; the warps of a CTA each have one task:
-//   0      copies the weights' 128 rows (a tensor copy, in the 128-byte swizzle that
-//          the tensor core reads)
-//   1      copies the step's scales to tensor memory and issues four products of 64
-//          columns; the tensor core applies the scales and adds into fp32 in tensor memory
+// memory; blocks of more rows are cut, blocks of fewer leave lanes unused) by BN = 128 or 192
+// outputs of its expert (the N side).  Rows on the lanes make the result a row per thread, so the
+// outputs leave as 32-byte stores of whole sectors; a block of 16 rows costs the tensor core as
+// much as one of 128, which it has time for: such calls wait for the weights.  A persistent CTA
+// per SM takes units round robin, a unit being one tile, or for short rows several output tiles of
+// one block; neighbours share a block's rows and an expert's weights in L2.
+//
+// Steps of 256 columns (128 bytes a row) go through two rings of shared-memory slots, one of rows
+// and one of weights; a unit of several tiles keeps its rows' slots until its last tile.  The
+// warps of a CTA each have one task:
+//   0      copies the weights (a tensor copy, in the 128-byte swizzle that the tensor core reads)
+//   1      copies a step's scales to tensor memory and issues four products of 64 columns; the
+//          tensor core applies the scales and adds into fp32 in tensor memory
 //   4-7    a finished tile from tensor memory to the output rows, while the next one is computed
 //          (two accumulators)
-//   8-11   the block's rows, 16 bytes a thread into the same swizzle; the copies arrive on the
-//          stage's barrier themselves, so the whole ring is in flight.  (Gathered by tensor copies
-//          of four rows each they took 37 ns a copy: 1.2 us a step of 128 rows, against 0.14 us
-//          of products.)
-//   12-15  the scales of rows and weights, from row-major bytes to the order that tensor memory
-//          wants (row r of 128: lane r % 32, word r / 32 of 4 scales)
-// Each task has the list entries of the next two tiles and the first scales of the next one in
-// flight, so a tile of two steps does not wait for them.  Every wait is bounded; a wait that gives
-// up ends its warp's task with the status bit set, and the CTA leaves once nothing of its own is
-// in flight.
+//   8-11   the block's rows, 16 bytes a thread into the same swizzle (the copies arrive on the
+//          slot's barrier themselves), and their scales
+//   12-15  the weights' scales
+// Scales go from row-major bytes to the order that tensor memory wants: row r of 128 on lane
+// r % 32, word r / 32 of 4 scales.
+//
+// What bounds it: an SM takes in at most 38 bytes a clock (measured, tensor copies, thread copies
+// and multicast alike, on one SM and on all), so a step of 128 x 128 costs 890 clocks and its
+// products 260; hence the wider tile, and rows that stay.  Few tokens are bound by HBM, which
+// gives an SM 23 bytes a clock.
+//
+// Each task has the list entries of the next two units and the first scales of the next one in
+// flight.  Every wait is bounded; a wait that gives up ends its warp's task with the status bit
+// set, and the CTA leaves once nothing of its own is in flight.
 #include <cuda_bf16.h>
 
 #include "mrs_args.h"
@@ -49,40 +55,64 @@ struct ExpertsArgs {
   unsigned long long wait_limit_ns;
   int routes, topk, per_route;
   int E, K, N, B, scols, max_rows;
-  int sub, subs;   // rows of a tile (<= 128), tiles along a block's rows
-  int ntile;       // tiles along the outputs
-  int ksteps;      // steps of 256 columns
-  int wide_scales; // scale rows start on 16 bytes
-  int wide_out;    // output rows start on 32 bytes
+  int sub, subs;    // rows of a tile (<= 128), tiles along a block's rows
+  int ntile;        // tiles along the outputs
+  int chunk;        // tiles of a unit (the last of a block may have fewer)
+  int nchunk;       // units along the outputs
+  int ksteps;       // steps of 256 columns
+  int wide_scales;  // scale rows start on 16 bytes
+  int wide_out;     // output rows start on 32 bytes
 };
 
 constexpr int kExpThreads = 512;  // warps 2 and 3 only fill the quarter of the epilogue's lanes
-constexpr int kExpRows = 128;      // lanes of a tile: rows of a block
-constexpr int kExpOuts = 128;      // outputs of a tile
-constexpr int kStepBytes = 128;    // bytes of a row per step
-constexpr int kXBytes = kExpRows * kStepBytes;
-constexpr int kWBytes = kExpOuts * kStepBytes;
-constexpr int kScaleBytes = 2048;  // rows' and weights' scales of a step: 2 x 2 x 512
-constexpr int kStageBytes = kXBytes + kWBytes + kScaleBytes;
-constexpr int kStages = 6;         // what fits in 227 KB
-constexpr size_t kExpSmem = static_cast<size_t>(kStages) * kStageBytes + 1024;
-constexpr int kTmemCols = 512;     // 2 accumulators of 128 columns, 16 of scales per stage
-constexpr int kTmemScales = 2 * kExpOuts;
+constexpr int kExpRows = 128;     // lanes of a tile: rows of a block
+constexpr int kStepBytes = 128;   // bytes of a row per step
+constexpr int kTmemCols = 512;
 
-// A tile of the list: its expert id is in flight or here (-1 past the last tile).
-struct ExpertsTile {
-  int it, p0, n0, e;
-  __device__ __forceinline__ void at(const ExpertsArgs& a, int i, int tiles) {
+// Slots of both rings and the places of everything, for tiles of BN outputs.
+template <int BN>
+struct ExpertsShape {
+  static constexpr int kAtoms = (BN + 127) / 128;             // scales come for 128 rows at a time
+  static constexpr int kX = kExpRows * kStepBytes;            // rows of a slot
+  static constexpr int kXSlot = kX + 2 * 512;                 // and their scales
+  static constexpr int kW = BN * kStepBytes;
+  static constexpr int kWSlot = kW + 2 * 512 * kAtoms;
+  static constexpr int kSlots = BN == 128 ? 6 : 5;            // what fits in 227 KB
+  static constexpr size_t kSmem = static_cast<size_t>(kSlots) * (kXSlot + kWSlot) + 1024;
+  // tensor memory: two accumulators, then the scales of each slot
+  static constexpr int kXScales = 2 * BN;
+  static constexpr int kWScales = kXScales + 8 * kSlots;
+  static_assert(kWScales + 8 * kAtoms * kSlots <= kTmemCols, "");
+};
+
+// A unit of the list: its expert id is in flight or here (-1 past the last unit).
+struct ExpertsUnit {
+  int it, p0, n0, tiles, e;
+  __device__ __forceinline__ void at(const ExpertsArgs& a, int i, int units, int bn) {
     it = i;
-    const int b = i / a.ntile;
-    n0 = (i - b * a.ntile) * kExpOuts;
+    const int b = i / a.nchunk, first = (i - b * a.nchunk) * a.chunk;
+    n0 = first * bn;
+    tiles = min(a.chunk, a.ntile - first);
     p0 = b * a.sub;
-    e = i < tiles ? __ldg(a.eid + b / a.subs) : -1;
+    e = i < units ? __ldg(a.eid + b / a.subs) : -1;
   }
   __device__ __forceinline__ bool valid(const ExpertsArgs& a) const { return e >= 0 && e < a.E; }
-  // Entry i of the tile's rows (-1: a lane unused, or past the last tile).
-  __device__ __forceinline__ int entry(const ExpertsArgs& a, int i, int tiles) const {
-    return (it < tiles && i < a.sub) ? __ldg(a.sid + p0 + i) : -1;
+  // Entry i of the unit's rows (-1: a lane unused, or past the last unit).
+  __device__ __forceinline__ int entry(const ExpertsArgs& a, int i, int units) const {
+    return (it < units && i < a.sub) ? __ldg(a.sid + p0 + i) : -1;
+  }
+};
+
+// A place in a ring of S slots, and the parity of its round.
+template <int S>
+struct RingPlace {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void advance() {
+    if (++slot == S) {
+      slot = 0;
+      phase ^= 1u;
+    }
   }
 };
 
@@ -114,22 +144,29 @@ __device__ __forceinline__ void store_shared(uint32_t dst, uint32_t v) {
 // Where the scales of row r of 128 start in a step's 512 bytes.
 __device__ __forceinline__ uint32_t scale_place(int r) { return 16 * (r & 31) + 4 * (r >> 5); }
 
-template <class Out>
+template <int BN, class Out>
 __global__ void __launch_bounds__(kExpThreads, 1)
     mrs_experts_kernel(const __grid_constant__ CUtensorMap wmap, const ExpertsArgs a) {
+  using Sh = ExpertsShape<BN>;
+  constexpr int S = Sh::kSlots;
   extern __shared__ unsigned char smem_raw[];
-  __shared__ unsigned long long full_s[kStages], empty_s[kStages], acc_full_s[2], acc_free_s[2],
-      done_s;
+  __shared__ unsigned long long xfull_s[S], xfree_s[S], wfull_s[S], wfree_s[S], acc_full_s[2],
+      acc_free_s[2], done_s;
   __shared__ uint32_t tmem_s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  // the operands' tiles first: each starts on 1024 bytes
+  const uint32_t xbase = base, wbase = base + S * Sh::kX;
+  const uint32_t xscales = wbase + S * Sh::kW, wscales = xscales + S * 1024;
   const unsigned long long limit = a.wait_limit_ns;
+  const int copiers = (a.sub + 31) / 32;  // warps with rows of the block
   pdl_trigger();
   if (tid == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      // the weights' copy, the scales' four warps, the threads of the warps that copy rows
-      mbar_init(&full_s[s], 1 + 4 + 32 * ((a.sub + 31) / 32));
-      mbar_init(&empty_s[s], 1);
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&xfull_s[s], 33 * copiers);  // every copying thread, and each warp for its scales
+      mbar_init(&xfree_s[s], 1);
+      mbar_init(&wfull_s[s], 1 + 4);  // the weights' copy, and the scales' four warps
+      mbar_init(&wfree_s[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full_s[b], 1);
@@ -145,89 +182,101 @@ __global__ void __launch_bounds__(kExpThreads, 1)
   const uint32_t tmem = tmem_s;
   pdl_wait();
 
+  // the first unit's list entries do not wait for the list's length
+  const int most = a.max_rows / a.B * a.subs * a.nchunk, step = gridDim.x;
+  ExpertsUnit t, n;
+  t.at(a, blockIdx.x, most, BN);
+  const int my_row = 32 * (warp & 3) + lane;  // of warps 4-7 and 8-11
+  int entry = warp >= 4 && warp < 12 ? t.entry(a, my_row, most) : -1;
   const int rows = min(max(__ldg(a.npp), 0), a.max_rows);
-  const int tiles = rows / a.B * a.subs * a.ntile;
-  const int step = gridDim.x;
+  const int units = rows / a.B * a.subs * a.nchunk;
   bool ok = true;
-  int stage = 0;
-  uint32_t phase = 0;  // parity of the ring's current round
-  auto advance = [&] {
-    if (++stage == kStages) {
-      stage = 0;
-      phase ^= 1u;
-    }
-  };
-  ExpertsTile t, n;
-  t.at(a, blockIdx.x, tiles);
+  RingPlace<S> x, w;
 
   if (warp == 0) {
     long long issued = 0;
-    for (; ok && t.it < tiles; t = n) {
-      n.at(a, t.it + step, tiles);
+    for (; ok && t.it < units; t = n) {
+      n.at(a, t.it + step, units, BN);
       if (!t.valid(a)) {
         if (lane == 0) atomicOr(a.status, MOE_RS_DEVICE_BAD_EXPERT_ID);
         continue;
       }
-      for (int ks = 0; ks < a.ksteps; ++ks) {
-        ok = warp_wait(&empty_s[stage], phase ^ 1u, limit);
-        if (!ok) break;
-        if (elect_one()) {
-          mbar_expect(&full_s[stage], kWBytes);
-          tma_load_3d(base + stage * kStageBytes + kXBytes, &wmap, ks * kStepBytes, t.n0, t.e,
-                      &full_s[stage]);
+      for (int c = 0; ok && c < t.tiles; ++c) {
+        for (int ks = 0; ks < a.ksteps; ++ks) {
+          ok = warp_wait(&wfree_s[w.slot], w.phase ^ 1u, limit);
+          if (!ok) break;
+          if (elect_one()) {
+            mbar_expect(&wfull_s[w.slot], Sh::kW);
+            tma_load_3d(wbase + w.slot * Sh::kW, &wmap, ks * kStepBytes, t.n0 + c * BN, t.e,
+                        &wfull_s[w.slot]);
+          }
+          __syncwarp();
+          ++issued;
+          w.advance();
         }
-        __syncwarp();
-        ++issued;
-        advance();
       }
     }
     if (!ok) {
       // a copy still on its way must land before the CTA leaves; the phase it completes may be
       // missing other arrivals, so this waits for what has no one to take it any more
-      for (long long q = issued > kStages ? issued - kStages : 0; q < issued; ++q)
-        warp_wait(&full_s[q % kStages], static_cast<uint32_t>(q / kStages) & 1u, kWaitLimitNs);
+      for (long long q = issued > S ? issued - S : 0; q < issued; ++q)
+        warp_wait(&wfull_s[q % S], static_cast<uint32_t>(q / S) & 1u, kWaitLimitNs);
     }
   } else if (warp == 1) {
     int buf = 0;
     uint32_t acc_phase = 0;
     bool any = false;
-    for (; ok && t.it < tiles; t = n) {
-      n.at(a, t.it + step, tiles);
+    for (; ok && t.it < units; t = n) {
+      n.at(a, t.it + step, units, BN);
       if (!t.valid(a)) continue;
-      ok = warp_wait(&acc_free_s[buf], acc_phase ^ 1u, limit);
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t d = tmem + buf * kExpOuts;
-      for (int ks = 0; ks < a.ksteps; ++ks) {
-        ok = warp_wait(&full_s[stage], phase, limit);
+      RingPlace<S> xs = x;
+      for (int c = 0; ok && c < t.tiles; ++c) {
+        ok = warp_wait(&acc_free_s[buf], acc_phase ^ 1u, limit);
         if (!ok) break;
         tc_fence_after();
-        fence_proxy_async_smem();  // the rows were written by threads
-        const uint32_t src = base + stage * kStageBytes, sc = src + kXBytes + kWBytes;
-        const uint32_t ts = tmem + kTmemScales + stage * 16;
-        const uint64_t dx = desc_rows128(src), dw = desc_rows128(src + kXBytes);
-        const int parts = (a.K - 256 * ks + 63) >> 6;
-        if (elect_one()) {
+        const uint32_t d = tmem + buf * BN;
+        xs = x;  // every tile of the unit takes the same rows
+        for (int ks = 0; ks < a.ksteps; ++ks) {
+          ok = __all_sync(kFull, (c > 0 || thread_wait(&xfull_s[xs.slot], xs.phase, limit)) &&
+                                     thread_wait(&wfull_s[w.slot], w.phase, limit));
+          if (!ok) break;
+          tc_fence_after();
+          if (c == 0) fence_proxy_async_smem();  // the rows were written by threads
+          const uint32_t xsc = xscales + xs.slot * 1024;
+          const uint32_t wsc = wscales + w.slot * (1024 * Sh::kAtoms);
+          const uint32_t tx = tmem + Sh::kXScales + xs.slot * 8;
+          const uint32_t tw = tmem + Sh::kWScales + w.slot * (8 * Sh::kAtoms);
+          const uint64_t dx = desc_rows128(xbase + xs.slot * Sh::kX);
+          const uint64_t dw = desc_rows128(wbase + w.slot * Sh::kW);
+          const int parts = (a.K - 256 * ks + 63) >> 6;
+          if (elect_one()) {
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            tc_copy_scales(ts + 4 * g, desc_scales(sc + 512 * g));
-            tc_copy_scales(ts + 8 + 4 * g, desc_scales(sc + 1024 + 512 * g));
+            for (int g = 0; g < 2; ++g) {
+              if (c == 0) tc_copy_scales(tx + 4 * g, desc_scales(xsc + 512 * g));
+#pragma unroll
+              for (int q = 0; q < Sh::kAtoms; ++q)
+                tc_copy_scales(tw + 4 * (Sh::kAtoms * g + q),
+                               desc_scales(wsc + 512 * (Sh::kAtoms * g + q)));
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              if (q < parts)  // else columns past K
+                // 32 bytes further along the swizzled rows: 2 units of 16
+                tc_mma_mxf4(d, dx + 2 * q, dw + 2 * q, mxf4_word(kExpRows, BN, (q & 1) * 2),
+                            tx + 4 * (q >> 1), tw + 4 * Sh::kAtoms * (q >> 1), ks > 0 || q > 0);
+            tc_commit(&wfree_s[w.slot]);
+            if (c + 1 == t.tiles) tc_commit(&xfree_s[xs.slot]);
+            if (ks + 1 == a.ksteps) tc_commit(&acc_full_s[buf]);
           }
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            if (q < parts)  // else columns past K
-              // 32 bytes further along the swizzled rows: 2 units of 16
-              tc_mma_mxf4(d, dx + 2 * q, dw + 2 * q, mxf4_word(kExpRows, kExpOuts, (q & 1) * 2),
-                          ts + 4 * (q >> 1), ts + 8 + 4 * (q >> 1), ks > 0 || q > 0);
-          tc_commit(&empty_s[stage]);
-          if (ks + 1 == a.ksteps) tc_commit(&acc_full_s[buf]);
+          __syncwarp();
+          any = true;
+          xs.advance();
+          w.advance();
         }
-        __syncwarp();
-        any = true;
-        advance();
+        buf ^= 1;
+        if (buf == 0) acc_phase ^= 1u;
       }
-      buf ^= 1;
-      if (buf == 0) acc_phase ^= 1u;
+      x = xs;
     }
     // nothing of the tensor core may be in flight when tensor memory is given back
     if (any) {
@@ -236,173 +285,206 @@ __global__ void __launch_bounds__(kExpThreads, 1)
       warp_wait(&done_s, 0, kWaitLimitNs);
     }
   } else if (warp >= 4 && warp < 8) {
-    const int i = 32 * (warp - 4) + lane;  // the thread's row of a tile
     const bool used = 32 * (warp - 4) < a.sub;
     int buf = 0;
     uint32_t acc_phase = 0;
-    int entry = t.entry(a, i, tiles);
-    for (; ok && t.it < tiles; t = n) {
-      n.at(a, t.it + step, tiles);
+    for (; ok && t.it < units; t = n) {
+      n.at(a, t.it + step, units, BN);
       const int r = entry;
-      entry = n.entry(a, i, tiles);
+      entry = n.entry(a, my_row, units);
       if (!t.valid(a)) continue;
       const bool put = r >= 0 && r < a.routes;
-      const float w = (a.sw != nullptr && put) ? __ldg(a.sw + t.p0 + i) : 1.0f;
-      ok = warp_wait(&acc_full_s[buf], acc_phase, limit);
-      if (!ok) break;
-      if (used) {
-        tc_fence_after();
-        const uint32_t src = tmem + buf * kExpOuts + (static_cast<uint32_t>(32 * (warp - 4)) << 16);
-        Out* out = static_cast<Out*>(a.out) + (put ? static_cast<size_t>(r) * a.N : 0) + t.n0;
-        const int left = a.N - t.n0;  // a multiple of 8
+      const float by = (a.sw != nullptr && put) ? __ldg(a.sw + t.p0 + my_row) : 1.0f;
+      for (int tile = 0; tile < t.tiles; ++tile) {
+        ok = warp_wait(&acc_full_s[buf], acc_phase, limit);
+        if (!ok) break;
+        if (used) {
+          tc_fence_after();
+          const uint32_t src = tmem + buf * BN + (static_cast<uint32_t>(32 * (warp - 4)) << 16);
+          const int n0 = t.n0 + tile * BN, left = a.N - n0;  // left: a multiple of 8
+          Out* out = static_cast<Out*>(a.out) + (put ? static_cast<size_t>(r) * a.N : 0) + n0;
 #pragma unroll
-        for (int c0 = 0; c0 < kExpOuts; c0 += 32) {
-          uint32_t v[32];
-          tmem_load32(src + c0, v);
-          if constexpr (sizeof(Out) == 4) {
+          for (int c0 = 0; c0 < BN; c0 += 32) {
+            if (c0 >= left) break;
+            uint32_t v[32];
+            tmem_load32(src + c0, v);
+            if constexpr (sizeof(Out) == 4) {
 #pragma unroll
-            for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(w * __uint_as_float(v[c]));
-          } else {
-#pragma unroll
-            for (int c = 0; c < 16; ++c) {
-              const __nv_bfloat162 h = __floats2bfloat162_rn(w * __uint_as_float(v[2 * c]),
-                                                             w * __uint_as_float(v[2 * c + 1]));
-              v[c] = *reinterpret_cast<const uint32_t*>(&h);
-            }
-          }
-          constexpr int kPer = 32 / sizeof(Out);  // outputs of 32 bytes
-#pragma unroll
-          for (int c = 0; put && c < 32 / kPer; ++c) {
-            const int at = c0 + kPer * c;
-            const uint32_t* q = v + 8 * c;
-            void* o = out + at;
-            if (a.wide_out && at + kPer <= left) {
-              asm volatile(
-                  "st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(o), "r"(q[0]),
-                  "r"(q[1]), "r"(q[2]), "r"(q[3]), "r"(q[4]), "r"(q[5]), "r"(q[6]), "r"(q[7])
-                  : "memory");
+              for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(by * __uint_as_float(v[c]));
             } else {
-              uint4* o4 = static_cast<uint4*>(o);
-              if (at + kPer / 2 <= left) o4[0] = make_uint4(q[0], q[1], q[2], q[3]);
-              if (at + kPer <= left) o4[1] = make_uint4(q[4], q[5], q[6], q[7]);
+#pragma unroll
+              for (int c = 0; c < 16; ++c) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(by * __uint_as_float(v[2 * c]),
+                                                               by * __uint_as_float(v[2 * c + 1]));
+                v[c] = *reinterpret_cast<const uint32_t*>(&h);
+              }
             }
+            constexpr int kPer = 32 / sizeof(Out);  // outputs of 32 bytes
+#pragma unroll
+            for (int c = 0; put && c < 32 / kPer; ++c) {
+              const int at = c0 + kPer * c;
+              const uint32_t* q = v + 8 * c;
+              void* o = out + at;
+              if (a.wide_out && at + kPer <= left) {
+                asm volatile(
+                    "st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(o),
+                    "r"(q[0]), "r"(q[1]), "r"(q[2]), "r"(q[3]), "r"(q[4]), "r"(q[5]), "r"(q[6]),
+                    "r"(q[7])
+                    : "memory");
+              } else {
+                uint4* o4 = static_cast<uint4*>(o);
+                if (at + kPer / 2 <= left) o4[0] = make_uint4(q[0], q[1], q[2], q[3]);
+                if (at + kPer <= left) o4[1] = make_uint4(q[4], q[5], q[6], q[7]);
+              }
+            }
+            __syncwarp();
           }
-          __syncwarp();
+          tc_fence_before();
         }
-        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&acc_free_s[buf]);
+        buf ^= 1;
+        if (buf == 0) acc_phase ^= 1u;
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&acc_free_s[buf]);
-      buf ^= 1;
-      if (buf == 0) acc_phase ^= 1u;
     }
   } else if (warp >= 8 && warp < 12) {
-    // warp w copies rows 32 w .. 32 w + 31 of the block, four rows (8 lanes each) at a time
+    // warp w copies rows 32 w .. 32 w + 31 of the block, four rows (8 lanes each) at a time, and
+    // lane l the scales of row 32 w + l
     const int w32 = 32 * (warp - 8);
     const int mine = min(a.sub - w32, 32);  // rows of this warp
     const int chunk = lane & 7, sub4 = lane >> 3;
     const size_t half = static_cast<size_t>(a.K / 2);
     // row 4 j + sub4 of the warp: two swizzles, for even and odd j
-    const uint32_t place = (w32 + sub4) * kStepBytes;
+    const uint32_t place = xbase + (w32 + sub4) * kStepBytes;
     const uint32_t even = place + 16 * (chunk ^ sub4), odd = place + 16 * (chunk ^ (sub4 + 4));
+    const uint32_t scale_at = xscales + scale_place(my_row);
     if (mine > 0) {
-      int entry = t.entry(a, w32 + lane, tiles);
-      for (; ok && t.it < tiles; t = n) {
-        n.at(a, t.it + step, tiles);
-        const int r = entry;
-        entry = n.entry(a, w32 + lane, tiles);
-        if (!t.valid(a)) continue;
-        const int src = r >= 0 && r < a.routes ? (a.per_route ? r : r / a.topk) : -1;
-        // rows that are no route keep what was there: any codes, in rows that are not stored
-        const unsigned char* from[8];
-        unsigned has = 0u;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int s = __shfl_sync(kFull, src, 4 * j + sub4);
-          from[j] = a.xc + static_cast<size_t>(max(s, 0)) * half + 16 * chunk;
-          has |= s >= 0 ? 1u << j : 0u;
-        }
-        for (int ks = 0; ks < a.ksteps; ++ks) {
-          ok = warp_wait(&empty_s[stage], phase ^ 1u, limit);
-          if (!ok) break;
-          const uint32_t dst = base + stage * kStageBytes;
-          // (columns past K keep what was there too: they meet weights that read as zero)
-          const unsigned live = ks * kStepBytes + 16 * chunk < a.K / 2 ? has : 0u;
+      auto source = [&](const ExpertsUnit& q, int r) -> int {
+        if (!q.valid(a) || r < 0 || r >= a.routes) return -1;
+        return a.per_route ? r : r / a.topk;
+      };
+      auto scales_of = [&](int s) -> const unsigned char* {
+        return s < 0 ? nullptr : a.xs + static_cast<size_t>(s) * a.scols;
+      };
+      ExpertsUnit f;
+      n.at(a, t.it + step, units, BN);
+      int src = source(t, entry);
+      entry = n.entry(a, my_row, units);
+      uint4 first = load_scales(scales_of(src), 0, a);
+      for (; ok && t.it < units; t = n, n = f) {
+        f.at(a, n.it + step, units, BN);
+        const int src_n = source(n, entry);
+        entry = f.entry(a, my_row, units);
+        const unsigned char* p = scales_of(src);
+        uint4 cur, nx = first, nn = load_scales(p, 1, a);
+        first = load_scales(scales_of(src_n), 0, a);
+        if (t.valid(a)) {
+          // rows that are no route keep what was there: any codes, in rows that are not stored
+          const unsigned char* from[8];
+          unsigned has = 0u;
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            if (4 * j >= mine) break;
-            if ((live >> j) & 1u) copy16(dst + ((j & 1) ? odd : even) + 512 * j, from[j]);
-            from[j] += kStepBytes;
+            const int s = __shfl_sync(kFull, src, 4 * j + sub4);
+            from[j] = a.xc + static_cast<size_t>(max(s, 0)) * half + 16 * chunk;
+            has |= s >= 0 ? 1u << j : 0u;
           }
-          copy_arrive(&full_s[stage]);
-          advance();
+          for (int ks = 0; ks < a.ksteps; ++ks) {
+            if ((ks & 1) == 0) {
+              cur = nx;
+              nx = nn;
+              nn = load_scales(p, ks / 2 + 2, a);
+            } else {
+              cur.x = cur.z;
+              cur.y = cur.w;
+            }
+            ok = warp_wait(&xfree_s[x.slot], x.phase ^ 1u, limit);
+            if (!ok) break;
+            const uint32_t dst = x.slot * Sh::kX;
+            // (columns past K keep what was there too: they meet weights that read as zero)
+            const unsigned live = ks * kStepBytes + 16 * chunk < a.K / 2 ? has : 0u;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              if (4 * j >= mine) break;
+              if ((live >> j) & 1u) copy16(dst + ((j & 1) ? odd : even) + 512 * j, from[j]);
+              from[j] += kStepBytes;
+            }
+            copy_arrive(&xfull_s[x.slot]);
+            const int left = a.K / 32 - 8 * ks;
+            store_shared(scale_at + x.slot * 1024, keep_scales(cur.x, left));
+            store_shared(scale_at + x.slot * 1024 + 512, keep_scales(cur.y, left - 4));
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&xfull_s[x.slot]);
+            x.advance();
+          }
         }
+        src = src_n;
       }
       copy_wait_all();
     }
   } else if (warp >= 12) {
-    // a thread has one row of the block and one of the weights
+    // a thread has one row of the weights, and the first 64 one of the second 128
     const int i = tid - 384;
-    ExpertsTile f;
-    n.at(a, t.it + step, tiles);
-    auto xrow = [&](const ExpertsTile& q, int r) -> const unsigned char* {
-      if (!q.valid(a) || r < 0 || r >= a.routes) return nullptr;
-      return a.xs + static_cast<size_t>(a.per_route ? r : r / a.topk) * a.scols;
-    };
-    auto wrow = [&](const ExpertsTile& q) -> const unsigned char* {
-      return q.valid(a) && q.n0 + i < a.N
-                 ? a.ws + (static_cast<size_t>(q.e) * a.N + q.n0 + i) * a.scols
+    constexpr int kRowsEach = Sh::kAtoms;
+    ExpertsUnit f;
+    n.at(a, t.it + step, units, BN);
+    // rows of tile `c` of a unit (past the unit's last: of the next unit's first)
+    auto wrow = [&](const ExpertsUnit& q, int c, int j) -> const unsigned char* {
+      const int r = i + 128 * j, o = q.n0 + c * BN + r;
+      return q.valid(a) && r < BN && o < a.N
+                 ? a.ws + (static_cast<size_t>(q.e) * a.N + o) * a.scols
                  : nullptr;
     };
-    const unsigned char *px = xrow(t, t.entry(a, i, tiles)), *pw = wrow(t);
-    int entry = n.entry(a, i, tiles);
-    uint4 firstx = load_scales(px, 0, a), firstw = load_scales(pw, 0, a);
-    const uint32_t place = base + kXBytes + kWBytes + scale_place(i);
-    for (; ok && t.it < tiles; t = n, n = f) {
-      f.at(a, n.it + step, tiles);
-      const unsigned char *nx = xrow(n, entry), *nw = wrow(n);
-      entry = f.entry(a, i, tiles);
-      uint4 cx, cw, ax = firstx, aw = firstw;
-      uint4 bx = load_scales(px, 1, a), bw = load_scales(pw, 1, a);
-      firstx = load_scales(nx, 0, a);
-      firstw = load_scales(nw, 0, a);
-      if (t.valid(a)) {
-        for (int ks = 0; ks < a.ksteps; ++ks) {
-          if ((ks & 1) == 0) {
-            cx = ax;
-            cw = aw;
-            ax = bx;
-            aw = bw;
-            bx = load_scales(px, ks / 2 + 2, a);
-            bw = load_scales(pw, ks / 2 + 2, a);
-          } else {
-            cx.x = cx.z;
-            cx.y = cx.w;
-            cw.x = cw.z;
-            cw.y = cw.w;
-          }
-          ok = warp_wait(&empty_s[stage], phase ^ 1u, limit);
-          if (!ok) break;
-          const uint32_t dst = place + stage * kStageBytes;
-          const int left = a.K / 32 - 8 * ks;
-          if (left < 8) {
-            cx.x = keep_scales(cx.x, left);
-            cx.y = keep_scales(cx.y, left - 4);
-            cw.x = keep_scales(cw.x, left);
-            cw.y = keep_scales(cw.y, left - 4);
-          }
-          store_shared(dst, cx.x);
-          store_shared(dst + 512, cx.y);
-          store_shared(dst + 1024, cw.x);
-          store_shared(dst + 1536, cw.y);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&full_s[stage]);
-          advance();
+    const unsigned char *p[kRowsEach], *pn[kRowsEach];
+    uint4 first[kRowsEach], cur[kRowsEach], nx[kRowsEach], nn[kRowsEach];
+#pragma unroll
+    for (int j = 0; j < kRowsEach; ++j) {
+      p[j] = wrow(t, 0, j);
+      first[j] = load_scales(p[j], 0, a);
+    }
+    const uint32_t place = wscales + scale_place(i);
+    for (; ok && t.it < units; t = n, n = f) {
+      f.at(a, n.it + step, units, BN);
+      const int tiles = t.valid(a) ? t.tiles : 1;  // one round that only looks ahead
+      for (int c = 0; ok && c < tiles; ++c) {
+#pragma unroll
+        for (int j = 0; j < kRowsEach; ++j) {
+          pn[j] = c + 1 < tiles ? wrow(t, c + 1, j) : wrow(n, 0, j);
+          nx[j] = first[j];
+          nn[j] = load_scales(p[j], 1, a);
+          first[j] = load_scales(pn[j], 0, a);
         }
+        if (t.valid(a)) {
+          for (int ks = 0; ks < a.ksteps; ++ks) {
+#pragma unroll
+            for (int j = 0; j < kRowsEach; ++j) {
+              if ((ks & 1) == 0) {
+                cur[j] = nx[j];
+                nx[j] = nn[j];
+                nn[j] = load_scales(p[j], ks / 2 + 2, a);
+              } else {
+                cur[j].x = cur[j].z;
+                cur[j].y = cur[j].w;
+              }
+            }
+            ok = warp_wait(&wfree_s[w.slot], w.phase ^ 1u, limit);
+            if (!ok) break;
+            const uint32_t dst = place + w.slot * (1024 * Sh::kAtoms);
+            const int left = a.K / 32 - 8 * ks;
+#pragma unroll
+            for (int j = 0; j < kRowsEach; ++j) {
+              store_shared(dst + 512 * j, keep_scales(cur[j].x, left));
+              store_shared(dst + 512 * (Sh::kAtoms + j), keep_scales(cur[j].y, left - 4));
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&wfull_s[w.slot]);
+            w.advance();
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < kRowsEach; ++j) p[j] = pn[j];
       }
-      px = nx;
-      pw = nw;
     }
   }
   if (!ok && lane == 0) atomicOr(a.status, MOE_RS_DEVICE_WAIT_TIMEOUT);
@@ -436,27 +518,55 @@ EncodeFn encode_fn() {
 }
 
 // The weights: `outs` rows of `row` bytes for each of E experts; the copied box is 128 bytes of
-// 128 rows of one expert (rows past the last and bytes past the row's end read as zero).
-bool encode_weights(CUtensorMap* map, const void* p, size_t row, size_t outs, size_t E) {
+// `tile` rows of one expert (rows past the last and bytes past the row's end read as zero).
+bool encode_weights(CUtensorMap* map, const void* p, size_t row, size_t outs, size_t E, int tile) {
   const EncodeFn fn = encode_fn();
   if (fn == nullptr) return false;
   const cuuint64_t dims[3] = {row, outs, E};
   const cuuint64_t strides[2] = {row, row * outs};
-  const cuuint32_t box[3] = {kStepBytes, kExpOuts, 1};
+  const cuuint32_t box[3] = {kStepBytes, static_cast<cuuint32_t>(tile), 1};
   const cuuint32_t one[3] = {1, 1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(p), dims, strides, box, one,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <class Out>
+template <int BN, class Out>
 cudaError_t launch_experts(const CUtensorMap& wmap, const ExpertsArgs& a, int grid,
                            cudaStream_t st) {
-  auto* k = mrs_experts_kernel<Out>;
+  auto* k = mrs_experts_kernel<BN, Out>;
+  constexpr size_t smem = ExpertsShape<BN>::kSmem;
   static SmemGrant granted;
-  const cudaError_t err = grant_smem(reinterpret_cast<const void*>(k), kExpSmem, granted);
+  const cudaError_t err = grant_smem(reinterpret_cast<const void*>(k), smem, granted);
   if (err != cudaSuccess) return err;
-  return launch_pdl(k, dim3(grid), dim3(kExpThreads), kExpSmem, st, wmap, a);
+  return launch_pdl(k, dim3(grid), dim3(kExpThreads), smem, st, wmap, a);
+}
+
+// Tile width and units of a call with `blocks` row tiles at most.  An SM's time for a tile goes
+// by the bytes it takes in, 128 rows and BN weights, so the width is the one with the smaller
+// product of rounds and bytes.  Rows of at most half a ring's steps stay for several tiles once
+// every SM has work for eight rounds without that.
+struct ExpertsPlan {
+  int bn, ntile, chunk, nchunk, ksteps;
+};
+ExpertsPlan experts_plan(int64_t blocks, int outs, int cols, int sms) {
+  ExpertsPlan p{};
+  auto cost = [&](int bn) {
+    const int64_t tiles = blocks * ((outs + bn - 1) / bn);
+    return (tiles + sms - 1) / sms * (kExpRows + bn);
+  };
+  p.bn = cost(192) < cost(128) ? 192 : 128;
+  p.ntile = (outs + p.bn - 1) / p.bn;
+  p.ksteps = (cols + 255) / 256;
+  p.chunk = 1;
+  const int slots = p.bn == 128 ? ExpertsShape<128>::kSlots : ExpertsShape<192>::kSlots;
+  if (2 * p.ksteps <= slots) {
+    const int64_t each = blocks * p.ntile / (8 * static_cast<int64_t>(sms));
+    p.chunk = each < 1 ? 1 : (each > p.ntile ? p.ntile : static_cast<int>(each));
+  }
+  p.nchunk = (p.ntile + p.chunk - 1) / p.chunk;
+  p.chunk = (p.ntile + p.nchunk - 1) / p.nchunk;
+  return p;
 }
 
 }  // namespace
@@ -517,12 +627,12 @@ int moe_experts_mxfp4(const uint8_t* x_codes, const uint8_t* x_scales, int x_per
                       span(num_tokens_post_pad, 4)};
   if (any_alias(outs_s, 2, ins, 8)) return MOE_RS_ERR_ALIAS;
   const bool f32 = out_dtype == MOE_RS_FP32;
-  const int64_t tiles = static_cast<int64_t>(P / block_m) *
-                        ((block_m + kExpRows - 1) / kExpRows) *
-                        ((outs + kExpOuts - 1) / kExpOuts);
-  if (tiles > INT32_MAX / 2) return MOE_RS_ERR_OVERFLOW;
+  const int sub = block_m < kExpRows ? block_m : kExpRows;
+  const int64_t blocks = static_cast<int64_t>(P / block_m) * (block_m / sub);
+  if (blocks * ((outs + 127) / 128) > INT32_MAX / 2) return MOE_RS_ERR_OVERFLOW;
   const int sms = sm_count();
   if (sms == 0) return launch_status(cudaErrorInvalidDevice);
+  const ExpertsPlan p = experts_plan(blocks, outs, cols, sms);
   ExpertsArgs a{};
   a.xc = x_codes;
   a.xs = x_scales;
@@ -543,17 +653,23 @@ int moe_experts_mxfp4(const uint8_t* x_codes, const uint8_t* x_scales, int x_per
   a.scols = scols;
   a.max_rows = static_cast<int>(P);
   a.wait_limit_ns = debug_wait_limit_ns();
-  a.sub = block_m < kExpRows ? block_m : kExpRows;
-  a.subs = block_m / a.sub;
-  a.ntile = (outs + kExpOuts - 1) / kExpOuts;
-  a.ksteps = (cols + 255) / 256;
+  a.sub = sub;
+  a.subs = block_m / sub;
+  a.ntile = p.ntile;
+  a.chunk = p.chunk;
+  a.nchunk = p.nchunk;
+  a.ksteps = p.ksteps;
   a.wide_scales = scols % 16 == 0 && aligned(x_scales, 16) && aligned(w_scales, 16);
   a.wide_out = aligned(out, 32) && outs * (f32 ? 4 : 2) % 32 == 0;
   CUtensorMap wmap;
-  if (!encode_weights(&wmap, w_codes, cols / 2, outs, E)) return MOE_RS_ERR_LAUNCH;
-  const int grid = tiles < sms ? static_cast<int>(tiles) : sms;
-  return launch_status(f32 ? launch_experts<float>(wmap, a, grid, stream)
-                           : launch_experts<__nv_bfloat16>(wmap, a, grid, stream));
+  if (!encode_weights(&wmap, w_codes, cols / 2, outs, E, p.bn)) return MOE_RS_ERR_LAUNCH;
+  const int64_t units = blocks * p.nchunk;
+  const int grid = units < sms ? static_cast<int>(units) : sms;
+  if (p.bn == 128)
+    return launch_status(f32 ? launch_experts<128, float>(wmap, a, grid, stream)
+                             : launch_experts<128, __nv_bfloat16>(wmap, a, grid, stream));
+  return launch_status(f32 ? launch_experts<192, float>(wmap, a, grid, stream)
+                           : launch_experts<192, __nv_bfloat16>(wmap, a, grid, stream));
 }
 
 }  // extern "C"

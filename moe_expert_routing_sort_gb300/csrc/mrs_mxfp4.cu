@@ -14,7 +14,8 @@
 // Bound: one read of the input and one write of half a byte per element plus a scale byte per
 // 32.  A thread takes 8 consecutive elements (one 16-byte load of a 16-bit type), the four
 // threads of a block agree on the maximum with two shuffles, and a warp writes 128 contiguous
-// bytes of codes.
+// bytes of codes.  A thread has four such units, a CTA's width apart, all loaded before the first
+// is used (one unit a thread: 8192 x 3584 in 20.9 us, and 17.3 back).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -25,6 +26,7 @@
 namespace mrs {
 
 constexpr int kMxThreads = 256;
+constexpr int kMxUnits = 4;  // units of 8 elements per thread
 
 struct MxQuantArgs {
   const void* x;
@@ -74,70 +76,117 @@ __device__ __forceinline__ void load8(const __half* p, float (&v)[8]) {
   }
 }
 
+// Where unit `u` lies: its row, and its place in the row.
+struct MxUnit {
+  size_t row;
+  unsigned c;
+  bool in;
+};
+// The thread's units.  The division is done once; the others are a CTA's width further.
+__device__ __forceinline__ void mx_units(size_t units, unsigned upr, MxUnit (&at)[kMxUnits]) {
+  size_t u = static_cast<size_t>(blockIdx.x) * (kMxThreads * kMxUnits) + threadIdx.x;
+  size_t row = u < units ? u / upr : 0;
+  unsigned c = static_cast<unsigned>(u - row * upr);
+  if (u >= units) c = 0;
+#pragma unroll
+  for (int j = 0; j < kMxUnits; ++j) {
+    at[j] = MxUnit{row, c, u < units};
+    u += kMxThreads;
+    c += kMxThreads;
+    if (c >= upr) {  // (32 bits: cheap)
+      row += c / upr;
+      c %= upr;
+    }
+  }
+}
+
 template <class In>
 __global__ void __launch_bounds__(kMxThreads) mrs_mxfp4_quantize_kernel(const MxQuantArgs a) {
   pdl_trigger();
+  MxUnit at[kMxUnits];
+  mx_units(a.units, a.upr, at);
   pdl_wait();
-  const size_t u = static_cast<size_t>(blockIdx.x) * kMxThreads + threadIdx.x;
-  // the four threads of a block are all in or all out (a row holds a multiple of four units)
-  const bool in = u < a.units;
-  const size_t row = in ? u / a.upr : 0;
-  const unsigned c = in ? static_cast<unsigned>(u - row * a.upr) : 0;
-  float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-  if (in) load8(static_cast<const In*>(a.x) + row * a.stride + 8 * static_cast<size_t>(c), v);
-  uint32_t top = 0u;  // bits of the largest magnitude (ordered like the magnitudes)
+  float v[kMxUnits][8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
-  top = max(top, __shfl_xor_sync(kFull, top, 1));
-  top = max(top, __shfl_xor_sync(kFull, top, 2));
-  if (!in) return;
-  const uint32_t ef = top >> 23;  // exponent field; 0 (zero, subnormal) clamps like 1 does
-  uint32_t scale = ef > 2u ? ef - 2u : 0u;
-  uint32_t code = 0u;
-  if (ef == 255u) {
-    scale = 255u;
-  } else {
-    const float inv = __uint_as_float((254u - scale) << 23);  // 2^(127 - scale), normal
+  for (int j = 0; j < kMxUnits; ++j) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] *= inv;
-    code = e2m1x8(v);
+    for (int i = 0; i < 8; ++i) v[j][i] = 0.0f;
+    // the four threads of a block are all in or all out (a row holds a multiple of four units)
+    if (at[j].in)
+      load8(static_cast<const In*>(a.x) + at[j].row * a.stride + 8 * static_cast<size_t>(at[j].c),
+            v[j]);
   }
-  *reinterpret_cast<uint32_t*>(a.codes + row * (4 * static_cast<size_t>(a.upr)) +
-                               4 * static_cast<size_t>(c)) = code;
-  if ((c & 3u) == 0u) {
-    unsigned char* s = a.scales + row * a.scols;
-    s[c >> 2] = static_cast<unsigned char>(scale);
-    if (c + 4u == a.upr)  // the row's last block also clears the padding bytes
-      for (unsigned p = (c >> 2) + 1u; p < a.scols; ++p) s[p] = 0;
+#pragma unroll
+  for (int j = 0; j < kMxUnits; ++j) {
+    uint32_t top = 0u;  // bits of the largest magnitude (ordered like the magnitudes)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[j][i]) & 0x7fffffffu);
+    top = max(top, __shfl_xor_sync(kFull, top, 1));
+    top = max(top, __shfl_xor_sync(kFull, top, 2));
+    if (at[j].in) {
+      const uint32_t ef = top >> 23;  // exponent field; 0 (zero, subnormal) clamps like 1 does
+      uint32_t scale = ef > 2u ? ef - 2u : 0u;
+      uint32_t code = 0u;
+      if (ef == 255u) {
+        scale = 255u;
+      } else {
+        const float inv = __uint_as_float((254u - scale) << 23);  // 2^(127 - scale), normal
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[j][i] *= inv;
+        code = e2m1x8(v[j]);
+      }
+      const size_t row = at[j].row;
+      const unsigned c = at[j].c;
+      *reinterpret_cast<uint32_t*>(a.codes + row * (4 * static_cast<size_t>(a.upr)) +
+                                   4 * static_cast<size_t>(c)) = code;
+      if ((c & 3u) == 0u) {
+        unsigned char* s = a.scales + row * a.scols;
+        s[c >> 2] = static_cast<unsigned char>(scale);
+        if (c + 4u == a.upr)  // the row's last block also clears the padding bytes
+          for (unsigned p = (c >> 2) + 1u; p < a.scols; ++p) s[p] = 0;
+      }
+    }
+    __syncwarp();
   }
 }
 
 template <class Out>
 __global__ void __launch_bounds__(kMxThreads) mrs_mxfp4_dequantize_kernel(const MxDequantArgs a) {
   pdl_trigger();
+  MxUnit at[kMxUnits];
+  mx_units(a.units, a.upr, at);
   pdl_wait();
-  const size_t u = static_cast<size_t>(blockIdx.x) * kMxThreads + threadIdx.x;
-  if (u >= a.units) return;
-  const size_t row = u / a.upr;
-  const unsigned c = static_cast<unsigned>(u - row * a.upr);
-  float v[8];
-  e2m1_values(__ldg(reinterpret_cast<const uint32_t*>(a.codes) + u), v);
-  const float s = e8m0_value(__ldg(a.scales + row * a.scols + (c >> 2)));
+  uint32_t code[kMxUnits], scale[kMxUnits];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] *= s;
-  Out* y = static_cast<Out*>(a.y) + row * a.stride + 8 * static_cast<size_t>(c);
-  if constexpr (sizeof(Out) == 4) {
-    reinterpret_cast<float4*>(y)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4*>(y)[1] = make_float4(v[4], v[5], v[6], v[7]);
-  } else {
-    // the one rounding of this direction: exact in bf16 down to its smallest subnormal
-    uint32_t w[4];
+  for (int j = 0; j < kMxUnits; ++j) {
+    code[j] = scale[j] = 0u;
+    if (!at[j].in) continue;
+    code[j] = __ldg(reinterpret_cast<const uint32_t*>(a.codes) +
+                    at[j].row * static_cast<size_t>(a.upr) + at[j].c);
+    scale[j] = __ldg(a.scales + at[j].row * a.scols + (at[j].c >> 2));
+  }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&b);
+  for (int j = 0; j < kMxUnits; ++j) {
+    if (!at[j].in) continue;
+    float v[8];
+    e2m1_values(code[j], v);
+    const float s = e8m0_value(scale[j]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] *= s;
+    Out* y = static_cast<Out*>(a.y) + at[j].row * a.stride + 8 * static_cast<size_t>(at[j].c);
+    if constexpr (sizeof(Out) == 4) {
+      reinterpret_cast<float4*>(y)[0] = make_float4(v[0], v[1], v[2], v[3]);
+      reinterpret_cast<float4*>(y)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+      // the one rounding of this direction: exact in bf16 down to its smallest subnormal
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&b);
+      }
+      *reinterpret_cast<uint4*>(y) = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    *reinterpret_cast<uint4*>(y) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
@@ -199,7 +248,7 @@ int moe_mxfp4_quantize(const void* x, int x_dtype, int64_t rows, int cols, int64
   a.scols = static_cast<unsigned>(scols);
   a.codes = codes;
   a.scales = scales;
-  const dim3 grid(static_cast<unsigned>((a.units + kMxThreads - 1) / kMxThreads));
+  const dim3 grid(static_cast<unsigned>((a.units + kMxThreads * kMxUnits - 1) / (kMxThreads * kMxUnits)));
   auto* k = x_dtype == MOE_RS_FP32   ? mrs_mxfp4_quantize_kernel<float>
             : x_dtype == MOE_RS_FP16 ? mrs_mxfp4_quantize_kernel<__half>
                                      : mrs_mxfp4_quantize_kernel<__nv_bfloat16>;
@@ -227,7 +276,7 @@ int moe_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t ro
   a.stride = static_cast<size_t>(y_stride);
   a.scols = static_cast<unsigned>(scols);
   a.y = y;
-  const dim3 grid(static_cast<unsigned>((a.units + kMxThreads - 1) / kMxThreads));
+  const dim3 grid(static_cast<unsigned>((a.units + kMxThreads * kMxUnits - 1) / (kMxThreads * kMxUnits)));
   auto* k = y_dtype == MOE_RS_FP32 ? mrs_mxfp4_dequantize_kernel<float>
                                    : mrs_mxfp4_dequantize_kernel<__nv_bfloat16>;
   return launch_status(launch_pdl(k, grid, dim3(kMxThreads), 0, stream, a));

@@ -147,7 +147,7 @@ def _rows(g, rows, cols, spread=1.0):
 
 def _routes(g, T, E, K, dist):
     if dist == "uniform":
-        return torch.stack([torch.randperm(E, generator=g)[:K] for _ in range(T)]).int()
+        return torch.rand(T, E, generator=g).topk(K, dim=1).indices.int()
     if dist == "one":
         return torch.full((T, K), E - 1, dtype=torch.int32)
     ids = torch.randint(0, E, (T, K), generator=g).int()  # repeats inside a token, drops
@@ -237,6 +237,19 @@ def test_product_output_widths(N):
 @pytest.mark.parametrize("per_route", [False, True])
 def test_product_shapes(T, E, K, cols, N, B, per_route):
     _check_product(T, E, K, cols, N, B, per_route=per_route, dtype=torch.bfloat16)
+
+
+@pytest.mark.parametrize("T,E,K,cols,N,B", [
+    (2000, 8, 4, 640, 1536, 64),    # wide tiles, one a unit
+    (8000, 8, 4, 320, 1536, 64),    # wide tiles, several a unit, the last unit of a block shorter
+    (8000, 8, 4, 512, 1432, 64),    # the same with a ragged last tile
+    (20000, 8, 4, 96, 256, 64),     # narrow tiles, several a unit
+    (9000, 8, 4, 768, 768, 128),    # the most steps whose rows could stay for narrow tiles
+    (3000, 700, 8, 256, 640, 16),   # many experts of few rows
+])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_product_many_tiles(T, E, K, cols, N, B, dtype):
+    _check_product(T, E, K, cols, N, B, dtype=dtype, per_route=dtype == torch.float32)
 
 
 @pytest.mark.parametrize("dist", ["one", "drops"])
