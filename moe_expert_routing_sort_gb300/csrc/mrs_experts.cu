@@ -7,8 +7,8 @@
 // (1 without weights) is applied in fp32, and the result is rounded once to the output type.
 //
 // One tile is the rows of one block (the M side of the tensor-core product, 128 lanes of tensor
-// memory; blocks of more rows are cut, blocks of fewer leave lanes unused) by BN = 128 or 192
-// outputs of its expert (the N side).  Rows on the lanes make the result a row per thread, so the
+// memory; blocks of more rows are cut, blocks of fewer leave lanes unused) by BN = 96, 128 or
+// 192 outputs of its expert (the N side).  Rows on the lanes make the result a row per thread, so the
 // outputs leave as 32-byte stores of whole sectors; a block of 16 rows costs the tensor core as
 // much as one of 128, which it has time for: such calls wait for the weights.  A persistent CTA
 // per SM takes units round robin, a unit being one tile, or for short rows several output tiles of
@@ -21,7 +21,8 @@
 //   1      copies a step's scales to tensor memory and issues four products of 64 columns; the
 //          tensor core applies the scales and adds into fp32 in tensor memory
 //   4-7    a finished tile from tensor memory to the output rows, while the next one is computed
-//          (two accumulators)
+//          (two accumulators; eight warps with half the columns each were slower, 484 us against
+//          444 at T = 8192, 384 -> 3584)
 //   8-11   the block's rows, 16 bytes a thread into the same swizzle (the copies arrive on the
 //          slot's barrier themselves), and their scales
 //   12-15  the weights' scales
@@ -36,6 +37,8 @@
 // Each task has the list entries of the next two units and the first scales of the next one in
 // flight.  Every wait is bounded; a wait that gives up ends its warp's task with the status bit
 // set, and the CTA leaves once nothing of its own is in flight.
+#include <type_traits>
+
 #include <cuda_bf16.h>
 
 #include "mrs_args.h"
@@ -64,7 +67,7 @@ struct ExpertsArgs {
   int wide_out;     // output rows start on 32 bytes
 };
 
-constexpr int kExpThreads = 512;  // warps 2 and 3 only fill the quarter of the epilogue's lanes
+constexpr int kExpThreads = 512;  // warps 2 and 3 are idle: a warp reads the lanes of its number mod 4
 constexpr int kExpRows = 128;     // lanes of a tile: rows of a block
 constexpr int kStepBytes = 128;   // bytes of a row per step
 constexpr int kTmemCols = 512;
@@ -77,7 +80,7 @@ struct ExpertsShape {
   static constexpr int kXSlot = kX + 2 * 512;                 // and their scales
   static constexpr int kW = BN * kStepBytes;
   static constexpr int kWSlot = kW + 2 * 512 * kAtoms;
-  static constexpr int kSlots = BN == 128 ? 6 : 5;            // what fits in 227 KB
+  static constexpr int kSlots = BN == 96 ? 7 : (BN == 128 ? 6 : 5);  // what fits in 227 KB
   static constexpr size_t kSmem = static_cast<size_t>(kSlots) * (kXSlot + kWSlot) + 1024;
   // tensor memory: two accumulators, then the scales of each slot
   static constexpr int kXScales = 2 * BN;
@@ -186,8 +189,8 @@ __global__ void __launch_bounds__(kExpThreads, 1)
   const int most = a.max_rows / a.B * a.subs * a.nchunk, step = gridDim.x;
   ExpertsUnit t, n;
   t.at(a, blockIdx.x, most, BN);
-  const int my_row = 32 * (warp & 3) + lane;  // of warps 4-7 and 8-11
-  int entry = warp >= 4 && warp < 12 ? t.entry(a, my_row, most) : -1;
+  const int my_row = 32 * (warp & 3) + lane;  // of warps 4-11
+  int entry = warp >= 4 ? t.entry(a, my_row, most) : -1;
   const int rows = min(max(__ldg(a.npp), 0), a.max_rows);
   const int units = rows / a.B * a.subs * a.nchunk;
   bool ok = true;
@@ -285,7 +288,7 @@ __global__ void __launch_bounds__(kExpThreads, 1)
       warp_wait(&done_s, 0, kWaitLimitNs);
     }
   } else if (warp >= 4 && warp < 8) {
-    const bool used = 32 * (warp - 4) < a.sub;
+    const bool used = 32 * (warp & 3) < a.sub;
     int buf = 0;
     uint32_t acc_phase = 0;
     for (; ok && t.it < units; t = n) {
@@ -300,7 +303,7 @@ __global__ void __launch_bounds__(kExpThreads, 1)
         if (!ok) break;
         if (used) {
           tc_fence_after();
-          const uint32_t src = tmem + buf * BN + (static_cast<uint32_t>(32 * (warp - 4)) << 16);
+          const uint32_t src = tmem + buf * BN + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
           const int n0 = t.n0 + tile * BN, left = a.N - n0;  // left: a multiple of 8
           Out* out = static_cast<Out*>(a.out) + (put ? static_cast<size_t>(r) * a.N : 0) + n0;
 #pragma unroll
@@ -376,7 +379,8 @@ __global__ void __launch_bounds__(kExpThreads, 1)
         const int src_n = source(n, entry);
         entry = f.entry(a, my_row, units);
         const unsigned char* p = scales_of(src);
-        uint4 cur, nx = first, nn = load_scales(p, 1, a);
+        uint4 cur, nx = first, nn = nx;
+        if (a.ksteps > 2) nn = load_scales(p, 1, a);
         first = load_scales(scales_of(src_n), 0, a);
         if (t.valid(a)) {
           // rows that are no route keep what was there: any codes, in rows that are not stored
@@ -392,7 +396,7 @@ __global__ void __launch_bounds__(kExpThreads, 1)
             if ((ks & 1) == 0) {
               cur = nx;
               nx = nn;
-              nn = load_scales(p, ks / 2 + 2, a);
+              if (ks + 4 < a.ksteps) nn = load_scales(p, ks / 2 + 2, a);
             } else {
               cur.x = cur.z;
               cur.y = cur.w;
@@ -451,7 +455,8 @@ __global__ void __launch_bounds__(kExpThreads, 1)
         for (int j = 0; j < kRowsEach; ++j) {
           pn[j] = c + 1 < tiles ? wrow(t, c + 1, j) : wrow(n, 0, j);
           nx[j] = first[j];
-          nn[j] = load_scales(p[j], 1, a);
+          nn[j] = nx[j];
+          if (a.ksteps > 2) nn[j] = load_scales(p[j], 1, a);
           first[j] = load_scales(pn[j], 0, a);
         }
         if (t.valid(a)) {
@@ -461,7 +466,7 @@ __global__ void __launch_bounds__(kExpThreads, 1)
               if ((ks & 1) == 0) {
                 cur[j] = nx[j];
                 nx[j] = nn[j];
-                nn[j] = load_scales(p[j], ks / 2 + 2, a);
+                if (ks + 4 < a.ksteps) nn[j] = load_scales(p[j], ks / 2 + 2, a);
               } else {
                 cur[j].x = cur[j].z;
                 cur[j].y = cur[j].w;
@@ -542,24 +547,28 @@ cudaError_t launch_experts(const CUtensorMap& wmap, const ExpertsArgs& a, int gr
   return launch_pdl(k, dim3(grid), dim3(kExpThreads), smem, st, wmap, a);
 }
 
-// Tile width and units of a call with `blocks` row tiles at most.  An SM's time for a tile goes
-// by the bytes it takes in, 128 rows and BN weights, so the width is the one with the smaller
-// product of rounds and bytes.  Rows of at most half a ring's steps stay for several tiles once
+// Tile width and units of a call with at most `blocks` row tiles of `sub` rows.  An SM's time for
+// a tile goes by the bytes it takes in, its rows and BN weights, so the width is the one with the
+// smallest product of rounds and bytes.  Rows of at most half a ring's steps stay for several tiles once
 // every SM has work for eight rounds without that.
 struct ExpertsPlan {
   int bn, ntile, chunk, nchunk, ksteps;
 };
-ExpertsPlan experts_plan(int64_t blocks, int outs, int cols, int sms) {
+ExpertsPlan experts_plan(int64_t blocks, int sub, int outs, int cols, int sms) {
   ExpertsPlan p{};
   auto cost = [&](int bn) {
     const int64_t tiles = blocks * ((outs + bn - 1) / bn);
-    return (tiles + sms - 1) / sms * (kExpRows + bn);
+    return (tiles + sms - 1) / sms * (sub + bn);
   };
-  p.bn = cost(192) < cost(128) ? 192 : 128;
+  p.bn = 128;
+  if (cost(192) < cost(p.bn)) p.bn = 192;
+  if (cost(96) < cost(p.bn)) p.bn = 96;
   p.ntile = (outs + p.bn - 1) / p.bn;
   p.ksteps = (cols + 255) / 256;
   p.chunk = 1;
-  const int slots = p.bn == 128 ? ExpertsShape<128>::kSlots : ExpertsShape<192>::kSlots;
+  const int slots = p.bn == 96    ? ExpertsShape<96>::kSlots
+                    : p.bn == 128 ? ExpertsShape<128>::kSlots
+                                  : ExpertsShape<192>::kSlots;
   if (2 * p.ksteps <= slots) {
     const int64_t each = blocks * p.ntile / (8 * static_cast<int64_t>(sms));
     p.chunk = each < 1 ? 1 : (each > p.ntile ? p.ntile : static_cast<int>(each));
@@ -632,7 +641,7 @@ int moe_experts_mxfp4(const uint8_t* x_codes, const uint8_t* x_scales, int x_per
   if (blocks * ((outs + 127) / 128) > INT32_MAX / 2) return MOE_RS_ERR_OVERFLOW;
   const int sms = sm_count();
   if (sms == 0) return launch_status(cudaErrorInvalidDevice);
-  const ExpertsPlan p = experts_plan(blocks, outs, cols, sms);
+  const ExpertsPlan p = experts_plan(blocks, sub, outs, cols, sms);
   ExpertsArgs a{};
   a.xc = x_codes;
   a.xs = x_scales;
@@ -665,11 +674,14 @@ int moe_experts_mxfp4(const uint8_t* x_codes, const uint8_t* x_scales, int x_per
   if (!encode_weights(&wmap, w_codes, cols / 2, outs, E, p.bn)) return MOE_RS_ERR_LAUNCH;
   const int64_t units = blocks * p.nchunk;
   const int grid = units < sms ? static_cast<int>(units) : sms;
-  if (p.bn == 128)
-    return launch_status(f32 ? launch_experts<128, float>(wmap, a, grid, stream)
-                             : launch_experts<128, __nv_bfloat16>(wmap, a, grid, stream));
-  return launch_status(f32 ? launch_experts<192, float>(wmap, a, grid, stream)
-                           : launch_experts<192, __nv_bfloat16>(wmap, a, grid, stream));
+  auto go = [&](auto n) {
+    constexpr int BN = decltype(n)::value;
+    return f32 ? launch_experts<BN, float>(wmap, a, grid, stream)
+               : launch_experts<BN, __nv_bfloat16>(wmap, a, grid, stream);
+  };
+  return launch_status(p.bn == 96    ? go(std::integral_constant<int, 96>{})
+                       : p.bn == 128 ? go(std::integral_constant<int, 128>{})
+                                     : go(std::integral_constant<int, 192>{}));
 }
 
 }  // extern "C"
