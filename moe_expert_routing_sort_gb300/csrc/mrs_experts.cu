@@ -134,10 +134,10 @@ __device__ __forceinline__ uint4 load_scales(const unsigned char* row, int pair,
   return q;
 }
 
-// The first `left` bytes of four scales: what lies behind a row's K / 32 scales is padding, and
-// its columns' products of zeros have to meet a finite scale.
-__device__ __forceinline__ uint32_t keep_scales(uint32_t w, int left) {
-  return left >= 4 ? w : (left <= 0 ? 0u : w & ((1u << (8 * left)) - 1u));
+// Mask of the first `left` bytes of four scales: what lies behind a row's K / 32 scales is
+// padding, and its columns' products of zeros have to meet a finite scale.
+__device__ __forceinline__ uint32_t scale_mask(int left) {
+  return left >= 4 ? ~0u : (left <= 0 ? 0u : (1u << (8 * left)) - 1u);
 }
 
 __device__ __forceinline__ void store_shared(uint32_t dst, uint32_t v) {
@@ -193,6 +193,9 @@ __global__ void __launch_bounds__(kExpThreads, 1)
   int entry = warp >= 4 ? t.entry(a, my_row, most) : -1;
   const int rows = min(max(__ldg(a.npp), 0), a.max_rows);
   const int units = rows / a.B * a.subs * a.nchunk;
+  // bytes of the last step's scales that are scales
+  const int tail = a.K / 32 - 8 * (a.ksteps - 1);
+  const uint32_t tail0 = scale_mask(tail), tail1 = scale_mask(tail - 4);
   bool ok = true;
   RingPlace<S> x, w;
 
@@ -306,11 +309,15 @@ __global__ void __launch_bounds__(kExpThreads, 1)
           const uint32_t src = tmem + buf * BN + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
           const int n0 = t.n0 + tile * BN, left = a.N - n0;  // left: a multiple of 8
           Out* out = static_cast<Out*>(a.out) + (put ? static_cast<size_t>(r) * a.N : 0) + n0;
+          // the next 32 columns are on their way while these are stored (columns past the
+          // outputs are read, as zeros, and not stored)
+          uint32_t ahead[2][32];
+          tmem_load32(src, ahead[0]);
 #pragma unroll
           for (int c0 = 0; c0 < BN; c0 += 32) {
-            if (c0 >= left) break;
-            uint32_t v[32];
-            tmem_load32(src + c0, v);
+            uint32_t(&v)[32] = ahead[(c0 / 32) & 1];
+            tmem_wait(v);
+            if (c0 + 32 < BN) tmem_load32(src + c0 + 32, ahead[(c0 / 32 + 1) & 1]);
             if constexpr (sizeof(Out) == 4) {
 #pragma unroll
               for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(by * __uint_as_float(v[c]));
@@ -413,9 +420,12 @@ __global__ void __launch_bounds__(kExpThreads, 1)
               from[j] += kStepBytes;
             }
             copy_arrive(&xfull_s[x.slot]);
-            const int left = a.K / 32 - 8 * ks;
-            store_shared(scale_at + x.slot * 1024, keep_scales(cur.x, left));
-            store_shared(scale_at + x.slot * 1024 + 512, keep_scales(cur.y, left - 4));
+            if (ks + 1 == a.ksteps) {
+              cur.x &= tail0;
+              cur.y &= tail1;
+            }
+            store_shared(scale_at + x.slot * 1024, cur.x);
+            store_shared(scale_at + x.slot * 1024 + 512, cur.y);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&xfull_s[x.slot]);
@@ -430,35 +440,36 @@ __global__ void __launch_bounds__(kExpThreads, 1)
     // a thread has one row of the weights, and the first 64 one of the second 128
     const int i = tid - 384;
     constexpr int kRowsEach = Sh::kAtoms;
+    const bool second = i + 128 < BN;
+    const size_t apart = static_cast<size_t>(BN) * a.scols;  // a row and the next tile's
+    const size_t down = static_cast<size_t>(128) * a.scols;
     ExpertsUnit f;
     n.at(a, t.it + step, units, BN);
-    // rows of tile `c` of a unit (past the unit's last: of the next unit's first)
-    auto wrow = [&](const ExpertsUnit& q, int c, int j) -> const unsigned char* {
-      const int r = i + 128 * j, o = q.n0 + c * BN + r;
-      return q.valid(a) && r < BN && o < a.N
-                 ? a.ws + (static_cast<size_t>(q.e) * a.N + o) * a.scols
-                 : nullptr;
+    // the thread's first row of a unit's first tile, and the outputs from it on (none: no row)
+    auto start = [&](const ExpertsUnit& q, int& left) -> const unsigned char* {
+      left = q.valid(a) ? a.N - (q.n0 + i) : 0;
+      return left > 0 ? a.ws + (static_cast<size_t>(q.e) * a.N + q.n0 + i) * a.scols : a.ws;
     };
-    const unsigned char *p[kRowsEach], *pn[kRowsEach];
+    auto load = [&](const unsigned char* p, int left, int pair, uint4 (&q)[kRowsEach]) {
+      q[0] = load_scales(left > 0 ? p : nullptr, pair, a);
+      if constexpr (kRowsEach == 2)
+        q[1] = load_scales(second && left > 128 ? p + down : nullptr, pair, a);
+    };
+    int left, left_n;
+    const unsigned char* p = start(t, left);
     uint4 first[kRowsEach], cur[kRowsEach], nx[kRowsEach], nn[kRowsEach];
-#pragma unroll
-    for (int j = 0; j < kRowsEach; ++j) {
-      p[j] = wrow(t, 0, j);
-      first[j] = load_scales(p[j], 0, a);
-    }
+    load(p, left, 0, first);
     const uint32_t place = wscales + scale_place(i);
     for (; ok && t.it < units; t = n, n = f) {
       f.at(a, n.it + step, units, BN);
+      const unsigned char* pn = start(n, left_n);
       const int tiles = t.valid(a) ? t.tiles : 1;  // one round that only looks ahead
       for (int c = 0; ok && c < tiles; ++c) {
 #pragma unroll
-        for (int j = 0; j < kRowsEach; ++j) {
-          pn[j] = c + 1 < tiles ? wrow(t, c + 1, j) : wrow(n, 0, j);
-          nx[j] = first[j];
-          nn[j] = nx[j];
-          if (a.ksteps > 2) nn[j] = load_scales(p[j], 1, a);
-          first[j] = load_scales(pn[j], 0, a);
-        }
+        for (int j = 0; j < kRowsEach; ++j) nn[j] = nx[j] = first[j];
+        if (a.ksteps > 2) load(p, left, 1, nn);
+        const bool more = c + 1 < tiles;
+        load(more ? p + apart : pn, more ? left - BN : left_n, 0, first);
         if (t.valid(a)) {
           for (int ks = 0; ks < a.ksteps; ++ks) {
 #pragma unroll
@@ -466,20 +477,23 @@ __global__ void __launch_bounds__(kExpThreads, 1)
               if ((ks & 1) == 0) {
                 cur[j] = nx[j];
                 nx[j] = nn[j];
-                if (ks + 4 < a.ksteps) nn[j] = load_scales(p[j], ks / 2 + 2, a);
               } else {
                 cur[j].x = cur[j].z;
                 cur[j].y = cur[j].w;
               }
             }
+            if ((ks & 1) == 0 && ks + 4 < a.ksteps) load(p, left, ks / 2 + 2, nn);
             ok = warp_wait(&wfree_s[w.slot], w.phase ^ 1u, limit);
             if (!ok) break;
             const uint32_t dst = place + w.slot * (1024 * Sh::kAtoms);
-            const int left = a.K / 32 - 8 * ks;
 #pragma unroll
             for (int j = 0; j < kRowsEach; ++j) {
-              store_shared(dst + 512 * j, keep_scales(cur[j].x, left));
-              store_shared(dst + 512 * (Sh::kAtoms + j), keep_scales(cur[j].y, left - 4));
+              if (ks + 1 == a.ksteps) {
+                cur[j].x &= tail0;
+                cur[j].y &= tail1;
+              }
+              store_shared(dst + 512 * j, cur[j].x);
+              store_shared(dst + 512 * (Sh::kAtoms + j), cur[j].y);
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -487,8 +501,8 @@ __global__ void __launch_bounds__(kExpThreads, 1)
             w.advance();
           }
         }
-#pragma unroll
-        for (int j = 0; j < kRowsEach; ++j) p[j] = pn[j];
+        p = more ? p + apart : pn;
+        left = more ? left - BN : left_n;
       }
     }
   }
