@@ -42,6 +42,7 @@ constexpr int kJoinThreads = 256;
 constexpr int kDepth = 4;          // rows of a lane in flight, the one it works on among them
 constexpr int kBalWarps = kBalThreads / 32;
 constexpr int kBalMaxCtas = 256;
+constexpr int kIdsAhead = 4;       // routes of a thread loaded ahead of a stretch's rows
 constexpr int kSoloRows = 4;       // rows per group up to which one CTA takes the call
 constexpr int kSoloSeqs = 8;
 constexpr int kBalMaxJoin = 1024;  // CTAs of the second kernel
@@ -78,6 +79,7 @@ struct RouteBackwardArgs {
   const int32_t* counts;   // [S, E] (null with gl)
   const int32_t* offsets;
   int T, E, K, S, W, tpc;
+  int wide_counts;         // counts start on 16 bytes
   float R, coef;
   void* out;
 };
@@ -98,13 +100,20 @@ __device__ __forceinline__ int seq_border(const int32_t* o, int i, int T) {
   return o == nullptr ? (i == 0 ? 0 : T) : min(max(__ldg(o + i), 0), T);
 }
 
-// First sequence that ends behind token t (S if none does).
+// First sequence that ends behind token t (S if none does); all lanes of a warp.  32 borders are
+// looked at together, so a packed batch takes one load's time and 65536 sequences four.
 __device__ __forceinline__ int seq_behind(const int32_t* o, int S, int T, int t) {
-  int lo = 0, hi = S;
-  while (lo < hi) {
-    const int m = (lo + hi) >> 1;
-    if (seq_border(o, m + 1, T) > t) hi = m;
-    else lo = m + 1;
+  if (o == nullptr) return t < T ? 0 : 1;
+  int lo = 0, n = S;  // the answer lies in [lo, lo + n]
+  const int lane = threadIdx.x & 31;
+  while (n > 0) {
+    const int each = (n + 31) / 32, i = lo + min((lane + 1) * each, n) - 1;
+    const unsigned behind = __ballot_sync(kFull, seq_border(o, i + 1, T) > t);
+    if (behind == 0u) return lo + n;
+    const int first = __ffs(behind) - 1;  // sequence lo + (first + 1) each - 1 ends behind t
+    lo += first * each;
+    n = min(each - 1, n - 1 - first * each);
+    n = n < 0 ? 0 : n;
   }
   return lo;
 }
@@ -120,43 +129,46 @@ struct RowStream {
   static constexpr int NV = NC / 8;
   static constexpr uint32_t kPast = kSoftmax ? 0xff80ff80u : 0xc220c220u;
   uint32_t next[kVec ? 1 : NC];
-  uint32_t ring;
-  int slot;
+  uint32_t ring, slot;     // slot: bytes into the ring of the row that is taken next
+  const uint16_t* from;    // the lane's first column of the row that is fetched next
+  int row;                 // and its number
 
-  __device__ __forceinline__ void fetch(const uint16_t* logits, int E, int row, int hi, int lane,
-                                        int lanes, int at) {
-    const uint16_t* p = logits + static_cast<size_t>(row) * E;
+  __device__ __forceinline__ void fetch(int E, int hi, int lane, int lanes, uint32_t to) {
     if constexpr (kVec) {
       if (row < hi) {
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-          const int c = 8 * (v * lanes + lane);
-          if (c < E) copy16(ring + 16 * kBalThreads * (at * NV + v), p + c);
-        }
+        for (int v = 0; v < NV; ++v)
+          if (8 * (v * lanes + lane) < E)
+            copy16(to + 16 * kBalThreads * v, from + 8 * v * lanes);
       }
       copy_close();  // a group per row, empty past the last, so that the count below holds
     } else if (row < hi) {
 #pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        const int c = i * lanes + lane;
-        next[i] = c < E ? static_cast<uint32_t>(__ldg(p + c)) << 16 : 0xff800000u;
-      }
+      for (int i = 0; i < NC; ++i)
+        next[i] = i * lanes + lane < E ? static_cast<uint32_t>(__ldg(from + i * lanes)) << 16
+                                       : 0xff800000u;
     }
   }
-  // Starts with rows row, row + step, ... below hi.
-  __device__ __forceinline__ void open(const uint16_t* logits, int E, int row, int step, int hi,
+  // Starts with rows first, first + step, ... below hi.
+  __device__ __forceinline__ void open(const uint16_t* logits, int E, int first, int step, int hi,
                                        int lane, int lanes, uint32_t ring_base) {
     ring = ring_base;
     slot = 0;
+    row = first;
+    from = logits + static_cast<size_t>(first) * E + (kVec ? 8 : 1) * lane;
 #pragma unroll
-    for (int d = 0; d < (kVec ? kDepth - 1 : 1); ++d)
-      fetch(logits, E, row + d * step, hi, lane, lanes, d);
+    for (int d = 0; d < (kVec ? kDepth - 1 : 1); ++d) {
+      fetch(E, hi, lane, lanes, ring + 16 * kBalThreads * NV * d);
+      row += step;
+      from += static_cast<size_t>(step) * E;
+    }
   }
-  // The values of row `row`, whose successors keep coming.
-  __device__ __forceinline__ void take(const uint16_t* logits, int E, int row, int step, int hi,
-                                       int lane, int lanes, float (&x)[NC]) {
+  // The values of the next row, whose successors keep coming.
+  __device__ __forceinline__ void take(int E, int step, int hi, int lane, int lanes,
+                                       float (&x)[NC]) {
+    constexpr uint32_t kRow = 16 * kBalThreads * NV;
     if constexpr (kVec) {
-      fetch(logits, E, row + (kDepth - 1) * step, hi, lane, lanes, (slot + kDepth - 1) % kDepth);
+      fetch(E, hi, lane, lanes, ring + (slot == 0 ? (kDepth - 1) * kRow : slot - kRow));
       copy_wait<kDepth - 1>();
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
@@ -164,7 +176,7 @@ struct RowStream {
         if (8 * (v * lanes + lane) < E)
           asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                        : "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3])
-                       : "r"(ring + 16 * kBalThreads * (slot * NV + v))
+                       : "r"(ring + slot + 16 * kBalThreads * v)
                        : "memory");
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -172,12 +184,14 @@ struct RowStream {
           x[8 * v + 2 * j + 1] = __uint_as_float(q[j] & 0xffff0000u);
         }
       }
-      slot = (slot + 1) % kDepth;
+      slot = slot == (kDepth - 1) * kRow ? 0 : slot + kRow;
     } else {
 #pragma unroll
       for (int i = 0; i < NC; ++i) x[i] = __uint_as_float(next[i]);
-      fetch(logits, E, row + step, hi, lane, lanes, 0);
+      fetch(E, hi, lane, lanes, 0);
     }
+    row += step;
+    from += static_cast<size_t>(step) * E;
   }
 };
 
@@ -340,13 +354,13 @@ __device__ __forceinline__ void row_terms(float (&x)[NC], const float (&g)[kDot 
 }
 
 // ------------------------------------------------------------------------------ the loss
-template <int NC, bool kVec, bool kSoftmax>
+template <int NC, bool kVec, bool kSoftmax, int kW>
 __global__ void __launch_bounds__(kBalThreads, 1) mrs_balance_rows_kernel(const BalanceArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ float4 xchg_s[kBalWarps][2];
   float* red = reinterpret_cast<float*>(smem + row_smem<NC, kVec>()) - kBalThreads * NC;
   int* hist = reinterpret_cast<int*>(smem + row_smem<NC, kVec>());  // [E]
-  const int tid = threadIdx.x, warp = tid >> 5, W = a.W, E = a.E;
+  const int tid = threadIdx.x, warp = tid >> 5, W = kW > 0 ? kW : a.W, E = a.E;
   const int grp = warp / W, gw = warp - grp * W, groups = groups_of(W);
   const int lanes = 32 * W, lane = 32 * gw + (tid & 31);
   const bool idle = grp >= groups;  // a W that does not divide the warps leaves some without a group
@@ -380,19 +394,19 @@ __global__ void __launch_bounds__(kBalThreads, 1) mrs_balance_rows_kernel(const 
     RowStream<NC, kVec, kSoftmax> rows;
     int row = lo + grp;
     if (!idle) rows.open(a.logits, E, row, groups, hi, lane, lanes, ring);
-    // counts of the stretch
+    // the stretch's routes: loaded now, counted after the rows
     const size_t r1 = static_cast<size_t>(hi) * a.K;
-    for (size_t r = static_cast<size_t>(lo) * a.K + tid; r < r1; r += kBalThreads) {
-      const int e = __ldg(a.ids + r);
-      if (e >= 0 && e < E) atomicAdd(hist + e, 1);  // integers: any order, the same sum
-    }
+    size_t r = static_cast<size_t>(lo) * a.K + tid;
+    int id[kIdsAhead];
+#pragma unroll
+    for (int q = 0; q < kIdsAhead; ++q, r += kBalThreads) id[q] = r < r1 ? __ldg(a.ids + r) : -1;
     if (!idle && row < hi) {
       float acc[NC];
 #pragma unroll
       for (int c = 0; c < NC; ++c) acc[c] = 0.0f;
       for (int buf = 0; row < hi; row += groups, buf ^= 1) {
         float x[NC], scale, dot;
-        rows.take(a.logits, E, row, groups, hi, lane, lanes, x);
+        rows.take(E, groups, hi, lane, lanes, x);
         row_terms<NC, kSoftmax, false>(x, g0, past, W, grp, gw, xchg, buf, scale, dot);
 #pragma unroll
         for (int c = 0; c < NC; ++c) acc[c] = fmaf(x[c], scale, acc[c]);
@@ -407,6 +421,12 @@ __global__ void __launch_bounds__(kBalThreads, 1) mrs_balance_rows_kernel(const 
           *to = acc[c];
       }
     }
+    auto count = [&](int e) {
+      if (e >= 0 && e < E) atomicAdd(hist + e, 1);  // integers: any order, the same sum
+    };
+#pragma unroll
+    for (int q = 0; q < kIdsAhead; ++q) count(id[q]);
+    for (; r < r1; r += kBalThreads) count(__ldg(a.ids + r));
     copy_wait_all();
     __syncthreads();
     const int had = min(groups, hi - lo);  // groups with a row of the stretch
@@ -503,12 +523,12 @@ __global__ void __launch_bounds__(kJoinThreads) mrs_balance_join_kernel(const Ba
 }
 
 // -------------------------------------------------------------------------- the gradient
-template <int NC, bool kVec, bool kSoftmax, class Out>
+template <int NC, bool kVec, bool kSoftmax, int kW, class Out>
 __global__ void __launch_bounds__(kBalThreads, 1)
     mrs_route_backward_kernel(const RouteBackwardArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ float4 xchg_s[kBalWarps][2];
-  const int tid = threadIdx.x, warp = tid >> 5, W = a.W, E = a.E, K = a.K, wl = tid & 31;
+  const int tid = threadIdx.x, warp = tid >> 5, W = kW > 0 ? kW : a.W, E = a.E, K = a.K, wl = tid & 31;
   const int grp = warp / W, gw = warp - grp * W, groups = groups_of(W);
   const int lanes = 32 * W, lane = 32 * gw + wl;
   float4* xchg = &xchg_s[0][0] + grp * 2 * W;
@@ -552,10 +572,24 @@ __global__ void __launch_bounds__(kBalThreads, 1)
     if (dense && in_seq) {
       const float n = static_cast<float>(hi_i - lo_i);
       const float f = gl * (a.coef / a.S) * (static_cast<float>(E) / K) / n / n;
+      const int32_t* counts = a.counts + static_cast<size_t>(i) * E;
+      if (kVec && a.wide_counts) {
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        const int e = column_of<kVec>(c, lane, lanes);
-        if (e < E) g[c] = f * static_cast<float>(__ldg(a.counts + static_cast<size_t>(i) * E + e));
+        for (int c = 0; c < NC; c += 4) {
+          const int e = column_of<kVec>(c, lane, lanes);
+          if (e >= E) continue;
+          const int4 q = __ldg(reinterpret_cast<const int4*>(counts + e));
+          g[c] = f * static_cast<float>(q.x);
+          g[c + 1] = f * static_cast<float>(q.y);
+          g[c + 2] = f * static_cast<float>(q.z);
+          g[c + 3] = f * static_cast<float>(q.w);
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          const int e = column_of<kVec>(c, lane, lanes);
+          if (e < E) g[c] = f * static_cast<float>(__ldg(counts + e));
+        }
       }
     }
     RowStream<NC, kVec, kSoftmax> rows;
@@ -578,7 +612,7 @@ __global__ void __launch_bounds__(kBalThreads, 1)
       const bool valid = sparse && wl < K && id >= 0 && id < E;
       float xk = valid ? bf16_bits_to_float(__ldg(xr + id)) : -INFINITY;
       fetch(row + groups);
-      rows.take(a.logits, E, row, groups, hi, lane, lanes, x);
+      rows.take(E, groups, hi, lane, lanes, x);
       float scale = 0.0f, dot = 0.0f;
       if (dense) {
         row_terms<NC, kSoftmax, true>(x, g, past, W, grp, gw, xchg, buf, scale, dot);
@@ -729,10 +763,10 @@ int check_router(int T, int E, int K, int S) {
   return MOE_RS_OK;
 }
 
-template <int NC, bool kVec>
+template <int NC, bool kVec, int kW>
 cudaError_t launch_balance(const BalanceArgs& a, bool softmax, int ctas, cudaStream_t st) {
-  auto* k = softmax ? mrs_balance_rows_kernel<NC, kVec, true>
-                    : mrs_balance_rows_kernel<NC, kVec, false>;
+  auto* k = softmax ? mrs_balance_rows_kernel<NC, kVec, true, kW>
+                    : mrs_balance_rows_kernel<NC, kVec, false, kW>;
   const size_t smem = row_smem<NC, kVec>() + sizeof(int) * static_cast<size_t>(a.E);
   static SmemGrant granted[2];
   const cudaError_t err =
@@ -742,10 +776,10 @@ cudaError_t launch_balance(const BalanceArgs& a, bool softmax, int ctas, cudaStr
   return launch_pdl(k, dim3(ctas), dim3(kBalThreads), smem, st, a);
 }
 
-template <int NC, bool kVec, class Out>
+template <int NC, bool kVec, int kW, class Out>
 cudaError_t launch_backward(const RouteBackwardArgs& a, bool softmax, int ctas, cudaStream_t st) {
-  auto* k = softmax ? mrs_route_backward_kernel<NC, kVec, true, Out>
-                    : mrs_route_backward_kernel<NC, kVec, false, Out>;
+  auto* k = softmax ? mrs_route_backward_kernel<NC, kVec, true, kW, Out>
+                    : mrs_route_backward_kernel<NC, kVec, false, kW, Out>;
   const size_t smem = row_smem<NC, kVec>();
   static SmemGrant granted[2];
   const cudaError_t err =
@@ -754,16 +788,24 @@ cudaError_t launch_backward(const RouteBackwardArgs& a, bool softmax, int ctas, 
   return launch_pdl(k, dim3(ctas), dim3(kBalThreads), smem, st, a);
 }
 
-// The kernels' instances: 8, 16 or 32 columns per lane in vectors, 8 or 16 without.
+// The kernels' instances: 8, 16 or 32 columns per lane in vectors, more than one warp a row only
+// with 32; 8 or 16 without, any number of warps.
 template <class Go>
 cudaError_t with_plan(const RowPlan& p, Go go) {
-  using N8 = std::integral_constant<int, 8>;
-  using N16 = std::integral_constant<int, 16>;
-  using N32 = std::integral_constant<int, 32>;
-  if (!p.vec) return p.NC == 8 ? go(N8{}, std::false_type{}) : go(N16{}, std::false_type{});
-  return p.NC == 8    ? go(N8{}, std::true_type{})
-         : p.NC == 16 ? go(N16{}, std::true_type{})
-                      : go(N32{}, std::true_type{});
+  using std::integral_constant;
+  using N8 = integral_constant<int, 8>;
+  using N16 = integral_constant<int, 16>;
+  using N32 = integral_constant<int, 32>;
+  using Any = integral_constant<int, 0>;
+  using W1 = integral_constant<int, 1>;
+  if (!p.vec)
+    return p.NC == 8 ? go(N8{}, std::false_type{}, Any{}) : go(N16{}, std::false_type{}, Any{});
+  if (p.W == 2) return go(N32{}, std::true_type{}, integral_constant<int, 2>{});
+  if (p.W == 3) return go(N32{}, std::true_type{}, integral_constant<int, 3>{});
+  if (p.W == 4) return go(N32{}, std::true_type{}, integral_constant<int, 4>{});
+  return p.NC == 8    ? go(N8{}, std::true_type{}, W1{})
+         : p.NC == 16 ? go(N16{}, std::true_type{}, W1{})
+                      : go(N32{}, std::true_type{}, W1{});
 }
 
 }  // namespace
@@ -827,8 +869,9 @@ int moe_balance_loss(const void* logits_bf16, const int32_t* topk_ids, const int
   a.psum = reinterpret_cast<float*>(ws + l.psum);
   a.csum = reinterpret_cast<int32_t*>(ws + l.csum);
   const int ctas = T > 0 ? (T + a.tpc - 1) / a.tpc : 1;
-  const cudaError_t err = with_plan(p, [&](auto nc, auto vec) {
-    return launch_balance<decltype(nc)::value, decltype(vec)::value>(a, softmax != 0, ctas, stream);
+  const cudaError_t err = with_plan(p, [&](auto nc, auto vec, auto w) {
+    return launch_balance<decltype(nc)::value, decltype(vec)::value, decltype(w)::value>(
+        a, softmax != 0, ctas, stream);
   });
   if (err != cudaSuccess || a.solo) return launch_status(err);
   const int gx = (E + 31) / 32;
@@ -879,16 +922,17 @@ int moe_route_backward(const void* logits_bf16, const int32_t* topk_ids, const f
   a.S = n_seq;
   a.W = p.W;
   a.tpc = tokens_per_cta(T, p.W, sms);
+  a.wide_counts = aligned(counts, 16);
   a.R = routed_scale;
   a.coef = coef;
   a.out = grad_logits;
   const int ctas = (T + a.tpc - 1) / a.tpc;
   const bool sm = softmax != 0, f32 = grad_dtype == MOE_RS_FP32;
-  return launch_status(with_plan(p, [&](auto nc, auto vec) {
-    constexpr int NC = decltype(nc)::value;
+  return launch_status(with_plan(p, [&](auto nc, auto vec, auto w) {
+    constexpr int NC = decltype(nc)::value, kW = decltype(w)::value;
     constexpr bool V = decltype(vec)::value;
-    return f32 ? launch_backward<NC, V, float>(a, sm, ctas, stream)
-               : launch_backward<NC, V, __nv_bfloat16>(a, sm, ctas, stream);
+    return f32 ? launch_backward<NC, V, kW, float>(a, sm, ctas, stream)
+               : launch_backward<NC, V, kW, __nv_bfloat16>(a, sm, ctas, stream);
   }));
 }
 
