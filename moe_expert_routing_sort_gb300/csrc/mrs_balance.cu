@@ -367,9 +367,9 @@ __global__ void __launch_bounds__(kBalThreads, 1) mrs_balance_rows_kernel(const 
   float4* xchg = &xchg_s[0][0] + grp * 2 * W;
   const uint32_t ring = smem_u32(smem) + 16 * tid;
   const unsigned past = vectors_past<NC, kVec>(E, lane, lanes);
-  pdl_trigger();
   for (int e = tid; e < E; e += kBalThreads) hist[e] = 0;
   pdl_wait();
+  pdl_trigger();  // only now: the second kernel reads the call's inputs before this one ends
   if (blockIdx.x == 0 && tid == 0 && !a.solo) *a.ticket = 0u;
   __syncthreads();
 
@@ -470,12 +470,13 @@ __global__ void __launch_bounds__(kJoinThreads) mrs_balance_join_kernel(const Ba
   __shared__ int cs[2][kWarps][32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int e = blockIdx.x * 32 + lane;
+  // the borders are inputs: the first kernel started after they were written
+  int lo = seq_border(a.offsets, blockIdx.y, a.T), hi = seq_border(a.offsets, blockIdx.y + 1, a.T);
   pdl_trigger();
   pdl_wait();
   float loss = 0.0f;
   int buf = 0;
   for (int i = blockIdx.y; i < a.S; i += gridDim.y, buf ^= 1) {
-    const int lo = seq_border(a.offsets, i, a.T), hi = seq_border(a.offsets, i + 1, a.T);
     float p = 0.0f;
     int c = 0;
     if (hi > lo && e < a.E) {
@@ -503,6 +504,8 @@ __global__ void __launch_bounds__(kJoinThreads) mrs_balance_join_kernel(const Ba
       a.mean[at] = mean;
       loss += static_cast<float>(c) * mean / n;
     }
+    lo = seq_border(a.offsets, min(i + static_cast<int>(gridDim.y), a.S), a.T);
+    hi = seq_border(a.offsets, min(i + static_cast<int>(gridDim.y) + 1, a.S), a.T);
   }
   if (warp != 0) return;
   // this CTA's part of the loss, then everybody's
@@ -511,9 +514,12 @@ __global__ void __launch_bounds__(kJoinThreads) mrs_balance_join_kernel(const Ba
   int last = 0;
   if (lane == 0) {
     a.partial[blockIdx.y * gridDim.x + blockIdx.x] = loss;
-    __threadfence();
-    last = atomicAdd(a.ticket, 1u) == static_cast<unsigned>(ctas - 1) ? 1 : 0;
-    __threadfence();
+    unsigned before;
+    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;"
+                 : "=r"(before)
+                 : "l"(a.ticket)
+                 : "memory");
+    last = before == static_cast<unsigned>(ctas - 1) ? 1 : 0;
   }
   if (__shfl_sync(kFull, last, 0) == 0) return;
   float s = 0.0f;
