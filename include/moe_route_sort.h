@@ -105,6 +105,8 @@ extern "C" {
                                              multiple of 8 in [8, 65536]                   */
 #define MOE_RS_ERR_BAD_SEQUENCES (-19)    /* n_seq outside [1, 65536], or > 1 with no offsets */
 #define MOE_RS_ERR_BAD_ROWS (-20)         /* a negative number of rows                     */
+#define MOE_RS_ERR_BAD_CALL (-21)         /* moe_call_packed: unknown operation, or not its
+                                             number of arguments                           */
 
 /* Device-side status bits, written to the first int32 of the workspace by every call. */
 #define MOE_RS_DEVICE_BAD_EXPERT_ID 0x1   /* moe_sort saw an id >= E; those routes dropped */
@@ -353,6 +355,19 @@ int moe_experts_mxfp4(const uint8_t* x_codes, const uint8_t* x_scales, int x_per
                       const float* sorted_weights, const int32_t* expert_ids,
                       const int32_t* num_tokens_post_pad, void* out, int out_dtype,
                       void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* One of the five operations above with its arguments as an array, for language bindings that pay
+ * per argument.  args: 8-byte values (8-byte aligned host memory): the operation's number, the
+ * number of its arguments, then the arguments in the order of its declaration -- pointers, the
+ * stream and integers as int64, floats as double.  Returns what the operation returns, or
+ * MOE_RS_ERR_BAD_CALL, MOE_RS_ERR_OVERFLOW for an integer outside its type, MOE_RS_ERR_NULL_POINTER
+ * or MOE_RS_ERR_MISALIGNED for args itself. */
+#define MOE_RS_CALL_BALANCE_LOSS 1
+#define MOE_RS_CALL_ROUTE_BACKWARD 2
+#define MOE_RS_CALL_MXFP4_QUANTIZE 3
+#define MOE_RS_CALL_MXFP4_DEQUANTIZE 4
+#define MOE_RS_CALL_EXPERTS_MXFP4 5
+int moe_call_packed(const void* args);
 
 /* ------------------------------------------------------- allocation-free variant */
 

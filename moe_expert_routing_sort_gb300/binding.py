@@ -101,6 +101,8 @@ def load() -> ctypes.CDLL:
         lib.moe_experts_mxfp4_workspace_bytes.restype = S
         lib.moe_experts_mxfp4.argtypes = [P, P, I, P, P, I, I, I, I, I, I, P, P, P, P, P, I, P, S, P]
         lib.moe_experts_mxfp4.restype = I
+        lib.moe_call_packed.argtypes = [ctypes.c_char_p]
+        lib.moe_call_packed.restype = I
         _lib = lib
         return lib
 

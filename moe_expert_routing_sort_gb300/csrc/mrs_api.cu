@@ -399,6 +399,8 @@ const char* moe_route_sort_strerror(int status) {
     case MOE_RS_ERR_BAD_SEQUENCES:
       return "n_seq must be in [1, 65536], and 1 without sequence offsets";
     case MOE_RS_ERR_BAD_ROWS: return "the number of rows must be >= 0";
+    case MOE_RS_ERR_BAD_CALL:
+      return "moe_call_packed: unknown operation, or not its number of arguments";
     default: return "unknown status";
   }
 }

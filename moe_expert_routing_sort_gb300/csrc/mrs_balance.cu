@@ -765,7 +765,9 @@ int check_router(int T, int E, int K, int S) {
   if (E < 1 || E > kMaxExperts) return MOE_RS_ERR_BAD_EXPERTS;
   if (K < 1 || K > kMaxTopk || K > E) return MOE_RS_ERR_BAD_TOPK;
   if (S < 1 || S > MOE_RS_MAX_SEQUENCES) return MOE_RS_ERR_BAD_SEQUENCES;
-  if (static_cast<int64_t>(T) * K > INT32_MAX) return MOE_RS_ERR_OVERFLOW;
+  // (row numbers run a few rows past T)
+  if (static_cast<int64_t>(T) * K > INT32_MAX || T > INT32_MAX - (1 << 16))
+    return MOE_RS_ERR_OVERFLOW;
   return MOE_RS_OK;
 }
 

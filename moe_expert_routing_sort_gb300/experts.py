@@ -131,7 +131,7 @@ def _list_args(T, E, topk, block_m, outs, dev, sorted_token_ids, sorted_weights,
     n = T * topk
     P = n + min(n, E) * (block_m - 1)  # as moe_sort_max_padded
     return (need(sorted_token_ids, torch.int32, P, dev, "sorted_token_ids"),
-            None if sorted_weights is None else need(sorted_weights, torch.float32, P, dev,
+            0 if sorted_weights is None else need(sorted_weights, torch.float32, P, dev,
                                                      "sorted_weights"),
             need(expert_ids, torch.int32, P // block_m if block_m > 0 else 0, dev, "expert_ids"),
             need(num_tokens_post_pad, torch.int32, 1, dev, "num_tokens_post_pad"),

@@ -5,6 +5,8 @@ each tensor for as little as it can, and containers check their own tensors once
 """
 from __future__ import annotations
 
+import struct
+
 import torch
 
 from .binding import _check, load
@@ -50,28 +52,44 @@ def rows_of(t: torch.Tensor, name: str):
     return rows, cols, (stride if rows > 1 else cols)
 
 
+# The operations' numbers and arguments (include/moe_route_sort.h): q an address, an integer or the
+# stream, d a float.
+_OPERATIONS = {
+    "moe_balance_loss": (1, "8qd6q"),
+    "moe_route_backward": (2, "11q2d3q"),
+    "moe_mxfp4_quantize": (3, "8q"),
+    "moe_mxfp4_dequantize": (4, "8q"),
+    "moe_experts_mxfp4": (5, "20q"),
+}
+
+
 class Entry:
     """C entry point ``name``, called with its device current and the stream as last argument;
-    raises on a negative status."""
+    raises on a negative status.  The arguments go as one array (moe_call_packed): converting 20
+    of them one by one takes longer than the smallest kernels.  A NULL is 0."""
 
-    __slots__ = ("name", "fn")
+    __slots__ = ("name", "op", "count", "pack", "fn")
 
     def __init__(self, name: str):
         self.name = name
+        self.op, args = _OPERATIONS[name]
+        self.pack = struct.Struct("=qq" + args).pack
+        self.count = (struct.calcsize("=" + args)) // 8
         self.fn = None
 
     def __call__(self, device: int, stream, *args) -> None:
         fn = self.fn
         if fn is None:
-            fn = self.fn = getattr(load(), self.name)
+            fn = self.fn = load().moe_call_packed
         if stream is None:
             handle = _raw_stream(device)
         else:
             handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        packed = self.pack(self.op, self.count, *args, handle)
         if _current_device() == device:
-            rc = fn(*args, handle)
+            rc = fn(packed)
         else:
             with torch.cuda.device(device):
-                rc = fn(*args, handle)
+                rc = fn(packed)
         if rc:
             _check(rc, self.name)

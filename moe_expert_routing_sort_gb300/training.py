@@ -56,13 +56,13 @@ def _router(logits, topk_ids, seq_offsets):
     if logits.dim() != 2:
         raise ValueError("logits must be [T, E]")
     T, E = logits.shape
-    K, pid = 1, None
+    K, pid = 1, 0
     if topk_ids is not None:
         if topk_ids.dim() != 2 or topk_ids.shape[0] != T:
             raise ValueError("topk_ids must be [T, topk] for logits [T, E]")
         K = topk_ids.shape[1]
         pid = need(topk_ids, torch.int32, 0, dev, "topk_ids")
-    S, po = 1, None
+    S, po = 1, 0
     if seq_offsets is not None:
         S = seq_offsets.numel() - 1
         po = need(seq_offsets, torch.int32, 1, dev, "seq_offsets")
@@ -114,10 +114,10 @@ def moe_route_backward(logits, topk_ids, grad_weights, grad_loss, counts, seq_of
     if dtype is not torch.bfloat16 and dtype is not torch.float32:
         raise ValueError(f"grad_logits must be bfloat16 or float32, got {dtype}")
     _backward(dev, stream, pl, pid,
-              None if grad_weights is None else need(grad_weights, torch.float32, T * K, dev,
+              0 if grad_weights is None else need(grad_weights, torch.float32, T * K, dev,
                                                      "grad_weights"),
-              None if grad_loss is None else need(grad_loss, torch.float32, 1, dev, "grad_loss"),
-              None if counts is None else need(counts, torch.int32, S * E, dev, "counts"),
+              0 if grad_loss is None else need(grad_loss, torch.float32, 1, dev, "grad_loss"),
+              0 if counts is None else need(counts, torch.int32, S * E, dev, "counts"),
               po, T, E, K, S, 1 if softmax else 0, routed_scale, coef,
               need(grad_logits, dtype, T * E, dev, "grad_logits"), DTYPE_CODE[dtype])
 

@@ -144,3 +144,39 @@ def test_binding_refuses_host_and_misshaped_buffers():
         mrs.Mxfp4Rows.allocate(4, 40, device="cpu")
     with pytest.raises(ValueError):
         mrs.BalanceBuffers.allocate(4, 0, device="cpu")
+
+
+def _packed(lib, op, n, *values):
+    import struct
+
+    fmt = "=qq" + "".join("d" if isinstance(v, float) else "q" for v in values)
+    return lib.moe_call_packed(struct.pack(fmt, op, n, *values))
+
+
+def test_packed_calls_reach_their_operations(lib):
+    # every operation's first refusals, and the counts of arguments
+    assert _packed(lib, 0, 0) == -21 and _packed(lib, 6, 0) == -21
+    for op in (1, 2, 3, 4, 5):
+        assert _packed(lib, op, 7) == -21
+    b = BASE
+    loss = [b, b, 0, -1, 64, 6, 1, 0, 0.5, b, b, b, b, 1 << 20, 0]
+    assert _packed(lib, 1, 15, *loss) == -6
+    loss[3], loss[4] = 4, 5000
+    assert _packed(lib, 1, 15, *loss) == -2
+    loss[4], loss[8] = 64, NAN
+    assert _packed(lib, 1, 15, *loss) == -11
+    loss[3] = 1 << 40  # does not fit the argument's type
+    assert _packed(lib, 1, 15, *loss) == -7
+    back = [b, b, b, b, b, 0, 4, 64, 6, 1, 0, 2.5, 0.1, b + 0x10000, 9, 0]
+    assert _packed(lib, 2, 16, *back) == -17
+    back[14], back[12] = 0, float("inf")
+    assert _packed(lib, 2, 16, *back) == -11
+    assert _packed(lib, 3, 8, b, 0, 8, 48, 48, b, b, 0) == -18
+    assert _packed(lib, 3, 8, b, 0, 1 << 41, 64, 64, b, b, 0) == -7
+    assert _packed(lib, 4, 8, b, b, -1, 64, b, 0, 64, 0) == -20
+    ex = [b, b, 0, b, b, 8, 4, 2, 64, 16, 24, b, b, b, b, b, 0, b, 256, 0]
+    assert _packed(lib, 5, 20, *ex) == -5
+    ex[10], ex[18] = 16, 8
+    assert _packed(lib, 5, 20, *ex) == -10
+    assert lib.moe_call_packed(None) == -1
+    assert mrs.strerror(-21) != "unknown status"
