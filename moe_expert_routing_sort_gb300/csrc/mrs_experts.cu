@@ -6,9 +6,11 @@
 // X and W are E2M1 codes with one E8M0 scale per 32 columns; sums are fp32, the row's weight
 // (1 without weights) is applied in fp32, and the result is rounded once to the output type.
 //
-// One tile is the rows of one block (the M side of the tensor-core product, 128 lanes of tensor
-// memory; blocks of more rows are cut, blocks of fewer leave lanes unused) by BN = 96, 128 or
-// 192 outputs of its expert (the N side).  Rows on the lanes make the result a row per thread, so the
+// One tile is up to 128 rows of one expert (the M side of the tensor-core product, 128 lanes of
+// tensor memory) by BN = 96, 128 or 192 outputs (the N side).  Blocks of more rows are cut;
+// neighbouring blocks of fewer rows that have the same expert share a tile: the list is taken in
+// windows of at most 128 rows and 32 blocks, and a tile is a run of one expert's blocks in a
+// window (block_m = 16, 4024 tokens, 191 experts, 1984 -> 656: 728 -> 113 us).  Rows on the lanes make the result a row per thread, so the
 // outputs leave as 32-byte stores of whole sectors; a block of 16 rows costs the tensor core as
 // much as one of 128, which it has time for: such calls wait for the weights.  A persistent CTA
 // per SM takes units round robin, a unit being one tile, or for short rows several output tiles of
@@ -58,7 +60,8 @@ struct ExpertsArgs {
   unsigned long long wait_limit_ns;
   int routes, topk, per_route;
   int E, K, N, B, scols, max_rows;
-  int sub, subs;    // rows of a tile (<= 128), tiles along a block's rows
+  int group;        // blocks of a window; 1: every block by itself, in `subs` parts
+  int span, subs;   // rows of a window or part (<= 128)
   int ntile;        // tiles along the outputs
   int chunk;        // tiles of a unit (the last of a block may have fewer)
   int nchunk;       // units along the outputs
@@ -88,21 +91,56 @@ struct ExpertsShape {
   static_assert(kWScales + 8 * kAtoms * kSlots <= kTmemCols, "");
 };
 
-// A unit of the list: its expert id is in flight or here (-1 past the last unit).
+// A unit of the list: run `slot` of a window (the run of blocks that starts at the window's block
+// `slot`, if one does), or a block's part, by some output tiles.  The expert ids it depends on are
+// in flight until resolve().  Runs are numbered after windows: the first runs of all windows, which
+// there always are, spread evenly over the CTAs.
 struct ExpertsUnit {
-  int it, p0, n0, tiles, e;
-  __device__ __forceinline__ void at(const ExpertsArgs& a, int i, int units, int bn) {
+  int it, p0, n0, tiles, slot, blocks;  // blocks: of the window that there are
+  int id;    // of the window's block `lane`
+  int e, rows;
+  bool lead;
+  __device__ __forceinline__ void at(const ExpertsArgs& a, int i, int units, int windows,
+                                     int total_blocks, int bn) {
     it = i;
-    const int b = i / a.nchunk, first = (i - b * a.nchunk) * a.chunk;
+    const int per = max(windows * a.nchunk, 1);
+    const int run = a.group > 1 ? i / per : 0;
+    slot = min(run, 31);  // (past the last unit it means nothing)
+    const int q = i - run * per, b = q / a.nchunk, first = (q - b * a.nchunk) * a.chunk;
     n0 = first * bn;
     tiles = min(a.chunk, a.ntile - first);
-    p0 = b * a.sub;
-    e = i < units ? __ldg(a.eid + b / a.subs) : -1;
+    id = -1;
+    if (a.group > 1) {
+      const int lane = threadIdx.x & 31, b0 = b * a.group;
+      p0 = (b0 + slot) * a.B;
+      blocks = min(a.group, total_blocks - b0);
+      if (i < units && lane < blocks) id = __ldg(a.eid + b0 + lane);
+    } else {
+      p0 = b * a.span;
+      blocks = 1;
+      if (i < units) id = __ldg(a.eid + b / a.subs);
+    }
   }
-  __device__ __forceinline__ bool valid(const ExpertsArgs& a) const { return e >= 0 && e < a.E; }
-  // Entry i of the unit's rows (-1: a lane unused, or past the last unit).
-  __device__ __forceinline__ int entry(const ExpertsArgs& a, int i, int units) const {
-    return (it < units && i < a.sub) ? __ldg(a.sid + p0 + i) : -1;
+  __device__ __forceinline__ void resolve(const ExpertsArgs& a, int units) {
+    if (a.group > 1) {
+      const int lane = threadIdx.x & 31;
+      e = __shfl_sync(kFull, id, slot);
+      const int before = __shfl_sync(kFull, id, max(slot - 1, 0));
+      lead = it < units && slot < blocks && (slot == 0 || before != e);
+      const unsigned same = __ballot_sync(kFull, id == e && lane < blocks) >> slot;
+      rows = (same == ~0u ? 32 : __ffs(~same) - 1) * a.B;
+    } else {
+      e = id;
+      lead = it < units;
+      rows = a.span;
+    }
+  }
+  __device__ __forceinline__ bool valid(const ExpertsArgs& a) const {
+    return lead && e >= 0 && e < a.E;
+  }
+  // Entry i behind the unit's first row (-1: none that could be the unit's).
+  __device__ __forceinline__ int entry(const ExpertsArgs& a, int i, int units, int total_rows) const {
+    return (it < units && i < a.span && p0 + i < total_rows) ? __ldg(a.sid + p0 + i) : -1;
   }
 };
 
@@ -162,7 +200,7 @@ __global__ void __launch_bounds__(kExpThreads, 1)
   const uint32_t xbase = base, wbase = base + S * Sh::kX;
   const uint32_t xscales = wbase + S * Sh::kW, wscales = xscales + S * 1024;
   const unsigned long long limit = a.wait_limit_ns;
-  const int copiers = (a.sub + 31) / 32;  // warps with rows of the block
+  const int copiers = (a.span + 31) / 32;  // warps with rows of a window
   pdl_trigger();
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
@@ -185,14 +223,24 @@ __global__ void __launch_bounds__(kExpThreads, 1)
   const uint32_t tmem = tmem_s;
   pdl_wait();
 
-  // the first unit's list entries do not wait for the list's length
-  const int most = a.max_rows / a.B * a.subs * a.nchunk, step = gridDim.x;
+  // one block a window: the first unit's list entries do not wait for the list's length
+  const int step = gridDim.x;
   ExpertsUnit t, n;
-  t.at(a, blockIdx.x, most, BN);
   const int my_row = 32 * (warp & 3) + lane;  // of warps 4-11
-  int entry = warp >= 4 ? t.entry(a, my_row, most) : -1;
-  const int rows = min(max(__ldg(a.npp), 0), a.max_rows);
-  const int units = rows / a.B * a.subs * a.nchunk;
+  int entry = -1;
+  if (a.group == 1) {
+    const int most = a.max_rows / a.B * a.subs * a.nchunk;
+    t.at(a, blockIdx.x, most, 0, 0, BN);
+    if (warp >= 4) entry = t.entry(a, my_row, most, a.max_rows);
+  }
+  const int rows = min(max(__ldg(a.npp), 0), a.max_rows) / a.B * a.B, blocks = rows / a.B;
+  const int windows = a.group > 1 ? (blocks + a.group - 1) / a.group : blocks * a.subs;
+  const int units = a.group * windows * a.nchunk;
+  if (a.group > 1) {
+    t.at(a, blockIdx.x, units, windows, blocks, BN);
+    if (warp >= 4) entry = t.entry(a, my_row, units, rows);
+  }
+  auto look = [&](ExpertsUnit& q, int i) { q.at(a, i, units, windows, blocks, BN); };
   // bytes of the last step's scales that are scales
   const int tail = a.K / 32 - 8 * (a.ksteps - 1);
   const uint32_t tail0 = scale_mask(tail), tail1 = scale_mask(tail - 4);
@@ -202,9 +250,10 @@ __global__ void __launch_bounds__(kExpThreads, 1)
   if (warp == 0) {
     long long issued = 0;
     for (; ok && t.it < units; t = n) {
-      n.at(a, t.it + step, units, BN);
+      look(n, t.it + step);
+      t.resolve(a, units);
       if (!t.valid(a)) {
-        if (lane == 0) atomicOr(a.status, MOE_RS_DEVICE_BAD_EXPERT_ID);
+        if (t.lead && lane == 0) atomicOr(a.status, MOE_RS_DEVICE_BAD_EXPERT_ID);
         continue;
       }
       for (int c = 0; ok && c < t.tiles; ++c) {
@@ -233,7 +282,8 @@ __global__ void __launch_bounds__(kExpThreads, 1)
     uint32_t acc_phase = 0;
     bool any = false;
     for (; ok && t.it < units; t = n) {
-      n.at(a, t.it + step, units, BN);
+      look(n, t.it + step);
+      t.resolve(a, units);
       if (!t.valid(a)) continue;
       RingPlace<S> xs = x;
       for (int c = 0; ok && c < t.tiles; ++c) {
@@ -291,15 +341,16 @@ __global__ void __launch_bounds__(kExpThreads, 1)
       warp_wait(&done_s, 0, kWaitLimitNs);
     }
   } else if (warp >= 4 && warp < 8) {
-    const bool used = 32 * (warp & 3) < a.sub;
     int buf = 0;
     uint32_t acc_phase = 0;
     for (; ok && t.it < units; t = n) {
-      n.at(a, t.it + step, units, BN);
+      look(n, t.it + step);
       const int r = entry;
-      entry = n.entry(a, my_row, units);
+      entry = n.entry(a, my_row, units, rows);
+      t.resolve(a, units);
       if (!t.valid(a)) continue;
-      const bool put = r >= 0 && r < a.routes;
+      const bool used = 32 * (warp & 3) < t.rows;
+      const bool put = my_row < t.rows && r >= 0 && r < a.routes;
       const float by = (a.sw != nullptr && put) ? __ldg(a.sw + t.p0 + my_row) : 1.0f;
       for (int tile = 0; tile < t.tiles; ++tile) {
         ok = warp_wait(&acc_full_s[buf], acc_phase, limit);
@@ -361,30 +412,31 @@ __global__ void __launch_bounds__(kExpThreads, 1)
     // warp w copies rows 32 w .. 32 w + 31 of the block, four rows (8 lanes each) at a time, and
     // lane l the scales of row 32 w + l
     const int w32 = 32 * (warp - 8);
-    const int mine = min(a.sub - w32, 32);  // rows of this warp
     const int chunk = lane & 7, sub4 = lane >> 3;
     const size_t half = static_cast<size_t>(a.K / 2);
     // row 4 j + sub4 of the warp: two swizzles, for even and odd j
     const uint32_t place = xbase + (w32 + sub4) * kStepBytes;
     const uint32_t even = place + 16 * (chunk ^ sub4), odd = place + 16 * (chunk ^ (sub4 + 4));
     const uint32_t scale_at = xscales + scale_place(my_row);
-    if (mine > 0) {
+    if (w32 < a.span) {
       auto source = [&](const ExpertsUnit& q, int r) -> int {
-        if (!q.valid(a) || r < 0 || r >= a.routes) return -1;
+        if (!q.valid(a) || my_row >= q.rows || r < 0 || r >= a.routes) return -1;
         return a.per_route ? r : r / a.topk;
       };
       auto scales_of = [&](int s) -> const unsigned char* {
         return s < 0 ? nullptr : a.xs + static_cast<size_t>(s) * a.scols;
       };
       ExpertsUnit f;
-      n.at(a, t.it + step, units, BN);
+      look(n, t.it + step);
+      t.resolve(a, units);
       int src = source(t, entry);
-      entry = n.entry(a, my_row, units);
+      entry = n.entry(a, my_row, units, rows);
       uint4 first = load_scales(scales_of(src), 0, a);
       for (; ok && t.it < units; t = n, n = f) {
-        f.at(a, n.it + step, units, BN);
+        look(f, n.it + step);
+        n.resolve(a, units);
         const int src_n = source(n, entry);
-        entry = f.entry(a, my_row, units);
+        entry = f.entry(a, my_row, units, rows);
         const unsigned char* p = scales_of(src);
         uint4 cur, nx = first, nn = nx;
         if (a.ksteps > 2) nn = load_scales(p, 1, a);
@@ -393,6 +445,7 @@ __global__ void __launch_bounds__(kExpThreads, 1)
           // rows that are no route keep what was there: any codes, in rows that are not stored
           const unsigned char* from[8];
           unsigned has = 0u;
+          const int mine = min(t.rows - w32, 32);  // rows of this warp, 0 or fewer: none
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const int s = __shfl_sync(kFull, src, 4 * j + sub4);
@@ -444,7 +497,8 @@ __global__ void __launch_bounds__(kExpThreads, 1)
     const size_t apart = static_cast<size_t>(BN) * a.scols;  // a row and the next tile's
     const size_t down = static_cast<size_t>(128) * a.scols;
     ExpertsUnit f;
-    n.at(a, t.it + step, units, BN);
+    look(n, t.it + step);
+    t.resolve(a, units);
     // the thread's first row of a unit's first tile, and the outputs from it on (none: no row)
     auto start = [&](const ExpertsUnit& q, int& left) -> const unsigned char* {
       left = q.valid(a) ? a.N - (q.n0 + i) : 0;
@@ -461,7 +515,8 @@ __global__ void __launch_bounds__(kExpThreads, 1)
     load(p, left, 0, first);
     const uint32_t place = wscales + scale_place(i);
     for (; ok && t.it < units; t = n, n = f) {
-      f.at(a, n.it + step, units, BN);
+      look(f, n.it + step);
+      n.resolve(a, units);
       const unsigned char* pn = start(n, left_n);
       const int tiles = t.valid(a) ? t.tiles : 1;  // one round that only looks ahead
       for (int c = 0; ok && c < tiles; ++c) {
@@ -561,18 +616,30 @@ cudaError_t launch_experts(const CUtensorMap& wmap, const ExpertsArgs& a, int gr
   return launch_pdl(k, dim3(grid), dim3(kExpThreads), smem, st, wmap, a);
 }
 
-// Tile width and units of a call with at most `blocks` row tiles of `sub` rows.  An SM's time for
-// a tile goes by the bytes it takes in, its rows and BN weights, so the width is the one with the
-// smallest product of rounds and bytes.  Rows of at most half a ring's steps stay for several tiles once
-// every SM has work for eight rounds without that.
+// Tile width and units of a call.  Blocks below 128 rows go in windows where some expert can have
+// more than one (more routes than a block holds).  `tiles` counts row tiles at most: parts of
+// blocks, or with windows one per 128 routes and expert.  An SM's time for a tile goes by the bytes
+// it takes in, its rows and BN weights, so the width is the one with the smallest product of
+// rounds and bytes.  Rows of at most half a ring's steps stay for several tiles once every SM has
+// work for eight rounds without that.
 struct ExpertsPlan {
+  int group, span, subs;
   int bn, ntile, chunk, nchunk, ksteps;
 };
-ExpertsPlan experts_plan(int64_t blocks, int sub, int outs, int cols, int sms) {
+ExpertsPlan experts_plan(int64_t blocks, int64_t routes, int E, int B, int outs, int cols,
+                         int sms) {
   ExpertsPlan p{};
+  p.group = B >= kExpRows || routes <= B ? 1 : (kExpRows / B < 32 ? kExpRows / B : 32);
+  p.span = p.group > 1 ? p.group * B : (B < kExpRows ? B : kExpRows);
+  p.subs = p.group > 1 ? 1 : B / p.span;
+  int64_t rowtiles = blocks * p.subs;
+  if (p.group > 1) {
+    const int64_t runs = routes / p.span + (routes < E ? routes : E);
+    rowtiles = rowtiles < runs ? rowtiles : runs;
+  }
   auto cost = [&](int bn) {
-    const int64_t tiles = blocks * ((outs + bn - 1) / bn);
-    return (tiles + sms - 1) / sms * (sub + bn);
+    const int64_t tiles = rowtiles * ((outs + bn - 1) / bn);
+    return (tiles + sms - 1) / sms * (p.span + bn);
   };
   p.bn = 128;
   if (cost(192) < cost(p.bn)) p.bn = 192;
@@ -584,7 +651,7 @@ ExpertsPlan experts_plan(int64_t blocks, int sub, int outs, int cols, int sms) {
                     : p.bn == 128 ? ExpertsShape<128>::kSlots
                                   : ExpertsShape<192>::kSlots;
   if (2 * p.ksteps <= slots) {
-    const int64_t each = blocks * p.ntile / (8 * static_cast<int64_t>(sms));
+    const int64_t each = rowtiles * p.ntile / (8 * static_cast<int64_t>(sms));
     p.chunk = each < 1 ? 1 : (each > p.ntile ? p.ntile : static_cast<int>(each));
   }
   p.nchunk = (p.ntile + p.chunk - 1) / p.chunk;
@@ -650,12 +717,14 @@ int moe_experts_mxfp4(const uint8_t* x_codes, const uint8_t* x_scales, int x_per
                       span(num_tokens_post_pad, 4)};
   if (any_alias(outs_s, 2, ins, 8)) return MOE_RS_ERR_ALIAS;
   const bool f32 = out_dtype == MOE_RS_FP32;
-  const int sub = block_m < kExpRows ? block_m : kExpRows;
-  const int64_t blocks = static_cast<int64_t>(P / block_m) * (block_m / sub);
-  if (blocks * ((outs + 127) / 128) > INT32_MAX / 2) return MOE_RS_ERR_OVERFLOW;
+  const int64_t blocks = static_cast<int64_t>(P / block_m);
+  // units: every part of 128 rows and every tile of outputs, windows of 32 blocks rounded up
+  if ((blocks * ((block_m + kExpRows - 1) / kExpRows) + 32) * ((outs + 95) / 96) > INT32_MAX / 2)
+    return MOE_RS_ERR_OVERFLOW;
   const int sms = sm_count();
   if (sms == 0) return launch_status(cudaErrorInvalidDevice);
-  const ExpertsPlan p = experts_plan(blocks, sub, outs, cols, sms);
+  const ExpertsPlan p =
+      experts_plan(blocks, static_cast<int64_t>(routes), E, block_m, outs, cols, sms);
   ExpertsArgs a{};
   a.xc = x_codes;
   a.xs = x_scales;
@@ -676,8 +745,9 @@ int moe_experts_mxfp4(const uint8_t* x_codes, const uint8_t* x_scales, int x_per
   a.scols = scols;
   a.max_rows = static_cast<int>(P);
   a.wait_limit_ns = debug_wait_limit_ns();
-  a.sub = sub;
-  a.subs = block_m / sub;
+  a.group = p.group;
+  a.span = p.span;
+  a.subs = p.subs;
   a.ntile = p.ntile;
   a.chunk = p.chunk;
   a.nchunk = p.nchunk;
@@ -686,7 +756,8 @@ int moe_experts_mxfp4(const uint8_t* x_codes, const uint8_t* x_scales, int x_per
   a.wide_out = aligned(out, 32) && outs * (f32 ? 4 : 2) % 32 == 0;
   CUtensorMap wmap;
   if (!encode_weights(&wmap, w_codes, cols / 2, outs, E, p.bn)) return MOE_RS_ERR_LAUNCH;
-  const int64_t units = blocks * p.nchunk;
+  const int64_t units = (p.group > 1 ? (blocks + p.group - 1) / p.group * p.group
+                                     : blocks * p.subs) * p.nchunk;
   const int grid = units < sms ? static_cast<int>(units) : sms;
   auto go = [&](auto n) {
     constexpr int BN = decltype(n)::value;

@@ -252,6 +252,13 @@ def test_product_many_tiles(T, E, K, cols, N, B, dtype):
     _check_product(T, E, K, cols, N, B, dtype=dtype, per_route=dtype == torch.float32)
 
 
+@pytest.mark.parametrize("B", [1, 2, 4, 16, 32, 64])
+@pytest.mark.parametrize("T,E,K", [(70, 2, 1), (300, 3, 2), (1000, 40, 4)])
+def test_product_blocks_that_share_a_tile(T, E, K, B):
+    # runs of one expert's blocks that start, end and are cut inside windows of 128 rows
+    _check_product(T, E, K, 288, 200, B, dist="drops" if K == 4 else "uniform")
+
+
 @pytest.mark.parametrize("dist", ["one", "drops"])
 @pytest.mark.parametrize("B", [16, 64, 128])
 @pytest.mark.parametrize("weighted", [False, True])
