@@ -10,7 +10,7 @@
 // tensor memory) by BN = 96, 128 or 192 outputs (the N side).  Blocks of more rows are cut;
 // neighbouring blocks of fewer rows that have the same expert share a tile: the list is taken in
 // windows of at most 128 rows and 32 blocks, and a tile is a run of one expert's blocks in a
-// window (block_m = 16, 4024 tokens, 191 experts, 1984 -> 656: 728 -> 113 us).  Rows on the lanes make the result a row per thread, so the
+// window (block_m = 16, 4024 tokens, 191 experts, 1984 -> 656: 728 -> 177 us).  Rows on the lanes make the result a row per thread, so the
 // outputs leave as 32-byte stores of whole sectors; a block of 16 rows costs the tensor core as
 // much as one of 128, which it has time for: such calls wait for the weights.  A persistent CTA
 // per SM takes units round robin, a unit being one tile, or for short rows several output tiles of
@@ -59,7 +59,7 @@ struct ExpertsArgs {
   void* out;
   unsigned long long wait_limit_ns;
   int routes, topk, per_route;
-  int E, K, N, B, scols, max_rows;
+  int E, K, N, B, log2B, scols, max_rows;
   int group;        // blocks of a window; 1: every block by itself, in `subs` parts
   int span, subs;   // rows of a window or part (<= 128)
   int ntile;        // tiles along the outputs
@@ -95,6 +95,7 @@ struct ExpertsShape {
 // `slot`, if one does), or a block's part, by some output tiles.  The expert ids it depends on are
 // in flight until resolve().  Runs are numbered after windows: the first runs of all windows, which
 // there always are, spread evenly over the CTAs.
+template <bool kWindows>
 struct ExpertsUnit {
   int it, p0, n0, tiles, slot, blocks;  // blocks: of the window that there are
   int id;    // of the window's block `lane`
@@ -104,13 +105,15 @@ struct ExpertsUnit {
                                      int total_blocks, int bn) {
     it = i;
     const int per = max(windows * a.nchunk, 1);
-    const int run = a.group > 1 ? i / per : 0;
+    const int run = kWindows ? i / per : 0;
     slot = min(run, 31);  // (past the last unit it means nothing)
-    const int q = i - run * per, b = q / a.nchunk, first = (q - b * a.nchunk) * a.chunk;
+    // (a division takes longer than a step of the ring; mostly there is nothing to divide by)
+    const int q = i - run * per, b = a.nchunk == 1 ? q : q / a.nchunk;
+    const int first = (q - b * a.nchunk) * a.chunk;
     n0 = first * bn;
     tiles = min(a.chunk, a.ntile - first);
     id = -1;
-    if (a.group > 1) {
+    if constexpr (kWindows) {
       const int lane = threadIdx.x & 31, b0 = b * a.group;
       p0 = (b0 + slot) * a.B;
       blocks = min(a.group, total_blocks - b0);
@@ -118,11 +121,11 @@ struct ExpertsUnit {
     } else {
       p0 = b * a.span;
       blocks = 1;
-      if (i < units) id = __ldg(a.eid + b / a.subs);
+      if (i < units) id = __ldg(a.eid + (a.subs == 1 ? b : b / a.subs));
     }
   }
   __device__ __forceinline__ void resolve(const ExpertsArgs& a, int units) {
-    if (a.group > 1) {
+    if constexpr (kWindows) {
       const int lane = threadIdx.x & 31;
       e = __shfl_sync(kFull, id, slot);
       const int before = __shfl_sync(kFull, id, max(slot - 1, 0));
@@ -185,7 +188,7 @@ __device__ __forceinline__ void store_shared(uint32_t dst, uint32_t v) {
 // Where the scales of row r of 128 start in a step's 512 bytes.
 __device__ __forceinline__ uint32_t scale_place(int r) { return 16 * (r & 31) + 4 * (r >> 5); }
 
-template <int BN, class Out>
+template <int BN, bool kWindows, class Out>
 __global__ void __launch_bounds__(kExpThreads, 1)
     mrs_experts_kernel(const __grid_constant__ CUtensorMap wmap, const ExpertsArgs a) {
   using Sh = ExpertsShape<BN>;
@@ -225,22 +228,23 @@ __global__ void __launch_bounds__(kExpThreads, 1)
 
   // one block a window: the first unit's list entries do not wait for the list's length
   const int step = gridDim.x;
-  ExpertsUnit t, n;
+  ExpertsUnit<kWindows> t, n;
   const int my_row = 32 * (warp & 3) + lane;  // of warps 4-11
   int entry = -1;
-  if (a.group == 1) {
-    const int most = a.max_rows / a.B * a.subs * a.nchunk;
+  if constexpr (!kWindows) {
+    const int most = (a.max_rows >> a.log2B) * a.subs * a.nchunk;
     t.at(a, blockIdx.x, most, 0, 0, BN);
     if (warp >= 4) entry = t.entry(a, my_row, most, a.max_rows);
   }
-  const int rows = min(max(__ldg(a.npp), 0), a.max_rows) / a.B * a.B, blocks = rows / a.B;
-  const int windows = a.group > 1 ? (blocks + a.group - 1) / a.group : blocks * a.subs;
-  const int units = a.group * windows * a.nchunk;
-  if (a.group > 1) {
+  const int blocks = min(max(__ldg(a.npp), 0), a.max_rows) >> a.log2B, rows = blocks << a.log2B;
+  const int windows =  // group and block_m are powers of two
+      kWindows ? (blocks + a.group - 1) >> (__ffs(a.group) - 1) : blocks * a.subs;
+  const int units = (kWindows ? a.group : 1) * windows * a.nchunk;
+  if constexpr (kWindows) {
     t.at(a, blockIdx.x, units, windows, blocks, BN);
     if (warp >= 4) entry = t.entry(a, my_row, units, rows);
   }
-  auto look = [&](ExpertsUnit& q, int i) { q.at(a, i, units, windows, blocks, BN); };
+  auto look = [&](ExpertsUnit<kWindows>& q, int i) { q.at(a, i, units, windows, blocks, BN); };
   // bytes of the last step's scales that are scales
   const int tail = a.K / 32 - 8 * (a.ksteps - 1);
   const uint32_t tail0 = scale_mask(tail), tail1 = scale_mask(tail - 4);
@@ -419,14 +423,14 @@ __global__ void __launch_bounds__(kExpThreads, 1)
     const uint32_t even = place + 16 * (chunk ^ sub4), odd = place + 16 * (chunk ^ (sub4 + 4));
     const uint32_t scale_at = xscales + scale_place(my_row);
     if (w32 < a.span) {
-      auto source = [&](const ExpertsUnit& q, int r) -> int {
+      auto source = [&](const ExpertsUnit<kWindows>& q, int r) -> int {
         if (!q.valid(a) || my_row >= q.rows || r < 0 || r >= a.routes) return -1;
         return a.per_route ? r : r / a.topk;
       };
       auto scales_of = [&](int s) -> const unsigned char* {
         return s < 0 ? nullptr : a.xs + static_cast<size_t>(s) * a.scols;
       };
-      ExpertsUnit f;
+      ExpertsUnit<kWindows> f;
       look(n, t.it + step);
       t.resolve(a, units);
       int src = source(t, entry);
@@ -496,11 +500,11 @@ __global__ void __launch_bounds__(kExpThreads, 1)
     const bool second = i + 128 < BN;
     const size_t apart = static_cast<size_t>(BN) * a.scols;  // a row and the next tile's
     const size_t down = static_cast<size_t>(128) * a.scols;
-    ExpertsUnit f;
+    ExpertsUnit<kWindows> f;
     look(n, t.it + step);
     t.resolve(a, units);
     // the thread's first row of a unit's first tile, and the outputs from it on (none: no row)
-    auto start = [&](const ExpertsUnit& q, int& left) -> const unsigned char* {
+    auto start = [&](const ExpertsUnit<kWindows>& q, int& left) -> const unsigned char* {
       left = q.valid(a) ? a.N - (q.n0 + i) : 0;
       return left > 0 ? a.ws + (static_cast<size_t>(q.e) * a.N + q.n0 + i) * a.scols : a.ws;
     };
@@ -605,10 +609,10 @@ bool encode_weights(CUtensorMap* map, const void* p, size_t row, size_t outs, si
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BN, class Out>
+template <int BN, bool kWindows, class Out>
 cudaError_t launch_experts(const CUtensorMap& wmap, const ExpertsArgs& a, int grid,
                            cudaStream_t st) {
-  auto* k = mrs_experts_kernel<BN, Out>;
+  auto* k = mrs_experts_kernel<BN, kWindows, Out>;
   constexpr size_t smem = ExpertsShape<BN>::kSmem;
   static SmemGrant granted;
   const cudaError_t err = grant_smem(reinterpret_cast<const void*>(k), smem, granted);
@@ -742,6 +746,7 @@ int moe_experts_mxfp4(const uint8_t* x_codes, const uint8_t* x_scales, int x_per
   a.K = cols;
   a.N = outs;
   a.B = block_m;
+  while ((1 << a.log2B) < block_m) ++a.log2B;
   a.scols = scols;
   a.max_rows = static_cast<int>(P);
   a.wait_limit_ns = debug_wait_limit_ns();
@@ -761,8 +766,11 @@ int moe_experts_mxfp4(const uint8_t* x_codes, const uint8_t* x_scales, int x_per
   const int grid = units < sms ? static_cast<int>(units) : sms;
   auto go = [&](auto n) {
     constexpr int BN = decltype(n)::value;
-    return f32 ? launch_experts<BN, float>(wmap, a, grid, stream)
-               : launch_experts<BN, __nv_bfloat16>(wmap, a, grid, stream);
+    if (p.group > 1)
+      return f32 ? launch_experts<BN, true, float>(wmap, a, grid, stream)
+                 : launch_experts<BN, true, __nv_bfloat16>(wmap, a, grid, stream);
+    return f32 ? launch_experts<BN, false, float>(wmap, a, grid, stream)
+               : launch_experts<BN, false, __nv_bfloat16>(wmap, a, grid, stream);
   };
   return launch_status(p.bn == 96    ? go(std::integral_constant<int, 96>{})
                        : p.bn == 128 ? go(std::integral_constant<int, 128>{})
