@@ -203,7 +203,7 @@ __device__ __forceinline__ unsigned vectors_past(int E, int lane, int lanes) {
   return p;
 }
 
-// Shared memory of both row kernels: the ring, then NC floats per thread.
+// Shared memory of the loss: the ring, then NC floats per thread.  (The gradient takes the ring.)
 template <int NC, bool kVec>
 __host__ __device__ constexpr size_t row_smem() {
   return (kVec ? 16ull * kBalThreads * kDepth * (NC / 8) : 0ull) +
@@ -272,24 +272,26 @@ __device__ __forceinline__ void sigmoids(float (&x)[NC]) {
 
 // Scores of one row in place, and the row's sums.  On return x holds the terms u_e of the lane
 // (scaled by a factor of its own for softmax), `scale` turns a term into a probability, and
-// `dot` is sum over e of p_e g_e (kDot).  xchg: [2][W] float4 of the group, buffer `buf`; bit v of
+// `dot` is sum over e of p_e g_e (kDot); 2^(x log2 e - `top`) `inv` is any column's
+// probability in a softmax.  xchg: [2][W] float4 of the group, buffer `buf`; bit v of
 // `past`: the lane's v-th vector of 8 columns lies past E.
 // A softmax lane takes 2^(x log2 e - m), m its own maximum times log2 e as rounded, and the
 // reduction rescales by differences of those same m: nothing is lost to the rounding of m.
 // (Two values per instruction, .f32x2, was tried: packing the exponentials cost what it saved.)
 template <int NC, bool kSoftmax, bool kDot>
 __device__ __forceinline__ void row_terms(float (&x)[NC], const float (&g)[kDot ? NC : 1],
-                                          unsigned past, int W, int grp, int gw, float4* xchg, int buf, float& scale,
-                                          float& dot) {
+                                          unsigned past, int W, int grp, int gw, float4* xchg,
+                                          int buf, float& scale, float& dot, float& top,
+                                          float& inv) {
   float m = 0.0f;
   if constexpr (kSoftmax) {
-    float top[2] = {kLowest, kLowest};
+    float m0 = kLowest, m1 = kLowest;
 #pragma unroll
     for (int i = 0; i < NC; i += 4) {
-      top[0] = max3(top[0], x[i], x[i + 1]);
-      top[1] = max3(top[1], x[i + 2], x[i + 3]);
+      m0 = max3(m0, x[i], x[i + 1]);
+      m1 = max3(m1, x[i + 2], x[i + 3]);
     }
-    m = fmaxf(top[0], top[1]);
+    m = fmaxf(m0, m1);
     if (!(fabsf(m) <= kFarLogit)) {  // also lanes of -inf alone
       m = fminf(fmaxf(m, -kFarLogit), kFarLogit);
 #pragma unroll
@@ -347,8 +349,10 @@ __device__ __forceinline__ void row_terms(float (&x)[NC], const float (&g)[kDot 
       if constexpr (kDot) sg = fmaf(q.z, r, sg);
     }
     if constexpr (kSoftmax) f *= ex2(m - M);
+    m = M;
   }
-  const float inv = sum > 0.0f ? rcp(sum) : 0.0f;
+  top = m;
+  inv = sum > 0.0f ? rcp(sum) : 0.0f;
   scale = f * inv;
   dot = sg * inv;
 }
@@ -405,9 +409,9 @@ __global__ void __launch_bounds__(kBalThreads, 1) mrs_balance_rows_kernel(const 
 #pragma unroll
       for (int c = 0; c < NC; ++c) acc[c] = 0.0f;
       for (int buf = 0; row < hi; row += groups, buf ^= 1) {
-        float x[NC], scale, dot;
+        float x[NC], scale, dot, top, inv;
         rows.take(E, groups, hi, lane, lanes, x);
-        row_terms<NC, kSoftmax, false>(x, g0, past, W, grp, gw, xchg, buf, scale, dot);
+        row_terms<NC, kSoftmax, false>(x, g0, past, W, grp, gw, xchg, buf, scale, dot, top, inv);
 #pragma unroll
         for (int c = 0; c < NC; ++c) acc[c] = fmaf(x[c], scale, acc[c]);
       }
@@ -538,17 +542,10 @@ __global__ void __launch_bounds__(kBalThreads, 1)
   const int grp = warp / W, gw = warp - grp * W, groups = groups_of(W);
   const int lanes = 32 * W, lane = 32 * gw + wl;
   float4* xchg = &xchg_s[0][0] + grp * 2 * W;
-  // the routed experts' part of the group's current row, zero elsewhere; a warp only touches the
-  // columns that its own lanes hold
-  float* add = reinterpret_cast<float*>(smem + row_smem<NC, kVec>()) - kBalThreads * NC +
-               static_cast<size_t>(grp) * lanes * NC;
   const uint32_t ring = smem_u32(smem) + 16 * tid;
   const unsigned past = vectors_past<NC, kVec>(E, lane, lanes);
   pdl_trigger();
   if (grp >= groups) return;  // a W that does not divide the warps leaves some without a group
-#pragma unroll
-  for (int c = 0; c < NC; ++c) add[column_of<kVec>(c, lane, lanes)] = 0.0f;
-  __syncwarp();
   pdl_wait();
   const bool dense = a.gl != nullptr, sparse = a.gw != nullptr;
   const float gl = dense ? __ldg(a.gl) : 0.0f;
@@ -572,13 +569,14 @@ __global__ void __launch_bounds__(kBalThreads, 1)
       in_seq = lo_i <= t;
       hi = min(t1, in_seq ? hi_i : lo_i);
     }
-    float g[NC];
+    float g[NC], f = 0.0f;
 #pragma unroll
     for (int c = 0; c < NC; ++c) g[c] = 0.0f;
+    const int32_t* counts = a.counts;
     if (dense && in_seq) {
       const float n = static_cast<float>(hi_i - lo_i);
-      const float f = gl * (a.coef / a.S) * (static_cast<float>(E) / K) / n / n;
-      const int32_t* counts = a.counts + static_cast<size_t>(i) * E;
+      f = gl * (a.coef / a.S) * (static_cast<float>(E) / K) / n / n;
+      counts += static_cast<size_t>(i) * E;
       if (kVec && a.wide_counts) {
 #pragma unroll
         for (int c = 0; c < NC; c += 4) {
@@ -616,12 +614,13 @@ __global__ void __launch_bounds__(kBalThreads, 1)
       int id = next_id;
       float wg = next_gw;
       const bool valid = sparse && wl < K && id >= 0 && id < E;
-      float xk = valid ? bf16_bits_to_float(__ldg(xr + id)) : -INFINITY;
+      const float xk = valid ? bf16_bits_to_float(__ldg(xr + id)) : -INFINITY;
+      const float gk = valid && f != 0.0f ? f * static_cast<float>(__ldg(counts + id)) : 0.0f;
       fetch(row + groups);
       rows.take(E, groups, hi, lane, lanes, x);
-      float scale = 0.0f, dot = 0.0f;
+      float scale = 0.0f, dot = 0.0f, top = 0.0f, inv = 0.0f;
       if (dense) {
-        row_terms<NC, kSoftmax, true>(x, g, past, W, grp, gw, xchg, buf, scale, dot);
+        row_terms<NC, kSoftmax, true>(x, g, past, W, grp, gw, xchg, buf, scale, dot, top, inv);
         buf ^= 1;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
@@ -631,52 +630,6 @@ __global__ void __launch_bounds__(kBalThreads, 1)
       } else {
 #pragma unroll
         for (int c = 0; c < NC; ++c) x[c] = 0.0f;
-      }
-      if (sparse) {
-        // every warp of the group works the K routes out, and keeps those in its columns
-        if (!valid) wg = 0.0f;
-        float u;
-        if (kSoftmax) {
-          const float m = fmaxf(warp_max(xk), kLowest);
-          u = ex2((xk - m) * kLog2e);
-        } else {
-          u = rcp(1.0f + ex2(-kLog2e * xk));  // 0 for a route that is none
-        }
-        const float su = warp_sum(u);
-        const float q = su > 0.0f ? u / su : 0.0f;
-        const float mean = warp_sum(q * wg);
-        float d = a.R * q * (wg - mean);
-        if (!kSoftmax) d *= 1.0f - u;
-        // an expert named twice: the lowest lane takes the sum, in slot order
-        const int key = valid ? id : -1 - wl;
-        const unsigned same = __match_any_sync(kFull, key);
-        if (__any_sync(kFull, (same & (same - 1u)) != 0u)) {
-          float s = 0.0f;
-          for (int l = 0; l < 32; ++l) {
-            const float o = __shfl_sync(kFull, d, l);
-            if ((same >> l) & 1u) s += o;
-          }
-          d = s;
-        }
-        const int owner = kVec ? (id >> 3) % lanes : id % lanes;
-        const bool put = valid && (same & lanemask_lt(wl)) == 0u && (owner >> 5) == gw;
-        if (put) add[id] = d;
-        __syncwarp();
-        if constexpr (kVec) {
-#pragma unroll
-          for (int c = 0; c < NC; c += 4) {
-            const float4 q = *reinterpret_cast<const float4*>(add + column_of<kVec>(c, lane, lanes));
-            x[c] += q.x;
-            x[c + 1] += q.y;
-            x[c + 2] += q.z;
-            x[c + 3] += q.w;
-          }
-        } else {
-#pragma unroll
-          for (int c = 0; c < NC; ++c) x[c] += add[column_of<kVec>(c, lane, lanes)];
-        }
-        __syncwarp();
-        if (put) add[id] = 0.0f;
       }
       Out* out = static_cast<Out*>(a.out) + static_cast<size_t>(row) * E;
       if constexpr (kVec) {
@@ -707,6 +660,45 @@ __global__ void __launch_bounds__(kBalThreads, 1)
           if (e >= E) continue;
           if constexpr (sizeof(Out) == 4) out[e] = x[c];
           else out[e] = __float2bfloat16_rn(x[c]);
+        }
+      }
+      if (sparse) {
+        // Every warp of the group works the K routes out, lane k route k, and writes those in its
+        // columns: the whole gradient there, its balance term taken anew from the row's sums, over
+        // the one that the column's lane has just written.
+        if (!valid) wg = 0.0f;
+        float u, s = 0.0f;
+        if (kSoftmax) {
+          const float m = fmaxf(warp_max(xk), kLowest);
+          u = ex2((xk - m) * kLog2e);
+        } else {
+          u = s = rcp(1.0f + ex2(-kLog2e * xk));  // 0 for a route that is none
+        }
+        const float su = warp_sum(u);
+        const float q = su > 0.0f ? u * rcp(su) : 0.0f;
+        const float mean = warp_sum(q * wg);
+        float d = a.R * q * (wg - mean);
+        if (!kSoftmax) d *= 1.0f - s;
+        // an expert named twice: the lowest lane takes the sum, in slot order
+        const int key = valid ? id : -1 - wl;
+        const unsigned same = __match_any_sync(kFull, key);
+        if (__any_sync(kFull, (same & (same - 1u)) != 0u)) {
+          float all = 0.0f;
+          for (int l = 0; l < 32; ++l) {
+            const float o = __shfl_sync(kFull, d, l);
+            if ((same >> l) & 1u) all += o;
+          }
+          d = all;
+        }
+        const int owner = kVec ? (id >> 3) % lanes : id % lanes;
+        const float xc = fminf(fmaxf(xk, -kFarLogit), kFarLogit);
+        const float p = kSoftmax ? (xk == -INFINITY ? 0.0f : ex2(fmaf(xc, kLog2e, -top)) * inv)
+                                 : s * inv;
+        d = fmaf(kSoftmax ? p : fmaf(-p, s, p), gk - dot, d);
+        __syncwarp();  // the row's own stores come first
+        if (valid && (same & lanemask_lt(wl)) == 0u && (owner >> 5) == gw) {
+          if constexpr (sizeof(Out) == 4) out[id] = d;
+          else out[id] = __float2bfloat16_rn(d);
         }
       }
     }
@@ -788,7 +780,7 @@ template <int NC, bool kVec, int kW, class Out>
 cudaError_t launch_backward(const RouteBackwardArgs& a, bool softmax, int ctas, cudaStream_t st) {
   auto* k = softmax ? mrs_route_backward_kernel<NC, kVec, true, kW, Out>
                     : mrs_route_backward_kernel<NC, kVec, false, kW, Out>;
-  const size_t smem = row_smem<NC, kVec>();
+  const size_t smem = row_smem<NC, kVec>() - sizeof(float) * kBalThreads * NC;  // the ring alone
   static SmemGrant granted[2];
   const cudaError_t err =
       grant_smem(reinterpret_cast<const void*>(k), smem, granted[softmax]);
