@@ -25,19 +25,20 @@
 //   4-7    a finished tile from tensor memory to the output rows, while the next one is computed
 //          (two accumulators; eight warps with half the columns each were slower, 484 us against
 //          444 at T = 8192, 384 -> 3584)
-//   8-11   the block's rows, 16 bytes a thread into the same swizzle (the copies arrive on the
-//          slot's barrier themselves), and their scales
-//   12-15  the weights' scales
+//   8-11   the rows, 16 bytes a thread into the same swizzle, and their scales, all copies that
+//          arrive on the slot's barrier themselves; where one warp or two hold the rows, the others
+//          take steps of their own
+//   12-15  the weights' scales, a step a warp in turn
 // Scales go from row-major bytes to the order that tensor memory wants: row r of 128 on lane
-// r % 32, word r / 32 of 4 scales.
+// r % 32, word r / 32 of 4 scales.  (A warp works through a step in 600 to 900 clocks whatever
+// there is to do, so taking turns is what keeps a single token's 14 steps short: 10.6 us before.)
 //
 // What bounds it: an SM takes in at most 38 bytes a clock (measured, tensor copies, thread copies
 // and multicast alike, on one SM and on all), so a step of 128 x 128 costs 890 clocks and its
 // products 260; hence the wider tile, and rows that stay.  Few tokens are bound by HBM, which
 // gives an SM 23 bytes a clock.
 //
-// Each task has the list entries of the next two units and the first scales of the next one in
-// flight.  Every wait is bounded; a wait that gives up ends its warp's task with the status bit
+// Each task has the list entries of the next unit in flight.  Every wait is bounded; a wait that gives up ends its warp's task with the status bit
 // set, and the CTA leaves once nothing of its own is in flight.
 #include <type_traits>
 
@@ -66,7 +67,7 @@ struct ExpertsArgs {
   int chunk;        // tiles of a unit (the last of a block may have fewer)
   int nchunk;       // units along the outputs
   int ksteps;       // steps of 256 columns
-  int wide_scales;  // scale rows start on 16 bytes
+  int wide_scales;  // the weights' scale rows start on 8 bytes
   int wide_out;     // output rows start on 32 bytes
 };
 
@@ -160,19 +161,13 @@ struct RingPlace {
   }
 };
 
-// Scales of one row, 16 bytes (two steps) at a time; zeros past the row's end and for null rows.
-// Nothing here looks at what it loads: a use would wait for it.
-__device__ __forceinline__ uint4 load_scales(const unsigned char* row, int pair, const ExpertsArgs& a) {
-  const int at = 16 * pair, left = a.K / 32 - at;
-  uint4 q = make_uint4(0u, 0u, 0u, 0u);
-  if (row == nullptr || left <= 0) return q;
-  if (a.wide_scales) return __ldg(reinterpret_cast<const uint4*>(row + at));
+// Scales of one row of weights for step `ks`; zeros past the row's end.  Nothing here looks at what
+// it loads: a use would wait for it.
+__device__ __forceinline__ uint2 load_scales(const unsigned char* row, int ks, const ExpertsArgs& a) {
+  const int at = 8 * ks, left = a.K / 32 - at;
+  if (a.wide_scales) return __ldg(reinterpret_cast<const uint2*>(row + at));
   const uint32_t* p = reinterpret_cast<const uint32_t*>(row + at);
-  q.x = __ldg(p);
-  if (left > 4) q.y = __ldg(p + 1);
-  if (left > 8) q.z = __ldg(p + 2);
-  if (left > 12) q.w = __ldg(p + 3);
-  return q;
+  return make_uint2(__ldg(p), left > 4 ? __ldg(p + 1) : 0u);
 }
 
 // Mask of the first `left` bytes of four scales: what lies behind a row's K / 32 scales is
@@ -181,8 +176,10 @@ __device__ __forceinline__ uint32_t scale_mask(int left) {
   return left >= 4 ? ~0u : (left <= 0 ? 0u : (1u << (8 * left)) - 1u);
 }
 
-__device__ __forceinline__ void store_shared(uint32_t dst, uint32_t v) {
-  asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst), "r"(v) : "memory");
+__device__ __forceinline__ void store_shared(uint32_t dst, uint32_t a, uint32_t b, uint32_t c,
+                                             uint32_t d) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
 }
 
 // Where the scales of row r of 128 start in a step's 512 bytes.
@@ -203,13 +200,13 @@ __global__ void __launch_bounds__(kExpThreads, 1)
   const uint32_t xbase = base, wbase = base + S * Sh::kX;
   const uint32_t xscales = wbase + S * Sh::kW, wscales = xscales + S * 1024;
   const unsigned long long limit = a.wait_limit_ns;
-  const int copiers = (a.span + 31) / 32;  // warps with rows of a window
+  const int copiers = (a.span + 31) / 32;  // warps that hold a window's rows: 1, 2 or 4
   pdl_trigger();
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(&xfull_s[s], 33 * copiers);  // every copying thread, and each warp for its scales
+      mbar_init(&xfull_s[s], 32 * copiers);  // every copying thread
       mbar_init(&xfree_s[s], 1);
-      mbar_init(&wfull_s[s], 1 + 4);  // the weights' copy, and the scales' four warps
+      mbar_init(&wfull_s[s], 1 + 1);  // the weights' copy, and the warp with its scales
       mbar_init(&wfree_s[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -229,12 +226,13 @@ __global__ void __launch_bounds__(kExpThreads, 1)
   // one block a window: the first unit's list entries do not wait for the list's length
   const int step = gridDim.x;
   ExpertsUnit<kWindows> t, n;
-  const int my_row = 32 * (warp & 3) + lane;  // of warps 4-11
+  // of warps 4-7 (a quarter of the lanes each) and 8-11
+  const int my_row = 32 * (warp < 8 ? warp & 3 : (warp - 8) & (copiers - 1)) + lane;
   int entry = -1;
   if constexpr (!kWindows) {
     const int most = (a.max_rows >> a.log2B) * a.subs * a.nchunk;
     t.at(a, blockIdx.x, most, 0, 0, BN);
-    if (warp >= 4) entry = t.entry(a, my_row, most, a.max_rows);
+    if (warp >= 4 && warp < 12) entry = t.entry(a, my_row, most, a.max_rows);
   }
   const int blocks = min(max(__ldg(a.npp), 0), a.max_rows) >> a.log2B, rows = blocks << a.log2B;
   const int windows =  // group and block_m are powers of two
@@ -242,7 +240,7 @@ __global__ void __launch_bounds__(kExpThreads, 1)
   const int units = (kWindows ? a.group : 1) * windows * a.nchunk;
   if constexpr (kWindows) {
     t.at(a, blockIdx.x, units, windows, blocks, BN);
-    if (warp >= 4) entry = t.entry(a, my_row, units, rows);
+    if (warp >= 4 && warp < 12) entry = t.entry(a, my_row, units, rows);
   }
   auto look = [&](ExpertsUnit<kWindows>& q, int i) { q.at(a, i, units, windows, blocks, BN); };
   // bytes of the last step's scales that are scales
@@ -413,157 +411,125 @@ __global__ void __launch_bounds__(kExpThreads, 1)
       }
     }
   } else if (warp >= 8 && warp < 12) {
-    // warp w copies rows 32 w .. 32 w + 31 of the block, four rows (8 lanes each) at a time, and
-    // lane l the scales of row 32 w + l
-    const int w32 = 32 * (warp - 8);
+    // a warp copies rows w32 .. w32 + 31 of the unit, four rows (8 lanes each) at a time, and lane l
+    // the scales of row w32 + l, in every turns-th step
+    const int w32 = my_row - lane, turns = 4 / copiers, turn = (warp - 8) / copiers;
+    int now = 0;  // whose step it is (at most 4 steps lie between two of a warp: less than a ring)
+    static_assert(S >= 4, "");
     const int chunk = lane & 7, sub4 = lane >> 3;
     const size_t half = static_cast<size_t>(a.K / 2);
     // row 4 j + sub4 of the warp: two swizzles, for even and odd j
     const uint32_t place = xbase + (w32 + sub4) * kStepBytes;
     const uint32_t even = place + 16 * (chunk ^ sub4), odd = place + 16 * (chunk ^ (sub4 + 4));
     const uint32_t scale_at = xscales + scale_place(my_row);
-    if (w32 < a.span) {
-      auto source = [&](const ExpertsUnit<kWindows>& q, int r) -> int {
-        if (!q.valid(a) || my_row >= q.rows || r < 0 || r >= a.routes) return -1;
-        return a.per_route ? r : r / a.topk;
-      };
-      auto scales_of = [&](int s) -> const unsigned char* {
-        return s < 0 ? nullptr : a.xs + static_cast<size_t>(s) * a.scols;
-      };
-      ExpertsUnit<kWindows> f;
+    for (; ok && t.it < units; t = n) {
       look(n, t.it + step);
-      t.resolve(a, units);
-      int src = source(t, entry);
+      const int r = entry;
       entry = n.entry(a, my_row, units, rows);
-      uint4 first = load_scales(scales_of(src), 0, a);
-      for (; ok && t.it < units; t = n, n = f) {
-        look(f, n.it + step);
-        n.resolve(a, units);
-        const int src_n = source(n, entry);
-        entry = f.entry(a, my_row, units, rows);
-        const unsigned char* p = scales_of(src);
-        uint4 cur, nx = first, nn = nx;
-        if (a.ksteps > 2) nn = load_scales(p, 1, a);
-        first = load_scales(scales_of(src_n), 0, a);
-        if (t.valid(a)) {
-          // rows that are no route keep what was there: any codes, in rows that are not stored
-          const unsigned char* from[8];
-          unsigned has = 0u;
-          const int mine = min(t.rows - w32, 32);  // rows of this warp, 0 or fewer: none
+      t.resolve(a, units);
+      if (!t.valid(a)) continue;
+      const int src = my_row < t.rows && r >= 0 && r < a.routes
+                          ? (a.per_route ? r : r / a.topk) : -1;
+      // rows that are no route keep the codes that were there, in rows that are not stored, and
+      // get scales of zero bytes
+      const unsigned char* scales = a.xs + static_cast<size_t>(max(src, 0)) * a.scols;
+      const unsigned char* from[8];
+      unsigned has = 0u;
+      const int mine = min(t.rows - w32, 32);  // rows of this warp, 0 or fewer: none
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int s = __shfl_sync(kFull, src, 4 * j + sub4);
+        from[j] = a.xc + static_cast<size_t>(max(s, 0)) * half + 16 * chunk;
+        has |= s >= 0 ? 1u << j : 0u;
+      }
+      for (int ks = 0; ks < a.ksteps; ++ks) {
+        if (now == turn) {
+          ok = warp_wait(&xfree_s[x.slot], x.phase ^ 1u, limit);
+          if (!ok) break;
+          const uint32_t dst = x.slot * Sh::kX;
+          // (columns past K keep what was there too: they meet weights that read as zero)
+          const unsigned live = ks * kStepBytes + 16 * chunk < a.K / 2 ? has : 0u;
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const int s = __shfl_sync(kFull, src, 4 * j + sub4);
-            from[j] = a.xc + static_cast<size_t>(max(s, 0)) * half + 16 * chunk;
-            has |= s >= 0 ? 1u << j : 0u;
+            if (4 * j >= mine) break;
+            if ((live >> j) & 1u)
+              copy16(dst + ((j & 1) ? odd : even) + 512 * j,
+                     from[j] + static_cast<size_t>(ks) * kStepBytes);
           }
-          for (int ks = 0; ks < a.ksteps; ++ks) {
-            if ((ks & 1) == 0) {
-              cur = nx;
-              nx = nn;
-              if (ks + 4 < a.ksteps) nn = load_scales(p, ks / 2 + 2, a);
-            } else {
-              cur.x = cur.z;
-              cur.y = cur.w;
-            }
-            ok = warp_wait(&xfree_s[x.slot], x.phase ^ 1u, limit);
-            if (!ok) break;
-            const uint32_t dst = x.slot * Sh::kX;
-            // (columns past K keep what was there too: they meet weights that read as zero)
-            const unsigned live = ks * kStepBytes + 16 * chunk < a.K / 2 ? has : 0u;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              if (4 * j >= mine) break;
-              if ((live >> j) & 1u) copy16(dst + ((j & 1) ? odd : even) + 512 * j, from[j]);
-              from[j] += kStepBytes;
-            }
-            copy_arrive(&xfull_s[x.slot]);
-            if (ks + 1 == a.ksteps) {
-              cur.x &= tail0;
-              cur.y &= tail1;
-            }
-            store_shared(scale_at + x.slot * 1024, cur.x);
-            store_shared(scale_at + x.slot * 1024 + 512, cur.y);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&xfull_s[x.slot]);
-            x.advance();
-          }
+          const int left = src < 0 ? 0 : a.K / 32 - 8 * ks;  // scales from this step on
+          const unsigned char* q = scales + (left > 0 ? 8 * ks : 0);
+          copy4(scale_at + x.slot * 1024, q, min(max(left, 0), 4));
+          copy4(scale_at + x.slot * 1024 + 512, left > 4 ? q + 4 : q, min(max(left - 4, 0), 4));
+          copy_arrive(&xfull_s[x.slot]);
         }
-        src = src_n;
+        if (++now == turns) now = 0;
+        x.advance();
       }
-      copy_wait_all();
     }
+    copy_wait_all();
   } else if (warp >= 12) {
-    // a thread has one row of the weights, and the first 64 one of the second 128
-    const int i = tid - 384;
-    constexpr int kRowsEach = Sh::kAtoms;
-    const bool second = i + 128 < BN;
-    const size_t apart = static_cast<size_t>(BN) * a.scols;  // a row and the next tile's
-    const size_t down = static_cast<size_t>(128) * a.scols;
-    ExpertsUnit<kWindows> f;
-    look(n, t.it + step);
-    t.resolve(a, units);
-    // the thread's first row of a unit's first tile, and the outputs from it on (none: no row)
-    auto start = [&](const ExpertsUnit<kWindows>& q, int& left) -> const unsigned char* {
-      left = q.valid(a) ? a.N - (q.n0 + i) : 0;
-      return left > 0 ? a.ws + (static_cast<size_t>(q.e) * a.N + q.n0 + i) * a.scols : a.ws;
-    };
-    auto load = [&](const unsigned char* p, int left, int pair, uint4 (&q)[kRowsEach]) {
-      q[0] = load_scales(left > 0 ? p : nullptr, pair, a);
-      if constexpr (kRowsEach == 2)
-        q[1] = load_scales(second && left > 128 ? p + down : nullptr, pair, a);
-    };
-    int left, left_n;
-    const unsigned char* p = start(t, left);
-    uint4 first[kRowsEach], cur[kRowsEach], nx[kRowsEach], nn[kRowsEach];
-    load(p, left, 0, first);
-    const uint32_t place = wscales + scale_place(i);
-    for (; ok && t.it < units; t = n, n = f) {
-      look(f, n.it + step);
-      n.resolve(a, units);
-      const unsigned char* pn = start(n, left_n);
-      const int tiles = t.valid(a) ? t.tiles : 1;  // one round that only looks ahead
-      for (int c = 0; ok && c < tiles; ++c) {
+    // Steps go to the four warps in turn, and a warp loads its next step's scales before it hands on
+    // the last one's.  Lane l has the rows l + 32 r.  (A slot's barrier only tells odd rounds from
+    // even ones: a warp may ask for a round only once the one two back is over, which its own step
+    // four back vouches for in a ring of four or more.)
+    static_assert(S >= 4, "");
+    constexpr int kR = BN / 32;  // rows of a lane
+    constexpr int kWords = 4 * Sh::kAtoms;
+    const int me = warp - 12;
+    int at = 0;  // steps so far, all warps' together
+    bool have = false, have_last = false;
+    RingPlace<S> had;
+    uint2 cur[kR], nx[kR];
+    auto hand_on = [&] {
+      if (!have) return;
+      ok = warp_wait(&wfree_s[had.slot], had.phase ^ 1u, limit);
+      if (!ok) return;
+      const uint32_t dst = wscales + had.slot * (1024 * Sh::kAtoms) + 16 * lane;
+      const uint32_t keep0 = have_last ? tail0 : ~0u, keep1 = have_last ? tail1 : ~0u;
+      uint32_t w0[kWords], w1[kWords];
 #pragma unroll
-        for (int j = 0; j < kRowsEach; ++j) nn[j] = nx[j] = first[j];
-        if (a.ksteps > 2) load(p, left, 1, nn);
-        const bool more = c + 1 < tiles;
-        load(more ? p + apart : pn, more ? left - BN : left_n, 0, first);
-        if (t.valid(a)) {
-          for (int ks = 0; ks < a.ksteps; ++ks) {
+      for (int r = 0; r < kWords; ++r) {
+        w0[r] = r < kR ? cur[r < kR ? r : 0].x & keep0 : 0u;
+        w1[r] = r < kR ? cur[r < kR ? r : 0].y & keep1 : 0u;
+      }
 #pragma unroll
-            for (int j = 0; j < kRowsEach; ++j) {
-              if ((ks & 1) == 0) {
-                cur[j] = nx[j];
-                nx[j] = nn[j];
-              } else {
-                cur[j].x = cur[j].z;
-                cur[j].y = cur[j].w;
-              }
+      for (int q = 0; q < Sh::kAtoms; ++q) {
+        store_shared(dst + 512 * q, w0[4 * q], w0[4 * q + 1], w0[4 * q + 2], w0[4 * q + 3]);
+        store_shared(dst + 512 * (Sh::kAtoms + q), w1[4 * q], w1[4 * q + 1], w1[4 * q + 2],
+                     w1[4 * q + 3]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&wfull_s[had.slot]);
+    };
+    for (; ok && t.it < units; t = n) {
+      look(n, t.it + step);
+      t.resolve(a, units);
+      if (!t.valid(a)) continue;
+      for (int c = 0; ok && c < t.tiles; ++c) {
+        const int o = t.n0 + c * BN + lane;
+        const unsigned char* p = a.ws + (static_cast<size_t>(t.e) * a.N + o) * a.scols;
+        for (int ks = 0; ks < a.ksteps; ++ks) {
+          if ((at++ & 3) == me) {
+#pragma unroll
+            for (int r = 0; r < kR; ++r) {
+              nx[r] = make_uint2(0u, 0u);
+              if (o + 32 * r < a.N)
+                nx[r] = load_scales(p + static_cast<size_t>(32 * r) * a.scols, ks, a);
             }
-            if ((ks & 1) == 0 && ks + 4 < a.ksteps) load(p, left, ks / 2 + 2, nn);
-            ok = warp_wait(&wfree_s[w.slot], w.phase ^ 1u, limit);
+            hand_on();
             if (!ok) break;
-            const uint32_t dst = place + w.slot * (1024 * Sh::kAtoms);
 #pragma unroll
-            for (int j = 0; j < kRowsEach; ++j) {
-              if (ks + 1 == a.ksteps) {
-                cur[j].x &= tail0;
-                cur[j].y &= tail1;
-              }
-              store_shared(dst + 512 * j, cur[j].x);
-              store_shared(dst + 512 * (Sh::kAtoms + j), cur[j].y);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&wfull_s[w.slot]);
-            w.advance();
+            for (int r = 0; r < kR; ++r) cur[r] = nx[r];
+            had = w;
+            have = true;
+            have_last = ks + 1 == a.ksteps;
           }
+          w.advance();
         }
-        p = more ? p + apart : pn;
-        left = more ? left - BN : left_n;
       }
     }
+    if (ok) hand_on();
   }
   if (!ok && lane == 0) atomicOr(a.status, MOE_RS_DEVICE_WAIT_TIMEOUT);
   tc_fence_before();
@@ -757,7 +723,7 @@ int moe_experts_mxfp4(const uint8_t* x_codes, const uint8_t* x_scales, int x_per
   a.chunk = p.chunk;
   a.nchunk = p.nchunk;
   a.ksteps = p.ksteps;
-  a.wide_scales = scols % 16 == 0 && aligned(x_scales, 16) && aligned(w_scales, 16);
+  a.wide_scales = scols % 8 == 0 && aligned(w_scales, 8);
   a.wide_out = aligned(out, 32) && outs * (f32 ? 4 : 2) % 32 == 0;
   CUtensorMap wmap;
   if (!encode_weights(&wmap, w_codes, cols / 2, outs, E, p.bn)) return MOE_RS_ERR_LAUNCH;

@@ -130,6 +130,11 @@ template <int kLeft>
 __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
+// 4 bytes, of which the first `bytes` are read and the others are zeros.
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
 // One arrival on the barrier (counted in its expected number) once this thread's copies so far
 // have landed.
 __device__ __forceinline__ void copy_arrive(unsigned long long* mbar) {
