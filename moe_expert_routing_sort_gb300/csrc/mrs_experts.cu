@@ -153,6 +153,11 @@ template <int S>
 struct RingPlace {
   int slot = 0;
   uint32_t phase = 0;
+  __device__ __forceinline__ void skip(int steps) {
+    const int to = slot + steps;
+    phase ^= static_cast<uint32_t>(to / S) & 1u;
+    slot = to % S;
+  }
   __device__ __forceinline__ void advance() {
     if (++slot == S) {
       slot = 0;
@@ -249,6 +254,8 @@ __global__ void __launch_bounds__(kExpThreads, 1)
   bool ok = true;
   RingPlace<S> x, w;
 
+  // Tasks that wait for every step do it without agreeing on the outcome (a vote takes 80 clocks):
+  // one thread works alone, or each lane for itself until the unit ends.
   if (warp == 0) {
     long long issued = 0;
     for (; ok && t.it < units; t = n) {
@@ -258,26 +265,29 @@ __global__ void __launch_bounds__(kExpThreads, 1)
         if (t.lead && lane == 0) atomicOr(a.status, MOE_RS_DEVICE_BAD_EXPERT_ID);
         continue;
       }
-      for (int c = 0; ok && c < t.tiles; ++c) {
-        for (int ks = 0; ks < a.ksteps; ++ks) {
-          ok = warp_wait(&wfree_s[w.slot], w.phase ^ 1u, limit);
-          if (!ok) break;
-          if (elect_one()) {
-            mbar_expect(&wfull_s[w.slot], Sh::kW);
-            tma_load_3d(wbase + w.slot * Sh::kW, &wmap, ks * kStepBytes, t.n0 + c * BN, t.e,
-                        &wfull_s[w.slot]);
+      const int steps = t.tiles * a.ksteps;
+      if (elect_one()) {
+        RingPlace<S> at = w;
+        for (int c = 0; ok && c < t.tiles; ++c) {
+          for (int ks = 0; ks < a.ksteps; ++ks) {
+            ok = thread_wait(&wfree_s[at.slot], at.phase ^ 1u, limit);
+            if (!ok) break;
+            mbar_expect(&wfull_s[at.slot], Sh::kW);
+            tma_load_3d(wbase + at.slot * Sh::kW, &wmap, ks * kStepBytes, t.n0 + c * BN, t.e,
+                        &wfull_s[at.slot]);
+            ++issued;
+            at.advance();
           }
-          __syncwarp();
-          ++issued;
-          w.advance();
+        }
+        if (!ok) {
+          // a copy still on its way must land before the CTA leaves; the phase it completes may be
+          // missing other arrivals, so this waits for what has no one to take it any more
+          for (long long q = issued > S ? issued - S : 0; q < issued; ++q)
+            thread_wait(&wfull_s[q % S], static_cast<uint32_t>(q / S) & 1u, kWaitLimitNs);
         }
       }
-    }
-    if (!ok) {
-      // a copy still on its way must land before the CTA leaves; the phase it completes may be
-      // missing other arrivals, so this waits for what has no one to take it any more
-      for (long long q = issued > S ? issued - S : 0; q < issued; ++q)
-        warp_wait(&wfull_s[q % S], static_cast<uint32_t>(q / S) & 1u, kWaitLimitNs);
+      ok = __all_sync(kFull, ok);
+      w.skip(steps);
     }
   } else if (warp == 1) {
     int buf = 0;
@@ -287,27 +297,30 @@ __global__ void __launch_bounds__(kExpThreads, 1)
       look(n, t.it + step);
       t.resolve(a, units);
       if (!t.valid(a)) continue;
-      RingPlace<S> xs = x;
-      for (int c = 0; ok && c < t.tiles; ++c) {
-        ok = warp_wait(&acc_free_s[buf], acc_phase ^ 1u, limit);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t d = tmem + buf * BN;
-        xs = x;  // every tile of the unit takes the same rows
-        for (int ks = 0; ks < a.ksteps; ++ks) {
-          ok = __all_sync(kFull, (c > 0 || thread_wait(&xfull_s[xs.slot], xs.phase, limit)) &&
-                                     thread_wait(&wfull_s[w.slot], w.phase, limit));
+      any = true;
+      if (elect_one()) {
+        RingPlace<S> xs, at = w;
+        int to = buf;
+        uint32_t to_phase = acc_phase;
+        for (int c = 0; ok && c < t.tiles; ++c) {
+          ok = thread_wait(&acc_free_s[to], to_phase ^ 1u, limit);
           if (!ok) break;
           tc_fence_after();
-          if (c == 0) fence_proxy_async_smem();  // the rows were written by threads
-          const uint32_t xsc = xscales + xs.slot * 1024;
-          const uint32_t wsc = wscales + w.slot * (1024 * Sh::kAtoms);
-          const uint32_t tx = tmem + Sh::kXScales + xs.slot * 8;
-          const uint32_t tw = tmem + Sh::kWScales + w.slot * (8 * Sh::kAtoms);
-          const uint64_t dx = desc_rows128(xbase + xs.slot * Sh::kX);
-          const uint64_t dw = desc_rows128(wbase + w.slot * Sh::kW);
-          const int parts = (a.K - 256 * ks + 63) >> 6;
-          if (elect_one()) {
+          const uint32_t d = tmem + to * BN;
+          xs = x;  // every tile of the unit takes the same rows
+          for (int ks = 0; ks < a.ksteps; ++ks) {
+            ok = (c > 0 || thread_wait(&xfull_s[xs.slot], xs.phase, limit)) &&
+                 thread_wait(&wfull_s[at.slot], at.phase, limit);
+            if (!ok) break;
+            tc_fence_after();
+            if (c == 0) fence_proxy_async_smem();  // the rows were written by threads
+            const uint32_t xsc = xscales + xs.slot * 1024;
+            const uint32_t wsc = wscales + at.slot * (1024 * Sh::kAtoms);
+            const uint32_t tx = tmem + Sh::kXScales + xs.slot * 8;
+            const uint32_t tw = tmem + Sh::kWScales + at.slot * (8 * Sh::kAtoms);
+            const uint64_t dx = desc_rows128(xbase + xs.slot * Sh::kX);
+            const uint64_t dw = desc_rows128(wbase + at.slot * Sh::kW);
+            const int parts = (a.K - 256 * ks + 63) >> 6;
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
               if (c == 0) tc_copy_scales(tx + 4 * g, desc_scales(xsc + 512 * g));
@@ -322,19 +335,21 @@ __global__ void __launch_bounds__(kExpThreads, 1)
                 // 32 bytes further along the swizzled rows: 2 units of 16
                 tc_mma_mxf4(d, dx + 2 * q, dw + 2 * q, mxf4_word(kExpRows, BN, (q & 1) * 2),
                             tx + 4 * (q >> 1), tw + 4 * Sh::kAtoms * (q >> 1), ks > 0 || q > 0);
-            tc_commit(&wfree_s[w.slot]);
+            tc_commit(&wfree_s[at.slot]);
             if (c + 1 == t.tiles) tc_commit(&xfree_s[xs.slot]);
-            if (ks + 1 == a.ksteps) tc_commit(&acc_full_s[buf]);
+            if (ks + 1 == a.ksteps) tc_commit(&acc_full_s[to]);
+            xs.advance();
+            at.advance();
           }
-          __syncwarp();
-          any = true;
-          xs.advance();
-          w.advance();
+          to ^= 1;
+          if (to == 0) to_phase ^= 1u;
         }
-        buf ^= 1;
-        if (buf == 0) acc_phase ^= 1u;
       }
-      x = xs;
+      ok = __all_sync(kFull, ok);
+      x.skip(a.ksteps);
+      w.skip(t.tiles * a.ksteps);
+      acc_phase ^= static_cast<uint32_t>(buf + t.tiles) >> 1 & 1u;
+      buf = (buf + t.tiles) & 1;
     }
     // nothing of the tensor core may be in flight when tensor memory is given back
     if (any) {
@@ -444,8 +459,8 @@ __global__ void __launch_bounds__(kExpThreads, 1)
       }
       for (int ks = 0; ks < a.ksteps; ++ks) {
         if (now == turn) {
-          ok = warp_wait(&xfree_s[x.slot], x.phase ^ 1u, limit);
-          if (!ok) break;
+          ok = thread_wait(&xfree_s[x.slot], x.phase ^ 1u, limit);
+          if (!ok) break;  // this lane; the others follow below
           const uint32_t dst = x.slot * Sh::kX;
           // (columns past K keep what was there too: they meet weights that read as zero)
           const unsigned live = ks * kStepBytes + 16 * chunk < a.K / 2 ? has : 0u;
@@ -465,6 +480,7 @@ __global__ void __launch_bounds__(kExpThreads, 1)
         if (++now == turns) now = 0;
         x.advance();
       }
+      ok = __all_sync(kFull, ok);
     }
     copy_wait_all();
   } else if (warp >= 12) {
@@ -482,8 +498,8 @@ __global__ void __launch_bounds__(kExpThreads, 1)
     uint2 cur[kR], nx[kR];
     auto hand_on = [&] {
       if (!have) return;
-      ok = warp_wait(&wfree_s[had.slot], had.phase ^ 1u, limit);
-      if (!ok) return;
+      // (a lane whose wait gave up goes along, without waiting again, until the tile ends)
+      ok = ok && thread_wait(&wfree_s[had.slot], had.phase ^ 1u, limit);
       const uint32_t dst = wscales + had.slot * (1024 * Sh::kAtoms) + 16 * lane;
       const uint32_t keep0 = have_last ? tail0 : ~0u, keep1 = have_last ? tail1 : ~0u;
       uint32_t w0[kWords], w1[kWords];
@@ -492,15 +508,17 @@ __global__ void __launch_bounds__(kExpThreads, 1)
         w0[r] = r < kR ? cur[r < kR ? r : 0].x & keep0 : 0u;
         w1[r] = r < kR ? cur[r < kR ? r : 0].y & keep1 : 0u;
       }
+      if (ok) {
 #pragma unroll
-      for (int q = 0; q < Sh::kAtoms; ++q) {
-        store_shared(dst + 512 * q, w0[4 * q], w0[4 * q + 1], w0[4 * q + 2], w0[4 * q + 3]);
-        store_shared(dst + 512 * (Sh::kAtoms + q), w1[4 * q], w1[4 * q + 1], w1[4 * q + 2],
-                     w1[4 * q + 3]);
+        for (int q = 0; q < Sh::kAtoms; ++q) {
+          store_shared(dst + 512 * q, w0[4 * q], w0[4 * q + 1], w0[4 * q + 2], w0[4 * q + 3]);
+          store_shared(dst + 512 * (Sh::kAtoms + q), w1[4 * q], w1[4 * q + 1], w1[4 * q + 2],
+                       w1[4 * q + 3]);
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&wfull_s[had.slot]);
+      if (ok && lane == 0) mbar_arrive(&wfull_s[had.slot]);
     };
     for (; ok && t.it < units; t = n) {
       look(n, t.it + step);
@@ -518,7 +536,6 @@ __global__ void __launch_bounds__(kExpThreads, 1)
                 nx[r] = load_scales(p + static_cast<size_t>(32 * r) * a.scols, ks, a);
             }
             hand_on();
-            if (!ok) break;
 #pragma unroll
             for (int r = 0; r < kR; ++r) cur[r] = nx[r];
             had = w;
@@ -527,9 +544,11 @@ __global__ void __launch_bounds__(kExpThreads, 1)
           }
           w.advance();
         }
+        ok = __all_sync(kFull, ok);
       }
     }
     if (ok) hand_on();
+    ok = __all_sync(kFull, ok);
   }
   if (!ok && lane == 0) atomicOr(a.status, MOE_RS_DEVICE_WAIT_TIMEOUT);
   tc_fence_before();
