@@ -68,13 +68,13 @@ struct ExpertsArgs {
   int nchunk;       // units along the outputs
   int ksteps;       // steps of 256 columns
   int wide_scales;  // the weights' scale rows start on 8 bytes
-  int wide_out;     // output rows start on 32 bytes
 };
 
 constexpr int kExpThreads = 512;  // warps 2 and 3 are idle: a warp reads the lanes of its number mod 4
 constexpr int kExpRows = 128;     // lanes of a tile: rows of a block
 constexpr int kStepBytes = 128;   // bytes of a row per step
 constexpr int kTmemCols = 512;
+constexpr int kStoreBytes = 2048;  // of a storing warp: 64 bytes of 32 rows
 
 // Slots of both rings and the places of everything, for tiles of BN outputs.
 template <int BN>
@@ -85,7 +85,8 @@ struct ExpertsShape {
   static constexpr int kW = BN * kStepBytes;
   static constexpr int kWSlot = kW + 2 * 512 * kAtoms;
   static constexpr int kSlots = BN == 96 ? 7 : (BN == 128 ? 6 : 5);  // what fits in 227 KB
-  static constexpr size_t kSmem = static_cast<size_t>(kSlots) * (kXSlot + kWSlot) + 1024;
+  static constexpr size_t kSmem =
+      static_cast<size_t>(kSlots) * (kXSlot + kWSlot) + 4 * kStoreBytes + 1024;
   // tensor memory: two accumulators, then the scales of each slot
   static constexpr int kXScales = 2 * BN;
   static constexpr int kWScales = kXScales + 8 * kSlots;
@@ -204,6 +205,7 @@ __global__ void __launch_bounds__(kExpThreads, 1)
   // the operands' tiles first: each starts on 1024 bytes
   const uint32_t xbase = base, wbase = base + S * Sh::kX;
   const uint32_t xscales = wbase + S * Sh::kW, wscales = xscales + S * 1024;
+  const uint32_t stores = wscales + S * 1024 * Sh::kAtoms;
   const unsigned long long limit = a.wait_limit_ns;
   const int copiers = (a.span + 31) / 32;  // warps that hold a window's rows: 1, 2 or 4
   pdl_trigger();
@@ -369,14 +371,22 @@ __global__ void __launch_bounds__(kExpThreads, 1)
       const bool used = 32 * (warp & 3) < t.rows;
       const bool put = my_row < t.rows && r >= 0 && r < a.routes;
       const float by = (a.sw != nullptr && put) ? __ldg(a.sw + t.p0 + my_row) : 1.0f;
+      int line[4];  // routes of the rows that this lane stores parts of
+#pragma unroll
+      for (int i = 0; i < 4; ++i) line[i] = __shfl_sync(kFull, put ? r : -1, 8 * i + (lane >> 2));
       for (int tile = 0; tile < t.tiles; ++tile) {
         ok = warp_wait(&acc_full_s[buf], acc_phase, limit);
         if (!ok) break;
         if (used) {
           tc_fence_after();
-          const uint32_t src = tmem + buf * BN + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+          const uint32_t src = tmem + buf * BN + (static_cast<uint32_t>(32 * (warp - 4)) << 16);
           const int n0 = t.n0 + tile * BN, left = a.N - n0;  // left: a multiple of 8
-          Out* out = static_cast<Out*>(a.out) + (put ? static_cast<size_t>(r) * a.N : 0) + n0;
+          // A lane holds a row; 64 bytes of each row go through shared memory so that four lanes
+          // store them side by side.  (A row a lane, 32 bytes at a time, each store touched 32
+          // lines: 411 us at T = 8192, 384 -> 3584, 204 without the stores.)
+          constexpr int kCols = 64 / sizeof(Out), kPiece = 16 / sizeof(Out);
+          const uint32_t to = stores + (warp - 4) * kStoreBytes;
+          const uint32_t put_at = to + 64 * lane, swz = (lane >> 1) & 3;
           // the next 32 columns are on their way while these are stored (columns past the
           // outputs are read, as zeros, and not stored)
           uint32_t ahead[2][32];
@@ -397,25 +407,30 @@ __global__ void __launch_bounds__(kExpThreads, 1)
                 v[c] = *reinterpret_cast<const uint32_t*>(&h);
               }
             }
-            constexpr int kPer = 32 / sizeof(Out);  // outputs of 32 bytes
 #pragma unroll
-            for (int c = 0; put && c < 32 / kPer; ++c) {
-              const int at = c0 + kPer * c;
-              const uint32_t* q = v + 8 * c;
-              void* o = out + at;
-              if (a.wide_out && at + kPer <= left) {
-                asm volatile(
-                    "st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(o),
-                    "r"(q[0]), "r"(q[1]), "r"(q[2]), "r"(q[3]), "r"(q[4]), "r"(q[5]), "r"(q[6]),
-                    "r"(q[7])
-                    : "memory");
-              } else {
-                uint4* o4 = static_cast<uint4*>(o);
-                if (at + kPer / 2 <= left) o4[0] = make_uint4(q[0], q[1], q[2], q[3]);
-                if (at + kPer <= left) o4[1] = make_uint4(q[4], q[5], q[6], q[7]);
+            for (int part = 0; part < 32 / kCols; ++part) {
+              const uint32_t* q = v + 16 * part;
+              __syncwarp();  // what was there has been read
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                store_shared(put_at + 16 * (c ^ swz), q[4 * c], q[4 * c + 1], q[4 * c + 2],
+                             q[4 * c + 3]);
+              __syncwarp();
+              const int col = c0 + kCols * part + kPiece * (lane & 3);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int row = 8 * i + (lane >> 2);
+                uint32_t w[4];
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                             : "r"(to + 64 * row + 16 * ((lane & 3) ^ ((row >> 1) & 3)))
+                             : "memory");
+                if (line[i] >= 0 && col < left)
+                  *reinterpret_cast<uint4*>(static_cast<Out*>(a.out) +
+                                            static_cast<size_t>(line[i]) * a.N + n0 + col) =
+                      make_uint4(w[0], w[1], w[2], w[3]);
               }
             }
-            __syncwarp();
           }
           tc_fence_before();
         }
@@ -743,7 +758,6 @@ int moe_experts_mxfp4(const uint8_t* x_codes, const uint8_t* x_scales, int x_per
   a.nchunk = p.nchunk;
   a.ksteps = p.ksteps;
   a.wide_scales = scols % 8 == 0 && aligned(w_scales, 8);
-  a.wide_out = aligned(out, 32) && outs * (f32 ? 4 : 2) % 32 == 0;
   CUtensorMap wmap;
   if (!encode_weights(&wmap, w_codes, cols / 2, outs, E, p.bn)) return MOE_RS_ERR_LAUNCH;
   const int64_t units = (p.group > 1 ? (blocks + p.group - 1) / p.group * p.group
