@@ -10,11 +10,11 @@
 // tensor memory) by BN = 96, 128 or 192 outputs (the N side).  Blocks of more rows are cut;
 // neighbouring blocks of fewer rows that have the same expert share a tile: the list is taken in
 // windows of at most 128 rows and 32 blocks, and a tile is a run of one expert's blocks in a
-// window (block_m = 16, 4024 tokens, 191 experts, 1984 -> 656: 728 -> 177 us).  Rows on the lanes make the result a row per thread, so the
-// outputs leave as 32-byte stores of whole sectors; a block of 16 rows costs the tensor core as
-// much as one of 128, which it has time for: such calls wait for the weights.  A persistent CTA
-// per SM takes units round robin, a unit being one tile, or for short rows several output tiles of
-// one block; neighbours share a block's rows and an expert's weights in L2.
+// window (block_m = 16, 4024 tokens, 191 experts, 1984 -> 656: a quarter of the time).  Rows on the
+// lanes make a unit of few rows the work of few storing warps; a block of 16 rows costs the tensor
+// core as much as one of 128, which it has time for: such calls wait for the weights.  A persistent
+// CTA per SM takes units round robin, a unit being one tile, or for short rows several output tiles
+// of one block; neighbours share a block's rows and an expert's weights in L2.
 //
 // Steps of 256 columns (128 bytes a row) go through two rings of shared-memory slots, one of rows
 // and one of weights; a unit of several tiles keeps its rows' slots until its last tile.  The
@@ -23,23 +23,27 @@
 //   1      copies a step's scales to tensor memory and issues four products of 64 columns; the
 //          tensor core applies the scales and adds into fp32 in tensor memory
 //   4-7    a finished tile from tensor memory to the output rows, while the next one is computed
-//          (two accumulators; eight warps with half the columns each were slower, 484 us against
-//          444 at T = 8192, 384 -> 3584)
+//          (two accumulators; eight warps, four per accumulator, took 204 us where four took 198
+//          at T = 512, 3584 -> 768, and gained 1% at T = 8192, 384 -> 3584)
 //   8-11   the rows, 16 bytes a thread into the same swizzle, and their scales, all copies that
 //          arrive on the slot's barrier themselves; where one warp or two hold the rows, the others
 //          take steps of their own
 //   12-15  the weights' scales, a step a warp in turn
 // Scales go from row-major bytes to the order that tensor memory wants: row r of 128 on lane
 // r % 32, word r / 32 of 4 scales.  (A warp works through a step in 600 to 900 clocks whatever
-// there is to do, so taking turns is what keeps a single token's 14 steps short: 10.6 us before.)
+// there is to do, so taking turns is what keeps a single token's 14 steps short: 10.6 us before, 9.0 so.)
 //
 // What bounds it: an SM takes in at most 38 bytes a clock (measured, tensor copies, thread copies
 // and multicast alike, on one SM and on all), so a step of 128 x 128 costs 890 clocks and its
 // products 260; hence the wider tile, and rows that stay.  Few tokens are bound by HBM, which
-// gives an SM 23 bytes a clock.
+// gives an SM 23 bytes a clock: 198 us at T = 512, 3584 -> 768, 1.32 GB at
+// 6.7 TB/s, 98% of a copy's rate.  Short rows are bound by both ways of an SM's traffic, 311 us at
+// T = 8192, 384 -> 3584, of which the stores alone are 100 (all to a few rows in L2: 80).  Many
+// tokens of few experts are bound by what an SM takes in, 676 us at T = 8192, E = 64.
 //
-// Each task has the list entries of the next unit in flight.  Every wait is bounded; a wait that gives up ends its warp's task with the status bit
-// set, and the CTA leaves once nothing of its own is in flight.
+// Each task has the list entries of the next unit in flight.  Every wait is bounded; a wait that
+// gives up ends its warp's task with the status bit set, and the CTA leaves once nothing of its own
+// is in flight.
 #include <type_traits>
 
 #include <cuda_bf16.h>
@@ -383,7 +387,9 @@ __global__ void __launch_bounds__(kExpThreads, 1)
           const int n0 = t.n0 + tile * BN, left = a.N - n0;  // left: a multiple of 8
           // A lane holds a row; 64 bytes of each row go through shared memory so that four lanes
           // store them side by side.  (A row a lane, 32 bytes at a time, each store touched 32
-          // lines: 411 us at T = 8192, 384 -> 3584, 204 without the stores.)
+          // lines: 411 us at T = 8192, 384 -> 3584, 204 without the stores.  Whole lines, 128 bytes
+          // of 16 rows at a time, were slower than this: 335 against 315.)  The outputs are marked
+          // as the first to leave L2, which the weights want for themselves: 311.
           constexpr int kCols = 64 / sizeof(Out), kPiece = 16 / sizeof(Out);
           const uint32_t to = stores + (warp - 4) * kStoreBytes;
           const uint32_t put_at = to + 64 * lane, swz = (lane >> 1) & 3;
@@ -426,9 +432,9 @@ __global__ void __launch_bounds__(kExpThreads, 1)
                              : "r"(to + 64 * row + 16 * ((lane & 3) ^ ((row >> 1) & 3)))
                              : "memory");
                 if (line[i] >= 0 && col < left)
-                  *reinterpret_cast<uint4*>(static_cast<Out*>(a.out) +
-                                            static_cast<size_t>(line[i]) * a.N + n0 + col) =
-                      make_uint4(w[0], w[1], w[2], w[3]);
+                  __stcs(reinterpret_cast<uint4*>(static_cast<Out*>(a.out) +
+                                                  static_cast<size_t>(line[i]) * a.N + n0 + col),
+                         make_uint4(w[0], w[1], w[2], w[3]));
               }
             }
           }
