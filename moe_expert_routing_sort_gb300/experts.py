@@ -11,7 +11,7 @@ from typing import Optional
 import torch
 
 from .binding import load
-from .marshal import DTYPE_CODE, Entry, cuda_device, need, rows_of
+from .marshal import DTYPE_CODE, Entry, cuda_device, made, need, rows_of
 
 _quantize = Entry("moe_mxfp4_quantize")
 _dequantize = Entry("moe_mxfp4_dequantize")
@@ -35,7 +35,7 @@ class Mxfp4Rows:
     both uint8 on one CUDA device.  Weights of E experts are [E, outs, ...].  The two tensors are
     checked here, once, and cannot be exchanged afterwards."""
 
-    __slots__ = ("_codes", "_scales", "lead", "cols", "device", "_args")
+    __slots__ = ("_codes", "_scales", "lead", "cols", "device")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor):
         self.device = cuda_device(codes, "codes")
@@ -45,11 +45,12 @@ class Mxfp4Rows:
         if tuple(scales.shape) != (*self.lead, _scale_cols(self.cols)):
             raise ValueError(f"scales must be {(*self.lead, _scale_cols(self.cols))} for codes "
                              f"{tuple(codes.shape)}, got {tuple(scales.shape)}")
-        self._args = (need(codes, torch.uint8, 0, self.device, "codes"),
-                      need(scales, torch.uint8, 0, self.device, "scales"))
+        need(codes, torch.uint8, 0, self.device, "codes")
+        need(scales, torch.uint8, 0, self.device, "scales")
 
     codes = property(lambda self: self._codes)
     scales = property(lambda self: self._scales)
+    tensors = property(lambda self: (self._codes, self._scales))
 
     @classmethod
     def allocate(cls, rows, cols: int, device="cuda") -> "Mxfp4Rows":
@@ -82,14 +83,16 @@ def mxfp4_quantize(x, out: Optional[Mxfp4Rows] = None, stream=None) -> Mxfp4Rows
         raise ValueError(f"x must be bfloat16, float16 or float32, got {x.dtype}")
     shape = x.shape
     if out is None:
-        out = Mxfp4Rows.allocate(shape[:-1], shape[-1], device=x.device)
+        out = made(dev, stream, lambda: Mxfp4Rows.allocate(shape[:-1], shape[-1], device=x.device))
     elif out.lead != shape[:-1] or out.cols != shape[-1] or out.device != dev:
         raise ValueError(f"out holds rows of shape {tuple(out.codes.shape)} on cuda:{out.device}, "
                          f"x is {tuple(shape)} on {x.device}")
     if len(shape) != 2:
-        x = x.reshape(-1, shape[-1])
+        given = x
+        x = made(dev, stream, lambda: given.reshape(-1, shape[-1]))  # a copy, if not a view
     rows, cols, stride = rows_of(x, "x")
-    _quantize(dev, stream, x.data_ptr(), code, rows, cols, stride, *out._args)
+    _quantize(dev, stream, x.data_ptr(), code, rows, cols, stride, out._codes.data_ptr(),
+              out._scales.data_ptr())
     return out
 
 
@@ -110,7 +113,8 @@ def mxfp4_dequantize(rows: Mxfp4Rows, dtype=torch.bfloat16, out: Optional[torch.
     """The values of ``rows`` as a tensor [..., cols]; allocates it unless ``out`` is given."""
     dev, cols = rows.device, rows.cols
     if out is None:
-        out = torch.empty((*rows.lead, cols), dtype=dtype, device=rows.codes.device)
+        out = made(dev, stream, lambda: torch.empty((*rows.lead, cols), dtype=dtype,
+                                                    device=rows.codes.device))
     elif out.shape != (*rows.lead, cols) or out.get_device() != dev:
         raise ValueError(f"out is {tuple(out.shape)} on {out.device}, the rows are "
                          f"{(*rows.lead, cols)} on cuda:{dev}")
@@ -118,7 +122,8 @@ def mxfp4_dequantize(rows: Mxfp4Rows, dtype=torch.bfloat16, out: Optional[torch.
     if kind is not torch.bfloat16 and kind is not torch.float32:
         raise ValueError(f"out must be bfloat16 or float32, got {kind}")
     n, _, stride = rows_of(out if out.dim() == 2 else out.view(-1, cols), "out")
-    _dequantize(dev, stream, *rows._args, n, cols, out.data_ptr(), DTYPE_CODE[kind], stride)
+    _dequantize(dev, stream, rows._codes.data_ptr(), rows._scales.data_ptr(), n, cols,
+                out.data_ptr(), DTYPE_CODE[kind], stride)
     return out
 
 
@@ -168,12 +173,14 @@ def experts_mxfp4(x: Mxfp4Rows, w: Mxfp4Rows, T: int, topk: int, block_m: int, s
     if xr != T and xr != T * topk:
         raise ValueError(f"x must have T = {T} or T * topk = {T * topk} rows, got {xr}")
     if out is None:
-        out = torch.zeros(T * topk, outs, dtype=dtype, device=w.codes.device)
+        out = made(dev, stream, lambda: torch.zeros(T * topk, outs, dtype=dtype,
+                                                    device=w.codes.device))
     if workspace is None:
-        workspace = torch.zeros(moe_experts_mxfp4_workspace_bytes(T, E, topk, block_m),
-                                dtype=torch.uint8, device=w.codes.device)
-    xc, xs = x._args
-    _experts(dev, stream, xc, xs, 0 if xr == T else 1, *w._args, T, E, topk, x.cols, outs, block_m,
+        workspace = made(dev, stream, lambda: torch.zeros(
+            moe_experts_mxfp4_workspace_bytes(T, E, topk, block_m), dtype=torch.uint8,
+            device=w.codes.device))
+    _experts(dev, stream, x._codes.data_ptr(), x._scales.data_ptr(), 0 if xr == T else 1,
+             w._codes.data_ptr(), w._scales.data_ptr(), T, E, topk, x.cols, outs, block_m,
              *_list_args(T, E, topk, block_m, outs, dev, sorted_token_ids, sorted_weights,
                          expert_ids, num_tokens_post_pad, out, workspace))
     return out

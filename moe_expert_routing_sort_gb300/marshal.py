@@ -41,6 +41,25 @@ def cuda_device(t: torch.Tensor, name: str) -> int:
     return d
 
 
+def made(device: int, stream, make):
+    """What ``make()`` allocates for a call on ``stream``: made on that stream, so that what fills
+    it, and what had its memory before, is over when the call runs.  The caller's current stream is
+    recorded on it, where it may be used and let go."""
+    if stream is None:
+        return make()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)),
+                                           device=device)
+    current = torch.cuda.current_stream(device)
+    if current == stream:
+        return make()
+    with torch.cuda.stream(stream):
+        got = make()
+    for t in getattr(got, "tensors", (got,)):
+        t.record_stream(current)
+    return got
+
+
 def rows_of(t: torch.Tensor, name: str):
     """(rows, cols, elements between rows) of a matrix whose rows are dense."""
     if t.dim() != 2:

@@ -11,7 +11,7 @@ from typing import Optional
 import torch
 
 from .binding import load
-from .marshal import DTYPE_CODE, Entry, cuda_device, need
+from .marshal import DTYPE_CODE, Entry, cuda_device, made, need
 
 _loss = Entry("moe_balance_loss")
 _backward = Entry("moe_route_backward")
@@ -26,7 +26,7 @@ class BalanceBuffers:
     ``counts`` [n_seq, E] int32, ``mean_probs`` [n_seq, E] float32.  The buffers are the
     container's own and cannot be exchanged."""
 
-    __slots__ = ("_loss", "_counts", "_mean", "_workspace", "_shape", "_args", "_ws")
+    __slots__ = ("_loss", "_counts", "_mean", "_workspace", "_shape")
 
     def __init__(self, T: int, E: int, n_seq: int, device):
         ws = moe_balance_workspace_bytes(T, E, n_seq)
@@ -37,13 +37,12 @@ class BalanceBuffers:
         self._mean = torch.empty(n_seq, E, dtype=torch.float32, device=device)
         self._workspace = torch.empty(ws, dtype=torch.uint8, device=device)
         self._shape = (T, E, n_seq, self._loss.get_device())
-        self._args = (self._loss.data_ptr(), self._counts.data_ptr(), self._mean.data_ptr(),
-                      self._workspace.data_ptr(), ws)
 
     loss = property(lambda self: self._loss)
     counts = property(lambda self: self._counts)
     mean_probs = property(lambda self: self._mean)
     workspace = property(lambda self: self._workspace)
+    tensors = property(lambda self: (self._loss, self._counts, self._mean, self._workspace))
 
     @classmethod
     def allocate(cls, T: int, E: int, n_seq: int = 1, device="cuda") -> "BalanceBuffers":
@@ -91,11 +90,13 @@ def balance_loss(logits, topk_ids, coef: float, softmax: bool = False,
         raise ValueError("topk_ids must be [T, topk]")
     T, E, K, S, dev, pl, pid, po = _router(logits, topk_ids, seq_offsets)
     if out is None:
-        out = BalanceBuffers.allocate(T, E, S, device=logits.device)
+        out = made(dev, stream, lambda: BalanceBuffers.allocate(T, E, S, device=logits.device))
     elif out._shape != (T, E, S, dev):
         raise ValueError(f"out is for (T, E, n_seq, device) {out._shape}, the call is "
                          f"{(T, E, S, dev)}")
-    _loss(dev, stream, pl, pid, po, T, E, K, S, 1 if softmax else 0, coef, *out._args)
+    ws = out._workspace
+    _loss(dev, stream, pl, pid, po, T, E, K, S, 1 if softmax else 0, coef, out._loss.data_ptr(),
+          out._counts.data_ptr(), out._mean.data_ptr(), ws.data_ptr(), ws.numel())
     return out
 
 
@@ -128,7 +129,8 @@ def route_backward(logits, topk_ids, grad_weights=None, routed_scale: float = 1.
                    out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Allocate (unless ``out`` is given) and run moe_route_backward; returns the gradient."""
     if out is None:
-        out = torch.empty(logits.shape, dtype=dtype, device=logits.device)
+        out = made(cuda_device(logits, "logits"), stream,
+                   lambda: torch.empty(logits.shape, dtype=dtype, device=logits.device))
     moe_route_backward(logits, topk_ids, grad_weights, grad_loss, counts, seq_offsets, softmax,
                        routed_scale, coef, out, stream)
     return out

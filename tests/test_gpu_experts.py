@@ -424,3 +424,47 @@ def test_waits_that_give_up_are_reported_and_leave_the_next_call_right(B, cols):
     ws.zero_()
     again = mrs.experts_mxfp4(x, W, T, K, B, *lists, workspace=ws)
     assert torch.equal(again, good) and int(ws[:4].view(torch.int32)) == 0
+
+
+def test_a_call_on_another_stream_makes_its_buffers_there():
+    # the current stream is busy for a while; what the calls allocate must not wait for it, nor be
+    # cleared or filled after the kernels on the other stream have run
+    T, E, K, cols, N, B = 50, 8, 2, 128, 64, 16
+    g = torch.Generator().manual_seed(8)
+    ids = _routes(g, T, E, K, "uniform")
+    x, W = _rows(g, T, cols), _rows(g, E * N, cols)
+    W = mrs.Mxfp4Rows(W.codes.view(E, N, -1), W.scales.view(E, N, -1))
+    m = _sorted(ids, torch.ones(T, K), E, B)
+    lists = (m.sorted_token_ids, m.expert_ids, m.num_tokens_post_pad)
+    want = mrs.experts_mxfp4(x, W, T, K, B, *lists)
+    three = torch.randn(4, 64, 6, generator=g).to(DEV).transpose(1, 2)  # copied to become rows
+    want3 = mrs.mxfp4_quantize(three.contiguous())
+    back3 = mrs.mxfp4_dequantize(want3)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        torch.cuda._sleep(50_000_000)
+        got = mrs.experts_mxfp4(x, W, T, K, B, *lists, stream=stream)
+        got3 = mrs.mxfp4_quantize(three, stream=stream)
+        got_back = mrs.mxfp4_dequantize(got3, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+        assert torch.equal(got3.codes, want3.codes) and torch.equal(got3.scales, want3.scales)
+        assert torch.equal(got_back, back3)
+
+
+def test_rows_whose_memory_was_exchanged():
+    # a caller may offload and bring back the memory behind a tensor that a container holds
+    x = torch.randn(64, 512, device=DEV)
+    q = mrs.mxfp4_quantize(x)
+    want = mrs.mxfp4_dequantize(q)
+    host = q.codes.cpu()
+    size = q.codes.untyped_storage().nbytes()
+    q.codes.untyped_storage().resize_(0)
+    with pytest.raises(mrs.RouteSortError):
+        mrs.mxfp4_dequantize(q)
+    keep = torch.full((size,), 255, dtype=torch.uint8, device=DEV)  # what was there is other data
+    q.codes.untyped_storage().resize_(size)
+    q.codes.copy_(host)
+    assert torch.equal(mrs.mxfp4_dequantize(q), want)
+    assert (keep == 255).all()

@@ -354,3 +354,19 @@ def test_outputs_stay_inside_their_buffers():
         for k, (raw, view) in bufs.items():
             n = view.numel() * view.element_size()
             assert (raw[:1024] == 0x5A).all() and (raw[1024 + n:] == 0x5A).all(), k
+
+
+def test_a_call_on_another_stream_makes_its_buffers_there():
+    logits, ids = _inputs(300, 129, 5)
+    gw = torch.randn(300, 5, device=DEV)
+    want = mrs.balance_loss(logits, ids, 0.1)
+    grad = mrs.route_backward(logits, ids, gw)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        torch.cuda._sleep(50_000_000)
+        got = mrs.balance_loss(logits, ids, 0.1, stream=stream)
+        got_grad = mrs.route_backward(logits, ids, gw, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(got.loss, want.loss) and torch.equal(got.counts, want.counts)
+        assert torch.equal(got_grad, grad)
