@@ -7,7 +7,7 @@
 // (1 without weights) is applied in fp32, and the result is rounded once to the output type.
 //
 // One tile is up to 128 rows of one expert (the M side of the tensor-core product, 128 lanes of
-// tensor memory) by BN = 96, 128 or 192 outputs (the N side).  Blocks of more rows are cut;
+// tensor memory) by BN = 96, 128, 192 or 256 outputs (the N side).  Blocks of more rows are cut;
 // neighbouring blocks of fewer rows that have the same expert share a tile: the list is taken in
 // windows of at most 128 rows and 32 blocks, and a tile is a run of one expert's blocks in a
 // window (block_m = 16, 4024 tokens, 191 experts, 1984 -> 656: a quarter of the time).  Rows on the
@@ -23,7 +23,7 @@
 //   1      copies a step's scales to tensor memory and issues four products of 64 columns; the
 //          tensor core applies the scales and adds into fp32 in tensor memory
 //   4-7    a finished tile from tensor memory to the output rows, while the next one is computed
-//          (two accumulators; eight warps, four per accumulator, took 204 us where four took 198
+//          (two accumulators, one of 256 outputs; eight warps, four per accumulator, took 204 us where four took 198
 //          at T = 512, 3584 -> 768, and gained 1% at T = 8192, 384 -> 3584)
 //   8-11   the rows, 16 bytes a thread into the same swizzle, and their scales, all copies that
 //          arrive on the slot's barrier themselves; where one warp or two hold the rows, the others
@@ -39,7 +39,8 @@
 // gives an SM 23 bytes a clock: 198 us at T = 512, 3584 -> 768, 1.32 GB at
 // 6.7 TB/s, 98% of a copy's rate.  Short rows are bound by both ways of an SM's traffic, 311 us at
 // T = 8192, 384 -> 3584, of which the stores alone are 100 (all to a few rows in L2: 80).  Many
-// tokens of few experts are bound by what an SM takes in, 676 us at T = 8192, E = 64.
+// tokens of few experts are bound by what an SM takes in: T = 8192, E = 64, 7168 -> 2048 takes
+// 578 us, and 674 with tiles of 192 outputs.
 //
 // Each task has the list entries of the next unit in flight.  Every wait is bounded; a wait that
 // gives up ends its warp's task with the status bit set, and the CTA leaves once nothing of its own
@@ -88,11 +89,12 @@ struct ExpertsShape {
   static constexpr int kXSlot = kX + 2 * 512;                 // and their scales
   static constexpr int kW = BN * kStepBytes;
   static constexpr int kWSlot = kW + 2 * 512 * kAtoms;
-  static constexpr int kSlots = BN == 96 ? 7 : (BN == 128 ? 6 : 5);  // what fits in 227 KB
+  static constexpr int kSlots = BN == 96 ? 7 : (BN == 128 ? 6 : (BN == 192 ? 5 : 4));  // 227 KB
   static constexpr size_t kSmem =
       static_cast<size_t>(kSlots) * (kXSlot + kWSlot) + 4 * kStoreBytes + 1024;
-  // tensor memory: two accumulators, then the scales of each slot
-  static constexpr int kXScales = 2 * BN;
+  // tensor memory: the accumulators, then the scales of each slot
+  static constexpr int kAcc = BN == 256 ? 1 : 2;
+  static constexpr int kXScales = kAcc * BN;
   static constexpr int kWScales = kXScales + 8 * kSlots;
   static_assert(kWScales + 8 * kAtoms * kSlots <= kTmemCols, "");
 };
@@ -347,15 +349,17 @@ __global__ void __launch_bounds__(kExpThreads, 1)
             xs.advance();
             at.advance();
           }
-          to ^= 1;
-          if (to == 0) to_phase ^= 1u;
+          if (++to == Sh::kAcc) {
+            to = 0;
+            to_phase ^= 1u;
+          }
         }
       }
       ok = __all_sync(kFull, ok);
       x.skip(a.ksteps);
       w.skip(t.tiles * a.ksteps);
-      acc_phase ^= static_cast<uint32_t>(buf + t.tiles) >> 1 & 1u;
-      buf = (buf + t.tiles) & 1;
+      acc_phase ^= static_cast<uint32_t>((buf + t.tiles) / Sh::kAcc) & 1u;
+      buf = (buf + t.tiles) % Sh::kAcc;
     }
     // nothing of the tensor core may be in flight when tensor memory is given back
     if (any) {
@@ -442,8 +446,10 @@ __global__ void __launch_bounds__(kExpThreads, 1)
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&acc_free_s[buf]);
-        buf ^= 1;
-        if (buf == 0) acc_phase ^= 1u;
+        if (++buf == Sh::kAcc) {
+          buf = 0;
+          acc_phase ^= 1u;
+        }
       }
     }
   } else if (warp >= 8 && warp < 12) {
@@ -630,7 +636,9 @@ cudaError_t launch_experts(const CUtensorMap& wmap, const ExpertsArgs& a, int gr
 // more than one (more routes than a block holds).  `tiles` counts row tiles at most: parts of
 // blocks, or with windows one per 128 routes and expert.  An SM's time for a tile goes by the bytes
 // it takes in, its rows and BN weights, so the width is the one with the smallest product of
-// rounds and bytes.  Rows of at most half a ring's steps stay for several tiles once every SM has
+// rounds and bytes.  Tiles of 256 outputs leave room for one accumulator, so that a tile is stored
+// before the next one's products; its copies cover that if the ring holds less than half a row.
+// Rows of at most half a ring's steps stay for several tiles once every SM has
 // work for eight rounds without that.
 struct ExpertsPlan {
   int group, span, subs;
@@ -654,12 +662,14 @@ ExpertsPlan experts_plan(int64_t blocks, int64_t routes, int E, int B, int outs,
   p.bn = 128;
   if (cost(192) < cost(p.bn)) p.bn = 192;
   if (cost(96) < cost(p.bn)) p.bn = 96;
-  p.ntile = (outs + p.bn - 1) / p.bn;
   p.ksteps = (cols + 255) / 256;
+  if (p.ksteps >= 2 * ExpertsShape<256>::kSlots && cost(256) < cost(p.bn)) p.bn = 256;
+  p.ntile = (outs + p.bn - 1) / p.bn;
   p.chunk = 1;
   const int slots = p.bn == 96    ? ExpertsShape<96>::kSlots
                     : p.bn == 128 ? ExpertsShape<128>::kSlots
-                                  : ExpertsShape<192>::kSlots;
+                  : p.bn == 192 ? ExpertsShape<192>::kSlots
+                                : ExpertsShape<256>::kSlots;
   if (2 * p.ksteps <= slots) {
     const int64_t each = rowtiles * p.ntile / (8 * static_cast<int64_t>(sms));
     p.chunk = each < 1 ? 1 : (each > p.ntile ? p.ntile : static_cast<int>(each));
@@ -779,7 +789,8 @@ int moe_experts_mxfp4(const uint8_t* x_codes, const uint8_t* x_scales, int x_per
   };
   return launch_status(p.bn == 96    ? go(std::integral_constant<int, 96>{})
                        : p.bn == 128 ? go(std::integral_constant<int, 128>{})
-                                     : go(std::integral_constant<int, 192>{}));
+                       : p.bn == 192 ? go(std::integral_constant<int, 192>{})
+                                     : go(std::integral_constant<int, 256>{}));
 }
 
 }  // extern "C"

@@ -223,6 +223,15 @@ def test_product_row_lengths(cols, B):
     _check_product(21, 5, 2, cols, 128, B)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("B", [16, 128])
+@pytest.mark.parametrize("T,dist", [(1500, "uniform"), (9000, "uniform"), (9000, "one"),
+                                    (3000, "drops")])
+def test_product_of_long_rows_and_many_tokens(T, dist, B, dtype):
+    # one wide accumulator: a tile ends before the next one starts, several times per CTA
+    _check_product(T, 4, 2, 2080, 1000, B, dist, dtype=dtype)
+
+
 @pytest.mark.parametrize("N", [8, 16, 72, 120, 128, 136, 256, 264, 768])
 def test_product_output_widths(N):
     _check_product(19, 4, 2, 192, N, 16)
