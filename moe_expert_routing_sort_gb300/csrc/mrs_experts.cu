@@ -40,7 +40,9 @@
 // 6.7 TB/s, 98% of a copy's rate.  Short rows are bound by both ways of an SM's traffic, 311 us at
 // T = 8192, 384 -> 3584, of which the stores alone are 100 (all to a few rows in L2: 80).  Many
 // tokens of few experts are bound by what an SM takes in: T = 8192, E = 64, 7168 -> 2048 takes
-// 578 us, and 674 with tiles of 192 outputs.
+// 578 us, and 674 with tiles of 192 outputs.  (256 rows by 192 outputs, two products a step on the
+// same weights, take in a fifth less for the same work but leave three slots for rows and twice the
+// outputs to store between tiles: 658 us, 580 without the stores.)
 //
 // Each task has the list entries of the next unit in flight.  Every wait is bounded; a wait that
 // gives up ends its warp's task with the status bit set, and the CTA leaves once nothing of its own
@@ -633,13 +635,14 @@ cudaError_t launch_experts(const CUtensorMap& wmap, const ExpertsArgs& a, int gr
 }
 
 // Tile width and units of a call.  Blocks below 128 rows go in windows where some expert can have
-// more than one (more routes than a block holds).  `tiles` counts row tiles at most: parts of
+// more than one (more routes than a block holds).  `rowtiles` counts row tiles at most: parts of
 // blocks, or with windows one per 128 routes and expert.  An SM's time for a tile goes by the bytes
-// it takes in, its rows and BN weights, so the width is the one with the smallest product of
-// rounds and bytes.  Tiles of 256 outputs leave room for one accumulator, so that a tile is stored
-// before the next one's products; its copies cover that if the ring holds less than half a row.
-// Rows of at most half a ring's steps stay for several tiles once every SM has
-// work for eight rounds without that.
+// it takes in, its rows and BN weights, so the width is the one with the smallest product of rounds
+// and bytes.  Tiles of 256 outputs leave room for one accumulator, so that a tile is stored before
+// the next one's products; the copies of rows that fill the ring cover most of that (T = 8192,
+// E = 64, outs = 2048, us with and without them: 91 71 at 512 columns, 128 144 at 1024, 153 185 at
+// 1536, 189 231 at 2048).  Rows of at most half a ring's steps stay for several tiles once every SM
+// has work for eight rounds without that.
 struct ExpertsPlan {
   int group, span, subs;
   int bn, ntile, chunk, nchunk, ksteps;
@@ -663,13 +666,13 @@ ExpertsPlan experts_plan(int64_t blocks, int64_t routes, int E, int B, int outs,
   if (cost(192) < cost(p.bn)) p.bn = 192;
   if (cost(96) < cost(p.bn)) p.bn = 96;
   p.ksteps = (cols + 255) / 256;
-  if (p.ksteps >= 2 * ExpertsShape<256>::kSlots && cost(256) < cost(p.bn)) p.bn = 256;
+  if (p.ksteps >= ExpertsShape<256>::kSlots && cost(256) < cost(p.bn)) p.bn = 256;
   p.ntile = (outs + p.bn - 1) / p.bn;
   p.chunk = 1;
   const int slots = p.bn == 96    ? ExpertsShape<96>::kSlots
                     : p.bn == 128 ? ExpertsShape<128>::kSlots
-                  : p.bn == 192 ? ExpertsShape<192>::kSlots
-                                : ExpertsShape<256>::kSlots;
+                    : p.bn == 192 ? ExpertsShape<192>::kSlots
+                                  : ExpertsShape<256>::kSlots;
   if (2 * p.ksteps <= slots) {
     const int64_t each = rowtiles * p.ntile / (8 * static_cast<int64_t>(sms));
     p.chunk = each < 1 ? 1 : (each > p.ntile ? p.ntile : static_cast<int>(each));

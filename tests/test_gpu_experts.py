@@ -224,12 +224,14 @@ def test_product_row_lengths(cols, B):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
-@pytest.mark.parametrize("B", [16, 128])
-@pytest.mark.parametrize("T,dist", [(1500, "uniform"), (9000, "uniform"), (9000, "one"),
-                                    (3000, "drops")])
+@pytest.mark.parametrize("B", [8, 16, 128, 256, 1024])
+@pytest.mark.parametrize("T,dist", [(1500, "uniform"), (7000, "uniform"), (9000, "uniform"),
+                                    (9000, "one"), (3000, "drops"), (9100, "drops")])
 def test_product_of_long_rows_and_many_tokens(T, dist, B, dtype):
-    # one wide accumulator: a tile ends before the next one starts, several times per CTA
+    # tiles of 256 outputs fill tensor memory: one ends before the next one starts, several times per
+    # CTA, in windows, in single blocks and in parts of blocks
     _check_product(T, 4, 2, 2080, 1000, B, dist, dtype=dtype)
+    _check_product(T, 4, 2, 1056, 520, B, dist, dtype=dtype)
 
 
 @pytest.mark.parametrize("N", [8, 16, 72, 120, 128, 136, 256, 264, 768])
