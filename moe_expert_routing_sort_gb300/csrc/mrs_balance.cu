@@ -542,7 +542,8 @@ __global__ void __launch_bounds__(kBalThreads, 1)
     mrs_route_backward_kernel(const RouteBackwardArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ float4 xchg_s[kBalWarps][2];
-  const int tid = threadIdx.x, warp = tid >> 5, W = kW > 0 ? kW : a.W, E = a.E, K = a.K, wl = tid & 31;
+  const int tid = threadIdx.x, warp = tid >> 5, wl = tid & 31;
+  const int W = kW > 0 ? kW : a.W, E = a.E, K = a.K;
   const int grp = warp / W, gw = warp - grp * W, groups = groups_of(W);
   const int lanes = 32 * W, lane = 32 * gw + wl;
   float4* xchg = &xchg_s[0][0] + grp * 2 * W;
@@ -696,8 +697,9 @@ __global__ void __launch_bounds__(kBalThreads, 1)
         }
         const int owner = kVec ? (id >> 3) % lanes : id % lanes;
         const float xc = fminf(fmaxf(xk, -kFarLogit), kFarLogit);
-        const float p = kSoftmax ? (xk == -INFINITY ? 0.0f : ex2(fmaf(xc, kLog2e, -top)) * inv)
-                                 : s * inv;
+        // (without the loss there are no sums to take the power against: it could leave the range)
+        const bool none = !dense || xk == -INFINITY;
+        const float p = kSoftmax ? (none ? 0.0f : ex2(fmaf(xc, kLog2e, -top)) * inv) : s * inv;
         d = fmaf(kSoftmax ? p : fmaf(-p, s, p), gk - dot, d);
         __syncwarp();  // the row's own stores come first
         if (valid && (same & lanemask_lt(wl)) == 0u && (owner >> 5) == gw) {

@@ -453,7 +453,7 @@ def test_a_call_on_another_stream_makes_its_buffers_there():
     back3 = mrs.mxfp4_dequantize(want3)
     torch.cuda.synchronize()
     side = torch.cuda.Stream()
-    for stream in (side, side.cuda_stream):
+    for stream in (side, side.cuda_stream, 0):
         torch.cuda._sleep(50_000_000)
         got = mrs.experts_mxfp4(x, W, T, K, B, *lists, stream=stream)
         got3 = mrs.mxfp4_quantize(three, stream=stream)

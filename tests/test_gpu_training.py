@@ -229,6 +229,16 @@ def test_gradient_of_either_term(softmax, weights, loss):
         assert not out.any()
 
 
+@pytest.mark.parametrize("weights,loss", [(True, False), (False, True), (True, True)])
+@pytest.mark.parametrize("softmax,shift", [(True, 200.0), (True, -200.0), (True, 5000.0),
+                                           (False, 60.0), (False, -60.0)])
+def test_gradient_far_from_zero(softmax, shift, weights, loss):
+    # e^200 is no fp32 number; a softmax only knows differences, and e^-60 is one
+    logits, ids = _inputs(200, 129, 5)
+    logits = (logits.float() + shift).bfloat16()
+    _check_grad(logits, ids, None, softmax, torch.float32, weights, loss)
+
+
 @pytest.mark.parametrize("softmax", [False, True])
 @pytest.mark.parametrize("T,off", [
     (300, [0, 1, 2, 3, 300]), (300, [5, 17, 17, 200, 280]), (300, [0, 0, 0, 299, 300]),
@@ -363,7 +373,7 @@ def test_a_call_on_another_stream_makes_its_buffers_there():
     grad = mrs.route_backward(logits, ids, gw)
     torch.cuda.synchronize()
     side = torch.cuda.Stream()
-    for stream in (side, side.cuda_stream):
+    for stream in (side, side.cuda_stream, 0):
         torch.cuda._sleep(50_000_000)
         got = mrs.balance_loss(logits, ids, 0.1, stream=stream)
         got_grad = mrs.route_backward(logits, ids, gw, stream=stream)
