@@ -81,7 +81,6 @@ constexpr int kExpThreads = 512;  // warps 2 and 3 are idle: a warp reads the la
 constexpr int kExpRows = 128;     // lanes of a tile: rows of a block
 constexpr int kStepBytes = 128;   // bytes of a row per step
 constexpr int kTmemCols = 512;
-constexpr int kStoreBytes = 2048;  // of a storing warp: 64 bytes of 32 rows
 
 // Slots of both rings and the places of everything, for tiles of BN outputs.
 template <int BN>
@@ -91,9 +90,13 @@ struct ExpertsShape {
   static constexpr int kXSlot = kX + 2 * 512;                 // and their scales
   static constexpr int kW = BN * kStepBytes;
   static constexpr int kWSlot = kW + 2 * 512 * kAtoms;
-  static constexpr int kSlots = BN == 96 ? 7 : (BN == 128 ? 6 : (BN == 192 ? 5 : 4));  // 227 KB
+  // what fits in 227 KB (five slots of 192 would, and take 311 us for T = 8192, 384 -> 3584, where
+  // four take 297)
+  static constexpr int kSlots = BN == 96 ? 7 : (BN == 128 ? 6 : 4);
+  static constexpr int kStoreBytes = 32 * (BN == 96 ? 64 : 128);  // of a storing warp
   static constexpr size_t kSmem =
       static_cast<size_t>(kSlots) * (kXSlot + kWSlot) + 4 * kStoreBytes + 1024;
+  static_assert(kSmem + 512 <= 227 * 1024, "");
   // tensor memory: the accumulators, then the scales of each slot
   static constexpr int kAcc = BN == 256 ? 1 : 2;
   static constexpr int kXScales = kAcc * BN;
@@ -381,9 +384,13 @@ __global__ void __launch_bounds__(kExpThreads, 1)
       const bool used = 32 * (warp & 3) < t.rows;
       const bool put = my_row < t.rows && r >= 0 && r < a.routes;
       const float by = (a.sw != nullptr && put) ? __ldg(a.sw + t.p0 + my_row) : 1.0f;
-      int line[4];  // routes of the rows that this lane stores parts of
+      // 64 or 128 bytes of a row are stored side by side, 16 by each of kLanes lanes
+      constexpr int kLine = BN > 96 && sizeof(Out) == 2 ? 128 : 64, kLanes = kLine / 16;
+      const int piece = lane % kLanes;
+      int line[kLanes];  // routes of the rows that this lane stores parts of
 #pragma unroll
-      for (int i = 0; i < 4; ++i) line[i] = __shfl_sync(kFull, put ? r : -1, 8 * i + (lane >> 2));
+      for (int i = 0; i < kLanes; ++i)
+        line[i] = __shfl_sync(kFull, put ? r : -1, 32 / kLanes * i + lane / kLanes);
       for (int tile = 0; tile < t.tiles; ++tile) {
         ok = warp_wait(&acc_full_s[buf], acc_phase, limit);
         if (!ok) break;
@@ -391,14 +398,16 @@ __global__ void __launch_bounds__(kExpThreads, 1)
           tc_fence_after();
           const uint32_t src = tmem + buf * BN + (static_cast<uint32_t>(32 * (warp - 4)) << 16);
           const int n0 = t.n0 + tile * BN, left = a.N - n0;  // left: a multiple of 8
-          // A lane holds a row; 64 bytes of each row go through shared memory so that four lanes
-          // store them side by side.  (A row a lane, 32 bytes at a time, each store touched 32
-          // lines: 411 us at T = 8192, 384 -> 3584, 204 without the stores.  Whole lines, 128 bytes
-          // of 16 rows at a time, were slower than this: 335 against 315.)  The outputs are marked
-          // as the first to leave L2, which the weights want for themselves: 311.
+          // A lane holds a row; a line's bytes of each row go through shared memory so that
+          // neighbouring lanes store them side by side.  (T = 8192, 384 -> 3584, us: 411 where a
+          // lane stored 32 bytes of its row, 297 with 64 bytes a row, 287 with 128; one token
+          // and 32-bit outputs are faster with 64.)  The outputs are marked as the first to leave
+          // L2, which the weights want for themselves (1%).
           constexpr int kCols = 64 / sizeof(Out), kPiece = 16 / sizeof(Out);
-          const uint32_t to = stores + (warp - 4) * kStoreBytes;
-          const uint32_t put_at = to + 64 * lane, swz = (lane >> 1) & 3;
+          const uint32_t to = stores + (warp - 4) * Sh::kStoreBytes;
+          auto place = [&](int row, int p) {  // 16 bytes, spread over the banks
+            return to + kLine * row + 16 * (p ^ (kLine == 128 ? row & 7 : (row >> 1) & 3));
+          };
           // the next 32 columns are on their way while these are stored (columns past the
           // outputs are read, as zeros, and not stored)
           uint32_t ahead[2][32];
@@ -419,25 +428,28 @@ __global__ void __launch_bounds__(kExpThreads, 1)
                 v[c] = *reinterpret_cast<const uint32_t*>(&h);
               }
             }
+            // pieces of the line that are there already
+            const int had = kLine == 128 ? (c0 & 32) / 8 : 0;
 #pragma unroll
-            for (int part = 0; part < 32 / kCols; ++part) {
+            for (int part = 0; part < (kLine == 128 ? 1 : 32 / kCols); ++part) {
               const uint32_t* q = v + 16 * part;
-              __syncwarp();  // what was there has been read
+              if (had == 0) __syncwarp();  // what was there has been read
 #pragma unroll
               for (int c = 0; c < 4; ++c)
-                store_shared(put_at + 16 * (c ^ swz), q[4 * c], q[4 * c + 1], q[4 * c + 2],
+                store_shared(place(lane, had + c), q[4 * c], q[4 * c + 1], q[4 * c + 2],
                              q[4 * c + 3]);
+              if (had + 4 < kLanes && c0 + 32 < BN) continue;  // the line is not full
               __syncwarp();
-              const int col = c0 + kCols * part + kPiece * (lane & 3);
+              const int col = c0 - 8 * had + kCols * part + kPiece * piece;
+              const bool mine = col < left && piece < had + 4;
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int row = 8 * i + (lane >> 2);
+              for (int i = 0; i < kLanes; ++i) {
                 uint32_t w[4];
                 asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                              : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                             : "r"(to + 64 * row + 16 * ((lane & 3) ^ ((row >> 1) & 3)))
+                             : "r"(place(32 / kLanes * i + lane / kLanes, piece))
                              : "memory");
-                if (line[i] >= 0 && col < left)
+                if (line[i] >= 0 && mine)
                   __stcs(reinterpret_cast<uint4*>(static_cast<Out*>(a.out) +
                                                   static_cast<size_t>(line[i]) * a.N + n0 + col),
                          make_uint4(w[0], w[1], w[2], w[3]));
