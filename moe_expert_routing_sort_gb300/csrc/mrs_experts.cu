@@ -23,24 +23,24 @@
 //   1      copies a step's scales to tensor memory and issues four products of 64 columns; the
 //          tensor core applies the scales and adds into fp32 in tensor memory
 //   4-7    a finished tile from tensor memory to the output rows, while the next one is computed
-//          (two accumulators, one of 256 outputs; eight warps, four per accumulator, took 204 us where four took 198
-//          at T = 512, 3584 -> 768, and gained 1% at T = 8192, 384 -> 3584)
+//          (two accumulators, one of 256 outputs; eight warps, four per accumulator, took 204 us
+//          where four took 198 at T = 512, 3584 -> 768)
 //   8-11   the rows, 16 bytes a thread into the same swizzle, and their scales, all copies that
 //          arrive on the slot's barrier themselves; where one warp or two hold the rows, the others
 //          take steps of their own
 //   12-15  the weights' scales, a step a warp in turn
 // Scales go from row-major bytes to the order that tensor memory wants: row r of 128 on lane
 // r % 32, word r / 32 of 4 scales.  (A warp works through a step in 600 to 900 clocks whatever
-// there is to do, so taking turns is what keeps a single token's 14 steps short: 10.6 us before, 9.0 so.)
+// there is to do, so taking turns is what keeps a single token's 14 steps short: 10.6 us before,
+// 9.1 so.)
 //
 // What bounds it: an SM takes in at most 38 bytes a clock (measured, tensor copies, thread copies
 // and multicast alike, on one SM and on all), so a step of 128 x 128 costs 890 clocks and its
 // products 260; hence the wider tile, and rows that stay.  Few tokens are bound by HBM, which
-// gives an SM 23 bytes a clock: 198 us at T = 512, 3584 -> 768, 1.32 GB at
-// 6.7 TB/s, 98% of a copy's rate.  Short rows are bound by both ways of an SM's traffic, 311 us at
-// T = 8192, 384 -> 3584, of which the stores alone are 100 (all to a few rows in L2: 80).  Many
-// tokens of few experts are bound by what an SM takes in: T = 8192, E = 64, 7168 -> 2048 takes
-// 578 us, and 674 with tiles of 192 outputs.  (256 rows by 192 outputs, two products a step on the
+// gives an SM 23 bytes a clock: 202 us at T = 512, 3584 -> 768, 1.32 GB at 6.5 TB/s.  Short rows are
+// bound by both ways of an SM's traffic, 287 us at T = 8192, 384 -> 3584, 215 without the stores.
+// Many tokens of few experts are bound by what an SM takes in: T = 8192, E = 64, 7168 -> 2048 takes
+// 571 us, and 674 with tiles of 192 outputs.  (256 rows by 192 outputs, two products a step on the
 // same weights, take in a fifth less for the same work but leave three slots for rows and twice the
 // outputs to store between tiles: 658 us, 580 without the stores.)
 //
@@ -650,11 +650,11 @@ cudaError_t launch_experts(const CUtensorMap& wmap, const ExpertsArgs& a, int gr
 // more than one (more routes than a block holds).  `rowtiles` counts row tiles at most: parts of
 // blocks, or with windows one per 128 routes and expert.  An SM's time for a tile goes by the bytes
 // it takes in, its rows and BN weights, so the width is the one with the smallest product of rounds
-// and bytes.  Tiles of 256 outputs leave room for one accumulator, so that a tile is stored before
-// the next one's products; the copies of rows that fill the ring cover most of that (T = 8192,
-// E = 64, outs = 2048, us with and without them: 91 71 at 512 columns, 128 144 at 1024, 153 185 at
-// 1536, 189 231 at 2048).  Rows of at most half a ring's steps stay for several tiles once every SM
-// has work for eight rounds without that.
+// and bytes.  Rows of at most half a ring's steps stay for several tiles once every SM has work for
+// eight rounds without that.  Tiles of 256 outputs leave room for one accumulator, so that a tile is
+// stored before the next one's products; they are for rows that do not stay, whose copies cover
+// most of that (T = 8192, E = 64, outs = 2048, us with and without them: 83 63 at 512 columns,
+// 101 119 at 768, 118 140 at 1024, 182 223 at 2048).
 struct ExpertsPlan {
   int group, span, subs;
   int bn, ntile, chunk, nchunk, ksteps;
@@ -678,7 +678,7 @@ ExpertsPlan experts_plan(int64_t blocks, int64_t routes, int E, int B, int outs,
   if (cost(192) < cost(p.bn)) p.bn = 192;
   if (cost(96) < cost(p.bn)) p.bn = 96;
   p.ksteps = (cols + 255) / 256;
-  if (p.ksteps >= ExpertsShape<256>::kSlots && cost(256) < cost(p.bn)) p.bn = 256;
+  if (2 * p.ksteps > ExpertsShape<256>::kSlots && cost(256) < cost(p.bn)) p.bn = 256;
   p.ntile = (outs + p.bn - 1) / p.bn;
   p.chunk = 1;
   const int slots = p.bn == 96    ? ExpertsShape<96>::kSlots
