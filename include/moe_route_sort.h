@@ -287,7 +287,8 @@ int moe_balance_loss(const void* logits_bf16, const int32_t* topk_ids, const int
  * the gradient (the bias and the groups only steer the selection).
  * grad_weights [T,K] fp32, or NULL: no weights term (topk_ids may then be NULL too).
  * grad_loss [1] fp32 device memory, or NULL: no loss term (counts may then be NULL too);
- * counts [S,E]: as moe_balance_loss wrote them, with the same sequences and coef.  Routes outside
+ * counts [S,E]: as moe_balance_loss wrote them, with the same sequences, coef and topk (the loss
+ * term is divided by topk, with topk_ids or without).  Routes outside
  * [0, E) take no part and their grad_weights are not used; an expert named twice by a token gets
  * the sum.  Tokens outside every sequence have no loss term.  Every element of grad_logits [T,E]
  * is written (16-byte aligned; grad_dtype MOE_RS_BF16 or MOE_RS_FP32, one rounding of an fp32

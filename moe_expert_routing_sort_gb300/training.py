@@ -49,17 +49,20 @@ class BalanceBuffers:
         return cls(T, E, n_seq, device)
 
 
-def _router(logits, topk_ids, seq_offsets):
-    """(T, E, K, S, device, addresses of logits, ids, offsets) of a router's call."""
+def _router(logits, topk_ids, seq_offsets, topk=None):
+    """(T, E, K, S, device, addresses of logits, ids, offsets) of a router's call; K is ``topk``
+    without ids."""
     dev = cuda_device(logits, "logits")
     if logits.dim() != 2:
         raise ValueError("logits must be [T, E]")
     T, E = logits.shape
-    K, pid = 1, 0
+    K, pid = 1 if topk is None else topk, 0
     if topk_ids is not None:
         if topk_ids.dim() != 2 or topk_ids.shape[0] != T:
             raise ValueError("topk_ids must be [T, topk] for logits [T, E]")
         K = topk_ids.shape[1]
+        if topk is not None and topk != K:
+            raise ValueError(f"topk_ids holds {K} routes per token, topk is {topk}")
         pid = need(topk_ids, torch.int32, 0, dev, "topk_ids")
     S, po = 1, 0
     if seq_offsets is not None:
@@ -102,15 +105,18 @@ def balance_loss(logits, topk_ids, coef: float, softmax: bool = False,
 
 def moe_route_backward(logits, topk_ids, grad_weights, grad_loss, counts, seq_offsets,
                        softmax: bool, routed_scale: float, coef: float, grad_logits,
-                       stream=None) -> None:
+                       stream=None, topk: Optional[int] = None) -> None:
     """Gradient to the logits of the routing weights (``grad_weights`` [T, topk], None: no such
     term) and of the balance loss (``grad_loss`` [1] and the ``counts`` of the forward call,
-    None: no such term) into ``grad_logits`` [T, E], bfloat16 or float32."""
-    T, E, K, S, dev, pl, pid, po = _router(logits, topk_ids, seq_offsets)
+    None: no such term) into ``grad_logits`` [T, E], bfloat16 or float32.  The loss term is
+    divided by the routes per token: without ``topk_ids`` (None) it needs ``topk``."""
+    T, E, K, S, dev, pl, pid, po = _router(logits, topk_ids, seq_offsets, topk)
     if grad_weights is not None and topk_ids is None:
         raise ValueError("grad_weights needs topk_ids")
     if grad_loss is not None and counts is None:
         raise ValueError("grad_loss needs the counts of the forward call")
+    if grad_loss is not None and topk_ids is None and topk is None:
+        raise ValueError("grad_loss without topk_ids needs topk, the routes per token")
     dtype = grad_logits.dtype
     if dtype is not torch.bfloat16 and dtype is not torch.float32:
         raise ValueError(f"grad_logits must be bfloat16 or float32, got {dtype}")
@@ -126,11 +132,12 @@ def moe_route_backward(logits, topk_ids, grad_weights, grad_loss, counts, seq_of
 def route_backward(logits, topk_ids, grad_weights=None, routed_scale: float = 1.0,
                    softmax: bool = False, grad_loss=None, counts=None, coef: float = 0.0,
                    seq_offsets=None, dtype=torch.bfloat16,
-                   out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+                   out: Optional[torch.Tensor] = None, stream=None,
+                   topk: Optional[int] = None) -> torch.Tensor:
     """Allocate (unless ``out`` is given) and run moe_route_backward; returns the gradient."""
     if out is None:
         out = made(cuda_device(logits, "logits"), stream,
                    lambda: torch.empty(logits.shape, dtype=dtype, device=logits.device))
     moe_route_backward(logits, topk_ids, grad_weights, grad_loss, counts, seq_offsets, softmax,
-                       routed_scale, coef, out, stream)
+                       routed_scale, coef, out, stream, topk)
     return out
