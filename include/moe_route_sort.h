@@ -334,6 +334,10 @@ int moe_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t ro
  * first use.  Calls that run at the same time may share it. */
 size_t moe_experts_mxfp4_workspace_bytes(int T, int E, int topk, int block_m);
 
+/* The MOE_RS_DEVICE_* bits that moe_experts_mxfp4 calls without a workspace have set on the current
+ * device, into dst[0] (device memory) in stream order; clear != 0: and clears them. */
+int moe_experts_mxfp4_status(int32_t* dst, int clear, cudaStream_t stream);
+
 /* The experts' products over a sorted list of routes (the block-grouped product that the sort
  * metadata exists for), MXFP4 rows times MXFP4 weights.  For every row p < num_tokens_post_pad[0]
  * whose r = sorted_token_ids[p] lies in [0, T*topk), e = expert_ids[p / block_m]:
@@ -348,7 +352,9 @@ size_t moe_experts_mxfp4_workspace_bytes(int T, int E, int topk, int block_m);
  * sorted_token_ids, sorted_weights, expert_ids and num_tokens_post_pad are those of moe_sort or
  * moe_route_sort with the same T, E, topk, block_m; blocks whose expert id lies outside [0, E)
  * are skipped and set MOE_RS_DEVICE_BAD_EXPERT_ID.  A wait on the device that gives up sets
- * MOE_RS_DEVICE_WAIT_TIMEOUT (outputs invalid).  Limits: those of moe_sort; cols as above; outs a
+ * MOE_RS_DEVICE_WAIT_TIMEOUT (outputs invalid).  The bits go to the workspace; with workspace NULL
+ * and workspace_bytes 0 to a word that the library keeps for each device, which all such calls share
+ * (moe_experts_mxfp4_status).  Limits: those of moe_sort; cols as above; outs a
  * multiple of 8 in [8, MOE_RS_MXFP4_MAX_OUTS].  No counterpart in the source pages, whose products
  * belong to another library; the sizes of its 4-bit operator are those this call is tuned on. */
 int moe_experts_mxfp4(const uint8_t* x_codes, const uint8_t* x_scales, int x_per_route,

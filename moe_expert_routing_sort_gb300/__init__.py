@@ -13,6 +13,7 @@ from .binding import (  # noqa: F401
     DEBUG_WARP_GRID_TOKENS,
     DEBUG_WAIT_LIMIT_NS,
     DEVICE_BAD_EXPERT_ID,
+    DEVICE_WAIT_TIMEOUT,
     RouteSortBuffers,
     RouteSortError,
     library_path,
@@ -39,9 +40,12 @@ from .binding import (  # noqa: F401
     strerror,
 )
 from .experts import (  # noqa: F401
+    ExpertsWorkspace,
     Mxfp4Rows,
     experts_mxfp4,
+    experts_status,
     moe_experts_mxfp4,
+    moe_experts_mxfp4_status,
     moe_experts_mxfp4_workspace_bytes,
     moe_mxfp4_dequantize,
     moe_mxfp4_quantize,

@@ -18,6 +18,7 @@ import torch
 from ._build import LIB_PATH
 
 DEVICE_BAD_EXPERT_ID = 0x1
+DEVICE_WAIT_TIMEOUT = 0x2
 
 _lock = threading.Lock()
 _lib = None
@@ -101,6 +102,8 @@ def load() -> ctypes.CDLL:
         lib.moe_experts_mxfp4_workspace_bytes.restype = S
         lib.moe_experts_mxfp4.argtypes = [P, P, I, P, P, I, I, I, I, I, I, P, P, P, P, P, I, P, S, P]
         lib.moe_experts_mxfp4.restype = I
+        lib.moe_experts_mxfp4_status.argtypes = [P, I, P]
+        lib.moe_experts_mxfp4_status.restype = I
         lib.moe_call_packed.argtypes = [ctypes.c_char_p]
         lib.moe_call_packed.restype = I
         _lib = lib

@@ -63,7 +63,7 @@ struct ExpertsArgs {
   const float* sw;  // or null
   const int32_t* eid;
   const int32_t* npp;
-  int32_t* status;
+  int32_t* status;  // or null: g_experts_status
   void* out;
   unsigned long long wait_limit_ns;
   int routes, topk, per_route;
@@ -81,6 +81,17 @@ constexpr int kExpThreads = 512;  // warps 2 and 3 are idle: a warp reads the la
 constexpr int kExpRows = 128;     // lanes of a tile: rows of a block
 constexpr int kStepBytes = 128;   // bytes of a row per step
 constexpr int kTmemCols = 512;
+
+// Bits of the calls on this device that bring no workspace.
+static __device__ int32_t g_experts_status;
+
+__device__ __forceinline__ void report(const ExpertsArgs& a, int bit) {
+  atomicOr(a.status != nullptr ? a.status : &g_experts_status, bit);
+}
+
+__global__ void mrs_experts_status_kernel(int32_t* dst, int clear) {
+  *dst = clear ? atomicExch(&g_experts_status, 0) : *const_cast<volatile int32_t*>(&g_experts_status);
+}
 
 // Slots of both rings and the places of everything, for tiles of BN outputs.
 template <int BN>
@@ -275,7 +286,7 @@ __global__ void __launch_bounds__(kExpThreads, 1)
       look(n, t.it + step);
       t.resolve(a, units);
       if (!t.valid(a)) {
-        if (t.lead && lane == 0) atomicOr(a.status, MOE_RS_DEVICE_BAD_EXPERT_ID);
+        if (t.lead && lane == 0) report(a, MOE_RS_DEVICE_BAD_EXPERT_ID);
         continue;
       }
       const int steps = t.tiles * a.ksteps;
@@ -591,7 +602,7 @@ __global__ void __launch_bounds__(kExpThreads, 1)
     if (ok) hand_on();
     ok = __all_sync(kFull, ok);
   }
-  if (!ok && lane == 0) atomicOr(a.status, MOE_RS_DEVICE_WAIT_TIMEOUT);
+  if (!ok && lane == 0) report(a, MOE_RS_DEVICE_WAIT_TIMEOUT);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -726,7 +737,8 @@ int moe_experts_mxfp4(const uint8_t* x_codes, const uint8_t* x_scales, int x_per
   if (static_cast<int64_t>(T) * topk > INT32_MAX ||
       static_cast<int64_t>(moe_sort_max_padded(T, E, topk, block_m)) > INT32_MAX)
     return MOE_RS_ERR_OVERFLOW;
-  if (!workspace || workspace_bytes < need) return MOE_RS_ERR_WORKSPACE;
+  const bool own_word = !workspace && workspace_bytes == 0;
+  if (!own_word && (!workspace || workspace_bytes < need)) return MOE_RS_ERR_WORKSPACE;
   if (T == 0) return MOE_RS_OK;
   if (!x_codes || !x_scales || !w_codes || !w_scales || !sorted_token_ids || !expert_ids ||
       !num_tokens_post_pad || !out)
@@ -806,6 +818,13 @@ int moe_experts_mxfp4(const uint8_t* x_codes, const uint8_t* x_scales, int x_per
                        : p.bn == 128 ? go(std::integral_constant<int, 128>{})
                        : p.bn == 192 ? go(std::integral_constant<int, 192>{})
                                      : go(std::integral_constant<int, 256>{}));
+}
+
+int moe_experts_mxfp4_status(int32_t* dst, int clear, cudaStream_t stream) {
+  if (!dst) return MOE_RS_ERR_NULL_POINTER;
+  if (!aligned(dst, 4)) return MOE_RS_ERR_MISALIGNED;
+  mrs_experts_status_kernel<<<1, 1, 0, stream>>>(dst, clear != 0);
+  return launch_status(cudaGetLastError());
 }
 
 }  // extern "C"

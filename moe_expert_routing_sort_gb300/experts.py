@@ -10,8 +10,8 @@ from typing import Optional
 
 import torch
 
-from .binding import load
-from .marshal import DTYPE_CODE, Entry, cuda_device, made, need, rows_of
+from .binding import _check, load
+from .marshal import DTYPE_CODE, Entry, cuda_device, made, need, rows_of, stream_handle
 
 _quantize = Entry("moe_mxfp4_quantize")
 _dequantize = Entry("moe_mxfp4_dequantize")
@@ -61,6 +61,51 @@ class Mxfp4Rows:
             raise ValueError(f"cols must be a multiple of 32 in [32, 32768], got {cols}")
         return cls(torch.empty(*lead, cols // 2, dtype=torch.uint8, device=device),
                    torch.empty(*lead, sc, dtype=torch.uint8, device=device))
+
+
+class ExpertsWorkspace:
+    """Workspace of the experts' products for one (T, E, topk, block_m), cleared when made.  It
+    collects the DEVICE_* bits of the calls that it is given to, which may run at the same time."""
+
+    __slots__ = ("tensor",)
+
+    def __init__(self, T: int, E: int, topk: int, block_m: int, device="cuda"):
+        n = moe_experts_mxfp4_workspace_bytes(T, E, topk, block_m)
+        if n == 0:
+            raise ValueError("invalid shape for an experts' workspace")
+        self.tensor = torch.zeros(n, dtype=torch.uint8, device=device)
+
+    @classmethod
+    def allocate(cls, T: int, E: int, topk: int, block_m: int, device="cuda") -> "ExpertsWorkspace":
+        return cls(T, E, topk, block_m, device)
+
+    def status_word(self) -> int:
+        """Device status bits of the completed calls so far (synchronises the device)."""
+        torch.cuda.synchronize(self.tensor.device)
+        return int(self.tensor[:4].view(torch.int32).item())
+
+    def clear(self) -> None:
+        """Clears the bits, in the order of the current stream."""
+        self.tensor.zero_()
+
+
+def moe_experts_mxfp4_status(dst, clear: bool = False, stream=None) -> None:
+    """Copy the status bits of the products without a workspace on dst's device into dst[0] (an
+    int32 CUDA tensor), and clear them if asked, enqueued on the stream."""
+    dev = cuda_device(dst, "dst")
+    address = need(dst, torch.int32, 1, dev, "dst")
+    with torch.cuda.device(dev):
+        rc = load().moe_experts_mxfp4_status(address, 1 if clear else 0, stream_handle(dev, stream))
+    _check(rc, "moe_experts_mxfp4_status")
+
+
+def experts_status(device="cuda", clear: bool = False) -> int:
+    """Device status bits (DEVICE_*; 0: nothing to report) of the products on ``device`` that were
+    given no workspace, since they were last cleared (synchronises the device)."""
+    dst = torch.empty(1, dtype=torch.int32, device=device)
+    torch.cuda.synchronize(dst.device)
+    moe_experts_mxfp4_status(dst, clear, stream=torch.cuda.current_stream(dst.device))
+    return int(dst.item())
 
 
 def moe_mxfp4_quantize(x, codes, scales, stream=None) -> None:
@@ -141,7 +186,8 @@ def _list_args(T, E, topk, block_m, outs, dev, sorted_token_ids, sorted_weights,
             need(expert_ids, torch.int32, P // block_m if block_m > 0 else 0, dev, "expert_ids"),
             need(num_tokens_post_pad, torch.int32, 1, dev, "num_tokens_post_pad"),
             need(out, kind, n * outs, dev, "out"), DTYPE_CODE[kind],
-            need(workspace, torch.uint8, 0, dev, "workspace"), workspace.numel())
+            *((0, 0) if workspace is None else
+              (need(workspace, torch.uint8, 0, dev, "workspace"), workspace.numel())))
 
 
 def moe_experts_mxfp4(x_codes, x_scales, w_codes, w_scales, T, topk, block_m, sorted_token_ids,
@@ -150,7 +196,8 @@ def moe_experts_mxfp4(x_codes, x_scales, w_codes, w_scales, T, topk, block_m, so
     """Products of MXFP4 rows with their experts' MXFP4 weights, into ``out`` [T * topk, outs]
     (bfloat16 or float32; row r is route r).  ``x_codes`` has T rows (one per token) or T * topk
     (one per route); ``w_codes`` is [E, outs, cols / 2]; the sorted list is that of moe_sort or
-    moe_route_sort; ``sorted_weights`` may be None (rows are not scaled)."""
+    moe_route_sort; ``sorted_weights`` may be None (rows are not scaled), ``workspace`` too (the
+    status bits are then those of moe_experts_mxfp4_status)."""
     experts_mxfp4(Mxfp4Rows(x_codes, x_scales), Mxfp4Rows(w_codes, w_scales), T, topk, block_m,
                   sorted_token_ids, expert_ids, num_tokens_post_pad, sorted_weights, out=out,
                   workspace=workspace, stream=stream)
@@ -158,11 +205,15 @@ def moe_experts_mxfp4(x_codes, x_scales, w_codes, w_scales, T, topk, block_m, so
 
 def experts_mxfp4(x: Mxfp4Rows, w: Mxfp4Rows, T: int, topk: int, block_m: int, sorted_token_ids,
                   expert_ids, num_tokens_post_pad, sorted_weights=None, dtype=torch.bfloat16,
-                  out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                  out: Optional[torch.Tensor] = None, workspace=None,
                   stream=None) -> torch.Tensor:
     """Run moe_experts_mxfp4 on rows ``x`` and weights ``w`` [E, outs, ...]; returns ``out``
-    [T * topk, outs].  Without ``out`` the rows of dropped routes are zero (a new buffer is
-    cleared first)."""
+    [T * topk, outs].  Without ``out`` the rows of dropped routes are zero: a new buffer is
+    cleared first, a pass over it that a call with ``out`` saves.
+
+    A bad expert id or a device wait that gave up shows in the status bits alone: of
+    ``workspace`` (an ExpertsWorkspace, or a tensor, see moe_experts_mxfp4_workspace_bytes), or,
+    without one, of ``experts_status(device)``."""
     dev = w.device
     if len(x.lead) != 1 or len(w.lead) != 2 or x.cols != w.cols:
         raise ValueError(f"x must be [rows, cols] and w [E, outs, cols], got {(*x.lead, x.cols)} "
@@ -175,10 +226,8 @@ def experts_mxfp4(x: Mxfp4Rows, w: Mxfp4Rows, T: int, topk: int, block_m: int, s
     if out is None:
         out = made(dev, stream, lambda: torch.zeros(T * topk, outs, dtype=dtype,
                                                     device=w.codes.device))
-    if workspace is None:
-        workspace = made(dev, stream, lambda: torch.zeros(
-            moe_experts_mxfp4_workspace_bytes(T, E, topk, block_m), dtype=torch.uint8,
-            device=w.codes.device))
+    if isinstance(workspace, ExpertsWorkspace):
+        workspace = workspace.tensor
     _experts(dev, stream, x._codes.data_ptr(), x._scales.data_ptr(), 0 if xr == T else 1,
              w._codes.data_ptr(), w._scales.data_ptr(), T, E, topk, x.cols, outs, block_m,
              *_list_args(T, E, topk, block_m, outs, dev, sorted_token_ids, sorted_weights,

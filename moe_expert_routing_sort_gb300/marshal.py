@@ -60,6 +60,13 @@ def made(device: int, stream, make):
     return got
 
 
+def stream_handle(device: int, stream) -> int:
+    """Address of ``stream`` (a stream or an address), or of the device's current one."""
+    if stream is None:
+        return _raw_stream(device)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
 def rows_of(t: torch.Tensor, name: str):
     """(rows, cols, elements between rows) of a matrix whose rows are dense."""
     if t.dim() != 2:
@@ -100,11 +107,7 @@ class Entry:
         fn = self.fn
         if fn is None:
             fn = self.fn = load().moe_call_packed
-        if stream is None:
-            handle = _raw_stream(device)
-        else:
-            handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-        packed = self.pack(self.op, self.count, *args, handle)
+        packed = self.pack(self.op, self.count, *args, stream_handle(device, stream))
         if _current_device() == device:
             rc = fn(packed)
         else:

@@ -36,3 +36,56 @@ def test_the_loss_gradient_does_not_need_the_ids(E, K, softmax):
     want = mrs.route_backward(logits, ids, **term)
     assert torch.equal(mrs.route_backward(logits, None, topk=K, **term), want)
     assert want.any()
+
+
+def _layer(T, E, K, cols, N, B, seed=0):
+    """Rows, weights and the lists of a small layer, every token to different experts."""
+    g = torch.Generator().manual_seed(seed)
+    ids = torch.rand(T, E, generator=g).topk(K, dim=1).indices.int().to(DEV)
+    x = mrs.mxfp4_quantize(torch.randn(T, cols, generator=g).to(DEV))
+    w = mrs.mxfp4_quantize(torch.randn(E, N, cols, generator=g).to(DEV))
+    m = mrs.RouteSortBuffers.allocate(T, E, K, B, device=DEV)
+    mrs.moe_sort(ids, torch.ones(T, K, device=DEV), E, B, m.sorted_token_ids, m.sorted_weights,
+                 m.expert_ids, m.num_tokens_post_pad, m.workspace)
+    return x, w, (m.sorted_token_ids, m.expert_ids, m.num_tokens_post_pad)
+
+
+def test_device_errors_show_on_every_path_of_the_products():
+    T, E, K, cols, N, B = 32, 4, 2, 128, 64, 16
+    x, w, (sid, eid, npp) = _layer(T, E, K, cols, N, B)
+    bad = eid.clone()
+    bad[1] = E + 7
+    own = mrs.ExpertsWorkspace.allocate(T, E, K, B, device=DEV)
+    mrs.experts_status(DEV, clear=True)
+    good = mrs.experts_mxfp4(x, w, T, K, B, sid, eid, npp)
+    assert torch.equal(mrs.experts_mxfp4(x, w, T, K, B, sid, eid, npp, workspace=own), good)
+    assert mrs.experts_status(DEV) == 0 and own.status_word() == 0
+    # with a workspace the bits are that one's alone
+    mrs.experts_mxfp4(x, w, T, K, B, sid, bad, npp, workspace=own)
+    assert own.status_word() == mrs.DEVICE_BAD_EXPERT_ID and mrs.experts_status(DEV) == 0
+    own.clear()
+    assert own.status_word() == 0
+    # without one, of the device: kept over good calls, cleared when asked; any stream, a graph too
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    mrs.experts_mxfp4(x, w, T, K, B, sid, bad, npp, stream=side)
+    mrs.experts_mxfp4(x, w, T, K, B, sid, eid, npp)
+    assert mrs.experts_status(DEV) == mrs.DEVICE_BAD_EXPERT_ID
+    assert mrs.experts_status(DEV, clear=True) == mrs.DEVICE_BAD_EXPERT_ID
+    assert mrs.experts_status(DEV) == 0 and own.status_word() == 0
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = mrs.experts_mxfp4(x, w, T, K, B, sid, bad, npp)
+    assert mrs.experts_status(DEV) == 0
+    graph.replay()
+    assert mrs.experts_status(DEV, clear=True) == mrs.DEVICE_BAD_EXPERT_ID
+    assert not torch.equal(got, good)
+    try:
+        mrs.moe_route_sort_debug_set(mrs.DEBUG_WAIT_LIMIT_NS, 0)
+        mrs.experts_mxfp4(x, w, T, K, B, sid, eid, npp)
+        torch.cuda.synchronize()
+    finally:
+        mrs.moe_route_sort_debug_set(mrs.DEBUG_WAIT_LIMIT_NS, -1)
+    assert mrs.experts_status(DEV, clear=True) == mrs.DEVICE_WAIT_TIMEOUT
+    assert torch.equal(mrs.experts_mxfp4(x, w, T, K, B, sid, eid, npp), good)
+    assert mrs.experts_status(DEV) == 0

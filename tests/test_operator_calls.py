@@ -2,7 +2,8 @@
 import pytest
 import torch
 
-from moe_expert_routing_sort_gb300 import training
+import moe_expert_routing_sort_gb300 as mrs
+from moe_expert_routing_sort_gb300 import _build, training
 
 
 @pytest.fixture
@@ -33,3 +34,29 @@ def test_a_loss_gradient_without_ids_has_its_routes_per_token(backward_args):
         training.route_backward(x, ids, topk=4, **loss)
     training.route_backward(x, None)  # no term at all: zeros, whatever topk
     assert len(backward_args) == 5
+
+
+@pytest.fixture(scope="module")
+def lib():
+    _build.build()
+    return mrs.load()
+
+
+def test_experts_without_a_workspace_take_the_librarys_word(lib):
+    b = 0x7F0000000000
+
+    def call(T, work, work_bytes, codes=0):
+        return lib.moe_experts_mxfp4(codes, b, 0, b, b, T, 4, 2, 64, 16, 16, b, None, b, b, b, 0,
+                                     work, work_bytes, None)
+
+    assert call(8, None, 0) == -1  # past the workspace's check: the codes are missing
+    assert call(0, None, 0) == 0
+    assert call(8, None, 256) == -10 and call(8, b, 0) == -10 and call(8, b, 128) == -10
+    assert lib.moe_experts_mxfp4_status(None, 0, None) == -1
+    assert lib.moe_experts_mxfp4_status(b + 2, 0, None) == -8
+    with pytest.raises(ValueError, match="CUDA"):
+        mrs.moe_experts_mxfp4_status(torch.zeros(1, dtype=torch.int32))
+    with pytest.raises(ValueError, match="invalid shape"):
+        mrs.ExpertsWorkspace.allocate(8, 4, 2, 24, device="cpu")
+    assert mrs.ExpertsWorkspace.allocate(8, 4, 2, 16, device="cpu").tensor.numel() >= 4
+    assert (mrs.DEVICE_BAD_EXPERT_ID, mrs.DEVICE_WAIT_TIMEOUT) == (1, 2)
