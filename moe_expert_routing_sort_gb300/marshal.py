@@ -15,7 +15,8 @@ from .binding import _check, load
 DTYPE_CODE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 _current_device = torch.cuda.current_device
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# (a torch without CUDA has none, nor tensors for a call that wants it)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def need(t: torch.Tensor, dtype, numel: int, device: int, name: str) -> int:

@@ -1,4 +1,8 @@
 """What the bindings of the training and experts operators make of a call's arguments (no GPU)."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -60,3 +64,15 @@ def test_experts_without_a_workspace_take_the_librarys_word(lib):
         mrs.ExpertsWorkspace.allocate(8, 4, 2, 24, device="cpu")
     assert mrs.ExpertsWorkspace.allocate(8, 4, 2, 16, device="cpu").tensor.numel() >= 4
     assert (mrs.DEVICE_BAD_EXPERT_ID, mrs.DEVICE_WAIT_TIMEOUT) == (1, 2)
+
+
+def test_the_package_imports_without_cuda_in_torch():
+    # size queries, host checks and the build ask nothing of torch's CUDA side
+    code = ("import torch\n"
+            "del torch._C._cuda_getCurrentRawStream\n"
+            "import moe_expert_routing_sort_gb300 as mrs\n"
+            "assert mrs.moe_mxfp4_scale_cols(160) == 8\n"
+            "assert mrs.moe_balance_workspace_bytes(8, 64, 1) > 0\n")
+    got = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True,
+                         cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert got.returncode == 0, got.stderr
