@@ -386,16 +386,21 @@ __global__ void __launch_bounds__(kBalThreads, 1) mrs_balance_rows_kernel(const 
   float g0[1] = {0.0f};
   float loss = 0.0f;  // solo: this thread's experts
   int t = t0;
-  for (int i = a.solo ? 0 : seq_behind(a.offsets, a.S, a.T, t0); i < a.S && (t < t1 || a.solo);
-       ++i) {
+  int i = a.solo ? 0 : seq_behind(a.offsets, a.S, a.T, t0);
+  while (i < a.S && (t < t1 || a.solo)) {
     const int lo_i = seq_border(a.offsets, i, a.T), hi_i = seq_border(a.offsets, i + 1, a.T);
     const int lo = max(lo_i, t), hi = min(hi_i, t1);
     if (hi <= lo) {
-      if (a.solo)
+      if (a.solo) {
         for (int e = tid; e < E; e += kBalThreads) {
           a.counts[static_cast<size_t>(i) * E + e] = 0;
           a.mean[static_cast<size_t>(i) * E + e] = 0.0f;
         }
+        ++i;
+      } else {
+        if (lo_i >= t1) break;
+        i = max(i + 1, seq_behind(a.offsets, a.S, a.T, lo));  // past any number of empty ones
+      }
       continue;
     }
     t = hi;
@@ -457,6 +462,7 @@ __global__ void __launch_bounds__(kBalThreads, 1) mrs_balance_rows_kernel(const 
       }
     }
     __syncthreads();
+    ++i;
   }
   if (a.solo) {
     loss = warp_sum(loss);
@@ -564,11 +570,12 @@ __global__ void __launch_bounds__(kBalThreads, 1)
     int hi = t1;
     bool in_seq = false;
     int lo_i = 0, hi_i = 0;
-    while (i < a.S) {
+    for (bool again = false; i < a.S; again = true) {
       lo_i = seq_border(a.offsets, i, a.T);
       hi_i = seq_border(a.offsets, i + 1, a.T);
       if (hi_i > t && hi_i > lo_i) break;
-      ++i;
+      ++i;  // mostly the next one; else past any number of empty ones
+      if (again) i = max(i, seq_behind(a.offsets, a.S, a.T, max(t, lo_i)));
     }
     if (i < a.S) {
       in_seq = lo_i <= t;

@@ -89,3 +89,59 @@ def test_device_errors_show_on_every_path_of_the_products():
     assert mrs.experts_status(DEV, clear=True) == mrs.DEVICE_WAIT_TIMEOUT
     assert torch.equal(mrs.experts_mxfp4(x, w, T, K, B, sid, eid, npp), good)
     assert mrs.experts_status(DEV) == 0
+
+
+def _gpu_time(call, n=10):
+    for _ in range(3):
+        call()
+    start, end = torch.cuda.Event(True), torch.cuda.Event(True)
+    start.record()
+    for _ in range(n):
+        call()
+    end.record()
+    torch.cuda.synchronize()
+    return start.elapsed_time(end) / n  # ms
+
+
+@pytest.mark.parametrize("where", ["behind padding", "in the middle", "at the start", "at the end",
+                                   "two clumps"])
+@pytest.mark.parametrize("softmax", [False, True])
+def test_any_number_of_empty_sequences(where, softmax):
+    # 60000 empty sequences change the mean over sequences and nothing else, and are stepped over
+    # by searching: one after another they took up to 12 ms at 8192 tokens
+    T, E, K, n = 3000, 64, 6, 60000
+    logits, ids = _router(T, E, K)
+    a, b = T // 3, T - 10
+    few = {"behind padding": [b, T], "in the middle": [0, a, T], "at the start": [0, a, T],
+           "at the end": [0, a, b], "two clumps": [5, a, b]}[where]
+    many = {"behind padding": [b] * n + [T], "in the middle": [0] + [a] * n + [T],
+            "at the start": [0] * n + [a, T], "at the end": [0, a] + [b] * n,
+            "two clumps": [5] + [a] * n + [b] * (n // 16)}[where]
+    got, one = [], torch.ones(1, device=DEV)
+    for offsets in (few, many):
+        off = torch.tensor(offsets, dtype=torch.int32, device=DEV)
+        S = len(offsets) - 1
+        out = mrs.BalanceBuffers.allocate(T, E, S, device=DEV)
+        grad = torch.empty(T, E, device=DEV)
+
+        def loss():
+            # (coef times S: a sequence weighs the same in both)
+            mrs.balance_loss(logits, ids, 0.5 * S, softmax=softmax, seq_offsets=off, out=out)
+
+        def backward():
+            mrs.route_backward(logits, ids, None, 1.0, softmax, one, out.counts, 0.5 * S, off,
+                               out=grad)
+
+        times = [_gpu_time(loss), _gpu_time(backward)]
+        full = [i for i in range(S) if offsets[i + 1] > offsets[i]]
+        got.append((out.loss.item(), out.counts[full], out.mean_probs[full], grad, times))
+        assert int(out.counts.sum()) == int(out.counts[full].sum())
+        assert not out.mean_probs.sum(1)[[i for i in (0, S // 2, S - 1) if i not in full]].any()
+    (l0, c0, m0, g0, t0), (l1, c1, m1, g1, t1) = got
+    assert torch.equal(c0, c1) and torch.equal(m0, m1)
+    # one more rounding of coef / S, and sums of the same terms in another order
+    assert abs(l0 - l1) <= 2.0 ** -20 * abs(l0)
+    assert torch.all((g0 - g1).abs() <= 2.0 ** -20 * g0.abs() + 1e-30)
+    # 60000 rows of counts and means are written (9 times the short call's 11 us); the gradient
+    # only searches (the same 8 us)
+    assert t1[0] <= 30 * t0[0] and t1[1] <= 10 * t0[1], (t0, t1)
