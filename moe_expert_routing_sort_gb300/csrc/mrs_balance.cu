@@ -47,6 +47,7 @@ constexpr int kDepth = 4;          // rows of a lane in flight, the one it works
 constexpr int kBalWarps = kBalThreads / 32;
 constexpr int kBalMaxCtas = 256;
 constexpr int kIdsAhead = 4;       // routes of a thread loaded ahead of a stretch's rows
+constexpr int kSumRows = 64;       // rows whose sum stays in registers, at least
 constexpr int kSoloRows = 4;       // rows per group up to which one CTA takes the call
 constexpr int kSoloSeqs = 8;
 constexpr int kBalMaxJoin = 1024;  // CTAs of the second kernel
@@ -414,24 +415,34 @@ __global__ void __launch_bounds__(kBalThreads, 1) mrs_balance_rows_kernel(const 
 #pragma unroll
     for (int q = 0; q < kIdsAhead; ++q, r += kBalThreads) id[q] = r < r1 ? __ldg(a.ids + r) : -1;
     if (!idle && row < hi) {
-      float acc[NC];
-#pragma unroll
-      for (int c = 0; c < NC; ++c) acc[c] = 0.0f;
-      for (int buf = 0; row < hi; row += groups, buf ^= 1) {
-        float x[NC], scale, dot, top, inv;
-        rows.take(E, groups, hi, lane, lanes, x);
-        row_terms<NC, kSoftmax, false>(x, g0, past, W, grp, gw, xchg, buf, scale, dot, top, inv);
-#pragma unroll
-        for (int c = 0; c < NC; ++c) acc[c] = fmaf(x[c], scale, acc[c]);
-      }
       float* mine = red + static_cast<size_t>(grp) * lanes * NC;
+      // Sums of up to `each` rows, then the sum of those: about 2 sqrt(rows) additions deep and not
+      // one per row, which for 7000 rows of equal terms is off by up to 2^-11.
+      int each = kSumRows;
+      while (static_cast<long long>(each) * each < (hi - row) / groups) each *= 2;
+      for (int buf = 0, part = 0; row < hi; ++part) {
+        float acc[NC];
 #pragma unroll
-      for (int c = 0; c < NC; c += kVec ? 4 : 1) {
-        float* to = mine + column_of<kVec>(c, lane, lanes);
-        if constexpr (kVec)
-          *reinterpret_cast<float4*>(to) = make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
-        else
-          *to = acc[c];
+        for (int c = 0; c < NC; ++c) acc[c] = 0.0f;
+        for (int q = 0; q < each && row < hi; ++q, row += groups, buf ^= 1) {
+          float x[NC], scale, dot, top, inv;
+          rows.take(E, groups, hi, lane, lanes, x);
+          row_terms<NC, kSoftmax, false>(x, g0, past, W, grp, gw, xchg, buf, scale, dot, top, inv);
+#pragma unroll
+          for (int c = 0; c < NC; ++c) acc[c] = fmaf(x[c], scale, acc[c]);
+        }
+#pragma unroll
+        for (int c = 0; c < NC; c += kVec ? 4 : 1) {
+          float* to = mine + column_of<kVec>(c, lane, lanes);
+          if constexpr (kVec) {
+            float4* to4 = reinterpret_cast<float4*>(to);
+            const float4 had = part > 0 ? *to4 : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            *to4 = make_float4(had.x + acc[c], had.y + acc[c + 1], had.z + acc[c + 2],
+                               had.w + acc[c + 3]);
+          } else {
+            *to = part > 0 ? *to + acc[c] : acc[c];
+          }
+        }
       }
     }
     auto count = [&](int e) {

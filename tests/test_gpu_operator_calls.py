@@ -145,3 +145,18 @@ def test_any_number_of_empty_sequences(where, softmax):
     # 60000 rows of counts and means are written (9 times the short call's 11 us); the gradient
     # only searches (the same 8 us)
     assert t1[0] <= 30 * t0[0] and t1[1] <= 10 * t0[1], (t0, t1)
+
+
+@pytest.mark.parametrize("softmax", [False, True])
+def test_the_means_of_many_tokens(softmax):
+    # equal logits: every probability is 1 / 56, a sum's roundings all go the same way, and one
+    # addition per token (6900 a group of warps) was off by 7.7e-5.  Now: a probability within
+    # 2^-22, sums 128 + 54 additions deep, 16 groups, 19 + 8 CTAs, each 2^-24: 2^-16 in all; the loss
+    # adds 56 terms to that.
+    T, E, K = 1 << 24, 56, 2
+    logits = torch.zeros(T, E, dtype=torch.bfloat16, device=DEV)
+    ids = torch.randint(0, E, (T, K), dtype=torch.int32, device=DEV)
+    out = mrs.balance_loss(logits, ids, 0.25, softmax=softmax)
+    assert (out.mean_probs.double() * E - 1).abs().max().item() <= 2.0 ** -16
+    assert abs(out.loss.item() / 0.25 - 1) <= 2.0 ** -15.5
+    assert torch.equal(out.counts[0].long(), torch.bincount(ids.flatten(), minlength=E))
