@@ -499,7 +499,7 @@ __global__ void __launch_bounds__(kJoinThreads) mrs_balance_join_kernel(const Ba
   int lo = seq_border(a.offsets, blockIdx.y, a.T), hi = seq_border(a.offsets, blockIdx.y + 1, a.T);
   pdl_trigger();
   pdl_wait();
-  float loss = 0.0f;
+  float loss = 0.0f, lost = 0.0f;  // a sum of up to 8192 sequences, and what its roundings left out
   int buf = 0;
   for (int i = blockIdx.y; i < a.S; i += gridDim.y, buf ^= 1) {
     float p = 0.0f;
@@ -527,7 +527,9 @@ __global__ void __launch_bounds__(kJoinThreads) mrs_balance_join_kernel(const Ba
       const size_t at = static_cast<size_t>(i) * a.E + e;
       a.counts[at] = c;
       a.mean[at] = mean;
-      loss += static_cast<float>(c) * mean / n;
+      const float add = static_cast<float>(c) * mean / n - lost, sum = loss + add;
+      lost = (sum - loss) - add;
+      loss = sum;
     }
     lo = seq_border(a.offsets, min(i + static_cast<int>(gridDim.y), a.S), a.T);
     hi = seq_border(a.offsets, min(i + static_cast<int>(gridDim.y) + 1, a.S), a.T);

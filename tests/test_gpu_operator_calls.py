@@ -160,3 +160,19 @@ def test_the_means_of_many_tokens(softmax):
     assert (out.mean_probs.double() * E - 1).abs().max().item() <= 2.0 ** -16
     assert abs(out.loss.item() / 0.25 - 1) <= 2.0 ** -15.5
     assert torch.equal(out.counts[0].long(), torch.bincount(ids.flatten(), minlength=E))
+
+
+def test_the_loss_of_many_sequences():
+    # one token each, all to the same experts: 8192 equal terms a thread, whose plain sum is off by
+    # 1.2e-4.  Against the loss of the
+    # call's own counts and means: a term is two roundings and the sum 1 + 31 + 10 additions of
+    # 2^-24 after the compensated one, the scale three more: 2^-18.
+    T = S = 65536
+    E, K = 4091, 32
+    logits = torch.zeros(T, E, dtype=torch.bfloat16, device=DEV)
+    ids = torch.arange(K, dtype=torch.int32, device=DEV).repeat(T, 1)
+    off = torch.arange(T + 1, dtype=torch.int32, device=DEV)
+    out = mrs.balance_loss(logits, ids, 1.0, seq_offsets=off)
+    want = (out.counts[:, :K].double() * out.mean_probs[:, :K].double()).sum() * (E / K / S)
+    assert int(out.counts.sum()) == T * K and int(out.counts[:, :K].min()) == 1
+    assert abs(out.loss.item() - want.item()) <= 2.0 ** -18 * want.item()
