@@ -388,6 +388,7 @@ __global__ void __launch_bounds__(kBalThreads, 1) mrs_balance_rows_kernel(const 
   float loss = 0.0f;  // solo: this thread's experts
   int t = t0;
   int i = a.solo ? 0 : seq_behind(a.offsets, a.S, a.T, t0);
+  bool again = false;
   while (i < a.S && (t < t1 || a.solo)) {
     const int lo_i = seq_border(a.offsets, i, a.T), hi_i = seq_border(a.offsets, i + 1, a.T);
     const int lo = max(lo_i, t), hi = min(hi_i, t1);
@@ -397,13 +398,15 @@ __global__ void __launch_bounds__(kBalThreads, 1) mrs_balance_rows_kernel(const 
           a.counts[static_cast<size_t>(i) * E + e] = 0;
           a.mean[static_cast<size_t>(i) * E + e] = 0.0f;
         }
-        ++i;
-      } else {
-        if (lo_i >= t1) break;
-        i = max(i + 1, seq_behind(a.offsets, a.S, a.T, lo));  // past any number of empty ones
+      } else if (lo_i >= t1) {
+        break;
       }
+      ++i;  // mostly one empty sequence; else past any number of them
+      if (again && !a.solo) i = max(i, seq_behind(a.offsets, a.S, a.T, lo));
+      again = true;
       continue;
     }
+    again = false;
     t = hi;
     RowStream<NC, kVec, kSoftmax> rows;
     int row = lo + grp;
@@ -419,7 +422,7 @@ __global__ void __launch_bounds__(kBalThreads, 1) mrs_balance_rows_kernel(const 
       // Sums of up to `each` rows, then the sum of those: about 2 sqrt(rows) additions deep and not
       // one per row, which for 7000 rows of equal terms is off by up to 2^-11.
       int each = kSumRows;
-      while (static_cast<long long>(each) * each < (hi - row) / groups) each *= 2;
+      while (static_cast<long long>(each) * each * groups < hi - lo) each *= 2;
       for (int buf = 0, part = 0; row < hi; ++part) {
         float acc[NC];
 #pragma unroll
