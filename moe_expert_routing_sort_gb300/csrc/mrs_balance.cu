@@ -123,6 +123,25 @@ __device__ __forceinline__ int seq_behind(const int32_t* o, int S, int T, int t)
   return lo;
 }
 
+// The largest and the most negative of a lane's logits, two bf16 patterns a word: among signed
+// numbers a positive pattern, among unsigned ones a negative pattern is the larger the further it is
+// from zero.
+struct Extremes {
+  uint32_t up, down;
+  __device__ __forceinline__ void add(uint32_t a, uint32_t b) {
+    up = __vimax3_s16x2(up, a, b);
+    down = __vimax3_u16x2(down, a, b);
+  }
+  // Any beyond 7.5, where 1 / (1 + e^-x) is too near 1 to be taken from it.
+  __device__ __forceinline__ bool high() const {
+    return max(static_cast<int>(up << 16), static_cast<int>(up & 0xffff0000u)) > 0x40f00000;
+  }
+  // Any at or below -43, where a product of two 1 + e^-x could leave the range.
+  __device__ __forceinline__ bool low() const {
+    return max(down << 16, down & 0xffff0000u) >= 0xc22c0000u;
+  }
+};
+
 // Rows of a lane on their way: the lane's columns of row `row`, `step` rows after the one before.
 // kVec: 16-byte vectors of 8 columns, vector v of the lane being vector v * lanes + lane of the
 // row, copied to shared memory (ring: 16 bytes per vector, thread and slot); else single columns
@@ -168,10 +187,11 @@ struct RowStream {
       from += static_cast<size_t>(step) * E;
     }
   }
-  // The values of the next row, whose successors keep coming.
+  // The values of the next row, whose successors keep coming.  (Sigmoids: their extremes too.)
   __device__ __forceinline__ void take(int E, int step, int hi, int lane, int lanes,
-                                       float (&x)[NC]) {
+                                       float (&x)[NC], Extremes& ext) {
     constexpr uint32_t kRow = 16 * kBalThreads * NV;
+    ext.up = ext.down = 0u;
     if constexpr (kVec) {
       fetch(E, hi, lane, lanes, ring + (slot == 0 ? (kDepth - 1) * kRow : slot - kRow));
       copy_wait<kDepth - 1>();
@@ -183,6 +203,10 @@ struct RowStream {
                        : "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3])
                        : "r"(ring + slot + 16 * kBalThreads * v)
                        : "memory");
+        if constexpr (!kSoftmax) {
+          ext.add(q[0], q[1]);
+          ext.add(q[2], q[3]);
+        }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           x[8 * v + 2 * j] = __uint_as_float(q[j] << 16);
@@ -193,6 +217,10 @@ struct RowStream {
     } else {
 #pragma unroll
       for (int i = 0; i < NC; ++i) x[i] = __uint_as_float(next[i]);
+      if constexpr (!kSoftmax) {
+#pragma unroll
+        for (int i = 0; i < NC; i += 2) ext.add(next[i], next[i + 1]);
+      }
       fetch(E, hi, lane, lanes, 0);
     }
     row += step;
@@ -226,11 +254,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-__device__ __forceinline__ float min3(float a, float b, float c) {
-  float r;
-  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(kFull, v, d);
@@ -248,20 +271,24 @@ __host__ __device__ constexpr int groups_of(int W) {
   return W > 1 && kBalWarps / W > 15 ? 15 : kBalWarps / W;
 }
 
+// A sigmoid (of 7.6) from which 1 - s is not taken as it stands: what s was rounded by, 2^-24, would
+// be 2^-13 of the difference and more, until at a logit of 17 nothing is left of it.
+constexpr float kHighSigmoid = 0.9995f;
+// 1 - s of the sigmoid s of x.
+__device__ __forceinline__ float one_less(float s, float x) {
+  return s > kHighSigmoid ? s * ex2(-kLog2e * x) : 1.0f - s;
+}
+
 // Barrier of the W warps of group `grp`.
 __device__ __forceinline__ void group_sync(int grp, int W) {
   asm volatile("bar.sync %0, %1;" ::"r"(grp + 1), "r"(32 * W) : "memory");
 }
 
 // Sigmoids in place.  One reciprocal serves two, 1 / (a b) times the other, unless a product of
-// two denominators could leave the range (a logit below about -43 in the lane).
+// two denominators could leave the range.
 template <int NC>
-__device__ __forceinline__ void sigmoids(float (&x)[NC]) {
-  float low = x[0];
-#pragma unroll
-  for (int i = 1; i + 1 < NC; i += 2) low = min3(low, x[i], x[i + 1]);
-  low = fminf(low, x[NC - 1]);
-  if (low > -43.0f) {
+__device__ __forceinline__ void sigmoids(float (&x)[NC], const Extremes& ext) {
+  if (!ext.low()) {
 #pragma unroll
     for (int i = 0; i < NC; i += 2) {
       const float e0 = 1.0f + ex2(-kLog2e * x[i]), e1 = 1.0f + ex2(-kLog2e * x[i + 1]);
@@ -284,8 +311,8 @@ __device__ __forceinline__ void sigmoids(float (&x)[NC]) {
 // reduction rescales by differences of those same m: nothing is lost to the rounding of m.
 // (Two values per instruction, .f32x2, was tried: packing the exponentials cost what it saved.)
 template <int NC, bool kSoftmax, bool kDot>
-__device__ __forceinline__ void row_terms(float (&x)[NC], const float (&g)[kDot ? NC : 1],
-                                          unsigned past, int W, int grp, int gw, float4* xchg,
+__device__ __forceinline__ void row_terms(float (&x)[NC], const Extremes& ext,
+                                          const float (&g)[kDot ? NC : 1], unsigned past, int W, int grp, int gw, float4* xchg,
                                           int buf, float& scale, float& dot, float& top,
                                           float& inv) {
   float m = 0.0f;
@@ -307,7 +334,7 @@ __device__ __forceinline__ void row_terms(float (&x)[NC], const float (&g)[kDot 
 #pragma unroll
     for (int i = 0; i < NC; ++i) x[i] = ex2(fmaf(x[i], kLog2e, -m));
   } else {
-    sigmoids<NC>(x);
+    sigmoids<NC>(x, ext);
   }
   float sum = 0.0f, d4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -429,8 +456,9 @@ __global__ void __launch_bounds__(kBalThreads, 1) mrs_balance_rows_kernel(const 
         for (int c = 0; c < NC; ++c) acc[c] = 0.0f;
         for (int q = 0; q < each && row < hi; ++q, row += groups, buf ^= 1) {
           float x[NC], scale, dot, top, inv;
-          rows.take(E, groups, hi, lane, lanes, x);
-          row_terms<NC, kSoftmax, false>(x, g0, past, W, grp, gw, xchg, buf, scale, dot, top, inv);
+          Extremes ext;
+          rows.take(E, groups, hi, lane, lanes, x, ext);
+          row_terms<NC, kSoftmax, false>(x, ext, g0, past, W, grp, gw, xchg, buf, scale, dot, top, inv);
 #pragma unroll
           for (int c = 0; c < NC; ++c) acc[c] = fmaf(x[c], scale, acc[c]);
         }
@@ -645,15 +673,27 @@ __global__ void __launch_bounds__(kBalThreads, 1)
       const float xk = valid ? bf16_bits_to_float(__ldg(xr + id)) : -INFINITY;
       const float gk = valid && f != 0.0f ? f * static_cast<float>(__ldg(counts + id)) : 0.0f;
       fetch(row + groups);
-      rows.take(E, groups, hi, lane, lanes, x);
+      Extremes ext;
+      rows.take(E, groups, hi, lane, lanes, x, ext);
       float scale = 0.0f, dot = 0.0f, top = 0.0f, inv = 0.0f;
       if (dense) {
-        row_terms<NC, kSoftmax, true>(x, g, past, W, grp, gw, xchg, buf, scale, dot, top, inv);
+        row_terms<NC, kSoftmax, true>(x, ext, g, past, W, grp, gw, xchg, buf, scale, dot, top, inv);
         buf ^= 1;
+        if (!kSoftmax && ext.high()) {
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          const float p = x[c] * scale;
-          x[c] = (kSoftmax ? p : fmaf(-p, x[c], p)) * (g[c] - dot);
+          for (int c = 0; c < NC; ++c) {
+            const float p = x[c] * scale;
+            float q = fmaf(-p, x[c], p);
+            if (x[c] > kHighSigmoid)
+              q = p * one_less(x[c], bf16_bits_to_float(__ldg(xr + column_of<kVec>(c, lane, lanes))));
+            x[c] = q * (g[c] - dot);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            const float p = x[c] * scale;
+            x[c] = (kSoftmax ? p : fmaf(-p, x[c], p)) * (g[c] - dot);
+          }
         }
       } else {
 #pragma unroll
@@ -695,18 +735,18 @@ __global__ void __launch_bounds__(kBalThreads, 1)
         // columns: the whole gradient there, its balance term taken anew from the row's sums, over
         // the one that the column's lane has just written.
         if (!valid) wg = 0.0f;
-        float u, s = 0.0f;
+        float u, s = 0.0f, less = 1.0f;
         if (kSoftmax) {
           const float m = fmaxf(warp_max(xk), kLowest);
           u = ex2((xk - m) * kLog2e);
         } else {
           u = s = rcp(1.0f + ex2(-kLog2e * xk));  // 0 for a route that is none
+          less = one_less(s, xk);
         }
         const float su = warp_sum(u);
         const float q = su > 0.0f ? u * rcp(su) : 0.0f;
         const float mean = warp_sum(q * wg);
-        float d = a.R * q * (wg - mean);
-        if (!kSoftmax) d *= 1.0f - s;
+        float d = a.R * q * (wg - mean) * less;
         // an expert named twice: the lowest lane takes the sum, in slot order
         const int key = valid ? id : -1 - wl;
         const unsigned same = __match_any_sync(kFull, key);
@@ -723,7 +763,7 @@ __global__ void __launch_bounds__(kBalThreads, 1)
         // (without the loss there are no sums to take the power against: it could leave the range)
         const bool none = !dense || xk == -INFINITY;
         const float p = kSoftmax ? (none ? 0.0f : ex2(fmaf(xc, kLog2e, -top)) * inv) : s * inv;
-        d = fmaf(kSoftmax ? p : fmaf(-p, s, p), gk - dot, d);
+        d = fmaf(p * less, gk - dot, d);
         __syncwarp();  // the row's own stores come first
         if (valid && (same & lanemask_lt(wl)) == 0u && (owner >> 5) == gw) {
           if constexpr (sizeof(Out) == 4) out[id] = d;

@@ -176,3 +176,41 @@ def test_the_loss_of_many_sequences():
     want = (out.counts[:, :K].double() * out.mean_probs[:, :K].double()).sum() * (E / K / S)
     assert int(out.counts.sum()) == T * K and int(out.counts[:, :K].min()) == 1
     assert abs(out.loss.item() - want.item()) <= 2.0 ** -18 * want.item()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("weights,loss", [(True, False), (False, True), (True, True)])
+@pytest.mark.parametrize("E,K", [(64, 6), (129, 5), (896, 16), (2056, 8)])
+def test_gradients_of_sigmoids_near_one(E, K, weights, loss, dtype):
+    # 1 - s, which both terms carry, is e^-17 at a logit of 17: half a step of an s near 1.
+    # Relative to |p (1 - s)| (|g| + sum p |g|) and the like of the weights: s is within 2^-23, and
+    # 1 - s at least 2^-11 where it is taken from s (2^-12); where it is s e^-x, an argument of 60
+    # rounded by 2^-18 and then 2^-21; all else below 2^-15.
+    T, R, coef = 200, 2.5, 0.5
+    g = torch.Generator().manual_seed(E)
+    logits = (24 * torch.rand(T, E, generator=g) + 12 * torch.rand(T, 1, generator=g) - 4).bfloat16()
+    logits[1] += 20
+    ids = torch.rand(T, E, generator=g).topk(K, dim=1).indices.int()
+    gw = torch.randn(T, K, generator=g)
+    counts = torch.bincount(ids.flatten().long(), minlength=E).int()[None]
+    got = mrs.route_backward(logits.to(DEV), ids.to(DEV), gw.to(DEV) if weights else None, R,
+                             grad_loss=torch.ones(1, device=DEV) if loss else None,
+                             counts=counts.to(DEV), coef=coef, dtype=dtype).double().cpu()
+    x = logits.double()
+    s, less = 1 / (1 + (-x).exp()), 1 / (1 + x.exp())
+    want, scale = torch.zeros_like(x), torch.zeros_like(x)
+    if loss:
+        p = s / s.sum(1, keepdim=True)
+        f = coef * E / (K * T * T) * counts.double()
+        dot = (p * f).sum(1, keepdim=True)
+        want += p * less * (f - dot)
+        scale += p * less * (f + dot)
+    if weights:
+        at = ids.long()
+        q = s.gather(1, at) / s.gather(1, at).sum(1, keepdim=True)
+        c, w = less.gather(1, at), gw.double()
+        want.scatter_add_(1, at, R * q * c * (w - (q * w).sum(1, keepdim=True)))
+        scale.scatter_add_(1, at, R * q * c * (w.abs() + (q * w.abs()).sum(1, keepdim=True)))
+    half = 2.0 ** -8 if dtype == torch.bfloat16 else 0.0
+    err = (got - want).abs()
+    assert torch.all(err <= 2.0 ** -11.5 * scale + half * want.abs() + 1e-36), (err / scale).max()
