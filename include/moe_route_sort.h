@@ -324,8 +324,9 @@ int moe_mxfp4_quantize(const void* x, int x_dtype, int64_t rows, int cols, int64
                        uint8_t* codes, uint8_t* scales, cudaStream_t stream);
 
 /* The values that MXFP4 rows stand for, into y (y_dtype MOE_RS_BF16 or MOE_RS_FP32, y_stride
- * elements between rows, each row 16-byte aligned).  fp32 holds every value; bf16 holds every
- * value that moe_mxfp4_quantize makes.  Errors as above. */
+ * elements between rows, each row 16-byte aligned).  Both types hold every value of scale bytes up
+ * to 252, the largest that moe_mxfp4_quantize makes; of bytes 253 and 254 the magnitudes from 2^128
+ * on become infinities of their sign.  Errors as above. */
 int moe_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int cols,
                          void* y, int y_dtype, int64_t y_stride, cudaStream_t stream);
 

@@ -214,3 +214,46 @@ def test_gradients_of_sigmoids_near_one(E, K, weights, loss, dtype):
     half = 2.0 ** -8 if dtype == torch.bfloat16 else 0.0
     err = (got - want).abs()
     assert torch.all(err <= 2.0 ** -11.5 * scale + half * want.abs() + 1e-36), (err / scale).max()
+
+
+GRID = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6, -0.0, -0.5, -1, -1.5, -2, -3, -4, -6],
+                    dtype=torch.float64)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_every_scale_byte_with_every_code(dtype):
+    # 2^(byte - 127) times the grid, exactly; beyond the type an infinity, byte 255 NaN
+    byte = torch.arange(256, dtype=torch.uint8)
+    code = torch.arange(32, dtype=torch.uint8) % 16
+    codes = (code[0::2] | (code[1::2] << 4)).repeat(256, 1)
+    scales = torch.zeros(256, 4, dtype=torch.uint8)
+    scales[:, 0] = byte
+    got = mrs.mxfp4_dequantize(mrs.Mxfp4Rows(codes.to(DEV), scales.to(DEV)), dtype=dtype).cpu()
+    want = torch.pow(2.0, byte.double() - 127)[:, None] * GRID.repeat(2)
+    want[255] = float("nan")
+    far = want.abs() > torch.finfo(dtype).max
+    # 2, 3, 4, 6 of byte 254 and 4, 6 of 253, either sign, each code twice in a block
+    assert int(far.sum()) == (4 + 2) * 2 * 2
+    want[far] = want[far].sign() * float("inf")
+    assert torch.equal(got.double().nan_to_num(7.0, 8.0, -8.0), want.nan_to_num(7.0, 8.0, -8.0))
+    assert torch.equal(torch.signbit(got[:255]), torch.signbit(GRID.repeat(2)).expand(255, 32))
+
+
+def test_products_of_the_furthest_scales():
+    # the largest and smallest scale bytes of rows against weights that bring the product back into
+    # fp32: exact values (a single product per sum), whatever either factor is by itself
+    T, E, K, cols, N, B = 16, 1, 1, 64, 16, 16
+    x, w, lists = _layer(T, E, K, cols, N, B)
+    x.codes.zero_()
+    w.codes.zero_()
+    x.codes[:, 0] = 7  # 6 in the first column
+    w.codes[0, :, 0] = torch.arange(16, dtype=torch.uint8, device=DEV)  # every code
+    for xb, wb in [(254, 20), (254, 120), (253, 100), (252, 127), (20, 254), (0, 200), (0, 254),
+                   (1, 252), (100, 30), (127, 254)]:
+        x.scales.fill_(xb)
+        w.scales.fill_(wb)
+        got = mrs.experts_mxfp4(x, w, T, K, B, *lists, dtype=torch.float32).double().cpu()
+        want = 6.0 * 2.0 ** (xb + wb - 254) * GRID
+        far = want.abs() > torch.finfo(torch.float32).max
+        want[far] = want[far].sign() * float("inf")
+        assert torch.equal(got, want.expand(T, N)), (xb, wb, got[0], want)
