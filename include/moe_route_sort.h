@@ -365,6 +365,13 @@ int moe_experts_mxfp4(const uint8_t* x_codes, const uint8_t* x_scales, int x_per
                       const int32_t* num_tokens_post_pad, void* out, int out_dtype,
                       void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
+/* How moe_experts_mxfp4 divides a call on a device of `sms` multiprocessors, for tests and tuning
+ * (host only): plan[0] outputs of a tile, [1] blocks of a window (1: blocks by themselves), [2] parts
+ * of a block, [3] tiles along the outputs, [4] tiles of a unit, whose rows stay where they are for
+ * them, [5] units along the outputs, [6] steps of 256 columns. */
+int moe_experts_mxfp4_plan(int T, int E, int topk, int cols, int outs, int block_m, int sms,
+                           int32_t* plan);
+
 /* One of the five operations above with its arguments as an array, for language bindings that pay
  * per argument.  args: 8-byte values (8-byte aligned host memory): the operation's number, the
  * number of its arguments, then the arguments in the order of its declaration -- pointers, the

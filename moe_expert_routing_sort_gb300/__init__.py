@@ -40,11 +40,13 @@ from .binding import (  # noqa: F401
     strerror,
 )
 from .experts import (  # noqa: F401
+    ExpertsPlan,
     ExpertsWorkspace,
     Mxfp4Rows,
     experts_mxfp4,
     experts_status,
     moe_experts_mxfp4,
+    moe_experts_mxfp4_plan,
     moe_experts_mxfp4_status,
     moe_experts_mxfp4_workspace_bytes,
     moe_mxfp4_dequantize,

@@ -104,6 +104,8 @@ def load() -> ctypes.CDLL:
         lib.moe_experts_mxfp4.restype = I
         lib.moe_experts_mxfp4_status.argtypes = [P, I, P]
         lib.moe_experts_mxfp4_status.restype = I
+        lib.moe_experts_mxfp4_plan.argtypes = [I] * 7 + [ctypes.POINTER(ctypes.c_int32)]
+        lib.moe_experts_mxfp4_plan.restype = I
         lib.moe_call_packed.argtypes = [ctypes.c_char_p]
         lib.moe_call_packed.restype = I
         _lib = lib

@@ -820,6 +820,24 @@ int moe_experts_mxfp4(const uint8_t* x_codes, const uint8_t* x_scales, int x_per
                                      : go(std::integral_constant<int, 256>{}));
 }
 
+int moe_experts_mxfp4_plan(int T, int E, int topk, int cols, int outs, int block_m, int sms,
+                           int32_t* plan) {
+  if (T < 1) return MOE_RS_ERR_BAD_TOKENS;
+  if (E < 1 || E > kMaxExperts) return MOE_RS_ERR_BAD_EXPERTS;
+  if (topk < 1 || topk > kMaxTopk) return MOE_RS_ERR_BAD_TOPK;
+  if (moe_experts_mxfp4_workspace_bytes(T, E, topk, block_m) == 0) return MOE_RS_ERR_BAD_BLOCK_M;
+  if (moe_mxfp4_scale_cols(cols) == 0 || outs < 8 || outs > MOE_RS_MXFP4_MAX_OUTS || outs % 8 != 0)
+    return MOE_RS_ERR_BAD_COLS;
+  if (sms < 1 || static_cast<int64_t>(T) * topk > INT32_MAX) return MOE_RS_ERR_OVERFLOW;
+  if (!plan) return MOE_RS_ERR_NULL_POINTER;
+  const int64_t blocks = static_cast<int64_t>(moe_sort_max_padded(T, E, topk, block_m) / block_m);
+  const ExpertsPlan p =
+      experts_plan(blocks, static_cast<int64_t>(T) * topk, E, block_m, outs, cols, sms);
+  const int32_t v[] = {p.bn, p.group, p.subs, p.ntile, p.chunk, p.nchunk, p.ksteps};
+  for (int i = 0; i < 7; ++i) plan[i] = v[i];
+  return MOE_RS_OK;
+}
+
 int moe_experts_mxfp4_status(int32_t* dst, int clear, cudaStream_t stream) {
   if (!dst) return MOE_RS_ERR_NULL_POINTER;
   if (!aligned(dst, 4)) return MOE_RS_ERR_MISALIGNED;

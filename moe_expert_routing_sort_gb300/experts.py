@@ -6,7 +6,8 @@ metadata, with the quantisation of rows and weights (see include/moe_route_sort.
 """
 from __future__ import annotations
 
-from typing import Optional
+import ctypes
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -61,6 +62,28 @@ class Mxfp4Rows:
             raise ValueError(f"cols must be a multiple of 32 in [32, 32768], got {cols}")
         return cls(torch.empty(*lead, cols // 2, dtype=torch.uint8, device=device),
                    torch.empty(*lead, sc, dtype=torch.uint8, device=device))
+
+
+class ExpertsPlan(NamedTuple):
+    """How a product is divided: outputs of a tile, blocks of a window (1: blocks by themselves),
+    parts of a block, tiles along the outputs, tiles of a unit, units along the outputs, steps of
+    256 columns."""
+
+    tile_outs: int
+    window: int
+    parts: int
+    tiles: int
+    unit_tiles: int
+    units: int
+    steps: int
+
+
+def moe_experts_mxfp4_plan(T: int, E: int, topk: int, cols: int, outs: int, block_m: int,
+                           sms: int = 152) -> ExpertsPlan:
+    plan = (ctypes.c_int32 * 7)()
+    _check(load().moe_experts_mxfp4_plan(T, E, topk, cols, outs, block_m, sms, plan),
+           "moe_experts_mxfp4_plan")
+    return ExpertsPlan(*plan)
 
 
 class ExpertsWorkspace:

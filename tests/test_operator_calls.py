@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import moe_expert_routing_sort_gb300 as mrs
+from _shapes import STAYING, plan_row
 from moe_expert_routing_sort_gb300 import _build, training
 
 
@@ -76,3 +77,27 @@ def test_the_package_imports_without_cuda_in_torch():
     got = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True,
                          cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
     assert got.returncode == 0, got.stderr
+
+
+@pytest.mark.parametrize("shape,row", [(s, tuple(r)) for s, *r in STAYING])
+def test_shapes_whose_rows_stay_for_several_tiles(lib, shape, row):
+    plan = mrs.moe_experts_mxfp4_plan(*shape, sms=152)
+    assert plan.unit_tiles > 1 and plan_row(plan, shape[4]) == row
+    assert plan.units == -(-plan.tiles // plan.unit_tiles) and plan.steps == -(-shape[3] // 256)
+
+
+def test_plans_of_other_calls(lib):
+    plan = mrs.moe_experts_mxfp4_plan
+    # one token: a block an expert, nothing stays; few wide experts: tiles of 256, which do not stay
+    assert plan(1, 896, 16, 3584, 768, 16) == (96, 1, 1, 8, 1, 8, 14)
+    assert plan(8192, 64, 8, 7168, 2048, 128) == (256, 1, 1, 8, 1, 8, 28)
+    assert plan(8192, 896, 16, 384, 3584, 128).unit_tiles == 19
+    assert any(s[2] and s[0] == 192 for _, *s in STAYING)
+    for bad in [(0, 4, 2, 64, 16, 16), (8, 0, 2, 64, 16, 16), (8, 4, 0, 64, 16, 16),
+                (8, 4, 2, 48, 16, 16), (8, 4, 2, 64, 12, 16), (8, 4, 2, 64, 16, 24),
+                (1 << 30, 4, 4, 64, 16, 16)]:
+        with pytest.raises(mrs.RouteSortError):
+            plan(*bad)
+    with pytest.raises(mrs.RouteSortError):
+        plan(8, 4, 2, 64, 16, 16, sms=0)
+    assert lib.moe_experts_mxfp4_plan(8, 4, 2, 64, 16, 16, 152, None) == -1
