@@ -580,6 +580,7 @@ __global__ void __launch_bounds__(kJoinThreads) mrs_balance_join_kernel(const Ba
     last = before == static_cast<unsigned>(ctas - 1) ? 1 : 0;
   }
   if (__shfl_sync(kFull, last, 0) == 0) return;
+  __syncwarp();  // (a shuffle orders no memory: the other lanes' reads come behind the ticket)
   float s = 0.0f;
   for (int q = lane; q < ctas; q += 32) s += __ldcg(a.partial + q);
   s = warp_sum(s);
