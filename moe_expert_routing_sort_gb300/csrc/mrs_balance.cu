@@ -737,8 +737,12 @@ __global__ void __launch_bounds__(kBalThreads, 1)
         // the one that the column's lane has just written.
         if (!valid) wg = 0.0f;
         float u, s = 0.0f, less = 1.0f;
+        const float m = fmaxf(warp_max(xk), kLowest);
+        // The weights' sum is constant, so their gradients count from any one of them: from the
+        // largest weight's, so that a route that holds nearly all has the others' small part as it
+        // is and not as a difference (a token's only route: 0, where u rcp(u) is not quite 1).
+        wg -= __shfl_sync(kFull, wg, (__ffs(__ballot_sync(kFull, xk == m)) - 1) & 31);
         if (kSoftmax) {
-          const float m = fmaxf(warp_max(xk), kLowest);
           u = ex2((xk - m) * kLog2e);
         } else {
           u = s = rcp(1.0f + ex2(-kLog2e * xk));  // 0 for a route that is none

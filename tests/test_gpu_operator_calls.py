@@ -257,3 +257,34 @@ def test_products_of_the_furthest_scales():
         far = want.abs() > torch.finfo(torch.float32).max
         want[far] = want[far].sign() * float("inf")
         assert torch.equal(got, want.expand(T, N)), (xb, wb, got[0], want)
+
+
+@pytest.mark.parametrize("softmax", [False, True])
+@pytest.mark.parametrize("E,K", [(64, 1), (376, 1), (129, 5), (896, 16), (2056, 32)])
+def test_gradients_of_a_route_that_holds_nearly_all(E, K, softmax):
+    # w_k = R q_k and sum q = 1: a token's only route has no gradient, and where one of several has
+    # nearly all the weight its gradient is what the others hold.  Relative to
+    # R q (|g - g_top| + sum q |g - g_top|): q is within 2^-21 + 30 * 2^-23 and sums are 5 deep: 2^-17
+    # (and 2^-12 of 1 - s, as above).
+    T, R = 300, 2.5
+    g = torch.Generator().manual_seed(E + K)
+    logits = (1.5 * torch.randn(T, E, generator=g) - 14).bfloat16()
+    ids = torch.rand(T, E, generator=g).topk(K, dim=1).indices.int()
+    top = torch.randint(0, K, (T, 1), generator=g)
+    lift = 20 * torch.rand(T, 1, generator=g)  # up to e^20 times the others' weights
+    logits.scatter_(1, ids.long().gather(1, top), (lift - 14).bfloat16())
+    gw = torch.randn(T, K, generator=g)
+    got = mrs.route_backward(logits.to(DEV), ids.to(DEV), gw.to(DEV), R, softmax,
+                             dtype=torch.float32).double().cpu()
+    x = logits.double().gather(1, ids.long())
+    u = (x - x.amax(1, keepdim=True)).exp() if softmax else 1 / (1 + (-x).exp())
+    q = u / u.sum(1, keepdim=True)
+    less = 1.0 if softmax else 1 / (1 + x.exp())
+    d = gw.double() - gw.double().gather(1, x.argmax(1, keepdim=True))
+    want = R * q * less * (d - (q * d).sum(1, keepdim=True))
+    scale = R * q * less * (d.abs() + (q * d.abs()).sum(1, keepdim=True))
+    err = (got.gather(1, ids.long()) - want).abs()
+    assert torch.all(err <= (2.0 ** -17 + (0 if softmax else 2.0 ** -12)) * scale), \
+        (err / scale.clamp(min=1e-300)).max()
+    if K == 1:
+        assert not got.any()
