@@ -630,8 +630,12 @@ __global__ void __launch_bounds__(kBalThreads, 1)
 #pragma unroll
     for (int c = 0; c < NC; ++c) g[c] = 0.0f;
     const int32_t* counts = a.counts;
+    int even = 0;
     if (dense && in_seq) {
       const float n = static_cast<float>(hi_i - lo_i);
+      // sum p = 1, so any number may be taken off the counts: that of an even router, for what an
+      // almost even one has left is little beside its counts
+      even = static_cast<int>(static_cast<float>(K) * n / E);
       f = gl * (a.coef / a.S) * (static_cast<float>(E) / K) / n / n;
       counts += static_cast<size_t>(i) * E;
       if (kVec && a.wide_counts) {
@@ -640,16 +644,16 @@ __global__ void __launch_bounds__(kBalThreads, 1)
           const int e = column_of<kVec>(c, lane, lanes);
           if (e >= E) continue;
           const int4 q = __ldg(reinterpret_cast<const int4*>(counts + e));
-          g[c] = f * static_cast<float>(q.x);
-          g[c + 1] = f * static_cast<float>(q.y);
-          g[c + 2] = f * static_cast<float>(q.z);
-          g[c + 3] = f * static_cast<float>(q.w);
+          g[c] = f * static_cast<float>(q.x - even);
+          g[c + 1] = f * static_cast<float>(q.y - even);
+          g[c + 2] = f * static_cast<float>(q.z - even);
+          g[c + 3] = f * static_cast<float>(q.w - even);
         }
       } else {
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
           const int e = column_of<kVec>(c, lane, lanes);
-          if (e < E) g[c] = f * static_cast<float>(__ldg(counts + e));
+          if (e < E) g[c] = f * static_cast<float>(__ldg(counts + e) - even);
         }
       }
     }
@@ -672,7 +676,7 @@ __global__ void __launch_bounds__(kBalThreads, 1)
       float wg = next_gw;
       const bool valid = sparse && wl < K && id >= 0 && id < E;
       const float xk = valid ? bf16_bits_to_float(__ldg(xr + id)) : -INFINITY;
-      const float gk = valid && f != 0.0f ? f * static_cast<float>(__ldg(counts + id)) : 0.0f;
+      const float gk = valid && f != 0.0f ? f * static_cast<float>(__ldg(counts + id) - even) : 0.0f;
       fetch(row + groups);
       Extremes ext;
       rows.take(E, groups, hi, lane, lanes, x, ext);

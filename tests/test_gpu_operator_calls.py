@@ -288,3 +288,33 @@ def test_gradients_of_a_route_that_holds_nearly_all(E, K, softmax):
         (err / scale.clamp(min=1e-300)).max()
     if K == 1:
         assert not got.any()
+
+
+@pytest.mark.parametrize("softmax", [False, True])
+@pytest.mark.parametrize("E,K", [(64, 8), (129, 5), (896, 16), (2056, 8)])
+def test_the_loss_gradient_of_an_almost_even_router(E, K, softmax):
+    # counts that differ by one in a hundred and more: the gradient p (g - sum p g) lives in those
+    # ones.  Relative to p (|g - g0| + sum p |g - g0|), g0 an even router's: a probability is within
+    # 2^-18 (as in the other gradient tests) and sum p within 2^-21 of 1, times at most one count;
+    # with a sigmoid 1 - s, at least 2^-11 where it is taken from an s within 2^-23: 2^-12.
+    T = 200 * E // K
+    logits, ids = _router(T, E, K, seed=E)
+    g = torch.Generator().manual_seed(E)
+    counts = (T * K // E + torch.randint(-1, 2, (1, E), generator=g)).int()
+    assert int(counts.min()) >= 198
+    got = mrs.route_backward(logits, ids, softmax=softmax, grad_loss=torch.ones(1, device=DEV),
+                             counts=counts.to(DEV), coef=0.5, dtype=torch.float32)
+    x = logits.double()
+    s = torch.softmax(x, 1) if softmax else torch.sigmoid(x)
+    p = s / s.sum(1, keepdim=True)
+    c = (counts.to(DEV).double() - T * K / E) * (0.5 * E / K / T / T)
+    less = 1.0 if softmax else 1 / (1 + x.exp())
+    dot = (p * c).sum(1, keepdim=True)
+    scale = p * less * (c.abs() + (p * c.abs()).sum(1, keepdim=True))
+    assert torch.all((got.double() - p * less * (c - dot)).abs()
+                     <= (2.0 ** -17 + (0 if softmax else 2.0 ** -12)) * scale)
+    # an even one has nothing to learn
+    even = torch.full_like(counts, 200).to(DEV)
+    none = mrs.route_backward(logits, ids, softmax=softmax, grad_loss=torch.ones(1, device=DEV),
+                              counts=even, coef=0.5, dtype=torch.float32)
+    assert none.abs().max().item() <= 2.0 ** -20 * 0.5 / T
