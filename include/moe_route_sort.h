@@ -270,8 +270,11 @@ size_t moe_balance_workspace_bytes(int T, int E, int n_seq);
  * Logits may be -inf (a score and probability of 0; a row of nothing else adds 0), and in a softmax
  * finite ones beyond +-2^26 count as that; a sigmoid below 2^-126 (logits under about -87) counts as
  * 0; NaN or +inf logits give unspecified results.
- * logits_bf16 [T,E] 16-byte aligned, topk_ids [T,K]; outputs loss [1] fp32, counts [S,E] int32, mean_probs [S,E] fp32, all overwritten.  Sums are fp32 in a
- * fixed order (the same bits every call); exponentials are the fast ones, within a few 2^-22.
+ * logits_bf16 [T,E] 16-byte aligned, topk_ids [T,K]; outputs loss [1] fp32, counts [S,E] int32,
+ * mean_probs [S,E] fp32, all overwritten.  Sums are fp32 in a fixed order (the same bits every call),
+ * about 2 sqrt(rows) deep.  Exponentials and reciprocals are the fast ones, not those of the route
+ * step: a score is within 2^-21 + |x| 2^-23 of its value, relatively (softmax: the distance to the
+ * row's largest logit for |x|).
  * Limits: 1 <= E <= 4096, 1 <= K <= min(32, E), 1 <= S <= 65536, T >= 0, T*K in int32.
  * No counterpart in the source pages. */
 int moe_balance_loss(const void* logits_bf16, const int32_t* topk_ids, const int32_t* seq_offsets,

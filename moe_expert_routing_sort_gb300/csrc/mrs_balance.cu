@@ -14,17 +14,18 @@
 // Both passes read the logits once.  A row belongs to a group of W warps (W = ceil(E / 1024), or
 // ceil(E / 512) for rows that do not start on 16 bytes), each lane holding up to 32 of its columns
 // in registers, the same columns for every row: the row sums are warp shuffles (and one exchange
-// through shared memory when W > 1), and the column sums of the loss stay in registers until the
-// sequence or the CTA's token range ends.  A softmax row needs one reduction: every lane takes
-// exponentials against its own maximum and the reduction joins (maximum, sum) pairs.  Each lane
-// copies its own columns of the next rows to shared memory in the background (kDepth rows, 96 KB
-// on their way per SM; one row ahead in registers, 16 KB, left the memory idle: T = 8192, E = 896
-// 16.7 us, 14.8 with the ring) and reads back only what it copied, so no wait is shared.  All sums
-// are fp32 in an order fixed by the shape: results are the same bits every call.
+// through shared memory when W > 1), and the column sums of the loss stay in registers for 64 rows
+// (about the square root of a longer stretch) or until the sequence or the CTA's token range ends.
+// A softmax row needs one reduction: every lane takes exponentials against its own maximum and the
+// reduction joins (maximum, sum) pairs.  Each lane copies its own columns of the next rows to shared
+// memory in the background (kDepth rows, 96 KB on their way per SM; one row ahead in registers,
+// 16 KB, left the memory idle: T = 8192, E = 896 16.7 us, 14.8 with the ring) and reads back only
+// what it copied, so no wait is shared.  All sums are fp32 in an order fixed by the shape: results
+// are the same bits every call.
 //
-// What it takes now: the loss 13.9 us at T = 8192, E = 896 (two kernels; 2.3 us of bytes) and 36 at
-// T = 16384, E = 4096 (19.9 of bytes; bound by the instructions of a row), the gradient 12.3 us at
-// T = 8192, E = 896 (4.5 of bytes).
+// What it takes now: the loss 14.2 us at T = 8192, E = 896 (two kernels; 2.3 us of bytes) and 37 at
+// T = 16384, E = 4096 (19.9 of bytes; 71% of the issue slots), the gradient 12.2 us at T = 8192,
+// E = 896 (4.5 of bytes; half of the slots, the rest is the first rows' way in).
 //
 // Partial column sums: CTA b of the first kernel and sequence i meet in at most one stretch of
 // tokens; it writes its sums to slot b + i (a monotone walk through (b, i): no two stretches
@@ -265,11 +266,9 @@ __device__ __forceinline__ float warp_max(float v) {
   return r;
 }
 
-// Groups of W warps in a CTA.  A group of several warps has a hardware barrier of its own, of
-// which there are 15 beside the CTA's.
-__host__ __device__ constexpr int groups_of(int W) {
-  return W > 1 && kBalWarps / W > 15 ? 15 : kBalWarps / W;
-}
+// Groups of W warps in a CTA.  A group of several warps (8 groups at most) has a hardware barrier of
+// its own beside the CTA's.
+__host__ __device__ constexpr int groups_of(int W) { return kBalWarps / W; }
 
 // A sigmoid (of 7.6) from which 1 - s is not taken as it stands: what s was rounded by, 2^-24, would
 // be 2^-13 of the difference and more, until at a logit of 17 nothing is left of it.
@@ -312,9 +311,9 @@ __device__ __forceinline__ void sigmoids(float (&x)[NC], const Extremes& ext) {
 // (Two values per instruction, .f32x2, was tried: packing the exponentials cost what it saved.)
 template <int NC, bool kSoftmax, bool kDot>
 __device__ __forceinline__ void row_terms(float (&x)[NC], const Extremes& ext,
-                                          const float (&g)[kDot ? NC : 1], unsigned past, int W, int grp, int gw, float4* xchg,
-                                          int buf, float& scale, float& dot, float& top,
-                                          float& inv) {
+                                          const float (&g)[kDot ? NC : 1], unsigned past, int W,
+                                          int grp, int gw, float4* xchg, int buf, float& scale,
+                                          float& dot, float& top, float& inv) {
   float m = 0.0f;
   if constexpr (kSoftmax) {
     float m0 = kLowest, m1 = kLowest;
@@ -519,7 +518,8 @@ __global__ void __launch_bounds__(kBalThreads, 1) mrs_balance_rows_kernel(const 
 
 // Joins the slots: CTA (bx, by) takes 32 experts of the sequences by, by + gridDim.y, ...; warp w
 // the slots w, w + 8, ... of a sequence.  The last CTA to finish adds the loss.  (In fp64 its few
-// divisions took 4 us; the terms are all of one sign, so fp32 loses nothing that shows.)
+// divisions took 4 us.  Its terms are all of one sign, and a thread's sum over sequences is
+// compensated: against 64 bits the losses of T = 64 to 16384 measured within 2e-7.)
 __global__ void __launch_bounds__(kJoinThreads) mrs_balance_join_kernel(const BalanceArgs a) {
   constexpr int kWarps = kJoinThreads / 32;
   __shared__ float ps[2][kWarps][32];
@@ -790,9 +790,9 @@ namespace {
 
 // Warps per row, columns per lane and the kind of loads for E experts.  16-byte loads need rows
 // that start on 16 bytes (E a multiple of 8); without them a lane's next row is in registers, and
-// more than 16 columns would not fit there.  (The kernels are bound by the instructions they
-// issue, a third of them per row and not per column: twice the warps with half the columns took
-// T = 16384, E = 4096 from 45 to 50 us.)
+// more than 16 columns would not fit there.  (The widest calls fill 71% of the issue slots, a third
+// of them per row and not per column: twice the warps with half the columns took T = 16384, E = 4096
+// from 45 to 50 us.)
 struct RowPlan {
   int W, NC;
   bool vec;

@@ -662,10 +662,12 @@ cudaError_t launch_experts(const CUtensorMap& wmap, const ExpertsArgs& a, int gr
 // blocks, or with windows one per 128 routes and expert.  An SM's time for a tile goes by the bytes
 // it takes in, its rows and BN weights, so the width is the one with the smallest product of rounds
 // and bytes.  Rows of at most half a ring's steps stay for several tiles once every SM has work for
-// eight rounds without that.  Tiles of 256 outputs leave room for one accumulator, so that a tile is
-// stored before the next one's products; they are for rows that do not stay, whose copies cover
-// most of that (T = 8192, E = 64, outs = 2048, us with and without them: 83 63 at 512 columns,
-// 101 119 at 768, 118 140 at 1024, 182 223 at 2048).
+// eight rounds without that (us with and without: T = 8192, E = 896, 384 -> 3584 307 505; T = 2048
+// 149 243; T = 3000, E = 700, 256 -> 640 48 65; T = 2048, E = 64, 384 -> 3584 42 51.  Four rounds,
+// where eight leave one or two tiles a unit: T = 1000, E = 128, 512 -> 2048 26 for 31).  Tiles of 256
+// outputs leave room for one accumulator, so that a tile is stored before the next one's products;
+// they are for rows that do not stay, whose copies cover most of that (T = 8192, E = 64, outs = 2048,
+// us with and without them: 83 63 at 512 columns, 101 119 at 768, 118 140 at 1024, 182 223 at 2048).
 struct ExpertsPlan {
   int group, span, subs;
   int bn, ntile, chunk, nchunk, ksteps;

@@ -28,6 +28,7 @@ def main(argv=None) -> int:
     p.add_argument("--gate-hidden", type=int, default=None,
                    help="run moe_gate_route_sort with this hidden size (gate GEMV ahead)")
     p.add_argument("--operator", choices=("loss", "backward", "quantize", "experts"))
+    p.add_argument("--softmax", action="store_true", help="loss and backward of softmax scores")
     p.add_argument("--cols", type=int, default=3584, help="row length of quantize and experts")
     p.add_argument("--outs", type=int, default=768, help="output width of experts")
     args = p.parse_args(argv)
@@ -74,7 +75,7 @@ def _operator(args, w, r, logits) -> None:
     from . import experts, training
 
     buf = training.BalanceBuffers.allocate(w.T, w.E, 1, device="cuda")
-    training.balance_loss(logits, r.topk_ids, 0.01, out=buf)
+    training.balance_loss(logits, r.topk_ids, 0.01, args.softmax, out=buf)
     grad = torch.empty_like(logits)
     upstream = torch.randn(w.T, w.topk, device="cuda")
     one = torch.ones(1, device="cuda")
@@ -92,10 +93,10 @@ def _operator(args, w, r, logits) -> None:
                          dtype=torch.uint8, device="cuda")
     for _ in range(args.calls):
         if args.operator == "loss":
-            training.balance_loss(logits, r.topk_ids, 0.01, out=buf)
+            training.balance_loss(logits, r.topk_ids, 0.01, args.softmax, out=buf)
         elif args.operator == "backward":
-            training.route_backward(logits, r.topk_ids, upstream, w.routed_scale, grad_loss=one,
-                                    counts=buf.counts, coef=0.01, out=grad)
+            training.route_backward(logits, r.topk_ids, upstream, w.routed_scale, args.softmax,
+                                    one, buf.counts, 0.01, out=grad)
         elif args.operator == "quantize":
             experts.mxfp4_quantize(x, out=rows)
         else:
