@@ -318,3 +318,94 @@ def test_the_loss_gradient_of_an_almost_even_router(E, K, softmax):
     none = mrs.route_backward(logits, ids, softmax=softmax, grad_loss=torch.ones(1, device=DEV),
                               counts=even, coef=0.5, dtype=torch.float32)
     assert none.abs().max().item() <= 2.0 ** -20 * 0.5 / T
+
+
+@pytest.mark.parametrize("softmax", [False, True])
+@pytest.mark.parametrize("E", [4096, 4095])
+def test_router_rows_past_32_bit_offsets(E, softmax):
+    # more than 2^31 logits: the last sequence against the same tokens in a call of their own (the
+    # CTAs' ranges differ, and with them the order of the column sums)
+    T, K, n = 525_000, 4, 1000
+    logits = torch.zeros(T, E, dtype=torch.bfloat16, device=DEV)
+    last, ids = _router(n, E, K)
+    logits[-n:] = last
+    all_ids = torch.zeros(T, K, dtype=torch.int32, device=DEV)
+    all_ids[-n:] = ids
+    off = torch.tensor([0, T - n, T], dtype=torch.int32, device=DEV)
+    big = mrs.balance_loss(logits, all_ids, 1.0, softmax=softmax, seq_offsets=off)
+    one = mrs.balance_loss(last, ids, 1.0, softmax=softmax)
+    assert torch.equal(big.counts[1], one.counts[0]) and int(big.counts[0, 0]) == (T - n) * K
+    assert torch.all((big.mean_probs[1] - one.mean_probs[0]).abs() <= 2.0 ** -18 * one.mean_probs[0])
+    assert (big.mean_probs[0].double() * E - 1).abs().max().item() <= 2.0 ** -16
+    gw = torch.randn(n, K, device=DEV)
+    all_gw = torch.zeros(T, K, device=DEV)
+    all_gw[-n:] = gw
+    gl = torch.ones(1, device=DEV)
+    grad = mrs.route_backward(logits, all_ids, all_gw, 2.5, softmax, gl, big.counts, 1.0, off)
+    # (two sequences: half the coefficient for each; 0.5 is exact)
+    want = mrs.route_backward(last, ids, gw, 2.5, softmax, gl, one.counts, 0.5)
+    assert torch.equal(grad[-n:], want)
+    assert torch.isfinite(grad[0].float()).all()
+
+
+def test_products_past_32_bit_offsets():
+    # outputs of more than 2^31 elements, and weights of more than 2^32 bytes: rows of the last
+    # experts against a call that holds those alone
+    T, E, K, cols, N, B = 33000, 8, 4, 32, 16400, 64
+    x, w, lists = _layer(T, E, K, cols, N, B)
+    out = mrs.experts_mxfp4(x, w, T, K, B, *lists)
+    xs, part = mrs.mxfp4_dequantize(x), slice(T - 5, T)
+    ids = torch.rand(T, E, generator=torch.Generator().manual_seed(0)).topk(K, dim=1).indices
+    wv = mrs.mxfp4_dequantize(w)[ids[part].to(DEV)].double()  # [5, K, N, cols]
+    want = torch.einsum("tc,tknc->tkn", xs[part].double(), wv)
+    mag = torch.einsum("tc,tknc->tkn", xs[part].double().abs(), wv.abs())
+    got = out.view(T, K, N)[part].double()
+    tol = cols * 2.0 ** -23 * mag
+    assert torch.all((got - want).abs() <= tol + 2.0 ** -8 * (want.abs() + tol) + 1e-38)
+    del out
+    T, E, K, cols, N, B = 40, 1100, 1, 4096, 2048, 16
+    codes = torch.randint(0, 256, (E, N, cols // 2), dtype=torch.uint8, device=DEV)
+    scales = torch.randint(118, 128, (E, N, cols // 32), dtype=torch.uint8, device=DEV)
+    assert codes.numel() > 1 << 32
+    x = mrs.mxfp4_quantize(torch.randn(T, cols, device=DEV))
+    m = mrs.RouteSortBuffers.allocate(T, E, K, B, device=DEV)
+
+    def call(ids, w, E):
+        mrs.moe_sort(ids, torch.ones(T, K, device=DEV), E, B, m.sorted_token_ids, m.sorted_weights,
+                     m.expert_ids, m.num_tokens_post_pad, m.workspace)
+        return mrs.experts_mxfp4(x, w, T, K, B, m.sorted_token_ids, m.expert_ids,
+                                 m.num_tokens_post_pad)
+
+    ids = (torch.arange(T, device=DEV)[:, None] % 4).int()
+    few = mrs.Mxfp4Rows(codes[-4:].clone(), scales[-4:].clone())
+    want = call(ids, few, 4)
+    assert torch.equal(call(ids + (E - 4), mrs.Mxfp4Rows(codes, scales), E), want)
+
+
+def test_buffers_that_start_between_vectors():
+    # 4-byte alignment is all that counts, ids, gradients and weights' scales have to have
+    T, E, K = 70, 256, 8
+    logits, ids = _router(T, E, K)
+    gw, gl = torch.randn(T, K, device=DEV), torch.ones(1, device=DEV)
+    off = torch.tensor([0, 30, T], dtype=torch.int32, device=DEV)
+
+    def shifted(t):
+        room = torch.zeros(t.numel() + 1, dtype=t.dtype, device=DEV)
+        room[1:] = t.flatten()
+        return room[1:].view(t.shape)
+
+    loss = mrs.balance_loss(logits, ids, 0.5, seq_offsets=off)
+    got = [shifted(torch.zeros_like(t)) for t in (loss.loss, loss.counts, loss.mean_probs)]
+    mrs.moe_balance_loss(logits, shifted(ids), shifted(off), False, 0.5, *got, loss.workspace)
+    assert all(torch.equal(a, b) for a, b in zip(got, (loss.loss, loss.counts, loss.mean_probs)))
+    want = mrs.route_backward(logits, ids, gw, 2.5, False, gl, loss.counts, 0.5, off)
+    grad = mrs.route_backward(logits, shifted(ids), shifted(gw), 2.5, False, shifted(gl), got[1], 0.5,
+                              shifted(off))
+    assert torch.equal(grad, want)
+    T, E, K, cols, N, B = 20, 4, 2, 512, 136, 16
+    x, w, lists = _layer(T, E, K, cols, N, B)
+    room = torch.zeros(w.scales.numel() + 4, dtype=torch.uint8, device=DEV)
+    room[4:] = w.scales.flatten()
+    moved = mrs.Mxfp4Rows(w.codes, room[4:].view(w.scales.shape))
+    assert torch.equal(mrs.experts_mxfp4(x, moved, T, K, B, *lists),
+                       mrs.experts_mxfp4(x, w, T, K, B, *lists))
