@@ -246,6 +246,7 @@ int moe_route_sort_from_host(const void* logits_host, void* logits_dev, const fl
 #define MOE_RS_BF16 0
 #define MOE_RS_FP16 1
 #define MOE_RS_FP32 2
+#define MOE_RS_FP8 3   /* e4m3: values up to 448, no infinities */
 
 /* Most sequences of one call. */
 #define MOE_RS_MAX_SEQUENCES 65536
@@ -375,8 +376,83 @@ int moe_experts_mxfp4(const uint8_t* x_codes, const uint8_t* x_scales, int x_per
 int moe_experts_mxfp4_plan(int T, int E, int topk, int cols, int outs, int block_m, int sms,
                            int32_t* plan);
 
-/* One of the five operations above with its arguments as an array, for language bindings that pay
- * per argument.  args: 8-byte values (8-byte aligned host memory): the operation's number, the
+/* --------------------------------------- between two routings: norm, gated activation, 8 bits */
+
+/* Longest rows of the operations on rows below; their length is a multiple of 8. */
+#define MOE_RS_ROWS_MAX_COLS 16384
+
+/* Rows in 8 bits: e4m3 codes [rows, cols] (8-byte aligned) and one fp32 scale a row, a value being
+ * code * scale.  The scale is the row's largest magnitude / 448, at least 2^-126; a row that holds
+ * an infinity or a NaN has a NaN for its scale and codes of zero.  Codes are the nearest of
+ * value / scale, ties to the even code (one rounding of 2^-24 ahead of it).
+ * moe_fp8_quantize makes them of `rows` rows of x (x_dtype MOE_RS_BF16, MOE_RS_FP16 or MOE_RS_FP32),
+ * x_stride elements apart, each row 16-byte aligned; weights are quantised by the same call, once.
+ * Errors: MOE_RS_ERR_BAD_DTYPE, _BAD_ROWS, _BAD_COLS, _OVERFLOW, _NULL_POINTER, _MISALIGNED, _ALIAS,
+ * _LAUNCH. */
+int moe_fp8_quantize(const void* x, int x_dtype, int64_t rows, int cols, int64_t x_stride,
+                     uint8_t* codes, float* scales, cudaStream_t stream);
+
+/* Root-mean-square norm of the residual plus the sum of a token's `parts` rows (1 to 32: a row for
+ * each of its experts, as the products leave them).  For each of `rows` tokens t:
+ *   s    = round(residual[t] + x[t * parts] + ... + x[t * parts + parts - 1])
+ *   rstd = 1 / sqrt(mean over c of s^2 + eps),   y[c] = s[c] * gain[c] * rstd
+ * Sums are fp32, in this order; s is rounded to `dtype` (MOE_RS_BF16 or MOE_RS_FP16: that of x,
+ * residual, y and sum) and the norm is that of the rounded s.  gain [cols]: `dtype` or MOE_RS_FP32.
+ * residual may be NULL (none).  Outputs, each of which may be NULL, but not all: y [rows, cols];
+ * sum [rows, cols] = s; codes and scales (together) = y in 8 bits, made from the fp32 y; rstd [rows]
+ * fp32.  sum may be the residual itself (dense, the same address): the residual stream is then
+ * updated in place.  x and residual: x_stride and residual_stride elements between rows (>= cols,
+ * multiples of 8), 16-byte aligned; the outputs are dense.  The sum of squares is an fp32 number.
+ * eps: in [0, 1] (MOE_RS_ERR_BAD_SCALE); parts outside its range is MOE_RS_ERR_BAD_TOPK.  Other
+ * errors as for moe_fp8_quantize.  No counterpart in the source pages. */
+int moe_rms_norm(const void* x, int dtype, int64_t x_stride, int parts, const void* residual,
+                 int64_t residual_stride, int64_t rows, int cols, const void* gain, int gain_dtype,
+                 float eps, void* y, void* sum, uint8_t* codes, float* scales, float* rstd,
+                 cudaStream_t stream);
+
+/* Bytes of device workspace that moe_rms_norm_backward needs for grad_gain (16-byte aligned, any
+ * contents).  One workspace must not be used by two calls that can run at the same time.  0 for
+ * invalid cols. */
+size_t moe_rms_norm_backward_workspace_bytes(int cols);
+
+/* Gradient of moe_rms_norm.  s (its sum), gain and rstd are those of the forward call;
+ * d = grad[t] + grad_rows[t * parts] + ... is the gradient of y: one row a token (for example the
+ * router's), `parts` rows a token (the experts'), or both; either may be NULL, not both.
+ * grad_sum [rows, cols]: the gradient that reaches s by itself (the residual stream's), or NULL.
+ *   xh = s * rstd,  g = d * gain,
+ *   grad_x[t] = rstd * (g - xh * mean over c of g * xh) + grad_sum[t]
+ *   grad_gain[c] = sum over t of d * xh
+ * grad_x [rows, cols] of type `dtype` (rounded once) is the gradient of the residual and of each of
+ * the token's rows of x; grad_gain [cols] fp32, or NULL (then no workspace is needed either).
+ * Everything dense and 16-byte aligned (rstd and grad_gain: 4).  The order of the sums is fixed.
+ * Errors as for moe_rms_norm, and MOE_RS_ERR_WORKSPACE. */
+int moe_rms_norm_backward(const void* s, int dtype, const void* gain, int gain_dtype,
+                          const float* rstd, const void* grad, const void* grad_rows, int parts,
+                          const void* grad_sum, int64_t rows, int cols, void* grad_x,
+                          float* grad_gain, void* workspace, size_t workspace_bytes,
+                          cudaStream_t stream);
+
+/* Gated activation between the experts' two products, times the routing weight.  Row r of x
+ * [rows, 2 * cols] (x_stride elements between rows, >= 2 * cols, a multiple of 8) holds a =
+ * x[r, c] and b = x[r, cols + c]:
+ *   y[r, c] = weights[r] * a * sigmoid(a) * b
+ * weights [rows] fp32 (topk_weights, in route order), or NULL: 1.  y [rows, cols] of type dtype
+ * (MOE_RS_BF16 or MOE_RS_FP16, that of x), codes and scales the same in 8 bits (from the fp32
+ * value); y may be NULL, codes and scales too, not both.  Finite a and b whose product is finite
+ * give what is written; infinities and NaN what fp32 arithmetic makes of them.
+ * Errors as for moe_fp8_quantize.  No counterpart in the source pages. */
+int moe_swiglu(const void* x, int dtype, int64_t x_stride, int64_t rows, int cols,
+               const float* weights, void* y, uint8_t* codes, float* scales, cudaStream_t stream);
+
+/* Its gradient: grad [rows, cols] to grad_x [rows, 2 * cols], both of type dtype and dense, and
+ * grad_weights [rows] fp32 (or NULL): sum over c of grad * a * sigmoid(a) * b, the grad_weights
+ * that moe_route_backward takes. */
+int moe_swiglu_backward(const void* grad, const void* x, int dtype, int64_t x_stride, int64_t rows,
+                        int cols, const float* weights, void* grad_x, float* grad_weights,
+                        cudaStream_t stream);
+
+/* One of the operations that have a number below with its arguments as an array, for language
+ * bindings that pay per argument.  args: 8-byte values (8-byte aligned host memory): the operation's number, the
  * number of its arguments, then the arguments in the order of its declaration -- pointers, the
  * stream and integers as int64, floats as double.  Returns what the operation returns, or
  * MOE_RS_ERR_BAD_CALL, MOE_RS_ERR_OVERFLOW for an integer outside its type, MOE_RS_ERR_NULL_POINTER
@@ -386,6 +462,11 @@ int moe_experts_mxfp4_plan(int T, int E, int topk, int cols, int outs, int block
 #define MOE_RS_CALL_MXFP4_QUANTIZE 3
 #define MOE_RS_CALL_MXFP4_DEQUANTIZE 4
 #define MOE_RS_CALL_EXPERTS_MXFP4 5
+#define MOE_RS_CALL_FP8_QUANTIZE 6
+#define MOE_RS_CALL_RMS_NORM 7
+#define MOE_RS_CALL_RMS_NORM_BACKWARD 8
+#define MOE_RS_CALL_SWIGLU 9
+#define MOE_RS_CALL_SWIGLU_BACKWARD 10
 int moe_call_packed(const void* args);
 
 /* ------------------------------------------------------- allocation-free variant */

@@ -55,6 +55,22 @@ from .experts import (  # noqa: F401
     mxfp4_dequantize,
     mxfp4_quantize,
 )
+from .rows import (  # noqa: F401
+    Fp8Rows,
+    NormBuffers,
+    NormGrads,
+    fp8_quantize,
+    moe_fp8_quantize,
+    moe_rms_norm,
+    moe_rms_norm_backward,
+    moe_rms_norm_backward_workspace_bytes,
+    moe_swiglu,
+    moe_swiglu_backward,
+    rms_norm,
+    rms_norm_backward,
+    swiglu,
+    swiglu_backward,
+)
 from .training import (  # noqa: F401
     BalanceBuffers,
     balance_loss,

@@ -106,6 +106,18 @@ def load() -> ctypes.CDLL:
         lib.moe_experts_mxfp4_status.restype = I
         lib.moe_experts_mxfp4_plan.argtypes = [I] * 7 + [ctypes.POINTER(ctypes.c_int32)]
         lib.moe_experts_mxfp4_plan.restype = I
+        lib.moe_fp8_quantize.argtypes = [P, I, L, I, L, P, P, P]
+        lib.moe_fp8_quantize.restype = I
+        lib.moe_rms_norm.argtypes = [P, I, L, I, P, L, L, I, P, I, F, P, P, P, P, P, P]
+        lib.moe_rms_norm.restype = I
+        lib.moe_rms_norm_backward_workspace_bytes.argtypes = [I]
+        lib.moe_rms_norm_backward_workspace_bytes.restype = S
+        lib.moe_rms_norm_backward.argtypes = [P, I, P, I, P, P, P, I, P, L, I, P, P, P, S, P]
+        lib.moe_rms_norm_backward.restype = I
+        lib.moe_swiglu.argtypes = [P, I, L, L, I, P, P, P, P, P]
+        lib.moe_swiglu.restype = I
+        lib.moe_swiglu_backward.argtypes = [P, P, I, L, L, I, P, P, P, P]
+        lib.moe_swiglu_backward.restype = I
         lib.moe_call_packed.argtypes = [ctypes.c_char_p]
         lib.moe_call_packed.restype = I
         _lib = lib

@@ -1,0 +1,282 @@
+// mrs_gated.cu -- the gated activation between two experts' products, its gradient, and rows to
+// 8 bits.
+//
+// Per row r, over c < cols, a = x[r, c], b = x[r, cols + c], w = weights[r] (1 without weights):
+//   y[r, c] = w * a * sig(a) * b                        to 16 bits, or to e4m3 with the row's scale
+// and its gradient, d = grad[r, c]:
+//   grad_a = w d b sig(a) (1 + a (1 - sig(a))),   grad_b = w d a sig(a)
+//   grad_w = sum over c of d a sig(a) b
+// All in fp32, one rounding at the end.  The routing weight belongs here in training: the second
+// product is then a plain one, and its gradients need no weights.  1 - sig(a) is sig(-a), which
+// keeps its bits where sig(a) is next to 1.
+//
+// Bound by memory: one read of every input, one write of every output.
+#include "mrs_rows.cuh"
+
+namespace mrs {
+
+struct GatedArgs {
+  const void* x;
+  const void* grad;       // of the gradient: [rows, cols]
+  const float* weights;   // or null
+  size_t x_stride;
+  int64_t rows;
+  int vecs, tpr, per_cta;
+  void* y;                // [rows, cols]; of the gradient [rows, 2 cols]
+  unsigned char* codes;
+  float* scales;
+  float* grad_weights;    // or null
+};
+
+// sig(a) and sig(-a).
+__device__ __forceinline__ void sigmoids(float a, float& up, float& down) {
+  const float e = __expf(-fabsf(a));  // in (0, 1]
+  const float big = __fdividef(1.0f, 1.0f + e), small = e * big;
+  up = a >= 0.0f ? big : small;
+  down = a >= 0.0f ? small : big;
+}
+
+template <class T, int kVec>
+__global__ void __launch_bounds__(kRowThreads<kVec>) mrs_gated_kernel(const GatedArgs a) {
+  __shared__ RowTotals meet[32];
+  pdl_trigger();
+  const int tid = threadIdx.x, in_cta = tid / a.tpr, place = tid - in_cta * a.tpr;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * a.per_cta + in_cta;
+  const bool live = row < a.rows;
+  const size_t cols = 8 * static_cast<size_t>(a.vecs);
+  pdl_wait();
+  const float w = live && a.weights != nullptr ? __ldg(a.weights + row) : 1.0f;
+  const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
+  float v[kVec][8];
+  uint32_t top = 0u;
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) {
+    const int at = i * a.tpr + place;
+    if (!live || at >= a.vecs) continue;
+    float b[8];
+    unpack8<T>(load8<T>(x, 8 * static_cast<size_t>(at)), v[i]);
+    unpack8<T>(load8<T>(x, cols + 8 * at), b);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      float up, down;
+      sigmoids(v[i][k], up, down);
+      v[i][k] = w * (v[i][k] * up * b[k]);
+      top = max(top, magnitude(v[i][k]));
+    }
+    if (a.y != nullptr)
+      *reinterpret_cast<uint4*>(static_cast<T*>(a.y) + row * cols + 8 * at) = pack8<T>(v[i]);
+  }
+  if (a.codes == nullptr) return;
+  const float scale = fp8_scale(row_totals(0.0f, top, a.tpr, meet).top);
+  const float inv = fp8_inverse(scale);
+  if (!live) return;
+  if (place == 0) a.scales[row] = scale;
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) {
+    const int at = i * a.tpr + place;
+    if (at < a.vecs)
+      *reinterpret_cast<uint2*>(a.codes + row * cols + 8 * at) = fp8_codes(v[i], inv);
+  }
+}
+
+template <class T, int kVec>
+__global__ void __launch_bounds__(kRowThreads<kVec>) mrs_gated_grad_kernel(const GatedArgs a) {
+  __shared__ RowTotals meet[32];
+  pdl_trigger();
+  const int tid = threadIdx.x, in_cta = tid / a.tpr, place = tid - in_cta * a.tpr;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * a.per_cta + in_cta;
+  const bool live = row < a.rows;
+  const size_t cols = 8 * static_cast<size_t>(a.vecs);
+  pdl_wait();
+  const float w = live && a.weights != nullptr ? __ldg(a.weights + row) : 1.0f;
+  const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
+  T* out = static_cast<T*>(a.y) + row * 2 * cols;
+  float dot = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) {
+    const int at = i * a.tpr + place;
+    if (!live || at >= a.vecs) continue;
+    float g[8], b[8], d[8], ga[8], gb[8];
+    unpack8<T>(load8<T>(x, 8 * static_cast<size_t>(at)), g);
+    unpack8<T>(load8<T>(x, cols + 8 * at), b);
+    unpack8<T>(load8<T>(a.grad, row * cols + 8 * at), d);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      float up, down;
+      sigmoids(g[k], up, down);
+      const float act = g[k] * up;
+      dot += d[k] * act * b[k];
+      ga[k] = w * d[k] * b[k] * (up * (1.0f + g[k] * down));
+      gb[k] = w * d[k] * act;
+    }
+    *reinterpret_cast<uint4*>(out + 8 * at) = pack8<T>(ga);
+    *reinterpret_cast<uint4*>(out + cols + 8 * at) = pack8<T>(gb);
+  }
+  if (a.grad_weights == nullptr) return;
+  const float sum = row_totals(dot, 0u, a.tpr, meet).sum;
+  if (live && place == 0) a.grad_weights[row] = sum;
+}
+
+// Rows of bf16, fp16 or fp32 to 8 bits.
+template <class T, int kVec>
+__global__ void __launch_bounds__(kRowThreads<kVec>) mrs_fp8_quantize_kernel(const GatedArgs a) {
+  __shared__ RowTotals meet[32];
+  pdl_trigger();
+  const int tid = threadIdx.x, in_cta = tid / a.tpr, place = tid - in_cta * a.tpr;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * a.per_cta + in_cta;
+  const bool live = row < a.rows;
+  const size_t cols = 8 * static_cast<size_t>(a.vecs);
+  pdl_wait();
+  const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
+  float v[kVec][8];
+  uint32_t top = 0u;
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) {
+    const int at = i * a.tpr + place;
+    if (!live || at >= a.vecs) continue;
+    if constexpr (sizeof(T) == 4)
+      load_columns<__half>(x, true, at, v[i]);
+    else
+      unpack8<T>(load8<T>(x, 8 * static_cast<size_t>(at)), v[i]);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) top = max(top, magnitude(v[i][k]));
+  }
+  const float scale = fp8_scale(row_totals(0.0f, top, a.tpr, meet).top);
+  const float inv = fp8_inverse(scale);
+  if (!live) return;
+  if (place == 0) a.scales[row] = scale;
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) {
+    const int at = i * a.tpr + place;
+    if (at < a.vecs)
+      *reinterpret_cast<uint2*>(a.codes + row * cols + 8 * at) = fp8_codes(v[i], inv);
+  }
+}
+
+namespace {
+
+enum class GatedKind { kForward, kGradient, kQuantize };
+
+template <class T, int kVec, GatedKind kKind>
+auto* gated_kernel() {
+  if constexpr (kKind == GatedKind::kForward) return mrs_gated_kernel<T, kVec>;
+  else if constexpr (kKind == GatedKind::kGradient) return mrs_gated_grad_kernel<T, kVec>;
+  else return mrs_fp8_quantize_kernel<T, kVec>;
+}
+
+template <class T, GatedKind kKind>
+cudaError_t launch_gated(const GatedArgs& a, const RowPlan& p, cudaStream_t st) {
+  const dim3 grid(static_cast<unsigned>((a.rows + p.rows - 1) / p.rows)), block(p.threads);
+  switch (p.vec) {
+    case 1: return launch_pdl(gated_kernel<T, 1, kKind>(), grid, block, 0, st, a);
+    case 2: return launch_pdl(gated_kernel<T, 2, kKind>(), grid, block, 0, st, a);
+    case 3: return launch_pdl(gated_kernel<T, 3, kKind>(), grid, block, 0, st, a);
+    default: return launch_pdl(gated_kernel<T, 4, kKind>(), grid, block, 0, st, a);
+  }
+}
+
+// Checks of `rows` rows of `width` elements of `size` bytes, `stride` elements apart.
+int check_gated(const void* x, int64_t x_stride, int64_t rows, int cols, int width, size_t size) {
+  if (rows < 0) return MOE_RS_ERR_BAD_ROWS;
+  if (cols < 8 || cols > kRowMaxCols || cols % 8 != 0 || x_stride < width)
+    return MOE_RS_ERR_BAD_COLS;
+  if (rows > INT32_MAX || x_stride > (int64_t{1} << 31)) return MOE_RS_ERR_OVERFLOW;
+  if (rows == 0) return MOE_RS_OK;
+  if (!x) return MOE_RS_ERR_NULL_POINTER;
+  if (!aligned(x, 16) || static_cast<size_t>(x_stride) * size % 16 != 0)
+    return MOE_RS_ERR_MISALIGNED;
+  return MOE_RS_OK;
+}
+
+GatedArgs gated_args(const void* x, int64_t x_stride, int64_t rows, int cols, const RowPlan& p) {
+  GatedArgs a{};
+  a.x = x;
+  a.x_stride = static_cast<size_t>(x_stride);
+  a.rows = rows;
+  a.vecs = cols / 8;
+  a.tpr = p.tpr;
+  a.per_cta = p.rows;
+  return a;
+}
+
+}  // namespace
+}  // namespace mrs
+
+using namespace mrs;
+
+extern "C" {
+
+int moe_swiglu(const void* x, int dtype, int64_t x_stride, int64_t rows, int cols,
+               const float* weights, void* y, uint8_t* codes, float* scales, cudaStream_t stream) {
+  if (dtype != MOE_RS_BF16 && dtype != MOE_RS_FP16) return MOE_RS_ERR_BAD_DTYPE;
+  const int rc = check_gated(x, x_stride, rows, cols, 2 * cols, 2);
+  if (rc || rows == 0) return rc;
+  if ((!y && !codes) || (codes == nullptr) != (scales == nullptr)) return MOE_RS_ERR_NULL_POINTER;
+  if (!aligned(weights, 4) || !aligned(y, 16) || !aligned(codes, 8) || !aligned(scales, 4))
+    return MOE_RS_ERR_MISALIGNED;
+  const size_t n = static_cast<size_t>(rows) * cols, r = static_cast<size_t>(rows);
+  const Span outs[] = {span(y, y ? 2 * n : 0), span(codes, codes ? n : 0),
+                       span(scales, scales ? 4 * r : 0)};
+  const Span ins[] = {rows_span(x, rows, 2 * cols, x_stride, 2), span(weights, weights ? 4 * r : 0)};
+  if (any_alias(outs, 3, ins, 2)) return MOE_RS_ERR_ALIAS;
+  const RowPlan p = row_plan(cols, 1);
+  GatedArgs a = gated_args(x, x_stride, rows, cols, p);
+  a.weights = weights;
+  a.y = y;
+  a.codes = codes;
+  a.scales = scales;
+  return launch_status(dtype == MOE_RS_BF16
+                           ? launch_gated<__nv_bfloat16, GatedKind::kForward>(a, p, stream)
+                           : launch_gated<__half, GatedKind::kForward>(a, p, stream));
+}
+
+int moe_swiglu_backward(const void* grad, const void* x, int dtype, int64_t x_stride, int64_t rows,
+                        int cols, const float* weights, void* grad_x, float* grad_weights,
+                        cudaStream_t stream) {
+  if (dtype != MOE_RS_BF16 && dtype != MOE_RS_FP16) return MOE_RS_ERR_BAD_DTYPE;
+  const int rc = check_gated(x, x_stride, rows, cols, 2 * cols, 2);
+  if (rc || rows == 0) return rc;
+  if (!grad || !grad_x) return MOE_RS_ERR_NULL_POINTER;
+  if (!aligned(grad, 16) || !aligned(weights, 4) || !aligned(grad_x, 16) ||
+      !aligned(grad_weights, 4))
+    return MOE_RS_ERR_MISALIGNED;
+  const size_t n = static_cast<size_t>(rows) * cols, r = static_cast<size_t>(rows);
+  const Span outs[] = {span(grad_x, 4 * n), span(grad_weights, grad_weights ? 4 * r : 0)};
+  const Span ins[] = {span(grad, 2 * n), rows_span(x, rows, 2 * cols, x_stride, 2),
+                      span(weights, weights ? 4 * r : 0)};
+  if (any_alias(outs, 2, ins, 3)) return MOE_RS_ERR_ALIAS;
+  const RowPlan p = row_plan(cols, 1);
+  GatedArgs a = gated_args(x, x_stride, rows, cols, p);
+  a.grad = grad;
+  a.weights = weights;
+  a.y = grad_x;
+  a.grad_weights = grad_weights;
+  return launch_status(dtype == MOE_RS_BF16
+                           ? launch_gated<__nv_bfloat16, GatedKind::kGradient>(a, p, stream)
+                           : launch_gated<__half, GatedKind::kGradient>(a, p, stream));
+}
+
+int moe_fp8_quantize(const void* x, int x_dtype, int64_t rows, int cols, int64_t x_stride,
+                     uint8_t* codes, float* scales, cudaStream_t stream) {
+  if (x_dtype != MOE_RS_BF16 && x_dtype != MOE_RS_FP16 && x_dtype != MOE_RS_FP32)
+    return MOE_RS_ERR_BAD_DTYPE;
+  const size_t size = x_dtype == MOE_RS_FP32 ? 4 : 2;
+  const int rc = check_gated(x, x_stride, rows, cols, cols, size);
+  if (rc || rows == 0) return rc;
+  if (!codes || !scales) return MOE_RS_ERR_NULL_POINTER;
+  if (!aligned(codes, 8) || !aligned(scales, 4)) return MOE_RS_ERR_MISALIGNED;
+  const Span outs[] = {span(codes, static_cast<size_t>(rows) * cols),
+                       span(scales, 4 * static_cast<size_t>(rows))};
+  const Span ins[] = {rows_span(x, rows, cols, x_stride, size)};
+  if (any_alias(outs, 2, ins, 1)) return MOE_RS_ERR_ALIAS;
+  const RowPlan p = row_plan(cols, 1);
+  GatedArgs a = gated_args(x, x_stride, rows, cols, p);
+  a.codes = codes;
+  a.scales = scales;
+  return launch_status(x_dtype == MOE_RS_FP32 ? launch_gated<float, GatedKind::kQuantize>(a, p, stream)
+                       : x_dtype == MOE_RS_FP16
+                           ? launch_gated<__half, GatedKind::kQuantize>(a, p, stream)
+                           : launch_gated<__nv_bfloat16, GatedKind::kQuantize>(a, p, stream));
+}
+
+}  // extern "C"

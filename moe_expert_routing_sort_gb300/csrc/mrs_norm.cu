@@ -1,0 +1,383 @@
+// mrs_norm.cu -- root-mean-square norm of the residual plus a token's expert rows, and its gradient.
+//
+// Per token t, over c < cols, with x rows t * parts + j of the experts' products:
+//   s[c]  = round16(residual[c] + x_0[c] + ... + x_{parts-1}[c])      sums in fp32, in this order
+//   rstd  = 1 / sqrt(mean of s^2 + eps)
+//   y[c]  = s[c] * gain[c] * rstd         to 16 bits, and / or to e4m3 with the row's scale
+// The norm is that of the rounded s, which is what the next layer and the gradient read.  The
+// 8-bit row is made from the fp32 y, not from its 16-bit rounding.  |y| is largest where |s * gain|
+// is, so the scale and rstd come from one reduction.
+//
+// Gradient, d = grad + grad_rows_0 + ... + grad_rows_{parts-1}, xh = s * rstd, g = d * gain:
+//   grad_x[c]    = rstd * (g - xh * mean of g * xh) + grad_sum[c]
+//   grad_gain[c] = sum over tokens of d * xh
+// grad_x is the gradient of the residual and of each of the token's rows.  A CTA keeps its columns'
+// sums in registers over its tokens (a block of 32 tokens at a time, so that sums stay short) and
+// leaves one row of partial sums; a second kernel adds these in a fixed order.
+#include "mrs_rows.cuh"
+
+namespace mrs {
+
+struct NormArgs {
+  const void *x, *residual, *gain;
+  size_t x_stride, residual_stride;
+  int64_t rows;
+  int parts, vecs, tpr, per_cta, gain_f32;
+  float eps, inv_cols;
+  void *y, *sum;
+  unsigned char* codes;
+  float *scales, *rstd;
+};
+
+template <class T, int kVec>
+__global__ void __launch_bounds__(kRowThreads<kVec>) mrs_norm_kernel(const NormArgs a) {
+  __shared__ RowTotals meet[32];
+  pdl_trigger();
+  const int tid = threadIdx.x, in_cta = tid / a.tpr, place = tid - in_cta * a.tpr;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * a.per_cta + in_cta;
+  const bool live = row < a.rows;
+  const size_t cols = 8 * static_cast<size_t>(a.vecs);
+  pdl_wait();
+  float v[kVec][8];
+  float squares = 0.0f;
+  uint32_t top = 0u;
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) {
+    const int at = i * a.tpr + place;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[i][k] = 0.0f;
+    if (!live || at >= a.vecs) continue;
+    if (a.residual != nullptr)
+      unpack8<T>(load8<T>(a.residual, row * a.residual_stride + 8 * at), v[i]);
+    const T* x = static_cast<const T*>(a.x) + static_cast<size_t>(row) * a.parts * a.x_stride + 8 * at;
+#pragma unroll 4
+    for (int j = 0; j < a.parts; ++j) {
+      float p[8];
+      unpack8<T>(load8<T>(x, j * a.x_stride), p);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[i][k] += p[k];
+    }
+    const uint4 s = pack8<T>(v[i]);
+    unpack8<T>(s, v[i]);
+    if (a.sum != nullptr)
+      *reinterpret_cast<uint4*>(static_cast<T*>(a.sum) + row * cols + 8 * at) = s;
+    float g[8];
+    load_columns<T>(a.gain, a.gain_f32 != 0, at, g);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      squares += v[i][k] * v[i][k];
+      v[i][k] *= g[k];
+      top = max(top, magnitude(v[i][k]));
+    }
+  }
+  const RowTotals r = row_totals(squares, top, a.tpr, meet);
+  const float rstd = __frsqrt_rn(r.sum * a.inv_cols + a.eps);
+  const float scale = fp8_scale(magnitude(__uint_as_float(r.top) * rstd));
+  const float inv = fp8_inverse(scale);
+  if (!live) return;
+  if (place == 0) {
+    if (a.rstd != nullptr) a.rstd[row] = rstd;
+    if (a.scales != nullptr) a.scales[row] = scale;
+  }
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) {
+    const int at = i * a.tpr + place;
+    if (at >= a.vecs) continue;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[i][k] *= rstd;
+    if (a.y != nullptr)
+      *reinterpret_cast<uint4*>(static_cast<T*>(a.y) + row * cols + 8 * at) = pack8<T>(v[i]);
+    if (a.codes != nullptr)
+      *reinterpret_cast<uint2*>(a.codes + row * cols + 8 * at) = fp8_codes(v[i], inv);
+  }
+}
+
+struct NormGradArgs {
+  const void *s, *gain, *grad, *grad_rows, *grad_sum;
+  const float* rstd;
+  int64_t rows;
+  int parts, vecs, tpr, per_cta, gain_f32;
+  float inv_cols;
+  void* grad_x;
+  float* partial;  // [CTAs * per_cta, cols], or null
+};
+
+constexpr int kNormSumRows = 32;
+
+template <class T, int kVec>
+__global__ void __launch_bounds__(kRowThreads<kVec>) mrs_norm_grad_kernel(const NormGradArgs a) {
+  __shared__ RowTotals meet[32];
+  pdl_trigger();
+  const int tid = threadIdx.x, in_cta = tid / a.tpr, place = tid - in_cta * a.tpr;
+  const size_t cols = 8 * static_cast<size_t>(a.vecs);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * a.per_cta;
+  pdl_wait();
+  float near[kVec][8], far[kVec][8];
+#pragma unroll
+  for (int i = 0; i < kVec; ++i)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) near[i][k] = far[i][k] = 0.0f;
+  int added = 0;
+  // (a CTA's rows take the same number of turns: they meet in the reduction)
+  for (int64_t first = static_cast<int64_t>(blockIdx.x) * a.per_cta; first < a.rows; first += step) {
+    const int64_t row = first + in_cta;
+    const bool live = row < a.rows;
+    const float rstd = live ? __ldg(a.rstd + row) : 0.0f;
+    float xh[kVec][8], g[kVec][8];
+    float dot = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      const int at = i * a.tpr + place;
+      if (!live || at >= a.vecs) continue;
+      const size_t here = row * cols + 8 * at;
+      unpack8<T>(load8<T>(a.s, here), xh[i]);
+      float d[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) d[k] = 0.0f;
+      if (a.grad != nullptr) unpack8<T>(load8<T>(a.grad, here), d);
+      if (a.grad_rows != nullptr) {
+        const T* p = static_cast<const T*>(a.grad_rows) + static_cast<size_t>(row) * a.parts * cols + 8 * at;
+#pragma unroll 4
+        for (int j = 0; j < a.parts; ++j) {
+          float q[8];
+          unpack8<T>(load8<T>(p, j * cols), q);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) d[k] += q[k];
+        }
+      }
+      load_columns<T>(a.gain, a.gain_f32 != 0, at, g[i]);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        xh[i][k] *= rstd;
+        near[i][k] += d[k] * xh[i][k];
+        g[i][k] *= d[k];
+        dot += g[i][k] * xh[i][k];
+      }
+    }
+    const float mean = row_totals(dot, 0u, a.tpr, meet).sum * a.inv_cols;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      const int at = i * a.tpr + place;
+      if (!live || at >= a.vecs) continue;
+      const size_t here = row * cols + 8 * at;
+      float d[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) d[k] = 0.0f;
+      if (a.grad_sum != nullptr) unpack8<T>(load8<T>(a.grad_sum, here), d);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) d[k] += rstd * (g[i][k] - xh[i][k] * mean);
+      *reinterpret_cast<uint4*>(static_cast<T*>(a.grad_x) + here) = pack8<T>(d);
+    }
+    if (++added == kNormSumRows) {
+      added = 0;
+#pragma unroll
+      for (int i = 0; i < kVec; ++i)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          far[i][k] += near[i][k];
+          near[i][k] = 0.0f;
+        }
+    }
+  }
+  if (a.partial == nullptr) return;
+  float* out = a.partial + (static_cast<size_t>(blockIdx.x) * a.per_cta + in_cta) * cols;
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) {
+    const int at = i * a.tpr + place;
+    if (at >= a.vecs) continue;
+    float4* q = reinterpret_cast<float4*>(out + 8 * at);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) near[i][k] += far[i][k];
+    q[0] = make_float4(near[i][0], near[i][1], near[i][2], near[i][3]);
+    q[1] = make_float4(near[i][4], near[i][5], near[i][6], near[i][7]);
+  }
+}
+
+// Column sums of `n` rows: a CTA has 32 columns, its 8 warps every eighth row each.
+__global__ void __launch_bounds__(256) mrs_norm_gain_kernel(const float* partial, int n, int cols,
+                                                            float* out) {
+  __shared__ float meet[8][32];
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = 32 * blockIdx.x + lane;
+  pdl_wait();
+  float sum = 0.0f;
+  if (c < cols) {
+#pragma unroll 4
+    for (int r = warp; r < n; r += 8) sum += partial[static_cast<size_t>(r) * cols + c];
+  }
+  meet[warp][lane] = sum;
+  __syncthreads();
+  if (warp == 0 && c < cols) {
+#pragma unroll
+    for (int w = 1; w < 8; ++w) sum += meet[w][lane];
+    out[c] = sum;
+  }
+}
+
+namespace {
+
+// CTAs of the gradient on a device of `sms` SMs, for a workspace that does not know the device.
+constexpr int kNormMaxSms = 256;
+int norm_grad_ctas(const RowPlan& p, int sms) {
+  const int per_sm = 1024 / p.threads;
+  return sms * (per_sm < 1 ? 1 : per_sm);
+}
+RowPlan norm_grad_plan(int cols) { return row_plan(cols, 1, 128); }
+
+template <class T>
+cudaError_t launch_norm(const NormArgs& a, const RowPlan& p, cudaStream_t st) {
+  const dim3 grid(static_cast<unsigned>((a.rows + p.rows - 1) / p.rows)), block(p.threads);
+  switch (p.vec) {
+    case 1: return launch_pdl(mrs_norm_kernel<T, 1>, grid, block, 0, st, a);
+    case 2: return launch_pdl(mrs_norm_kernel<T, 2>, grid, block, 0, st, a);
+    case 3: return launch_pdl(mrs_norm_kernel<T, 3>, grid, block, 0, st, a);
+    default: return launch_pdl(mrs_norm_kernel<T, 4>, grid, block, 0, st, a);
+  }
+}
+template <class T>
+cudaError_t launch_norm_grad(const NormGradArgs& a, const RowPlan& p, int ctas, cudaStream_t st) {
+  const dim3 grid(ctas), block(p.threads);
+  switch (p.vec) {
+    case 1: return launch_pdl(mrs_norm_grad_kernel<T, 1>, grid, block, 0, st, a);
+    case 2: return launch_pdl(mrs_norm_grad_kernel<T, 2>, grid, block, 0, st, a);
+    case 3: return launch_pdl(mrs_norm_grad_kernel<T, 3>, grid, block, 0, st, a);
+    default: return launch_pdl(mrs_norm_grad_kernel<T, 4>, grid, block, 0, st, a);
+  }
+}
+
+bool bad_row_cols(int cols) { return cols < 8 || cols > kRowMaxCols || cols % 8 != 0; }
+bool bad_half(int dtype) { return dtype != MOE_RS_BF16 && dtype != MOE_RS_FP16; }
+bool bad_gain(int gain_dtype, int dtype) {
+  return gain_dtype != dtype && gain_dtype != MOE_RS_FP32;
+}
+// Rows that a launch and every offset hold.
+bool too_many(int64_t rows, int64_t parts, int64_t stride) {
+  return rows > INT32_MAX || parts * rows > (int64_t{1} << 40) || stride > (int64_t{1} << 31);
+}
+
+}  // namespace
+}  // namespace mrs
+
+using namespace mrs;
+
+extern "C" {
+
+int moe_rms_norm(const void* x, int dtype, int64_t x_stride, int parts, const void* residual,
+                 int64_t residual_stride, int64_t rows, int cols, const void* gain, int gain_dtype,
+                 float eps, void* y, void* sum, uint8_t* codes, float* scales, float* rstd,
+                 cudaStream_t stream) {
+  if (bad_half(dtype) || bad_gain(gain_dtype, dtype)) return MOE_RS_ERR_BAD_DTYPE;
+  if (rows < 0) return MOE_RS_ERR_BAD_ROWS;
+  if (parts < 1 || parts > kMaxTopk) return MOE_RS_ERR_BAD_TOPK;
+  if (bad_row_cols(cols) || x_stride < cols || (residual && residual_stride < cols))
+    return MOE_RS_ERR_BAD_COLS;
+  if (!(eps >= 0.0f) || eps > 1.0f) return MOE_RS_ERR_BAD_SCALE;
+  if (too_many(rows, parts, x_stride) || (residual && residual_stride > (int64_t{1} << 31)))
+    return MOE_RS_ERR_OVERFLOW;
+  if (rows == 0) return MOE_RS_OK;
+  if (!x || !gain || (!y && !sum && !codes && !rstd) || (codes == nullptr) != (scales == nullptr))
+    return MOE_RS_ERR_NULL_POINTER;
+  if (!aligned(x, 16) || x_stride % 8 != 0 || !aligned(residual, 16) ||
+      (residual && residual_stride % 8 != 0) || !aligned(gain, 16) || !aligned(y, 16) ||
+      !aligned(sum, 16) || !aligned(codes, 8) || !aligned(scales, 4) || !aligned(rstd, 4))
+    return MOE_RS_ERR_MISALIGNED;
+  const size_t n = static_cast<size_t>(rows) * cols;
+  const size_t c = static_cast<size_t>(cols);
+  // the residual stream may be updated in place
+  const bool in_place = sum != nullptr && sum == residual && residual_stride == cols;
+  const Span outs[] = {span(y, y ? 2 * n : 0), span(sum, sum ? 2 * n : 0),
+                       span(codes, codes ? n : 0), span(scales, scales ? 4 * rows : 0),
+                       span(rstd, rstd ? 4 * rows : 0)};
+  const Span ins[] = {rows_span(x, rows * parts, cols, x_stride, 2),
+                      span(gain, c * (gain_dtype == MOE_RS_FP32 ? 4 : 2)),
+                      rows_span(in_place ? nullptr : residual, rows, cols, residual_stride, 2)};
+  if (any_alias(outs, 5, ins, 3)) return MOE_RS_ERR_ALIAS;
+  const RowPlan p = row_plan(cols, 1);
+  NormArgs a{};
+  a.x = x;
+  a.residual = residual;
+  a.gain = gain;
+  a.x_stride = static_cast<size_t>(x_stride);
+  a.residual_stride = static_cast<size_t>(residual_stride);
+  a.rows = rows;
+  a.parts = parts;
+  a.vecs = cols / 8;
+  a.tpr = p.tpr;
+  a.per_cta = p.rows;
+  a.gain_f32 = gain_dtype == MOE_RS_FP32;
+  a.eps = eps;
+  a.inv_cols = 1.0f / static_cast<float>(cols);
+  a.y = y;
+  a.sum = sum;
+  a.codes = codes;
+  a.scales = scales;
+  a.rstd = rstd;
+  return launch_status(dtype == MOE_RS_BF16 ? launch_norm<__nv_bfloat16>(a, p, stream)
+                                            : launch_norm<__half>(a, p, stream));
+}
+
+size_t moe_rms_norm_backward_workspace_bytes(int cols) {
+  if (bad_row_cols(cols)) return 0;
+  const RowPlan p = norm_grad_plan(cols);
+  return static_cast<size_t>(norm_grad_ctas(p, kNormMaxSms)) * p.rows * cols * 4;
+}
+
+int moe_rms_norm_backward(const void* s, int dtype, const void* gain, int gain_dtype,
+                          const float* rstd, const void* grad, const void* grad_rows, int parts,
+                          const void* grad_sum, int64_t rows, int cols, void* grad_x,
+                          float* grad_gain, void* workspace, size_t workspace_bytes,
+                          cudaStream_t stream) {
+  if (bad_half(dtype) || bad_gain(gain_dtype, dtype)) return MOE_RS_ERR_BAD_DTYPE;
+  if (rows < 0) return MOE_RS_ERR_BAD_ROWS;
+  if (parts < 1 || parts > kMaxTopk) return MOE_RS_ERR_BAD_TOPK;
+  if (bad_row_cols(cols)) return MOE_RS_ERR_BAD_COLS;
+  if (too_many(rows, parts, cols)) return MOE_RS_ERR_OVERFLOW;
+  const size_t need = moe_rms_norm_backward_workspace_bytes(cols);
+  if (grad_gain && (!workspace || workspace_bytes < need)) return MOE_RS_ERR_WORKSPACE;
+  if (rows > 0 && (!s || !gain || !rstd || !grad_x || (!grad && !grad_rows)))
+    return MOE_RS_ERR_NULL_POINTER;
+  if (!aligned(s, 16) || !aligned(gain, 16) || !aligned(rstd, 4) || !aligned(grad, 16) ||
+      !aligned(grad_rows, 16) || !aligned(grad_sum, 16) || !aligned(grad_x, 16) ||
+      !aligned(grad_gain, 4) || !aligned(workspace, 16))
+    return MOE_RS_ERR_MISALIGNED;
+  const size_t n = 2 * static_cast<size_t>(rows) * cols, c = static_cast<size_t>(cols);
+  const Span outs[] = {span(grad_x, n), span(grad_gain, grad_gain ? 4 * c : 0),
+                       span(workspace, grad_gain ? workspace_bytes : 0)};
+  const Span ins[] = {span(s, n), span(gain, c * (gain_dtype == MOE_RS_FP32 ? 4 : 2)),
+                      span(rstd, 4 * static_cast<size_t>(rows)), span(grad, grad ? n : 0),
+                      span(grad_rows, grad_rows ? n * parts : 0), span(grad_sum, grad_sum ? n : 0)};
+  if (any_alias(outs, 3, ins, 6)) return MOE_RS_ERR_ALIAS;
+  if (rows == 0 && !grad_gain) return MOE_RS_OK;
+  const int sms = sm_count();
+  if (sms == 0) return launch_status(cudaErrorInvalidDevice);
+  const RowPlan p = norm_grad_plan(cols);
+  NormGradArgs a{};
+  a.s = s;
+  a.gain = gain;
+  a.grad = grad;
+  a.grad_rows = grad_rows;
+  a.grad_sum = grad_sum;
+  a.rstd = rstd;
+  a.rows = rows;
+  a.parts = parts;
+  a.vecs = cols / 8;
+  a.tpr = p.tpr;
+  a.per_cta = p.rows;
+  a.gain_f32 = gain_dtype == MOE_RS_FP32;
+  a.inv_cols = 1.0f / static_cast<float>(cols);
+  a.grad_x = grad_x;
+  a.partial = grad_gain ? static_cast<float*>(workspace) : nullptr;
+  // without rows one CTA leaves the zeros that the sums are made of
+  const int64_t most = rows == 0 ? 1 : (rows + p.rows - 1) / p.rows;
+  const int full = norm_grad_ctas(p, sms < kNormMaxSms ? sms : kNormMaxSms);
+  const int ctas = most < full ? static_cast<int>(most) : full;
+  cudaError_t err = dtype == MOE_RS_BF16 ? launch_norm_grad<__nv_bfloat16>(a, p, ctas, stream)
+                                         : launch_norm_grad<__half>(a, p, ctas, stream);
+  if (err == cudaSuccess && grad_gain)
+    err = launch_pdl(mrs_norm_gain_kernel, dim3((cols + 31) / 32), dim3(256), 0, stream,
+                     static_cast<const float*>(a.partial), ctas * p.rows, cols, grad_gain);
+  return launch_status(err);
+}
+
+}  // extern "C"

@@ -1,9 +1,11 @@
-// mrs_packed.cu -- the operations of training and experts behind one call that takes its arguments
+// mrs_packed.cu -- the operations of training, rows and experts behind one call that takes its arguments
 // as an array: for bindings that pay for every argument they convert (20 arguments through ctypes
 // take 1.8 us on the host, an array of them 0.5, and a small call's kernel 4).
 #include <climits>
 #include <cstdint>
 #include <cstring>
+#include <tuple>
+#include <type_traits>
 
 #include "moe_route_sort.h"
 
@@ -35,7 +37,24 @@ struct Packed {
     return static_cast<float>(d);
   }
   cudaStream_t stream() { return ptr<CUstream_st>(); }
+  template <class A>
+  A get() {
+    if constexpr (std::is_pointer_v<A>) return ptr<std::remove_pointer_t<A>>();
+    else if constexpr (std::is_same_v<A, float>) return real();
+    else if constexpr (std::is_same_v<A, int>) return num();
+    else if constexpr (std::is_same_v<A, size_t>) return size();
+    else return next();
+  }
 };
+
+// `fn` with the n arguments that follow, each as fn's declaration has it.
+template <class... A>
+int call(int (*fn)(A...), int64_t n, Packed& p) {
+  if (n != static_cast<int64_t>(sizeof...(A))) return MOE_RS_ERR_BAD_CALL;
+  const std::tuple<A...> args{p.get<A>()...};  // (braces: from the first to the last)
+  if (!p.fits) return MOE_RS_ERR_OVERFLOW;
+  return std::apply(fn, args);
+}
 
 }  // namespace
 
@@ -127,6 +146,11 @@ extern "C" int moe_call_packed(const void* args) {
       return moe_experts_mxfp4(xc, xs, per_route, wc, ws, T, E, K, cols, outs, block_m, sid, sw,
                                eid, npp, out, dtype, work, bytes, st);
     }
+    case MOE_RS_CALL_FP8_QUANTIZE: return call(moe_fp8_quantize, n, p);
+    case MOE_RS_CALL_RMS_NORM: return call(moe_rms_norm, n, p);
+    case MOE_RS_CALL_RMS_NORM_BACKWARD: return call(moe_rms_norm_backward, n, p);
+    case MOE_RS_CALL_SWIGLU: return call(moe_swiglu, n, p);
+    case MOE_RS_CALL_SWIGLU_BACKWARD: return call(moe_swiglu_backward, n, p);
     default: return MOE_RS_ERR_BAD_CALL;
   }
 }

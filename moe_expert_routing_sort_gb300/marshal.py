@@ -87,6 +87,11 @@ _OPERATIONS = {
     "moe_mxfp4_quantize": (3, "8q"),
     "moe_mxfp4_dequantize": (4, "8q"),
     "moe_experts_mxfp4": (5, "20q"),
+    "moe_fp8_quantize": (6, "8q"),
+    "moe_rms_norm": (7, "10qd6q"),
+    "moe_rms_norm_backward": (8, "16q"),
+    "moe_swiglu": (9, "10q"),
+    "moe_swiglu_backward": (10, "10q"),
 }
 
 
