@@ -451,6 +451,65 @@ int moe_swiglu_backward(const void* grad, const void* x, int dtype, int64_t x_st
                         int cols, const float* weights, void* grad_x, float* grad_weights,
                         cudaStream_t stream);
 
+/* ------------------------------------------------- experts' products in 16 and 8 bits */
+
+/* Widest rows and outputs of the products below. */
+#define MOE_RS_PRODUCT_MAX_COLS 65536
+
+/* Bytes of device workspace of the three products below (16-byte aligned).  Its first int32
+ * collects the MOE_RS_DEVICE_* bits of the calls that use it and is never cleared by them: zero it
+ * before first use; the rest may hold anything.  One workspace must not be used by two calls that
+ * can run at the same time.  0 for invalid arguments. */
+size_t moe_experts_product_workspace_bytes(int T, int E, int topk, int block_m);
+
+/* The experts' products over a sorted list of routes, in 16 bits or in 8.  For every row
+ * p < num_tokens_post_pad[0] whose r = sorted_token_ids[p] lies in [0, T*topk), e = expert_ids[p /
+ * block_m]:
+ *   out[r, n] = w_p * sum over k < cols of X[row, k] * W[e, n, k],     n < outs
+ * with row = r (x_per_route != 0: X has T*topk rows) or r / topk (X has T rows), and w_p =
+ * sorted_weights[p], or 1 when sorted_weights is NULL.  X [rows, cols] and W [E, outs, cols] are
+ * both of type x_dtype: MOE_RS_BF16, MOE_RS_FP16, or MOE_RS_FP8 with fp32 scales x_scales [rows] and
+ * w_scales [E, outs] (16-bit types: both NULL), by which the sum is multiplied.  Sums are fp32, and
+ * scales and w_p are applied before the one rounding to out_dtype (MOE_RS_BF16, MOE_RS_FP16 or
+ * MOE_RS_FP32).  out [T*topk, outs], row r being route r; rows of dropped routes are not written.
+ * The list is that of moe_sort or moe_route_sort with the same T, E, topk, block_m: blocks of an
+ * expert side by side, expert ids ascending.  One that is not, or an expert id outside [0, E), sets
+ * MOE_RS_DEVICE_BAD_EXPERT_ID, and the outputs are then unspecified (every access stays within the
+ * buffers); a device wait that gives up sets MOE_RS_DEVICE_WAIT_TIMEOUT (outputs invalid).
+ * cols and outs: multiples of 8 (cols of 16 for MOE_RS_FP8) in [8, MOE_RS_PRODUCT_MAX_COLS];
+ * limits of T, E, topk, block_m as for moe_sort.  X, W, out: 16-byte aligned.
+ * No counterpart in the source pages, whose products belong to another library. */
+int moe_experts_product(const void* x, int x_dtype, const float* x_scales, int x_per_route,
+                        const void* w, const float* w_scales, int T, int E, int topk, int cols,
+                        int outs, int block_m, const int32_t* sorted_token_ids,
+                        const float* sorted_weights, const int32_t* expert_ids,
+                        const int32_t* num_tokens_post_pad, void* out, int out_dtype,
+                        void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Gradient of that product's rows (16-bit types, no weights w_p): for every route r of the list
+ *   grad_rows[r, k] = sum over n < outs of G[row, n] * W[e, n, k],     k < cols
+ * G [rows, outs]: a row for each route (g_per_route != 0) or each token (the gradient of a sum over
+ * the token's experts).  grad_rows [T*topk, cols], of type out_dtype, one row for each route: of
+ * rows of X shared by a token's routes the gradient is the sum of topk adjacent rows.  Rows of
+ * dropped routes are not written.  Everything else as above. */
+int moe_experts_grad_rows(const void* grad, int dtype, int g_per_route, const void* w, int T, int E,
+                          int topk, int cols, int outs, int block_m,
+                          const int32_t* sorted_token_ids, const int32_t* expert_ids,
+                          const int32_t* num_tokens_post_pad, void* grad_rows, int out_dtype,
+                          void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Gradient of its weights: for every expert e, n < outs, k < cols
+ *   grad_w[e, n, k] = sum over routes r of e in the list of G[row, n] * X[row', k]
+ * (row and row' as above, each by its own per_route argument).  Every element of grad_w [E, outs,
+ * cols] is written: experts without routes get zeros.  out_dtype: that of the rows, or
+ * MOE_RS_FP32.  Everything else as above. */
+int moe_experts_grad_weights(const void* grad, int dtype, int g_per_route, const void* x,
+                             int x_per_route, int T, int E, int topk, int cols, int outs,
+                             int block_m, const int32_t* sorted_token_ids,
+                             const int32_t* expert_ids, const int32_t* num_tokens_post_pad,
+                             void* grad_w, int out_dtype, void* workspace, size_t workspace_bytes,
+                             cudaStream_t stream);
+
 /* One of the operations that have a number below with its arguments as an array, for language
  * bindings that pay per argument.  args: 8-byte values (8-byte aligned host memory): the operation's number, the
  * number of its arguments, then the arguments in the order of its declaration -- pointers, the
@@ -467,6 +526,9 @@ int moe_swiglu_backward(const void* grad, const void* x, int dtype, int64_t x_st
 #define MOE_RS_CALL_RMS_NORM_BACKWARD 8
 #define MOE_RS_CALL_SWIGLU 9
 #define MOE_RS_CALL_SWIGLU_BACKWARD 10
+#define MOE_RS_CALL_EXPERTS_PRODUCT 11
+#define MOE_RS_CALL_EXPERTS_GRAD_ROWS 12
+#define MOE_RS_CALL_EXPERTS_GRAD_WEIGHTS 13
 int moe_call_packed(const void* args);
 
 /* ------------------------------------------------------- allocation-free variant */

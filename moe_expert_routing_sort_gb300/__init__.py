@@ -55,6 +55,16 @@ from .experts import (  # noqa: F401
     mxfp4_dequantize,
     mxfp4_quantize,
 )
+from .products import (  # noqa: F401
+    ProductWorkspace,
+    experts_grad_rows,
+    experts_grad_weights,
+    experts_product,
+    moe_experts_grad_rows,
+    moe_experts_grad_weights,
+    moe_experts_product,
+    moe_experts_product_workspace_bytes,
+)
 from .rows import (  # noqa: F401
     Fp8Rows,
     NormBuffers,

@@ -118,6 +118,16 @@ def load() -> ctypes.CDLL:
         lib.moe_swiglu.restype = I
         lib.moe_swiglu_backward.argtypes = [P, P, I, L, L, I, P, P, P, P]
         lib.moe_swiglu_backward.restype = I
+        lib.moe_experts_product_workspace_bytes.argtypes = [I, I, I, I]
+        lib.moe_experts_product_workspace_bytes.restype = S
+        lib.moe_experts_product.argtypes = [P, I, P, I, P, P, I, I, I, I, I, I, P, P, P, P, P, I,
+                                            P, S, P]
+        lib.moe_experts_product.restype = I
+        lib.moe_experts_grad_rows.argtypes = [P, I, I, P, I, I, I, I, I, I, P, P, P, P, I, P, S, P]
+        lib.moe_experts_grad_rows.restype = I
+        lib.moe_experts_grad_weights.argtypes = [P, I, I, P, I, I, I, I, I, I, I, P, P, P, P, I, P,
+                                                 S, P]
+        lib.moe_experts_grad_weights.restype = I
         lib.moe_call_packed.argtypes = [ctypes.c_char_p]
         lib.moe_call_packed.restype = I
         _lib = lib

@@ -151,6 +151,9 @@ extern "C" int moe_call_packed(const void* args) {
     case MOE_RS_CALL_RMS_NORM_BACKWARD: return call(moe_rms_norm_backward, n, p);
     case MOE_RS_CALL_SWIGLU: return call(moe_swiglu, n, p);
     case MOE_RS_CALL_SWIGLU_BACKWARD: return call(moe_swiglu_backward, n, p);
+    case MOE_RS_CALL_EXPERTS_PRODUCT: return call(moe_experts_product, n, p);
+    case MOE_RS_CALL_EXPERTS_GRAD_ROWS: return call(moe_experts_grad_rows, n, p);
+    case MOE_RS_CALL_EXPERTS_GRAD_WEIGHTS: return call(moe_experts_grad_weights, n, p);
     default: return MOE_RS_ERR_BAD_CALL;
   }
 }

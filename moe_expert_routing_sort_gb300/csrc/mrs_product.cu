@@ -1,0 +1,654 @@
+// mrs_product.cu -- the experts' products in 16 and 8 bits, driven by the sort step, and the
+// gradient of their rows.
+//
+// For every route r of the sorted list, with e the owner of its block:
+//   out[r, m] = w_r * sx_row * sw_em * sum over k of X[row, k] A_e[m, k]
+// A_e is W[e] (m an output, k a column), or for the rows' gradient its transpose (m a column, k an
+// output).  Sums are fp32; the row's weight, its scale and the output's scale are applied in fp32,
+// and the result is rounded once.
+//
+// A pair of CTAs computes tiles of 256 m by up to 256 (or 64) rows of one expert.  m, which is
+// regular and long, is on the 256 lanes of both tensor memories, the ragged rows are the product's
+// N, which goes in steps of 32: an expert's last rows cost what they are, not a whole tile.  Each
+// CTA brings 128 m and half of the rows into shared memory, 128 bytes of each a step, so that a
+// byte of either operand serves twice the products that it would in one CTA.  Rows are gathered by
+// tensor copies, four rows an instruction.
+//
+// The warps of a CTA each have one task:
+//   0      copies of a step's weights and rows
+//   1      the list: rows, routes and factors of the next units into a ring in shared memory
+//   2      in the first CTA of a pair the products, in the second the word that its half is there
+//   3      nothing
+//   4-11   finished tiles from tensor memory to the output rows, while the next one is computed
+// Every wait is bounded; one that gives up ends its warp's task with the status bit set.  The CTAs
+// of a pair leave together.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "mrs_product.cuh"
+
+namespace mrs {
+
+// ------------------------------------------------------------------------ the row tiles
+constexpr int kTableThreads = 1024;
+constexpr int kTableEach = kMaxExperts / kTableThreads;
+
+__global__ void __launch_bounds__(kTableThreads) mrs_product_table_kernel(const TableArgs a) {
+  __shared__ int start[kMaxExperts + 1];
+  __shared__ int meet[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_trigger();
+  pdl_wait();
+  const int blocks = min(max(__ldg(a.npp), 0), a.max_rows) >> a.log2B;
+  for (int e = tid; e <= a.E; e += kTableThreads) start[e] = blocks;
+  __syncthreads();
+  bool bad = false;
+#pragma unroll 4
+  for (int b = tid; b < blocks; b += kTableThreads) {
+    const int e = __ldg(a.eid + b), before = b > 0 ? __ldg(a.eid + b - 1) : -1;
+    if (e < 0 || e >= a.E || e < before) bad = true;
+    else if (e != before) start[e] = b;
+  }
+  if (__syncthreads_or(bad) && tid == 0) atomicOr(a.t.head, MOE_RS_DEVICE_BAD_EXPERT_ID);
+  // an expert without a run starts where the next one does: the least start from it on (which is
+  // in order whatever the list holds)
+  const int e0 = tid * kTableEach;
+  int first[kTableEach + 1];
+  int least = blocks;
+#pragma unroll
+  for (int i = kTableEach - 1; i >= 0; --i) {
+    least = min(least, e0 + i < a.E ? start[e0 + i] : blocks);
+    first[i] = least;
+  }
+  int after = least;  // of the threads from this one on
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_down_sync(kFull, after, o);
+    if (lane + o < 32) after = min(after, v);
+  }
+  if (lane == 0) meet[warp] = after;
+  int next = __shfl_down_sync(kFull, after, 1);
+  if (lane == 31) next = blocks;
+  __syncthreads();
+  for (int w = warp + 1; w < 32; ++w) next = min(next, meet[w]);
+  first[kTableEach] = next;
+#pragma unroll
+  for (int i = 0; i < kTableEach; ++i) first[i] = min(first[i], next);
+  int count = 0;
+#pragma unroll
+  for (int i = 0; i < kTableEach; ++i) {
+    const int64_t rows = static_cast<int64_t>(first[i + 1] - first[i]) * a.B;
+    count += static_cast<int>((rows + a.rows - 1) / a.rows);
+  }
+  int sum = count;  // tiles up to this thread's experts
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(kFull, sum, o);
+    if (lane >= o) sum += v;
+  }
+  __syncthreads();
+  if (lane == 31) meet[warp] = sum;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) sum += meet[w];
+  int at = sum - count;
+  if (tid == kTableThreads - 1) a.t.head[1] = min(sum, a.max_tiles);
+#pragma unroll
+  for (int i = 0; i < kTableEach; ++i) {
+    const int e = e0 + i;
+    if (e > a.E) break;
+    a.t.offs[e] = first[i];
+    if (e == a.E) break;
+    if (e + 1 == a.E && i + 1 == kTableEach) a.t.offs[a.E] = first[kTableEach];
+    const int p0 = first[i] * a.B, rows = (first[i + 1] - first[i]) * a.B;
+    for (int64_t r = 0; r < rows; r += a.rows, ++at)
+      if (at < a.max_tiles)
+        a.t.tiles[at] = make_int4(e, p0 + static_cast<int>(r),
+                                  min(a.rows, rows - static_cast<int>(r)), 0);
+    if (a.want_used) {
+      // routes come first in the last block: how many
+      int lo = rows > 0 ? rows - a.B : 0, hi = rows;
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        const int s = __ldg(a.sid + p0 + mid);
+        if (s >= 0 && s < a.routes) lo = mid + 1;
+        else hi = mid;
+      }
+      a.t.used[e] = lo;
+    }
+  }
+}
+
+cudaError_t launch_product_table(const TableArgs& a, cudaStream_t st) {
+  return launch_pdl(mrs_product_table_kernel, dim3(1), dim3(kTableThreads), 0, st, a);
+}
+
+// ------------------------------------------------------------------------- the products
+struct ProductArgs {
+  ProductTable t;
+  const int32_t* sid;
+  const float *sw, *xs, *ws;  // or null
+  void* out;
+  unsigned long long wait_limit_ns;
+  int routes, topk, per_route, max_tiles;
+  int E, M, K, P;  // M: outputs of the product; K: the contraction; P: rows of the list at most
+  int mtiles, chunk, nchunk, ksteps;
+  int type;        // of the operands: 0 fp16 or e4m3, 1 bf16
+  int out_type;
+};
+
+constexpr int kProductThreads = 384;
+constexpr int kProductTmem = 512;
+constexpr int kPairRows = 256;  // m of a tile
+constexpr int kInfoSlots = 3;
+constexpr int kInfoUsers = 10;  // copies, products, eight storing warps
+
+template <int R>
+struct ProductShape {
+  static constexpr int kW = 128 * 128;
+  static constexpr int kX = R / 2 * 128;
+  static constexpr int kSlots = R == 256 ? 6 : 9;
+  static constexpr size_t kSmem = static_cast<size_t>(kSlots) * (kW + kX) + 1024;
+};
+
+template <int R>
+struct ProductInfo {
+  int e, n, m0, tiles, half, pad[3];  // e < 0: no more units
+  int src[R / 2];                     // rows of X that this CTA copies
+  int route[R];                       // -1: none
+  float factor[R];
+};
+
+template <class Out>
+__device__ __forceinline__ Out rounded(float v, int type) {
+  if constexpr (sizeof(Out) == 4) {
+    return v;
+  } else {
+    if (type == MOE_RS_BF16) {
+      const __nv_bfloat16 h = __float2bfloat16_rn(v);
+      return *reinterpret_cast<const uint16_t*>(&h);
+    }
+    const __half h = __float2half_rn(v);
+    return *reinterpret_cast<const uint16_t*>(&h);
+  }
+}
+
+template <bool kFp8, bool kTranspose, int R, class Out>
+__global__ void __launch_bounds__(kProductThreads, 1)
+    mrs_product_kernel(const __grid_constant__ CUtensorMap wmap,
+                       const __grid_constant__ CUtensorMap xmap, const ProductArgs a) {
+  using Sh = ProductShape<R>;
+  constexpr int S = Sh::kSlots;
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ unsigned long long full_s[S], free_s[S], other_s[S], acc_full_s[2], acc_free_s[2],
+      info_full_s[kInfoSlots], info_free_s[kInfoSlots], done_s;
+  __shared__ __align__(16) ProductInfo<R> info_s[kInfoSlots];
+  __shared__ uint32_t tmem_s;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = static_cast<int>(pair_rank());
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t wbase = base, xbase = base + S * Sh::kW;
+  const unsigned long long limit = a.wait_limit_ns;
+  pdl_trigger();
+  if (tid == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full_s[s], 1);
+      mbar_init(&free_s[s], 1);
+      mbar_init(&other_s[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full_s[b], 1);
+      mbar_init(&acc_free_s[b], 16);  // the storing warps of both CTAs
+    }
+    for (int i = 0; i < kInfoSlots; ++i) {
+      mbar_init(&info_full_s[i], 32);
+      mbar_init(&info_free_s[i], kInfoUsers);
+    }
+    mbar_init(&done_s, 1);
+    fence_mbar_init();
+  }
+  if (warp == 2) pair_tmem_alloc(&tmem_s, kProductTmem);
+  tc_fence_before();
+  __syncthreads();
+  pair_sync();
+  tc_fence_after();
+  const uint32_t tmem = tmem_s;
+  pdl_wait();
+
+  bool ok = true;
+  Ring<kInfoSlots> at_info;
+  // The next unit for one of its users (a whole warp): false when there is none.
+  auto next_unit = [&]() -> const ProductInfo<R>* {
+    ok = ok && warp_wait(&info_full_s[at_info.slot], at_info.phase, limit);
+    if (!ok) return nullptr;
+    const ProductInfo<R>* q = &info_s[at_info.slot];
+    return q->e < 0 ? nullptr : q;
+  };
+  auto leave_unit = [&] {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&info_free_s[at_info.slot]);
+    at_info.advance();
+  };
+
+  if (warp == 0) {
+    Ring<S> at;
+    long long issued = 0;
+    while (const ProductInfo<R>* q = next_unit()) {
+      const int half = q->half;
+      const bool mine = 4 * lane < half;
+      const int4 src = mine ? *reinterpret_cast<const int4*>(&q->src[4 * lane])
+                            : make_int4(0, 0, 0, 0);
+      const int e = q->e, m0 = q->m0 + 128 * rank, tiles = q->tiles;
+      for (int c = 0; ok && c < tiles; ++c) {
+        for (int ks = 0; ks < a.ksteps; ++ks) {
+          ok = warp_wait(&free_s[at.slot], at.phase ^ 1u, limit);
+          if (!ok) break;
+          const uint32_t wto = wbase + at.slot * Sh::kW, xto = xbase + at.slot * Sh::kX;
+          if (elect_one()) {
+            mbar_expect(&full_s[at.slot], Sh::kW + half * 128);
+            const int m = m0 + c * kPairRows;
+            if constexpr (kTranspose) {
+              tma_load_3d(wto, &wmap, m, 64 * ks, e, &full_s[at.slot]);
+              tma_load_3d(wto + 64 * 128, &wmap, m + 64, 64 * ks, e, &full_s[at.slot]);
+            } else {
+              tma_load_3d(wto, &wmap, (kFp8 ? 128 : 64) * ks, m, e, &full_s[at.slot]);
+            }
+          }
+          if (mine)
+            tma_gather4(xto + 512 * lane, &xmap, (kFp8 ? 128 : 64) * ks, src, &full_s[at.slot]);
+          ++issued;
+          at.advance();
+        }
+      }
+      leave_unit();
+    }
+    // nothing may land in the shared memory of a CTA that has left
+    for (long long i = issued > S ? issued - S : 0; i < issued; ++i)
+      warp_wait(&full_s[i % S], static_cast<uint32_t>(i / S) & 1u, kWaitLimitNs);
+  } else if (warp == 1) {
+    // (of this call at most, whatever another one may have left there)
+    const int tiles = min(max(__ldg(a.t.head + 1), 0), a.max_tiles);
+    const int units = tiles * a.nchunk;
+    for (int u = blockIdx.x >> 1; ok && u < units; u += gridDim.x >> 1) {
+      const int t = u / a.nchunk, first = (u - t * a.nchunk) * a.chunk;
+      const int4 tile = __ldg(a.t.tiles + t);
+      // (a table that another call overwrites must not lead out of this call's buffers)
+      const int e = min(max(tile.x, 0), a.E - 1), p0 = min(max(tile.y, 0), a.P);
+      const int rows = min(min(tile.z, R), a.P - p0);
+      int r[R / 32];
+      int used = 0;
+#pragma unroll
+      for (int j = 0; j < R / 32; ++j) {
+        const int i = 32 * j + lane;
+        const int s = i < rows ? __ldg(a.sid + p0 + i) : -1;
+        r[j] = s >= 0 && s < a.routes ? s : -1;
+        const unsigned some = __ballot_sync(kFull, r[j] >= 0);
+        if (some != 0u) used = 32 * j + 32 - __clz(some);
+      }
+      if (used == 0) continue;
+      float f[R / 32];
+      int src[R / 32];
+#pragma unroll
+      for (int j = 0; j < R / 32; ++j) {
+        const bool is = r[j] >= 0;
+        src[j] = is ? (a.per_route ? r[j] : r[j] / a.topk) : 0;
+        f[j] = 1.0f;
+        if (a.sw != nullptr && is) f[j] = __ldg(a.sw + p0 + 32 * j + lane);
+        if (a.xs != nullptr && is) f[j] *= __ldg(a.xs + src[j]);
+      }
+      const int n = (used + 31) & ~31, half = n >> 1;
+      ok = warp_wait(&info_free_s[at_info.slot], at_info.phase ^ 1u, limit);
+      if (!ok) break;
+      ProductInfo<R>* q = &info_s[at_info.slot];
+      if (lane == 0) {
+        q->e = e;
+        q->n = n;
+        q->m0 = first * kPairRows;
+        q->tiles = min(a.chunk, a.mtiles - first);
+        q->half = half;
+      }
+#pragma unroll
+      for (int j = 0; j < R / 32; ++j) {
+        const int i = 32 * j + lane, mine = i - rank * half;
+        if (mine >= 0 && mine < half) q->src[mine] = src[j];
+        q->route[i] = r[j];
+        q->factor[i] = f[j];
+      }
+      mbar_arrive(&info_full_s[at_info.slot]);
+      at_info.advance();
+    }
+    ok = ok && warp_wait(&info_free_s[at_info.slot], at_info.phase ^ 1u, limit);
+    if (ok) {
+      if (lane == 0) info_s[at_info.slot].e = -1;
+      mbar_arrive(&info_full_s[at_info.slot]);
+    }
+  } else if (warp == 2) {
+    Ring<S> at;
+    int buf = 0;
+    uint32_t acc_phase = 0;
+    bool any = false;
+    while (const ProductInfo<R>* q = next_unit()) {
+      const int n = q->n, tiles = q->tiles;
+      any = true;
+      if (elect_one()) {
+        Ring<S> s = at;
+        int to = buf;
+        uint32_t to_phase = acc_phase;
+        const uint32_t word = pair_word(a.type, kTranspose, false, n);
+        for (int c = 0; ok && c < tiles; ++c) {
+          if (rank == 0) ok = pair_wait(&acc_free_s[to], to_phase ^ 1u, limit);
+          if (!ok) break;
+          tc_fence_after();
+          for (int ks = 0; ks < a.ksteps; ++ks) {
+            ok = thread_wait(&full_s[s.slot], s.phase, limit);
+            if (!ok) break;
+            if (rank != 0) {
+              pair_arrive_first(&other_s[s.slot]);
+            } else {
+              ok = pair_wait(&other_s[s.slot], s.phase, limit);
+              if (!ok) break;
+              tc_fence_after();
+              const uint32_t wat = wbase + s.slot * Sh::kW;
+              const uint64_t dw = kTranspose ? desc_lines128(wat, 64) : desc_rows128(wat);
+              const uint64_t dx = desc_rows128(xbase + s.slot * Sh::kX);
+#pragma unroll
+              for (int g = 0; g < 4; ++g)
+                // 32 bytes further along the rows; along the lines 16 of them
+                pair_mma<kFp8>(tmem + to * R, dw + (kTranspose ? 16 * 128 / 16 : 2) * g, dx + 2 * g,
+                               word, ks > 0 || g > 0);
+              pair_commit(&free_s[s.slot]);
+            }
+            s.advance();
+          }
+          if (rank == 0 && ok) pair_commit(&acc_full_s[to]);
+          if (++to == 2) {
+            to = 0;
+            to_phase ^= 1u;
+          }
+        }
+      }
+      ok = __all_sync(kFull, ok);
+      at.skip(tiles * a.ksteps);
+      acc_phase ^= static_cast<uint32_t>((buf + tiles) / 2) & 1u;
+      buf = (buf + tiles) % 2;
+      leave_unit();
+    }
+    // nothing of the tensor core may be in flight when tensor memory is given back
+    if (rank == 0 && any) {
+      if (elect_one()) pair_commit_first(&done_s);
+      __syncwarp();
+      warp_wait(&done_s, 0, kWaitLimitNs);
+    }
+  } else if (warp >= 4) {
+    const int quarter = warp & 3, half = (warp - 4) >> 2;
+    const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
+    int buf = 0;
+    uint32_t acc_phase = 0;
+    while (const ProductInfo<R>* q = next_unit()) {
+      const int n = q->n, e = q->e;
+      for (int c = 0; c < q->tiles; ++c) {
+        const int m = q->m0 + c * kPairRows + 128 * rank + 32 * quarter + lane;
+        const bool live = m < a.M;
+        float scale = 1.0f;
+        if (a.ws != nullptr && live) scale = __ldg(a.ws + static_cast<size_t>(e) * a.M + m);
+        ok = warp_wait(&acc_full_s[buf], acc_phase, limit);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t src = tmem + buf * R + lanes;
+        for (int j0 = 32 * half; j0 < n; j0 += 64) {
+          uint32_t v[32];
+          __syncwarp();
+          tmem_load32(src + j0, v);
+          tmem_wait(v);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const int r = q->route[j0 + j];
+            const float y = __uint_as_float(v[j]) * (scale * q->factor[j0 + j]);
+            if (r >= 0 && live)
+              static_cast<Out*>(a.out)[static_cast<size_t>(r) * a.M + m] =
+                  rounded<Out>(y, a.out_type);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) pair_arrive_first(&acc_free_s[buf]);
+        if (++buf == 2) {
+          buf = 0;
+          acc_phase ^= 1u;
+        }
+      }
+      leave_unit();
+    }
+  }
+  if (!ok && lane == 0) atomicOr(a.t.head, MOE_RS_DEVICE_WAIT_TIMEOUT);
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  pair_sync();
+  tc_fence_after();
+  if (warp == 2) pair_tmem_free(tmem, kProductTmem);
+}
+
+// ------------------------------------------------------------------------------ host side
+namespace {
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+  static EncodeFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess) {
+      cudaGetLastError();
+      p = nullptr;
+    }
+    return reinterpret_cast<EncodeFn>(p);
+  }();
+  return fn;
+}
+
+CUtensorMapDataType map_type(int type) {
+  return type == MOE_RS_BF16   ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+         : type == MOE_RS_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                               : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+}
+
+}  // namespace
+
+bool encode_rows(CUtensorMap* map, const void* p, int type, int size, size_t cols, size_t rows) {
+  const EncodeFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[2] = {cols, rows};
+  const cuuint64_t strides[1] = {cols * size};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / size), 1};
+  const cuuint32_t one[2] = {1, 1};
+  return fn(map, map_type(type), 2, const_cast<void*>(p), dims, strides, box, one,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_weights3(CUtensorMap* map, const void* p, int type, int size, size_t cols, size_t rows,
+                     size_t E, int box_rows) {
+  const EncodeFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[3] = {cols, rows, E};
+  const cuuint64_t strides[2] = {cols * size, cols * size * rows};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / size), static_cast<cuuint32_t>(box_rows),
+                             1};
+  const cuuint32_t one[3] = {1, 1, 1};
+  return fn(map, map_type(type), 3, const_cast<void*>(p), dims, strides, box, one,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+namespace {
+
+template <bool kFp8, bool kTranspose, int R, class Out>
+cudaError_t launch_product(const CUtensorMap& w, const CUtensorMap& x, const ProductArgs& a,
+                           int pairs, cudaStream_t st) {
+  auto* k = mrs_product_kernel<kFp8, kTranspose, R, Out>;
+  constexpr size_t smem = ProductShape<R>::kSmem;
+  static SmemGrant granted;
+  const cudaError_t err = grant_smem(reinterpret_cast<const void*>(k), smem, granted);
+  if (err != cudaSuccess) return err;
+  return launch_pairs(k, pairs, kProductThreads, smem, st, w, x, a);
+}
+
+template <int R, class Out>
+cudaError_t launch_product(bool fp8, bool transpose, const CUtensorMap& w, const CUtensorMap& x,
+                           const ProductArgs& a, int pairs, cudaStream_t st) {
+  return transpose ? launch_product<false, true, R, Out>(w, x, a, pairs, st)
+         : fp8     ? launch_product<true, false, R, Out>(w, x, a, pairs, st)
+                   : launch_product<false, false, R, Out>(w, x, a, pairs, st);
+}
+
+size_t most_tiles(int T, int E, int topk, int block_m, int rows) {
+  const size_t P = moe_sort_max_padded(T, E, topk, block_m), n = static_cast<size_t>(T) * topk;
+  return P / rows + (n < static_cast<size_t>(E) ? n : E);
+}
+
+// The product (transpose: the rows' gradient, whose contraction runs over W's rows).
+int product(const void* x, int type, const float* x_scales, int per_route, const void* w,
+            const float* w_scales, int T, int E, int topk, int cols, int outs, int block_m,
+            const int32_t* sid, const float* sw, const int32_t* eid, const int32_t* npp, void* out,
+            int out_type, void* workspace, size_t workspace_bytes, bool transpose,
+            cudaStream_t stream) {
+  const bool fp8 = type == MOE_RS_FP8;
+  if (T < 0) return MOE_RS_ERR_BAD_TOKENS;
+  if (E < 1 || E > kMaxExperts) return MOE_RS_ERR_BAD_EXPERTS;
+  if (topk < 1 || topk > kMaxTopk) return MOE_RS_ERR_BAD_TOPK;
+  if (block_m < 1 || block_m > 1024 || (block_m & (block_m - 1)) != 0)
+    return MOE_RS_ERR_BAD_BLOCK_M;
+  if (type != MOE_RS_BF16 && type != MOE_RS_FP16 && (!fp8 || transpose)) return MOE_RS_ERR_BAD_DTYPE;
+  if (out_type != MOE_RS_BF16 && out_type != MOE_RS_FP16 && out_type != MOE_RS_FP32)
+    return MOE_RS_ERR_BAD_DTYPE;
+  if (cols < 8 || cols > MOE_RS_PRODUCT_MAX_COLS || cols % (fp8 ? 16 : 8) != 0 || outs < 8 ||
+      outs > MOE_RS_PRODUCT_MAX_COLS || outs % 8 != 0)
+    return MOE_RS_ERR_BAD_COLS;
+  if (static_cast<int64_t>(T) * topk > INT32_MAX ||
+      static_cast<int64_t>(moe_sort_max_padded(T, E, topk, block_m)) > INT32_MAX)
+    return MOE_RS_ERR_OVERFLOW;
+  const size_t need = moe_experts_product_workspace_bytes(T, E, topk, block_m);
+  if (!workspace || workspace_bytes < need) return MOE_RS_ERR_WORKSPACE;
+  if (T == 0) return MOE_RS_OK;
+  if (!x || !w || !sid || !eid || !npp || !out || (fp8 && (!x_scales || !w_scales)))
+    return MOE_RS_ERR_NULL_POINTER;
+  if (!fp8 && (x_scales || w_scales)) return MOE_RS_ERR_BAD_DTYPE;
+  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(x_scales, 4) || !aligned(w_scales, 4) ||
+      !aligned(sid, 4) || !aligned(sw, 4) || !aligned(eid, 4) || !aligned(npp, 4) ||
+      !aligned(out, 16) || !aligned(workspace, 16))
+    return MOE_RS_ERR_MISALIGNED;
+  const size_t routes = static_cast<size_t>(T) * topk, size = fp8 ? 1 : 2;
+  const size_t xrows = per_route ? routes : static_cast<size_t>(T);
+  const size_t wrows = static_cast<size_t>(E) * outs;
+  const size_t P = moe_sort_max_padded(T, E, topk, block_m);
+  const int M = transpose ? cols : outs, K = transpose ? outs : cols;
+  const Span outs_s[] = {span(out, routes * M * (out_type == MOE_RS_FP32 ? 4 : 2)),
+                         span(workspace, workspace_bytes)};
+  const Span ins[] = {span(x, xrows * K * size),
+                      span(x_scales, x_scales ? 4 * xrows : 0),
+                      span(w, wrows * cols * size),
+                      span(w_scales, w_scales ? 4 * wrows : 0),
+                      span(sid, 4 * P),
+                      span(sw, sw ? 4 * P : 0),
+                      span(eid, 4 * (P / block_m)),
+                      span(npp, 4)};
+  if (any_alias(outs_s, 2, ins, 8)) return MOE_RS_ERR_ALIAS;
+  const int sms = sm_count();
+  if (sms == 0) return launch_status(cudaErrorInvalidDevice);
+  const size_t hit = routes < static_cast<size_t>(E) ? routes : E;
+  const int R = routes <= 48 * hit ? 64 : 256;
+  TableArgs ta{};
+  ta.t = product_table(workspace, E);
+  ta.eid = eid;
+  ta.sid = sid;
+  ta.npp = npp;
+  ta.E = E;
+  ta.B = block_m;
+  while ((1 << ta.log2B) < block_m) ++ta.log2B;
+  ta.max_rows = static_cast<int>(P);
+  ta.routes = static_cast<int>(routes);
+  ta.rows = R;
+  const size_t tiles = most_tiles(T, E, topk, block_m, R);
+  ta.max_tiles = static_cast<int>(tiles);
+  ProductArgs a{};
+  a.t = ta.t;
+  a.sid = sid;
+  a.sw = sw;
+  a.xs = x_scales;
+  a.ws = w_scales;
+  a.out = out;
+  a.wait_limit_ns = product_wait_limit();
+  a.routes = static_cast<int>(routes);
+  a.topk = topk;
+  a.per_route = per_route != 0;
+  a.max_tiles = ta.max_tiles;
+  a.E = E;
+  a.M = M;
+  a.K = K;
+  a.P = static_cast<int>(P);
+  a.mtiles = (M + kPairRows - 1) / kPairRows;
+  a.ksteps = (K * static_cast<int>(size) + 127) / 128;
+  a.type = type == MOE_RS_BF16 ? 1 : 0;
+  a.out_type = out_type;
+  const int pairs = sms / 2;
+  a.chunk = 1;
+  a.nchunk = (a.mtiles + a.chunk - 1) / a.chunk;
+  if (tiles * a.nchunk > INT32_MAX / 2) return MOE_RS_ERR_OVERFLOW;
+  CUtensorMap wmap, xmap;
+  if (!encode_weights3(&wmap, w, type, static_cast<int>(size), cols, outs, E, transpose ? 64 : 128) ||
+      !encode_rows(&xmap, x, type, static_cast<int>(size), K, xrows))
+    return MOE_RS_ERR_LAUNCH;
+  cudaError_t err = launch_product_table(ta, stream);
+  if (err != cudaSuccess) return launch_status(err);
+  const size_t units = tiles * a.nchunk;
+  const int grid = units < static_cast<size_t>(pairs) ? static_cast<int>(units) : pairs;
+  auto go = [&](auto o) {
+    using Out = decltype(o);
+    return R == 64 ? launch_product<64, Out>(fp8, transpose, wmap, xmap, a, grid, stream)
+                   : launch_product<256, Out>(fp8, transpose, wmap, xmap, a, grid, stream);
+  };
+  return launch_status(out_type == MOE_RS_FP32 ? go(float{}) : go(uint16_t{}));
+}
+
+}  // namespace
+}  // namespace mrs
+
+using namespace mrs;
+
+extern "C" {
+
+size_t moe_experts_product_workspace_bytes(int T, int E, int topk, int block_m) {
+  if (T < 0 || E < 1 || E > kMaxExperts || topk < 1 || topk > kMaxTopk || block_m < 1 ||
+      block_m > 1024 || (block_m & (block_m - 1)) != 0)
+    return 0;
+  if (static_cast<int64_t>(T) * topk > INT32_MAX ||
+      static_cast<int64_t>(moe_sort_max_padded(T, E, topk, block_m)) > INT32_MAX)
+    return 0;
+  return product_table_bytes(E, most_tiles(T, E, topk, block_m, kTileRowsLeast));
+}
+
+int moe_experts_product(const void* x, int x_dtype, const float* x_scales, int x_per_route,
+                        const void* w, const float* w_scales, int T, int E, int topk, int cols,
+                        int outs, int block_m, const int32_t* sorted_token_ids,
+                        const float* sorted_weights, const int32_t* expert_ids,
+                        const int32_t* num_tokens_post_pad, void* out, int out_dtype,
+                        void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  return product(x, x_dtype, x_scales, x_per_route, w, w_scales, T, E, topk, cols, outs, block_m,
+                 sorted_token_ids, sorted_weights, expert_ids, num_tokens_post_pad, out, out_dtype,
+                 workspace, workspace_bytes, false, stream);
+}
+
+int moe_experts_grad_rows(const void* grad, int dtype, int g_per_route, const void* w, int T, int E,
+                          int topk, int cols, int outs, int block_m,
+                          const int32_t* sorted_token_ids, const int32_t* expert_ids,
+                          const int32_t* num_tokens_post_pad, void* grad_rows, int out_dtype,
+                          void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  return product(grad, dtype, nullptr, g_per_route, w, nullptr, T, E, topk, cols, outs, block_m,
+                 sorted_token_ids, nullptr, expert_ids, num_tokens_post_pad, grad_rows, out_dtype,
+                 workspace, workspace_bytes, true, stream);
+}
+
+}  // extern "C"

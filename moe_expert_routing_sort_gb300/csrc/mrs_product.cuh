@@ -1,0 +1,105 @@
+// mrs_product.cuh -- what the experts' products in 16 and 8 bits and their gradients share: the
+// table of row tiles that a call's sorted list is cut into, and the host side of tensor maps.
+#pragma once
+
+#include <climits>
+#include <cstdint>
+
+#include "mrs_args.h"
+#include "mrs_internal.h"
+#include "mrs_tc.cuh"
+
+namespace mrs {
+
+// The workspace: the status word and the number of tiles, the first block of every expert's run
+// (offs[E]: the blocks of the list), the rows of it up to the last route, and the tiles.
+struct ProductTable {
+  int32_t* head;   // [0] status bits (sticky), [1] tiles
+  int32_t* offs;   // [E + 1]
+  int32_t* used;   // [E]
+  int4* tiles;     // expert, first row of the list, rows, -
+};
+constexpr int kTileRowsLeast = 64;
+
+inline size_t product_table_bytes(int E, size_t max_tiles) {
+  return 256 + align16(sizeof(int32_t) * (static_cast<size_t>(E) + 1)) +
+         align16(sizeof(int32_t) * static_cast<size_t>(E)) + sizeof(int4) * max_tiles;
+}
+inline ProductTable product_table(void* workspace, int E) {
+  char* p = static_cast<char*>(workspace);
+  ProductTable t{};
+  t.head = reinterpret_cast<int32_t*>(p);
+  p += 256;
+  t.offs = reinterpret_cast<int32_t*>(p);
+  p += align16(sizeof(int32_t) * (static_cast<size_t>(E) + 1));
+  t.used = reinterpret_cast<int32_t*>(p);
+  p += align16(sizeof(int32_t) * static_cast<size_t>(E));
+  t.tiles = reinterpret_cast<int4*>(p);
+  return t;
+}
+
+struct TableArgs {
+  ProductTable t;
+  const int32_t *eid, *sid, *npp;
+  int E, B, log2B, max_rows, routes;
+  int rows;       // rows of a tile
+  int max_tiles;
+  int want_used;  // rows up to the last route are asked for
+};
+// One CTA: the boundaries of the runs, their tiles' places by a prefix sum, and the tiles.
+cudaError_t launch_product_table(const TableArgs& a, cudaStream_t st);
+
+// A tensor of up to three dimensions of `size`-byte elements; `box` elements of the innermost
+// dimension are 128 bytes, swizzled by 128; what lies outside reads as zero.  rank 2: for gathers
+// of rows (a box is one row high).
+bool encode_rows(CUtensorMap* map, const void* p, int type, int size, size_t cols, size_t rows);
+bool encode_weights3(CUtensorMap* map, const void* p, int type, int size, size_t cols, size_t rows,
+                     size_t E, int box_rows);
+
+// Waits give up after the test hook's limit, but not before whatever a CTA has in flight has had
+// ample time to land.
+inline unsigned long long product_wait_limit() {
+  const unsigned long long v = debug_wait_limit_ns();
+  return v == 0ull || v > 5000000ull ? v : 5000000ull;
+}
+
+// Launch in clusters of two CTAs, ordered like launch_pdl.
+template <class... Params, class... Args>
+cudaError_t launch_pairs(void (*kernel)(Params...), int pairs, int threads, size_t smem,
+                         cudaStream_t st, Args&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(2 * pairs);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+// A place in a ring of S slots, and the parity of its round.
+template <int S>
+struct Ring {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void advance() {
+    if (++slot == S) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
+  __device__ __forceinline__ void skip(int steps) {
+    const int to = slot + steps;
+    phase ^= static_cast<uint32_t>(to / S) & 1u;
+    slot = to % S;
+  }
+};
+
+}  // namespace mrs

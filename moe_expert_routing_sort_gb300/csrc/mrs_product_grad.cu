@@ -1,0 +1,409 @@
+// mrs_product_grad.cu -- gradient of the experts' products' weights.
+//
+// For every expert e, m < outs, k < cols:
+//   grad_w[e, m, k] = sum over routes r of e in the list of G[row, m] * X[row', k]
+// with fp32 sums, rounded once.  The contraction runs over the ragged rows of an expert, which lie
+// one behind another in the sorted list: both operands are gathered row by row, 128 bytes of four
+// rows an instruction, so that in shared memory each position of the contraction is a line of
+// consecutive m (or k), the transposed layout of the tensor core.  Rows past an expert's last are
+// read as zeros.
+//
+// A pair of CTAs computes tiles of 256 m by 256 k of one expert, 64 rows a step; each CTA brings
+// 128 m and 128 k.  The tasks of the warps are those of mrs_product.cu.  Experts without routes get
+// their zeros from the storing warps alone.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "mrs_mx.cuh"
+#include "mrs_product.cuh"
+
+namespace mrs {
+
+struct WeightGradArgs {
+  ProductTable t;
+  const int32_t* sid;
+  void* out;
+  unsigned long long wait_limit_ns;
+  int routes, topk, g_per_route, x_per_route, g_rows, x_rows;
+  int E, N, K, P, B;
+  int mtiles, ktiles;
+  int type, out_type;
+  int wide;  // rows of the output start on 32 bytes
+};
+
+constexpr int kGradThreads = 384;
+constexpr int kGradTmem = 512;
+constexpr int kGradSlots = 6;
+constexpr int kGradInfo = 4;
+constexpr int kGradUsers = 10;
+constexpr int kGradDeep = 64;            // rows of a step
+constexpr int kGradTile = 128 * 128;     // bytes of an operand in a CTA and step
+constexpr size_t kGradSmem = static_cast<size_t>(kGradSlots) * 2 * kGradTile + 1024;
+
+struct GradInfo {
+  int e, p0, rows, m0, k0;  // e < 0: no more units
+};
+
+template <class Out>
+__global__ void __launch_bounds__(kGradThreads, 1)
+    mrs_weight_grad_kernel(const __grid_constant__ CUtensorMap gmap,
+                           const __grid_constant__ CUtensorMap xmap, const WeightGradArgs a) {
+  constexpr int S = kGradSlots;
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ unsigned long long full_s[S], free_s[S], other_s[S], acc_full_s[2], acc_free_s[2],
+      info_full_s[kGradInfo], info_free_s[kGradInfo], done_s;
+  __shared__ GradInfo info_s[kGradInfo];
+  __shared__ uint32_t tmem_s;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = static_cast<int>(pair_rank());
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t gbase = base, xbase = base + S * kGradTile;
+  const unsigned long long limit = a.wait_limit_ns;
+  pdl_trigger();
+  if (tid == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full_s[s], 1);
+      mbar_init(&free_s[s], 1);
+      mbar_init(&other_s[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full_s[b], 1);
+      mbar_init(&acc_free_s[b], 16);
+    }
+    for (int i = 0; i < kGradInfo; ++i) {
+      mbar_init(&info_full_s[i], 1);
+      mbar_init(&info_free_s[i], kGradUsers);
+    }
+    mbar_init(&done_s, 1);
+    fence_mbar_init();
+  }
+  if (warp == 2) pair_tmem_alloc(&tmem_s, kGradTmem);
+  tc_fence_before();
+  __syncthreads();
+  pair_sync();
+  tc_fence_after();
+  const uint32_t tmem = tmem_s;
+  pdl_wait();
+
+  bool ok = true;
+  Ring<kGradInfo> at_info;
+  auto next_unit = [&]() -> const GradInfo* {
+    ok = ok && warp_wait(&info_full_s[at_info.slot], at_info.phase, limit);
+    if (!ok) return nullptr;
+    const GradInfo* q = &info_s[at_info.slot];
+    return q->e < 0 ? nullptr : q;
+  };
+  auto leave_unit = [&] {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&info_free_s[at_info.slot]);
+    at_info.advance();
+  };
+
+  if (warp == 0) {
+    Ring<S> at;
+    long long issued = 0;
+    const int quad = lane & 15, seg = lane >> 4;
+    while (const GradInfo* q = next_unit()) {
+      const int p0 = q->p0, rows = q->rows;
+      const int gx = q->m0 + 128 * rank + 64 * seg, xx = q->k0 + 128 * rank + 64 * seg;
+      auto routes_of = [&](int first, int (&s)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int at_row = first + 4 * quad + i;
+          s[i] = at_row < rows ? __ldg(a.sid + p0 + at_row) : -1;
+        }
+      };
+      int ahead[4];
+      routes_of(0, ahead);
+      for (int r0 = 0; r0 < rows; r0 += kGradDeep) {
+        int g[4], x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const bool is = ahead[i] >= 0 && ahead[i] < a.routes;
+          const int token = is ? ahead[i] / a.topk : 0;
+          // past the last row of either: zeros
+          g[i] = !is ? a.g_rows : (a.g_per_route ? ahead[i] : token);
+          x[i] = !is ? a.x_rows : (a.x_per_route ? ahead[i] : token);
+        }
+        if (r0 + kGradDeep < rows) routes_of(r0 + kGradDeep, ahead);
+        ok = warp_wait(&free_s[at.slot], at.phase ^ 1u, limit);
+        if (!ok) break;
+        if (elect_one()) mbar_expect(&full_s[at.slot], 2 * kGradTile);
+        const uint32_t to = at.slot * kGradTile + seg * (kGradDeep * 128) + quad * 512;
+        tma_gather4(gbase + to, &gmap, gx, make_int4(g[0], g[1], g[2], g[3]), &full_s[at.slot]);
+        tma_gather4(xbase + to, &xmap, xx, make_int4(x[0], x[1], x[2], x[3]), &full_s[at.slot]);
+        ++issued;
+        at.advance();
+      }
+      leave_unit();
+    }
+    // nothing may land in the shared memory of a CTA that has left
+    for (long long i = issued > S ? issued - S : 0; i < issued; ++i)
+      warp_wait(&full_s[i % S], static_cast<uint32_t>(i / S) & 1u, kWaitLimitNs);
+  } else if (warp == 1) {
+    const int each = a.mtiles * a.ktiles, units = a.E * each, step = gridDim.x >> 1;
+    for (int u0 = blockIdx.x >> 1; ok && u0 < units; u0 += 32 * step) {
+      // a lane looks up one of the next 32 units
+      const long long u = u0 + static_cast<long long>(lane) * step;
+      int e = -1, p0 = 0, rows = 0, m0 = 0, k0 = 0;
+      if (u < units) {
+        e = static_cast<int>(u) / each;
+        const int i = static_cast<int>(u) - e * each, mt = i / a.ktiles;
+        m0 = mt * 256;
+        k0 = (i - mt * a.ktiles) * 256;
+        // (a table that another call overwrites must not lead out of this call's buffers)
+        p0 = static_cast<int>(min(max(static_cast<long long>(__ldg(a.t.offs + e)) * a.B, 0ll),
+                                  static_cast<long long>(a.P)));
+        rows = min(max(__ldg(a.t.used + e), 0), a.P - p0);
+      }
+      for (int i = 0; ok && i < 32; ++i) {
+        const int ei = __shfl_sync(kFull, e, i);
+        if (ei < 0) break;
+        ok = warp_wait(&info_free_s[at_info.slot], at_info.phase ^ 1u, limit);
+        if (!ok) break;
+        if (lane == i) {
+          info_s[at_info.slot] = GradInfo{e, p0, rows, m0, k0};
+          mbar_arrive(&info_full_s[at_info.slot]);
+        }
+        __syncwarp();
+        at_info.advance();
+      }
+    }
+    ok = ok && warp_wait(&info_free_s[at_info.slot], at_info.phase ^ 1u, limit);
+    if (ok && lane == 0) {
+      info_s[at_info.slot].e = -1;
+      mbar_arrive(&info_full_s[at_info.slot]);
+    }
+  } else if (warp == 2) {
+    Ring<S> at;
+    int buf = 0;
+    uint32_t acc_phase = 0;
+    bool any = false;
+    const uint32_t word = pair_word(a.type, true, true, 256);
+    while (const GradInfo* q = next_unit()) {
+      const int rows = q->rows, steps = (rows + kGradDeep - 1) / kGradDeep;
+      if (steps > 0) {
+        any = true;
+        if (elect_one()) {
+          Ring<S> s = at;
+          if (rank == 0) ok = pair_wait(&acc_free_s[buf], acc_phase ^ 1u, limit);
+          tc_fence_after();
+          for (int ks = 0; ok && ks < steps; ++ks) {
+            ok = thread_wait(&full_s[s.slot], s.phase, limit);
+            if (!ok) break;
+            if (rank != 0) {
+              pair_arrive_first(&other_s[s.slot]);
+            } else {
+              ok = pair_wait(&other_s[s.slot], s.phase, limit);
+              if (!ok) break;
+              tc_fence_after();
+              const uint64_t dg = desc_lines128(gbase + s.slot * kGradTile, kGradDeep);
+              const uint64_t dx = desc_lines128(xbase + s.slot * kGradTile, kGradDeep);
+              const int parts = (rows - ks * kGradDeep + 15) >> 4;
+#pragma unroll
+              for (int g = 0; g < 4; ++g)
+                if (g < parts)  // else rows past the last: zeros
+                  pair_mma<false>(tmem + buf * 256, dg + 128 * g, dx + 128 * g, word,
+                                  ks > 0 || g > 0);
+              pair_commit(&free_s[s.slot]);
+            }
+            s.advance();
+          }
+          if (rank == 0 && ok) pair_commit(&acc_full_s[buf]);
+        }
+        ok = __all_sync(kFull, ok);
+        at.skip(steps);
+        if (++buf == 2) {
+          buf = 0;
+          acc_phase ^= 1u;
+        }
+      }
+      leave_unit();
+    }
+    if (rank == 0 && any) {
+      if (elect_one()) pair_commit_first(&done_s);
+      __syncwarp();
+      warp_wait(&done_s, 0, kWaitLimitNs);
+    }
+  } else if (warp >= 4) {
+    const int quarter = warp & 3, half = (warp - 4) >> 2;
+    const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
+    int buf = 0;
+    uint32_t acc_phase = 0;
+    while (const GradInfo* q = next_unit()) {
+      const int m = q->m0 + 128 * rank + 32 * quarter + lane, k0 = q->k0;
+      const bool some = q->rows > 0;
+      Out* row = static_cast<Out*>(a.out) +
+                 (static_cast<size_t>(q->e) * a.N + min(m, a.N - 1)) * a.K;
+      if (some) {
+        ok = warp_wait(&acc_full_s[buf], acc_phase, limit);
+        if (!ok) break;
+        tc_fence_after();
+      }
+      const uint32_t src = tmem + buf * 256 + lanes;
+#pragma unroll 1
+      for (int c0 = 32 * half; c0 < 256; c0 += 64) {
+        uint32_t v[32];
+        __syncwarp();
+        if (some) {
+          tmem_load32(src + c0, v);
+          tmem_wait(v);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) v[c] = 0u;
+        }
+        if (m >= a.N) continue;
+        if constexpr (sizeof(Out) == 4) {
+#pragma unroll
+          for (int c = 0; c < 32; c += 8)
+            if (k0 + c0 + c < a.K) store32(row + k0 + c0 + c, a.wide != 0, v + c);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const float lo = __uint_as_float(v[2 * c]), hi = __uint_as_float(v[2 * c + 1]);
+            if (a.out_type == MOE_RS_BF16) {
+              const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+              v[c] = *reinterpret_cast<const uint32_t*>(&h);
+            } else {
+              const __half2 h = __floats2half2_rn(lo, hi);
+              v[c] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+          }
+#pragma unroll
+          for (int c = 0; c < 32; c += 16) {
+            const int left = a.K - (k0 + c0 + c);  // a multiple of 8
+            Out* p = row + k0 + c0 + c;
+            if (left >= 16) store32(p, a.wide != 0, v + c / 2);
+            else if (left > 0)
+              *reinterpret_cast<uint4*>(p) = make_uint4(v[c / 2], v[c / 2 + 1], v[c / 2 + 2],
+                                                        v[c / 2 + 3]);
+          }
+        }
+      }
+      if (some) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) pair_arrive_first(&acc_free_s[buf]);
+        if (++buf == 2) {
+          buf = 0;
+          acc_phase ^= 1u;
+        }
+      }
+      leave_unit();
+    }
+  }
+  if (!ok && lane == 0) atomicOr(a.t.head, MOE_RS_DEVICE_WAIT_TIMEOUT);
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  pair_sync();
+  tc_fence_after();
+  if (warp == 2) pair_tmem_free(tmem, kGradTmem);
+}
+
+namespace {
+
+template <class Out>
+cudaError_t launch_weight_grad(const CUtensorMap& g, const CUtensorMap& x, const WeightGradArgs& a,
+                               int pairs, cudaStream_t st) {
+  auto* k = mrs_weight_grad_kernel<Out>;
+  static SmemGrant granted;
+  const cudaError_t err = grant_smem(reinterpret_cast<const void*>(k), kGradSmem, granted);
+  if (err != cudaSuccess) return err;
+  return launch_pairs(k, pairs, kGradThreads, kGradSmem, st, g, x, a);
+}
+
+}  // namespace
+}  // namespace mrs
+
+using namespace mrs;
+
+extern "C" int moe_experts_grad_weights(
+    const void* grad, int dtype, int g_per_route, const void* x, int x_per_route, int T, int E,
+    int topk, int cols, int outs, int block_m, const int32_t* sorted_token_ids,
+    const int32_t* expert_ids, const int32_t* num_tokens_post_pad, void* grad_w, int out_dtype,
+    void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  if (T < 0) return MOE_RS_ERR_BAD_TOKENS;
+  if (E < 1 || E > kMaxExperts) return MOE_RS_ERR_BAD_EXPERTS;
+  if (topk < 1 || topk > kMaxTopk) return MOE_RS_ERR_BAD_TOPK;
+  if (block_m < 1 || block_m > 1024 || (block_m & (block_m - 1)) != 0)
+    return MOE_RS_ERR_BAD_BLOCK_M;
+  if (dtype != MOE_RS_BF16 && dtype != MOE_RS_FP16) return MOE_RS_ERR_BAD_DTYPE;
+  if (out_dtype != dtype && out_dtype != MOE_RS_FP32) return MOE_RS_ERR_BAD_DTYPE;
+  if (cols < 8 || cols > MOE_RS_PRODUCT_MAX_COLS || cols % 8 != 0 || outs < 8 ||
+      outs > MOE_RS_PRODUCT_MAX_COLS || outs % 8 != 0)
+    return MOE_RS_ERR_BAD_COLS;
+  if (static_cast<int64_t>(T) * topk > INT32_MAX ||
+      static_cast<int64_t>(moe_sort_max_padded(T, E, topk, block_m)) > INT32_MAX)
+    return MOE_RS_ERR_OVERFLOW;
+  const size_t need = moe_experts_product_workspace_bytes(T, E, topk, block_m);
+  if (!workspace || workspace_bytes < need) return MOE_RS_ERR_WORKSPACE;
+  const size_t routes = static_cast<size_t>(T) * topk;
+  const size_t out_size = out_dtype == MOE_RS_FP32 ? 4 : 2;
+  const size_t n = static_cast<size_t>(E) * outs * cols;
+  if (!grad_w) return MOE_RS_ERR_NULL_POINTER;
+  if (T > 0 && (!grad || !x || !sorted_token_ids || !expert_ids || !num_tokens_post_pad))
+    return MOE_RS_ERR_NULL_POINTER;
+  if (!aligned(grad, 16) || !aligned(x, 16) || !aligned(sorted_token_ids, 4) ||
+      !aligned(expert_ids, 4) || !aligned(num_tokens_post_pad, 4) || !aligned(grad_w, 16) ||
+      !aligned(workspace, 16))
+    return MOE_RS_ERR_MISALIGNED;
+  if (T == 0)  // no route of any expert
+    return launch_status(cudaMemsetAsync(grad_w, 0, n * out_size, stream));
+  const size_t grows = g_per_route ? routes : static_cast<size_t>(T);
+  const size_t xrows = x_per_route ? routes : static_cast<size_t>(T);
+  const size_t P = moe_sort_max_padded(T, E, topk, block_m);
+  const Span outs_s[] = {span(grad_w, n * out_size), span(workspace, workspace_bytes)};
+  const Span ins[] = {span(grad, 2 * grows * outs), span(x, 2 * xrows * cols),
+                      span(sorted_token_ids, 4 * P), span(expert_ids, 4 * (P / block_m)),
+                      span(num_tokens_post_pad, 4)};
+  if (any_alias(outs_s, 2, ins, 5)) return MOE_RS_ERR_ALIAS;
+  const int64_t units = static_cast<int64_t>(E) * ((outs + 255) / 256) * ((cols + 255) / 256);
+  if (units > INT32_MAX / 2) return MOE_RS_ERR_OVERFLOW;
+  const int sms = sm_count();
+  if (sms == 0) return launch_status(cudaErrorInvalidDevice);
+  TableArgs ta{};
+  ta.t = product_table(workspace, E);
+  ta.eid = expert_ids;
+  ta.sid = sorted_token_ids;
+  ta.npp = num_tokens_post_pad;
+  ta.E = E;
+  ta.B = block_m;
+  while ((1 << ta.log2B) < block_m) ++ta.log2B;
+  ta.max_rows = static_cast<int>(P);
+  ta.routes = static_cast<int>(routes);
+  ta.rows = INT32_MAX / 2;  // no tiles are wanted
+  ta.max_tiles = 0;
+  ta.want_used = 1;
+  WeightGradArgs a{};
+  a.t = ta.t;
+  a.sid = sorted_token_ids;
+  a.out = grad_w;
+  a.wait_limit_ns = product_wait_limit();
+  a.routes = static_cast<int>(routes);
+  a.topk = topk;
+  a.g_per_route = g_per_route != 0;
+  a.x_per_route = x_per_route != 0;
+  a.g_rows = static_cast<int>(grows);
+  a.x_rows = static_cast<int>(xrows);
+  a.E = E;
+  a.N = outs;
+  a.K = cols;
+  a.P = static_cast<int>(P);
+  a.B = block_m;
+  a.mtiles = (outs + 255) / 256;
+  a.ktiles = (cols + 255) / 256;
+  a.type = dtype == MOE_RS_BF16 ? 1 : 0;
+  a.out_type = out_dtype;
+  a.wide = aligned(grad_w, 32) && cols * out_size % 32 == 0;
+  CUtensorMap gmap, xmap;
+  if (!encode_rows(&gmap, grad, dtype, 2, outs, grows) ||
+      !encode_rows(&xmap, x, dtype, 2, cols, xrows))
+    return MOE_RS_ERR_LAUNCH;
+  cudaError_t err = launch_product_table(ta, stream);
+  if (err != cudaSuccess) return launch_status(err);
+  const int pairs = units < sms / 2 ? static_cast<int>(units) : sms / 2;
+  return launch_status(out_dtype == MOE_RS_FP32
+                           ? launch_weight_grad<float>(gmap, xmap, a, pairs, stream)
+                           : launch_weight_grad<uint16_t>(gmap, xmap, a, pairs, stream));
+}

@@ -159,4 +159,112 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       "l"(map), "r"(smem_u32(mbar)), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
+
+// ------------------------------------------------------------------------ pairs of CTAs
+// Two CTAs of a cluster work on one product of 256 rows: each holds its half of both operands and
+// of the sums, and the CTA of rank 0 issues for both.
+__device__ __forceinline__ uint32_t pair_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// Every thread of both CTAs; what either wrote to shared memory before is visible behind it.
+__device__ __forceinline__ void pair_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+__device__ __forceinline__ void pair_tmem_alloc(uint32_t* where, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                   smem_u32(where)),
+               "r"(cols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void pair_tmem_free(uint32_t addr, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols)
+               : "memory");
+}
+// One arrival on the barrier that lies at this address in the CTA of rank 0.
+__device__ __forceinline__ void pair_arrive_first(unsigned long long* mbar) {
+  asm volatile(
+      "{ .reg .b32 at; mapa.shared::cluster.u32 at, %0, 0;\n"
+      " mbarrier.arrive.release.cluster.shared::cluster.b64 _, [at]; }" ::"r"(smem_u32(mbar))
+      : "memory");
+}
+// thread_wait for arrivals that may come from the other CTA.
+__device__ __forceinline__ bool pair_wait(unsigned long long* mbar, uint32_t phase,
+                                          unsigned long long limit_ns) {
+  if (limit_ns == 0ull) return false;
+  unsigned long long t0 = 0ull;
+  for (uint32_t i = 1;; ++i) {
+    uint32_t done;
+    asm volatile(
+        "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; "
+        "selp.u32 %0, 1, 0, p; }"
+        : "=r"(done)
+        : "r"(smem_u32(mbar)), "r"(phase)
+        : "memory");
+    if (done != 0u) return true;
+    if ((i & 63u) != 0u) continue;
+    const unsigned long long t = globaltimer_ns();
+    if (t0 == 0ull) t0 = t;
+    else if (t - t0 > limit_ns) return false;
+  }
+}
+// Arrives on the barrier at this address of both CTAs once everything this thread issued before
+// has completed.
+__device__ __forceinline__ void pair_commit(unsigned long long* mbar) {
+  asm volatile(
+      "{ .reg .b16 m; mov.b16 m, 3;\n"
+      " tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], m; }" ::"r"(smem_u32(mbar))
+      : "memory");
+}
+__device__ __forceinline__ void pair_commit_first(unsigned long long* mbar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+          smem_u32(mbar))
+      : "memory");
+}
+// 256 x N products of 32 bytes of each row; 16-bit operands, or e4m3 ones.
+template <bool kFp8>
+__device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t word,
+                                         bool add) {
+  if constexpr (kFp8)
+    asm volatile(
+        "{ .reg .pred p; setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p; }" ::"r"(d),
+        "l"(a), "l"(b), "r"(word), "r"(add ? 1u : 0u)
+        : "memory");
+  else
+    asm volatile(
+        "{ .reg .pred p; setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
+        "l"(a), "l"(b), "r"(word), "r"(add ? 1u : 0u)
+        : "memory");
+}
+// Instruction word of these kinds: fp32 sums, M = 256 rows of both CTAs by N; type: 0 fp16 or e4m3,
+// 1 bf16 (both operands); an operand is transposed where its rows run along the contraction.
+__device__ __forceinline__ uint32_t pair_word(int type, bool transpose_a, bool transpose_b, int N) {
+  return (1u << 4) | (static_cast<uint32_t>(type) << 7) | (static_cast<uint32_t>(type) << 10) |
+         (transpose_a ? 1u << 15 : 0u) | (transpose_b ? 1u << 16 : 0u) |
+         (static_cast<uint32_t>(N >> 3) << 17) | ((256u >> 4) << 24);
+}
+// A transposed operand: lines of 64 elements (128 bytes, swizzled by 128) along its rows, one line
+// for each of the contraction's `deep` positions, the next 64 elements behind them.
+__device__ __forceinline__ uint64_t desc_lines128(uint32_t smem_addr, int deep) {
+  return static_cast<uint64_t>((smem_addr & 0x3ffffu) >> 4) |
+         (static_cast<uint64_t>(deep * 128 >> 4) << 16) | (uint64_t{1024 >> 4} << 32) |
+         (uint64_t{1} << 46) | (uint64_t{2} << 61);
+}
+// 128 bytes, from element x on, of four rows of a matrix; rows past its last read as zeros.
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, int x, int4 row,
+                                            unsigned long long* mbar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+      "l"(map), "r"(smem_u32(mbar)), "r"(x), "r"(row.x), "r"(row.y), "r"(row.z), "r"(row.w)
+      : "memory");
+}
+
 }  // namespace mrs

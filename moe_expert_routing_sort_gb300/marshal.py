@@ -92,6 +92,9 @@ _OPERATIONS = {
     "moe_rms_norm_backward": (8, "16q"),
     "moe_swiglu": (9, "10q"),
     "moe_swiglu_backward": (10, "10q"),
+    "moe_experts_product": (11, "21q"),
+    "moe_experts_grad_rows": (12, "18q"),
+    "moe_experts_grad_weights": (13, "19q"),
 }
 
 
