@@ -15,11 +15,12 @@
 // tensor copies, four rows an instruction.
 //
 // The warps of a CTA each have one task:
-//   0      copies of a step's weights and rows
+//   0      copies of a step's weights
 //   1      the list: rows, routes and factors of the next units into a ring in shared memory
-//   2      in the first CTA of a pair the products, in the second the word that its half is there
+//   2      in the first CTA of a pair the products; both CTAs' copies are counted on its barriers
 //   3      nothing
 //   4-11   finished tiles from tensor memory to the output rows, while the next one is computed
+//   12-15  copies of a step's rows, a quarter of them each
 // Every wait is bounded; one that gives up ends its warp's task with the status bit set.  The CTAs
 // of a pair leave together.
 #include <cuda_bf16.h>
@@ -134,11 +135,12 @@ struct ProductArgs {
   int out_type;
 };
 
-constexpr int kProductThreads = 384;
+constexpr int kProductThreads = 512;
+constexpr int kGatherers = 4;
 constexpr int kProductTmem = 512;
 constexpr int kPairRows = 256;  // m of a tile
 constexpr int kInfoSlots = 3;
-constexpr int kInfoUsers = 10;  // copies, products, eight storing warps
+constexpr int kInfoUsers = 10 + kGatherers;  // weights, products, eight storing warps, rows
 
 template <int R>
 struct ProductShape {
@@ -177,7 +179,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   using Sh = ProductShape<R>;
   constexpr int S = Sh::kSlots;
   extern __shared__ unsigned char smem_raw[];
-  __shared__ unsigned long long full_s[S], free_s[S], other_s[S], acc_full_s[2], acc_free_s[2],
+  __shared__ unsigned long long full_s[S], free_s[S], acc_full_s[2], acc_free_s[2],
       info_full_s[kInfoSlots], info_free_s[kInfoSlots], done_s;
   __shared__ __align__(16) ProductInfo<R> info_s[kInfoSlots];
   __shared__ uint32_t tmem_s;
@@ -191,7 +193,6 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     for (int s = 0; s < S; ++s) {
       mbar_init(&full_s[s], 1);
       mbar_init(&free_s[s], 1);
-      mbar_init(&other_s[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full_s[b], 1);
@@ -199,7 +200,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     }
     for (int i = 0; i < kInfoSlots; ++i) {
       mbar_init(&info_full_s[i], 32);
-      mbar_init(&info_free_s[i], kInfoUsers);
+      mbar_init(&info_free_s[i], kInfoUsers - rank);  // the second CTA issues no products
     }
     mbar_init(&done_s, 1);
     fence_mbar_init();
@@ -227,41 +228,67 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     at_info.advance();
   };
 
-  if (warp == 0) {
+  // The next unit's steps: wait for a slot, `copy` into it.
+  auto copy_steps = [&](auto&& open, auto&& copy) {
     Ring<S> at;
     long long issued = 0;
     while (const ProductInfo<R>* q = next_unit()) {
-      const int half = q->half;
-      const bool mine = 4 * lane < half;
-      const int4 src = mine ? *reinterpret_cast<const int4*>(&q->src[4 * lane])
-                            : make_int4(0, 0, 0, 0);
-      const int e = q->e, m0 = q->m0 + 128 * rank, tiles = q->tiles;
+      const int tiles = q->tiles;
+      open(*q);
       for (int c = 0; ok && c < tiles; ++c) {
         for (int ks = 0; ks < a.ksteps; ++ks) {
           ok = warp_wait(&free_s[at.slot], at.phase ^ 1u, limit);
           if (!ok) break;
-          const uint32_t wto = wbase + at.slot * Sh::kW, xto = xbase + at.slot * Sh::kX;
-          if (elect_one()) {
-            mbar_expect(&full_s[at.slot], Sh::kW + half * 128);
-            const int m = m0 + c * kPairRows;
-            if constexpr (kTranspose) {
-              tma_load_3d(wto, &wmap, m, 64 * ks, e, &full_s[at.slot]);
-              tma_load_3d(wto + 64 * 128, &wmap, m + 64, 64 * ks, e, &full_s[at.slot]);
-            } else {
-              tma_load_3d(wto, &wmap, (kFp8 ? 128 : 64) * ks, m, e, &full_s[at.slot]);
-            }
-          }
-          if (mine)
-            tma_gather4(xto + 512 * lane, &xmap, (kFp8 ? 128 : 64) * ks, src, &full_s[at.slot]);
+          copy(at.slot, c, ks);
           ++issued;
           at.advance();
         }
       }
       leave_unit();
     }
-    // nothing may land in the shared memory of a CTA that has left
+    // Nothing may land in the shared memory of a CTA that has left: what was copied has been used,
+    // or, where a wait gave up, had this long to land.
     for (long long i = issued > S ? issued - S : 0; i < issued; ++i)
-      warp_wait(&full_s[i % S], static_cast<uint32_t>(i / S) & 1u, kWaitLimitNs);
+      warp_wait(&free_s[i % S], static_cast<uint32_t>(i / S) & 1u, kWaitLimitNs);
+  };
+
+  if (warp == 0) {
+    int e = 0, m0 = 0, half = 0;
+    copy_steps(
+        [&](const ProductInfo<R>& q) {
+          e = q.e;
+          m0 = q.m0 + 128 * rank;
+          half = q.half;
+        },
+        [&](int slot, int c, int ks) {
+          if (!elect_one()) return;
+          // both CTAs' bytes
+          if (rank == 0) mbar_expect(&full_s[slot], 2 * (Sh::kW + half * 128));
+          const uint32_t to = wbase + slot * Sh::kW, bar = pair_first(&full_s[slot]);
+          const int m = m0 + c * kPairRows;
+          if constexpr (kTranspose) {
+            pair_load_3d(to, &wmap, m, 64 * ks, e, bar);
+            pair_load_3d(to + 64 * 128, &wmap, m + 64, 64 * ks, e, bar);
+          } else {
+            pair_load_3d(to, &wmap, (kFp8 ? 128 : 64) * ks, m, e, bar);
+          }
+        });
+  } else if (warp >= 12) {
+    constexpr int kQuads = R / 8 / kGatherers;  // fours of rows of a warp
+    const int quad = (warp - 12) * kQuads + lane;
+    int4 src;
+    bool mine = false;
+    copy_steps(
+        [&](const ProductInfo<R>& q) {
+          mine = lane < kQuads && 4 * quad < q.half;
+          if (mine) src = *reinterpret_cast<const int4*>(&q.src[4 * quad]);
+        },
+        [&](int slot, int, int ks) {
+          if (mine)
+            pair_gather4(xbase + slot * Sh::kX + 512 * quad, &xmap, (kFp8 ? 128 : 64) * ks, src,
+                         pair_first(&full_s[slot]));
+          __syncwarp();
+        });
   } else if (warp == 1) {
     // (of this call at most, whatever another one may have left there)
     const int tiles = min(max(__ldg(a.t.head + 1), 0), a.max_tiles);
@@ -319,7 +346,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       if (lane == 0) info_s[at_info.slot].e = -1;
       mbar_arrive(&info_full_s[at_info.slot]);
     }
-  } else if (warp == 2) {
+  } else if (warp == 2 && rank == 0) {
     Ring<S> at;
     int buf = 0;
     uint32_t acc_phase = 0;
@@ -333,31 +360,25 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         uint32_t to_phase = acc_phase;
         const uint32_t word = pair_word(a.type, kTranspose, false, n);
         for (int c = 0; ok && c < tiles; ++c) {
-          if (rank == 0) ok = pair_wait(&acc_free_s[to], to_phase ^ 1u, limit);
+          ok = pair_wait(&acc_free_s[to], to_phase ^ 1u, limit);
           if (!ok) break;
           tc_fence_after();
           for (int ks = 0; ks < a.ksteps; ++ks) {
-            ok = thread_wait(&full_s[s.slot], s.phase, limit);
+            ok = pair_wait(&full_s[s.slot], s.phase, limit);
             if (!ok) break;
-            if (rank != 0) {
-              pair_arrive_first(&other_s[s.slot]);
-            } else {
-              ok = pair_wait(&other_s[s.slot], s.phase, limit);
-              if (!ok) break;
-              tc_fence_after();
-              const uint32_t wat = wbase + s.slot * Sh::kW;
-              const uint64_t dw = kTranspose ? desc_lines128(wat, 64) : desc_rows128(wat);
-              const uint64_t dx = desc_rows128(xbase + s.slot * Sh::kX);
+            tc_fence_after();
+            const uint32_t wat = wbase + s.slot * Sh::kW;
+            const uint64_t dw = kTranspose ? desc_lines128(wat, 64) : desc_rows128(wat);
+            const uint64_t dx = desc_rows128(xbase + s.slot * Sh::kX);
 #pragma unroll
-              for (int g = 0; g < 4; ++g)
-                // 32 bytes further along the rows; along the lines 16 of them
-                pair_mma<kFp8>(tmem + to * R, dw + (kTranspose ? 16 * 128 / 16 : 2) * g, dx + 2 * g,
-                               word, ks > 0 || g > 0);
-              pair_commit(&free_s[s.slot]);
-            }
+            for (int g = 0; g < 4; ++g)
+              // 32 bytes further along the rows; along the lines 16 of them
+              pair_mma<kFp8>(tmem + to * R, dw + (kTranspose ? 16 * 128 / 16 : 2) * g, dx + 2 * g,
+                             word, ks > 0 || g > 0);
+            pair_commit(&free_s[s.slot]);
             s.advance();
           }
-          if (rank == 0 && ok) pair_commit(&acc_full_s[to]);
+          if (ok) pair_commit(&acc_full_s[to]);
           if (++to == 2) {
             to = 0;
             to_phase ^= 1u;
@@ -371,12 +392,12 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       leave_unit();
     }
     // nothing of the tensor core may be in flight when tensor memory is given back
-    if (rank == 0 && any) {
+    if (any) {
       if (elect_one()) pair_commit_first(&done_s);
       __syncwarp();
       warp_wait(&done_s, 0, kWaitLimitNs);
     }
-  } else if (warp >= 4) {
+  } else if (warp >= 4 && warp < 12) {
     const int quarter = warp & 3, half = (warp - 4) >> 2;
     const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
     int buf = 0;

@@ -31,11 +31,12 @@ struct WeightGradArgs {
   int wide;  // rows of the output start on 32 bytes
 };
 
-constexpr int kGradThreads = 384;
+constexpr int kGradThreads = 640;
+constexpr int kGradCopiers = 8;          // four for each operand
 constexpr int kGradTmem = 512;
 constexpr int kGradSlots = 6;
 constexpr int kGradInfo = 4;
-constexpr int kGradUsers = 10;
+constexpr int kGradUsers = 9 + kGradCopiers;  // products, eight storing warps, copies
 constexpr int kGradDeep = 64;            // rows of a step
 constexpr int kGradTile = 128 * 128;     // bytes of an operand in a CTA and step
 constexpr size_t kGradSmem = static_cast<size_t>(kGradSlots) * 2 * kGradTile + 1024;
@@ -50,7 +51,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                            const __grid_constant__ CUtensorMap xmap, const WeightGradArgs a) {
   constexpr int S = kGradSlots;
   extern __shared__ unsigned char smem_raw[];
-  __shared__ unsigned long long full_s[S], free_s[S], other_s[S], acc_full_s[2], acc_free_s[2],
+  __shared__ unsigned long long full_s[S], free_s[S], acc_full_s[2], acc_free_s[2],
       info_full_s[kGradInfo], info_free_s[kGradInfo], done_s;
   __shared__ GradInfo info_s[kGradInfo];
   __shared__ uint32_t tmem_s;
@@ -64,7 +65,6 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     for (int s = 0; s < S; ++s) {
       mbar_init(&full_s[s], 1);
       mbar_init(&free_s[s], 1);
-      mbar_init(&other_s[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full_s[b], 1);
@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     }
     for (int i = 0; i < kGradInfo; ++i) {
       mbar_init(&info_full_s[i], 1);
-      mbar_init(&info_free_s[i], kGradUsers);
+      mbar_init(&info_free_s[i], kGradUsers - rank);  // the second CTA issues no products
     }
     mbar_init(&done_s, 1);
     fence_mbar_init();
@@ -99,47 +99,54 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     at_info.advance();
   };
 
-  if (warp == 0) {
+  if (warp >= 12) {
+    // a warp copies every fourth four of a step's rows of one operand, two lines of 64 each
     Ring<S> at;
     long long issued = 0;
-    const int quad = lane & 15, seg = lane >> 4;
+    const bool is_x = warp >= 16;
+    const int quad = 4 * (lane >> 1) + (warp & 3), seg = lane & 1;  // of lanes 0 to 7
+    const bool mine = lane < 8;
+    const CUtensorMap* map = is_x ? &xmap : &gmap;
+    const int per_route = is_x ? a.x_per_route : a.g_per_route, none = is_x ? a.x_rows : a.g_rows;
+    const uint32_t to = (is_x ? xbase : gbase) + seg * (kGradDeep * 128) + quad * 512;
     while (const GradInfo* q = next_unit()) {
       const int p0 = q->p0, rows = q->rows;
-      const int gx = q->m0 + 128 * rank + 64 * seg, xx = q->k0 + 128 * rank + 64 * seg;
+      const int col = (is_x ? q->k0 : q->m0) + 128 * rank + 64 * seg;
       auto routes_of = [&](int first, int (&s)[4]) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int at_row = first + 4 * quad + i;
-          s[i] = at_row < rows ? __ldg(a.sid + p0 + at_row) : -1;
+          s[i] = mine && at_row < rows ? __ldg(a.sid + p0 + at_row) : -1;
         }
       };
       int ahead[4];
       routes_of(0, ahead);
       for (int r0 = 0; r0 < rows; r0 += kGradDeep) {
-        int g[4], x[4];
+        int g[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const bool is = ahead[i] >= 0 && ahead[i] < a.routes;
-          const int token = is ? ahead[i] / a.topk : 0;
-          // past the last row of either: zeros
-          g[i] = !is ? a.g_rows : (a.g_per_route ? ahead[i] : token);
-          x[i] = !is ? a.x_rows : (a.x_per_route ? ahead[i] : token);
+          // past the operand's last row: zeros
+          g[i] = !is ? none : (per_route ? ahead[i] : ahead[i] / a.topk);
         }
         if (r0 + kGradDeep < rows) routes_of(r0 + kGradDeep, ahead);
         ok = warp_wait(&free_s[at.slot], at.phase ^ 1u, limit);
         if (!ok) break;
-        if (elect_one()) mbar_expect(&full_s[at.slot], 2 * kGradTile);
-        const uint32_t to = at.slot * kGradTile + seg * (kGradDeep * 128) + quad * 512;
-        tma_gather4(gbase + to, &gmap, gx, make_int4(g[0], g[1], g[2], g[3]), &full_s[at.slot]);
-        tma_gather4(xbase + to, &xmap, xx, make_int4(x[0], x[1], x[2], x[3]), &full_s[at.slot]);
+        // both operands of both CTAs
+        if (warp == 12 && rank == 0 && elect_one()) mbar_expect(&full_s[at.slot], 4 * kGradTile);
+        if (mine)
+          pair_gather4(to + at.slot * kGradTile, map, col, make_int4(g[0], g[1], g[2], g[3]),
+                       pair_first(&full_s[at.slot]));
+        __syncwarp();
         ++issued;
         at.advance();
       }
       leave_unit();
     }
-    // nothing may land in the shared memory of a CTA that has left
+    // Nothing may land in the shared memory of a CTA that has left: what was copied has been used,
+    // or, where a wait gave up, had this long to land.
     for (long long i = issued > S ? issued - S : 0; i < issued; ++i)
-      warp_wait(&full_s[i % S], static_cast<uint32_t>(i / S) & 1u, kWaitLimitNs);
+      warp_wait(&free_s[i % S], static_cast<uint32_t>(i / S) & 1u, kWaitLimitNs);
   } else if (warp == 1) {
     const int each = a.mtiles * a.ktiles, units = a.E * each, step = gridDim.x >> 1;
     for (int u0 = blockIdx.x >> 1; ok && u0 < units; u0 += 32 * step) {
@@ -174,7 +181,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       info_s[at_info.slot].e = -1;
       mbar_arrive(&info_full_s[at_info.slot]);
     }
-  } else if (warp == 2) {
+  } else if (warp == 2 && rank == 0) {
     Ring<S> at;
     int buf = 0;
     uint32_t acc_phase = 0;
@@ -186,30 +193,24 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         any = true;
         if (elect_one()) {
           Ring<S> s = at;
-          if (rank == 0) ok = pair_wait(&acc_free_s[buf], acc_phase ^ 1u, limit);
+          ok = pair_wait(&acc_free_s[buf], acc_phase ^ 1u, limit);
           tc_fence_after();
           for (int ks = 0; ok && ks < steps; ++ks) {
-            ok = thread_wait(&full_s[s.slot], s.phase, limit);
+            ok = pair_wait(&full_s[s.slot], s.phase, limit);
             if (!ok) break;
-            if (rank != 0) {
-              pair_arrive_first(&other_s[s.slot]);
-            } else {
-              ok = pair_wait(&other_s[s.slot], s.phase, limit);
-              if (!ok) break;
-              tc_fence_after();
-              const uint64_t dg = desc_lines128(gbase + s.slot * kGradTile, kGradDeep);
-              const uint64_t dx = desc_lines128(xbase + s.slot * kGradTile, kGradDeep);
-              const int parts = (rows - ks * kGradDeep + 15) >> 4;
+            tc_fence_after();
+            const uint64_t dg = desc_lines128(gbase + s.slot * kGradTile, kGradDeep);
+            const uint64_t dx = desc_lines128(xbase + s.slot * kGradTile, kGradDeep);
+            const int parts = (rows - ks * kGradDeep + 15) >> 4;
 #pragma unroll
-              for (int g = 0; g < 4; ++g)
-                if (g < parts)  // else rows past the last: zeros
-                  pair_mma<false>(tmem + buf * 256, dg + 128 * g, dx + 128 * g, word,
-                                  ks > 0 || g > 0);
-              pair_commit(&free_s[s.slot]);
-            }
+            for (int g = 0; g < 4; ++g)
+              if (g < parts)  // else rows past the last: zeros
+                pair_mma<false>(tmem + buf * 256, dg + 128 * g, dx + 128 * g, word,
+                                ks > 0 || g > 0);
+            pair_commit(&free_s[s.slot]);
             s.advance();
           }
-          if (rank == 0 && ok) pair_commit(&acc_full_s[buf]);
+          if (ok) pair_commit(&acc_full_s[buf]);
         }
         ok = __all_sync(kFull, ok);
         at.skip(steps);
@@ -220,12 +221,12 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       }
       leave_unit();
     }
-    if (rank == 0 && any) {
+    if (any) {
       if (elect_one()) pair_commit_first(&done_s);
       __syncwarp();
       warp_wait(&done_s, 0, kWaitLimitNs);
     }
-  } else if (warp >= 4) {
+  } else if (warp >= 4 && warp < 12) {
     const int quarter = warp & 3, half = (warp - 4) >> 2;
     const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
     int buf = 0;

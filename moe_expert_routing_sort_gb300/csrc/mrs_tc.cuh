@@ -257,13 +257,29 @@ __device__ __forceinline__ uint64_t desc_lines128(uint32_t smem_addr, int deep) 
          (static_cast<uint64_t>(deep * 128 >> 4) << 16) | (uint64_t{1024 >> 4} << 32) |
          (uint64_t{1} << 46) | (uint64_t{2} << 61);
 }
-// 128 bytes, from element x on, of four rows of a matrix; rows past its last read as zeros.
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, int x, int4 row,
-                                            unsigned long long* mbar) {
+// The address of a CTA's shared memory in the CTA of rank 0.
+__device__ __forceinline__ uint32_t pair_first(const void* p) {
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(at) : "r"(smem_u32(p)));
+  return at;
+}
+// Tensor copies into this CTA whose bytes are counted on a barrier of either CTA of the pair
+// (mbar: an address of the cluster).
+__device__ __forceinline__ void pair_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y,
+                                             int z, uint32_t mbar) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
-      "l"(map), "r"(smem_u32(mbar)), "r"(x), "r"(row.x), "r"(row.y), "r"(row.z), "r"(row.w)
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::"
+      "bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(map), "r"(mbar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+// 128 bytes, from element x on, of four rows of a matrix; rows past its last read as zeros.
+__device__ __forceinline__ void pair_gather4(uint32_t dst, const CUtensorMap* map, int x, int4 row,
+                                             uint32_t mbar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile::gather4.mbarrier::"
+      "complete_tx::bytes [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+      "l"(map), "r"(mbar), "r"(x), "r"(row.x), "r"(row.y), "r"(row.z), "r"(row.w)
       : "memory");
 }
 
