@@ -126,6 +126,7 @@ struct ProductArgs {
   ProductTable t;
   const int32_t* sid;
   const float *sw, *xs, *ws;  // or null
+  const unsigned char* x;
   void* out;
   unsigned long long wait_limit_ns;
   int routes, topk, per_route, max_tiles;
@@ -141,6 +142,10 @@ constexpr int kProductTmem = 512;
 constexpr int kPairRows = 256;  // m of a tile
 constexpr int kInfoSlots = 3;
 constexpr int kInfoUsers = 10 + kGatherers;  // weights, products, eight storing warps, rows
+// The first rows of a CTA's half are copied by threads, 32 by each of so many warps; those behind
+// them are gathered by tensor copies.
+template <int R>
+constexpr int kThreadWarps = R > 64 ? 4 : 0;
 
 template <int R>
 struct ProductShape {
@@ -179,7 +184,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   using Sh = ProductShape<R>;
   constexpr int S = Sh::kSlots;
   extern __shared__ unsigned char smem_raw[];
-  __shared__ unsigned long long full_s[S], free_s[S], acc_full_s[2], acc_free_s[2],
+  __shared__ unsigned long long full_s[S], free_s[S], rows_s[S], other_s[S], acc_full_s[2], acc_free_s[2],
       info_full_s[kInfoSlots], info_free_s[kInfoSlots], done_s;
   __shared__ __align__(16) ProductInfo<R> info_s[kInfoSlots];
   __shared__ uint32_t tmem_s;
@@ -193,6 +198,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     for (int s = 0; s < S; ++s) {
       mbar_init(&full_s[s], 1);
       mbar_init(&free_s[s], 1);
+      mbar_init(&rows_s[s], kThreadWarps<R> > 0 ? 32 * kThreadWarps<R> : 1);  // every copying thread
+      mbar_init(&other_s[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full_s[b], 1);
@@ -200,7 +207,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     }
     for (int i = 0; i < kInfoSlots; ++i) {
       mbar_init(&info_full_s[i], 32);
-      mbar_init(&info_free_s[i], kInfoUsers - rank);  // the second CTA issues no products
+      mbar_init(&info_free_s[i], kInfoUsers);
     }
     mbar_init(&done_s, 1);
     fence_mbar_init();
@@ -263,7 +270,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         [&](int slot, int c, int ks) {
           if (!elect_one()) return;
           // both CTAs' bytes
-          if (rank == 0) mbar_expect(&full_s[slot], 2 * (Sh::kW + half * 128));
+          if (rank == 0)
+            mbar_expect(&full_s[slot], 2 * (Sh::kW + max(half - 32 * kThreadWarps<R>, 0) * 128));
           const uint32_t to = wbase + slot * Sh::kW, bar = pair_first(&full_s[slot]);
           const int m = m0 + c * kPairRows;
           if constexpr (kTranspose) {
@@ -273,9 +281,10 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             pair_load_3d(to, &wmap, (kFp8 ? 128 : 64) * ks, m, e, bar);
           }
         });
-  } else if (warp >= 12) {
-    constexpr int kQuads = R / 8 / kGatherers;  // fours of rows of a warp
-    const int quad = (warp - 12) * kQuads + lane;
+  } else if (warp >= 12 + kThreadWarps<R>) {
+    constexpr int kWarps = kThreadWarps<R> < kGatherers ? kGatherers - kThreadWarps<R> : 1;
+    constexpr int kQuads = (R / 2 - 32 * kThreadWarps<R>) / 4 / kWarps;  // fours of rows of a warp
+    const int quad = 8 * kThreadWarps<R> + (warp - 12 - kThreadWarps<R>) * kQuads + lane;
     int4 src;
     bool mine = false;
     copy_steps(
@@ -289,6 +298,39 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                          pair_first(&full_s[slot]));
           __syncwarp();
         });
+  } else if (warp >= 12) {
+    // a warp copies 32 rows of the CTA's half, four rows (8 lanes each) at a time
+    Ring<S> at;
+    const int w32 = 32 * (warp - 12), chunk = lane & 7, sub = lane >> 3;
+    const size_t row_bytes = static_cast<size_t>(a.K) * (kFp8 ? 1 : 2);
+    // row 4 j + sub of the warp: two swizzles, for even and odd j
+    const uint32_t place = xbase + (w32 + sub) * 128;
+    const uint32_t even = place + 16 * (chunk ^ sub), odd = place + 16 * (chunk ^ (sub + 4));
+    while (const ProductInfo<R>* q = next_unit()) {
+      const int tiles = q->tiles, mine = q->half - w32;
+      const unsigned char* from[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        from[j] = a.x + (4 * j < mine ? q->src[w32 + 4 * j + sub] * row_bytes : 0) + 16 * chunk;
+      for (int c = 0; ok && c < tiles; ++c) {
+        for (int ks = 0; ks < a.ksteps; ++ks) {
+          ok = thread_wait(&free_s[at.slot], at.phase ^ 1u, limit);
+          if (!ok) break;  // this lane; the others follow below
+          const uint32_t to = at.slot * Sh::kX;
+          // columns past K are zeros
+          const bool in = static_cast<size_t>(128 * ks + 16 * chunk) < row_bytes;
+          const size_t off = in ? 128 * static_cast<size_t>(ks) : 0;
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (4 * j < mine) copy16(((j & 1) ? odd : even) + to + 512 * j, from[j] + off, in ? 16 : 0);
+          copy_arrive(&rows_s[at.slot]);
+          at.advance();
+        }
+        ok = __all_sync(kFull, ok);
+      }
+      leave_unit();
+    }
+    copy_wait_all();
   } else if (warp == 1) {
     // (of this call at most, whatever another one may have left there)
     const int tiles = min(max(__ldg(a.t.head + 1), 0), a.max_tiles);
@@ -346,7 +388,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       if (lane == 0) info_s[at_info.slot].e = -1;
       mbar_arrive(&info_full_s[at_info.slot]);
     }
-  } else if (warp == 2 && rank == 0) {
+  } else if (warp == 2) {
     Ring<S> at;
     int buf = 0;
     uint32_t acc_phase = 0;
@@ -360,10 +402,25 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         uint32_t to_phase = acc_phase;
         const uint32_t word = pair_word(a.type, kTranspose, false, n);
         for (int c = 0; ok && c < tiles; ++c) {
-          ok = pair_wait(&acc_free_s[to], to_phase ^ 1u, limit);
+          if (rank == 0) ok = pair_wait(&acc_free_s[to], to_phase ^ 1u, limit);
           if (!ok) break;
           tc_fence_after();
           for (int ks = 0; ks < a.ksteps; ++ks) {
+            if constexpr (kThreadWarps<R> > 0) {
+              // this CTA's rows, written by threads; then the other's
+              ok = thread_wait(&rows_s[s.slot], s.phase, limit);
+              if (!ok) break;
+              fence_proxy_async_smem();
+              if (rank != 0) {
+                pair_arrive_first(&other_s[s.slot]);
+                s.advance();
+                continue;
+              }
+              ok = pair_wait(&other_s[s.slot], s.phase, limit);
+              if (!ok) break;
+            } else if (rank != 0) {
+              break;
+            }
             ok = pair_wait(&full_s[s.slot], s.phase, limit);
             if (!ok) break;
             tc_fence_after();
@@ -378,7 +435,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             pair_commit(&free_s[s.slot]);
             s.advance();
           }
-          if (ok) pair_commit(&acc_full_s[to]);
+          if (ok && rank == 0) pair_commit(&acc_full_s[to]);
           if (++to == 2) {
             to = 0;
             to_phase ^= 1u;
@@ -392,7 +449,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       leave_unit();
     }
     // nothing of the tensor core may be in flight when tensor memory is given back
-    if (any) {
+    if (any && rank == 0) {
       if (elect_one()) pair_commit_first(&done_s);
       __syncwarp();
       warp_wait(&done_s, 0, kWaitLimitNs);
@@ -600,6 +657,7 @@ int product(const void* x, int type, const float* x_scales, int per_route, const
   a.sw = sw;
   a.xs = x_scales;
   a.ws = w_scales;
+  a.x = static_cast<const unsigned char*>(x);
   a.out = out;
   a.wait_limit_ns = product_wait_limit();
   a.routes = static_cast<int>(routes);

@@ -3,10 +3,9 @@
 // For every expert e, m < outs, k < cols:
 //   grad_w[e, m, k] = sum over routes r of e in the list of G[row, m] * X[row', k]
 // with fp32 sums, rounded once.  The contraction runs over the ragged rows of an expert, which lie
-// one behind another in the sorted list: both operands are gathered row by row, 128 bytes of four
-// rows an instruction, so that in shared memory each position of the contraction is a line of
-// consecutive m (or k), the transposed layout of the tensor core.  Rows past an expert's last are
-// read as zeros.
+// one behind another in the sorted list: both operands are copied row by row, so that in shared
+// memory each position of the contraction is a line of consecutive m (or k), the transposed layout
+// of the tensor core.  Rows past an expert's last are zeros.
 //
 // A pair of CTAs computes tiles of 256 m by 256 k of one expert, 64 rows a step; each CTA brings
 // 128 m and 128 k.  The tasks of the warps are those of mrs_product.cu.  Experts without routes get
@@ -22,9 +21,10 @@ namespace mrs {
 struct WeightGradArgs {
   ProductTable t;
   const int32_t* sid;
+  const unsigned char *g, *x;
   void* out;
   unsigned long long wait_limit_ns;
-  int routes, topk, g_per_route, x_per_route, g_rows, x_rows;
+  int routes, topk, g_per_route, x_per_route;
   int E, N, K, P, B;
   int mtiles, ktiles;
   int type, out_type;
@@ -47,11 +47,10 @@ struct GradInfo {
 
 template <class Out>
 __global__ void __launch_bounds__(kGradThreads, 1)
-    mrs_weight_grad_kernel(const __grid_constant__ CUtensorMap gmap,
-                           const __grid_constant__ CUtensorMap xmap, const WeightGradArgs a) {
+    mrs_weight_grad_kernel(const WeightGradArgs a) {
   constexpr int S = kGradSlots;
   extern __shared__ unsigned char smem_raw[];
-  __shared__ unsigned long long full_s[S], free_s[S], acc_full_s[2], acc_free_s[2],
+  __shared__ unsigned long long rows_s[S], free_s[S], other_s[S], acc_full_s[2], acc_free_s[2],
       info_full_s[kGradInfo], info_free_s[kGradInfo], done_s;
   __shared__ GradInfo info_s[kGradInfo];
   __shared__ uint32_t tmem_s;
@@ -63,8 +62,9 @@ __global__ void __launch_bounds__(kGradThreads, 1)
   pdl_trigger();
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(&full_s[s], 1);
+      mbar_init(&rows_s[s], 32 * kGradCopiers);
       mbar_init(&free_s[s], 1);
+      mbar_init(&other_s[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full_s[b], 1);
@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     }
     for (int i = 0; i < kGradInfo; ++i) {
       mbar_init(&info_full_s[i], 1);
-      mbar_init(&info_free_s[i], kGradUsers - rank);  // the second CTA issues no products
+      mbar_init(&info_free_s[i], kGradUsers);
     }
     mbar_init(&done_s, 1);
     fence_mbar_init();
@@ -100,53 +100,51 @@ __global__ void __launch_bounds__(kGradThreads, 1)
   };
 
   if (warp >= 12) {
-    // a warp copies every fourth four of a step's rows of one operand, two lines of 64 each
+    // a warp copies 16 rows of a step of one operand, 256 bytes of two rows at a time
     Ring<S> at;
-    long long issued = 0;
     const bool is_x = warp >= 16;
-    const int quad = 4 * (lane >> 1) + (warp & 3), seg = lane & 1;  // of lanes 0 to 7
-    const bool mine = lane < 8;
-    const CUtensorMap* map = is_x ? &xmap : &gmap;
-    const int per_route = is_x ? a.x_per_route : a.g_per_route, none = is_x ? a.x_rows : a.g_rows;
-    const uint32_t to = (is_x ? xbase : gbase) + seg * (kGradDeep * 128) + quad * 512;
+    const int w16 = 16 * (warp & 3), chunk = lane & 15, sub = lane >> 4;
+    const int per_route = is_x ? a.x_per_route : a.g_per_route, cols = is_x ? a.K : a.N;
+    const unsigned char* from = is_x ? a.x : a.g;
+    const size_t row_bytes = 2 * static_cast<size_t>(cols);
+    const uint32_t place = (is_x ? xbase : gbase) + (chunk >> 3) * (kGradDeep * 128) +
+                           (w16 + sub) * 128;
     while (const GradInfo* q = next_unit()) {
       const int p0 = q->p0, rows = q->rows;
-      const int col = (is_x ? q->k0 : q->m0) + 128 * rank + 64 * seg;
-      auto routes_of = [&](int first, int (&s)[4]) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int at_row = first + 4 * quad + i;
-          s[i] = mine && at_row < rows ? __ldg(a.sid + p0 + at_row) : -1;
-        }
+      const int col = (is_x ? q->k0 : q->m0) + 128 * rank + 8 * chunk;
+      const bool in = col < cols;
+      const unsigned char* mine = from + (in ? 2 * static_cast<size_t>(col) : 0);
+      // lanes 0 to 15 look up a row each, a step ahead
+      auto route_of = [&](int first) {
+        const int r = first + w16 + lane;
+        return lane < 16 && r < rows ? __ldg(a.sid + p0 + r) : -1;
       };
-      int ahead[4];
-      routes_of(0, ahead);
+      int ahead = route_of(0);
       for (int r0 = 0; r0 < rows; r0 += kGradDeep) {
-        int g[4];
+        const int r = ahead >= 0 && ahead < a.routes ? (per_route ? ahead : ahead / a.topk) : -1;
+        if (r0 + kGradDeep < rows) ahead = route_of(r0 + kGradDeep);
+        int row[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const bool is = ahead[i] >= 0 && ahead[i] < a.routes;
-          // past the operand's last row: zeros
-          g[i] = !is ? none : (per_route ? ahead[i] : ahead[i] / a.topk);
+        for (int j = 0; j < 8; ++j) row[j] = __shfl_sync(kFull, r, 2 * j + sub);
+        ok = ok && thread_wait(&free_s[at.slot], at.phase ^ 1u, limit);
+        if (ok) {  // (a lane whose wait gave up goes along until the unit ends)
+          if (r0 + w16 < rows) {  // (no product takes rows behind the last 16 that hold one)
+            const uint32_t to = place + at.slot * kGradTile;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const bool is = in && row[j] >= 0;
+              copy16(to + 256 * j + 16 * ((chunk & 7) ^ ((2 * j + sub) & 7)),
+                     mine + (is ? row[j] * row_bytes : 0), is ? 16 : 0);
+            }
+          }
+          copy_arrive(&rows_s[at.slot]);
         }
-        if (r0 + kGradDeep < rows) routes_of(r0 + kGradDeep, ahead);
-        ok = warp_wait(&free_s[at.slot], at.phase ^ 1u, limit);
-        if (!ok) break;
-        // both operands of both CTAs
-        if (warp == 12 && rank == 0 && elect_one()) mbar_expect(&full_s[at.slot], 4 * kGradTile);
-        if (mine)
-          pair_gather4(to + at.slot * kGradTile, map, col, make_int4(g[0], g[1], g[2], g[3]),
-                       pair_first(&full_s[at.slot]));
-        __syncwarp();
-        ++issued;
         at.advance();
       }
+      ok = __all_sync(kFull, ok);
       leave_unit();
     }
-    // Nothing may land in the shared memory of a CTA that has left: what was copied has been used,
-    // or, where a wait gave up, had this long to land.
-    for (long long i = issued > S ? issued - S : 0; i < issued; ++i)
-      warp_wait(&free_s[i % S], static_cast<uint32_t>(i / S) & 1u, kWaitLimitNs);
+    copy_wait_all();
   } else if (warp == 1) {
     const int each = a.mtiles * a.ktiles, units = a.E * each, step = gridDim.x >> 1;
     for (int u0 = blockIdx.x >> 1; ok && u0 < units; u0 += 32 * step) {
@@ -181,7 +179,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       info_s[at_info.slot].e = -1;
       mbar_arrive(&info_full_s[at_info.slot]);
     }
-  } else if (warp == 2 && rank == 0) {
+  } else if (warp == 2) {
     Ring<S> at;
     int buf = 0;
     uint32_t acc_phase = 0;
@@ -193,10 +191,19 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         any = true;
         if (elect_one()) {
           Ring<S> s = at;
-          ok = pair_wait(&acc_free_s[buf], acc_phase ^ 1u, limit);
+          if (rank == 0) ok = pair_wait(&acc_free_s[buf], acc_phase ^ 1u, limit);
           tc_fence_after();
           for (int ks = 0; ok && ks < steps; ++ks) {
-            ok = pair_wait(&full_s[s.slot], s.phase, limit);
+            // this CTA's rows, written by threads; then the other's
+            ok = thread_wait(&rows_s[s.slot], s.phase, limit);
+            if (!ok) break;
+            fence_proxy_async_smem();
+            if (rank != 0) {
+              pair_arrive_first(&other_s[s.slot]);
+              s.advance();
+              continue;
+            }
+            ok = pair_wait(&other_s[s.slot], s.phase, limit);
             if (!ok) break;
             tc_fence_after();
             const uint64_t dg = desc_lines128(gbase + s.slot * kGradTile, kGradDeep);
@@ -210,7 +217,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
             pair_commit(&free_s[s.slot]);
             s.advance();
           }
-          if (ok) pair_commit(&acc_full_s[buf]);
+          if (ok && rank == 0) pair_commit(&acc_full_s[buf]);
         }
         ok = __all_sync(kFull, ok);
         at.skip(steps);
@@ -221,7 +228,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       }
       leave_unit();
     }
-    if (any) {
+    if (any && rank == 0) {
       if (elect_one()) pair_commit_first(&done_s);
       __syncwarp();
       warp_wait(&done_s, 0, kWaitLimitNs);
@@ -305,13 +312,12 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 namespace {
 
 template <class Out>
-cudaError_t launch_weight_grad(const CUtensorMap& g, const CUtensorMap& x, const WeightGradArgs& a,
-                               int pairs, cudaStream_t st) {
+cudaError_t launch_weight_grad(const WeightGradArgs& a, int pairs, cudaStream_t st) {
   auto* k = mrs_weight_grad_kernel<Out>;
   static SmemGrant granted;
   const cudaError_t err = grant_smem(reinterpret_cast<const void*>(k), kGradSmem, granted);
   if (err != cudaSuccess) return err;
-  return launch_pairs(k, pairs, kGradThreads, kGradSmem, st, g, x, a);
+  return launch_pairs(k, pairs, kGradThreads, kGradSmem, st, a);
 }
 
 }  // namespace
@@ -379,14 +385,14 @@ extern "C" int moe_experts_grad_weights(
   WeightGradArgs a{};
   a.t = ta.t;
   a.sid = sorted_token_ids;
+  a.g = static_cast<const unsigned char*>(grad);
+  a.x = static_cast<const unsigned char*>(x);
   a.out = grad_w;
   a.wait_limit_ns = product_wait_limit();
   a.routes = static_cast<int>(routes);
   a.topk = topk;
   a.g_per_route = g_per_route != 0;
   a.x_per_route = x_per_route != 0;
-  a.g_rows = static_cast<int>(grows);
-  a.x_rows = static_cast<int>(xrows);
   a.E = E;
   a.N = outs;
   a.K = cols;
@@ -397,14 +403,10 @@ extern "C" int moe_experts_grad_weights(
   a.type = dtype == MOE_RS_BF16 ? 1 : 0;
   a.out_type = out_dtype;
   a.wide = aligned(grad_w, 32) && cols * out_size % 32 == 0;
-  CUtensorMap gmap, xmap;
-  if (!encode_rows(&gmap, grad, dtype, 2, outs, grows) ||
-      !encode_rows(&xmap, x, dtype, 2, cols, xrows))
-    return MOE_RS_ERR_LAUNCH;
   cudaError_t err = launch_product_table(ta, stream);
   if (err != cudaSuccess) return launch_status(err);
   const int pairs = units < sms / 2 ? static_cast<int>(units) : sms / 2;
   return launch_status(out_dtype == MOE_RS_FP32
-                           ? launch_weight_grad<float>(gmap, xmap, a, pairs, stream)
-                           : launch_weight_grad<uint16_t>(gmap, xmap, a, pairs, stream));
+                           ? launch_weight_grad<float>(a, pairs, stream)
+                           : launch_weight_grad<uint16_t>(a, pairs, stream));
 }
