@@ -35,7 +35,7 @@ constexpr int kTableThreads = 1024;
 constexpr int kTableEach = kMaxExperts / kTableThreads;
 
 __global__ void __launch_bounds__(kTableThreads) mrs_product_table_kernel(const TableArgs a) {
-  __shared__ int start[kMaxExperts + 1];
+  __shared__ int start[kMaxExperts + 1], used[kMaxExperts];
   __shared__ int meet[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_trigger();
@@ -74,18 +74,57 @@ __global__ void __launch_bounds__(kTableThreads) mrs_product_table_kernel(const 
   first[kTableEach] = next;
 #pragma unroll
   for (int i = 0; i < kTableEach; ++i) first[i] = min(first[i], next);
-  int count = 0;
+  __syncthreads();  // meet has been read, start too
+#pragma unroll
+  for (int i = 0; i < kTableEach; ++i)
+    if (e0 + i <= a.E) start[e0 + i] = first[i];
+  if (e0 + kTableEach == a.E) start[a.E] = first[kTableEach];
+  __syncthreads();
+  for (int e = tid; e <= a.E; e += kTableThreads) a.t.offs[e] = start[e];
+  // rows of each run; where asked for, up to its last route: routes come first in the last block,
+  // whose quarters are searched
+  for (int e = tid; e < a.E; e += kTableThreads) {
+    const int rows = (start[e + 1] - start[e]) * a.B;
+    int lo = rows;
+    if (a.want_used && rows > 0) {
+      const int32_t* s = a.sid + start[e] * static_cast<int64_t>(a.B) + rows - a.B;
+      int n = a.B;  // of the last block's entries lo .. lo + n - 1 it is not known
+      lo = 0;
+      while (n > 0) {
+        const int q = (n + 3) >> 2;
+        int routes = 0;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          const int at = min((i + 1) * q, n) - 1;
+          const int r = __ldg(s + lo + at);
+          routes += r >= 0 && r < a.routes ? 1 : 0;
+        }
+        const int before = min(routes * q, n), last = min(before + q, n);
+        lo += before;
+        n = routes == 3 ? n - before : last - before - 1;  // (the last of a quarter is no route)
+      }
+      lo += rows - a.B;
+    }
+    used[e] = lo;
+    if (a.want_used) a.t.used[e] = lo;
+  }
+  __syncthreads();
+  // tiles of at most a.rows rows, the tiles of a run alike where its length is known
+  int each[kTableEach], count = 0;
 #pragma unroll
   for (int i = 0; i < kTableEach; ++i) {
-    const int64_t rows = static_cast<int64_t>(first[i + 1] - first[i]) * a.B;
-    count += static_cast<int>((rows + a.rows - 1) / a.rows);
+    const int64_t rows = e0 + i < a.E ? used[e0 + i] : 0;
+    const int64_t n = (rows + a.rows - 1) / a.rows;
+    each[i] = n == 0 ? a.rows
+                     : min(static_cast<int>(((rows + n - 1) / n + 31) & ~int64_t{31}), a.rows);
+    if (!a.want_used) each[i] = a.rows;
+    count += static_cast<int>((rows + each[i] - 1) / each[i]);
   }
   int sum = count;  // tiles up to this thread's experts
   for (int o = 1; o < 32; o <<= 1) {
     const int v = __shfl_up_sync(kFull, sum, o);
     if (lane >= o) sum += v;
   }
-  __syncthreads();
   if (lane == 31) meet[warp] = sum;
   __syncthreads();
   for (int w = 0; w < warp; ++w) sum += meet[w];
@@ -94,26 +133,12 @@ __global__ void __launch_bounds__(kTableThreads) mrs_product_table_kernel(const 
 #pragma unroll
   for (int i = 0; i < kTableEach; ++i) {
     const int e = e0 + i;
-    if (e > a.E) break;
-    a.t.offs[e] = first[i];
-    if (e == a.E) break;
-    if (e + 1 == a.E && i + 1 == kTableEach) a.t.offs[a.E] = first[kTableEach];
-    const int p0 = first[i] * a.B, rows = (first[i + 1] - first[i]) * a.B;
-    for (int64_t r = 0; r < rows; r += a.rows, ++at)
+    if (e >= a.E) break;
+    const int p0 = start[e] * a.B, rows = used[e];
+    for (int64_t r = 0; r < rows; r += each[i], ++at)
       if (at < a.max_tiles)
         a.t.tiles[at] = make_int4(e, p0 + static_cast<int>(r),
-                                  min(a.rows, rows - static_cast<int>(r)), 0);
-    if (a.want_used) {
-      // routes come first in the last block: how many
-      int lo = rows > 0 ? rows - a.B : 0, hi = rows;
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        const int s = __ldg(a.sid + p0 + mid);
-        if (s >= 0 && s < a.routes) lo = mid + 1;
-        else hi = mid;
-      }
-      a.t.used[e] = lo;
-    }
+                                  min(each[i], rows - static_cast<int>(r)), 0);
   }
 }
 
@@ -137,15 +162,17 @@ struct ProductArgs {
 };
 
 constexpr int kProductThreads = 512;
-constexpr int kGatherers = 4;
 constexpr int kProductTmem = 512;
 constexpr int kPairRows = 256;  // m of a tile
 constexpr int kInfoSlots = 3;
-constexpr int kInfoUsers = 10 + kGatherers;  // weights, products, eight storing warps, rows
+constexpr int kInfoUsers = 10;  // weights, products, eight storing warps; and those with rows
 // The first rows of a CTA's half are copied by threads, 32 by each of so many warps; those behind
 // them are gathered by tensor copies.
 template <int R>
-constexpr int kThreadWarps = R > 64 ? 4 : 0;
+constexpr int kThreadWarps = R > 64 ? 3 : 0;
+// Warps that gather: 15 and 3, or 12 to 15.
+template <int R>
+constexpr int kGatherWarps = R > 64 ? 2 : 4;
 
 template <int R>
 struct ProductShape {
@@ -163,18 +190,14 @@ struct ProductInfo {
   float factor[R];
 };
 
-template <class Out>
-__device__ __forceinline__ Out rounded(float v, int type) {
-  if constexpr (sizeof(Out) == 4) {
-    return v;
-  } else {
-    if (type == MOE_RS_BF16) {
-      const __nv_bfloat16 h = __float2bfloat16_rn(v);
-      return *reinterpret_cast<const uint16_t*>(&h);
-    }
-    const __half h = __float2half_rn(v);
-    return *reinterpret_cast<const uint16_t*>(&h);
+// Two values to 16 bits, one rounding each.
+__device__ __forceinline__ uint32_t rounded2(float lo, float hi, int type) {
+  if (type == MOE_RS_BF16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
   }
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 template <bool kFp8, bool kTranspose, int R, class Out>
@@ -187,6 +210,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   __shared__ unsigned long long full_s[S], free_s[S], rows_s[S], other_s[S], acc_full_s[2], acc_free_s[2],
       info_full_s[kInfoSlots], info_free_s[kInfoSlots], done_s;
   __shared__ __align__(16) ProductInfo<R> info_s[kInfoSlots];
+  __shared__ __align__(16) uint16_t stage_s[sizeof(Out) == 2 ? 8 : 1][32 * 32];
   __shared__ uint32_t tmem_s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = static_cast<int>(pair_rank());
@@ -207,7 +231,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     }
     for (int i = 0; i < kInfoSlots; ++i) {
       mbar_init(&info_full_s[i], 32);
-      mbar_init(&info_free_s[i], kInfoUsers);
+      mbar_init(&info_free_s[i], kInfoUsers + kThreadWarps<R> + kGatherWarps<R>);
     }
     mbar_init(&done_s, 1);
     fence_mbar_init();
@@ -281,10 +305,11 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             pair_load_3d(to, &wmap, (kFp8 ? 128 : 64) * ks, m, e, bar);
           }
         });
-  } else if (warp >= 12 + kThreadWarps<R>) {
-    constexpr int kWarps = kThreadWarps<R> < kGatherers ? kGatherers - kThreadWarps<R> : 1;
-    constexpr int kQuads = (R / 2 - 32 * kThreadWarps<R>) / 4 / kWarps;  // fours of rows of a warp
-    const int quad = 8 * kThreadWarps<R> + (warp - 12 - kThreadWarps<R>) * kQuads + lane;
+  } else if (warp >= 12 + kThreadWarps<R> || (warp == 3 && R > 64)) {
+    // fours of rows of a warp
+    constexpr int kQuads = (R / 2 - 32 * kThreadWarps<R>) / 4 / kGatherWarps<R>;
+    const int quad = 8 * kThreadWarps<R> + (15 - warp) % 4 * (R > 64 ? 0 : kQuads) +
+                     (warp == 3 ? kQuads : 0) + lane;
     int4 src;
     bool mine = false;
     copy_steps(
@@ -456,6 +481,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     }
   } else if (warp >= 4 && warp < 12) {
     const int quarter = warp & 3, half = (warp - 4) >> 2;
+    uint16_t* stage = stage_s[sizeof(Out) == 2 ? warp - 4 : 0];
     const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
     int buf = 0;
     uint32_t acc_phase = 0;
@@ -470,18 +496,55 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         if (!ok) break;
         tc_fence_after();
         const uint32_t src = tmem + buf * R + lanes;
-        for (int j0 = 32 * half; j0 < n; j0 += 64) {
-          uint32_t v[32];
-          __syncwarp();
-          tmem_load32(src + j0, v);
-          tmem_wait(v);
+        // a lane has one m of 32 rows at a time; the next 32 are on their way
+        uint32_t ahead[2][32];
+        int turn = 0;
+        if (32 * half < n) tmem_load32(src + 32 * half, ahead[0]);
+        for (int j0 = 32 * half; j0 < n; j0 += 64, turn ^= 1) {
+          float v[32];
+          auto take = [&](uint32_t(&from)[32], uint32_t(&to)[32]) {
+            tmem_wait(from);
+            if (j0 + 64 < n) tmem_load32(src + j0 + 64, to);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const int r = q->route[j0 + j];
-            const float y = __uint_as_float(v[j]) * (scale * q->factor[j0 + j]);
-            if (r >= 0 && live)
-              static_cast<Out*>(a.out)[static_cast<size_t>(r) * a.M + m] =
-                  rounded<Out>(y, a.out_type);
+            for (int j = 0; j < 32; j += 4) {
+              const float4 f = *reinterpret_cast<const float4*>(&q->factor[j0 + j]);
+              v[j] = __uint_as_float(from[j]) * (scale * f.x);
+              v[j + 1] = __uint_as_float(from[j + 1]) * (scale * f.y);
+              v[j + 2] = __uint_as_float(from[j + 2]) * (scale * f.z);
+              v[j + 3] = __uint_as_float(from[j + 3]) * (scale * f.w);
+            }
+          };
+          if (turn == 0) take(ahead[0], ahead[1]);
+          else take(ahead[1], ahead[0]);
+          if constexpr (sizeof(Out) == 4) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+              const int4 r = *reinterpret_cast<const int4*>(&q->route[j0 + j]);
+              const int to[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (to[i] >= 0 && live)
+                  static_cast<float*>(a.out)[static_cast<size_t>(to[i]) * a.M + m] = v[j + i];
+            }
+          } else {
+            // through shared memory, so that four lanes store 64 bytes of a row side by side
+            __syncwarp();  // what was there has been read
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+              const uint32_t w = rounded2(v[j], v[j + 1], a.out_type);
+              stage[32 * j + lane] = static_cast<uint16_t>(w);
+              stage[32 * j + 32 + lane] = static_cast<uint16_t>(w >> 16);
+            }
+            __syncwarp();
+            const int piece = 8 * (lane & 3), m8 = m - lane + piece;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int row = 8 * i + (lane >> 2), r = q->route[j0 + row];
+              const uint4 w = *reinterpret_cast<const uint4*>(&stage[32 * row + piece]);
+              if (r >= 0 && m8 < a.M)  // M is a multiple of 8
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) +
+                                          static_cast<size_t>(r) * a.M + m8) = w;
+            }
           }
         }
         tc_fence_before();
@@ -649,6 +712,7 @@ int product(const void* x, int type, const float* x_scales, int per_route, const
   ta.max_rows = static_cast<int>(P);
   ta.routes = static_cast<int>(routes);
   ta.rows = R;
+  ta.want_used = R > 64;
   const size_t tiles = most_tiles(T, E, topk, block_m, R);
   ta.max_tiles = static_cast<int>(tiles);
   ProductArgs a{};
@@ -673,7 +737,12 @@ int product(const void* x, int type, const float* x_scales, int per_route, const
   a.type = type == MOE_RS_BF16 ? 1 : 0;
   a.out_type = out_type;
   const int pairs = sms / 2;
-  a.chunk = 1;
+  // A unit is as many output tiles of one row tile as leave eight rounds of units.
+  const size_t row_tiles = routes / R + hit;
+  const size_t each = row_tiles * a.mtiles / (8000 * static_cast<size_t>(pairs));
+  a.chunk = each < 1 ? 1 : (each > static_cast<size_t>(a.mtiles) ? a.mtiles : static_cast<int>(each));
+  a.nchunk = (a.mtiles + a.chunk - 1) / a.chunk;
+  a.chunk = (a.mtiles + a.nchunk - 1) / a.nchunk;
   a.nchunk = (a.mtiles + a.chunk - 1) / a.chunk;
   if (tiles * a.nchunk > INT32_MAX / 2) return MOE_RS_ERR_OVERFLOW;
   CUtensorMap wmap, xmap;
