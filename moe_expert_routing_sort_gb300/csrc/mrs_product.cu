@@ -359,54 +359,87 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   } else if (warp == 1) {
     // (of this call at most, whatever another one may have left there)
     const int tiles = min(max(__ldg(a.t.head + 1), 0), a.max_tiles);
-    const int units = tiles * a.nchunk;
-    for (int u = blockIdx.x >> 1; ok && u < units; u += gridDim.x >> 1) {
-      const int t = u / a.nchunk, first = (u - t * a.nchunk) * a.chunk;
+    const int units = tiles * a.nchunk, step = gridDim.x >> 1;
+    // What a unit takes is looked up over three rounds, so that no round waits for more than one
+    // access: its tile, the tile's routes, their factors.
+    struct Ahead {
+      int e, p0, rows, m0, tiles;
+      int r[R / 32], src[R / 32];
+      float w[R / 32], x[R / 32];
+    } now{}, next{}, later{};
+    auto find = [&](int u, Ahead& q) {
+      q.rows = 0;
+      if (u >= units) return;
+      const int t = a.nchunk == 1 ? u : u / a.nchunk, first = (u - t * a.nchunk) * a.chunk;
       const int4 tile = __ldg(a.t.tiles + t);
       // (a table that another call overwrites must not lead out of this call's buffers)
-      const int e = min(max(tile.x, 0), a.E - 1), p0 = min(max(tile.y, 0), a.P);
-      const int rows = min(min(tile.z, R), a.P - p0);
-      int r[R / 32];
-      int used = 0;
+      q.e = min(max(tile.x, 0), a.E - 1);
+      q.p0 = min(max(tile.y, 0), a.P);
+      q.rows = min(min(tile.z, R), a.P - q.p0);
+      q.m0 = first * kPairRows;
+      q.tiles = min(a.chunk, a.mtiles - first);
+    };
+    auto load_routes = [&](Ahead& q) {
 #pragma unroll
       for (int j = 0; j < R / 32; ++j) {
         const int i = 32 * j + lane;
-        const int s = i < rows ? __ldg(a.sid + p0 + i) : -1;
-        r[j] = s >= 0 && s < a.routes ? s : -1;
-        const unsigned some = __ballot_sync(kFull, r[j] >= 0);
+        q.r[j] = i < q.rows ? __ldg(a.sid + q.p0 + i) : -1;
+      }
+    };
+    auto load_factors = [&](Ahead& q) {
+#pragma unroll
+      for (int j = 0; j < R / 32; ++j) {
+        if (q.r[j] >= a.routes) q.r[j] = -1;
+        const bool is = q.r[j] >= 0;
+        if (!is) q.r[j] = -1;
+        q.src[j] = is ? (a.per_route ? q.r[j] : q.r[j] / a.topk) : 0;
+        q.w[j] = a.sw != nullptr && is ? __ldg(a.sw + q.p0 + 32 * j + lane) : 1.0f;
+        q.x[j] = a.xs != nullptr && is ? __ldg(a.xs + q.src[j]) : 1.0f;
+      }
+    };
+    const int u0 = blockIdx.x >> 1;
+    find(u0, now);
+    find(u0 + step, next);
+    find(u0 + 2 * step, later);
+    load_routes(now);
+    load_routes(next);
+    load_factors(now);
+    for (int u = u0; ok && u < units; u += step) {
+      load_routes(later);
+      load_factors(next);
+      Ahead last;
+      find(u + 3 * step, last);
+      int used = 0;
+#pragma unroll
+      for (int j = 0; j < R / 32; ++j) {
+        const unsigned some = __ballot_sync(kFull, now.r[j] >= 0);
         if (some != 0u) used = 32 * j + 32 - __clz(some);
       }
-      if (used == 0) continue;
-      float f[R / 32];
-      int src[R / 32];
+      if (used > 0) {
+        const int n = (used + 31) & ~31, half = n >> 1;
+        ok = warp_wait(&info_free_s[at_info.slot], at_info.phase ^ 1u, limit);
+        if (!ok) break;
+        ProductInfo<R>* q = &info_s[at_info.slot];
+        if (lane == 0) {
+          q->e = now.e;
+          q->n = n;
+          q->m0 = now.m0;
+          q->tiles = now.tiles;
+          q->half = half;
+        }
 #pragma unroll
-      for (int j = 0; j < R / 32; ++j) {
-        const bool is = r[j] >= 0;
-        src[j] = is ? (a.per_route ? r[j] : r[j] / a.topk) : 0;
-        f[j] = 1.0f;
-        if (a.sw != nullptr && is) f[j] = __ldg(a.sw + p0 + 32 * j + lane);
-        if (a.xs != nullptr && is) f[j] *= __ldg(a.xs + src[j]);
+        for (int j = 0; j < R / 32; ++j) {
+          const int i = 32 * j + lane, mine = i - rank * half;
+          if (mine >= 0 && mine < half) q->src[mine] = now.src[j];
+          q->route[i] = now.r[j];
+          q->factor[i] = now.w[j] * now.x[j];
+        }
+        mbar_arrive(&info_full_s[at_info.slot]);
+        at_info.advance();
       }
-      const int n = (used + 31) & ~31, half = n >> 1;
-      ok = warp_wait(&info_free_s[at_info.slot], at_info.phase ^ 1u, limit);
-      if (!ok) break;
-      ProductInfo<R>* q = &info_s[at_info.slot];
-      if (lane == 0) {
-        q->e = e;
-        q->n = n;
-        q->m0 = first * kPairRows;
-        q->tiles = min(a.chunk, a.mtiles - first);
-        q->half = half;
-      }
-#pragma unroll
-      for (int j = 0; j < R / 32; ++j) {
-        const int i = 32 * j + lane, mine = i - rank * half;
-        if (mine >= 0 && mine < half) q->src[mine] = src[j];
-        q->route[i] = r[j];
-        q->factor[i] = f[j];
-      }
-      mbar_arrive(&info_full_s[at_info.slot]);
-      at_info.advance();
+      now = next;
+      next = later;
+      later = last;
     }
     ok = ok && warp_wait(&info_free_s[at_info.slot], at_info.phase ^ 1u, limit);
     if (ok) {
@@ -481,71 +514,92 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     }
   } else if (warp >= 4 && warp < 12) {
     const int quarter = warp & 3, half = (warp - 4) >> 2;
-    uint16_t* stage = stage_s[sizeof(Out) == 2 ? warp - 4 : 0];
+    const uint32_t stage = smem_u32(stage_s[sizeof(Out) == 2 ? warp - 4 : 0]);
     const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
     int buf = 0;
     uint32_t acc_phase = 0;
     while (const ProductInfo<R>* q = next_unit()) {
       const int n = q->n, e = q->e;
       for (int c = 0; c < q->tiles; ++c) {
-        const int m = q->m0 + c * kPairRows + 128 * rank + 32 * quarter + lane;
-        const bool live = m < a.M;
-        float scale = 1.0f;
-        if (a.ws != nullptr && live) scale = __ldg(a.ws + static_cast<size_t>(e) * a.M + m);
+        // the warp's 32 m; a lane has those of its accumulator lanes
+        const int m32 = q->m0 + c * kPairRows + 128 * rank + 32 * quarter;
+        float scale[sizeof(Out) == 4 ? 1 : 4];
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(scale) / 4); ++i) {
+          const int m = m32 + (sizeof(Out) == 4 ? lane : 8 * i + (lane >> 2));
+          scale[i] = a.ws != nullptr && m < a.M ? __ldg(a.ws + static_cast<size_t>(e) * a.M + m)
+                                                : 1.0f;
+        }
         ok = warp_wait(&acc_full_s[buf], acc_phase, limit);
         if (!ok) break;
         tc_fence_after();
         const uint32_t src = tmem + buf * R + lanes;
-        // a lane has one m of 32 rows at a time; the next 32 are on their way
-        uint32_t ahead[2][32];
-        int turn = 0;
-        if (32 * half < n) tmem_load32(src + 32 * half, ahead[0]);
-        for (int j0 = 32 * half; j0 < n; j0 += 64, turn ^= 1) {
-          float v[32];
-          auto take = [&](uint32_t(&from)[32], uint32_t(&to)[32]) {
-            tmem_wait(from);
-            if (j0 + 64 < n) tmem_load32(src + j0 + 64, to);
-#pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-              const float4 f = *reinterpret_cast<const float4*>(&q->factor[j0 + j]);
-              v[j] = __uint_as_float(from[j]) * (scale * f.x);
-              v[j + 1] = __uint_as_float(from[j + 1]) * (scale * f.y);
-              v[j + 2] = __uint_as_float(from[j + 2]) * (scale * f.z);
-              v[j + 3] = __uint_as_float(from[j + 3]) * (scale * f.w);
-            }
-          };
-          if (turn == 0) take(ahead[0], ahead[1]);
-          else take(ahead[1], ahead[0]);
+        auto load = [&](int j0, uint32_t(&to)[32]) {
           if constexpr (sizeof(Out) == 4) {
+            tmem_load32(src + j0, to);
+          } else {
+            tmem_load_fragments(src + j0, to);
+            tmem_load_fragments(src + j0 + (16u << 16), to + 16);
+          }
+        };
+        // 32 rows of the list by 32 m, the next 32 rows on their way
+        auto store = [&](int j0, uint32_t(&v)[32], uint32_t(&ahead)[32]) {
+          tmem_wait(v);
+          if (j0 + 64 < n) load(j0 + 64, ahead);
+          if constexpr (sizeof(Out) == 4) {
+            const int m = m32 + lane;
 #pragma unroll
             for (int j = 0; j < 32; j += 4) {
               const int4 r = *reinterpret_cast<const int4*>(&q->route[j0 + j]);
+              const float4 f = *reinterpret_cast<const float4*>(&q->factor[j0 + j]);
               const int to[4] = {r.x, r.y, r.z, r.w};
+              const float by[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                if (to[i] >= 0 && live)
-                  static_cast<float*>(a.out)[static_cast<size_t>(to[i]) * a.M + m] = v[j + i];
+                if (to[i] >= 0 && m < a.M)
+                  static_cast<float*>(a.out)[static_cast<size_t>(to[i]) * a.M + m] =
+                      __uint_as_float(v[j + i]) * (scale[0] * by[i]);
             }
           } else {
-            // through shared memory, so that four lanes store 64 bytes of a row side by side
+            // through shared memory, so that four lanes store 64 bytes of a row side by side: 32
+            // rows of 64 bytes, their 16-byte pieces spread over the banks
             __syncwarp();  // what was there has been read
 #pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-              const uint32_t w = rounded2(v[j], v[j + 1], a.out_type);
-              stage[32 * j + lane] = static_cast<uint16_t>(w);
-              stage[32 * j + 32 + lane] = static_cast<uint16_t>(w >> 16);
+            for (int k = 0; k < 4; ++k) {
+              const float2 f =
+                  *reinterpret_cast<const float2*>(&q->factor[j0 + 8 * k + 2 * (lane & 3)]);
+              uint32_t w[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t* p = v + 16 * (i >> 1) + 4 * k + 2 * (i & 1);
+                w[i] = rounded2(__uint_as_float(p[0]) * (scale[i] * f.x),
+                                __uint_as_float(p[1]) * (scale[i] * f.y), a.out_type);
+              }
+              const int row = 8 * k + (lane & 7);
+              store_transposed(stage + 64 * row + 16 * ((lane >> 3) ^ ((row >> 1) & 3)), w[0], w[1],
+                               w[2], w[3]);
             }
             __syncwarp();
-            const int piece = 8 * (lane & 3), m8 = m - lane + piece;
+            const int m = m32 + 8 * (lane & 3);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int row = 8 * i + (lane >> 2), r = q->route[j0 + row];
-              const uint4 w = *reinterpret_cast<const uint4*>(&stage[32 * row + piece]);
-              if (r >= 0 && m8 < a.M)  // M is a multiple of 8
+              uint4 w;
+              asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                           : "r"(stage + 64 * row + 16 * ((lane & 3) ^ ((row >> 1) & 3)))
+                           : "memory");
+              if (r >= 0 && m < a.M)  // M is a multiple of 8
                 *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) +
-                                          static_cast<size_t>(r) * a.M + m8) = w;
+                                          static_cast<size_t>(r) * a.M + m) = w;
             }
           }
+        };
+        uint32_t one[32], two[32];
+        if (32 * half < n) load(32 * half, one);
+        for (int j0 = 32 * half; j0 < n; j0 += 128) {
+          store(j0, one, two);
+          if (j0 + 64 < n) store(j0 + 64, two, one);
         }
         tc_fence_before();
         __syncwarp();
@@ -737,9 +791,9 @@ int product(const void* x, int type, const float* x_scales, int per_route, const
   a.type = type == MOE_RS_BF16 ? 1 : 0;
   a.out_type = out_type;
   const int pairs = sms / 2;
-  // A unit is as many output tiles of one row tile as leave eight rounds of units.
+  // A unit is as many output tiles of one row tile as leave 32 rounds of units.
   const size_t row_tiles = routes / R + hit;
-  const size_t each = row_tiles * a.mtiles / (8000 * static_cast<size_t>(pairs));
+  const size_t each = row_tiles * a.mtiles / (32 * static_cast<size_t>(pairs));
   a.chunk = each < 1 ? 1 : (each > static_cast<size_t>(a.mtiles) ? a.mtiles : static_cast<int>(each));
   a.nchunk = (a.mtiles + a.chunk - 1) / a.chunk;
   a.chunk = (a.mtiles + a.nchunk - 1) / a.nchunk;

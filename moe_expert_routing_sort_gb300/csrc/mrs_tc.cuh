@@ -49,6 +49,27 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&r)[32]) {
   for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
 }
 
+// 16 lanes x 32 columns of 32 bits in fragments: of eight columns (8 k on) a thread t of the warp has
+// columns 2 (t % 4) and the next, of lane t / 4 in r[4 k], r[4 k + 1] and of lane t / 4 + 8 in
+// r[4 k + 2], r[4 k + 3].
+__device__ __forceinline__ void tmem_load_fragments(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
+}
+// Four 8 x 8 matrices of 16-bit elements, transposed: thread t has row t / 4, columns 2 (t % 4) and
+// the next of each; column c of matrix i goes to the 16 bytes at thread 8 i + c's address.
+__device__ __forceinline__ void store_transposed(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                                 uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+               "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+
 // -------------------------------------------------------------------------- descriptors
 // Shared-memory operand: rows of 128 bytes swizzled by 128, eight rows (1024 bytes) a group.
 __device__ __forceinline__ uint64_t desc_rows128(uint32_t smem_addr) {
