@@ -18,9 +18,9 @@
 //   0      copies of a step's weights
 //   1      the list: rows, routes and factors of the next units into a ring in shared memory
 //   2      in the first CTA of a pair the products; both CTAs' copies are counted on its barriers
-//   3      nothing
 //   4-11   finished tiles from tensor memory to the output rows, while the next one is computed
-//   12-15  copies of a step's rows, a quarter of them each
+//   12-14  copies of a step's rows by threads; 15 and 3 those of the last rows; 16 says when they
+//          are there (tiles of 64 rows: 12 to 15 gather them)
 // Every wait is bounded; one that gives up ends its warp's task with the status bit set.  The CTAs
 // of a pair leave together.
 #include <cuda_bf16.h>
@@ -161,24 +161,25 @@ struct ProductArgs {
   int out_type;
 };
 
-constexpr int kProductThreads = 512;
 constexpr int kProductTmem = 512;
 constexpr int kPairRows = 256;  // m of a tile
 constexpr int kInfoSlots = 3;
-constexpr int kInfoUsers = 10;  // weights, products, eight storing warps; and those with rows
+constexpr int kInfoUsers = 9;  // weights and eight storing warps; products and those with rows
 // The first rows of a CTA's half are copied by threads, 32 by each of so many warps; those behind
 // them are gathered by tensor copies.
 template <int R>
 constexpr int kThreadWarps = R > 64 ? 3 : 0;
-// Warps that gather: 15 and 3, or 12 to 15.
+// Warps that gather: 15 and the weights' one, or 12 to 15.
 template <int R>
 constexpr int kGatherWarps = R > 64 ? 2 : 4;
+constexpr int kProductThreads = 512;
 
-template <int R>
+// H: 256 m at a time, one or two of them on the same rows
+template <int R, int H>
 struct ProductShape {
-  static constexpr int kW = 128 * 128;
+  static constexpr int kW = H * 128 * 128;
   static constexpr int kX = R / 2 * 128;
-  static constexpr int kSlots = R == 256 ? 6 : 9;
+  static constexpr int kSlots = R == 256 ? (H == 2 ? 4 : 6) : 9;
   static constexpr size_t kSmem = static_cast<size_t>(kSlots) * (kW + kX) + 1024;
 };
 
@@ -200,14 +201,14 @@ __device__ __forceinline__ uint32_t rounded2(float lo, float hi, int type) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-template <bool kFp8, bool kTranspose, int R, class Out>
+template <bool kFp8, bool kTranspose, int R, int H, class Out>
 __global__ void __launch_bounds__(kProductThreads, 1)
     mrs_product_kernel(const __grid_constant__ CUtensorMap wmap,
                        const __grid_constant__ CUtensorMap xmap, const ProductArgs a) {
-  using Sh = ProductShape<R>;
+  using Sh = ProductShape<R, H>;
   constexpr int S = Sh::kSlots;
   extern __shared__ unsigned char smem_raw[];
-  __shared__ unsigned long long full_s[S], free_s[S], rows_s[S], other_s[S], acc_full_s[2], acc_free_s[2],
+  __shared__ unsigned long long full_s[S], free_s[S], rows_s[S], acc_full_s[2], acc_free_s[2],
       info_full_s[kInfoSlots], info_free_s[kInfoSlots], done_s;
   __shared__ __align__(16) ProductInfo<R> info_s[kInfoSlots];
   __shared__ __align__(16) uint16_t stage_s[sizeof(Out) == 2 ? 8 : 1][32 * 32];
@@ -220,10 +221,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   pdl_trigger();
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(&full_s[s], 1);
+      mbar_init(&full_s[s], kThreadWarps<R> > 0 ? 3 : 1);  // the copies, both CTAs' threads
       mbar_init(&free_s[s], 1);
       mbar_init(&rows_s[s], kThreadWarps<R> > 0 ? 32 * kThreadWarps<R> : 1);  // every copying thread
-      mbar_init(&other_s[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full_s[b], 1);
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     }
     for (int i = 0; i < kInfoSlots; ++i) {
       mbar_init(&info_full_s[i], 32);
-      mbar_init(&info_free_s[i], kInfoUsers + kThreadWarps<R> + kGatherWarps<R>);
+      mbar_init(&info_free_s[i], kInfoUsers + (rank == 0 ? 1 : 0) + (R > 64 ? 5 : 4));
     }
     mbar_init(&done_s, 1);
     fence_mbar_init();
@@ -283,46 +283,84 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       warp_wait(&free_s[i % S], static_cast<uint32_t>(i / S) & 1u, kWaitLimitNs);
   };
 
+  // Fours of rows that are gathered: kQuads by the first lanes of gathering warp `g`.
+  constexpr int kQuads = (R / 2 - 32 * kThreadWarps<R>) / 4 / kGatherWarps<R>;
+  const auto quad_of = [&](int g) { return 8 * kThreadWarps<R> + g * kQuads + lane; };
+  auto rows_to_gather = [&](const ProductInfo<R>& q, int g, int4& src) {
+    const bool mine = lane < kQuads && 4 * quad_of(g) < q.half;
+    if (mine) src = *reinterpret_cast<const int4*>(&q.src[4 * quad_of(g)]);
+    return mine;
+  };
+  auto gather = [&](int slot, int g, int ks, const int4& src) {
+    pair_gather4(xbase + slot * Sh::kX + 512 * quad_of(g), &xmap, (kFp8 ? 128 : 64) * ks, src,
+                 pair_first(&full_s[slot]));
+  };
+
   if (warp == 0) {
     int e = 0, m0 = 0, half = 0;
+    int4 src;
+    bool mine = false;
     copy_steps(
         [&](const ProductInfo<R>& q) {
           e = q.e;
           m0 = q.m0 + 128 * rank;
           half = q.half;
+          if constexpr (kThreadWarps<R> > 0) mine = rows_to_gather(q, 1, src);
         },
         [&](int slot, int c, int ks) {
-          if (!elect_one()) return;
-          // both CTAs' bytes
-          if (rank == 0)
-            mbar_expect(&full_s[slot], 2 * (Sh::kW + max(half - 32 * kThreadWarps<R>, 0) * 128));
-          const uint32_t to = wbase + slot * Sh::kW, bar = pair_first(&full_s[slot]);
-          const int m = m0 + c * kPairRows;
-          if constexpr (kTranspose) {
-            pair_load_3d(to, &wmap, m, 64 * ks, e, bar);
-            pair_load_3d(to + 64 * 128, &wmap, m + 64, 64 * ks, e, bar);
-          } else {
-            pair_load_3d(to, &wmap, (kFp8 ? 128 : 64) * ks, m, e, bar);
+          if (elect_one()) {
+            // both CTAs' bytes
+            if (rank == 0)
+              mbar_expect(&full_s[slot],
+                          2 * (Sh::kW + max(half - 32 * kThreadWarps<R>, 0) * 128));
+            const uint32_t bar = pair_first(&full_s[slot]);
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+              const uint32_t to = wbase + slot * Sh::kW + h * (128 * 128);
+              const int m = m0 + (c * H + h) * kPairRows;
+              if constexpr (kTranspose) {
+                pair_load_3d(to, &wmap, m, 64 * ks, e, bar);
+                pair_load_3d(to + 64 * 128, &wmap, m + 64, 64 * ks, e, bar);
+              } else {
+                pair_load_3d(to, &wmap, (kFp8 ? 128 : 64) * ks, m, e, bar);
+              }
+            }
           }
-        });
-  } else if (warp >= 12 + kThreadWarps<R> || (warp == 3 && R > 64)) {
-    // fours of rows of a warp
-    constexpr int kQuads = (R / 2 - 32 * kThreadWarps<R>) / 4 / kGatherWarps<R>;
-    const int quad = 8 * kThreadWarps<R> + (15 - warp) % 4 * (R > 64 ? 0 : kQuads) +
-                     (warp == 3 ? kQuads : 0) + lane;
-    int4 src;
-    bool mine = false;
-    copy_steps(
-        [&](const ProductInfo<R>& q) {
-          mine = lane < kQuads && 4 * quad < q.half;
-          if (mine) src = *reinterpret_cast<const int4*>(&q.src[4 * quad]);
-        },
-        [&](int slot, int, int ks) {
-          if (mine)
-            pair_gather4(xbase + slot * Sh::kX + 512 * quad, &xmap, (kFp8 ? 128 : 64) * ks, src,
-                         pair_first(&full_s[slot]));
+          if constexpr (kThreadWarps<R> > 0) {
+            __syncwarp();
+            if (mine) gather(slot, 1, ks, src);
+          }
           __syncwarp();
         });
+  } else if (warp == 3 && kThreadWarps<R> > 0) {
+    // Rows written by threads are announced to the tensor cores.  (The thread that issues the
+    // products would spend more clocks on these waits and the fence than the products take: 1340 us
+    // for T = 8192, E = 64, 7168 -> 2048.)
+    Ring<S> at;
+    while (const ProductInfo<R>* q = next_unit()) {
+      const int steps = q->tiles * a.ksteps;
+      if (elect_one()) {
+        Ring<S> s = at;
+        for (int i = 0; ok && i < steps; ++i) {
+          ok = thread_wait(&rows_s[s.slot], s.phase, limit);
+          if (!ok) break;
+          fence_proxy_async_smem();
+          pair_arrive_first(&full_s[s.slot]);
+          s.advance();
+        }
+      }
+      ok = __all_sync(kFull, ok);
+      at.skip(steps);
+      leave_unit();
+    }
+  } else if (warp >= 12 + kThreadWarps<R>) {
+    int4 src;
+    bool mine = false;
+    copy_steps([&](const ProductInfo<R>& q) { mine = rows_to_gather(q, 15 - warp, src); },
+               [&](int slot, int, int ks) {
+                 if (mine) gather(slot, 15 - warp, ks, src);
+                 __syncwarp();
+               });
   } else if (warp >= 12) {
     // a warp copies 32 rows of the CTA's half, four rows (8 lanes each) at a time
     Ring<S> at;
@@ -376,7 +414,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       q.e = min(max(tile.x, 0), a.E - 1);
       q.p0 = min(max(tile.y, 0), a.P);
       q.rows = min(min(tile.z, R), a.P - q.p0);
-      q.m0 = first * kPairRows;
+      q.m0 = first * H * kPairRows;
       q.tiles = min(a.chunk, a.mtiles - first);
     };
     auto load_routes = [&](Ahead& q) {
@@ -446,7 +484,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       if (lane == 0) info_s[at_info.slot].e = -1;
       mbar_arrive(&info_full_s[at_info.slot]);
     }
-  } else if (warp == 2) {
+  } else if (warp == 2 && rank == 0) {
     Ring<S> at;
     int buf = 0;
     uint32_t acc_phase = 0;
@@ -460,41 +498,33 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         uint32_t to_phase = acc_phase;
         const uint32_t word = pair_word(a.type, kTranspose, false, n);
         for (int c = 0; ok && c < tiles; ++c) {
-          if (rank == 0) ok = pair_wait(&acc_free_s[to], to_phase ^ 1u, limit);
+          ok = pair_wait(&acc_free_s[to], to_phase ^ 1u, limit) &&
+               (H == 1 || pair_wait(&acc_free_s[1], to_phase ^ 1u, limit));
           if (!ok) break;
           tc_fence_after();
           for (int ks = 0; ks < a.ksteps; ++ks) {
-            if constexpr (kThreadWarps<R> > 0) {
-              // this CTA's rows, written by threads; then the other's
-              ok = thread_wait(&rows_s[s.slot], s.phase, limit);
-              if (!ok) break;
-              fence_proxy_async_smem();
-              if (rank != 0) {
-                pair_arrive_first(&other_s[s.slot]);
-                s.advance();
-                continue;
-              }
-              ok = pair_wait(&other_s[s.slot], s.phase, limit);
-              if (!ok) break;
-            } else if (rank != 0) {
-              break;
-            }
             ok = pair_wait(&full_s[s.slot], s.phase, limit);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t wat = wbase + s.slot * Sh::kW;
-            const uint64_t dw = kTranspose ? desc_lines128(wat, 64) : desc_rows128(wat);
             const uint64_t dx = desc_rows128(xbase + s.slot * Sh::kX);
 #pragma unroll
-            for (int g = 0; g < 4; ++g)
-              // 32 bytes further along the rows; along the lines 16 of them
-              pair_mma<kFp8>(tmem + to * R, dw + (kTranspose ? 16 * 128 / 16 : 2) * g, dx + 2 * g,
-                             word, ks > 0 || g > 0);
+            for (int h = 0; h < H; ++h) {
+              const uint32_t wat = wbase + s.slot * Sh::kW + h * (128 * 128);
+              const uint64_t dw = kTranspose ? desc_lines128(wat, 64) : desc_rows128(wat);
+#pragma unroll
+              for (int g = 0; g < 4; ++g)
+                // 32 bytes further along the rows; along the lines 16 of them
+                pair_mma<kFp8>(tmem + (H == 2 ? h : to) * R, dw + (kTranspose ? 16 * 128 / 16 : 2) * g,
+                               dx + 2 * g, word, ks > 0 || g > 0);
+              if (H == 2 && ks + 1 == a.ksteps) pair_commit(&acc_full_s[h]);
+            }
             pair_commit(&free_s[s.slot]);
             s.advance();
           }
-          if (ok && rank == 0) pair_commit(&acc_full_s[to]);
-          if (++to == 2) {
+          if (H == 1 && ok) pair_commit(&acc_full_s[to]);
+          if (H == 2) {
+            to_phase ^= 1u;
+          } else if (++to == 2) {
             to = 0;
             to_phase ^= 1u;
           }
@@ -502,12 +532,12 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       }
       ok = __all_sync(kFull, ok);
       at.skip(tiles * a.ksteps);
-      acc_phase ^= static_cast<uint32_t>((buf + tiles) / 2) & 1u;
-      buf = (buf + tiles) % 2;
+      acc_phase ^= static_cast<uint32_t>((buf + tiles * H) / 2) & 1u;
+      buf = (buf + tiles * H) % 2;
       leave_unit();
     }
     // nothing of the tensor core may be in flight when tensor memory is given back
-    if (any && rank == 0) {
+    if (any) {
       if (elect_one()) pair_commit_first(&done_s);
       __syncwarp();
       warp_wait(&done_s, 0, kWaitLimitNs);
@@ -520,7 +550,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     uint32_t acc_phase = 0;
     while (const ProductInfo<R>* q = next_unit()) {
       const int n = q->n, e = q->e;
-      for (int c = 0; c < q->tiles; ++c) {
+      for (int c = 0; c < H * q->tiles; ++c) {
         // the warp's 32 m; a lane has those of its accumulator lanes
         const int m32 = q->m0 + c * kPairRows + 128 * rank + 32 * quarter;
         float scale[sizeof(Out) == 4 ? 1 : 4];
@@ -680,23 +710,23 @@ bool encode_weights3(CUtensorMap* map, const void* p, int type, int size, size_t
 
 namespace {
 
-template <bool kFp8, bool kTranspose, int R, class Out>
+template <bool kFp8, bool kTranspose, int R, int H, class Out>
 cudaError_t launch_product(const CUtensorMap& w, const CUtensorMap& x, const ProductArgs& a,
                            int pairs, cudaStream_t st) {
-  auto* k = mrs_product_kernel<kFp8, kTranspose, R, Out>;
-  constexpr size_t smem = ProductShape<R>::kSmem;
+  auto* k = mrs_product_kernel<kFp8, kTranspose, R, H, Out>;
+  constexpr size_t smem = ProductShape<R, H>::kSmem;
   static SmemGrant granted;
   const cudaError_t err = grant_smem(reinterpret_cast<const void*>(k), smem, granted);
   if (err != cudaSuccess) return err;
   return launch_pairs(k, pairs, kProductThreads, smem, st, w, x, a);
 }
 
-template <int R, class Out>
+template <int R, int H, class Out>
 cudaError_t launch_product(bool fp8, bool transpose, const CUtensorMap& w, const CUtensorMap& x,
                            const ProductArgs& a, int pairs, cudaStream_t st) {
-  return transpose ? launch_product<false, true, R, Out>(w, x, a, pairs, st)
-         : fp8     ? launch_product<true, false, R, Out>(w, x, a, pairs, st)
-                   : launch_product<false, false, R, Out>(w, x, a, pairs, st);
+  return transpose ? launch_product<false, true, R, H, Out>(w, x, a, pairs, st)
+         : fp8     ? launch_product<true, false, R, H, Out>(w, x, a, pairs, st)
+                   : launch_product<false, false, R, H, Out>(w, x, a, pairs, st);
 }
 
 size_t most_tiles(int T, int E, int topk, int block_m, int rows) {
@@ -786,8 +816,9 @@ int product(const void* x, int type, const float* x_scales, int per_route, const
   a.M = M;
   a.K = K;
   a.P = static_cast<int>(P);
-  a.mtiles = (M + kPairRows - 1) / kPairRows;
   a.ksteps = (K * static_cast<int>(size) + 127) / 128;
+  const int H = R > 64 && a.ksteps >= 16 && M > kPairRows ? 2 : 1;
+  a.mtiles = (M + H * kPairRows - 1) / (H * kPairRows);
   a.type = type == MOE_RS_BF16 ? 1 : 0;
   a.out_type = out_type;
   const int pairs = sms / 2;
@@ -809,8 +840,9 @@ int product(const void* x, int type, const float* x_scales, int per_route, const
   const int grid = units < static_cast<size_t>(pairs) ? static_cast<int>(units) : pairs;
   auto go = [&](auto o) {
     using Out = decltype(o);
-    return R == 64 ? launch_product<64, Out>(fp8, transpose, wmap, xmap, a, grid, stream)
-                   : launch_product<256, Out>(fp8, transpose, wmap, xmap, a, grid, stream);
+    return R == 64  ? launch_product<64, 1, Out>(fp8, transpose, wmap, xmap, a, grid, stream)
+           : H == 2 ? launch_product<256, 2, Out>(fp8, transpose, wmap, xmap, a, grid, stream)
+                    : launch_product<256, 1, Out>(fp8, transpose, wmap, xmap, a, grid, stream);
   };
   return launch_status(out_type == MOE_RS_FP32 ? go(float{}) : go(uint16_t{}));
 }

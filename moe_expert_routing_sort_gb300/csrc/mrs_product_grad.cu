@@ -36,7 +36,7 @@ constexpr int kGradCopiers = 8;          // four for each operand
 constexpr int kGradTmem = 512;
 constexpr int kGradSlots = 6;
 constexpr int kGradInfo = 4;
-constexpr int kGradUsers = 9 + kGradCopiers;  // products, eight storing warps, copies
+constexpr int kGradUsers = 9 + kGradCopiers;  // eight storing warps, copies, their announcer
 constexpr int kGradDeep = 64;            // rows of a step
 constexpr int kGradTile = 128 * 128;     // bytes of an operand in a CTA and step
 constexpr size_t kGradSmem = static_cast<size_t>(kGradSlots) * 2 * kGradTile + 1024;
@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     mrs_weight_grad_kernel(const WeightGradArgs a) {
   constexpr int S = kGradSlots;
   extern __shared__ unsigned char smem_raw[];
-  __shared__ unsigned long long rows_s[S], free_s[S], other_s[S], acc_full_s[2], acc_free_s[2],
+  __shared__ unsigned long long rows_s[S], free_s[S], full_s[S], acc_full_s[2], acc_free_s[2],
       info_full_s[kGradInfo], info_free_s[kGradInfo], done_s;
   __shared__ GradInfo info_s[kGradInfo];
   __shared__ uint32_t tmem_s;
@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     for (int s = 0; s < S; ++s) {
       mbar_init(&rows_s[s], 32 * kGradCopiers);
       mbar_init(&free_s[s], 1);
-      mbar_init(&other_s[s], 1);
+      mbar_init(&full_s[s], 2);  // both CTAs' rows
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full_s[b], 1);
@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     }
     for (int i = 0; i < kGradInfo; ++i) {
       mbar_init(&info_full_s[i], 1);
-      mbar_init(&info_free_s[i], kGradUsers);
+      mbar_init(&info_free_s[i], kGradUsers + (rank == 0 ? 1 : 0));  // and the products
     }
     mbar_init(&done_s, 1);
     fence_mbar_init();
@@ -179,7 +179,26 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       info_s[at_info.slot].e = -1;
       mbar_arrive(&info_full_s[at_info.slot]);
     }
-  } else if (warp == 2) {
+  } else if (warp == 3) {
+    // announces the rows that threads have written to the tensor cores
+    Ring<S> at;
+    while (const GradInfo* q = next_unit()) {
+      const int steps = (q->rows + kGradDeep - 1) / kGradDeep;
+      if (elect_one()) {
+        Ring<S> s = at;
+        for (int i = 0; ok && i < steps; ++i) {
+          ok = thread_wait(&rows_s[s.slot], s.phase, limit);
+          if (!ok) break;
+          fence_proxy_async_smem();
+          pair_arrive_first(&full_s[s.slot]);
+          s.advance();
+        }
+      }
+      ok = __all_sync(kFull, ok);
+      at.skip(steps);
+      leave_unit();
+    }
+  } else if (warp == 2 && rank == 0) {
     Ring<S> at;
     int buf = 0;
     uint32_t acc_phase = 0;
@@ -191,19 +210,10 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         any = true;
         if (elect_one()) {
           Ring<S> s = at;
-          if (rank == 0) ok = pair_wait(&acc_free_s[buf], acc_phase ^ 1u, limit);
+          ok = pair_wait(&acc_free_s[buf], acc_phase ^ 1u, limit);
           tc_fence_after();
           for (int ks = 0; ok && ks < steps; ++ks) {
-            // this CTA's rows, written by threads; then the other's
-            ok = thread_wait(&rows_s[s.slot], s.phase, limit);
-            if (!ok) break;
-            fence_proxy_async_smem();
-            if (rank != 0) {
-              pair_arrive_first(&other_s[s.slot]);
-              s.advance();
-              continue;
-            }
-            ok = pair_wait(&other_s[s.slot], s.phase, limit);
+            ok = pair_wait(&full_s[s.slot], s.phase, limit);
             if (!ok) break;
             tc_fence_after();
             const uint64_t dg = desc_lines128(gbase + s.slot * kGradTile, kGradDeep);
@@ -217,7 +227,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
             pair_commit(&free_s[s.slot]);
             s.advance();
           }
-          if (ok && rank == 0) pair_commit(&acc_full_s[buf]);
+          if (ok) pair_commit(&acc_full_s[buf]);
         }
         ok = __all_sync(kFull, ok);
         at.skip(steps);
@@ -228,7 +238,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       }
       leave_unit();
     }
-    if (any && rank == 0) {
+    if (any) {
       if (elect_one()) pair_commit_first(&done_s);
       __syncwarp();
       warp_wait(&done_s, 0, kWaitLimitNs);
