@@ -31,12 +31,13 @@ struct WeightGradArgs {
   int wide;  // rows of the output start on 32 bytes
 };
 
-constexpr int kGradThreads = 640;
-constexpr int kGradCopiers = 8;          // four for each operand
+constexpr int kGradCopiers = 8;          // warps that copy a step, four for each operand
+constexpr int kGradTurns = 2;            // steps go to so many sets of them in turn
+constexpr int kGradThreads = 32 * (12 + kGradTurns * kGradCopiers);
 constexpr int kGradTmem = 512;
 constexpr int kGradSlots = 6;
 constexpr int kGradInfo = 4;
-constexpr int kGradUsers = 9 + kGradCopiers;  // eight storing warps, copies, their announcer
+constexpr int kGradUsers = 9 + kGradTurns * kGradCopiers;  // eight storing warps, copies, their announcer
 constexpr int kGradDeep = 64;            // rows of a step
 constexpr int kGradTile = 128 * 128;     // bytes of an operand in a CTA and step
 constexpr size_t kGradSmem = static_cast<size_t>(kGradSlots) * 2 * kGradTile + 1024;
@@ -102,7 +103,9 @@ __global__ void __launch_bounds__(kGradThreads, 1)
   if (warp >= 12) {
     // a warp copies 16 rows of a step of one operand, 256 bytes of two rows at a time
     Ring<S> at;
-    const bool is_x = warp >= 16;
+    const bool is_x = ((warp - 12) & 4) != 0;
+    const int turn = (warp - 12) / kGradCopiers;
+    int now = 0;  // whose step it is
     const int w16 = 16 * (warp & 3), chunk = lane & 15, sub = lane >> 4;
     const int per_route = is_x ? a.x_per_route : a.g_per_route, cols = is_x ? a.K : a.N;
     const unsigned char* from = is_x ? a.x : a.g;
@@ -121,16 +124,20 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         return lane < 16 && r < rows ? __ldg(a.sid + p0 + r) : -1;
       };
       int ahead[4];
+      const int skipped = (turn - now + kGradTurns) % kGradTurns, steps = (rows + kGradDeep - 1) / kGradDeep;
+      constexpr int kStride = kGradTurns * kGradDeep;
+      const int r1 = skipped * kGradDeep;
+      at.skip(min(skipped, steps));
 #pragma unroll
-      for (int k = 0; k < 4; ++k) ahead[k] = route_of(k * kGradDeep);
-      for (int r4 = 0; r4 < rows; r4 += 4 * kGradDeep) {
+      for (int k = 0; k < 4; ++k) ahead[k] = route_of(r1 + k * kStride);
+      for (int r4 = r1; r4 < rows; r4 += 4 * kStride) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const int r0 = r4 + k * kGradDeep;
+          const int r0 = r4 + k * kStride;
           if (r0 >= rows) break;
           const int r = ahead[k] >= 0 && ahead[k] < a.routes
                             ? (per_route ? ahead[k] : ahead[k] / a.topk) : -1;
-          ahead[k] = route_of(r0 + 4 * kGradDeep);
+          ahead[k] = route_of(r0 + 4 * kStride);
           int row[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j) row[j] = __shfl_sync(kFull, r, 2 * j + sub);
@@ -147,9 +154,10 @@ __global__ void __launch_bounds__(kGradThreads, 1)
             }
             copy_arrive(&rows_s[at.slot]);
           }
-          at.advance();
+          at.skip(min(kGradTurns, steps - r0 / kGradDeep));
         }
       }
+      now = (now + steps) % kGradTurns;
       ok = __all_sync(kFull, ok);
       leave_unit();
     }
