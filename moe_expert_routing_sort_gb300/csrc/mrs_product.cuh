@@ -49,6 +49,21 @@ struct TableArgs {
 // One CTA: the boundaries of the runs, their tiles' places by a prefix sum, and the tiles.
 cudaError_t launch_product_table(const TableArgs& a, cudaStream_t st);
 
+// The product of a few routes, straight from the list; its weights' map.
+bool encode_few(CUtensorMap* map, const void* p, size_t row_bytes, size_t rows, size_t E);
+struct FewArgs {
+  const unsigned char* x;
+  const int32_t *sid, *eid, *npp;
+  const float *sw, *xs, *ws;  // or null
+  int32_t* status;
+  void* out;
+  unsigned long long wait_limit_ns;
+  int routes, topk, per_route, E, N, K, B, blocks, out_type;
+  int nchunk, ksteps;  // set by the launch
+};
+cudaError_t launch_product_few(const CUtensorMap& wmap, FewArgs a, int type, int sms,
+                               cudaStream_t st);
+
 // A tensor of up to three dimensions of `size`-byte elements; `box` elements of the innermost
 // dimension are 128 bytes, swizzled by 128; what lies outside reads as zero.  rank 2: for gathers
 // of rows (a box is one row high).
