@@ -48,7 +48,7 @@ __global__ void __launch_bounds__(kRowThreads<kVec>) mrs_gated_kernel(const Gate
   const float w = live && a.weights != nullptr ? __ldg(a.weights + row) : 1.0f;
   const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
   float v[kVec][8];
-  uint32_t top = 0u;
+  float top = 0.0f;
 #pragma unroll
   for (int i = 0; i < kVec; ++i) {
     const int at = i * a.tpr + place;
@@ -61,21 +61,20 @@ __global__ void __launch_bounds__(kRowThreads<kVec>) mrs_gated_kernel(const Gate
       float up, down;
       sigmoids(v[i][k], up, down);
       v[i][k] = w * (v[i][k] * up * b[k]);
-      top = max(top, magnitude(v[i][k]));
+      top = larger(top, v[i][k]);
     }
     if (a.y != nullptr)
       *reinterpret_cast<uint4*>(static_cast<T*>(a.y) + row * cols + 8 * at) = pack8<T>(v[i]);
   }
   if (a.codes == nullptr) return;
-  const float scale = fp8_scale(row_totals(0.0f, top, a.tpr, meet).top);
-  const float inv = fp8_inverse(scale);
+  const float scale = fp8_scale(row_totals(0.0f, __float_as_uint(top), a.tpr, meet).top);
   if (!live) return;
   if (place == 0) a.scales[row] = scale;
 #pragma unroll
   for (int i = 0; i < kVec; ++i) {
     const int at = i * a.tpr + place;
     if (at < a.vecs)
-      *reinterpret_cast<uint2*>(a.codes + row * cols + 8 * at) = fp8_codes(v[i], inv);
+      *reinterpret_cast<uint2*>(a.codes + row * cols + 8 * at) = fp8_codes_of(v[i], scale);
   }
 }
 
@@ -129,7 +128,7 @@ __global__ void __launch_bounds__(kRowThreads<kVec>) mrs_fp8_quantize_kernel(con
   pdl_wait();
   const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
   float v[kVec][8];
-  uint32_t top = 0u;
+  float top = 0.0f;
 #pragma unroll
   for (int i = 0; i < kVec; ++i) {
     const int at = i * a.tpr + place;
@@ -139,17 +138,16 @@ __global__ void __launch_bounds__(kRowThreads<kVec>) mrs_fp8_quantize_kernel(con
     else
       unpack8<T>(load8<T>(x, 8 * static_cast<size_t>(at)), v[i]);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) top = max(top, magnitude(v[i][k]));
+    for (int k = 0; k < 8; ++k) top = larger(top, v[i][k]);
   }
-  const float scale = fp8_scale(row_totals(0.0f, top, a.tpr, meet).top);
-  const float inv = fp8_inverse(scale);
+  const float scale = fp8_scale(row_totals(0.0f, __float_as_uint(top), a.tpr, meet).top);
   if (!live) return;
   if (place == 0) a.scales[row] = scale;
 #pragma unroll
   for (int i = 0; i < kVec; ++i) {
     const int at = i * a.tpr + place;
     if (at < a.vecs)
-      *reinterpret_cast<uint2*>(a.codes + row * cols + 8 * at) = fp8_codes(v[i], inv);
+      *reinterpret_cast<uint2*>(a.codes + row * cols + 8 * at) = fp8_codes_of(v[i], scale);
   }
 }
 

@@ -29,66 +29,98 @@ struct NormArgs {
   float *scales, *rstd;
 };
 
-template <class T, int kVec>
+// kOne: a row takes the whole CTA.
+template <class T, int kVec, int kDepth, bool kOne>
 __global__ void __launch_bounds__(kRowThreads<kVec>) mrs_norm_kernel(const NormArgs a) {
+  extern __shared__ __align__(16) unsigned char smem_raw[];
   __shared__ RowTotals meet[32];
   pdl_trigger();
-  const int tid = threadIdx.x, in_cta = tid / a.tpr, place = tid - in_cta * a.tpr;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * a.per_cta + in_cta;
-  const bool live = row < a.rows;
-  const size_t cols = 8 * static_cast<size_t>(a.vecs);
+  const int tid = threadIdx.x, in_cta = kOne ? 0 : tid / a.tpr, place = tid - in_cta * a.tpr;
+  const int per_cta = kOne ? 1 : a.per_cta;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * per_cta + in_cta;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * per_cta;
+  const size_t row_bytes = 16 * static_cast<size_t>(a.vecs);
+  RowStream<kVec, kDepth> stream(smem_raw, place, a.tpr, a.vecs);
   pdl_wait();
-  float v[kVec][8];
-  float squares = 0.0f;
-  uint32_t top = 0u;
-#pragma unroll
-  for (int i = 0; i < kVec; ++i) {
-    const int at = i * a.tpr + place;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[i][k] = 0.0f;
-    if (!live || at >= a.vecs) continue;
-    if (a.residual != nullptr)
-      unpack8<T>(load8<T>(a.residual, row * a.residual_stride + 8 * at), v[i]);
-    const T* x = static_cast<const T*>(a.x) + static_cast<size_t>(row) * a.parts * a.x_stride + 8 * at;
-#pragma unroll 4
-    for (int j = 0; j < a.parts; ++j) {
-      float p[8];
-      unpack8<T>(load8<T>(x, j * a.x_stride), p);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[i][k] += p[k];
+  // a token's items: its rows behind the residual, if there is one
+  const bool lead = a.residual != nullptr;
+  const unsigned char* next_x = static_cast<const unsigned char*>(a.x) +
+                                2 * static_cast<size_t>(first) * a.parts * a.x_stride;
+  const unsigned char* next_r =
+      static_cast<const unsigned char*>(a.residual) + 2 * first * a.residual_stride;
+  int64_t ahead = first;
+  int item = lead ? -1 : 0;
+  auto put = [&] {
+    stream.put(ahead < a.rows, item < 0 ? next_r : next_x);
+    if (item >= 0) next_x += 2 * a.x_stride;
+    if (++item == a.parts) {
+      item = lead ? -1 : 0;
+      ahead += step;
+      next_x += 2 * static_cast<size_t>(step - 1) * a.parts * a.x_stride;
+      next_r += 2 * step * a.residual_stride;
     }
-    const uint4 s = pack8<T>(v[i]);
-    unpack8<T>(s, v[i]);
-    if (a.sum != nullptr)
-      *reinterpret_cast<uint4*>(static_cast<T*>(a.sum) + row * cols + 8 * at) = s;
-    float g[8];
-    load_columns<T>(a.gain, a.gain_f32 != 0, at, g);
+  };
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      squares += v[i][k] * v[i][k];
-      v[i][k] *= g[k];
-      top = max(top, magnitude(v[i][k]));
+  for (int i = 0; i < kDepth - 1; ++i) put();
+  // (the rows of a CTA take the same number of turns: they meet in the reduction)
+  for (int64_t row = first; row - in_cta < a.rows; row += step) {
+    const bool live = row < a.rows;
+    float v[kVec][8];
+    uint4 q[kVec];
+    put();
+    stream.get(q);
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) unpack8<T>(q[i], v[i]);
+    for (int j = lead ? 0 : 1; j < a.parts; ++j) {
+      put();
+      stream.get(q);
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) {
+        float p[8];
+        unpack8<T>(q[i], p);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[i][k] += p[k];
+      }
     }
-  }
-  const RowTotals r = row_totals(squares, top, a.tpr, meet);
-  const float rstd = __frsqrt_rn(r.sum * a.inv_cols + a.eps);
-  const float scale = fp8_scale(magnitude(__uint_as_float(r.top) * rstd));
-  const float inv = fp8_inverse(scale);
-  if (!live) return;
-  if (place == 0) {
-    if (a.rstd != nullptr) a.rstd[row] = rstd;
-    if (a.scales != nullptr) a.scales[row] = scale;
-  }
+    float squares = 0.0f, top = 0.0f;
+    const size_t here = row * row_bytes;
 #pragma unroll
-  for (int i = 0; i < kVec; ++i) {
-    const int at = i * a.tpr + place;
-    if (at >= a.vecs) continue;
+    for (int i = 0; i < kVec; ++i) {
+      if (!live || i >= stream.count) continue;  // (what was read there is not of this row)
+      const uint4 s = pack8<T>(v[i]);
+      unpack8<T>(s, v[i]);
+      if (a.sum != nullptr)
+        *reinterpret_cast<uint4*>(static_cast<unsigned char*>(a.sum) + here + stream.off[i]) = s;
+      float g[8];
+      load_columns<T>(a.gain, a.gain_f32 != 0, i * a.tpr + place, g);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[i][k] *= rstd;
-    if (a.y != nullptr)
-      *reinterpret_cast<uint4*>(static_cast<T*>(a.y) + row * cols + 8 * at) = pack8<T>(v[i]);
-    if (a.codes != nullptr)
-      *reinterpret_cast<uint2*>(a.codes + row * cols + 8 * at) = fp8_codes(v[i], inv);
+      for (int k = 0; k < 8; ++k) {
+        squares += v[i][k] * v[i][k];
+        v[i][k] *= g[k];
+      }
+      if (a.codes != nullptr) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) top = larger(top, v[i][k]);
+      }
+    }
+    const RowTotals r = row_totals(squares, __float_as_uint(top), a.tpr, meet);
+    const float rstd = __frsqrt_rn(r.sum * a.inv_cols + a.eps);
+    const float scale = fp8_scale(magnitude(__uint_as_float(r.top) * rstd));
+    if (live && place == 0) {
+      if (a.rstd != nullptr) a.rstd[row] = rstd;
+      if (a.scales != nullptr) a.scales[row] = scale;
+    }
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      if (!live || i >= stream.count) continue;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[i][k] *= rstd;
+      if (a.y != nullptr)
+        *reinterpret_cast<uint4*>(static_cast<unsigned char*>(a.y) + here + stream.off[i]) =
+            pack8<T>(v[i]);
+      if (a.codes != nullptr)
+        *reinterpret_cast<uint2*>(a.codes + (here + stream.off[i]) / 2) = fp8_codes_of(v[i], scale);
+    }
   }
 }
 
@@ -104,14 +136,40 @@ struct NormGradArgs {
 
 constexpr int kNormSumRows = 32;
 
-template <class T, int kVec>
+template <class T, int kVec, bool kOne>
 __global__ void __launch_bounds__(kRowThreads<kVec>) mrs_norm_grad_kernel(const NormGradArgs a) {
+  extern __shared__ __align__(16) unsigned char smem_raw[];
   __shared__ RowTotals meet[32];
   pdl_trigger();
-  const int tid = threadIdx.x, in_cta = tid / a.tpr, place = tid - in_cta * a.tpr;
-  const size_t cols = 8 * static_cast<size_t>(a.vecs);
-  const int64_t step = static_cast<int64_t>(gridDim.x) * a.per_cta;
+  const int tid = threadIdx.x, in_cta = kOne ? 0 : tid / a.tpr, place = tid - in_cta * a.tpr;
+  const int per_cta = kOne ? 1 : a.per_cta;
+  const size_t row_bytes = 16 * static_cast<size_t>(a.vecs), cols = 8 * static_cast<size_t>(a.vecs);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * per_cta;
+  const int64_t begin = static_cast<int64_t>(blockIdx.x) * per_cta;
+  RowStream<kVec, kRowDepth<kVec>> stream(smem_raw, place, a.tpr, a.vecs);
   pdl_wait();
+  // a token's items: s, grad, its rows, grad_sum, those that there are
+  const int rows_of = a.grad_rows != nullptr ? a.parts : 0, behind = a.grad != nullptr ? 2 : 1;
+  const int summed = behind + rows_of, items = summed + (a.grad_sum != nullptr ? 1 : 0);
+  int64_t ahead = begin + in_cta;
+  size_t token = ahead * row_bytes;
+  const unsigned char* next_rows = static_cast<const unsigned char*>(a.grad_rows) + token * a.parts;
+  int item = 0;
+  auto put = [&] {
+    const bool of_rows = item >= behind && item < summed;
+    const void* base = item == 0 ? a.s : (item < behind ? a.grad : a.grad_sum);
+    stream.put(ahead < a.rows,
+               of_rows ? next_rows : static_cast<const unsigned char*>(base) + token);
+    if (of_rows) next_rows += row_bytes;
+    if (++item == items) {
+      item = 0;
+      ahead += step;
+      token += step * row_bytes;
+      next_rows += static_cast<size_t>(step - 1) * a.parts * row_bytes;
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < kRowDepth<kVec> - 1; ++i) put();
   float near[kVec][8], far[kVec][8];
 #pragma unroll
   for (int i = 0; i < kVec; ++i)
@@ -119,54 +177,61 @@ __global__ void __launch_bounds__(kRowThreads<kVec>) mrs_norm_grad_kernel(const 
     for (int k = 0; k < 8; ++k) near[i][k] = far[i][k] = 0.0f;
   int added = 0;
   // (a CTA's rows take the same number of turns: they meet in the reduction)
-  for (int64_t first = static_cast<int64_t>(blockIdx.x) * a.per_cta; first < a.rows; first += step) {
+  for (int64_t first = begin; first < a.rows; first += step) {
     const int64_t row = first + in_cta;
     const bool live = row < a.rows;
     const float rstd = live ? __ldg(a.rstd + row) : 0.0f;
     float xh[kVec][8], g[kVec][8];
     float dot = 0.0f;
+    uint4 q[kVec];
+    put();
+    stream.get(q);
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
-      const int at = i * a.tpr + place;
-      if (!live || at >= a.vecs) continue;
-      const size_t here = row * cols + 8 * at;
-      unpack8<T>(load8<T>(a.s, here), xh[i]);
-      float d[8];
+      unpack8<T>(q[i], xh[i]);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) d[k] = 0.0f;
-      if (a.grad != nullptr) unpack8<T>(load8<T>(a.grad, here), d);
-      if (a.grad_rows != nullptr) {
-        const T* p = static_cast<const T*>(a.grad_rows) + static_cast<size_t>(row) * a.parts * cols + 8 * at;
-#pragma unroll 4
-        for (int j = 0; j < a.parts; ++j) {
-          float q[8];
-          unpack8<T>(load8<T>(p, j * cols), q);
+      for (int k = 0; k < 8; ++k) g[i][k] = 0.0f;
+    }
+    for (int j = 1; j < summed; ++j) {
+      put();
+      stream.get(q);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) d[k] += q[k];
-        }
+      for (int i = 0; i < kVec; ++i) {
+        float p[8];
+        unpack8<T>(q[i], p);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) g[i][k] += p[k];
       }
-      load_columns<T>(a.gain, a.gain_f32 != 0, at, g[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      if (!live || i >= stream.count) continue;  // (what was read there is not of this row)
+      float w[8];
+      load_columns<T>(a.gain, a.gain_f32 != 0, i * a.tpr + place, w);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         xh[i][k] *= rstd;
-        near[i][k] += d[k] * xh[i][k];
-        g[i][k] *= d[k];
+        near[i][k] += g[i][k] * xh[i][k];
+        g[i][k] *= w[k];
         dot += g[i][k] * xh[i][k];
       }
     }
     const float mean = row_totals(dot, 0u, a.tpr, meet).sum * a.inv_cols;
+    if (a.grad_sum != nullptr) {
+      put();
+      stream.get(q);
+    }
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
-      const int at = i * a.tpr + place;
-      if (!live || at >= a.vecs) continue;
-      const size_t here = row * cols + 8 * at;
+      if (!live || i >= stream.count) continue;
       float d[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) d[k] = 0.0f;
-      if (a.grad_sum != nullptr) unpack8<T>(load8<T>(a.grad_sum, here), d);
+      if (a.grad_sum != nullptr) unpack8<T>(q[i], d);
 #pragma unroll
       for (int k = 0; k < 8; ++k) d[k] += rstd * (g[i][k] - xh[i][k] * mean);
-      *reinterpret_cast<uint4*>(static_cast<T*>(a.grad_x) + here) = pack8<T>(d);
+      *reinterpret_cast<uint4*>(static_cast<unsigned char*>(a.grad_x) + row * row_bytes +
+                                stream.off[i]) = pack8<T>(d);
     }
     if (++added == kNormSumRows) {
       added = 0;
@@ -225,24 +290,56 @@ int norm_grad_ctas(const RowPlan& p, int sms) {
 }
 RowPlan norm_grad_plan(int cols) { return row_plan(cols, 1, 128); }
 
+constexpr int kNormDeepThreads = 640;  // of CTAs with twice as many items ahead
+
+template <class T, int kVec, int kDepth, bool kOne>
+cudaError_t launch_norm(const NormArgs& a, const RowPlan& p, int sms, cudaStream_t st) {
+  auto* k = mrs_norm_kernel<T, kVec, kDepth, kOne>;
+  const size_t smem = RowStream<kVec, kDepth>::bytes(p.threads);
+  constexpr int most_threads = kDepth > kRowDepth<kVec> ? kNormDeepThreads : kRowThreads<kVec>;
+  static SmemGrant granted;
+  const cudaError_t err = grant_smem(reinterpret_cast<const void*>(k),
+                                     RowStream<kVec, kDepth>::bytes(most_threads), granted);
+  if (err != cudaSuccess) return err;
+  const int64_t most = (a.rows + p.rows - 1) / p.rows, full = row_ctas(p.threads, smem, sms);
+  return launch_pdl(k, dim3(static_cast<unsigned>(most < full ? most : full)), dim3(p.threads), smem,
+                    st, a);
+}
 template <class T>
-cudaError_t launch_norm(const NormArgs& a, const RowPlan& p, cudaStream_t st) {
-  const dim3 grid(static_cast<unsigned>((a.rows + p.rows - 1) / p.rows)), block(p.threads);
+cudaError_t launch_norm(const NormArgs& a, const RowPlan& p, int sms, cudaStream_t st) {
+  // few rows of many items: twice as many on their way
+  if (p.vec == 1 && p.rows == 1 && a.rows <= sms && p.threads <= kNormDeepThreads)
+    return launch_norm<T, 1, 16, true>(a, p, sms, st);
+  const bool one = p.rows == 1;  // (of at most two vectors a thread)
   switch (p.vec) {
-    case 1: return launch_pdl(mrs_norm_kernel<T, 1>, grid, block, 0, st, a);
-    case 2: return launch_pdl(mrs_norm_kernel<T, 2>, grid, block, 0, st, a);
-    case 3: return launch_pdl(mrs_norm_kernel<T, 3>, grid, block, 0, st, a);
-    default: return launch_pdl(mrs_norm_kernel<T, 4>, grid, block, 0, st, a);
+    case 1: return one ? launch_norm<T, 1, kRowDepth<1>, true>(a, p, sms, st)
+                       : launch_norm<T, 1, kRowDepth<1>, false>(a, p, sms, st);
+    case 2: return one ? launch_norm<T, 2, kRowDepth<2>, true>(a, p, sms, st)
+                       : launch_norm<T, 2, kRowDepth<2>, false>(a, p, sms, st);
+    case 3: return launch_norm<T, 3, kRowDepth<3>, false>(a, p, sms, st);
+    default: return launch_norm<T, 4, kRowDepth<4>, false>(a, p, sms, st);
   }
+}
+template <class T, int kVec, bool kOne>
+cudaError_t launch_norm_grad(const NormGradArgs& a, const RowPlan& p, int ctas, cudaStream_t st) {
+  auto* k = mrs_norm_grad_kernel<T, kVec, kOne>;
+  using Stream = RowStream<kVec, kRowDepth<kVec>>;
+  static SmemGrant granted;
+  const cudaError_t err =
+      grant_smem(reinterpret_cast<const void*>(k), Stream::bytes(kRowThreads<kVec>), granted);
+  if (err != cudaSuccess) return err;
+  return launch_pdl(k, dim3(ctas), dim3(p.threads), Stream::bytes(p.threads), st, a);
 }
 template <class T>
 cudaError_t launch_norm_grad(const NormGradArgs& a, const RowPlan& p, int ctas, cudaStream_t st) {
-  const dim3 grid(ctas), block(p.threads);
+  const bool one = p.rows == 1;
   switch (p.vec) {
-    case 1: return launch_pdl(mrs_norm_grad_kernel<T, 1>, grid, block, 0, st, a);
-    case 2: return launch_pdl(mrs_norm_grad_kernel<T, 2>, grid, block, 0, st, a);
-    case 3: return launch_pdl(mrs_norm_grad_kernel<T, 3>, grid, block, 0, st, a);
-    default: return launch_pdl(mrs_norm_grad_kernel<T, 4>, grid, block, 0, st, a);
+    case 1: return one ? launch_norm_grad<T, 1, true>(a, p, ctas, st)
+                       : launch_norm_grad<T, 1, false>(a, p, ctas, st);
+    case 2: return one ? launch_norm_grad<T, 2, true>(a, p, ctas, st)
+                       : launch_norm_grad<T, 2, false>(a, p, ctas, st);
+    case 3: return launch_norm_grad<T, 3, false>(a, p, ctas, st);
+    default: return launch_norm_grad<T, 4, false>(a, p, ctas, st);
   }
 }
 
@@ -313,8 +410,10 @@ int moe_rms_norm(const void* x, int dtype, int64_t x_stride, int parts, const vo
   a.codes = codes;
   a.scales = scales;
   a.rstd = rstd;
-  return launch_status(dtype == MOE_RS_BF16 ? launch_norm<__nv_bfloat16>(a, p, stream)
-                                            : launch_norm<__half>(a, p, stream));
+  const int sms = sm_count();
+  if (sms == 0) return launch_status(cudaErrorInvalidDevice);
+  return launch_status(dtype == MOE_RS_BF16 ? launch_norm<__nv_bfloat16>(a, p, sms, stream)
+                                            : launch_norm<__half>(a, p, sms, stream));
 }
 
 size_t moe_rms_norm_backward_workspace_bytes(int cols) {
