@@ -19,8 +19,7 @@
 //   1      the list: rows, routes and factors of the next units into a ring in shared memory
 //   2      in the first CTA of a pair the products; both CTAs' copies are counted on its barriers
 //   4-11   finished tiles from tensor memory to the output rows, while the next one is computed
-//   12-14  copies of a step's rows by threads; 15 and 3 those of the last rows; 16 says when they
-//          are there (tiles of 64 rows: 12 to 15 gather them)
+//   12-15  copies of a step's rows; 3 says when those that threads write are there
 // Every wait is bounded; one that gives up ends its warp's task with the status bit set.  The CTAs
 // of a pair leave together.
 #include <cuda_bf16.h>
@@ -164,14 +163,17 @@ struct ProductArgs {
 constexpr int kProductTmem = 512;
 constexpr int kPairRows = 256;  // m of a tile
 constexpr int kInfoSlots = 3;
-constexpr int kInfoUsers = 9;  // weights and eight storing warps; products and those with rows
-// The first rows of a CTA's half are copied by threads, 32 by each of so many warps; those behind
-// them are gathered by tensor copies.
+constexpr int kInfoUsers = 14;  // weights, announcer, eight that store, four with rows; the products
+// A CTA's half of a tile's rows is copied by threads, 32 rows by a warp: of wide tiles the first 96 rows
+// by a warp each and those behind them gathered by tensor copies, on the first lanes of warp 15 and of
+// the weights' warp; of tiles of 64 rows all 32, by four warps that take steps in turn.  (A gather of
+// four rows takes its warp up to 400 clocks.)
 template <int R>
-constexpr int kThreadWarps = R > 64 ? 3 : 0;
-// Warps that gather: 15 and the weights' one, or 12 to 15.
+constexpr int kRowWarps = R > 64 ? 3 : 1;   // of a step
 template <int R>
-constexpr int kGatherWarps = R > 64 ? 2 : 4;
+constexpr int kRowTurns = R > 64 ? 1 : 4;
+template <int R>
+constexpr int kGatherWarps = R > 64 ? 2 : 0;
 constexpr int kProductThreads = 512;
 
 // H: 256 m at a time, one or two of them on the same rows
@@ -221,9 +223,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   pdl_trigger();
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(&full_s[s], kThreadWarps<R> > 0 ? 3 : 1);  // the copies, both CTAs' threads
+      mbar_init(&full_s[s], 3);  // the tensor copies, both CTAs' threads
       mbar_init(&free_s[s], 1);
-      mbar_init(&rows_s[s], kThreadWarps<R> > 0 ? 32 * kThreadWarps<R> : 1);  // every copying thread
+      mbar_init(&rows_s[s], 32 * kRowWarps<R>);  // every copying thread
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full_s[b], 1);
@@ -231,7 +233,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     }
     for (int i = 0; i < kInfoSlots; ++i) {
       mbar_init(&info_full_s[i], 32);
-      mbar_init(&info_free_s[i], kInfoUsers + (rank == 0 ? 1 : 0) + (R > 64 ? 5 : 4));
+      mbar_init(&info_free_s[i], kInfoUsers + (rank == 0 ? 1 : 0));
     }
     mbar_init(&done_s, 1);
     fence_mbar_init();
@@ -283,9 +285,10 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       warp_wait(&free_s[i % S], static_cast<uint32_t>(i / S) & 1u, kWaitLimitNs);
   };
 
-  // Fours of rows that are gathered: kQuads by the first lanes of gathering warp `g`.
-  constexpr int kQuads = (R / 2 - 32 * kThreadWarps<R>) / 4 / kGatherWarps<R>;
-  const auto quad_of = [&](int g) { return 8 * kThreadWarps<R> + g * kQuads + lane; };
+  // Fours of rows that are gathered, by the first lanes of gathering warp `g`.
+  constexpr int kFirst = 32 * kRowWarps<R>;  // row of those that are gathered
+  constexpr int kQuads = (R / 2 - kFirst) / 4 / (kGatherWarps<R> > 0 ? kGatherWarps<R> : 1);
+  const auto quad_of = [&](int g) { return kFirst / 4 + g * kQuads + lane; };
   auto rows_to_gather = [&](const ProductInfo<R>& q, int g, int4& src) {
     const bool mine = lane < kQuads && 4 * quad_of(g) < q.half;
     if (mine) src = *reinterpret_cast<const int4*>(&q.src[4 * quad_of(g)]);
@@ -295,6 +298,14 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     pair_gather4(xbase + slot * Sh::kX + 512 * quad_of(g), &xmap, (kFp8 ? 128 : 64) * ks, src,
                  pair_first(&full_s[slot]));
   };
+  // Boxes of weights that lie behind the last m are not copied: what is there meets no output.
+  constexpr int kBoxM = kTranspose ? 64 : 128;
+  auto weight_bytes = [&](int m) {  // of both CTAs, for the tile at m
+    int boxes = 0;
+#pragma unroll
+    for (int i = 0; i < H * kPairRows / kBoxM; ++i) boxes += m + i * kBoxM < a.M ? 1 : 0;
+    return boxes * kBoxM * 128;
+  };
 
   if (warp == 0) {
     int e = 0, m0 = 0, half = 0;
@@ -303,36 +314,34 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     copy_steps(
         [&](const ProductInfo<R>& q) {
           e = q.e;
-          m0 = q.m0 + 128 * rank;
+          m0 = q.m0;
           half = q.half;
-          if constexpr (kThreadWarps<R> > 0) mine = rows_to_gather(q, 1, src);
+          if constexpr (kGatherWarps<R> > 0) mine = rows_to_gather(q, 1, src);
         },
         [&](int slot, int c, int ks) {
           if (elect_one()) {
-            // both CTAs' bytes
+            const int m = m0 + c * H * kPairRows;
             if (rank == 0)
-              mbar_expect(&full_s[slot],
-                          2 * (Sh::kW + max(half - 32 * kThreadWarps<R>, 0) * 128));
+              mbar_expect(&full_s[slot], weight_bytes(m) + 2 * 128 * max(half - kFirst, 0));
             const uint32_t bar = pair_first(&full_s[slot]);
 #pragma unroll
-            for (int h = 0; h < H; ++h) {
-              const uint32_t to = wbase + slot * Sh::kW + h * (128 * 128);
-              const int m = m0 + (c * H + h) * kPairRows;
-              if constexpr (kTranspose) {
-                pair_load_3d(to, &wmap, m, 64 * ks, e, bar);
-                pair_load_3d(to + 64 * 128, &wmap, m + 64, 64 * ks, e, bar);
-              } else {
-                pair_load_3d(to, &wmap, (kFp8 ? 128 : 64) * ks, m, e, bar);
+            for (int h = 0; h < H; ++h)
+#pragma unroll
+              for (int i = 0; i < 128 / kBoxM; ++i) {
+                const uint32_t to = wbase + slot * Sh::kW + h * (128 * 128) + i * (64 * 128);
+                const int at_m = m + h * kPairRows + 128 * rank + i * kBoxM;
+                if (at_m >= a.M) continue;
+                if constexpr (kTranspose) pair_load_3d(to, &wmap, at_m, 64 * ks, e, bar);
+                else pair_load_3d(to, &wmap, (kFp8 ? 128 : 64) * ks, at_m, e, bar);
               }
-            }
           }
-          if constexpr (kThreadWarps<R> > 0) {
+          if constexpr (kGatherWarps<R> > 0) {
             __syncwarp();
             if (mine) gather(slot, 1, ks, src);
           }
           __syncwarp();
         });
-  } else if (warp == 3 && kThreadWarps<R> > 0) {
+  } else if (warp == 3) {
     // Rows written by threads are announced to the tensor cores.  (The thread that issues the
     // products would spend more clocks on these waits and the fence than the products take: 1340 us
     // for T = 8192, E = 64, 7168 -> 2048.)
@@ -353,32 +362,39 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       at.skip(steps);
       leave_unit();
     }
-  } else if (warp >= 12 + kThreadWarps<R>) {
+  } else if (warp == 15 && kGatherWarps<R> > 0) {
     int4 src;
     bool mine = false;
-    copy_steps([&](const ProductInfo<R>& q) { mine = rows_to_gather(q, 15 - warp, src); },
+    copy_steps([&](const ProductInfo<R>& q) { mine = rows_to_gather(q, 0, src); },
                [&](int slot, int, int ks) {
-                 if (mine) gather(slot, 15 - warp, ks, src);
+                 if (mine) gather(slot, 0, ks, src);
                  __syncwarp();
                });
   } else if (warp >= 12) {
-    // a warp copies 32 rows of the CTA's half, four rows (8 lanes each) at a time
+    // a warp copies 32 rows of the CTA's half, four rows (8 lanes each) at a time, in every step or
+    // in every kRowTurns-th
+    constexpr int kTurns = kRowTurns<R>;
     Ring<S> at;
-    const int w32 = 32 * (warp - 12), chunk = lane & 7, sub = lane >> 3;
+    const int w32 = kTurns == 1 ? 32 * (warp - 12) : 0, chunk = lane & 7, sub = lane >> 3;
+    const int turn = (warp - 12) % kTurns;
+    int now = 0;  // whose step it is
     const size_t row_bytes = static_cast<size_t>(a.K) * (kFp8 ? 1 : 2);
     // row 4 j + sub of the warp: two swizzles, for even and odd j
     const uint32_t place = xbase + (w32 + sub) * 128;
     const uint32_t even = place + 16 * (chunk ^ sub), odd = place + 16 * (chunk ^ (sub + 4));
     while (const ProductInfo<R>* q = next_unit()) {
-      const int tiles = q->tiles, mine = q->half - w32;
+      const int steps = q->tiles * a.ksteps, mine = q->half - w32;
       const unsigned char* from[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         from[j] = a.x + (4 * j < mine ? q->src[w32 + 4 * j + sub] * row_bytes : 0) + 16 * chunk;
-      for (int c = 0; ok && c < tiles; ++c) {
-        for (int ks = 0; ks < a.ksteps; ++ks) {
-          ok = thread_wait(&free_s[at.slot], at.phase ^ 1u, limit);
-          if (!ok) break;  // this lane; the others follow below
+      const int first = (turn - now + kTurns) % kTurns;
+      at.skip(min(first, steps));
+      int ks = first;
+      for (int i = first; i < steps; i += kTurns) {
+        while (ks >= a.ksteps) ks -= a.ksteps;
+        ok = ok && thread_wait(&free_s[at.slot], at.phase ^ 1u, limit);
+        if (ok) {  // (a lane whose wait gave up goes along until the unit ends)
           const uint32_t to = at.slot * Sh::kX;
           // columns past K are zeros
           const bool in = static_cast<size_t>(128 * ks + 16 * chunk) < row_bytes;
@@ -387,10 +403,12 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           for (int j = 0; j < 8; ++j)
             if (4 * j < mine) copy16(((j & 1) ? odd : even) + to + 512 * j, from[j] + off, in ? 16 : 0);
           copy_arrive(&rows_s[at.slot]);
-          at.advance();
         }
-        ok = __all_sync(kFull, ok);
+        at.skip(min(kTurns, steps - i));
+        ks += kTurns;
       }
+      now = (now + steps) % kTurns;
+      ok = __all_sync(kFull, ok);
       leave_unit();
     }
     copy_wait_all();
@@ -626,10 +644,12 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           }
         };
         uint32_t one[32], two[32];
-        if (32 * half < n) load(32 * half, one);
-        for (int j0 = 32 * half; j0 < n; j0 += 128) {
-          store(j0, one, two);
-          if (j0 + 64 < n) store(j0 + 64, two, one);
+        if (32 * half < n && m32 < a.M) load(32 * half, one);
+        if (m32 < a.M) {
+          for (int j0 = 32 * half; j0 < n; j0 += 128) {
+            store(j0, one, two);
+            if (j0 + 64 < n) store(j0 + 64, two, one);
+          }
         }
         tc_fence_before();
         __syncwarp();
@@ -677,6 +697,7 @@ EncodeFn encode_fn() {
 CUtensorMapDataType map_type(int type) {
   return type == MOE_RS_BF16   ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
          : type == MOE_RS_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+         : type == MOE_RS_FP32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                : CU_TENSOR_MAP_DATA_TYPE_UINT8;
 }
 

@@ -13,7 +13,6 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
-#include "mrs_mx.cuh"
 #include "mrs_product.cuh"
 
 namespace mrs {
@@ -22,13 +21,11 @@ struct WeightGradArgs {
   ProductTable t;
   const int32_t* sid;
   const unsigned char *g, *x;
-  void* out;
   unsigned long long wait_limit_ns;
   int routes, topk, g_per_route, x_per_route;
   int E, N, K, P, B;
   int mtiles, ktiles;
   int type, out_type;
-  int wide;  // rows of the output start on 32 bytes
 };
 
 constexpr int kGradCopiers = 8;          // warps that copy a step, four for each operand
@@ -40,7 +37,9 @@ constexpr int kGradInfo = 4;
 constexpr int kGradUsers = 9 + kGradTurns * kGradCopiers;  // eight storing warps, copies, their announcer
 constexpr int kGradDeep = 64;            // rows of a step
 constexpr int kGradTile = 128 * 128;     // bytes of an operand in a CTA and step
-constexpr size_t kGradSmem = static_cast<size_t>(kGradSlots) * 2 * kGradTile + 1024;
+constexpr int kGradStage = 32 * 128;     // of a storing warp: 128 bytes of 32 rows
+constexpr size_t kGradSmem =
+    static_cast<size_t>(kGradSlots) * 2 * kGradTile + 8 * kGradStage + 1024;
 
 struct GradInfo {
   int e, p0, rows, m0, k0;  // e < 0: no more units
@@ -48,7 +47,7 @@ struct GradInfo {
 
 template <class Out>
 __global__ void __launch_bounds__(kGradThreads, 1)
-    mrs_weight_grad_kernel(const WeightGradArgs a) {
+    mrs_weight_grad_kernel(const __grid_constant__ CUtensorMap omap, const WeightGradArgs a) {
   constexpr int S = kGradSlots;
   extern __shared__ unsigned char smem_raw[];
   __shared__ unsigned long long rows_s[S], free_s[S], full_s[S], acc_full_s[2], acc_free_s[2],
@@ -147,9 +146,11 @@ __global__ void __launch_bounds__(kGradThreads, 1)
               const uint32_t to = place + at.slot * kGradTile;
 #pragma unroll
               for (int j = 0; j < 8; ++j) {
-                const bool is = in && row[j] >= 0;
-                copy16(to + 256 * j + 16 * ((chunk & 7) ^ ((2 * j + sub) & 7)),
-                       mine + (is ? row[j] * row_bytes : 0), is ? 16 : 0);
+                const bool is = row[j] >= 0;
+                // (columns behind the last meet no output)
+                if (in)
+                  copy16(to + 256 * j + 16 * ((chunk & 7) ^ ((2 * j + sub) & 7)),
+                         mine + (is ? row[j] * row_bytes : 0), is ? 16 : 0);
               }
             }
             copy_arrive(&rows_s[at.slot]);
@@ -262,58 +263,66 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     }
   } else if (warp >= 4 && warp < 12) {
     const int quarter = warp & 3, half = (warp - 4) >> 2;
+    const uint32_t stage = base + S * 2 * kGradTile + (warp - 4) * kGradStage;
     const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
     int buf = 0;
     uint32_t acc_phase = 0;
     while (const GradInfo* q = next_unit()) {
-      const int m = q->m0 + 128 * rank + 32 * quarter + lane, k0 = q->k0;
+      const int m = q->m0 + 128 * rank + 32 * quarter, k0 = q->k0, e = q->e;
       const bool some = q->rows > 0;
-      Out* row = static_cast<Out*>(a.out) +
-                 (static_cast<size_t>(q->e) * a.N + min(m, a.N - 1)) * a.K;
       if (some) {
         ok = warp_wait(&acc_full_s[buf], acc_phase, limit);
         if (!ok) break;
         tc_fence_after();
       }
       const uint32_t src = tmem + buf * 256 + lanes;
+      // Tiles of 32 rows by 128 bytes go through shared memory, in the swizzle of the tensor copy that
+      // stores them.  (Lanes that store 32 bytes of a row each take 32 lines an access, beside the
+      // copies that wait for the same unit.)
+      constexpr int kCols = 128 / sizeof(Out);
+      const int last = m < a.N ? min(256, a.K - k0) : 0;
 #pragma unroll 1
-      for (int c0 = 32 * half; c0 < 256; c0 += 64) {
-        uint32_t v[32];
-        __syncwarp();
-        if (some) {
-          tmem_load32(src + c0, v);
-          tmem_wait(v);
-        } else {
+      for (int c0 = kCols * half; c0 < last; c0 += 2 * kCols) {
+        uint32_t w[32];  // the lane's row of the tile
 #pragma unroll
-          for (int c = 0; c < 32; ++c) v[c] = 0u;
-        }
-        if (m >= a.N) continue;
-        if constexpr (sizeof(Out) == 4) {
+        for (int part = 0; part < kCols / 32; ++part) {
+          uint32_t v[32];
+          __syncwarp();
+          if (some) {
+            tmem_load32(src + c0 + 32 * part, v);
+            tmem_wait(v);
+          } else {
 #pragma unroll
-          for (int c = 0; c < 32; c += 8)
-            if (k0 + c0 + c < a.K) store32(row + k0 + c0 + c, a.wide != 0, v + c);
-        } else {
+            for (int c = 0; c < 32; ++c) v[c] = 0u;
+          }
+          if constexpr (sizeof(Out) == 4) {
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const float lo = __uint_as_float(v[2 * c]), hi = __uint_as_float(v[2 * c + 1]);
-            if (a.out_type == MOE_RS_BF16) {
-              const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-              v[c] = *reinterpret_cast<const uint32_t*>(&h);
-            } else {
-              const __half2 h = __floats2half2_rn(lo, hi);
-              v[c] = *reinterpret_cast<const uint32_t*>(&h);
+            for (int c = 0; c < 32; ++c) w[c] = v[c];
+          } else {
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              const float lo = __uint_as_float(v[2 * c]), hi = __uint_as_float(v[2 * c + 1]);
+              if (a.out_type == MOE_RS_BF16) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+                w[16 * part + c] = *reinterpret_cast<const uint32_t*>(&h);
+              } else {
+                const __half2 h = __floats2half2_rn(lo, hi);
+                w[16 * part + c] = *reinterpret_cast<const uint32_t*>(&h);
+              }
             }
           }
-#pragma unroll
-          for (int c = 0; c < 32; c += 16) {
-            const int left = a.K - (k0 + c0 + c);  // a multiple of 8
-            Out* p = row + k0 + c0 + c;
-            if (left >= 16) store32(p, a.wide != 0, v + c / 2);
-            else if (left > 0)
-              *reinterpret_cast<uint4*>(p) = make_uint4(v[c / 2], v[c / 2 + 1], v[c / 2 + 2],
-                                                        v[c / 2 + 3]);
-          }
         }
+        if (lane == 0) tma_store_read();  // what was there has been read
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                           stage + 128 * lane + 16 * (c ^ (lane & 7))),
+                       "r"(w[4 * c]), "r"(w[4 * c + 1]), "r"(w[4 * c + 2]), "r"(w[4 * c + 3])
+                       : "memory");
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tma_store_3d(&omap, stage, k0 + c0, m, e);
       }
       if (some) {
         tc_fence_before();
@@ -326,6 +335,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       }
       leave_unit();
     }
+    if (lane == 0) tma_store_done();  // (a CTA that leaves takes its shared memory along)
+    __syncwarp();
   }
   if (!ok && lane == 0) atomicOr(a.t.head, MOE_RS_DEVICE_WAIT_TIMEOUT);
   __syncwarp();
@@ -339,12 +350,13 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 namespace {
 
 template <class Out>
-cudaError_t launch_weight_grad(const WeightGradArgs& a, int pairs, cudaStream_t st) {
+cudaError_t launch_weight_grad(const CUtensorMap& o, const WeightGradArgs& a, int pairs,
+                               cudaStream_t st) {
   auto* k = mrs_weight_grad_kernel<Out>;
   static SmemGrant granted;
   const cudaError_t err = grant_smem(reinterpret_cast<const void*>(k), kGradSmem, granted);
   if (err != cudaSuccess) return err;
-  return launch_pairs(k, pairs, kGradThreads, kGradSmem, st, a);
+  return launch_pairs(k, pairs, kGradThreads, kGradSmem, st, o, a);
 }
 
 }  // namespace
@@ -414,7 +426,6 @@ extern "C" int moe_experts_grad_weights(
   a.sid = sorted_token_ids;
   a.g = static_cast<const unsigned char*>(grad);
   a.x = static_cast<const unsigned char*>(x);
-  a.out = grad_w;
   a.wait_limit_ns = product_wait_limit();
   a.routes = static_cast<int>(routes);
   a.topk = topk;
@@ -429,11 +440,13 @@ extern "C" int moe_experts_grad_weights(
   a.ktiles = (cols + 255) / 256;
   a.type = dtype == MOE_RS_BF16 ? 1 : 0;
   a.out_type = out_dtype;
-  a.wide = aligned(grad_w, 32) && cols * out_size % 32 == 0;
+  CUtensorMap map;
+  if (!encode_weights3(&map, grad_w, out_dtype, static_cast<int>(out_size), cols, outs, E, 32))
+    return MOE_RS_ERR_LAUNCH;
   cudaError_t err = launch_product_table(ta, stream);
   if (err != cudaSuccess) return launch_status(err);
   const int pairs = units < sms / 2 ? static_cast<int>(units) : sms / 2;
   return launch_status(out_dtype == MOE_RS_FP32
-                           ? launch_weight_grad<float>(a, pairs, stream)
-                           : launch_weight_grad<uint16_t>(a, pairs, stream));
+                           ? launch_weight_grad<float>(map, a, pairs, stream)
+                           : launch_weight_grad<uint16_t>(map, a, pairs, stream));
 }
