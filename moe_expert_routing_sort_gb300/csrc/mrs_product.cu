@@ -11,8 +11,9 @@
 // regular and long, is on the 256 lanes of both tensor memories, the ragged rows are the product's
 // N, which goes in steps of 32: an expert's last rows cost what they are, not a whole tile.  Each
 // CTA brings 128 m and half of the rows into shared memory, 128 bytes of each a step, so that a
-// byte of either operand serves twice the products that it would in one CTA.  Rows are gathered by
-// tensor copies, four rows an instruction.
+// byte of either operand serves twice the products that it would in one CTA.  Rows are copied by
+// threads: tensor copies that gather four rows take their warp 100 to 400 clocks each (T = 8192,
+// E = 64, 7168 -> 2048: 1600 us with four warps of them, 1380 with four warps of thread copies).
 //
 // The warps of a CTA each have one task:
 //   0      copies of a step's weights
@@ -164,16 +165,12 @@ constexpr int kProductTmem = 512;
 constexpr int kPairRows = 256;  // m of a tile
 constexpr int kInfoSlots = 3;
 constexpr int kInfoUsers = 14;  // weights, announcer, eight that store, four with rows; the products
-// A CTA's half of a tile's rows is copied by threads, 32 rows by a warp: of wide tiles the first 96 rows
-// by a warp each and those behind them gathered by tensor copies, on the first lanes of warp 15 and of
-// the weights' warp; of tiles of 64 rows all 32, by four warps that take steps in turn.  (A gather of
-// four rows takes its warp up to 400 clocks.)
+// A CTA's half of a tile's rows is copied by threads, 32 rows by a warp: those of wide tiles by four
+// warps, the 32 of narrow ones by four that take steps in turn.
 template <int R>
-constexpr int kRowWarps = R > 64 ? 3 : 1;   // of a step
+constexpr int kRowWarps = R > 64 ? 4 : 1;  // of a step
 template <int R>
-constexpr int kRowTurns = R > 64 ? 1 : 4;
-template <int R>
-constexpr int kGatherWarps = R > 64 ? 2 : 0;
+constexpr int kRowTurns = 4 / kRowWarps<R>;
 constexpr int kProductThreads = 512;
 
 // H: 256 m at a time, one or two of them on the same rows
@@ -205,8 +202,7 @@ __device__ __forceinline__ uint32_t rounded2(float lo, float hi, int type) {
 
 template <bool kFp8, bool kTranspose, int R, int H, class Out>
 __global__ void __launch_bounds__(kProductThreads, 1)
-    mrs_product_kernel(const __grid_constant__ CUtensorMap wmap,
-                       const __grid_constant__ CUtensorMap xmap, const ProductArgs a) {
+    mrs_product_kernel(const __grid_constant__ CUtensorMap wmap, const ProductArgs a) {
   using Sh = ProductShape<R, H>;
   constexpr int S = Sh::kSlots;
   extern __shared__ unsigned char smem_raw[];
@@ -261,43 +257,6 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     at_info.advance();
   };
 
-  // The next unit's steps: wait for a slot, `copy` into it.
-  auto copy_steps = [&](auto&& open, auto&& copy) {
-    Ring<S> at;
-    long long issued = 0;
-    while (const ProductInfo<R>* q = next_unit()) {
-      const int tiles = q->tiles;
-      open(*q);
-      for (int c = 0; ok && c < tiles; ++c) {
-        for (int ks = 0; ks < a.ksteps; ++ks) {
-          ok = warp_wait(&free_s[at.slot], at.phase ^ 1u, limit);
-          if (!ok) break;
-          copy(at.slot, c, ks);
-          ++issued;
-          at.advance();
-        }
-      }
-      leave_unit();
-    }
-    // Nothing may land in the shared memory of a CTA that has left: what was copied has been used,
-    // or, where a wait gave up, had this long to land.
-    for (long long i = issued > S ? issued - S : 0; i < issued; ++i)
-      warp_wait(&free_s[i % S], static_cast<uint32_t>(i / S) & 1u, kWaitLimitNs);
-  };
-
-  // Fours of rows that are gathered, by the first lanes of gathering warp `g`.
-  constexpr int kFirst = 32 * kRowWarps<R>;  // row of those that are gathered
-  constexpr int kQuads = (R / 2 - kFirst) / 4 / (kGatherWarps<R> > 0 ? kGatherWarps<R> : 1);
-  const auto quad_of = [&](int g) { return kFirst / 4 + g * kQuads + lane; };
-  auto rows_to_gather = [&](const ProductInfo<R>& q, int g, int4& src) {
-    const bool mine = lane < kQuads && 4 * quad_of(g) < q.half;
-    if (mine) src = *reinterpret_cast<const int4*>(&q.src[4 * quad_of(g)]);
-    return mine;
-  };
-  auto gather = [&](int slot, int g, int ks, const int4& src) {
-    pair_gather4(xbase + slot * Sh::kX + 512 * quad_of(g), &xmap, (kFp8 ? 128 : 64) * ks, src,
-                 pair_first(&full_s[slot]));
-  };
   // Boxes of weights that lie behind the last m are not copied: what is there meets no output.
   constexpr int kBoxM = kTranspose ? 64 : 128;
   auto weight_bytes = [&](int m) {  // of both CTAs, for the tile at m
@@ -308,39 +267,40 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   };
 
   if (warp == 0) {
-    int e = 0, m0 = 0, half = 0;
-    int4 src;
-    bool mine = false;
-    copy_steps(
-        [&](const ProductInfo<R>& q) {
-          e = q.e;
-          m0 = q.m0;
-          half = q.half;
-          if constexpr (kGatherWarps<R> > 0) mine = rows_to_gather(q, 1, src);
-        },
-        [&](int slot, int c, int ks) {
+    Ring<S> at;
+    long long issued = 0;
+    while (const ProductInfo<R>* q = next_unit()) {
+      const int e = q->e, tiles = q->tiles;
+      for (int c = 0; ok && c < tiles; ++c) {
+        const int m = q->m0 + c * H * kPairRows;
+        for (int ks = 0; ks < a.ksteps; ++ks) {
+          ok = warp_wait(&free_s[at.slot], at.phase ^ 1u, limit);
+          if (!ok) break;
           if (elect_one()) {
-            const int m = m0 + c * H * kPairRows;
-            if (rank == 0)
-              mbar_expect(&full_s[slot], weight_bytes(m) + 2 * 128 * max(half - kFirst, 0));
-            const uint32_t bar = pair_first(&full_s[slot]);
+            if (rank == 0) mbar_expect(&full_s[at.slot], weight_bytes(m));
+            const uint32_t bar = pair_first(&full_s[at.slot]);
 #pragma unroll
             for (int h = 0; h < H; ++h)
 #pragma unroll
               for (int i = 0; i < 128 / kBoxM; ++i) {
-                const uint32_t to = wbase + slot * Sh::kW + h * (128 * 128) + i * (64 * 128);
+                const uint32_t to = wbase + at.slot * Sh::kW + h * (128 * 128) + i * (64 * 128);
                 const int at_m = m + h * kPairRows + 128 * rank + i * kBoxM;
                 if (at_m >= a.M) continue;
                 if constexpr (kTranspose) pair_load_3d(to, &wmap, at_m, 64 * ks, e, bar);
                 else pair_load_3d(to, &wmap, (kFp8 ? 128 : 64) * ks, at_m, e, bar);
               }
           }
-          if constexpr (kGatherWarps<R> > 0) {
-            __syncwarp();
-            if (mine) gather(slot, 1, ks, src);
-          }
           __syncwarp();
-        });
+          ++issued;
+          at.advance();
+        }
+      }
+      leave_unit();
+    }
+    // Nothing may land in the shared memory of a CTA that has left: what was copied has been used,
+    // or, where a wait gave up, had this long to land.
+    for (long long i = issued > S ? issued - S : 0; i < issued; ++i)
+      warp_wait(&free_s[i % S], static_cast<uint32_t>(i / S) & 1u, kWaitLimitNs);
   } else if (warp == 3) {
     // Rows written by threads are announced to the tensor cores.  (The thread that issues the
     // products would spend more clocks on these waits and the fence than the products take: 1340 us
@@ -362,14 +322,6 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       at.skip(steps);
       leave_unit();
     }
-  } else if (warp == 15 && kGatherWarps<R> > 0) {
-    int4 src;
-    bool mine = false;
-    copy_steps([&](const ProductInfo<R>& q) { mine = rows_to_gather(q, 0, src); },
-               [&](int slot, int, int ks) {
-                 if (mine) gather(slot, 0, ks, src);
-                 __syncwarp();
-               });
   } else if (warp >= 12) {
     // a warp copies 32 rows of the CTA's half, four rows (8 lanes each) at a time, in every step or
     // in every kRowTurns-th
@@ -703,18 +655,6 @@ CUtensorMapDataType map_type(int type) {
 
 }  // namespace
 
-bool encode_rows(CUtensorMap* map, const void* p, int type, int size, size_t cols, size_t rows) {
-  const EncodeFn fn = encode_fn();
-  if (fn == nullptr) return false;
-  const cuuint64_t dims[2] = {cols, rows};
-  const cuuint64_t strides[1] = {cols * size};
-  const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / size), 1};
-  const cuuint32_t one[2] = {1, 1};
-  return fn(map, map_type(type), 2, const_cast<void*>(p), dims, strides, box, one,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 bool encode_few(CUtensorMap* map, const void* p, size_t row_bytes, size_t rows, size_t E) {
   const EncodeFn fn = encode_fn();
   if (fn == nullptr) return false;
@@ -745,22 +685,21 @@ bool encode_weights3(CUtensorMap* map, const void* p, int type, int size, size_t
 namespace {
 
 template <bool kFp8, bool kTranspose, int R, int H, class Out>
-cudaError_t launch_product(const CUtensorMap& w, const CUtensorMap& x, const ProductArgs& a,
-                           int pairs, cudaStream_t st) {
+cudaError_t launch_product(const CUtensorMap& w, const ProductArgs& a, int pairs, cudaStream_t st) {
   auto* k = mrs_product_kernel<kFp8, kTranspose, R, H, Out>;
   constexpr size_t smem = ProductShape<R, H>::kSmem;
   static SmemGrant granted;
   const cudaError_t err = grant_smem(reinterpret_cast<const void*>(k), smem, granted);
   if (err != cudaSuccess) return err;
-  return launch_pairs(k, pairs, kProductThreads, smem, st, w, x, a);
+  return launch_pairs(k, pairs, kProductThreads, smem, st, w, a);
 }
 
 template <int R, int H, class Out>
-cudaError_t launch_product(bool fp8, bool transpose, const CUtensorMap& w, const CUtensorMap& x,
-                           const ProductArgs& a, int pairs, cudaStream_t st) {
-  return transpose ? launch_product<false, true, R, H, Out>(w, x, a, pairs, st)
-         : fp8     ? launch_product<true, false, R, H, Out>(w, x, a, pairs, st)
-                   : launch_product<false, false, R, H, Out>(w, x, a, pairs, st);
+cudaError_t launch_product(bool fp8, bool transpose, const CUtensorMap& w, const ProductArgs& a,
+                           int pairs, cudaStream_t st) {
+  return transpose ? launch_product<false, true, R, H, Out>(w, a, pairs, st)
+         : fp8     ? launch_product<true, false, R, H, Out>(w, a, pairs, st)
+                   : launch_product<false, false, R, H, Out>(w, a, pairs, st);
 }
 
 size_t most_tiles(int T, int E, int topk, int block_m, int rows) {
@@ -895,9 +834,8 @@ int product(const void* x, int type, const float* x_scales, int per_route, const
   a.chunk = (a.mtiles + a.nchunk - 1) / a.nchunk;
   a.nchunk = (a.mtiles + a.chunk - 1) / a.chunk;
   if (tiles * a.nchunk > INT32_MAX / 2) return MOE_RS_ERR_OVERFLOW;
-  CUtensorMap wmap, xmap;
-  if (!encode_weights3(&wmap, w, type, static_cast<int>(size), cols, outs, E, transpose ? 64 : 128) ||
-      !encode_rows(&xmap, x, type, static_cast<int>(size), K, xrows))
+  CUtensorMap wmap;
+  if (!encode_weights3(&wmap, w, type, static_cast<int>(size), cols, outs, E, transpose ? 64 : 128))
     return MOE_RS_ERR_LAUNCH;
   cudaError_t err = launch_product_table(ta, stream);
   if (err != cudaSuccess) return launch_status(err);
@@ -905,9 +843,9 @@ int product(const void* x, int type, const float* x_scales, int per_route, const
   const int grid = units < static_cast<size_t>(pairs) ? static_cast<int>(units) : pairs;
   auto go = [&](auto o) {
     using Out = decltype(o);
-    return R == 64  ? launch_product<64, 1, Out>(fp8, transpose, wmap, xmap, a, grid, stream)
-           : H == 2 ? launch_product<256, 2, Out>(fp8, transpose, wmap, xmap, a, grid, stream)
-                    : launch_product<256, 1, Out>(fp8, transpose, wmap, xmap, a, grid, stream);
+    return R == 64  ? launch_product<64, 1, Out>(fp8, transpose, wmap, a, grid, stream)
+           : H == 2 ? launch_product<256, 2, Out>(fp8, transpose, wmap, a, grid, stream)
+                    : launch_product<256, 1, Out>(fp8, transpose, wmap, a, grid, stream);
   };
   return launch_status(out_type == MOE_RS_FP32 ? go(float{}) : go(uint16_t{}));
 }

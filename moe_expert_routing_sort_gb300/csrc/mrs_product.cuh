@@ -64,10 +64,8 @@ struct FewArgs {
 cudaError_t launch_product_few(const CUtensorMap& wmap, FewArgs a, int type, int sms,
                                cudaStream_t st);
 
-// A tensor of up to three dimensions of `size`-byte elements; `box` elements of the innermost
-// dimension are 128 bytes, swizzled by 128; what lies outside reads as zero.  rank 2: for gathers
-// of rows (a box is one row high).
-bool encode_rows(CUtensorMap* map, const void* p, int type, int size, size_t cols, size_t rows);
+// E matrices of `size`-byte elements; a box is 128 bytes of `box_rows` rows of one, swizzled by 128.
+// What lies outside reads as zero and is not stored.
 bool encode_weights3(CUtensorMap* map, const void* p, int type, int size, size_t cols, size_t rows,
                      size_t E, int box_rows);
 

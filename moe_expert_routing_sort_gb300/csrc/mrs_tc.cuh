@@ -322,14 +322,5 @@ __device__ __forceinline__ void pair_load_3d(uint32_t dst, const CUtensorMap* ma
       "l"(map), "r"(mbar), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
-// 128 bytes, from element x on, of four rows of a matrix; rows past its last read as zeros.
-__device__ __forceinline__ void pair_gather4(uint32_t dst, const CUtensorMap* map, int x, int4 row,
-                                             uint32_t mbar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile::gather4.mbarrier::"
-      "complete_tx::bytes [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
-      "l"(map), "r"(mbar), "r"(x), "r"(row.x), "r"(row.y), "r"(row.z), "r"(row.w)
-      : "memory");
-}
 
 }  // namespace mrs
