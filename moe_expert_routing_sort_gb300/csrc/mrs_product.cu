@@ -31,37 +31,31 @@
 namespace mrs {
 
 // ------------------------------------------------------------------------ the row tiles
-constexpr int kTableThreads = 1024;
-constexpr int kTableEach = kMaxExperts / kTableThreads;
-
-__global__ void __launch_bounds__(kTableThreads) mrs_product_table_kernel(const TableArgs a) {
-  __shared__ int start[kMaxExperts + 1], used[kMaxExperts];
-  __shared__ int meet[32];
+// Cuts the list into tiles: kThreads threads of a CTA, start [E + 1] and used [E] its shared memory,
+// meet a word for each warp.  put(i, expert, first row, rows) gets tile i; returns how many there are.
+template <int kThreads, class Put>
+__device__ __forceinline__ int cut_list(const ListArgs& a, int* start, int* used, int* meet,
+                                        int32_t* status, Put&& put) {
+  constexpr int kWarps = kThreads / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  pdl_trigger();
-  pdl_wait();
   const int blocks = min(max(__ldg(a.npp), 0), a.max_rows) >> a.log2B;
-  for (int e = tid; e <= a.E; e += kTableThreads) start[e] = blocks;
+  for (int e = tid; e <= a.E; e += kThreads) start[e] = blocks;
   __syncthreads();
   bool bad = false;
 #pragma unroll 4
-  for (int b = tid; b < blocks; b += kTableThreads) {
+  for (int b = tid; b < blocks; b += kThreads) {
     const int e = __ldg(a.eid + b), before = b > 0 ? __ldg(a.eid + b - 1) : -1;
     if (e < 0 || e >= a.E || e < before) bad = true;
     else if (e != before) start[e] = b;
   }
-  if (__syncthreads_or(bad) && tid == 0) atomicOr(a.t.head, MOE_RS_DEVICE_BAD_EXPERT_ID);
+  if (__syncthreads_or(bad) && tid == 0) atomicOr(status, MOE_RS_DEVICE_BAD_EXPERT_ID);
   // an expert without a run starts where the next one does: the least start from it on (which is
   // in order whatever the list holds)
-  const int e0 = tid * kTableEach;
-  int first[kTableEach + 1];
+  const int each = (a.E + kThreads - 1) / kThreads, e0 = min(tid * each, a.E), e1 = min(e0 + each, a.E);
   int least = blocks;
+  for (int e = e0; e < e1; ++e) least = min(least, start[e]);
+  int after = least;  // of the warp's threads from this one on
 #pragma unroll
-  for (int i = kTableEach - 1; i >= 0; --i) {
-    least = min(least, e0 + i < a.E ? start[e0 + i] : blocks);
-    first[i] = least;
-  }
-  int after = least;  // of the threads from this one on
   for (int o = 1; o < 32; o <<= 1) {
     const int v = __shfl_down_sync(kFull, after, o);
     if (lane + o < 32) after = min(after, v);
@@ -70,91 +64,79 @@ __global__ void __launch_bounds__(kTableThreads) mrs_product_table_kernel(const 
   int next = __shfl_down_sync(kFull, after, 1);
   if (lane == 31) next = blocks;
   __syncthreads();
-  for (int w = warp + 1; w < 32; ++w) next = min(next, meet[w]);
-  first[kTableEach] = next;
-#pragma unroll
-  for (int i = 0; i < kTableEach; ++i) first[i] = min(first[i], next);
-  __syncthreads();  // meet has been read, start too
-#pragma unroll
-  for (int i = 0; i < kTableEach; ++i)
-    if (e0 + i <= a.E) start[e0 + i] = first[i];
-  if (e0 + kTableEach == a.E) start[a.E] = first[kTableEach];
+  for (int w = warp + 1; w < kWarps; ++w) next = min(next, meet[w]);
+  for (int e = e1 - 1; e >= e0; --e) start[e] = next = min(next, start[e]);
   __syncthreads();
-  for (int e = tid; e <= a.E; e += kTableThreads) a.t.offs[e] = start[e];
-  // rows of each run; where asked for, up to its last route: routes come first in the last block,
-  // whose quarters are searched
-  for (int e = tid; e < a.E; e += kTableThreads) {
-    const int rows = (start[e + 1] - start[e]) * a.B;
-    int lo = rows;
-    if (a.want_used && rows > 0) {
-      const int32_t* s = a.sid + start[e] * static_cast<int64_t>(a.B) + rows - a.B;
-      int n = a.B;  // of the last block's entries lo .. lo + n - 1 it is not known
-      lo = 0;
-      while (n > 0) {
-        const int q = (n + 3) >> 2;
-        int routes = 0;
-#pragma unroll
-        for (int i = 0; i < 3; ++i) {
-          const int at = min((i + 1) * q, n) - 1;
-          const int r = __ldg(s + lo + at);
-          routes += r >= 0 && r < a.routes ? 1 : 0;
-        }
-        const int before = min(routes * q, n), last = min(before + q, n);
-        lo += before;
-        n = routes == 3 ? n - before : last - before - 1;  // (the last of a quarter is no route)
-      }
-      lo += rows - a.B;
+  // rows of each run; where asked for, up to its last route: routes come first in its last block
+  for (int e = tid; e < a.E; e += kThreads) {
+    const int p0 = start[e] * a.B, rows = (start[e + 1] - start[e]) * a.B;
+    used[e] = rows;
+    if (a.by_used && rows > 0) {
+      const int32_t* s = a.sid + p0 + rows - a.B;
+      used[e] = rows - a.B + prefix_length(a.B, [&](int i) {
+                  const int r = __ldg(s + i);
+                  return r >= 0 && r < a.routes;
+                });
     }
-    used[e] = lo;
-    if (a.want_used) a.t.used[e] = lo;
   }
   __syncthreads();
-  // tiles of at most a.rows rows, the tiles of a run alike where its length is known
-  int each[kTableEach], count = 0;
-#pragma unroll
-  for (int i = 0; i < kTableEach; ++i) {
-    const int64_t rows = e0 + i < a.E ? used[e0 + i] : 0;
-    const int64_t n = (rows + a.rows - 1) / a.rows;
-    each[i] = n == 0 ? a.rows
-                     : min(static_cast<int>(((rows + n - 1) / n + 31) & ~int64_t{31}), a.rows);
-    if (!a.want_used) each[i] = a.rows;
-    count += static_cast<int>((rows + each[i] - 1) / each[i]);
+  auto tile_rows = [&](int e) {
+    const int64_t rows = used[e], n = (rows + a.rows - 1) / a.rows;
+    if (!a.by_used || n == 0) return a.rows;
+    return min(static_cast<int>((rows + n - 1) / n + 31) & ~31, a.rows);
+  };
+  int count = 0;
+  for (int e = e0; e < e1; ++e) {
+    const int64_t t = tile_rows(e);
+    count += static_cast<int>((used[e] + t - 1) / t);
   }
   int sum = count;  // tiles up to this thread's experts
+#pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int v = __shfl_up_sync(kFull, sum, o);
     if (lane >= o) sum += v;
   }
   if (lane == 31) meet[warp] = sum;
   __syncthreads();
-  for (int w = 0; w < warp; ++w) sum += meet[w];
-  int at = sum - count;
-  if (tid == kTableThreads - 1) a.t.head[1] = min(sum, a.max_tiles);
-#pragma unroll
-  for (int i = 0; i < kTableEach; ++i) {
-    const int e = e0 + i;
-    if (e >= a.E) break;
-    const int p0 = start[e] * a.B, rows = used[e];
-    for (int64_t r = 0; r < rows; r += each[i], ++at)
-      if (at < a.max_tiles)
-        a.t.tiles[at] = make_int4(e, p0 + static_cast<int>(r),
-                                  min(each[i], rows - static_cast<int>(r)), 0);
+  int total = 0;
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) sum += meet[w];
+    total += meet[w];
   }
+  int at = sum - count;
+  for (int e = e0; e < e1; ++e) {
+    const int p0 = start[e] * a.B, rows = used[e], t = tile_rows(e);
+    for (int64_t r = 0; r < rows; r += t, ++at)
+      put(at, e, p0 + static_cast<int>(r), min(t, rows - static_cast<int>(r)));
+  }
+  return total;
 }
 
-cudaError_t launch_product_table(const TableArgs& a, cudaStream_t st) {
-  return launch_pdl(mrs_product_table_kernel, dim3(1), dim3(kTableThreads), 0, st, a);
+// Of lists that are too long for every CTA of the product to cut them: one CTA, into the workspace.
+constexpr int kTableThreads = 1024;
+
+__global__ void __launch_bounds__(kTableThreads)
+    mrs_product_table_kernel(const ListArgs a, const ProductTable t, int max_tiles) {
+  __shared__ int start[kMaxExperts + 1], used[kMaxExperts], meet[32];
+  pdl_trigger();
+  pdl_wait();
+  const int n = cut_list<kTableThreads>(a, start, used, meet, t.head,
+                                        [&](int i, int e, int p0, int rows) {
+                                          if (i < max_tiles) t.tiles[i] = make_int4(e, p0, rows, 0);
+                                        });
+  if (threadIdx.x == 0) t.head[1] = min(n, max_tiles);
 }
 
 // ------------------------------------------------------------------------- the products
 struct ProductArgs {
+  ListArgs list;
   ProductTable t;
-  const int32_t* sid;
+  int here;  // every CTA cuts the list by itself
   const float *sw, *xs, *ws;  // or null
   const unsigned char* x;
   void* out;
   unsigned long long wait_limit_ns;
-  int routes, topk, per_route, max_tiles;
+  int topk, per_route, max_tiles;
   int E, M, K, P;  // M: outputs of the product; K: the contraction; P: rows of the list at most
   int mtiles, chunk, nchunk, ksteps;
   int type;        // of the operands: 0 fp16 or e4m3, 1 bf16
@@ -164,6 +146,8 @@ struct ProductArgs {
 constexpr int kProductTmem = 512;
 constexpr int kPairRows = 256;  // m of a tile
 constexpr int kInfoSlots = 3;
+constexpr int kTilesHere = 1024;    // of a list that every CTA cuts by itself
+constexpr int kBlocksHere = 8192;
 constexpr int kInfoUsers = 14;  // weights, announcer, eight that store, four with rows; the products
 // A CTA's half of a tile's rows is copied by threads, 32 rows by a warp: those of wide tiles by four
 // warps, the 32 of narrow ones by four that take steps in turn.
@@ -210,6 +194,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       info_full_s[kInfoSlots], info_free_s[kInfoSlots], done_s;
   __shared__ __align__(16) ProductInfo<R> info_s[kInfoSlots];
   __shared__ __align__(16) uint16_t stage_s[sizeof(Out) == 2 ? 8 : 1][32 * 32];
+  __shared__ int2 tiles_s[kTilesHere];  // first row of the list; expert, rows - 1
+  __shared__ int meet_s[32];
   __shared__ uint32_t tmem_s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = static_cast<int>(pair_rank());
@@ -241,6 +227,16 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   tc_fence_after();
   const uint32_t tmem = tmem_s;
   pdl_wait();
+  int tiles_here = 0;
+  if (a.here) {  // (the rings are empty: their memory is used for the cut)
+    int* start = reinterpret_cast<int*>(smem_raw);
+    tiles_here = cut_list<kProductThreads>(
+        a.list, start, start + kMaxExperts + 1, meet_s, a.t.head, [&](int i, int e, int p0, int rows) {
+          if (i < kTilesHere) tiles_s[i] = make_int2(p0, (e << 16) | (rows - 1));
+        });
+    fence_proxy_async_smem();  // the rings' copies come behind these accesses
+    __syncthreads();
+  }
 
   bool ok = true;
   Ring<kInfoSlots> at_info;
@@ -366,7 +362,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     copy_wait_all();
   } else if (warp == 1) {
     // (of this call at most, whatever another one may have left there)
-    const int tiles = min(max(__ldg(a.t.head + 1), 0), a.max_tiles);
+    const int tiles = a.here ? min(tiles_here, kTilesHere)
+                             : min(max(__ldg(a.t.head + 1), 0), a.max_tiles);
     const int units = tiles * a.nchunk, step = gridDim.x >> 1;
     // What a unit takes is looked up over three rounds, so that no round waits for more than one
     // access: its tile, the tile's routes, their factors.
@@ -379,7 +376,13 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       q.rows = 0;
       if (u >= units) return;
       const int t = a.nchunk == 1 ? u : u / a.nchunk, first = (u - t * a.nchunk) * a.chunk;
-      const int4 tile = __ldg(a.t.tiles + t);
+      int4 tile;
+      if (a.here) {
+        const int2 v = tiles_s[t];
+        tile = make_int4(v.y >> 16, v.x, (v.y & 0xffff) + 1, 0);
+      } else {
+        tile = __ldg(a.t.tiles + t);
+      }
       // (a table that another call overwrites must not lead out of this call's buffers)
       q.e = min(max(tile.x, 0), a.E - 1);
       q.p0 = min(max(tile.y, 0), a.P);
@@ -391,13 +394,13 @@ __global__ void __launch_bounds__(kProductThreads, 1)
 #pragma unroll
       for (int j = 0; j < R / 32; ++j) {
         const int i = 32 * j + lane;
-        q.r[j] = i < q.rows ? __ldg(a.sid + q.p0 + i) : -1;
+        q.r[j] = i < q.rows ? __ldg(a.list.sid + q.p0 + i) : -1;
       }
     };
     auto load_factors = [&](Ahead& q) {
 #pragma unroll
       for (int j = 0; j < R / 32; ++j) {
-        if (q.r[j] >= a.routes) q.r[j] = -1;
+        if (q.r[j] >= a.list.routes) q.r[j] = -1;
         const bool is = q.r[j] >= 0;
         if (!is) q.r[j] = -1;
         q.src[j] = is ? (a.per_route ? q.r[j] : q.r[j] / a.topk) : 0;
@@ -789,33 +792,32 @@ int product(const void* x, int type, const float* x_scales, int per_route, const
   }
   const size_t hit = routes < static_cast<size_t>(E) ? routes : E;
   const int R = routes <= 48 * hit ? 64 : 256;
-  TableArgs ta{};
-  ta.t = product_table(workspace, E);
-  ta.eid = eid;
-  ta.sid = sid;
-  ta.npp = npp;
-  ta.E = E;
-  ta.B = block_m;
-  while ((1 << ta.log2B) < block_m) ++ta.log2B;
-  ta.max_rows = static_cast<int>(P);
-  ta.routes = static_cast<int>(routes);
-  ta.rows = R;
-  ta.want_used = R > 64;
+  ListArgs list{};
+  list.eid = eid;
+  list.sid = sid;
+  list.npp = npp;
+  list.E = E;
+  list.B = block_m;
+  while ((1 << list.log2B) < block_m) ++list.log2B;
+  list.max_rows = static_cast<int>(P);
+  list.routes = static_cast<int>(routes);
+  list.rows = R;
+  list.by_used = R > 64;
   const size_t tiles = most_tiles(T, E, topk, block_m, R);
-  ta.max_tiles = static_cast<int>(tiles);
   ProductArgs a{};
-  a.t = ta.t;
-  a.sid = sid;
+  a.list = list;
+  a.t = product_table(workspace);
+  // (a cut takes a CTA 3 us, the table kernel 8)
+  a.here = tiles <= kTilesHere && P / block_m <= kBlocksHere;
   a.sw = sw;
   a.xs = x_scales;
   a.ws = w_scales;
   a.x = static_cast<const unsigned char*>(x);
   a.out = out;
   a.wait_limit_ns = product_wait_limit();
-  a.routes = static_cast<int>(routes);
   a.topk = topk;
   a.per_route = per_route != 0;
-  a.max_tiles = ta.max_tiles;
+  a.max_tiles = static_cast<int>(tiles);
   a.E = E;
   a.M = M;
   a.K = K;
@@ -837,8 +839,11 @@ int product(const void* x, int type, const float* x_scales, int per_route, const
   CUtensorMap wmap;
   if (!encode_weights3(&wmap, w, type, static_cast<int>(size), cols, outs, E, transpose ? 64 : 128))
     return MOE_RS_ERR_LAUNCH;
-  cudaError_t err = launch_product_table(ta, stream);
-  if (err != cudaSuccess) return launch_status(err);
+  if (!a.here) {
+    const cudaError_t err = launch_pdl(mrs_product_table_kernel, dim3(1), dim3(kTableThreads), 0,
+                                       stream, list, a.t, a.max_tiles);
+    if (err != cudaSuccess) return launch_status(err);
+  }
   const size_t units = tiles * a.nchunk;
   const int grid = units < static_cast<size_t>(pairs) ? static_cast<int>(units) : pairs;
   auto go = [&](auto o) {
@@ -864,7 +869,7 @@ size_t moe_experts_product_workspace_bytes(int T, int E, int topk, int block_m) 
   if (static_cast<int64_t>(T) * topk > INT32_MAX ||
       static_cast<int64_t>(moe_sort_max_padded(T, E, topk, block_m)) > INT32_MAX)
     return 0;
-  return product_table_bytes(E, most_tiles(T, E, topk, block_m, kTileRowsLeast));
+  return product_table_bytes(most_tiles(T, E, topk, block_m, kTileRowsLeast));
 }
 
 int moe_experts_product(const void* x, int x_dtype, const float* x_scales, int x_per_route,

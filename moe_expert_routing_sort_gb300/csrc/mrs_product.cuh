@@ -1,5 +1,5 @@
-// mrs_product.cuh -- what the experts' products in 16 and 8 bits and their gradients share: the
-// table of row tiles that a call's sorted list is cut into, and the host side of tensor maps.
+// mrs_product.cuh -- what the experts' products in 16 and 8 bits and their gradients share: how a
+// call's sorted list is searched and cut into row tiles, and the host side of tensor maps.
 #pragma once
 
 #include <climits>
@@ -11,43 +11,45 @@
 
 namespace mrs {
 
-// The workspace: the status word and the number of tiles, the first block of every expert's run
-// (offs[E]: the blocks of the list), the rows of it up to the last route, and the tiles.
+// The workspace: the status word, the number of tiles, and the tiles of lists that are too long for a
+// CTA to cut by itself.
 struct ProductTable {
   int32_t* head;   // [0] status bits (sticky), [1] tiles
-  int32_t* offs;   // [E + 1]
-  int32_t* used;   // [E]
   int4* tiles;     // expert, first row of the list, rows, -
 };
 constexpr int kTileRowsLeast = 64;
 
-inline size_t product_table_bytes(int E, size_t max_tiles) {
-  return 256 + align16(sizeof(int32_t) * (static_cast<size_t>(E) + 1)) +
-         align16(sizeof(int32_t) * static_cast<size_t>(E)) + sizeof(int4) * max_tiles;
-}
-inline ProductTable product_table(void* workspace, int E) {
+inline size_t product_table_bytes(size_t max_tiles) { return 256 + sizeof(int4) * max_tiles; }
+inline ProductTable product_table(void* workspace) {
   char* p = static_cast<char*>(workspace);
-  ProductTable t{};
-  t.head = reinterpret_cast<int32_t*>(p);
-  p += 256;
-  t.offs = reinterpret_cast<int32_t*>(p);
-  p += align16(sizeof(int32_t) * (static_cast<size_t>(E) + 1));
-  t.used = reinterpret_cast<int32_t*>(p);
-  p += align16(sizeof(int32_t) * static_cast<size_t>(E));
-  t.tiles = reinterpret_cast<int4*>(p);
-  return t;
+  return ProductTable{reinterpret_cast<int32_t*>(p), reinterpret_cast<int4*>(p + 256)};
 }
 
-struct TableArgs {
-  ProductTable t;
+// Of n places whose first ones satisfy `is`, how many do: quarters are looked at side by side, so that
+// it takes half as many accesses one behind another as halves.  (Where others do too the answer is some
+// number up to n.)
+template <class P>
+__device__ __forceinline__ int prefix_length(int n, P&& is) {
+  int lo = 0;
+  while (n > 0) {
+    const int q = (n + 3) >> 2;
+    int c = 0;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) c += is(lo + min((i + 1) * q, n) - 1) ? 1 : 0;
+    const int before = min(c * q, n), last = min(before + q, n);
+    lo += before;
+    n = c == 3 ? n - before : last - before - 1;  // (the last of the quarter does not)
+  }
+  return lo;
+}
+
+// The sorted list of a call.
+struct ListArgs {
   const int32_t *eid, *sid, *npp;
   int E, B, log2B, max_rows, routes;
-  int rows;       // rows of a tile
-  int max_tiles;
-  int want_used;  // rows up to the last route are asked for
+  int rows;       // rows of a tile at most
+  int by_used;    // tiles of a run alike, up to its last route; else of `rows` each, up to its last block
 };
-// One CTA: the boundaries of the runs, their tiles' places by a prefix sum, and the tiles.
-cudaError_t launch_product_table(const TableArgs& a, cudaStream_t st);
 
 // The product of a few routes, straight from the list; its weights' map.
 bool encode_few(CUtensorMap* map, const void* p, size_t row_bytes, size_t rows, size_t E);

@@ -18,12 +18,12 @@
 namespace mrs {
 
 struct WeightGradArgs {
-  ProductTable t;
-  const int32_t* sid;
+  ListArgs list;
+  int32_t* status;
   const unsigned char *g, *x;
   unsigned long long wait_limit_ns;
-  int routes, topk, g_per_route, x_per_route;
-  int E, N, K, P, B;
+  int topk, g_per_route, x_per_route;
+  int E, N, K;
   int mtiles, ktiles;
   int type, out_type;
 };
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       // the access: 2200 us for T = 8192, E = 64, 7168 -> 2048)
       auto route_of = [&](int first) {
         const int r = first + w16 + lane;
-        return lane < 16 && r < rows ? __ldg(a.sid + p0 + r) : -1;
+        return lane < 16 && r < rows ? __ldg(a.list.sid + p0 + r) : -1;
       };
       int ahead[4];
       const int skipped = (turn - now + kGradTurns) % kGradTurns, steps = (rows + kGradDeep - 1) / kGradDeep;
@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         for (int k = 0; k < 4; ++k) {
           const int r0 = r4 + k * kStride;
           if (r0 >= rows) break;
-          const int r = ahead[k] >= 0 && ahead[k] < a.routes
+          const int r = ahead[k] >= 0 && ahead[k] < a.list.routes
                             ? (per_route ? ahead[k] : ahead[k] / a.topk) : -1;
           ahead[k] = route_of(r0 + 4 * kStride);
           int row[8];
@@ -165,8 +165,18 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     copy_wait_all();
   } else if (warp == 1) {
     const int each = a.mtiles * a.ktiles, units = a.E * each, step = gridDim.x >> 1;
+    const ListArgs& l = a.list;
+    const int blocks = min(max(__ldg(l.npp), 0), l.max_rows) >> l.log2B;
+    // the searches below take owners in order: every CTA looks at some
+    bool bad = false;
+    for (int b = blockIdx.x * 32 + lane; b < blocks; b += gridDim.x * 32) {
+      const int e = __ldg(l.eid + b);
+      bad |= e < 0 || e >= a.E || (b > 0 && __ldg(l.eid + b - 1) > e);
+    }
+    if (bad) atomicOr(a.status, MOE_RS_DEVICE_BAD_EXPERT_ID);
     for (int u0 = blockIdx.x >> 1; ok && u0 < units; u0 += 32 * step) {
-      // a lane looks up one of the next 32 units
+      // a lane looks up one of the next 32 units: the run of its expert's blocks, and the rows of it
+      // up to the last route (routes come first in its last block)
       const long long u = u0 + static_cast<long long>(lane) * step;
       int e = -1, p0 = 0, rows = 0, m0 = 0, k0 = 0;
       if (u < units) {
@@ -174,10 +184,16 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         const int i = static_cast<int>(u) - e * each, mt = i / a.ktiles;
         m0 = mt * 256;
         k0 = (i - mt * a.ktiles) * 256;
-        // (a table that another call overwrites must not lead out of this call's buffers)
-        p0 = static_cast<int>(min(max(static_cast<long long>(__ldg(a.t.offs + e)) * a.B, 0ll),
-                                  static_cast<long long>(a.P)));
-        rows = min(max(__ldg(a.t.used + e), 0), a.P - p0);
+        const int b0 = prefix_length(blocks, [&](int b) { return __ldg(l.eid + b) < e; });
+        const int n = prefix_length(blocks - b0, [&](int b) { return __ldg(l.eid + b0 + b) <= e; });
+        p0 = b0 * l.B;
+        if (n > 0) {
+          const int32_t* last = l.sid + p0 + (n - 1) * l.B;
+          rows = (n - 1) * l.B + prefix_length(l.B, [&](int i) {
+                   const int r = __ldg(last + i);
+                   return r >= 0 && r < l.routes;
+                 });
+        }
       }
       for (int i = 0; ok && i < 32; ++i) {
         const int ei = __shfl_sync(kFull, e, i);
@@ -338,7 +354,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     if (lane == 0) tma_store_done();  // (a CTA that leaves takes its shared memory along)
     __syncwarp();
   }
-  if (!ok && lane == 0) atomicOr(a.t.head, MOE_RS_DEVICE_WAIT_TIMEOUT);
+  if (!ok && lane == 0) atomicOr(a.status, MOE_RS_DEVICE_WAIT_TIMEOUT);
   __syncwarp();
   tc_fence_before();
   __syncthreads();
@@ -408,34 +424,25 @@ extern "C" int moe_experts_grad_weights(
   if (units > INT32_MAX / 2) return MOE_RS_ERR_OVERFLOW;
   const int sms = sm_count();
   if (sms == 0) return launch_status(cudaErrorInvalidDevice);
-  TableArgs ta{};
-  ta.t = product_table(workspace, E);
-  ta.eid = expert_ids;
-  ta.sid = sorted_token_ids;
-  ta.npp = num_tokens_post_pad;
-  ta.E = E;
-  ta.B = block_m;
-  while ((1 << ta.log2B) < block_m) ++ta.log2B;
-  ta.max_rows = static_cast<int>(P);
-  ta.routes = static_cast<int>(routes);
-  ta.rows = INT32_MAX / 2;  // no tiles are wanted
-  ta.max_tiles = 0;
-  ta.want_used = 1;
   WeightGradArgs a{};
-  a.t = ta.t;
-  a.sid = sorted_token_ids;
+  a.list.eid = expert_ids;
+  a.list.sid = sorted_token_ids;
+  a.list.npp = num_tokens_post_pad;
+  a.list.E = E;
+  a.list.B = block_m;
+  while ((1 << a.list.log2B) < block_m) ++a.list.log2B;
+  a.list.max_rows = static_cast<int>(P);
+  a.status = static_cast<int32_t*>(workspace);
   a.g = static_cast<const unsigned char*>(grad);
   a.x = static_cast<const unsigned char*>(x);
   a.wait_limit_ns = product_wait_limit();
-  a.routes = static_cast<int>(routes);
+  a.list.routes = static_cast<int>(routes);
   a.topk = topk;
   a.g_per_route = g_per_route != 0;
   a.x_per_route = x_per_route != 0;
   a.E = E;
   a.N = outs;
   a.K = cols;
-  a.P = static_cast<int>(P);
-  a.B = block_m;
   a.mtiles = (outs + 255) / 256;
   a.ktiles = (cols + 255) / 256;
   a.type = dtype == MOE_RS_BF16 ? 1 : 0;
@@ -443,8 +450,6 @@ extern "C" int moe_experts_grad_weights(
   CUtensorMap map;
   if (!encode_weights3(&map, grad_w, out_dtype, static_cast<int>(out_size), cols, outs, E, 32))
     return MOE_RS_ERR_LAUNCH;
-  cudaError_t err = launch_product_table(ta, stream);
-  if (err != cudaSuccess) return launch_status(err);
   const int pairs = units < sms / 2 ? static_cast<int>(units) : sms / 2;
   return launch_status(out_dtype == MOE_RS_FP32
                            ? launch_weight_grad<float>(map, a, pairs, stream)
