@@ -153,6 +153,9 @@ __global__ void __launch_bounds__(kRowThreads<kVec>) mrs_fp8_quantize_kernel(con
 
 namespace {
 
+// Rows up to which a row is spread over as many threads as it has vectors.
+constexpr int64_t kGatedFewRows = 152;
+
 enum class GatedKind { kForward, kGradient, kQuantize };
 
 template <class T, int kVec, GatedKind kKind>
@@ -217,7 +220,7 @@ int moe_swiglu(const void* x, int dtype, int64_t x_stride, int64_t rows, int col
                        span(scales, scales ? 4 * r : 0)};
   const Span ins[] = {rows_span(x, rows, 2 * cols, x_stride, 2), span(weights, weights ? 4 * r : 0)};
   if (any_alias(outs, 3, ins, 2)) return MOE_RS_ERR_ALIAS;
-  const RowPlan p = row_plan(cols, 1);
+  const RowPlan p = row_plan(cols, rows <= kGatedFewRows ? 1 : 2);
   GatedArgs a = gated_args(x, x_stride, rows, cols, p);
   a.weights = weights;
   a.y = y;
@@ -243,7 +246,7 @@ int moe_swiglu_backward(const void* grad, const void* x, int dtype, int64_t x_st
   const Span ins[] = {span(grad, 2 * n), rows_span(x, rows, 2 * cols, x_stride, 2),
                       span(weights, weights ? 4 * r : 0)};
   if (any_alias(outs, 2, ins, 3)) return MOE_RS_ERR_ALIAS;
-  const RowPlan p = row_plan(cols, 1);
+  const RowPlan p = row_plan(cols, rows <= kGatedFewRows ? 1 : 2);
   GatedArgs a = gated_args(x, x_stride, rows, cols, p);
   a.grad = grad;
   a.weights = weights;
@@ -267,7 +270,7 @@ int moe_fp8_quantize(const void* x, int x_dtype, int64_t rows, int cols, int64_t
                        span(scales, 4 * static_cast<size_t>(rows))};
   const Span ins[] = {rows_span(x, rows, cols, x_stride, size)};
   if (any_alias(outs, 2, ins, 1)) return MOE_RS_ERR_ALIAS;
-  const RowPlan p = row_plan(cols, 1);
+  const RowPlan p = row_plan(cols, rows <= kGatedFewRows ? 1 : 2);
   GatedArgs a = gated_args(x, x_stride, rows, cols, p);
   a.codes = codes;
   a.scales = scales;

@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(kRowThreads<kVec>) mrs_norm_kernel(const NormA
   // (the rows of a CTA take the same number of turns: they meet in the reduction)
   for (int64_t row = first; row - in_cta < a.rows; row += step) {
     const bool live = row < a.rows;
-    float v[kVec][8];
+    F2 v[kVec][4];
     uint4 q[kVec];
     put();
     stream.get(q);
@@ -76,13 +76,14 @@ __global__ void __launch_bounds__(kRowThreads<kVec>) mrs_norm_kernel(const NormA
       stream.get(q);
 #pragma unroll
       for (int i = 0; i < kVec; ++i) {
-        float p[8];
+        F2 p[4];
         unpack8<T>(q[i], p);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[i][k] += p[k];
+        for (int k = 0; k < 4; ++k) v[i][k] = v[i][k] + p[k];
       }
     }
-    float squares = 0.0f, top = 0.0f;
+    F2 squares = f2(0.0f, 0.0f);
+    float top = 0.0f;
     const size_t here = row * row_bytes;
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
@@ -91,19 +92,22 @@ __global__ void __launch_bounds__(kRowThreads<kVec>) mrs_norm_kernel(const NormA
       unpack8<T>(s, v[i]);
       if (a.sum != nullptr)
         *reinterpret_cast<uint4*>(static_cast<unsigned char*>(a.sum) + here + stream.off[i]) = s;
-      float g[8];
+      F2 g[4];
       load_columns<T>(a.gain, a.gain_f32 != 0, i * a.tpr + place, g);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        squares += v[i][k] * v[i][k];
-        v[i][k] *= g[k];
+      for (int k = 0; k < 4; ++k) {
+        squares = f2_fma(v[i][k], v[i][k], squares);
+        v[i][k] = v[i][k] * g[k];
       }
       if (a.codes != nullptr) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) top = larger(top, v[i][k]);
+        for (int k = 0; k < 4; ++k) {
+          const float2 p = f2_pair(v[i][k]);
+          top = larger(larger(top, p.x), p.y);
+        }
       }
     }
-    const RowTotals r = row_totals(squares, __float_as_uint(top), a.tpr, meet);
+    const RowTotals r = row_totals(f2_sum(squares), __float_as_uint(top), a.tpr, meet);
     const float rstd = __frsqrt_rn(r.sum * a.inv_cols + a.eps);
     const float scale = fp8_scale(magnitude(__uint_as_float(r.top) * rstd));
     if (live && place == 0) {
@@ -114,7 +118,7 @@ __global__ void __launch_bounds__(kRowThreads<kVec>) mrs_norm_kernel(const NormA
     for (int i = 0; i < kVec; ++i) {
       if (!live || i >= stream.count) continue;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[i][k] *= rstd;
+      for (int k = 0; k < 4; ++k) v[i][k] = v[i][k] * f2(rstd, rstd);
       if (a.y != nullptr)
         *reinterpret_cast<uint4*>(static_cast<unsigned char*>(a.y) + here + stream.off[i]) =
             pack8<T>(v[i]);
@@ -136,8 +140,10 @@ struct NormGradArgs {
 
 constexpr int kNormSumRows = 32;
 
-template <class T, int kVec, bool kOne>
-__global__ void __launch_bounds__(kRowThreads<kVec>) mrs_norm_grad_kernel(const NormGradArgs a) {
+// kThreads: of the CTA at most, and two such CTAs an SM where that is below 512.
+template <class T, int kVec, bool kOne, int kThreads = kRowThreads<kVec>>
+__global__ void __launch_bounds__(kThreads, kThreads < 512 && kOne ? 2 : 1)
+    mrs_norm_grad_kernel(const NormGradArgs a) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   __shared__ RowTotals meet[32];
   pdl_trigger();
@@ -170,91 +176,101 @@ __global__ void __launch_bounds__(kRowThreads<kVec>) mrs_norm_grad_kernel(const 
   };
 #pragma unroll
   for (int i = 0; i < kRowDepth<kVec> - 1; ++i) put();
-  float near[kVec][8], far[kVec][8];
+  // Column sums: 32 tokens' at a time in registers, those behind the items in shared memory.
+  F2 near[kVec][4];
+  float4* far = reinterpret_cast<float4*>(
+                    smem_raw + RowStream<kVec, kRowDepth<kVec>>::bytes(blockDim.x)) + tid;
 #pragma unroll
-  for (int i = 0; i < kVec; ++i)
+  for (int i = 0; i < kVec; ++i) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) near[i][k] = far[i][k] = 0.0f;
+    for (int k = 0; k < 4; ++k) near[i][k] = f2(0.0f, 0.0f);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) far[(2 * i + k) * blockDim.x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  }
+  auto add_far = [&] {
+#pragma unroll
+    for (int i = 0; i < kVec; ++i)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float4& f = far[(2 * i + k) * blockDim.x];
+        const float2 lo = f2_pair(near[i][2 * k]), hi = f2_pair(near[i][2 * k + 1]);
+        f = make_float4(f.x + lo.x, f.y + lo.y, f.z + hi.x, f.w + hi.y);
+        near[i][2 * k] = near[i][2 * k + 1] = f2(0.0f, 0.0f);
+      }
+  };
   int added = 0;
   // (a CTA's rows take the same number of turns: they meet in the reduction)
   for (int64_t first = begin; first < a.rows; first += step) {
     const int64_t row = first + in_cta;
     const bool live = row < a.rows;
     const float rstd = live ? __ldg(a.rstd + row) : 0.0f;
-    float xh[kVec][8], g[kVec][8];
-    float dot = 0.0f;
-    uint4 q[kVec];
+    F2 g[kVec][4], dot2 = f2(0.0f, 0.0f);
+    uint4 s[kVec], q[kVec];
     put();
-    stream.get(q);
+    stream.get(s);
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-      unpack8<T>(q[i], xh[i]);
+    for (int i = 0; i < kVec; ++i)
 #pragma unroll
-      for (int k = 0; k < 8; ++k) g[i][k] = 0.0f;
-    }
+      for (int k = 0; k < 4; ++k) g[i][k] = f2(0.0f, 0.0f);
     for (int j = 1; j < summed; ++j) {
       put();
       stream.get(q);
 #pragma unroll
       for (int i = 0; i < kVec; ++i) {
-        float p[8];
+        F2 p[4];
         unpack8<T>(q[i], p);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) g[i][k] += p[k];
+        for (int k = 0; k < 4; ++k) g[i][k] = g[i][k] + p[k];
       }
     }
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
       if (!live || i >= stream.count) continue;  // (what was read there is not of this row)
-      float w[8];
+      F2 w[4], xh[4];
       load_columns<T>(a.gain, a.gain_f32 != 0, i * a.tpr + place, w);
+      unpack8<T>(s[i], xh);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        xh[i][k] *= rstd;
-        near[i][k] += g[i][k] * xh[i][k];
-        g[i][k] *= w[k];
-        dot += g[i][k] * xh[i][k];
+      for (int k = 0; k < 4; ++k) {
+        xh[k] = xh[k] * f2(rstd, rstd);
+        near[i][k] = f2_fma(g[i][k], xh[k], near[i][k]);
+        g[i][k] = g[i][k] * w[k];
+        dot2 = f2_fma(g[i][k], xh[k], dot2);
       }
     }
-    const float mean = row_totals(dot, 0u, a.tpr, meet).sum * a.inv_cols;
+    const float mean = row_totals(f2_sum(dot2), 0u, a.tpr, meet).sum * a.inv_cols;
     if (a.grad_sum != nullptr) {
       put();
       stream.get(q);
     }
+    const F2 by = f2(rstd, rstd), less = f2(-mean * rstd, -mean * rstd);
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
       if (!live || i >= stream.count) continue;
-      float d[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) d[k] = 0.0f;
+      F2 d[4], x[4];
+      unpack8<T>(s[i], x);
       if (a.grad_sum != nullptr) unpack8<T>(q[i], d);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) d[k] += rstd * (g[i][k] - xh[i][k] * mean);
+      for (int k = 0; k < 4; ++k) {
+        const F2 u = f2_fma(x[k], less, g[i][k]);  // g - xh * mean
+        d[k] = a.grad_sum != nullptr ? f2_fma(u, by, d[k]) : u * by;
+      }
       *reinterpret_cast<uint4*>(static_cast<unsigned char*>(a.grad_x) + row * row_bytes +
                                 stream.off[i]) = pack8<T>(d);
     }
     if (++added == kNormSumRows) {
       added = 0;
-#pragma unroll
-      for (int i = 0; i < kVec; ++i)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          far[i][k] += near[i][k];
-          near[i][k] = 0.0f;
-        }
+      add_far();
     }
   }
   if (a.partial == nullptr) return;
+  add_far();
   float* out = a.partial + (static_cast<size_t>(blockIdx.x) * a.per_cta + in_cta) * cols;
 #pragma unroll
   for (int i = 0; i < kVec; ++i) {
-    const int at = i * a.tpr + place;
-    if (at >= a.vecs) continue;
-    float4* q = reinterpret_cast<float4*>(out + 8 * at);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) near[i][k] += far[i][k];
-    q[0] = make_float4(near[i][0], near[i][1], near[i][2], near[i][3]);
-    q[1] = make_float4(near[i][4], near[i][5], near[i][6], near[i][7]);
+    if (i >= stream.count) continue;
+    float4* p = reinterpret_cast<float4*>(out + stream.off[i] / 2);
+    p[0] = far[2 * i * blockDim.x];
+    p[1] = far[(2 * i + 1) * blockDim.x];
   }
 }
 
@@ -288,9 +304,10 @@ int norm_grad_ctas(const RowPlan& p, int sms) {
   const int per_sm = 1024 / p.threads;
   return sms * (per_sm < 1 ? 1 : per_sm);
 }
-RowPlan norm_grad_plan(int cols) { return row_plan(cols, 1, 128); }
+RowPlan norm_grad_plan(int cols) { return row_plan(cols, 2, 128); }
 
 constexpr int kNormDeepThreads = 640;  // of CTAs with twice as many items ahead
+constexpr int kNormTwoThreads = 448;   // of the gradient's CTAs that share an SM, 72 registers each
 
 template <class T, int kVec, int kDepth, bool kOne>
 cudaError_t launch_norm(const NormArgs& a, const RowPlan& p, int sms, cudaStream_t st) {
@@ -320,19 +337,23 @@ cudaError_t launch_norm(const NormArgs& a, const RowPlan& p, int sms, cudaStream
     default: return launch_norm<T, 4, kRowDepth<4>, false>(a, p, sms, st);
   }
 }
-template <class T, int kVec, bool kOne>
+template <class T, int kVec, bool kOne, int kThreads = kRowThreads<kVec>>
 cudaError_t launch_norm_grad(const NormGradArgs& a, const RowPlan& p, int ctas, cudaStream_t st) {
-  auto* k = mrs_norm_grad_kernel<T, kVec, kOne>;
-  using Stream = RowStream<kVec, kRowDepth<kVec>>;
+  auto* k = mrs_norm_grad_kernel<T, kVec, kOne, kThreads>;
+  auto bytes = [](int threads) {  // the items, and 32 bytes of sums for each vector
+    return RowStream<kVec, kRowDepth<kVec>>::bytes(threads) + static_cast<size_t>(32) * kVec * threads;
+  };
   static SmemGrant granted;
   const cudaError_t err =
-      grant_smem(reinterpret_cast<const void*>(k), Stream::bytes(kRowThreads<kVec>), granted);
+      grant_smem(reinterpret_cast<const void*>(k), bytes(kThreads), granted);
   if (err != cudaSuccess) return err;
-  return launch_pdl(k, dim3(ctas), dim3(p.threads), Stream::bytes(p.threads), st, a);
+  return launch_pdl(k, dim3(ctas), dim3(p.threads), bytes(p.threads), st, a);
 }
 template <class T>
 cudaError_t launch_norm_grad(const NormGradArgs& a, const RowPlan& p, int ctas, cudaStream_t st) {
   const bool one = p.rows == 1;
+  if (p.vec == 2 && one && p.threads <= kNormTwoThreads)
+    return launch_norm_grad<T, 2, true, kNormTwoThreads>(a, p, ctas, st);
   switch (p.vec) {
     case 1: return one ? launch_norm_grad<T, 1, true>(a, p, ctas, st)
                        : launch_norm_grad<T, 1, false>(a, p, ctas, st);
@@ -390,7 +411,11 @@ int moe_rms_norm(const void* x, int dtype, int64_t x_stride, int parts, const vo
                       span(gain, c * (gain_dtype == MOE_RS_FP32 ? 4 : 2)),
                       rows_span(in_place ? nullptr : residual, rows, cols, residual_stride, 2)};
   if (any_alias(outs, 5, ins, 3)) return MOE_RS_ERR_ALIAS;
-  const RowPlan p = row_plan(cols, 1);
+  const int sms = sm_count();
+  if (sms == 0) return launch_status(cudaErrorInvalidDevice);
+  // Two vectors a thread halve the instructions of an item (8192 x 3584: 60 us with one, 52 with two);
+  // few rows are spread over more threads (one token of 16 rows 8.9 and 10.9).
+  const RowPlan p = row_plan(cols, rows <= sms ? 1 : 2);
   NormArgs a{};
   a.x = x;
   a.residual = residual;
@@ -410,8 +435,6 @@ int moe_rms_norm(const void* x, int dtype, int64_t x_stride, int parts, const vo
   a.codes = codes;
   a.scales = scales;
   a.rstd = rstd;
-  const int sms = sm_count();
-  if (sms == 0) return launch_status(cudaErrorInvalidDevice);
   return launch_status(dtype == MOE_RS_BF16 ? launch_norm<__nv_bfloat16>(a, p, sms, stream)
                                             : launch_norm<__half>(a, p, sms, stream));
 }

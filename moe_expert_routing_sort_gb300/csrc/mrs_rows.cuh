@@ -71,6 +71,71 @@ __device__ __forceinline__ void load_columns(const void* p, bool f32, int i, flo
   }
 }
 
+// Two fp32 values side by side, one instruction for both.
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 f2_pair(F2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+  return r;
+}
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ float f2_sum(F2 a) {
+  const float2 p = f2_pair(a);
+  return p.x + p.y;
+}
+template <class T>
+__device__ __forceinline__ void unpack8(const uint4& q, F2 (&v)[4]) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+      v[i] = f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    } else {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      v[i] = f2(f.x, f.y);
+    }
+  }
+}
+template <class T>
+__device__ __forceinline__ uint4 pack8(const F2 (&v)[4]) {
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = f2_pair(v[i]);
+    f[2 * i] = p.x;
+    f[2 * i + 1] = p.y;
+  }
+  return pack8<T>(f);
+}
+template <class T>
+__device__ __forceinline__ void load_columns(const void* p, bool f32, int i, F2 (&v)[4]) {
+  float f[8];
+  load_columns<T>(p, f32, i, f);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] = f2(f[2 * k], f[2 * k + 1]);
+}
+
 // --------------------------------------------------------------------------- 8-bit rows
 // A row's scale is its largest magnitude / 448 (the largest e4m3 value), at least 2^-126 so that
 // its reciprocal is finite; a row that holds an infinity or a NaN takes a NaN for its scale and
@@ -95,6 +160,16 @@ __device__ __forceinline__ uint2 fp8_codes(const float (&v)[8], float inv) {
 // A row's codes where its scale is a number, zeros otherwise.
 __device__ __forceinline__ uint2 fp8_codes_of(const float (&v)[8], float scale) {
   return scale == scale ? fp8_codes(v, 1.0f / scale) : make_uint2(0u, 0u);
+}
+__device__ __forceinline__ uint2 fp8_codes_of(const F2 (&v)[4], float scale) {
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = f2_pair(v[i]);
+    f[2 * i] = p.x;
+    f[2 * i + 1] = p.y;
+  }
+  return fp8_codes_of(f, scale);
 }
 // The larger magnitude, a NaN where one is.
 __device__ __forceinline__ float larger(float top, float v) {
@@ -183,7 +258,7 @@ struct RowStream {
     from += slot_bytes;
     if (from == kDepth * slot_bytes) from = 0;
   }
-  static size_t bytes(int threads) { return static_cast<size_t>(16) * kVec * kDepth * threads; }
+  static __host__ __device__ size_t bytes(int threads) { return static_cast<size_t>(16) * kVec * kDepth * threads; }
 };
 // Items ahead: 128 bytes a thread, 256 where a CTA has an SM to itself.
 template <int kVec>
