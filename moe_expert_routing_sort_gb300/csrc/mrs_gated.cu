@@ -36,45 +36,72 @@ __device__ __forceinline__ void sigmoids(float a, float& up, float& down) {
   down = a >= 0.0f ? small : big;
 }
 
+// What a thread takes of a row, on its way while the row before is computed.
+template <int kVec>
+struct GatedRow {
+  uint4 a[kVec], b[kVec];
+  float w;
+};
+
 template <class T, int kVec>
 __global__ void __launch_bounds__(kRowThreads<kVec>) mrs_gated_kernel(const GatedArgs a) {
   __shared__ RowTotals meet[32];
   pdl_trigger();
   const int tid = threadIdx.x, in_cta = tid / a.tpr, place = tid - in_cta * a.tpr;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * a.per_cta + in_cta;
-  const bool live = row < a.rows;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * a.per_cta;
   const size_t cols = 8 * static_cast<size_t>(a.vecs);
-  pdl_wait();
-  const float w = live && a.weights != nullptr ? __ldg(a.weights + row) : 1.0f;
-  const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
-  float v[kVec][8];
-  float top = 0.0f;
+  auto load = [&](int64_t row, GatedRow<kVec>& r) {
+    if (row >= a.rows) return;
+    r.w = a.weights != nullptr ? __ldg(a.weights + row) : 1.0f;
+    const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
 #pragma unroll
-  for (int i = 0; i < kVec; ++i) {
-    const int at = i * a.tpr + place;
-    if (!live || at >= a.vecs) continue;
-    float b[8];
-    unpack8<T>(load8<T>(x, 8 * static_cast<size_t>(at)), v[i]);
-    unpack8<T>(load8<T>(x, cols + 8 * at), b);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      float up, down;
-      sigmoids(v[i][k], up, down);
-      v[i][k] = w * (v[i][k] * up * b[k]);
-      top = larger(top, v[i][k]);
+    for (int i = 0; i < kVec; ++i) {
+      const int at = i * a.tpr + place;
+      if (at >= a.vecs) continue;
+      r.a[i] = load8<T>(x, 8 * static_cast<size_t>(at));
+      r.b[i] = load8<T>(x, cols + 8 * at);
     }
-    if (a.y != nullptr)
-      *reinterpret_cast<uint4*>(static_cast<T*>(a.y) + row * cols + 8 * at) = pack8<T>(v[i]);
-  }
-  if (a.codes == nullptr) return;
-  const float scale = fp8_scale(row_totals(0.0f, __float_as_uint(top), a.tpr, meet).top);
-  if (!live) return;
-  if (place == 0) a.scales[row] = scale;
+  };
+  pdl_wait();
+  int64_t row = static_cast<int64_t>(blockIdx.x) * a.per_cta + in_cta;
+  GatedRow<kVec> now, next;
+  load(row, now);
+  // (the rows of a CTA take the same number of turns: they meet in the reduction)
+  for (; row - in_cta < a.rows; row += step, now = next) {
+    const bool live = row < a.rows;
+    load(row + step, next);
+    float v[kVec][8];
+    float top = 0.0f;
 #pragma unroll
-  for (int i = 0; i < kVec; ++i) {
-    const int at = i * a.tpr + place;
-    if (at < a.vecs)
-      *reinterpret_cast<uint2*>(a.codes + row * cols + 8 * at) = fp8_codes_of(v[i], scale);
+    for (int i = 0; i < kVec; ++i) {
+      const int at = i * a.tpr + place;
+      if (!live || at >= a.vecs) continue;
+      float b[8];
+      unpack8<T>(now.a[i], v[i]);
+      unpack8<T>(now.b[i], b);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        float up, down;
+        sigmoids(v[i][k], up, down);
+        v[i][k] = now.w * (v[i][k] * up * b[k]);
+      }
+      if (a.y != nullptr)
+        *reinterpret_cast<uint4*>(static_cast<T*>(a.y) + row * cols + 8 * at) = pack8<T>(v[i]);
+      if (a.codes != nullptr) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) top = larger(top, v[i][k]);
+      }
+    }
+    if (a.codes == nullptr) continue;
+    const float scale = fp8_scale(row_totals(0.0f, __float_as_uint(top), a.tpr, meet).top);
+    if (!live) continue;
+    if (place == 0) a.scales[row] = scale;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      const int at = i * a.tpr + place;
+      if (at < a.vecs)
+        *reinterpret_cast<uint2*>(a.codes + row * cols + 8 * at) = fp8_codes_of(v[i], scale);
+    }
   }
 }
 
@@ -165,14 +192,26 @@ auto* gated_kernel() {
   else return mrs_fp8_quantize_kernel<T, kVec>;
 }
 
+template <class T, int kVec, GatedKind kKind>
+cudaError_t launch_gated(const GatedArgs& a, const RowPlan& p, int sms, cudaStream_t st) {
+  auto* k = gated_kernel<T, kVec, kKind>();
+  const int64_t most = (a.rows + p.rows - 1) / p.rows;
+  // The activation's CTAs go round (131072 x 384: 46 us, and 54 with a CTA for every 16 rows); the
+  // gradient's do not (65536 x 2048: 196 us, and 224 so: its next row takes registers that its CTAs
+  // have no room for).
+  const int64_t full = kKind == GatedKind::kForward ? row_ctas(p.threads, 0, sms) : most;
+  return launch_pdl(k, dim3(static_cast<unsigned>(most < full ? most : full)), dim3(p.threads), 0, st,
+                    a);
+}
 template <class T, GatedKind kKind>
 cudaError_t launch_gated(const GatedArgs& a, const RowPlan& p, cudaStream_t st) {
-  const dim3 grid(static_cast<unsigned>((a.rows + p.rows - 1) / p.rows)), block(p.threads);
+  const int sms = sm_count();
+  if (sms == 0) return cudaErrorInvalidDevice;
   switch (p.vec) {
-    case 1: return launch_pdl(gated_kernel<T, 1, kKind>(), grid, block, 0, st, a);
-    case 2: return launch_pdl(gated_kernel<T, 2, kKind>(), grid, block, 0, st, a);
-    case 3: return launch_pdl(gated_kernel<T, 3, kKind>(), grid, block, 0, st, a);
-    default: return launch_pdl(gated_kernel<T, 4, kKind>(), grid, block, 0, st, a);
+    case 1: return launch_gated<T, 1, kKind>(a, p, sms, st);
+    case 2: return launch_gated<T, 2, kKind>(a, p, sms, st);
+    case 3: return launch_gated<T, 3, kKind>(a, p, sms, st);
+    default: return launch_gated<T, 4, kKind>(a, p, sms, st);
   }
 }
 
