@@ -27,6 +27,7 @@
 #include <cuda_fp16.h>
 
 #include "mrs_product.cuh"
+#include "mrs_rows.cuh"
 
 namespace mrs {
 
@@ -523,16 +524,26 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     uint32_t acc_phase = 0;
     while (const ProductInfo<R>* q = next_unit()) {
       const int n = q->n, e = q->e;
-      for (int c = 0; c < H * q->tiles; ++c) {
-        // the warp's 32 m; a lane has those of its accumulator lanes
+      const int count = H * q->tiles;
+      // the outputs' scales, a tile ahead: of the lane's accumulator lanes among the warp's 32 m
+      constexpr int kScales = sizeof(Out) == 4 ? 1 : 4;
+      float ahead[kScales];
+      auto load_scales = [&](int c) {
         const int m32 = q->m0 + c * kPairRows + 128 * rank + 32 * quarter;
-        float scale[sizeof(Out) == 4 ? 1 : 4];
 #pragma unroll
-        for (int i = 0; i < static_cast<int>(sizeof(scale) / 4); ++i) {
+        for (int i = 0; i < kScales; ++i) {
           const int m = m32 + (sizeof(Out) == 4 ? lane : 8 * i + (lane >> 2));
-          scale[i] = a.ws != nullptr && m < a.M ? __ldg(a.ws + static_cast<size_t>(e) * a.M + m)
-                                                : 1.0f;
+          ahead[i] = a.ws != nullptr && c < count && m < a.M
+                         ? __ldg(a.ws + static_cast<size_t>(e) * a.M + m) : 1.0f;
         }
+      };
+      load_scales(0);
+      for (int c = 0; c < count; ++c) {
+        const int m32 = q->m0 + c * kPairRows + 128 * rank + 32 * quarter;
+        float scale[kScales];
+#pragma unroll
+        for (int i = 0; i < kScales; ++i) scale[i] = ahead[i];
+        load_scales(c + 1);
         ok = warp_wait(&acc_full_s[buf], acc_phase, limit);
         if (!ok) break;
         tc_fence_after();
@@ -571,12 +582,15 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             for (int k = 0; k < 4; ++k) {
               const float2 f =
                   *reinterpret_cast<const float2*>(&q->factor[j0 + 8 * k + 2 * (lane & 3)]);
+              const F2 by = f2(f.x, f.y);
               uint32_t w[4];
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const uint32_t* p = v + 16 * (i >> 1) + 4 * k + 2 * (i & 1);
-                w[i] = rounded2(__uint_as_float(p[0]) * (scale[i] * f.x),
-                                __uint_as_float(p[1]) * (scale[i] * f.y), a.out_type);
+                const F2 y = f2(__uint_as_float(p[0]), __uint_as_float(p[1])) *
+                             (f2(scale[i], scale[i]) * by);
+                const float2 r = f2_pair(y);
+                w[i] = rounded2(r.x, r.y, a.out_type);
               }
               const int row = 8 * k + (lane & 7);
               store_transposed(stage + 64 * row + 16 * ((lane >> 3) ^ ((row >> 1) & 3)), w[0], w[1],
@@ -598,10 +612,12 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             }
           }
         };
+        // (of an odd number of 32 rows the two warps of a quarter have the one more in turn)
+        const int begin = 32 * (half ^ buf);
         uint32_t one[32], two[32];
-        if (32 * half < n && m32 < a.M) load(32 * half, one);
+        if (begin < n && m32 < a.M) load(begin, one);
         if (m32 < a.M) {
-          for (int j0 = 32 * half; j0 < n; j0 += 128) {
+          for (int j0 = begin; j0 < n; j0 += 128) {
             store(j0, one, two);
             if (j0 + 64 < n) store(j0 + 64, two, one);
           }
