@@ -14,7 +14,8 @@ from .binding import _check, load
 # type codes of include/moe_route_sort.h
 DTYPE_CODE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
-_current_device = torch.cuda.current_device
+# (the call behind torch.cuda.current_device, which a tensor of a call has initialised CUDA for)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 # (a torch without CUDA has none, nor tensors for a call that wants it)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
@@ -116,7 +117,8 @@ class Entry:
         fn = self.fn
         if fn is None:
             fn = self.fn = load().moe_call_packed
-        packed = self.pack(self.op, self.count, *args, stream_handle(device, stream))
+        packed = self.pack(self.op, self.count, *args,
+                           _raw_stream(device) if stream is None else stream_handle(device, stream))
         if _current_device() == device:
             rc = fn(packed)
         else:

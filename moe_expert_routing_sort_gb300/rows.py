@@ -144,21 +144,25 @@ class NormBuffers:
 
 def _norm_inputs(x, weight, residual, parts):
     """(device, T, cols, arguments up to the weight's type) of a norm's call."""
-    dev = cuda_device(x, "x")
-    code = _half(x, "x")
+    dev, dtype = x.get_device(), x.dtype
+    code = _HALF.get(dtype)
+    if dev < 0 or code is None:
+        cuda_device(x, "x")
+        _half(x, "x")
     rows, cols, stride = rows_of(x, "x")
     if parts < 1 or rows % parts:
         raise ValueError(f"x has {rows} rows, no multiple of {parts} parts a token")
     T, pr, sr = rows // parts, 0, cols
     if residual is not None:
-        if residual.shape != (T, cols) or residual.dtype is not x.dtype:
-            raise ValueError(f"residual must be {x.dtype} [{T}, {cols}], got {residual.dtype} "
+        if residual.dtype is not dtype or residual.shape != (T, cols):
+            raise ValueError(f"residual must be {dtype} [{T}, {cols}], got {residual.dtype} "
                              f"{tuple(residual.shape)}")
         if residual.get_device() != dev:
             raise ValueError(f"residual is on {residual.device}, other buffers on cuda:{dev}")
-        _, _, sr = rows_of(residual, "residual")
         pr = residual.data_ptr()
-    pw, kind = _gain(weight, x.dtype, cols, dev)
+        if not residual.is_contiguous():
+            _, _, sr = rows_of(residual, "residual")
+    pw, kind = _gain(weight, dtype, cols, dev)
     return dev, T, cols, (x.data_ptr(), code, stride, parts, pr, sr, T, cols, pw, kind)
 
 
