@@ -807,6 +807,8 @@ int product(const void* x, int type, const float* x_scales, int per_route, const
     return launch_status(launch_product_few(map, f, type, sms, stream));
   }
   const size_t hit = routes < static_cast<size_t>(E) ? routes : E;
+  // us in tiles of 64 rows and of 256: E = 64, 3584 -> 768 in bf16, 32, 64 and 96 rows an expert 83 87,
+  // 87 88, 101 89; in 8 bits 50 54, 52 55, 60 56; E = 16, 7168 -> 2048 in bf16 99 103, 113 105, 130 105
   const int R = routes <= 48 * hit ? 64 : 256;
   ListArgs list{};
   list.eid = eid;
@@ -839,14 +841,21 @@ int product(const void* x, int type, const float* x_scales, int per_route, const
   a.K = K;
   a.P = static_cast<int>(P);
   a.ksteps = (K * static_cast<int>(size) + 127) / 128;
-  const int H = R > 64 && a.ksteps >= 16 && M > kPairRows ? 2 : 1;
+  // 512 m on the same rows take in a quarter less for the same products, and leave no second
+  // accumulator for the next tile; half as many units fill the pairs less evenly.  us with 256 and with
+  // 512, bf16: T = 8192, E = 64, topk = 8, 7168 -> 2048 1250 1213; E = 16, 7168 -> 2048, 256, 384 and
+  // 768 rows an expert 130 160, 156 148, 230 229; E = 64, 3584 -> 768, 96 and 256 rows 89 92, 105 132.
+  const int pairs = sms / 2;
+  const double row_tiles = static_cast<double>(routes) / R + 0.5 * static_cast<double>(hit);
+  auto rounds = [&](int h) {
+    return row_tiles * ((M + h * kPairRows - 1) / (h * kPairRows)) / pairs + 0.5;
+  };
+  const int H = R > 64 && a.ksteps >= 16 && 2 * 0.95 * rounds(2) < rounds(1) ? 2 : 1;
   a.mtiles = (M + H * kPairRows - 1) / (H * kPairRows);
   a.type = type == MOE_RS_BF16 ? 1 : 0;
   a.out_type = out_type;
-  const int pairs = sms / 2;
   // A unit is as many output tiles of one row tile as leave 32 rounds of units.
-  const size_t row_tiles = routes / R + hit;
-  const size_t each = row_tiles * a.mtiles / (32 * static_cast<size_t>(pairs));
+  const size_t each = (routes / R + hit) * a.mtiles / (32 * static_cast<size_t>(pairs));
   a.chunk = each < 1 ? 1 : (each > static_cast<size_t>(a.mtiles) ? a.mtiles : static_cast<int>(each));
   a.nchunk = (a.mtiles + a.chunk - 1) / a.chunk;
   a.chunk = (a.mtiles + a.nchunk - 1) / a.nchunk;

@@ -32,6 +32,10 @@ PATHS = [
     (129, 1, 1, 80, 40, 16),
     (128, 1, 1, 80, 40, 1024),
     (9, 2, 2, 4160, 40, 64),
+    (4096, 8, 2, 2064, 5128, 64),    # 512 outputs on the same rows
+    (4096, 8, 2, 5136, 1032, 64),    # and 512 columns of the rows' gradient
+    (4000, 1100, 16, 64, 3592, 16),  # several output tiles a unit, wide and narrow row tiles
+    (3000, 2000, 2, 72, 1544, 16),
 ]
 
 
