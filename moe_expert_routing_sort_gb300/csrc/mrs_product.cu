@@ -572,7 +572,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
               for (int i = 0; i < 4; ++i)
                 if (to[i] >= 0 && m < a.M)
                   static_cast<float*>(a.out)[static_cast<size_t>(to[i]) * a.M + m] =
-                      __uint_as_float(v[j + i]) * (scale[0] * by[i]);
+                      __uint_as_float(v[j + i]) * scale[0] * by[i];
             }
           } else {
             // through shared memory, so that four lanes store 64 bytes of a row side by side: 32
@@ -587,8 +587,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const uint32_t* p = v + 16 * (i >> 1) + 4 * k + 2 * (i & 1);
+                // (one scale after the other: their product may leave fp32 where the result does not)
                 const F2 y = f2(__uint_as_float(p[0]), __uint_as_float(p[1])) *
-                             (f2(scale[i], scale[i]) * by);
+                             f2(scale[i], scale[i]) * by;
                 const float2 r = f2_pair(y);
                 w[i] = rounded2(r.x, r.y, a.out_type);
               }

@@ -199,11 +199,13 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       // what this thread will store: output `lane` of the unit's route `warp`
       const bool stores = warp < rows && n < a.N;
       const int route = q->route[warp < rows ? warp : 0];
-      float by = 1.0f;
+      float by = 1.0f, scale = 1.0f;
       if (stores) {
         if (a.sw != nullptr) by = __ldg(a.sw + q->place[warp]);
-        if (a.xs != nullptr)
-          by *= __ldg(a.xs + row_of(route)) * __ldg(a.ws + static_cast<size_t>(e) * a.N + n);
+        if (a.xs != nullptr) {
+          by *= __ldg(a.xs + row_of(route));
+          scale = __ldg(a.ws + static_cast<size_t>(e) * a.N + n);
+        }
       }
       const bool some = g < rows;  // a column of X that there is
       constexpr int kLoads = kFewPart / 64;  // of a lane and row in a step
@@ -268,7 +270,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         float sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < kFewWarps / 2; ++i) sum += sums[unit & 1][i][warp][lane];
-        store_rounded(a.out, static_cast<size_t>(route) * a.N + n, sum * by, a.out_type);
+        store_rounded(a.out, static_cast<size_t>(route) * a.N + n, sum * scale * by, a.out_type);
       }
       ++unit;
     }
