@@ -62,6 +62,10 @@ __global__ void __launch_bounds__(kRowThreads<kVec>) mrs_norm_kernel(const NormA
   };
 #pragma unroll
   for (int i = 0; i < kDepth - 1; ++i) put();
+  F2 gain[kVec][4];  // every row's
+#pragma unroll
+  for (int i = 0; i < kVec; ++i)
+    if (i < stream.count) load_columns<T>(a.gain, a.gain_f32 != 0, i * a.tpr + place, gain[i]);
   // (the rows of a CTA take the same number of turns: they meet in the reduction)
   for (int64_t row = first; row - in_cta < a.rows; row += step) {
     const bool live = row < a.rows;
@@ -92,12 +96,10 @@ __global__ void __launch_bounds__(kRowThreads<kVec>) mrs_norm_kernel(const NormA
       unpack8<T>(s, v[i]);
       if (a.sum != nullptr)
         *reinterpret_cast<uint4*>(static_cast<unsigned char*>(a.sum) + here + stream.off[i]) = s;
-      F2 g[4];
-      load_columns<T>(a.gain, a.gain_f32 != 0, i * a.tpr + place, g);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         squares = f2_fma(v[i][k], v[i][k], squares);
-        v[i][k] = v[i][k] * g[k];
+        v[i][k] = v[i][k] * gain[i][k];
       }
       if (a.codes != nullptr) {
 #pragma unroll

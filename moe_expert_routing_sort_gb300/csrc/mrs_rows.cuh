@@ -162,14 +162,16 @@ __device__ __forceinline__ uint2 fp8_codes_of(const float (&v)[8], float scale) 
   return scale == scale ? fp8_codes(v, 1.0f / scale) : make_uint2(0u, 0u);
 }
 __device__ __forceinline__ uint2 fp8_codes_of(const F2 (&v)[4], float scale) {
-  float f[8];
+  if (scale != scale) return make_uint2(0u, 0u);
+  const float inv = 1.0f / scale;
+  uint16_t h[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 p = f2_pair(v[i]);
-    f[2 * i] = p.x;
-    f[2 * i + 1] = p.y;
+    const float2 p = f2_pair(v[i] * f2(inv, inv));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h[i]) : "f"(p.y), "f"(p.x));
   }
-  return fp8_codes_of(f, scale);
+  return make_uint2(h[0] | (static_cast<uint32_t>(h[1]) << 16),
+                    h[2] | (static_cast<uint32_t>(h[3]) << 16));
 }
 // The larger magnitude, a NaN where one is.
 __device__ __forceinline__ float larger(float top, float v) {
