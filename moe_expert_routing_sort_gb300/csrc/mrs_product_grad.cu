@@ -9,7 +9,13 @@
 //
 // A pair of CTAs computes tiles of 256 m by 256 k of one expert, 64 rows a step; each CTA brings
 // 128 m and 128 k.  The tasks of the warps are those of mrs_product.cu.  Experts without routes get
-// their zeros from the storing warps alone.
+// their zeros from the storing warps alone.  Two sets of eight warps copy the steps in turn, so that
+// one set's look at the list is hidden behind the other's copies; tiles leave by tensor copies.
+//
+// T = 8192, E = 64, topk = 8, 2048 x 7168: 1580 to 1700 us, of 996 at the tensor cores' rate.  Bound
+// by the copies: both operands are rows somewhere in memory, a thread's copy takes 16 bytes, and an SM
+// takes in 512 bytes of such copies every 16 clocks, 64 KB a step in 1024 clocks more or less where
+// its products need 512.  E = 129, T = 1000: the latency of the two or three units that a pair has.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -36,6 +42,9 @@ constexpr int kGradSlots = 6;
 constexpr int kGradInfo = 4;
 constexpr int kGradUsers = 9 + kGradTurns * kGradCopiers;  // eight storing warps, copies, their announcer
 constexpr int kGradDeep = 64;            // rows of a step
+// Steps from which a tile's sums are made in two accumulators, half of the rows each: the tensor core
+// cuts where an addition would round, and sums come out low by 1.2e-9 of themselves for every row.
+constexpr int kGradLong = 64;
 constexpr int kGradTile = 128 * 128;     // bytes of an operand in a CTA and step
 constexpr int kGradStage = 32 * 128;     // of a storing warp: 128 bytes of 32 rows
 constexpr size_t kGradSmem =
@@ -244,9 +253,16 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         any = true;
         if (elect_one()) {
           Ring<S> s = at;
+          int into = buf;
+          const int second = steps > kGradLong ? steps / 2 : steps;  // its first step
           ok = pair_wait(&acc_free_s[buf], acc_phase ^ 1u, limit);
-          tc_fence_after();
           for (int ks = 0; ok && ks < steps; ++ks) {
+            if (ks == second) {
+              pair_commit(&acc_full_s[into]);
+              into ^= 1;
+              ok = pair_wait(&acc_free_s[into], acc_phase ^ (buf == 0 ? 1u : 0u), limit);
+              if (!ok) break;
+            }
             ok = pair_wait(&full_s[s.slot], s.phase, limit);
             if (!ok) break;
             tc_fence_after();
@@ -256,16 +272,18 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 #pragma unroll
             for (int g = 0; g < 4; ++g)
               if (g < parts)  // else rows past the last: zeros
-                pair_mma<false>(tmem + buf * 256, dg + 128 * g, dx + 128 * g, word,
-                                ks > 0 || g > 0);
+                pair_mma<false>(tmem + into * 256, dg + 128 * g, dx + 128 * g, word,
+                                (ks > 0 && ks != second) || g > 0);
             pair_commit(&free_s[s.slot]);
             s.advance();
           }
-          if (ok) pair_commit(&acc_full_s[buf]);
+          if (ok) pair_commit(&acc_full_s[into]);
         }
         ok = __all_sync(kFull, ok);
         at.skip(steps);
-        if (++buf == 2) {
+        if (steps > kGradLong) {  // both, and back to this one
+          acc_phase ^= 1u;
+        } else if (++buf == 2) {
           buf = 0;
           acc_phase ^= 1u;
         }
@@ -285,13 +303,17 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     uint32_t acc_phase = 0;
     while (const GradInfo* q = next_unit()) {
       const int m = q->m0 + 128 * rank + 32 * quarter, k0 = q->k0, e = q->e;
-      const bool some = q->rows > 0;
+      const bool some = q->rows > 0, both = q->rows > kGradLong * kGradDeep;
       if (some) {
         ok = warp_wait(&acc_full_s[buf], acc_phase, limit);
         if (!ok) break;
+        if (both) {
+          ok = warp_wait(&acc_full_s[buf ^ 1], acc_phase ^ (buf == 0 ? 0u : 1u), limit);
+          if (!ok) break;
+        }
         tc_fence_after();
       }
-      const uint32_t src = tmem + buf * 256 + lanes;
+      const uint32_t src = tmem + buf * 256 + lanes, src2 = tmem + (buf ^ 1) * 256 + lanes;
       // Tiles of 32 rows by 128 bytes go through shared memory, in the swizzle of the tensor copy that
       // stores them.  (Lanes that store 32 bytes of a row each take 32 lines an access, beside the
       // copies that wait for the same unit.)
@@ -307,6 +329,10 @@ __global__ void __launch_bounds__(kGradThreads, 1)
           if (some) {
             tmem_load32(src + c0 + 32 * part, v);
             tmem_wait(v);
+            if (both) {
+#pragma unroll
+              for (int c = 0; c < 32; c += 8) tmem_add8(src2 + c0 + 32 * part + c, v + c);
+            }
           } else {
 #pragma unroll
             for (int c = 0; c < 32; ++c) v[c] = 0u;
@@ -344,7 +370,10 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) pair_arrive_first(&acc_free_s[buf]);
-        if (++buf == 2) {
+        if (both) {
+          if (lane == 0) pair_arrive_first(&acc_free_s[buf ^ 1]);
+          acc_phase ^= 1u;
+        } else if (++buf == 2) {
           buf = 0;
           acc_phase ^= 1u;
         }

@@ -49,6 +49,21 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&r)[32]) {
   for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
 }
 
+// Eight columns of the lane, added as fp32.
+__device__ __forceinline__ void tmem_add8(uint32_t addr, uint32_t* v) {
+  uint32_t r[8];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7])
+      : "r"(addr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(r[i]));
+}
+
 // 16 lanes x 32 columns of 32 bits in fragments: of eight columns (8 k on) a thread t of the warp has
 // columns 2 (t % 4) and the next, of lane t / 4 in r[4 k], r[4 k + 1] and of lane t / 4 + 8 in
 // r[4 k + 2], r[4 k + 3].

@@ -412,6 +412,42 @@ def test_rows_and_outputs_past_32_bit_offsets():
           grad[last].double().abs() @ w[0].double().abs(), 72)
 
 
+def test_gradient_of_weights_over_thousands_of_rows():
+    """Experts of 1000, 5000, 4097, 0 and 4096 rows, each with several tiles for a pair of CTAs."""
+    g = _gen("long")
+    counts, cols, outs = (1000, 5000, 4097, 0, 4096), 2056, 1288
+    T = sum(counts)
+    r = Routes(g, T, len(counts), 1, 16)
+    owner = torch.cat([torch.full((n,), e, device=DEV) for e, n in enumerate(counts)])
+    r.ids = owner[torch.randperm(T, generator=g, device=DEV)].int().view(T, 1)
+    ws = torch.zeros(mrs.moe_route_sort_workspace_bytes(T, r.E, 1, 16), dtype=torch.uint8,
+                     device=DEV)
+    mrs.moe_sort(r.ids, r.weights, r.E, 16, r.sid, r.sw, r.eid, r.npp, ws)
+    x, grad = _rows(g, T, cols, FH), _rows(g, T, outs, FH)
+    owner = r.owners()
+    for kind in (F32, FH):
+        dw = mrs.experts_grad_weights(grad, x, len(counts), *r.lists, dtype=kind)
+        for e, n in enumerate(counts):
+            at = (owner == e).nonzero()[:, 0]
+            assert at.numel() == n
+            gd, xd = grad[at].double(), x[at].double()
+            _near(dw[e], gd.T @ xd, gd.T.abs() @ xd.abs(), max(n, 1))
+
+
+def test_long_sums_stay_near_fp32():
+    """An addition to an accumulator takes 16 products and cuts what is below its last bit, half of
+    that bit on average: at most 2^-24 of the sum so far.  The sums on the way to a sum of n random
+    terms have n / 2 in common with it on average, so that it is low by n / 16 / 2 * 2^-24 at most.
+    Two accumulators have half of the rows each."""
+    n = 8192
+    g = _gen("low")
+    r = Routes(g, n, 1, 1, 16)
+    x, grad = _rows(g, n, 256, FH), _rows(g, n, 256, FH)
+    want = grad.double().T @ x.double()
+    dw = mrs.experts_grad_weights(grad, x, 1, *r.lists, dtype=F32)
+    assert ((dw[0].double() - want).norm() / want.norm()).item() <= n / 2 / 16 / 2 * 2**-24
+
+
 def test_weights_past_32_bit_offsets():
     g = _gen("heavy")
     E, outs, cols = 68, 512, 65536  # 2.3e9 elements
