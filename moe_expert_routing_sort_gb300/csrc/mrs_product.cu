@@ -23,6 +23,17 @@
 //   12-15  copies of a step's rows; 3 says when those that threads write are there
 // Every wait is bounded; one that gives up ends its warp's task with the status bit set.  The CTAs
 // of a pair leave together.
+//
+// The sums are the tensor core's: it keeps fp32 and cuts where an addition would round, so that they
+// come out low, by 1.0e-6 of their size over 1024 columns, 4.4e-6 over 4096 and 1.9e-5 over 16384.
+//
+// Bound by the weights' bytes where an expert has few rows (T = 512, E = 896, 3584 -> 768, 16 bits:
+// 721 us, the floor of 729 at the rate of a copy) and by the tensor cores where it has many: T = 8192,
+// E = 64, topk = 8, 7168 -> 2048 in 1200 to 1315 us, 73 % of the tensor cores' clocks; a library
+// product of the same size in one piece takes 996 at the rate of a short run and 1116 at that of a
+// long one, where power holds the clock.  Short contractions (8192 skewed tokens, E = 896,
+// 384 -> 3584 in 8 bits, 434 us of 329) wait for the warps that store: three steps of products are
+// 130 KB of output.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -16,7 +16,9 @@
 // every weight to fp32 first: 467 us for 512 routes in 8 bits, 3584 -> 768, E = 896, and 232 so.)
 // The four warps' sums of an output meet in shared memory and are added in a fixed order.
 //
-// Bound by the weights' bytes and, before them, by an access to the list.
+// Bound by the weights' bytes and, before them, by an access to the list: one token in 8 bits, E = 896,
+// topk = 16, 3584 -> 768, 44 MB in 13.7 us (11.1 in a graph, 6.5 at the rate of a copy).  These
+// products keep their sums to 1.3e-7.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
