@@ -50,16 +50,21 @@ __device__ __forceinline__ int cut_list(const ListArgs& a, int* start, int* used
                                         int32_t* status, Put&& put) {
   constexpr int kWarps = kThreads / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // (the first owners are on their way together with the list's length)
+  const bool holds = tid < a.max_rows >> a.log2B;
+  const int owner = holds ? __ldg(a.eid + tid) : 0, previous = holds && tid > 0 ? __ldg(a.eid + tid - 1) : -1;
   const int blocks = min(max(__ldg(a.npp), 0), a.max_rows) >> a.log2B;
   for (int e = tid; e <= a.E; e += kThreads) start[e] = blocks;
   __syncthreads();
   bool bad = false;
-#pragma unroll 4
-  for (int b = tid; b < blocks; b += kThreads) {
-    const int e = __ldg(a.eid + b), before = b > 0 ? __ldg(a.eid + b - 1) : -1;
+  auto look = [&](int b, int e, int before) {
     if (e < 0 || e >= a.E || e < before) bad = true;
     else if (e != before) start[e] = b;
-  }
+  };
+  if (tid < blocks) look(tid, owner, previous);
+#pragma unroll 4
+  for (int b = tid + kThreads; b < blocks; b += kThreads)
+    look(b, __ldg(a.eid + b), __ldg(a.eid + b - 1));
   if (__syncthreads_or(bad) && tid == 0) atomicOr(status, MOE_RS_DEVICE_BAD_EXPERT_ID);
   // an expert without a run starts where the next one does: the least start from it on (which is
   // in order whatever the list holds)
@@ -93,14 +98,15 @@ __device__ __forceinline__ int cut_list(const ListArgs& a, int* start, int* used
   }
   __syncthreads();
   auto tile_rows = [&](int e) {
-    const int64_t rows = used[e], n = (rows + a.rows - 1) / a.rows;
-    if (!a.by_used || n == 0) return a.rows;
-    return min(static_cast<int>((rows + n - 1) / n + 31) & ~31, a.rows);
+    // (rows and a.rows, in 32 bits without a sign, stay below 2^32)
+    const unsigned rows = used[e], most = a.rows, n = (rows + most - 1) >> a.log2R;
+    if (!a.by_used || n <= 1) return n == 0 || !a.by_used ? most : min((rows + 31) & ~31u, most);
+    return min(((rows + n - 1) / n + 31) & ~31u, most);
   };
   int count = 0;
   for (int e = e0; e < e1; ++e) {
-    const int64_t t = tile_rows(e);
-    count += static_cast<int>((used[e] + t - 1) / t);
+    const unsigned rows = used[e], t = tile_rows(e);
+    count += t == static_cast<unsigned>(a.rows) ? (rows + t - 1) >> a.log2R : (rows + t - 1) / t;
   }
   int sum = count;  // tiles up to this thread's experts
 #pragma unroll
@@ -117,7 +123,7 @@ __device__ __forceinline__ int cut_list(const ListArgs& a, int* start, int* used
   }
   int at = sum - count;
   for (int e = e0; e < e1; ++e) {
-    const int p0 = start[e] * a.B, rows = used[e], t = tile_rows(e);
+    const int p0 = start[e] * a.B, rows = used[e], t = static_cast<int>(tile_rows(e));
     for (int64_t r = 0; r < rows; r += t, ++at)
       put(at, e, p0 + static_cast<int>(r), min(t, rows - static_cast<int>(r)));
   }
@@ -168,6 +174,10 @@ constexpr int kRowWarps = R > 64 ? 4 : 1;  // of a step
 template <int R>
 constexpr int kRowTurns = 4 / kRowWarps<R>;
 constexpr int kProductThreads = 512;
+// Accumulators.  With two, a narrow tile's products wait for the stores of the tile before the last:
+// the ways from products to stores and back take longer than either.
+template <int R>
+constexpr int kAccs = kProductTmem / R;
 
 // H: 256 m at a time, one or two of them on the same rows
 template <int R, int H>
@@ -202,8 +212,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   using Sh = ProductShape<R, H>;
   constexpr int S = Sh::kSlots;
   extern __shared__ unsigned char smem_raw[];
-  __shared__ unsigned long long full_s[S], free_s[S], rows_s[S], acc_full_s[2], acc_free_s[2],
-      info_full_s[kInfoSlots], info_free_s[kInfoSlots], done_s;
+  __shared__ unsigned long long full_s[S], free_s[S], rows_s[S], acc_full_s[kAccs<R>],
+      acc_free_s[kAccs<R>], info_full_s[kInfoSlots], info_free_s[kInfoSlots], done_s;
   __shared__ __align__(16) ProductInfo<R> info_s[kInfoSlots];
   __shared__ __align__(16) uint16_t stage_s[sizeof(Out) == 2 ? 8 : 1][32 * 32];
   __shared__ int2 tiles_s[kTilesHere];  // first row of the list; expert, rows - 1
@@ -221,7 +231,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       mbar_init(&free_s[s], 1);
       mbar_init(&rows_s[s], 32 * kRowWarps<R>);  // every copying thread
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < kAccs<R>; ++b) {
       mbar_init(&acc_full_s[b], 1);
       mbar_init(&acc_free_s[b], 16);  // the storing warps of both CTAs
     }
@@ -509,7 +519,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           if (H == 1 && ok) pair_commit(&acc_full_s[to]);
           if (H == 2) {
             to_phase ^= 1u;
-          } else if (++to == 2) {
+          } else if (++to == kAccs<R>) {
             to = 0;
             to_phase ^= 1u;
           }
@@ -517,8 +527,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       }
       ok = __all_sync(kFull, ok);
       at.skip(tiles * a.ksteps);
-      acc_phase ^= static_cast<uint32_t>((buf + tiles * H) / 2) & 1u;
-      buf = (buf + tiles * H) % 2;
+      acc_phase ^= static_cast<uint32_t>((buf + tiles * H) / kAccs<R>) & 1u;
+      buf = (buf + tiles * H) % kAccs<R>;
       leave_unit();
     }
     // nothing of the tensor core may be in flight when tensor memory is given back
@@ -625,7 +635,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           }
         };
         // (of an odd number of 32 rows the two warps of a quarter have the one more in turn)
-        const int begin = 32 * (half ^ buf);
+        const int begin = 32 * (half ^ (buf & 1));
         uint32_t one[32], two[32];
         if (begin < n && m32 < a.M) load(begin, one);
         if (m32 < a.M) {
@@ -637,7 +647,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) pair_arrive_first(&acc_free_s[buf]);
-        if (++buf == 2) {
+        if (++buf == kAccs<R>) {
           buf = 0;
           acc_phase ^= 1u;
         }
@@ -832,6 +842,7 @@ int product(const void* x, int type, const float* x_scales, int per_route, const
   list.max_rows = static_cast<int>(P);
   list.routes = static_cast<int>(routes);
   list.rows = R;
+  list.log2R = R == 64 ? 6 : 8;
   list.by_used = R > 64;
   const size_t tiles = most_tiles(T, E, topk, block_m, R);
   ProductArgs a{};

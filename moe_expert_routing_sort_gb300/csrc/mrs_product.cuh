@@ -43,11 +43,39 @@ __device__ __forceinline__ int prefix_length(int n, P&& is) {
   return lo;
 }
 
+// How many of n ascending values are below v, and how many are not above it: two such searches at
+// once, which take no longer than one.  (Of values in another order: some numbers up to n.)
+template <class V>
+__device__ __forceinline__ void prefix_lengths(int n, V&& value, int v, int& below, int& upto) {
+  int lo[2] = {0, 0}, m[2] = {n, n};
+  while (m[0] > 0 || m[1] > 0) {
+    int x[2][3];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        x[k][i] = m[k] > 0 ? value(lo[k] + min((i + 1) * ((m[k] + 3) >> 2), m[k]) - 1) : 0;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (m[k] <= 0) continue;
+      const int q = (m[k] + 3) >> 2;
+      int c = 0;
+#pragma unroll
+      for (int i = 0; i < 3; ++i) c += x[k][i] < v + k ? 1 : 0;
+      const int before = min(c * q, m[k]), last = min(before + q, m[k]);
+      lo[k] += before;
+      m[k] = c == 3 ? m[k] - before : last - before - 1;
+    }
+  }
+  below = lo[0];
+  upto = lo[1];
+}
+
 // The sorted list of a call.
 struct ListArgs {
   const int32_t *eid, *sid, *npp;
   int E, B, log2B, max_rows, routes;
-  int rows;       // rows of a tile at most
+  int rows, log2R;  // rows of a tile at most
   int by_used;    // tiles of a run alike, up to its last route; else of `rows` each, up to its last block
 };
 

@@ -38,17 +38,17 @@ constexpr int kGradCopiers = 8;          // warps that copy a step, four for eac
 constexpr int kGradTurns = 2;            // steps go to so many sets of them in turn
 constexpr int kGradThreads = 32 * (12 + kGradTurns * kGradCopiers);
 constexpr int kGradTmem = 512;
-constexpr int kGradSlots = 6;
-constexpr int kGradInfo = 4;
+constexpr int kGradSlots = 5;
+constexpr int kGradInfo = 16;  // units ahead: where they have one step each, all slots are on their way
 constexpr int kGradUsers = 9 + kGradTurns * kGradCopiers;  // eight storing warps, copies, their announcer
 constexpr int kGradDeep = 64;            // rows of a step
 // Steps from which a tile's sums are made in two accumulators, half of the rows each: the tensor core
 // cuts where an addition would round, and sums come out low by 1.2e-9 of themselves for every row.
 constexpr int kGradLong = 64;
 constexpr int kGradTile = 128 * 128;     // bytes of an operand in a CTA and step
-constexpr int kGradStage = 32 * 128;     // of a storing warp: 128 bytes of 32 rows
+constexpr int kGradStage = 32 * 128;     // of a storing warp: 128 bytes of 32 rows, twice
 constexpr size_t kGradSmem =
-    static_cast<size_t>(kGradSlots) * 2 * kGradTile + 8 * kGradStage + 1024;
+    static_cast<size_t>(kGradSlots) * 2 * kGradTile + 16 * kGradStage + 1024;
 
 struct GradInfo {
   int e, p0, rows, m0, k0;  // e < 0: no more units
@@ -175,14 +175,15 @@ __global__ void __launch_bounds__(kGradThreads, 1)
   } else if (warp == 1) {
     const int each = a.mtiles * a.ktiles, units = a.E * each, step = gridDim.x >> 1;
     const ListArgs& l = a.list;
-    const int blocks = min(max(__ldg(l.npp), 0), l.max_rows) >> l.log2B;
-    // the searches below take owners in order: every CTA looks at some
-    bool bad = false;
-    for (int b = blockIdx.x * 32 + lane; b < blocks; b += gridDim.x * 32) {
-      const int e = __ldg(l.eid + b);
-      bad |= e < 0 || e >= a.E || (b > 0 && __ldg(l.eid + b - 1) > e);
+    // the owners (most of them, for long lists) come while the list's length does
+    int touched = 0;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int b = 1024 * k + 32 * lane;
+      if (b < l.max_rows >> l.log2B)
+        asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(touched) : "l"(l.eid + b));
     }
-    if (bad) atomicOr(a.status, MOE_RS_DEVICE_BAD_EXPERT_ID);
+    const int blocks = min(max(__ldg(l.npp), 0), l.max_rows) >> l.log2B;
     for (int u0 = blockIdx.x >> 1; ok && u0 < units; u0 += 32 * step) {
       // a lane looks up one of the next 32 units: the run of its expert's blocks, and the rows of it
       // up to the last route (routes come first in its last block)
@@ -193,8 +194,9 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         const int i = static_cast<int>(u) - e * each, mt = i / a.ktiles;
         m0 = mt * 256;
         k0 = (i - mt * a.ktiles) * 256;
-        const int b0 = prefix_length(blocks, [&](int b) { return __ldg(l.eid + b) < e; });
-        const int n = prefix_length(blocks - b0, [&](int b) { return __ldg(l.eid + b0 + b) <= e; });
+        int b0, b1;
+        prefix_lengths(blocks, [&](int b) { return __ldg(l.eid + b); }, e, b0, b1);
+        const int n = max(b1 - b0, 0);
         p0 = b0 * l.B;
         if (n > 0) {
           const int32_t* last = l.sid + p0 + (n - 1) * l.B;
@@ -222,6 +224,13 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       info_s[at_info.slot].e = -1;
       mbar_arrive(&info_full_s[at_info.slot]);
     }
+    // the searches take owners in order: every CTA looks at some
+    bool bad = false;
+    for (int b = blockIdx.x * 32 + lane; b < blocks; b += gridDim.x * 32) {
+      const int e = __ldg(l.eid + b);
+      bad |= e < 0 || e >= a.E || (b > 0 && __ldg(l.eid + b - 1) > e);
+    }
+    if (bad) atomicOr(a.status, MOE_RS_DEVICE_BAD_EXPERT_ID);
   } else if (warp == 3) {
     // announces the rows that threads have written to the tensor cores
     Ring<S> at;
@@ -297,8 +306,9 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     }
   } else if (warp >= 4 && warp < 12) {
     const int quarter = warp & 3, half = (warp - 4) >> 2;
-    const uint32_t stage = base + S * 2 * kGradTile + (warp - 4) * kGradStage;
+    const uint32_t stage = base + S * 2 * kGradTile + 2 * (warp - 4) * kGradStage;
     const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
+    uint32_t to = 0;  // of the two stages
     int buf = 0;
     uint32_t acc_phase = 0;
     while (const GradInfo* q = next_unit()) {
@@ -354,17 +364,18 @@ __global__ void __launch_bounds__(kGradThreads, 1)
             }
           }
         }
-        if (lane == 0) tma_store_read();  // what was there has been read
+        if (lane == 0) tma_store_read<1>();  // what was there has been read
         __syncwarp();
 #pragma unroll
         for (int c = 0; c < 8; ++c)
           asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                           stage + 128 * lane + 16 * (c ^ (lane & 7))),
+                           stage + to + 128 * lane + 16 * (c ^ (lane & 7))),
                        "r"(w[4 * c]), "r"(w[4 * c + 1]), "r"(w[4 * c + 2]), "r"(w[4 * c + 3])
                        : "memory");
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) tma_store_3d(&omap, stage, k0 + c0, m, e);
+        if (lane == 0) tma_store_3d(&omap, stage + to, k0 + c0, m, e);
+        to ^= kGradStage;
       }
       if (some) {
         tc_fence_before();
