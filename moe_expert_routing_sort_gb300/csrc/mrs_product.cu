@@ -28,11 +28,11 @@
 // come out low, by 1.0e-6 of their size over 1024 columns, 4.4e-6 over 4096 and 1.9e-5 over 16384.
 //
 // Bound by the weights' bytes where an expert has few rows (T = 512, E = 896, 3584 -> 768, 16 bits:
-// 721 us, the floor of 729 at the rate of a copy) and by the tensor cores where it has many: T = 8192,
-// E = 64, topk = 8, 7168 -> 2048 in 1200 to 1315 us, 73 % of the tensor cores' clocks; a library
-// product of the same size in one piece takes 996 at the rate of a short run and 1116 at that of a
-// long one, where power holds the clock.  Short contractions (8192 skewed tokens, E = 896,
-// 384 -> 3584 in 8 bits, 434 us of 329) wait for the warps that store: three steps of products are
+// 720 us, the floor of 729 at the rate of a copy) and by the tensor cores where it has many: T = 8192,
+// E = 64, topk = 8, 7168 -> 2048 in 1150 to 1320 us, cool and warm, up to 84 % of the tensor cores'
+// clocks; a library product of the same size in one piece takes 996 at the rate of a short run and 1116
+// at that of a long one, where power holds the clock.  Short contractions (8192 skewed tokens, E = 896,
+// 384 -> 3584 in 8 bits, 430 us of 329) wait for the warps that store: three steps of products are
 // 130 KB of output.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -864,16 +864,18 @@ int product(const void* x, int type, const float* x_scales, int per_route, const
   a.K = K;
   a.P = static_cast<int>(P);
   a.ksteps = (K * static_cast<int>(size) + 127) / 128;
-  // 512 m on the same rows take in a quarter less for the same products, and leave no second
-  // accumulator for the next tile; half as many units fill the pairs less evenly.  us with 256 and with
-  // 512, bf16: T = 8192, E = 64, topk = 8, 7168 -> 2048 1250 1213; E = 16, 7168 -> 2048, 256, 384 and
-  // 768 rows an expert 130 160, 156 148, 230 229; E = 64, 3584 -> 768, 96 and 256 rows 89 92, 105 132.
+  // 512 m on the same rows take in a quarter less for the same products, which pays in long calls,
+  // where power holds the clock; they leave no second accumulator for the next tile, and half as many
+  // units fill the pairs less evenly.  us with 256 and with 512, bf16, by the rounds of units of 256: 106
+  // (rows' gradient of T = 8192, E = 64, topk = 8, 7168 -> 2048) 1380 1290, 31 (its product) 1152 1225,
+  // 15 (E = 8, 2048 rows an expert, 4096 -> 4096) 340 370; E = 16, 7168 -> 2048, 256 and 384 rows 130
+  // 160, 156 148; E = 64, 3584 -> 768, 96 and 256 rows 89 92, 105 132.
   const int pairs = sms / 2;
   const double row_tiles = static_cast<double>(routes) / R + 0.5 * static_cast<double>(hit);
   auto rounds = [&](int h) {
     return row_tiles * ((M + h * kPairRows - 1) / (h * kPairRows)) / pairs + 0.5;
   };
-  const int H = R > 64 && a.ksteps >= 16 && 2 * 0.95 * rounds(2) < rounds(1) ? 2 : 1;
+  const int H = R > 64 && a.ksteps >= 16 && 2 * 0.9875 * rounds(2) < rounds(1) ? 2 : 1;
   a.mtiles = (M + H * kPairRows - 1) / (H * kPairRows);
   a.type = type == MOE_RS_BF16 ? 1 : 0;
   a.out_type = out_type;

@@ -32,8 +32,8 @@ PATHS = [
     (129, 1, 1, 80, 40, 16),
     (128, 1, 1, 80, 40, 1024),
     (9, 2, 2, 4160, 40, 64),
-    (4096, 8, 2, 2064, 5128, 64),    # 512 outputs on the same rows
-    (4096, 8, 2, 5136, 1032, 64),    # and 512 columns of the rows' gradient
+    (4096, 8, 2, 2064, 5128, 64),
+    (4096, 8, 2, 5136, 1032, 64),
     (4000, 1100, 16, 64, 3592, 16),  # several output tiles a unit, wide and narrow row tiles
     (3000, 2000, 2, 72, 1544, 16),
 ]
@@ -62,6 +62,38 @@ def test_paths(T, E, topk, cols, outs, B):
     for e in range(E):
         at = (owner == e).nonzero()[:, 0]
         _near(dw[e], gd[at].T @ xd[at], gd[at].T.abs() @ xd[at].abs(), max(at.numel(), 1))
+    assert ws.status_word() == 0
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "rows"])
+def test_wide_outputs_over_many_rounds(kind, dtype):
+    """Outputs (or the gradient's columns) that leave a pair of CTAs more than 40 tiles, which are
+    then of 512 outputs.  Checked at both ends and in 400 places."""
+    T, E, topk, B, wide, deep = 3000, 2, 2, 64, 41416, 2080 if kind == "fp8" else 1040
+    g = _gen("rounds", kind)
+    r = Routes(g, T, E, topk, B)
+    pick = torch.cat([torch.arange(300, device=DEV), torch.arange(wide - 300, wide, device=DEV),
+                      torch.randperm(wide, generator=g, device=DEV)[:400]])
+    ws = mrs.ProductWorkspace(T, E, topk, B, device=DEV)
+    terms = 4 if kind == "fp8" else 1
+    if kind == "rows":
+        w = _rows(g, E * deep, wide, BF).view(E, deep, wide)
+        x = _rows(g, T * topk, deep, BF)
+        y = mrs.experts_grad_rows(x, w, *r.lists, dtype=dtype, workspace=ws)
+        want, size = _ref(x, w.transpose(1, 2)[:, pick], r)
+    else:
+        x, w = _rows(g, T, deep, BF), _rows(g, E * wide, deep, BF).view(E, wide, deep)
+        if kind == "fp8":
+            x, w = mrs.fp8_quantize(x), mrs.fp8_quantize(w)
+        y = mrs.experts_product(x, w, *r.lists, dtype=dtype, workspace=ws)
+        if kind == "fp8":
+            x = x.codes.double() * x.scales.double()[:, None]
+            w = w.codes.double()[:, pick] * w.scales.double()[:, pick, None]
+        else:
+            w = w[:, pick]
+        want, size = _ref(x, w, r)
+    _near(y[:, pick], want, size, deep, terms)
     assert ws.status_word() == 0
 
 
