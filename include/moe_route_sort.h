@@ -478,8 +478,9 @@ size_t moe_experts_product_workspace_bytes(int T, int E, int topk, int block_m);
  * buffers); a device wait that gives up sets MOE_RS_DEVICE_WAIT_TIMEOUT (outputs invalid).
  * The sums of more than 128 routes, and those of the gradients below, are the tensor core's, whose
  * additions cut where others round: results of random terms are small by about 1.2e-9 of their size
- * for every term, 1.0e-6 over 1024 terms and 1.9e-5 over 16384 (in 8 bits less), before they are
- * rounded.  Results are the same bits every call.
+ * for every term, 1.0e-6 over 1024 terms and 1.9e-5 over 16384 (in 8 bits less; weights'
+ * gradients in fp32 over more than 1024 rows half of it), before they are rounded.  Results are the
+ * same bits every call.
  * cols and outs: multiples of 8 (cols of 16 for MOE_RS_FP8) in [8, MOE_RS_PRODUCT_MAX_COLS];
  * limits of T, E, topk, block_m as for moe_sort.  X, W, out: 16-byte aligned.
  * No counterpart in the source pages, whose products belong to another library. */

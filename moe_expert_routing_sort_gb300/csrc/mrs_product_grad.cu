@@ -12,10 +12,11 @@
 // their zeros from the storing warps alone.  Two sets of eight warps copy the steps in turn, so that
 // one set's look at the list is hidden behind the other's copies; tiles leave by tensor copies.
 //
-// T = 8192, E = 64, topk = 8, 2048 x 7168: 1580 to 1700 us, of 996 at the tensor cores' rate.  Bound
+// T = 8192, E = 64, topk = 8, 2048 x 7168: 1600 to 1700 us, of 996 at the tensor cores' rate.  Bound
 // by the copies: both operands are rows somewhere in memory, a thread's copy takes 16 bytes, and an SM
-// takes in 512 bytes of such copies every 16 clocks, 64 KB a step in 1024 clocks more or less where
-// its products need 512.  E = 129, T = 1000: the latency of the two or three units that a pair has.
+// takes in 512 bytes of such copies every 16 clocks, the 32 KB of a step in 1024 clocks or so where
+// its products need 512.  T = 1000, E = 129, 264 x 520: 24.5 us, the storing warps' latency for ten tiles
+// of one step each.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -43,8 +44,12 @@ constexpr int kGradInfo = 16;  // units ahead: where they have one step each, al
 constexpr int kGradUsers = 9 + kGradTurns * kGradCopiers;  // eight storing warps, copies, their announcer
 constexpr int kGradDeep = 64;            // rows of a step
 // Steps from which a tile's sums are made in two accumulators, half of the rows each: the tensor core
-// cuts where an addition would round, and sums come out low by 1.2e-9 of themselves for every row.
-constexpr int kGradLong = 64;
+// cuts where an addition would round, and sums come out low by 1e-9 of themselves for every row, 1e-6
+// over 1024.  fp32 results that have more rows give up the overlap of the next tile's products with the
+// stores (T = 8192, E = 64, 2048 x 7168: 1620 us with a limit of 1024 rows, 1700 with 512, 1551 with
+// 4096); in 16 bits it does not show before 4096 rows.
+template <class Out>
+constexpr int kGradLong = sizeof(Out) == 4 ? 16 : 64;
 constexpr int kGradTile = 128 * 128;     // bytes of an operand in a CTA and step
 constexpr int kGradStage = 32 * 128;     // of a storing warp: 128 bytes of 32 rows, twice
 constexpr size_t kGradSmem =
@@ -263,7 +268,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         if (elect_one()) {
           Ring<S> s = at;
           int into = buf;
-          const int second = steps > kGradLong ? steps / 2 : steps;  // its first step
+          const int second = steps > kGradLong<Out> ? steps / 2 : steps;  // its first step
           ok = pair_wait(&acc_free_s[buf], acc_phase ^ 1u, limit);
           for (int ks = 0; ok && ks < steps; ++ks) {
             if (ks == second) {
@@ -290,7 +295,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         }
         ok = __all_sync(kFull, ok);
         at.skip(steps);
-        if (steps > kGradLong) {  // both, and back to this one
+        if (steps > kGradLong<Out>) {  // both, and back to this one
           acc_phase ^= 1u;
         } else if (++buf == 2) {
           buf = 0;
@@ -313,7 +318,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     uint32_t acc_phase = 0;
     while (const GradInfo* q = next_unit()) {
       const int m = q->m0 + 128 * rank + 32 * quarter, k0 = q->k0, e = q->e;
-      const bool some = q->rows > 0, both = q->rows > kGradLong * kGradDeep;
+      const bool some = q->rows > 0, both = q->rows > kGradLong<Out> * kGradDeep;
       if (some) {
         ok = warp_wait(&acc_full_s[buf], acc_phase, limit);
         if (!ok) break;

@@ -445,9 +445,10 @@ def test_rows_and_outputs_past_32_bit_offsets():
 
 
 def test_gradient_of_weights_over_thousands_of_rows():
-    """Experts of 1000, 5000, 4097, 0 and 4096 rows, each with several tiles for a pair of CTAs."""
+    """Experts of up to 5000 rows, at and beside the numbers from which tiles are summed in two parts,
+    each with several tiles for a pair of CTAs."""
     g = _gen("long")
-    counts, cols, outs = (1000, 5000, 4097, 0, 4096), 2056, 1288
+    counts, cols, outs = (1000, 5000, 4097, 0, 4096, 1024, 1025), 2056, 1288
     T = sum(counts)
     r = Routes(g, T, len(counts), 1, 16)
     owner = torch.cat([torch.full((n,), e, device=DEV) for e, n in enumerate(counts)])
