@@ -12,10 +12,10 @@
 // their zeros from the storing warps alone.  Two sets of eight warps copy the steps in turn, so that
 // one set's look at the list is hidden behind the other's copies; tiles leave by tensor copies.
 //
-// T = 8192, E = 64, topk = 8, 2048 x 7168: 1600 to 1700 us, of 996 at the tensor cores' rate.  Bound
+// T = 8192, E = 64, topk = 8, 2048 x 7168: 1570 to 1700 us, of 996 at the tensor cores' rate.  Bound
 // by the copies: both operands are rows somewhere in memory, a thread's copy takes 16 bytes, and an SM
 // takes in 512 bytes of such copies every 16 clocks, the 32 KB of a step in 1024 clocks or so where
-// its products need 512.  T = 1000, E = 129, 264 x 520: 24.5 us, the storing warps' latency for ten tiles
+// its products need 512.  T = 1000, E = 129, 264 x 520: 24.9 us, the storing warps' latency for ten tiles
 // of one step each.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -39,21 +39,23 @@ constexpr int kGradCopiers = 8;          // warps that copy a step, four for eac
 constexpr int kGradTurns = 2;            // steps go to so many sets of them in turn
 constexpr int kGradThreads = 32 * (12 + kGradTurns * kGradCopiers);
 constexpr int kGradTmem = 512;
-constexpr int kGradSlots = 5;
+// (Five slots and a second stage for each storing warp: T = 8192, E = 64, 2048 x 7168 1600 us and 1570 so,
+// E = 128, 768 x 3584 408 and 378; T = 1000, E = 129, 264 x 520 24.5 and 24.9.)
+constexpr int kGradSlots = 6;
 constexpr int kGradInfo = 16;  // units ahead: where they have one step each, all slots are on their way
 constexpr int kGradUsers = 9 + kGradTurns * kGradCopiers;  // eight storing warps, copies, their announcer
 constexpr int kGradDeep = 64;            // rows of a step
 // Steps from which a tile's sums are made in two accumulators, half of the rows each: the tensor core
 // cuts where an addition would round, and sums come out low by 1e-9 of themselves for every row, 1e-6
 // over 1024.  fp32 results that have more rows give up the overlap of the next tile's products with the
-// stores (T = 8192, E = 64, 2048 x 7168: 1620 us with a limit of 1024 rows, 1700 with 512, 1551 with
+// stores (T = 8192, E = 64, 2048 x 7168: 1570 us with a limit of 1024 rows, 1690 with 512, 1550 with
 // 4096); in 16 bits it does not show before 4096 rows.
 template <class Out>
 constexpr int kGradLong = sizeof(Out) == 4 ? 16 : 64;
 constexpr int kGradTile = 128 * 128;     // bytes of an operand in a CTA and step
-constexpr int kGradStage = 32 * 128;     // of a storing warp: 128 bytes of 32 rows, twice
+constexpr int kGradStage = 32 * 128;     // of a storing warp: 128 bytes of 32 rows
 constexpr size_t kGradSmem =
-    static_cast<size_t>(kGradSlots) * 2 * kGradTile + 16 * kGradStage + 1024;
+    static_cast<size_t>(kGradSlots) * 2 * kGradTile + 8 * kGradStage + 1024;
 
 struct GradInfo {
   int e, p0, rows, m0, k0;  // e < 0: no more units
@@ -311,9 +313,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     }
   } else if (warp >= 4 && warp < 12) {
     const int quarter = warp & 3, half = (warp - 4) >> 2;
-    const uint32_t stage = base + S * 2 * kGradTile + 2 * (warp - 4) * kGradStage;
+    const uint32_t stage = base + S * 2 * kGradTile + (warp - 4) * kGradStage;
     const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
-    uint32_t to = 0;  // of the two stages
     int buf = 0;
     uint32_t acc_phase = 0;
     while (const GradInfo* q = next_unit()) {
@@ -369,18 +370,17 @@ __global__ void __launch_bounds__(kGradThreads, 1)
             }
           }
         }
-        if (lane == 0) tma_store_read<1>();  // what was there has been read
+        if (lane == 0) tma_store_read();  // what was there has been read
         __syncwarp();
 #pragma unroll
         for (int c = 0; c < 8; ++c)
           asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                           stage + to + 128 * lane + 16 * (c ^ (lane & 7))),
+                           stage + 128 * lane + 16 * (c ^ (lane & 7))),
                        "r"(w[4 * c]), "r"(w[4 * c + 1]), "r"(w[4 * c + 2]), "r"(w[4 * c + 3])
                        : "memory");
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) tma_store_3d(&omap, stage + to, k0 + c0, m, e);
-        to ^= kGradStage;
+        if (lane == 0) tma_store_3d(&omap, stage, k0 + c0, m, e);
       }
       if (some) {
         tc_fence_before();

@@ -214,9 +214,8 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t sr
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 // The groups so far have been read from shared memory; and have been written.
-template <int kLeft>
 __device__ __forceinline__ void tma_store_read() {
-  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kLeft) : "memory");
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 __device__ __forceinline__ void tma_store_done() {
   asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
