@@ -34,6 +34,7 @@
 // at that of a long one, where power holds the clock.  Short contractions (8192 skewed tokens, E = 896,
 // 384 -> 3584 in 8 bits, 430 us of 329) wait for the warps that store: three steps of products are
 // 130 KB of output.
+#include <algorithm>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -879,9 +880,12 @@ int product(const void* x, int type, const float* x_scales, int per_route, const
   a.mtiles = (M + H * kPairRows - 1) / (H * kPairRows);
   a.type = type == MOE_RS_BF16 ? 1 : 0;
   a.out_type = out_type;
-  // A unit is as many output tiles of one row tile as leave 32 rounds of units.
+  // A unit is as many output tiles of one row tile as leave 32 rounds of units, but no more than 32768
+  // steps (some 20 ms): the list waits for a unit as a whole, and 65536 x 65536 outputs and columns have
+  // 262144 of them, more than half of the default limit.
   const size_t each = (routes / R + hit) * a.mtiles / (32 * static_cast<size_t>(pairs));
-  a.chunk = each < 1 ? 1 : (each > static_cast<size_t>(a.mtiles) ? a.mtiles : static_cast<int>(each));
+  const size_t most = std::min(static_cast<size_t>(a.mtiles), static_cast<size_t>(32768 / (H * a.ksteps)));
+  a.chunk = static_cast<int>(each < 1 ? 1 : (each > most ? most : each));
   a.nchunk = (a.mtiles + a.chunk - 1) / a.chunk;
   a.chunk = (a.mtiles + a.nchunk - 1) / a.nchunk;
   a.nchunk = (a.mtiles + a.chunk - 1) / a.chunk;

@@ -57,6 +57,13 @@ constexpr int kGradStage = 32 * 128;     // of a storing warp: 128 bytes of 32 r
 constexpr size_t kGradSmem =
     static_cast<size_t>(kGradSlots) * 2 * kGradTile + 8 * kGradStage + 1024;
 
+// Waits that last as long as a tile takes (its storing warps', and the list's for a unit to be done)
+// have the limit once more for every 2^21 rows: 33 M clocks of products and copies, 6 % of the default
+// limit.  (With one limit whatever the rows, experts of 25 million rows and more gave up.)
+__device__ __forceinline__ unsigned long long grad_limit(unsigned long long limit, unsigned rows) {
+  return limit * (1u + (rows >> 21));
+}
+
 struct GradInfo {
   int e, p0, rows, m0, k0;  // e < 0: no more units
 };
@@ -191,6 +198,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(touched) : "l"(l.eid + b));
     }
     const int blocks = min(max(__ldg(l.npp), 0), l.max_rows) >> l.log2B;
+    unsigned most = 0;  // rows of a unit so far
     for (int u0 = blockIdx.x >> 1; ok && u0 < units; u0 += 32 * step) {
       // a lane looks up one of the next 32 units: the run of its expert's blocks, and the rows of it
       // up to the last route (routes come first in its last block)
@@ -216,8 +224,9 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       for (int i = 0; ok && i < 32; ++i) {
         const int ei = __shfl_sync(kFull, e, i);
         if (ei < 0) break;
-        ok = warp_wait(&info_free_s[at_info.slot], at_info.phase ^ 1u, limit);
+        ok = warp_wait(&info_free_s[at_info.slot], at_info.phase ^ 1u, grad_limit(limit, most));
         if (!ok) break;
+        most = max(most, static_cast<unsigned>(__shfl_sync(kFull, rows, i)));
         if (lane == i) {
           info_s[at_info.slot] = GradInfo{e, p0, rows, m0, k0};
           mbar_arrive(&info_full_s[at_info.slot]);
@@ -226,7 +235,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         at_info.advance();
       }
     }
-    ok = ok && warp_wait(&info_free_s[at_info.slot], at_info.phase ^ 1u, limit);
+    ok = ok && warp_wait(&info_free_s[at_info.slot], at_info.phase ^ 1u, grad_limit(limit, most));
     if (ok && lane == 0) {
       info_s[at_info.slot].e = -1;
       mbar_arrive(&info_full_s[at_info.slot]);
@@ -321,10 +330,11 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       const int m = q->m0 + 128 * rank + 32 * quarter, k0 = q->k0, e = q->e;
       const bool some = q->rows > 0, both = q->rows > kGradLong<Out> * kGradDeep;
       if (some) {
-        ok = warp_wait(&acc_full_s[buf], acc_phase, limit);
+        const unsigned long long whole = grad_limit(limit, q->rows);
+        ok = warp_wait(&acc_full_s[buf], acc_phase, whole);
         if (!ok) break;
         if (both) {
-          ok = warp_wait(&acc_full_s[buf ^ 1], acc_phase ^ (buf == 0 ? 0u : 1u), limit);
+          ok = warp_wait(&acc_full_s[buf ^ 1], acc_phase ^ (buf == 0 ? 0u : 1u), whole);
           if (!ok) break;
         }
         tc_fence_after();
