@@ -64,7 +64,7 @@ __device__ __forceinline__ int cut_list(const ListArgs& a, int* start, int* used
   };
   if (tid < blocks) look(tid, owner, previous);
 #pragma unroll 4
-  for (int b = tid + kThreads; b < blocks; b += kThreads)
+  for (unsigned b = tid + kThreads; b < static_cast<unsigned>(blocks); b += kThreads)
     look(b, __ldg(a.eid + b), __ldg(a.eid + b - 1));
   if (__syncthreads_or(bad) && tid == 0) atomicOr(status, MOE_RS_DEVICE_BAD_EXPERT_ID);
   // an expert without a run starts where the next one does: the least start from it on (which is

@@ -47,24 +47,26 @@ __device__ __forceinline__ int prefix_length(int n, P&& is) {
 // once, which take no longer than one.  (Of values in another order: some numbers up to n.)
 template <class V>
 __device__ __forceinline__ void prefix_lengths(int n, V&& value, int v, int& below, int& upto) {
-  int lo[2] = {0, 0}, m[2] = {n, n};
+  // (without a sign: four quarters of 2^31 - 1 values end past them)
+  unsigned lo[2] = {0, 0}, m[2] = {static_cast<unsigned>(n), static_cast<unsigned>(n)};
   while (m[0] > 0 || m[1] > 0) {
     int x[2][3];
 #pragma unroll
     for (int k = 0; k < 2; ++k)
 #pragma unroll
       for (int i = 0; i < 3; ++i)
-        x[k][i] = m[k] > 0 ? value(lo[k] + min((i + 1) * ((m[k] + 3) >> 2), m[k]) - 1) : 0;
+        x[k][i] = m[k] > 0 ? value(lo[k] + min((i + 1u) * ((m[k] + 3) >> 2), m[k]) - 1) : 0;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      if (m[k] <= 0) continue;
-      const int q = (m[k] + 3) >> 2;
-      int c = 0;
+      if (m[k] == 0) continue;
+      const unsigned q = (m[k] + 3) >> 2;
+      unsigned c = 0;
 #pragma unroll
       for (int i = 0; i < 3; ++i) c += x[k][i] < v + k ? 1 : 0;
-      const int before = min(c * q, m[k]), last = min(before + q, m[k]);
+      const unsigned before = min(c * q, m[k]), last = min(before + q, m[k]);
       lo[k] += before;
-      m[k] = c == 3 ? m[k] - before : last - before - 1;
+      // (of values in another order nothing may be left before the last)
+      m[k] = c == 3 ? m[k] - before : (last > before ? last - before - 1 : 0);
     }
   }
   below = lo[0];

@@ -67,6 +67,7 @@ __device__ __forceinline__ unsigned long long grad_limit(unsigned long long limi
 struct GradInfo {
   int e, p0, rows, m0, k0;  // e < 0: no more units
 };
+__device__ __forceinline__ int grad_steps(unsigned rows) { return (rows + kGradDeep - 1) / kGradDeep; }
 
 template <class Out>
 __global__ void __launch_bounds__(kGradThreads, 1)
@@ -135,27 +136,29 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     const uint32_t place = (is_x ? xbase : gbase) + (chunk >> 3) * (kGradDeep * 128) +
                            (w16 + sub) * 128;
     while (const GradInfo* q = next_unit()) {
-      const int p0 = q->p0, rows = q->rows;
+      // (what looks past the last row is counted without a sign: a list has up to 2^31 - 1 rows)
+      const int p0 = q->p0;
+      const unsigned rows = q->rows;
       const int col = (is_x ? q->k0 : q->m0) + 128 * rank + 8 * chunk;
       const bool in = col < cols;
       const unsigned char* mine = from + (in ? 2 * static_cast<size_t>(col) : 0);
       // lanes 0 to 15 look up a row each, four steps ahead (one step ahead every step took as long as
       // the access: 2200 us for T = 8192, E = 64, 7168 -> 2048)
-      auto route_of = [&](int first) {
-        const int r = first + w16 + lane;
+      auto route_of = [&](unsigned first) {
+        const unsigned r = first + w16 + lane;
         return lane < 16 && r < rows ? __ldg(a.list.sid + p0 + r) : -1;
       };
       int ahead[4];
-      const int skipped = (turn - now + kGradTurns) % kGradTurns, steps = (rows + kGradDeep - 1) / kGradDeep;
-      constexpr int kStride = kGradTurns * kGradDeep;
-      const int r1 = skipped * kGradDeep;
+      const int skipped = (turn - now + kGradTurns) % kGradTurns, steps = grad_steps(rows);
+      constexpr unsigned kStride = kGradTurns * kGradDeep;
+      const unsigned r1 = skipped * kGradDeep;
       at.skip(min(skipped, steps));
 #pragma unroll
       for (int k = 0; k < 4; ++k) ahead[k] = route_of(r1 + k * kStride);
-      for (int r4 = r1; r4 < rows; r4 += 4 * kStride) {
+      for (unsigned r4 = r1; r4 < rows; r4 += 4 * kStride) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const int r0 = r4 + k * kStride;
+          const unsigned r0 = r4 + k * kStride;
           if (r0 >= rows) break;
           const int r = ahead[k] >= 0 && ahead[k] < a.list.routes
                             ? (per_route ? ahead[k] : ahead[k] / a.topk) : -1;
@@ -178,7 +181,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
             }
             copy_arrive(&rows_s[at.slot]);
           }
-          at.skip(min(kGradTurns, steps - r0 / kGradDeep));
+          at.skip(min(kGradTurns, steps - static_cast<int>(r0 / kGradDeep)));
         }
       }
       now = (now + steps) % kGradTurns;
@@ -242,7 +245,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     }
     // the searches take owners in order: every CTA looks at some
     bool bad = false;
-    for (int b = blockIdx.x * 32 + lane; b < blocks; b += gridDim.x * 32) {
+    for (unsigned b = blockIdx.x * 32 + lane; b < static_cast<unsigned>(blocks); b += gridDim.x * 32) {
       const int e = __ldg(l.eid + b);
       bad |= e < 0 || e >= a.E || (b > 0 && __ldg(l.eid + b - 1) > e);
     }
@@ -251,7 +254,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     // announces the rows that threads have written to the tensor cores
     Ring<S> at;
     while (const GradInfo* q = next_unit()) {
-      const int steps = (q->rows + kGradDeep - 1) / kGradDeep;
+      const int steps = grad_steps(q->rows);
       if (elect_one()) {
         Ring<S> s = at;
         for (int i = 0; ok && i < steps; ++i) {
@@ -273,7 +276,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     bool any = false;
     const uint32_t word = pair_word(a.type, true, true, 256);
     while (const GradInfo* q = next_unit()) {
-      const int rows = q->rows, steps = (rows + kGradDeep - 1) / kGradDeep;
+      const unsigned rows = q->rows;
+      const int steps = grad_steps(rows);
       if (steps > 0) {
         any = true;
         if (elect_one()) {
@@ -293,7 +297,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
             tc_fence_after();
             const uint64_t dg = desc_lines128(gbase + s.slot * kGradTile, kGradDeep);
             const uint64_t dx = desc_lines128(xbase + s.slot * kGradTile, kGradDeep);
-            const int parts = (rows - ks * kGradDeep + 15) >> 4;
+            const int parts = (min(rows - ks * kGradDeep, 64u) + 15) >> 4;
 #pragma unroll
             for (int g = 0; g < 4; ++g)
               if (g < parts)  // else rows past the last: zeros

@@ -62,3 +62,30 @@ def _check_grad_weights(lists, dtype, seed):
 def test_gradient_of_weights_of_an_expert_of_134_million_rows(dtype):
     # two million steps of one tile: the waits for it last as long
     _check_grad_weights(_one_expert(1 << 22, 32, 128), dtype, 1)
+
+
+# 2^31 - 2 routes in blocks of one row: what is counted ahead of the last row, and past the last block,
+# does not fit 31 bits
+LONGEST = (69273666, 31, 1)
+
+
+def test_products_of_the_longest_list():
+    T, topk, B = LONGEST
+    lists = _one_expert(T, topk, B)
+    x, at = _few_rows(T, 8, 2)
+    g = torch.Generator(device=DEV).manual_seed(3)
+    w = torch.randint(-2, 3, (1, 8, 8), generator=g, device=DEV).to(BF)
+    ws = mrs.ProductWorkspace(T, 1, topk, B, device=DEV)
+    out = torch.empty(T * topk, 8, dtype=BF, device=DEV)
+    for call, by in ((mrs.experts_product, w[0].T), (mrs.experts_grad_rows, w[0])):
+        out.fill_(7.0)
+        call(x, w, *lists, out=out, workspace=ws)
+        assert ws.status_word() == 0
+        want = (x.float() @ by.float()).to(BF)
+        each = out.view(T, topk, 8)
+        for i in range(0, T, 1 << 22):
+            assert (each[i:i + (1 << 22)] == want[i:i + (1 << 22), None]).all()
+
+
+def test_gradient_of_weights_of_the_longest_list():
+    _check_grad_weights(_one_expert(*LONGEST), F32, 4)
