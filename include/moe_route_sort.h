@@ -439,7 +439,8 @@ int moe_rms_norm_backward(const void* s, int dtype, const void* gain, int gain_d
  * weights [rows] fp32 (topk_weights, in route order), or NULL: 1.  y [rows, cols] of type dtype
  * (MOE_RS_BF16 or MOE_RS_FP16, that of x), codes and scales the same in 8 bits (from the fp32
  * value); y may be NULL, codes and scales too, not both.  Finite a and b whose product is finite
- * give what is written; infinities and NaN what fp32 arithmetic makes of them.
+ * give what is written, where sigmoid(a) alone would be zero too (a result below 2^-124 may be zero
+ * for a < -174); infinities and NaN give what fp32 arithmetic makes of them.
  * Errors as for moe_fp8_quantize.  No counterpart in the source pages. */
 int moe_swiglu(const void* x, int dtype, int64_t x_stride, int64_t rows, int cols,
                const float* weights, void* y, uint8_t* codes, float* scales, cudaStream_t stream);
