@@ -84,12 +84,16 @@ def _rows(x, name, T, topk, cols, dtype, dev):
     return need(x, dtype, 0, dev, name), 0 if x.shape[0] == T else 1
 
 
+def _three(name, w):
+    if w.dim() != 3:
+        raise ValueError(f"{name} must be [E, outs, cols], got {tuple(w.shape)}")
+
+
 def _half_weights(w):
     dev = cuda_device(w, "w")
     if w.dtype not in _HALF:
         raise ValueError(f"w must be bfloat16 or float16, got {w.dtype}")
-    if w.dim() != 3:
-        raise ValueError(f"w must be [E, outs, cols], got {tuple(w.shape)}")
+    _three("w", w)
     return dev, need(w, w.dtype, 0, dev, "w")
 
 
@@ -150,6 +154,7 @@ def experts_product(x, w, T: int, topk: int, block_m: int, sorted_token_ids, exp
     if out is None:
         eight = isinstance(w, Fp8Rows)
         dev, like = (w.device, w.codes) if eight else (cuda_device(w, "w"), w)
+        _three("w", like)
         kind = dtype or (torch.bfloat16 if eight else w.dtype)
         out = made(dev, stream, lambda: torch.zeros(T * topk, like.shape[1], dtype=kind,
                                                     device=like.device))
@@ -179,6 +184,7 @@ def experts_grad_rows(grad, w, T: int, topk: int, block_m: int, sorted_token_ids
     """Run moe_experts_grad_rows; returns ``out`` [T * topk, cols], of type ``dtype`` (w's).
     Without ``out`` the rows of dropped routes are zero."""
     if out is None:
+        _three("w", w)
         out = made(cuda_device(w, "w"), stream,
                    lambda: torch.zeros(T * topk, w.shape[-1], dtype=dtype or w.dtype,
                                        device=w.device))
@@ -193,8 +199,7 @@ def moe_experts_grad_weights(grad, x, T, topk, block_m, sorted_token_ids, expert
     float32), every element of it.  ``grad`` has T or T * topk rows of outs elements, ``x`` T or
     T * topk of cols, both of one 16-bit type."""
     dev = cuda_device(grad_weights, "grad_weights")
-    if grad_weights.dim() != 3:
-        raise ValueError(f"grad_weights must be [E, outs, cols], got {tuple(grad_weights.shape)}")
+    _three("grad_weights", grad_weights)
     E, outs, cols = grad_weights.shape
     if grad.dtype not in _HALF:
         raise ValueError(f"grad must be bfloat16 or float16, got {grad.dtype}")
@@ -215,10 +220,13 @@ def experts_grad_weights(grad, x, E: int, T: int, topk: int, block_m: int, sorte
                          stream=None) -> torch.Tensor:
     """Run moe_experts_grad_weights; returns ``out`` [E, outs, cols], of type ``dtype``."""
     if out is None:
+        if grad.dim() != 2 or x.dim() != 2:
+            raise ValueError(f"grad and x must be matrices, got {tuple(grad.shape)} and "
+                             f"{tuple(x.shape)}")
         out = made(cuda_device(grad, "grad"), stream,
                    lambda: torch.empty(E, grad.shape[-1], x.shape[-1], dtype=dtype,
                                        device=grad.device))
-    elif out.shape[0] != E:
+    elif out.dim() > 0 and out.shape[0] != E:
         raise ValueError(f"out must be of {E} experts, got {tuple(out.shape)}")
     moe_experts_grad_weights(grad, x, T, topk, block_m, sorted_token_ids, expert_ids,
                              num_tokens_post_pad, out, workspace, stream)

@@ -271,6 +271,8 @@ def rms_norm_backward(s, weight, rstd, grad=None, grad_rows=None, parts: int = 1
                       stream=None) -> NormGrads:
     """Allocate (unless ``out`` is given) and run moe_rms_norm_backward; returns the gradients."""
     if out is None:
+        if s.dim() != 2:
+            raise ValueError(f"s must be [T, cols], got {tuple(s.shape)}")
         out = made(cuda_device(s, "s"), stream,
                    lambda: NormGrads.allocate(*s.shape, s.dtype, weight_grad, device=s.device))
     elif out._shape != (*s.shape, s.dtype, s.get_device()):
