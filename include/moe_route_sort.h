@@ -84,15 +84,18 @@ extern "C" {
 #define MOE_RS_ERR_NULL_POINTER (-1)      /* a required pointer is NULL (with T > 0)        */
 #define MOE_RS_ERR_BAD_EXPERTS (-2)       /* E outside [1, 4096]                           */
 #define MOE_RS_ERR_BAD_GROUPS (-3)        /* G outside [1, 64], E % G != 0, Kg outside [1,G] */
-#define MOE_RS_ERR_BAD_TOPK (-4)          /* K outside [1, 32] or K > Kg * g               */
+#define MOE_RS_ERR_BAD_TOPK (-4)          /* K (the norm: parts) outside [1, 32], or K > Kg * g */
 #define MOE_RS_ERR_BAD_BLOCK_M (-5)       /* B not a power of two in [1, 1024]             */
 #define MOE_RS_ERR_BAD_TOKENS (-6)        /* T < 0 (or T > 8 for moe_gate_route_sort)      */
-#define MOE_RS_ERR_OVERFLOW (-7)          /* N or the padded length does not fit in int32  */
-#define MOE_RS_ERR_MISALIGNED (-8)        /* logits not 16-byte aligned, or another buffer
-                                             not aligned to its element size (workspace: 16) */
+#define MOE_RS_ERR_OVERFLOW (-7)          /* N, the padded length, a number of rows or a row
+                                             stride does not fit in int32                  */
+#define MOE_RS_ERR_MISALIGNED (-8)        /* logits, rows, weights, 16-bit results, products'
+                                             results or workspace not 16-byte aligned (row
+                                             strides too), 8-bit codes not 8-byte aligned, or
+                                             another buffer not to its element size        */
 #define MOE_RS_ERR_ALIAS (-9)             /* an output overlaps an input or another output */
 #define MOE_RS_ERR_WORKSPACE (-10)        /* workspace NULL or smaller than required       */
-#define MOE_RS_ERR_BAD_SCALE (-11)        /* routed_scale not finite                       */
+#define MOE_RS_ERR_BAD_SCALE (-11)        /* routed_scale not finite, or eps outside [0, 1] */
 #define MOE_RS_ERR_LAUNCH (-12)           /* the CUDA runtime rejected a kernel launch     */
 #define MOE_RS_ERR_TOO_LARGE (-13)        /* shape needs more than the static scratch of
                                              moe_route_sort_noalloc                        */
@@ -100,9 +103,12 @@ extern "C" {
 #define MOE_RS_ERR_NOT_MAPPED (-15)       /* host memory not mapped into the device space  */
 #define MOE_RS_ERR_BAD_DEBUG_KNOB (-16)   /* moe_route_sort_debug_set: unknown knob         */
 #define MOE_RS_ERR_BAD_DTYPE (-17)        /* a type code the operation does not take       */
-#define MOE_RS_ERR_BAD_COLS (-18)         /* row length not a multiple of 32 in [32, 32768],
-                                             a row stride below it, or an output width not a
-                                             multiple of 8 in [8, 65536]                   */
+#define MOE_RS_ERR_BAD_COLS (-18)         /* row length or output width that the operation does
+                                             not take, or a row stride below the length: 4-bit
+                                             rows multiples of 32 in [32, 32768]; norm, gated
+                                             activation and rows to 8 bits of 8 in [8, 16384];
+                                             experts' products of 8 (8-bit rows 16) in
+                                             [8, 65536]; outputs of 8 in [8, 65536]        */
 #define MOE_RS_ERR_BAD_SEQUENCES (-19)    /* n_seq outside [1, 65536], or > 1 with no offsets */
 #define MOE_RS_ERR_BAD_ROWS (-20)         /* a negative number of rows                     */
 #define MOE_RS_ERR_BAD_CALL (-21)         /* moe_call_packed: unknown operation, or not its
@@ -384,7 +390,7 @@ int moe_experts_mxfp4_plan(int T, int E, int topk, int cols, int outs, int block
 /* Rows in 8 bits: e4m3 codes [rows, cols] (8-byte aligned) and one fp32 scale a row, a value being
  * code * scale.  The scale is the row's largest magnitude / 448, at least 2^-126; a row that holds
  * an infinity or a NaN has a NaN for its scale and codes of zero.  Codes are the nearest of
- * value / scale, ties to the even code (one rounding of 2^-24 ahead of it).
+ * value / scale, ties to the even code (two roundings of 2^-24 ahead of it).
  * moe_fp8_quantize makes them of `rows` rows of x (x_dtype MOE_RS_BF16, MOE_RS_FP16 or MOE_RS_FP32),
  * x_stride elements apart, each row 16-byte aligned; weights are quantised by the same call, once.
  * Errors: MOE_RS_ERR_BAD_DTYPE, _BAD_ROWS, _BAD_COLS, _OVERFLOW, _NULL_POINTER, _MISALIGNED, _ALIAS,

@@ -374,16 +374,18 @@ const char* moe_route_sort_strerror(int status) {
     case MOE_RS_ERR_BAD_GROUPS:
       return "n_group must be in [1, 64] and divide E; topk_group must be in [1, n_group]";
     case MOE_RS_ERR_BAD_TOPK:
-      return "topk must be in [1, 32] and at most topk_group * (E / n_group)";
+      return "topk (the norm: a token's rows) must be in [1, 32], topk at most topk_group * (E / n_group)";
     case MOE_RS_ERR_BAD_BLOCK_M: return "block_m must be a power of two in [1, 1024]";
     case MOE_RS_ERR_BAD_TOKENS:
       return "number of tokens T must be >= 0 (and at most 8 for moe_gate_route_sort)";
-    case MOE_RS_ERR_OVERFLOW: return "T*topk or the padded length does not fit in int32";
+    case MOE_RS_ERR_OVERFLOW:
+      return "T*topk, the padded length, a number of rows or a row stride does not fit in int32";
     case MOE_RS_ERR_MISALIGNED:
-      return "logits/workspace must be 16-byte aligned, other buffers 4-byte aligned";
+      return "logits, rows, weights, 16-bit results, the products' results and workspaces must be 16-byte "
+             "aligned (row strides too), 8-bit codes 8-byte aligned, other buffers to their element size";
     case MOE_RS_ERR_ALIAS: return "an output buffer overlaps an input or another output";
     case MOE_RS_ERR_WORKSPACE: return "workspace is NULL or smaller than required";
-    case MOE_RS_ERR_BAD_SCALE: return "routed_scale must be finite";
+    case MOE_RS_ERR_BAD_SCALE: return "routed_scale must be finite, the norm's eps in [0, 1]";
     case MOE_RS_ERR_LAUNCH: return "the CUDA runtime rejected a kernel launch";
     case MOE_RS_ERR_TOO_LARGE:
       return "the shape needs more scratch than moe_route_sort_noalloc's static 32 MiB";
@@ -394,8 +396,9 @@ const char* moe_route_sort_strerror(int status) {
     case MOE_RS_ERR_BAD_DEBUG_KNOB: return "unknown moe_route_sort_debug_set knob";
     case MOE_RS_ERR_BAD_DTYPE: return "a type code this operation does not take";
     case MOE_RS_ERR_BAD_COLS:
-      return "row length must be a multiple of 32 in [32, 32768] (row strides at least that), "
-             "output width a multiple of 8 in [8, 65536]";
+      return "row length must be a multiple of 32 in [32, 32768] (4-bit rows), of 8 in [8, 16384] (norm, "
+             "gated activation, rows to 8 bits) or of 8, in 8 bits 16, up to 65536 (experts' products); "
+             "row strides at least that; output width a multiple of 8 in [8, 65536]";
     case MOE_RS_ERR_BAD_SEQUENCES:
       return "n_seq must be in [1, 65536], and 1 without sequence offsets";
     case MOE_RS_ERR_BAD_ROWS: return "the number of rows must be >= 0";

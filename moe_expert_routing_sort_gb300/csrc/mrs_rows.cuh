@@ -146,7 +146,7 @@ __device__ __forceinline__ float fp8_scale(uint32_t top) {
   return fmaxf(__uint_as_float(top) / 448.0f, __uint_as_float(0x00800000u));
 }
 // Eight values times `inv` (1 / scale) to codes, to nearest even, saturating at 448.  The product is
-// one rounding of 2^-24 away from the quotient, ahead of one of 2^-4.
+// two roundings of 2^-24 away from the quotient, ahead of one of 2^-4.
 __device__ __forceinline__ uint2 fp8_codes(const float (&v)[8], float inv) {
   uint16_t h[4];
 #pragma unroll
