@@ -17,7 +17,7 @@
 // The four warps' sums of an output meet in shared memory and are added in a fixed order.
 //
 // Bound by the weights' bytes and, before them, by an access to the list: one token in 8 bits, E = 896,
-// topk = 16, 3584 -> 768, 44 MB in 13.7 us (11.1 in a graph, 6.5 at the rate of a copy).  These
+// topk = 16, 3584 -> 768, 44 MB in 13.9 us (11.1 in a graph, 6.5 at the rate of a copy).  These
 // products keep their sums to 1.3e-7.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -160,6 +160,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             for (; part < a.ksteps; ++part) {
               ok = thread_wait(&free_s[to.slot], to.phase ^ 1u, limit);
               if (!ok) break;
+              fence_proxy_async_smem();  // the slot's reads are behind the wait, its copy ahead
               mbar_expect(&full_s[to.slot], kFewStep);
               tma_load_3d(base + to.slot * kFewStep, &wmap, kFewWide / 4 * part, n0, e,
                           &full_s[to.slot]);
@@ -238,14 +239,23 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                        : "r"(w + 64 * (i >> 1) + 8 * kFewWide * (i & 1))
                        : "memory");
         }
+        // The slot is let go once its bytes are in registers: which lane arrives hangs on a word of each
+        // load, and the copying thread has a proxy fence between its wait and the next copy.  (The
+        // arrival by itself held up neither: tensor copies are of another proxy, and in e4m3 up to a
+        // hundred of 200 thousand results had some of the next step's weights.  A proxy fence by every
+        // lane mends it too, and takes one token from 13.8 to 15.1 us.)
+        uint32_t word = 0;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) word ^= p[i][0][0] ^ p[i][1][0];
+        const int who = __any_sync(kFull, word == 0x9e3779b9u) ? 1 : 0;
+        __syncwarp();
+        if (lane == who) mbar_arrive(&free_s[at.slot]);
+        at.advance();
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
           few_mma<kType>(c[0], p[i][0][0], p[i][1][0], p[i][0][1], p[i][1][1], v[i].x, v[i].y);
           few_mma<kType>(c[1], p[i][0][2], p[i][1][2], p[i][0][3], p[i][1][3], v[i].z, v[i].w);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&free_s[at.slot]);
-        at.advance();
         load_x(ks + 2, v);
       };
       for (int ks = 0; ks < a.ksteps; ks += 2) {
