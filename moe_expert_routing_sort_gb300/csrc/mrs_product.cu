@@ -180,12 +180,11 @@ constexpr int kProductThreads = 512;
 template <int R>
 constexpr int kAccs = kProductTmem / R;
 
-// H: 256 m at a time, one or two of them on the same rows
-template <int R, int H>
+template <int R>
 struct ProductShape {
-  static constexpr int kW = H * 128 * 128;
+  static constexpr int kW = 128 * 128;
   static constexpr int kX = R / 2 * 128;
-  static constexpr int kSlots = R == 256 ? (H == 2 ? 4 : 6) : 9;
+  static constexpr int kSlots = R == 256 ? 6 : 9;
   static constexpr size_t kSmem = static_cast<size_t>(kSlots) * (kW + kX) + 1024;
 };
 
@@ -207,10 +206,10 @@ __device__ __forceinline__ uint32_t rounded2(float lo, float hi, int type) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-template <bool kFp8, bool kTranspose, int R, int H, class Out>
+template <bool kFp8, bool kTranspose, int R, class Out>
 __global__ void __launch_bounds__(kProductThreads, 1)
     mrs_product_kernel(const __grid_constant__ CUtensorMap wmap, const ProductArgs a) {
-  using Sh = ProductShape<R, H>;
+  using Sh = ProductShape<R>;
   constexpr int S = Sh::kSlots;
   extern __shared__ unsigned char smem_raw[];
   __shared__ unsigned long long full_s[S], free_s[S], rows_s[S], acc_full_s[kAccs<R>],
@@ -281,7 +280,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   auto weight_bytes = [&](int m) {  // of both CTAs, for the tile at m
     int boxes = 0;
 #pragma unroll
-    for (int i = 0; i < H * kPairRows / kBoxM; ++i) boxes += m + i * kBoxM < a.M ? 1 : 0;
+    for (int i = 0; i < kPairRows / kBoxM; ++i) boxes += m + i * kBoxM < a.M ? 1 : 0;
     return boxes * kBoxM * 128;
   };
 
@@ -291,7 +290,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     while (const ProductInfo<R>* q = next_unit()) {
       const int e = q->e, tiles = q->tiles;
       for (int c = 0; ok && c < tiles; ++c) {
-        const int m = q->m0 + c * H * kPairRows;
+        const int m = q->m0 + c * kPairRows;
         for (int ks = 0; ks < a.ksteps; ++ks) {
           ok = warp_wait(&free_s[at.slot], at.phase ^ 1u, limit);
           if (!ok) break;
@@ -299,15 +298,13 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             if (rank == 0) mbar_expect(&full_s[at.slot], weight_bytes(m));
             const uint32_t bar = pair_first(&full_s[at.slot]);
 #pragma unroll
-            for (int h = 0; h < H; ++h)
-#pragma unroll
-              for (int i = 0; i < 128 / kBoxM; ++i) {
-                const uint32_t to = wbase + at.slot * Sh::kW + h * (128 * 128) + i * (64 * 128);
-                const int at_m = m + h * kPairRows + 128 * rank + i * kBoxM;
-                if (at_m >= a.M) continue;
-                if constexpr (kTranspose) pair_load_3d(to, &wmap, at_m, 64 * ks, e, bar);
-                else pair_load_3d(to, &wmap, (kFp8 ? 128 : 64) * ks, at_m, e, bar);
-              }
+            for (int i = 0; i < 128 / kBoxM; ++i) {
+              const uint32_t to = wbase + at.slot * Sh::kW + i * (64 * 128);
+              const int at_m = m + 128 * rank + i * kBoxM;
+              if (at_m >= a.M) continue;
+              if constexpr (kTranspose) pair_load_3d(to, &wmap, at_m, 64 * ks, e, bar);
+              else pair_load_3d(to, &wmap, (kFp8 ? 128 : 64) * ks, at_m, e, bar);
+            }
           }
           __syncwarp();
           ++issued;
@@ -410,7 +407,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       q.e = min(max(tile.x, 0), a.E - 1);
       q.p0 = min(max(tile.y, 0), a.P);
       q.rows = min(min(tile.z, R), a.P - q.p0);
-      q.m0 = first * H * kPairRows;
+      q.m0 = first * kPairRows;
       q.tiles = min(a.chunk, a.mtiles - first);
     };
     auto load_routes = [&](Ahead& q) {
@@ -494,8 +491,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         uint32_t to_phase = acc_phase;
         const uint32_t word = pair_word(a.type, kTranspose, false, n);
         for (int c = 0; ok && c < tiles; ++c) {
-          ok = pair_wait(&acc_free_s[to], to_phase ^ 1u, limit) &&
-               (H == 1 || pair_wait(&acc_free_s[1], to_phase ^ 1u, limit));
+          ok = pair_wait(&acc_free_s[to], to_phase ^ 1u, limit);
           if (!ok) break;
           tc_fence_after();
           for (int ks = 0; ks < a.ksteps; ++ks) {
@@ -503,24 +499,18 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             if (!ok) break;
             tc_fence_after();
             const uint64_t dx = desc_rows128(xbase + s.slot * Sh::kX);
+            const uint32_t wat = wbase + s.slot * Sh::kW;
+            const uint64_t dw = kTranspose ? desc_lines128(wat, 64) : desc_rows128(wat);
 #pragma unroll
-            for (int h = 0; h < H; ++h) {
-              const uint32_t wat = wbase + s.slot * Sh::kW + h * (128 * 128);
-              const uint64_t dw = kTranspose ? desc_lines128(wat, 64) : desc_rows128(wat);
-#pragma unroll
-              for (int g = 0; g < 4; ++g)
-                // 32 bytes further along the rows; along the lines 16 of them
-                pair_mma<kFp8>(tmem + (H == 2 ? h : to) * R, dw + (kTranspose ? 16 * 128 / 16 : 2) * g,
-                               dx + 2 * g, word, ks > 0 || g > 0);
-              if (H == 2 && ks + 1 == a.ksteps) pair_commit(&acc_full_s[h]);
-            }
+            for (int g = 0; g < 4; ++g)
+              // 32 bytes further along the rows; along the lines 16 of them
+              pair_mma<kFp8>(tmem + to * R, dw + (kTranspose ? 16 * 128 / 16 : 2) * g, dx + 2 * g, word,
+                             ks > 0 || g > 0);
             pair_commit(&free_s[s.slot]);
             s.advance();
           }
-          if (H == 1 && ok) pair_commit(&acc_full_s[to]);
-          if (H == 2) {
-            to_phase ^= 1u;
-          } else if (++to == kAccs<R>) {
+          if (ok) pair_commit(&acc_full_s[to]);
+          if (++to == kAccs<R>) {
             to = 0;
             to_phase ^= 1u;
           }
@@ -528,8 +518,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       }
       ok = __all_sync(kFull, ok);
       at.skip(tiles * a.ksteps);
-      acc_phase ^= static_cast<uint32_t>((buf + tiles * H) / kAccs<R>) & 1u;
-      buf = (buf + tiles * H) % kAccs<R>;
+      acc_phase ^= static_cast<uint32_t>((buf + tiles) / kAccs<R>) & 1u;
+      buf = (buf + tiles) % kAccs<R>;
       leave_unit();
     }
     // nothing of the tensor core may be in flight when tensor memory is given back
@@ -546,7 +536,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     uint32_t acc_phase = 0;
     while (const ProductInfo<R>* q = next_unit()) {
       const int n = q->n, e = q->e;
-      const int count = H * q->tiles;
+      const int count = q->tiles;
       // the outputs' scales, a tile ahead: of the lane's accumulator lanes among the warp's 32 m
       constexpr int kScales = sizeof(Out) == 4 ? 1 : 4;
       float ahead[kScales];
@@ -726,22 +716,22 @@ bool encode_weights3(CUtensorMap* map, const void* p, int type, int size, size_t
 
 namespace {
 
-template <bool kFp8, bool kTranspose, int R, int H, class Out>
+template <bool kFp8, bool kTranspose, int R, class Out>
 cudaError_t launch_product(const CUtensorMap& w, const ProductArgs& a, int pairs, cudaStream_t st) {
-  auto* k = mrs_product_kernel<kFp8, kTranspose, R, H, Out>;
-  constexpr size_t smem = ProductShape<R, H>::kSmem;
+  auto* k = mrs_product_kernel<kFp8, kTranspose, R, Out>;
+  constexpr size_t smem = ProductShape<R>::kSmem;
   static SmemGrant granted;
   const cudaError_t err = grant_smem(reinterpret_cast<const void*>(k), smem, granted);
   if (err != cudaSuccess) return err;
   return launch_pairs(k, pairs, kProductThreads, smem, st, w, a);
 }
 
-template <int R, int H, class Out>
+template <int R, class Out>
 cudaError_t launch_product(bool fp8, bool transpose, const CUtensorMap& w, const ProductArgs& a,
                            int pairs, cudaStream_t st) {
-  return transpose ? launch_product<false, true, R, H, Out>(w, a, pairs, st)
-         : fp8     ? launch_product<true, false, R, H, Out>(w, a, pairs, st)
-                   : launch_product<false, false, R, H, Out>(w, a, pairs, st);
+  return transpose ? launch_product<false, true, R, Out>(w, a, pairs, st)
+         : fp8     ? launch_product<true, false, R, Out>(w, a, pairs, st)
+                   : launch_product<false, false, R, Out>(w, a, pairs, st);
 }
 
 size_t most_tiles(int T, int E, int topk, int block_m, int rows) {
@@ -865,26 +855,20 @@ int product(const void* x, int type, const float* x_scales, int per_route, const
   a.K = K;
   a.P = static_cast<int>(P);
   a.ksteps = (K * static_cast<int>(size) + 127) / 128;
-  // 512 m on the same rows take in a quarter less for the same products, which pays in long calls,
-  // where power holds the clock; they leave no second accumulator for the next tile, and half as many
-  // units fill the pairs less evenly.  us with 256 and with 512, bf16, by the rounds of units of 256: 106
-  // (rows' gradient of T = 8192, E = 64, topk = 8, 7168 -> 2048) 1380 1290, 31 (its product) 1152 1225,
-  // 15 (E = 8, 2048 rows an expert, 4096 -> 4096) 340 370; E = 16, 7168 -> 2048, 256 and 384 rows 130
-  // 160, 156 148; E = 64, 3584 -> 768, 96 and 256 rows 89 92, 105 132.
+  // (512 m on the same rows take in a quarter less for the same products, but leave no second
+  // accumulator for the next tile and half as many units.  Both in turn, us with 256 and with 512: T =
+  // 16384, E = 64, topk = 8, 7168 -> 2048 2400 2450, its rows' gradient 2350 2750; T = 32768, 1024 -> 2048
+  // 690 830; in 8 bits T = 8192, 7168 -> 2048 640 680; only T = 8192, 2048 -> 7168 and its like gain, 1240
+  // 1210.)
   const int pairs = sms / 2;
-  const double row_tiles = static_cast<double>(routes) / R + 0.5 * static_cast<double>(hit);
-  auto rounds = [&](int h) {
-    return row_tiles * ((M + h * kPairRows - 1) / (h * kPairRows)) / pairs + 0.5;
-  };
-  const int H = R > 64 && a.ksteps >= 16 && 2 * 0.9875 * rounds(2) < rounds(1) ? 2 : 1;
-  a.mtiles = (M + H * kPairRows - 1) / (H * kPairRows);
+  a.mtiles = (M + kPairRows - 1) / kPairRows;
   a.type = type == MOE_RS_BF16 ? 1 : 0;
   a.out_type = out_type;
   // A unit is as many output tiles of one row tile as leave 32 rounds of units, but no more than 32768
   // steps (some 20 ms): the list waits for a unit as a whole, and 65536 x 65536 outputs and columns have
   // 262144 of them, more than half of the default limit.
   const size_t each = (routes / R + hit) * a.mtiles / (32 * static_cast<size_t>(pairs));
-  const size_t most = std::min(static_cast<size_t>(a.mtiles), static_cast<size_t>(32768 / (H * a.ksteps)));
+  const size_t most = std::min(static_cast<size_t>(a.mtiles), static_cast<size_t>(32768 / a.ksteps));
   a.chunk = static_cast<int>(each < 1 ? 1 : (each > most ? most : each));
   a.nchunk = (a.mtiles + a.chunk - 1) / a.chunk;
   a.chunk = (a.mtiles + a.nchunk - 1) / a.nchunk;
@@ -902,9 +886,8 @@ int product(const void* x, int type, const float* x_scales, int per_route, const
   const int grid = units < static_cast<size_t>(pairs) ? static_cast<int>(units) : pairs;
   auto go = [&](auto o) {
     using Out = decltype(o);
-    return R == 64  ? launch_product<64, 1, Out>(fp8, transpose, wmap, a, grid, stream)
-           : H == 2 ? launch_product<256, 2, Out>(fp8, transpose, wmap, a, grid, stream)
-                    : launch_product<256, 1, Out>(fp8, transpose, wmap, a, grid, stream);
+    return R == 64 ? launch_product<64, Out>(fp8, transpose, wmap, a, grid, stream)
+                   : launch_product<256, Out>(fp8, transpose, wmap, a, grid, stream);
   };
   return launch_status(out_type == MOE_RS_FP32 ? go(float{}) : go(uint16_t{}));
 }
