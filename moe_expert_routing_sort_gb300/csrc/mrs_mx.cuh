@@ -1,5 +1,4 @@
-// mrs_mx.cuh -- device helpers of the microscaled 4-bit format: E2M1 codes, E8M0 scale bytes; and
-// accesses of 32 bytes.
+// mrs_mx.cuh -- device helpers of the microscaled 4-bit format: E2M1 codes, E8M0 scale bytes.
 #pragma once
 
 #include <cstdint>
@@ -37,30 +36,6 @@ __device__ __forceinline__ void e2m1_values(uint32_t w, float (&v)[8]) {
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
     v[2 * i] = f.x;
     v[2 * i + 1] = f.y;
-  }
-}
-
-// 32 bytes, as one access where the address allows it.
-__device__ __forceinline__ void load32(const void* p, bool wide, uint32_t* w) {
-  if (wide) {
-    asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),
-                   "=r"(w[6]), "=r"(w[7])
-                 : "l"(p));
-  } else {
-    const uint4 a = __ldg(static_cast<const uint4*>(p)), b = __ldg(static_cast<const uint4*>(p) + 1);
-    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-    w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
-  }
-}
-__device__ __forceinline__ void store32(void* p, bool wide, const uint32_t* w) {
-  if (wide) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
-                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
-  } else {
-    static_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    static_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
   }
 }
 
