@@ -483,11 +483,11 @@ size_t moe_experts_product_workspace_bytes(int T, int E, int topk, int block_m);
  * expert side by side, expert ids ascending.  One that is not, or an expert id outside [0, E), sets
  * MOE_RS_DEVICE_BAD_EXPERT_ID, and the outputs are then unspecified (every access stays within the
  * buffers); a device wait that gives up sets MOE_RS_DEVICE_WAIT_TIMEOUT (outputs invalid).
- * The sums of more than 128 routes, and those of the gradients below, are the tensor core's, whose
- * additions cut where others round: results of random terms are small by about 1.2e-9 of their size
- * for every term, 1.0e-6 over 1024 terms and 1.9e-5 over 16384 (in 8 bits less; weights'
- * gradients in fp32 over more than 1024 rows half of it), before they are rounded.  Results are the
- * same bits every call.
+ * The sums are the tensor core's, whose additions cut where others round: of more than 128 routes, and
+ * of the gradients below, results of random terms are small by about 1.2e-9 of their size for every
+ * term, 1.0e-6 over 1024 terms, 1.9e-5 over 16384 and 7.7e-5 over 65536 (in 8 bits a tenth of it;
+ * weights' gradients in fp32 over more than 1024 rows half of it; products of up to 128 routes an
+ * eighth), before they are rounded.  Results are the same bits every call.
  * cols and outs: multiples of 8 (cols of 16 for MOE_RS_FP8) in [8, MOE_RS_PRODUCT_MAX_COLS];
  * limits of T, E, topk, block_m as for moe_sort.  X, W, out: 16-byte aligned.
  * No counterpart in the source pages, whose products belong to another library. */

@@ -28,10 +28,10 @@
 // come out low, by 1.0e-6 of their size over 1024 columns, 4.4e-6 over 4096 and 1.9e-5 over 16384.
 //
 // Bound by the weights' bytes where an expert has few rows (T = 512, E = 896, 3584 -> 768, 16 bits:
-// 720 us, the floor of 729 at the rate of a copy) and by the tensor cores where it has many: T = 8192,
-// E = 64, topk = 8, 7168 -> 2048 in 1150 to 1320 us, cool and warm, up to 84 % of the tensor cores'
-// clocks; a library product of the same size in one piece takes 996 at the rate of a short run and 1116
-// at that of a long one, where power holds the clock.  Short contractions (8192 skewed tokens, E = 896,
+// 720 us, the floor of 729 at the rate of a copy; 8 bits 388 of 365) and by the tensor cores where it has
+// many: T = 8192, E = 64, topk = 8, 7168 -> 2048 in 1150 to 1340 us, cool and warm, up to 84 % of the tensor
+// cores' clocks; a library product of the same size in one piece takes 996 at the rate of a short run and
+// 1116 at that of a long one, where power holds the clock.  In 8 bits 600 to 650 us, of 498.  Short contractions (8192 skewed tokens, E = 896,
 // 384 -> 3584 in 8 bits, 430 us of 329) wait for the warps that store: three steps of products are
 // 130 KB of output.
 #include <algorithm>
@@ -739,10 +739,18 @@ size_t most_tiles(int T, int E, int topk, int block_m, int rows) {
   return P / rows + (n < static_cast<size_t>(E) ? n : E);
 }
 
-// Routes up to which a product goes by the blocks of the list.  us with it and in tiles, 3584 -> 768: 16
-// routes of E = 896 in 8 bits 21.2 27.3, 128 76 83, 512 214 188; in bf16 27 37, 124 131, 326 341; 64
-// routes of E = 64 36 41 and 52 62, of E = 8 19 23 and 23 29.
-int few_routes() { return 128; }
+// Routes up to which a product goes by the blocks of the list.  us with it and in tiles, each call by
+// itself, weights from HBM, 3584 -> 768:
+//                       8 bits                                  bf16
+//   routes   E = 1    4        8        64       896      1        4        8        64       896
+//   16       14 18    12 18    15 18    21 23    21 23    14 25    14 25    18 26    27 31    27 33
+//   64       14 21    16 18    20 18    37 39    45 49    16 27    18 25    23 27    52 57    74 80
+//   128      22 23    23 18    23 18    45 47    74 75    25 27    27 25    27 27    70 79    122 125
+//   256      29 24    29 20    31 18    49 49    127 117  34 31    35 29    35 27    76 80    197 201
+//   512      49 24    49 23    49 23    68 49    213 185  57 31    59 29    59 29    81 80    332 350
+// A unit has eight routes of a block at most, so that 128 routes of a few experts read the same weights
+// again, from L2; at the limit that costs 5 us at most (8 bits, 4 or 8 experts).
+constexpr int kFewRoutes = 128;
 
 // The product (transpose: the rows' gradient, whose contraction runs over W's rows).
 int product(const void* x, int type, const float* x_scales, int per_route, const void* w,
@@ -793,7 +801,7 @@ int product(const void* x, int type, const float* x_scales, int per_route, const
   if (any_alias(outs_s, 2, ins, 8)) return MOE_RS_ERR_ALIAS;
   const int sms = sm_count();
   if (sms == 0) return launch_status(cudaErrorInvalidDevice);
-  if (!transpose && routes <= static_cast<size_t>(few_routes())) {
+  if (!transpose && routes <= kFewRoutes) {
     FewArgs f{};
     f.x = static_cast<const unsigned char*>(x);
     f.sid = sid;
@@ -820,8 +828,9 @@ int product(const void* x, int type, const float* x_scales, int per_route, const
     return launch_status(launch_product_few(map, f, type, sms, stream));
   }
   const size_t hit = routes < static_cast<size_t>(E) ? routes : E;
-  // us in tiles of 64 rows and of 256: E = 64, 3584 -> 768 in bf16, 32, 64 and 96 rows an expert 83 87,
-  // 87 88, 101 89; in 8 bits 50 54, 52 55, 60 56; E = 16, 7168 -> 2048 in bf16 99 103, 113 105, 130 105
+  // us in tiles of 64 rows and of 256, of 32, 48, 64 and 96 rows an expert: E = 64, 3584 -> 768 in bf16 83
+  // 85, 84 87, 87 89, 104 92; in 8 bits 50 53, 51 53, 53 55, 61 57; E = 16, 7168 -> 2048 in bf16 98 103,
+  // 99 103, 115 105, 130 107; in 8 bits 61 64, 61 64, 68 66, 74 66
   const int R = routes <= 48 * hit ? 64 : 256;
   ListArgs list{};
   list.eid = eid;
@@ -864,9 +873,11 @@ int product(const void* x, int type, const float* x_scales, int per_route, const
   a.mtiles = (M + kPairRows - 1) / kPairRows;
   a.type = type == MOE_RS_BF16 ? 1 : 0;
   a.out_type = out_type;
-  // A unit is as many output tiles of one row tile as leave 32 rounds of units, but no more than 32768
-  // steps (some 20 ms): the list waits for a unit as a whole, and 65536 x 65536 outputs and columns have
-  // 262144 of them, more than half of the default limit.
+  // A unit is as many output tiles of one row tile as leave 32 rounds of units (us with 4, 16, 32, 64
+  // rounds and single tiles: 8192 skewed tokens, 384 -> 3584 in 8 bits 371 372 376 395 423; T = 8192, E =
+  // 64, 7168 -> 2048 in bf16 1350 1250 1200 1205 1205), but no more than 32768 steps (some 20 ms): the list
+  // waits for a unit as a whole, and 65536 x 65536 outputs and columns have 262144 of them, more than half
+  // of the default limit.
   const size_t each = (routes / R + hit) * a.mtiles / (32 * static_cast<size_t>(pairs));
   const size_t most = std::min(static_cast<size_t>(a.mtiles), static_cast<size_t>(32768 / a.ksteps));
   a.chunk = static_cast<int>(each < 1 ? 1 : (each > most ? most : each));
